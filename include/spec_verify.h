@@ -65,7 +65,8 @@ typedef enum sv_status {
   SV_ERR_TREE = 5,        /* tree parent stride neither 0 nor N */
   SV_ERR_WORKSPACE = 6,   /* workspace NULL, not 256-byte aligned, or too small */
   SV_ERR_CUDA = 7,        /* a CUDA runtime call or kernel launch failed */
-  SV_ERR_FILTER = 8       /* top_k negative, top_p outside (0, 1], or eps / delta negative */
+  SV_ERR_FILTER = 8,      /* top_k negative, top_p outside (0, 1], or eps / delta negative */
+  SV_ERR_ALIAS = 9        /* an output overlaps an input that it must not overlap */
 } sv_status;
 
 typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
@@ -84,6 +85,10 @@ typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_MAX_V (1 << 24)      /* vocabulary size */
 #define SV_MAX_TREE_NODES 256   /* candidate nodes per tree (root excluded) */
 #define SV_MAX_NGRAM 32         /* longest n-gram the proposer matches */
+#define SV_MAX_TOP 128          /* logits of a top-logits record, candidates a beam selection keeps */
+#define SV_MAX_BEAMS 64         /* beams per request */
+#define SV_MAX_ROWS (1 << 27)   /* rows (B * P) of a top-logits or distillation call */
+#define SV_MAX_DISTILL_ROW 1572864 /* bytes of a student row (V * sizeof(logit)) */
 
 /* Bytes of workspace that spec_verify_sample / _greedy need for B requests
  * of K draft positions over a vocabulary of V (the dense-draft sampling case,
@@ -380,6 +385,134 @@ sv_status spec_ngram_propose(const int32_t* tokens, const int32_t* lens, int B, 
                              int n_min, int n_max, int K, int32_t* out_drafts,
                              int32_t* out_draft_lens, int32_t* out_match, int32_t* out_status,
                              sv_stream_t stream);
+
+/* The record of a teacher's rows: each row's k largest logits and its
+ * log-sum-exp.  The verification step has the target's logits at hand at
+ * every position; with lens = out_accept_len the rows on the accepted path
+ * are recorded, and spec_distill trains a draft model on the records.
+ *
+ *   logits      [B, P, V] dtype (P = K+1 for the rows of a verify call).
+ *   k           1 <= k <= SV_MAX_TOP logits kept per row.
+ *   temperature T > 0, finite: out_lse is of the tempered logits.
+ *   lens        [B] int32 or NULL: rows i < lens[b] of request b are recorded,
+ *               the others are not read.  lens[b] outside [0, P] gives every
+ *               row of the request SV_REQ_BAD_DRAFT_LEN and no record.
+ *   out_ids     [B, P, k] int32: the tokens of the k largest logits, in
+ *               descending order, equal logits (-0.0 == +0.0) by ascending
+ *               token; only finite logits are kept, -1 past the last of them.
+ *   out_logits  [B, P, k] fp32: their logits (exact), -inf past the last.
+ *   out_lse     [B, P] fp32: log sum_j exp(l_j / T); -inf for a row that is
+ *               not read or has no finite logit.
+ *   out_status  [B, P] int32 or NULL: SV_REQ_* bits per row.  A row with NaN or
+ *               +inf (SV_REQ_BAD_LOGITS) has no record (-1, -inf) and lse NaN.
+ *   B, P, V     0 <= B <= SV_MAX_B, P >= 1, B * P <= SV_MAX_ROWS, 1 <= V <= SV_MAX_V.
+ * No workspace: a call keeps nothing, so calls may overlap on any streams. */
+sv_status spec_top_logits(const void* logits, int k, float temperature, const int32_t* lens,
+                          int32_t* out_ids, float* out_logits, float* out_lse,
+                          int32_t* out_status, sv_dtype dtype, int B, int P, int V,
+                          sv_stream_t stream);
+
+/* Distillation of a draft model from a teacher's top logits: the divergence
+ * KL(p || q) of each row, and its gradient by the student's logits.
+ *
+ * With a record (ids, t_j) of a row, T the temperature, x = s / T the
+ * student's tempered logits and q = softmax(x):
+ *   top_lse given (L, the teacher's log-sum-exp at the same T): p_j =
+ *     exp(t_j / T - L) on the recorded tokens, and every other token in one
+ *     bucket of p_rest = max(0, 1 - sum p_j) against q_rest, the student's mass
+ *     outside the record:
+ *       loss = sum_j p_j (log p_j - log q_j) + p_rest (log p_rest - log q_rest)
+ *     (a record of all V tokens has no rest);
+ *   top_lse NULL: p is the softmax of t / T over the record alone and
+ *       loss = sum_j p_j (log p_j - log q_j).
+ *   gradient by s_i: (q_i - p_i) / T on recorded tokens, elsewhere
+ *     (q_i - p_rest q_i / q_rest) / T, each times grad_loss of the row.
+ * A term with p = 0 is 0.  A recorded token with p_j > 0 whose student logit is
+ * -inf gives loss +inf (the gradient stays finite).
+ *
+ *   student_logits [B, P, V] dtype, V * sizeof(logit) <= SV_MAX_DISTILL_ROW.
+ *   top_ids     [B, P, k] int32: distinct tokens in [0, V); -1 marks an unused
+ *               entry.  A row without a used entry has loss 0 and gradient 0.
+ *   top_logits  [B, P, k] fp32: finite, or -inf (p_j = 0).
+ *   top_lse     [B, P] fp32 or NULL.
+ *   lens        [B] int32 or NULL: rows i >= lens[b] are not read; their loss and
+ *               gradient are 0.  lens[b] outside [0, P]: SV_REQ_BAD_DRAFT_LEN.
+ *   grad_loss   [B, P] fp32 or NULL: with it the call also writes out_grad, the
+ *               gradient of sum(grad_loss * loss), reading the student once.
+ *   out_loss    [B, P] fp32.
+ *   out_stats   [B, P, 4] fp32 (16-byte aligned) or NULL: what spec_distill_grad
+ *               needs of this call.
+ *   out_grad    [B, P, V] dtype: written when grad_loss is given (every row).
+ *               It may be student_logits itself, and overlap it in no other way
+ *               (SV_ERR_ALIAS).
+ *   out_status  [B, P] int32 or NULL: SV_REQ_BAD_LOGITS (student NaN, +inf or no
+ *               finite logit; a used entry's logit NaN or +inf, or a top_lse beside
+ *               it that is not finite), SV_REQ_BAD_TOKEN (a token outside [-1, V) or
+ *               given twice), SV_REQ_BAD_DRAFT_LEN.  Such a row has loss NaN and
+ *               gradient 0.
+ *   k, B, P, V, temperature: as in spec_top_logits.  No workspace. */
+sv_status spec_distill(const void* student_logits, const int32_t* top_ids,
+                       const float* top_logits, const float* top_lse, const int32_t* lens,
+                       const float* grad_loss, float temperature, float* out_loss,
+                       float* out_stats, void* out_grad, int32_t* out_status, sv_dtype dtype,
+                       int B, int P, int V, int k, sv_stream_t stream);
+
+/* The backward pass of spec_distill alone: out_grad [B, P, V] = the gradient
+ * of sum(grad_loss * loss), from the out_stats of a spec_distill call with the
+ * same student_logits, record, lens and temperature. */
+sv_status spec_distill_grad(const void* student_logits, const int32_t* top_ids,
+                            const float* top_logits, const float* top_lse, const int32_t* lens,
+                            const float* stats, const float* grad_loss, float temperature,
+                            void* out_grad, sv_dtype dtype, int B, int P, int V, int k,
+                            sv_stream_t stream);
+
+/* One step of beam selection: of all continuations (beam w, token v) of a
+ * request, the n of largest score
+ *     scores[b, w] + l[b, w, v] - log sum_j exp(l[b, w, j]),
+ * in descending order, equal scores by ascending w * V + v.  With a draft
+ * model's logits each call is one level of a candidate tree (the kept
+ * (parent, token) pairs are its nodes) for spec_verify_tree and its kin.
+ *
+ *   logits      [B, W, V] dtype.
+ *   scores      [B, W] fp32: each beam's score so far; -inf marks a finished
+ *               beam, whose row is not read.  At the first step all beams but one
+ *               are -inf.
+ *   out_tokens, out_parents [B, n] int32: token v and beam w of each kept
+ *               candidate; out_scores [B, n] fp32.  Candidates have finite logits; past
+ *               the last one the slots hold -1, -1 and -inf.
+ *   out_status  [B] int32 or NULL: SV_REQ_BAD_LOGITS when a live beam's row has NaN
+ *               or +inf, or a score is NaN or +inf; nothing is kept then.
+ *   1 <= W <= SV_MAX_BEAMS, 1 <= n <= SV_MAX_TOP, 0 <= B <= SV_MAX_B, and
+ *   ceil(W / 8) * ceil(V / 8192) <= 320 (V <= 2621440 up to 8 beams, 327680 with
+ *   64).  Scores are compared in 64 bits (their row sums are of 32-bit terms).
+ * No workspace. */
+sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out_tokens,
+                           int32_t* out_parents, float* out_scores, int32_t* out_status,
+                           sv_dtype dtype, int B, int W, int V, int n, sv_stream_t stream);
+
+/* Reordering of per-beam states: out[g, b, w, h, l] = state[g, b, parents[b, w],
+ * h, l] for l < lens[b], each entry a run of row_bytes contiguous bytes.  It
+ * moves a draft model's states (hidden states, keys and values, block tables)
+ * along a beam selection's parents, and gathers the accepted path's entries out
+ * of a candidate tree's (parents = out_path of a tree call, which names node ids).
+ *
+ *   state       G x B x W x H x L entries at byte strides state_strides[5].
+ *   out         G x B x W_out x H x L entries at byte strides out_strides[5].
+ *               Strides are >= 0 and may come in any order (heads before or after
+ *               beams); entries of `out` must not overlap each other, nor state's
+ *               memory (SV_ERR_ALIAS).
+ *   parents     [B, W_out] int32: -1 leaves the slot as it is.
+ *   lens        [B] int32 or NULL (all L): entries l >= lens[b] of out are left as
+ *               they are.
+ *   out_status  [B] int32 or NULL: SV_REQ_BAD_TREE for a parent outside [-1, W)
+ *               (its slot is left as it is), SV_REQ_BAD_DRAFT_LEN for lens[b] outside
+ *               [0, L] (nothing is moved).
+ * Every extent but row_bytes may be 0.  B <= SV_MAX_B, W and W_out < 65536; G,
+ * H, L and row_bytes < 2^31.  No workspace. */
+sv_status spec_beam_reorder(const void* state, const int64_t* state_strides,
+                            const int32_t* parents, const int32_t* lens, void* out,
+                            const int64_t* out_strides, int32_t* out_status, int G, int B, int W,
+                            int W_out, int H, int L, int row_bytes, sv_stream_t stream);
 
 /* Allocation-free variant of spec_verify_sample.  The pages have no
  * counterpart to this entry point; it exists for callers that cannot

@@ -18,6 +18,8 @@ SYMBOLS = (
     "spec_verify_greedy_masked", "spec_ngram_propose", "spec_verify_sample_filtered",
     "spec_verify_typical", "spec_verify_tree_typical", "spec_verify_tree_workspace_size",
     "spec_verify_tree_sample", "spec_verify_set_wait_limit_ns", "spec_verify_wait_limit_ns",
+    "spec_top_logits", "spec_distill", "spec_distill_grad", "spec_beam_select",
+    "spec_beam_reorder",
 )
 
 _lock = threading.Lock()
@@ -74,6 +76,16 @@ def lib():
         l.spec_ngram_propose.restype = I
         l.spec_verify_tree.argtypes = [P, P, I, P, P, P, I, I, I, I, I, P, P, P]
         l.spec_verify_tree.restype = I
+        l.spec_top_logits.argtypes = [P, I, F, P, P, P, P, P, I, I, I, I, P]
+        l.spec_top_logits.restype = I
+        l.spec_distill.argtypes = [P, P, P, P, P, P, F, P, P, P, P, I, I, I, I, I, P]
+        l.spec_distill.restype = I
+        l.spec_distill_grad.argtypes = [P, P, P, P, P, P, P, F, P, I, I, I, I, I, P]
+        l.spec_distill_grad.restype = I
+        l.spec_beam_select.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P]
+        l.spec_beam_select.restype = I
+        l.spec_beam_reorder.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]
+        l.spec_beam_reorder.restype = I
         l.spec_verify_status_string.argtypes = [I]
         l.spec_verify_status_string.restype = ctypes.c_char_p
         l.spec_verify_version.argtypes = []

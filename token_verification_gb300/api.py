@@ -388,3 +388,243 @@ def spec_ngram_propose(tokens, lens, K=5, n_min=1, n_max=4, out: Optional[NgramO
     if rc:
         raise VerifyError(rc)
     return out
+
+
+# ---------------------------------------------------------------------------
+# draft training and tree drafting: a teacher's top logits, distillation, beams
+# ---------------------------------------------------------------------------
+
+MAX_TOP = 128
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(device, fn, *args):
+    """fn(*args, stream) on the device's current stream, with the device current."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc:
+        raise VerifyError(rc)
+
+
+def _rows(logits, name, shape):
+    """(dims..., device) of a [B, P, V] / [B, W, V] CUDA logit tensor."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise ValueError("%s must be a %s tensor" % (name, shape))
+    device = logits.device
+    if device.type != "cuda":
+        raise ValueError("%s must be a CUDA tensor" % name)
+    _check(logits, name, device)
+    return (*logits.shape, device)
+
+
+def _count(k):
+    """A record's or selection's size; refused here, before it sizes an output."""
+    k = int(k)
+    if not 1 <= k <= MAX_TOP:
+        raise VerifyError(2)
+    return k
+
+
+def _given(out, device, **like):
+    """Check caller-given output tensors: name -> (dtype, shape), None fields are left out."""
+    for name, (dtype, shape) in like.items():
+        t = getattr(out, name)
+        if t is not None:
+            _check(t, "out." + name, device, dtype, shape)
+
+
+@dataclass
+class TopLogits:
+    ids: torch.Tensor      # [B, P, k] int32, -1 past the last finite logit
+    logits: torch.Tensor   # [B, P, k] fp32, -inf past it
+    lse: torch.Tensor      # [B, P] fp32
+    status: Optional[torch.Tensor] = None  # [B, P]
+
+
+def spec_top_logits(logits, k, temperature=1.0, out: Optional[TopLogits] = None, *, lens=None,
+                    status=True) -> TopLogits:
+    """The k largest logits of each row and its log-sum-exp (see
+    spec_verify.h): logits [B, P, V] bf16/fp32 CUDA, 1 <= k <= 128, temperature
+    > 0 (of the log-sum-exp), lens [B] int32 or None (rows i >= lens[b] are not
+    read: pass accept_len to record a verify call's accepted positions)."""
+    B, P, V, device = _rows(logits, "logits", "[B, P, V]")
+    k = _count(k)
+    if lens is not None:
+        _check(lens, "lens", device, torch.int32, (B,))
+    if out is None:
+        shape = (B, P, k)
+        out = TopLogits(torch.empty(shape, dtype=torch.int32, device=device),
+                        torch.empty(shape, dtype=torch.float32, device=device),
+                        torch.empty((B, P), dtype=torch.float32, device=device),
+                        torch.empty((B, P), dtype=torch.int32, device=device) if status else None)
+    else:
+        _given(out, device, ids=(torch.int32, (B, P, k)), logits=(torch.float32, (B, P, k)),
+               lse=(torch.float32, (B, P)), status=(torch.int32, (B, P)))
+    _launch(device, _native.lib().spec_top_logits, logits.data_ptr(), k, float(temperature),
+            _addr(lens), out.ids.data_ptr(), out.logits.data_ptr(), out.lse.data_ptr(),
+            _addr(out.status), _dtype_code(logits), B, P, V)
+    return out
+
+
+@dataclass
+class DistillOutputs:
+    loss: torch.Tensor                     # [B, P] fp32
+    stats: Optional[torch.Tensor] = None   # [B, P, 4] fp32, for spec_distill_grad
+    grad: Optional[torch.Tensor] = None    # [B, P, V]
+    status: Optional[torch.Tensor] = None  # [B, P]
+
+
+def _distill_args(student_logits, top_ids, top_logits, top_lse, lens, grad_loss):
+    B, P, V, device = _rows(student_logits, "student_logits", "[B, P, V]")
+    if not isinstance(top_ids, torch.Tensor) or top_ids.dim() != 3:
+        raise ValueError("top_ids must be a [B, P, k] tensor")
+    k = top_ids.shape[2]
+    _check(top_ids, "top_ids", device, torch.int32, (B, P, k))
+    _check(top_logits, "top_logits", device, torch.float32, (B, P, k))
+    for t, name, shape, dtype in ((top_lse, "top_lse", (B, P), torch.float32),
+                                  (lens, "lens", (B,), torch.int32),
+                                  (grad_loss, "grad_loss", (B, P), torch.float32)):
+        if t is not None:
+            _check(t, name, device, dtype, shape)
+    return B, P, V, k, device
+
+
+def spec_distill(student_logits, top_ids, top_logits, temperature=1.0,
+                 out: Optional[DistillOutputs] = None, *, top_lse=None, lens=None, grad_loss=None,
+                 stats=True, status=True) -> DistillOutputs:
+    """The distillation loss of each row from a teacher's top logits (see
+    spec_verify.h): student_logits [B, P, V] bf16/fp32 CUDA; top_ids,
+    top_logits [B, P, k] and top_lse [B, P] as spec_top_logits returns them
+    (top_lse None: the teacher renormalised over its record); lens [B] int32
+    or None.  With grad_loss [B, P] fp32 the same pass also writes out.grad,
+    the gradient of (grad_loss * loss).sum() in the student's type, for
+    ``student_logits.backward(out.grad)``; out.grad may be student_logits."""
+    B, P, V, k, device = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
+                                       grad_loss)
+    if out is None:
+        f32 = dict(dtype=torch.float32, device=device)
+        out = DistillOutputs(
+            loss=torch.empty((B, P), **f32),
+            stats=torch.empty((B, P, 4), **f32) if stats else None,
+            grad=torch.empty((B, P, V), dtype=student_logits.dtype, device=device)
+            if grad_loss is not None else None,
+            status=torch.empty((B, P), dtype=torch.int32, device=device) if status else None)
+    else:
+        _given(out, device, loss=(torch.float32, (B, P)), stats=(torch.float32, (B, P, 4)),
+               grad=(student_logits.dtype, (B, P, V)), status=(torch.int32, (B, P)))
+    _launch(device, _native.lib().spec_distill, student_logits.data_ptr(), top_ids.data_ptr(),
+            top_logits.data_ptr(), _addr(top_lse), _addr(lens), _addr(grad_loss),
+            float(temperature), out.loss.data_ptr(), _addr(out.stats),
+            _addr(out.grad) if grad_loss is not None else None, _addr(out.status),
+            _dtype_code(student_logits), B, P, V, k)
+    return out
+
+
+def spec_distill_grad(student_logits, top_ids, top_logits, temperature, stats, grad_loss,
+                      grad=None, *, top_lse=None, lens=None) -> torch.Tensor:
+    """The backward pass alone: the gradient of (grad_loss * loss).sum() by
+    student_logits, from the stats of a spec_distill call on the same inputs.
+    grad: the tensor to write ([B, P, V], the student's type; student_logits
+    itself is allowed), or None for a new one."""
+    if grad_loss is None or stats is None:
+        raise ValueError("stats and grad_loss are required")
+    B, P, V, k, device = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
+                                       grad_loss)
+    _check(stats, "stats", device, torch.float32, (B, P, 4))
+    if grad is None:
+        grad = torch.empty((B, P, V), dtype=student_logits.dtype, device=device)
+    else:
+        _check(grad, "grad", device, student_logits.dtype, (B, P, V))
+    _launch(device, _native.lib().spec_distill_grad, student_logits.data_ptr(),
+            top_ids.data_ptr(), top_logits.data_ptr(), _addr(top_lse), _addr(lens),
+            stats.data_ptr(), grad_loss.data_ptr(), float(temperature), grad.data_ptr(),
+            _dtype_code(student_logits), B, P, V, k)
+    return grad
+
+
+@dataclass
+class BeamOutputs:
+    tokens: torch.Tensor   # [B, n] int32, -1 past the last candidate
+    parents: torch.Tensor  # [B, n] int32, the beam of each
+    scores: torch.Tensor   # [B, n] fp32, descending
+    status: Optional[torch.Tensor] = None  # [B]
+
+
+def spec_beam_select(logits, scores, n, out: Optional[BeamOutputs] = None, *,
+                     status=True) -> BeamOutputs:
+    """One step of beam selection (see spec_verify.h): logits [B, W, V]
+    bf16/fp32 CUDA, scores [B, W] fp32 (-inf: a finished beam, not read); the
+    n best continuations by scores + log_softmax(logits), best first."""
+    B, W, V, device = _rows(logits, "logits", "[B, W, V]")
+    n = _count(n)
+    _check(scores, "scores", device, torch.float32, (B, W))
+    if out is None:
+        shape = (B, n)
+        out = BeamOutputs(torch.empty(shape, dtype=torch.int32, device=device),
+                          torch.empty(shape, dtype=torch.int32, device=device),
+                          torch.empty(shape, dtype=torch.float32, device=device),
+                          torch.empty((B,), dtype=torch.int32, device=device) if status else None)
+    else:
+        _given(out, device, tokens=(torch.int32, (B, n)), parents=(torch.int32, (B, n)),
+               scores=(torch.float32, (B, n)), status=(torch.int32, (B,)))
+    _launch(device, _native.lib().spec_beam_select, logits.data_ptr(), scores.data_ptr(),
+            out.tokens.data_ptr(), out.parents.data_ptr(), out.scores.data_ptr(),
+            _addr(out.status), _dtype_code(logits), B, W, V, n)
+    return out
+
+
+_Strides = ctypes.c_int64 * 5
+
+
+def spec_beam_reorder(state, parents, out=None, *, lens=None, status=None) -> torch.Tensor:
+    """Move per-beam states along a selection's parents (see spec_verify.h):
+    out[g, b, w, h, l] = state[g, b, parents[b, w], h, l] for l < lens[b].
+
+    state [G, B, W, H, L, D] CUDA of any type, the last dimension contiguous,
+    the others at any strides (a permuted view of a cache is fine; a dimension
+    the state does not have is 1); parents [B, W_out] int32 (-1 leaves a slot as
+    it is); lens [B] int32 or None; out [G, B, W_out, H, L, D] of the same
+    type (None: a new tensor of zeros); status: an int32 [B] tensor to receive
+    the request status, or None."""
+    if not isinstance(state, torch.Tensor) or state.dim() != 6:
+        raise ValueError("state must be a [G, B, W, H, L, D] tensor")
+    device = state.device
+    if device.type != "cuda":
+        raise ValueError("state must be a CUDA tensor")
+    G, B, W, H, L, D = state.shape
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+        raise ValueError("parents must be a [B, W_out] tensor")
+    W_out = parents.shape[1]
+    _check(parents, "parents", device, torch.int32, (B, W_out))
+    if lens is not None:
+        _check(lens, "lens", device, torch.int32, (B,))
+    if status is not None:
+        _check(status, "status", device, torch.int32, (B,))
+    if out is None:
+        out = torch.zeros((G, B, W_out, H, L, D), dtype=state.dtype, device=device)
+    elif not isinstance(out, torch.Tensor) or out.device != device:
+        raise ValueError("out must be a tensor on %s" % device)
+    elif out.dtype != state.dtype:
+        raise TypeError("out must be %s (got %s)" % (state.dtype, out.dtype))
+    elif tuple(out.shape) != (G, B, W_out, H, L, D):
+        raise ValueError("out must have shape %s (got %s)" % ((G, B, W_out, H, L, D),
+                                                             tuple(out.shape)))
+    for t, name in ((state, "state"), (out, "out")):
+        if D > 1 and t.stride(5) != 1:
+            raise ValueError("the last dimension of %s must be contiguous" % name)
+    size = state.element_size()
+    row_bytes = D * size
+    if D == 0:
+        raise ValueError("state must have entries of at least one element")
+    _launch(device, _native.lib().spec_beam_reorder, state.data_ptr(),
+            _Strides(*[x * size for x in state.stride()[:5]]), _addr(parents), _addr(lens),
+            out.data_ptr(), _Strides(*[x * size for x in out.stride()[:5]]), _addr(status), G, B,
+            W, W_out, H, L, row_bytes)
+    return out

@@ -479,6 +479,7 @@ const char* spec_verify_status_string(sv_status s) {
     case SV_ERR_WORKSPACE: return "workspace NULL, misaligned or too small";
     case SV_ERR_CUDA: return "CUDA launch failed";
     case SV_ERR_FILTER: return "top_k negative or top_p outside (0, 1]";
+    case SV_ERR_ALIAS: return "an output overlaps an input or itself";
   }
   return "unknown status";
 }

@@ -1,0 +1,571 @@
+// sv_top.cu - the k largest logits of each row with its log-sum-exp
+// (spec_top_logits), and beam selection over beams and vocabulary
+// (spec_beam_select): one kernel, a thread-block cluster per row or request.
+//
+// A row (of a request's W beams, or the one row of a record) is cut into
+// `slices`; the (row, slice) items are dealt to the cluster's CTAs.  One pass
+// over an item reads every logit once and keeps, per thread, a running
+// softmax sum and max, and per 32 elements their max (rounded up to bf16, in
+// shared memory).  The selection then follows from the thread maxes alone:
+// if `units` disjoint parts of the data have maxes u_1.., the n-th largest of
+// them is a bound that at least n elements reach, so every kept element is at
+// or above it, and little else is: with n of 256 parts occupied, about
+// 256 ln(256 / (256 - n)) elements (74 for n = 64).  Only the 32-element
+// groups whose max reaches the bound are read again (from L2), their elements
+// at or above it are listed, and the list is sorted by counting.
+//
+// A beam's candidates compare by score = offset + logit with offset =
+// scores[w] - lse[w] in 64 bits; a record's offset is 0.  Bounds are in fp32
+// rounded down, which can only lengthen the list.
+//
+// When the list does not fit (long rows of equal logits), the leader CTA
+// selects each row by radix descent on whole-number keys, 8 bits a pass.
+#include <string.h>
+
+#include "../../include/spec_verify.h"
+#include "sv_launch.h"
+#include "sv_rows.cuh"
+#include "sv_vec.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kTopThreads = 256;
+constexpr int kTopWarps = kTopThreads / kWarp;
+constexpr int kTopSpan = 8192;        // elements a CTA reads per iteration
+constexpr int kMaxItems = 64;         // (row, slice) items per cluster
+constexpr int kMaxUnits = 512;        // thread-max units per cluster (4 per kept element)
+constexpr int kMaxHits = 1024;        // 32-element groups a CTA reads again
+constexpr int kMaxCands = 2048;       // candidates of a cluster
+constexpr int kMaxTables = 320;       // iterations of a CTA over its items: 512 bytes each
+constexpr int kRankAll = 384;         // lists longer than this are cut to the bound first
+
+struct TopParams {
+  const void* logits;   // [B*P, V] (record) or [B*W, V] (beams)
+  const int* lens;      // [B] or null (record)
+  const float* scores;  // [B*W] (beams)
+  int* out_ids;         // [B*P, k] / tokens [B, n]
+  int* out_parents;     // beams: [B, n]
+  float* out_values;    // [B*P, k] / scores [B, n]
+  float* out_lse;       // record: [B*P]
+  int* out_status;
+  int P;                // record: rows per request
+  int W;                // rows per cluster (record: 1)
+  int V, n;
+  int slices, slice;    // slices per row, elements per slice (a multiple of 256)
+  int iters;            // iterations per item
+  int upi;              // units per item (a power of two)
+  float cc;             // log2(e) / T
+  float T;
+  RowSpan span;
+};
+
+struct TopShared {
+  float2 part[kMaxItems][kTopWarps];  // per item and warp: {max, sum of 2^((l - max) c)}
+  float unit[kMaxUnits];              // unit maxes, item by item
+  double off[SV_MAX_BEAMS];           // score - lse of each row
+  double lse[SV_MAX_BEAMS];
+  float thr[SV_MAX_BEAMS];            // the lowest logit a candidate of the row can have
+  unsigned hit[kMaxHits];
+  unsigned long long key[kMaxCands];  // candidates: ordered score, flat index w * V + v
+  int idx[kMaxCands];
+  unsigned hist[256];
+  int n_hits, n_cands, overflow, bad, pick[4];
+  float bound;
+};
+
+// The upper 16 bits of v rounded up: a bf16 value >= v (v itself for bf16).
+__device__ __forceinline__ uint16_t up_bf16(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return (uint16_t)((b & 0x80000000u) ? b >> 16 : (b + 0xffffu) >> 16);
+}
+__device__ __forceinline__ float of_bf16(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+
+// The n-th largest of the cluster's unit bounds to 16 bits (rounded down), by
+// bisection on ordered keys; -inf when fewer than n are finite.  One warp.
+__device__ float unit_bound(const float* unit, int units, int n) {
+  constexpr int kPer = kMaxUnits / kWarp;
+  uint32_t k[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = j * kWarp + lane_id();
+    const float v = i < units ? unit[i] : -INFINITY;
+    k[j] = v > -INFINITY ? ordered(v) >> 16 : 0u;  // -inf (key 0x007f) sorts below every value
+  }
+  uint32_t t = 0;
+  for (uint32_t bit = 0x8000u; bit; bit >>= 1) {
+    const uint32_t at = t | bit;
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) c += k[j] >= at ? 1 : 0;
+    if ((int)__reduce_add_sync(0xffffffffu, (unsigned)c) >= n) t = at;
+  }
+  return t ? of_ordered(t << 16) : -INFINITY;
+}
+
+// One row's n largest finite elements by radix descent, appended to the list
+// from `at` on (a whole-CTA call); returns how many.
+template <typename T>
+__device__ int select_row_slow(TopShared& s, const T* row, int V, int n, double off, int base,
+                               int at) {
+  const int t = threadIdx.x;
+  auto key_of = [&](int j) {  // (logit in order, index from the end), 0 if not finite
+    const float l = j < V ? load_logit(row, j) : -INFINITY;
+    return l > -INFINITY
+               ? ((unsigned long long)ordered(l) << 24) | (unsigned long long)(0xffffff - j)
+               : 0ull;
+  };
+  unsigned long long cut = 0;
+  int need = n;
+  bool all = false;
+  for (int shift = 48; shift >= 0; shift -= 8) {
+    for (int i = t; i < 256; i += kTopThreads) s.hist[i] = 0;
+    __syncthreads();
+    for (int j0 = 0; j0 < V; j0 += kTopThreads) {
+      const unsigned long long k = key_of(j0 + t);
+      const bool in = k != 0 && ((k ^ cut) >> (shift + 8)) == 0;
+      const unsigned digit = in ? (unsigned)(k >> shift) & 255u : 256u;
+      const unsigned peers = __match_any_sync(0xffffffffu, digit);
+      if (in && lane_id() == __ffs(peers) - 1) atomicAdd(&s.hist[digit], (unsigned)__popc(peers));
+    }
+    __syncthreads();
+    if (t == 0) {
+      int d = 255, above = 0;
+      for (; d > 0 && above + (int)s.hist[d] < need; --d) above += (int)s.hist[d];
+      s.pick[0] = d;
+      s.pick[1] = above;
+      s.pick[2] = (int)s.hist[d];
+    }
+    __syncthreads();
+    const int above = s.pick[1], here = s.pick[2];
+    cut |= (unsigned long long)s.pick[0] << shift;
+    __syncthreads();
+    if (above + here < need) {  // (first pass only) fewer than n finite elements: all of them
+      all = true;
+      break;
+    }
+    need -= above;
+    if (here == need) break;  // every element of this prefix is kept
+  }
+  if (all) cut = 1;
+  if (t == 0) s.pick[3] = at;
+  __syncthreads();
+  for (int j0 = 0; j0 < V; j0 += kTopThreads) {
+    const unsigned long long k = key_of(j0 + t);
+    if (k != 0 && k >= cut) {
+      const int o = atomicAdd(&s.pick[3], 1);
+      s.key[o] = ordered(off + (double)load_logit(row, j0 + t));
+      s.idx[o] = base + j0 + t;
+    }
+  }
+  __syncthreads();
+  return s.pick[3] - at;
+}
+
+// How many of the list's entries come before entry i.
+__device__ __forceinline__ int rank_of(const TopShared& s, int count, unsigned long long key,
+                                       int idx) {
+  int r = 0;
+  for (int j = 0; j < count; ++j) {
+    const unsigned long long kj = s.key[j];
+    r += (kj > key || (kj == key && s.idx[j] < idx)) ? 1 : 0;
+  }
+  return r;
+}
+
+// Cuts the list to the entries at or above its n-th largest 32-bit key prefix.
+__device__ int prune(TopShared& s, int count, int n) {
+  constexpr int kPer = kMaxCands / kTopThreads;
+  unsigned long long k[kPer];
+  int ix[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int i = q * kTopThreads + threadIdx.x;
+    k[q] = i < count ? s.key[i] : 0ull;
+    ix[q] = i < count ? s.idx[i] : 0;
+  }
+  uint32_t t = 0;
+  for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+    const uint32_t at = t | bit;
+    int c = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) c += (uint32_t)(k[q] >> 32) >= at ? 1 : 0;
+    c = (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
+    if (threadIdx.x == 0) s.pick[0] = 0;
+    __syncthreads();
+    if (lane_id() == 0) atomicAdd(&s.pick[0], c);
+    __syncthreads();
+    if (s.pick[0] >= n) t = at;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) s.pick[1] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kPer; ++q)
+    if (k[q] != 0 && (uint32_t)(k[q] >> 32) >= t) {
+      const int o = atomicAdd(&s.pick[1], 1);
+      s.key[o] = k[q];
+      s.idx[o] = ix[q];
+    }
+  __syncthreads();
+  return s.pick[1];
+}
+
+template <bool kBeam>
+__device__ __forceinline__ void write_slot(const TopParams& p, long long grp, int slot,
+                                           unsigned long long key, int idx) {
+  const long long o = grp * p.n + slot;
+  const int w = kBeam && idx >= 0 ? idx / p.V : 0;
+  p.out_ids[o] = idx < 0 ? -1 : idx - w * p.V;
+  if (kBeam) p.out_parents[o] = idx < 0 ? -1 : w;
+  p.out_values[o] = idx < 0 ? -INFINITY : (float)of_ordered(key);
+}
+
+template <typename T, bool kAligned, bool kBeam>
+__global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) {
+  constexpr int VEC = Group<T>::VEC;
+  constexpr int UN = kTopSpan / (kTopThreads * VEC);  // 4 (bf16) or 8 (fp32): 32 elements
+  extern __shared__ __align__(16) unsigned char smem[];
+  TopShared& s = *reinterpret_cast<TopShared*>(smem);
+  uint16_t* table = reinterpret_cast<uint16_t*>(smem + sizeof(TopShared));
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const long long grp = blockIdx.x / C;
+  const int t = threadIdx.x, lane = lane_id(), warp = t / kWarp;
+  const int items = p.W * p.slices;
+  const T* tag = nullptr;
+
+  if (!kBeam && p.lens) {  // a record's row that is not needed (the whole cluster leaves)
+    const int b = (int)(grp / p.P), i = (int)(grp - (long long)b * p.P);
+    const int len = p.lens[b];
+    const bool ok = len >= 0 && len <= p.P;
+    if (!ok || i >= len) {
+      if (rank == 0) {
+        for (int j = t; j < p.n; j += kTopThreads) write_slot<kBeam>(p, grp, j, 0, -1);
+        if (t == 0) {
+          p.out_lse[grp] = -INFINITY;
+          if (p.out_status) p.out_status[grp] = ok ? 0 : SV_REQ_BAD_DRAFT_LEN;
+        }
+      }
+      return;
+    }
+  }
+  if (t == 0) s.n_hits = s.n_cands = s.overflow = s.bad = 0;
+  // every CTA of the cluster has started (and cleared its counters) before any writes to another
+  if (C > 1) cluster.sync();
+
+  // One pass over each item.
+  for (int it = rank, mine = 0; it < items; it += C, ++mine) {
+    const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
+    const int e1 = min(e0 + p.slice, p.V);
+    const long long rowid = grp * p.W + w;
+    const T* row = reinterpret_cast<const T*>(p.logits) + rowid * (long long)p.V;
+    const float score = kBeam ? p.scores[rowid] : 0.f;
+    RunningSum r;
+    if (score != -INFINITY) {
+      for (int i = 0; i < p.iters; ++i) {
+        uint4 g[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          const int j = e0 + ((i * UN + u) * kTopThreads + t) * VEC;
+          g[u] = j < e1 ? load_group<T, kAligned>(row, j, p.V, p.span) : Lane<T, VEC>::pad();
+        }
+        const float gm = r.add(g, p.cc, tag);
+        table[(mine * p.iters + i) * kTopThreads + t] = up_bf16(gm);
+      }
+    } else {
+      for (int i = 0; i < p.iters; ++i)
+        table[(mine * p.iters + i) * kTopThreads + t] = 0xff80u;
+    }
+    const float2 wr = warp_running(r, p.cc);
+    const int fold = kTopThreads / p.upi;
+    float um = r.m;
+    for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
+    for (int c = 0; c < C; ++c) {
+      TopShared* to = C > 1 ? cluster.map_shared_rank(&s, c) : &s;
+      if (lane == 0) to->part[it][warp] = wr;
+      if ((t & (fold - 1)) == 0) to->unit[it * p.upi + t / fold] = um;
+    }
+  }
+  if (C > 1) cluster.sync(); else __syncthreads();
+
+  // Each row's log-sum-exp and offset (every CTA for itself).
+  const int parts = p.slices * kTopWarps;  // <= 64
+  for (int w = warp; w < p.W; w += kTopWarps) {
+    float m = -INFINITY;
+    const float2* pt = &s.part[w * p.slices][0];
+    for (int q = lane; q < parts; q += kWarp) m = max_nan(m, pt[q].x);
+    m = warp_max_nan(m);
+    double sum = 0.0;
+    for (int q = lane; q < parts; q += kWarp)
+      sum += (double)(pt[q].y * to_frame(pt[q].x, m, p.cc));
+    sum = warp_sum(sum);
+    if (lane == 0) {
+      const float score = kBeam ? p.scores[grp * p.W + w] : 0.f;
+      const bool dead = kBeam && score == -INFINITY;
+      const bool bad = !dead && (m != m || m == INFINITY || score != score || score == INFINITY);
+      if (bad) s.bad = 1;
+      const double lse = m == -INFINITY ? -INFINITY : (double)m / (double)p.T + log(sum);
+      s.lse[w] = lse;
+      s.off[w] = kBeam ? (dead || m == -INFINITY ? -INFINITY : (double)score - lse) : 0.0;
+    }
+  }
+  __syncthreads();
+  const bool bad = s.bad != 0;
+  if (!kBeam && rank == 0 && t == 0) {
+    p.out_lse[grp] = bad ? qnan() : (float)s.lse[0];
+    if (p.out_status) p.out_status[grp] = bad ? SV_REQ_BAD_LOGITS : 0;
+  }
+  if (kBeam && rank == 0 && t == 0 && p.out_status)
+    p.out_status[grp] = bad ? SV_REQ_BAD_LOGITS : 0;
+  if (bad) {  // the same in every CTA
+    if (rank == 0)
+      for (int j = t; j < p.n; j += kTopThreads) write_slot<kBeam>(p, grp, j, 0, -1);
+    return;
+  }
+
+  // The bound that n elements reach, and each row's lowest candidate logit.
+  const int units = items * p.upi;
+  if (kBeam) {
+    for (int u = t; u < units; u += kTopThreads) {
+      const float l = s.unit[u];
+      const double off = s.off[u / (p.upi * p.slices)];
+      s.unit[u] = l == -INFINITY || off == -INFINITY ? -INFINITY
+                                                     : __fadd_rd(__double2float_rd(off), l);
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+    const float b = unit_bound(s.unit, units, p.n);
+    if (lane == 0) s.bound = b;
+    for (int w = lane; w < p.W; w += kWarp) {
+      float thr = b;
+      if (kBeam) {
+        const double off = s.off[w];
+        // below it, off + l rounds below the bound (the slack covers the roundings)
+        thr = off == -INFINITY ? INFINITY
+              : b == -INFINITY ? -INFINITY
+                               : __double2float_rd(((double)b - off) -
+                                                   1e-7 * (fabs((double)b) + fabs(off)));
+      }
+      s.thr[w] = thr;
+    }
+  }
+  __syncthreads();
+
+  // The groups that reach it.
+  {
+    int mine = 0;
+    for (int it = rank; it < items; it += C, ++mine) {
+      const float thr = s.thr[it / p.slices];
+      for (int i = 0; i < p.iters; ++i) {
+        const int at = (mine * p.iters + i) * kTopThreads + t;
+        const float gm = of_bf16(table[at]);
+        if (gm >= thr && gm > -INFINITY) {
+          const int h = atomicAdd(&s.n_hits, 1);
+          if (h < kMaxHits) s.hit[h] = (unsigned)at;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  TopShared* lead = C > 1 ? cluster.map_shared_rank(&s, 0) : &s;
+  {
+    const int hits = s.n_hits;
+    if (hits > kMaxHits) {
+      if (t == 0) lead->overflow = 1;
+    } else {
+      for (int q = t; q < hits * UN; q += kTopThreads) {
+        const unsigned at = s.hit[q / UN];
+        const int u = q % UN;
+        const int ti = (int)(at % kTopThreads), mi = (int)(at / kTopThreads);
+        const int mine = mi / p.iters, i = mi - mine * p.iters;
+        const int it = rank + mine * C;
+        const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
+        const int e1 = min(e0 + p.slice, p.V);
+        const int j = e0 + ((i * UN + u) * kTopThreads + ti) * VEC;
+        if (j >= e1) continue;
+        const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
+        const uint4 g = load_group<T, kAligned>(row, j, p.V, p.span);
+        const float thr = s.thr[w];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float l = Lane<T, VEC>::get(g, e);
+          if (l >= thr && l > -INFINITY) {
+            const int o = atomicAdd(&lead->n_cands, 1);
+            if (o < kMaxCands) {
+              lead->key[o] = ordered(s.off[w] + (double)l);
+              lead->idx[o] = w * p.V + j + e;
+            }
+          }
+        }
+      }
+    }
+  }
+  if (C > 1) cluster.sync(); else __syncthreads();
+  if (rank != 0) return;
+
+  int count = s.n_cands;
+  if (s.overflow || count > kMaxCands) {
+    count = 0;
+    for (int w = 0; w < p.W; ++w) {
+      const double off = s.off[w];
+      if (off == -INFINITY) continue;
+      const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
+      const int got = select_row_slow<T>(s, row, p.V, p.n, off, w * p.V, count);
+      // keep the n best of the rows so far (at most 2 n <= 256 entries, one a thread)
+      const int total = count + got;
+      unsigned long long key = 0;
+      int idx = 0, r = p.n;
+      if (t < total) {
+        key = s.key[t];
+        idx = s.idx[t];
+        r = rank_of(s, total, key, idx);
+      }
+      __syncthreads();
+      if (r < p.n) {
+        s.key[r] = key;
+        s.idx[r] = idx;
+      }
+      count = min(total, p.n);
+      __syncthreads();
+    }
+  } else if (count > kRankAll) {
+    count = prune(s, count, p.n);
+  }
+  for (int i = t; i < count; i += kTopThreads) {
+    const int r = rank_of(s, count, s.key[i], s.idx[i]);
+    if (r < p.n) write_slot<kBeam>(p, grp, r, s.key[i], s.idx[i]);
+  }
+  for (int j = count + t; j < p.n; j += kTopThreads) write_slot<kBeam>(p, grp, j, 0, -1);
+}
+
+template <typename T, bool kAligned, bool kBeam>
+cudaError_t launch_top(const TopParams& p, long long groups, int C, cudaStream_t stream) {
+  static PerDevice once;
+  auto* fn = top_kernel<T, kAligned, kBeam>;
+  const cudaError_t err = per_device(once, nullptr, [&](int&) {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(TopShared) + kMaxTables * kTopThreads * 2);
+  });
+  if (err != cudaSuccess) return err;
+  const int per_cta = (p.W * p.slices + C - 1) / C;
+  const size_t smem = sizeof(TopShared) + (size_t)per_cta * p.iters * kTopThreads * 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(groups * C));
+  cfg.blockDim = dim3(kTopThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+template <bool kBeam>
+sv_status run_top(TopParams& p, sv_dtype dtype, long long groups, cudaStream_t stream) {
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return SV_ERR_CUDA;
+  // The cluster: 8 CTAs while the rows do not fill the GPU by themselves (or
+  // the row's group maxes need the shared memory of several), else one per row
+  // (beams: one per beam, up to 8).
+  int C = 1;
+  while (C < 8 && C < p.W) C *= 2;
+  while (C < 8 && (groups * C < 2LL * dev.sms ||
+                   ((long long)p.W * ((p.V + kTopSpan - 1) / kTopSpan) + C - 1) / C > kMaxTables))
+    C *= 2;
+  p.slices = C > p.W ? C / p.W : 1;
+  // no more slices than 256-element pieces
+  const int pieces = (p.V + 255) / 256;
+  p.slices = p.slices < pieces ? p.slices : pieces;
+  p.slice = (pieces + p.slices - 1) / p.slices * 256;
+  p.iters = (p.slice + kTopSpan - 1) / kTopSpan;
+  const int items = p.W * p.slices;
+  if (items > kMaxItems || (long long)((items + C - 1) / C) * p.iters > kMaxTables)
+    return SV_ERR_SHAPE;
+  p.upi = kTopThreads;
+  while (items * p.upi > kMaxUnits) p.upi /= 2;
+  const size_t esz = dtype == SV_BF16 ? 2 : 4;
+  const char* first = static_cast<const char*>(p.logits);
+  p.span.first = first;
+  p.span.last = first + (size_t)groups * p.W * (size_t)p.V * esz;
+  const bool aligned = ((uintptr_t)first & 15u) == 0 && ((size_t)p.V * esz) % 16 == 0;
+  cudaError_t err;
+  if (dtype == SV_BF16)
+    err = aligned ? launch_top<uint16_t, true, kBeam>(p, groups, C, stream)
+                  : launch_top<uint16_t, false, kBeam>(p, groups, C, stream);
+  else
+    err = aligned ? launch_top<float, true, kBeam>(p, groups, C, stream)
+                  : launch_top<float, false, kBeam>(p, groups, C, stream);
+  return err == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+sv_status spec_top_logits(const void* logits, int k, float temperature, const int32_t* lens,
+                          int32_t* out_ids, float* out_logits, float* out_lse,
+                          int32_t* out_status, sv_dtype dtype, int B, int P, int V,
+                          sv_stream_t stream) {
+  if (!(temperature > 0.f) || isinf(temperature)) return SV_ERR_TEMPERATURE;
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  if (B < 0 || B > SV_MAX_B || P < 1 || (long long)B * P > SV_MAX_ROWS || V < 1 || V > SV_MAX_V ||
+      k < 1 || k > SV_MAX_TOP)
+    return SV_ERR_SHAPE;
+  if (B == 0) return SV_OK;
+  if (!logits || !out_ids || !out_logits || !out_lse) return SV_ERR_NULL;
+  if ((uintptr_t)logits & (dtype == SV_BF16 ? 1u : 3u)) return SV_ERR_NULL;
+  TopParams p;
+  memset(&p, 0, sizeof p);
+  p.logits = logits;
+  p.lens = lens;
+  p.out_ids = out_ids;
+  p.out_values = out_logits;
+  p.out_lse = out_lse;
+  p.out_status = out_status;
+  p.P = P;
+  p.W = 1;
+  p.V = V;
+  p.n = k;
+  p.cc = exponent_scale(temperature);
+  p.T = temperature;
+  return run_top<false>(p, dtype, (long long)B * P, (cudaStream_t)stream);
+}
+
+sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out_tokens,
+                           int32_t* out_parents, float* out_scores, int32_t* out_status,
+                           sv_dtype dtype, int B, int W, int V, int n, sv_stream_t stream) {
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  if (B < 0 || B > SV_MAX_B || W < 1 || W > SV_MAX_BEAMS || V < 1 || V > SV_MAX_V || n < 1 ||
+      n > SV_MAX_TOP ||
+      (long long)((W + 7) / 8) * ((V + kTopSpan - 1) / kTopSpan) > kMaxTables)
+    return SV_ERR_SHAPE;
+  if (B == 0) return SV_OK;
+  if (!logits || !scores || !out_tokens || !out_parents || !out_scores) return SV_ERR_NULL;
+  if ((uintptr_t)logits & (dtype == SV_BF16 ? 1u : 3u)) return SV_ERR_NULL;
+  TopParams p;
+  memset(&p, 0, sizeof p);
+  p.logits = logits;
+  p.scores = scores;
+  p.out_ids = out_tokens;
+  p.out_parents = out_parents;
+  p.out_values = out_scores;
+  p.out_status = out_status;
+  p.P = 1;
+  p.W = W;
+  p.V = V;
+  p.n = n;
+  p.cc = 1.4426950408889634f;
+  p.T = 1.f;
+  return run_top<true>(p, dtype, B, (cudaStream_t)stream);
+}
+
+}  // extern "C"

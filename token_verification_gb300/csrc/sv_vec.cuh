@@ -1,0 +1,233 @@
+// sv_vec.cuh - rows of any alignment in 16-byte groups, ordered keys, and
+// cluster-wide shared memory: helpers of the top-logits, beam-selection and
+// distillation kernels.
+//
+// Those kernels cut a row by element index - group i holds elements i*VEC ..
+// i*VEC + VEC - 1 whatever the row's address - so that the order of every sum
+// follows from the row's contents alone: equal rows give equal sums, and equal
+// candidates of different beams stay equal.  A row that does not start on a
+// 16-byte boundary (odd vocabularies) is read as the two aligned 16-byte
+// words around each group, shifted together in registers.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "sv_common.cuh"
+
+namespace sv {
+namespace {
+
+namespace cg = cooperative_groups;
+
+// Bytes r .. r + 15 of the 32 bytes a, b (0 <= r < 16, r even).
+__device__ __forceinline__ uint4 shift_pair(const uint4& a, const uint4& b, uint32_t r) {
+  uint32_t w0 = a.x, w1 = a.y, w2 = a.z, w3 = a.w, w4 = b.x;
+  if (r & 8u) {
+    w0 = a.z; w1 = a.w; w2 = b.x; w3 = b.y; w4 = b.z;
+  }
+  if (r & 4u) {
+    const uint32_t w5 = (r & 8u) ? b.w : b.y;
+    w0 = w1; w1 = w2; w2 = w3; w3 = w4; w4 = w5;
+  }
+  if (r & 2u) {
+    w0 = __funnelshift_r(w0, w1, 16);
+    w1 = __funnelshift_r(w1, w2, 16);
+    w2 = __funnelshift_r(w2, w3, 16);
+    w3 = __funnelshift_r(w3, w4, 16);
+  }
+  return make_uint4(w0, w1, w2, w3);
+}
+
+// A tensor of logit rows: [first, last) is its memory, read nowhere else.
+struct RowSpan {
+  const char* first;
+  const char* last;
+};
+
+template <typename T>
+struct Group {
+  static constexpr int VEC = 16 / (int)sizeof(T);
+};
+
+__device__ __forceinline__ void put(uint4& v, int e, uint16_t x) {
+  uint32_t* w = e < 2 ? &v.x : e < 4 ? &v.y : e < 6 ? &v.z : &v.w;
+  *w = (e & 1) ? (*w & 0x0000ffffu) | ((uint32_t)x << 16) : (*w & 0xffff0000u) | x;
+}
+__device__ __forceinline__ void put(uint4& v, int e, float x) {
+  uint32_t* w = e == 0 ? &v.x : e == 1 ? &v.y : e == 2 ? &v.z : &v.w;
+  *w = __float_as_uint(x);
+}
+
+__device__ __forceinline__ uint4 load128(const void* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+
+// Elements j .. j + VEC - 1 of a row of V elements, -inf past its end.
+// kAligned: every row of the tensor starts on a 16-byte boundary.
+template <typename T, bool kAligned>
+__device__ __forceinline__ uint4 load_group(const T* row, int j, int V, const RowSpan& span) {
+  constexpr int VEC = Group<T>::VEC;
+  if (j + VEC <= V) {
+    const char* p = reinterpret_cast<const char*>(row + j);
+    if (kAligned) return load128(p);
+    const uint32_t r = (uint32_t)(uintptr_t)p & 15u;
+    if (r == 0) return load128(p);
+    const char* a = p - r;
+    if (a >= span.first && a + 32 <= span.last) return shift_pair(load128(a), load128(a + 16), r);
+  }
+  uint4 v = Lane<T, VEC>::pad();
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+    if (j + e < V) put(v, e, row[j + e]);
+  return v;
+}
+
+// Unsigned keys in the order of the values (-0.0 counts as +0.0).
+__device__ __forceinline__ uint32_t ordered(float v) {
+  uint32_t b = __float_as_uint(v);
+  if (b == 0x80000000u) b = 0u;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float of_ordered(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+__device__ __forceinline__ unsigned long long ordered(double v) {
+  unsigned long long b = (unsigned long long)__double_as_longlong(v);
+  if (b == 0x8000000000000000ull) b = 0ull;
+  return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double of_ordered(unsigned long long k) {
+  return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
+}
+
+// Weights are 2^((l - m) c) in the frame of a max m: the difference first, so
+// that rows of any magnitude (masks of the type's lowest value included) keep
+// their precision; fma(l, c, -m c) would carry the rounding of m c into every
+// exponent.  The frame of a part without a finite element is 0 (its weights
+// are 2^-inf = 0).
+__device__ __forceinline__ float frame_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+// c = log2(e) / T (a denormal T must not make it infinite: 0 * inf).
+inline float exponent_scale(float T) {
+  const double c = 1.4426950408889634 / (double)T;
+  return c < (double)FLT_MAX ? (float)c : FLT_MAX;
+}
+
+// Moves a sum from the frame of a to that of b >= a (an empty part has sum 0).
+__device__ __forceinline__ float to_frame(float a, float b, float c) {
+  return ex2(fminf(frame_of(a) - frame_of(b), 0.f) * c);
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// NaN-propagating max of N groups.
+template <int N>
+__device__ __forceinline__ float groups_max(const uint4 (&g)[N], const uint16_t*) {
+  uint32_t m[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    m[k] = bf16x2_max_nan(bf16x2_max_nan(g[k].x, g[k].y), bf16x2_max_nan(g[k].z, g[k].w));
+#pragma unroll
+  for (int o = N / 2; o > 0; o /= 2)
+#pragma unroll
+    for (int k = 0; k < o; ++k) m[k] = bf16x2_max_nan(m[k], m[k + o]);
+  return max_nan(bf16_lo(m[0]), bf16_hi(m[0]));
+}
+template <int N>
+__device__ __forceinline__ float groups_max(const uint4 (&g)[N], const float*) {
+  float m[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    m[k] = max_nan(max_nan(__uint_as_float(g[k].x), __uint_as_float(g[k].y)),
+                   max_nan(__uint_as_float(g[k].z), __uint_as_float(g[k].w)));
+#pragma unroll
+  for (int o = N / 2; o > 0; o /= 2)
+#pragma unroll
+    for (int k = 0; k < o; ++k) m[k] = max_nan(m[k], m[k + o]);
+  return m[0];
+}
+
+// Sum of 2^((l - m) c) over N groups, in packed pairs.
+template <int N>
+__device__ __forceinline__ float groups_sum(const uint4 (&g)[N], float c, float m,
+                                            const uint16_t*) {
+  const f32x2 c2 = pack2(c, c), nm2 = pack2(-m, -m);
+  f32x2 acc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc[q] = pack2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint32_t w[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float a0, a1;
+      unpack2(mul2(add2(pack2(bf16_lo(w[q]), bf16_hi(w[q])), nm2), c2), a0, a1);
+      acc[q] = add2(acc[q], pack2(ex2(a0), ex2(a1)));
+    }
+  }
+  float s0, s1, s2, s3;
+  unpack2(add2(acc[0], acc[1]), s0, s1);
+  unpack2(add2(acc[2], acc[3]), s2, s3);
+  return (s0 + s1) + (s2 + s3);
+}
+template <int N>
+__device__ __forceinline__ float groups_sum(const uint4 (&g)[N], float c, float m,
+                                            const float*) {
+  const f32x2 c2 = pack2(c, c), nm2 = pack2(-m, -m);
+  f32x2 acc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc[q] = pack2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    float a0, a1, a2, a3;
+    unpack2(mul2(add2(pack2(__uint_as_float(g[k].x), __uint_as_float(g[k].y)), nm2), c2), a0,
+            a1);
+    unpack2(mul2(add2(pack2(__uint_as_float(g[k].z), __uint_as_float(g[k].w)), nm2), c2), a2,
+            a3);
+    acc[(2 * k) & 3] = add2(acc[(2 * k) & 3], pack2(ex2(a0), ex2(a1)));
+    acc[(2 * k + 1) & 3] = add2(acc[(2 * k + 1) & 3], pack2(ex2(a2), ex2(a3)));
+  }
+  float s0, s1, s2, s3;
+  unpack2(add2(acc[0], acc[1]), s0, s1);
+  unpack2(add2(acc[2], acc[3]), s2, s3);
+  return (s0 + s1) + (s2 + s3);
+}
+
+// A running softmax sum: s = sum of 2^((l - m) c) over the elements so far,
+// m their max (NaN once a NaN was seen).
+struct RunningSum {
+  float m = -INFINITY, s = 0.f;
+  template <int N, typename T>
+  __device__ __forceinline__ float add(const uint4 (&g)[N], float c, const T* tag) {
+    const float gm = groups_max(g, tag);
+    const float mn = max_nan(m, gm);
+    s = s * to_frame(m, mn, c) + groups_sum(g, c, frame_of(mn), tag);
+    m = mn;
+    return gm;
+  }
+};
+
+// The warp's running sums as one (the lanes' frames moved to the warp max's).
+__device__ __forceinline__ float2 warp_running(const RunningSum& r, float c) {
+  const float wm = warp_max_nan(r.m);
+  return make_float2(wm, warp_sum(r.s * to_frame(r.m, wm, c)));
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+}  // namespace
+}  // namespace sv
