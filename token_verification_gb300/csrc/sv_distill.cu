@@ -55,11 +55,14 @@ struct DistillShared {
   float4 part[kMaxCluster];      // each CTA's {max, sum, -, -} over its slice without the record
   float2 warp_part[kDistillWarps];
   int id[SV_MAX_TOP];            // the record (-1: unused)
+  float t[SV_MAX_TOP];           // its logits (-inf: unused)
   float p[SV_MAX_TOP];           // its teacher probabilities
-  float lp[SV_MAX_TOP];          // their logarithms
   float sv[SV_MAX_TOP];          // the student's logits at its tokens
   int bad, used;
-  float p_rest;
+  double norm;                   // the teacher's log-sum-exp: log p_j = t_j / T - norm
+  double p_rest;
+  float m, M;                    // the student's max outside the record, and over all
+  double S, Z;                   // its sums there, in the frames of m and M
   float4 stat;                   // {m, beta, M, 1/Z}
 };
 
@@ -142,7 +145,7 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     const int id = p.top_ids[row * p.k + t];
     const float v = p.top_logits[row * p.k + t];
     s.id[t] = id;
-    s.lp[t] = id < 0 ? -INFINITY : v;
+    s.t[t] = id < 0 ? -INFINITY : v;
     if (id < -1 || id >= p.V) atomicOr(&s.bad, SV_REQ_BAD_TOKEN);
     if (id >= 0) {
       atomicAdd(&s.used, 1);
@@ -156,12 +159,12 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
       if (s.id[j] == s.id[t]) atomicOr(&s.bad, SV_REQ_BAD_TOKEN);
   if (t < kWarp) {
     constexpr int kPer = SV_MAX_TOP / kWarp;
-    double x[kPer];  // log p (with the log-sum-exp) or t / T
+    double x[kPer];
     float m = -INFINITY;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int j = q * kWarp + t;
-      const float v = j < p.k ? s.lp[j] : -INFINITY;
+      const float v = j < p.k ? s.t[j] : -INFINITY;
       x[q] = (double)v * p.inv_t;
       m = fmaxf(m, v);
     }
@@ -169,26 +172,46 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     if (!p.top_lse) {
       m = warp_max(m);
       const double mt = m == -INFINITY ? 0.0 : (double)m * p.inv_t;
-      float z = 0.f;
+      double z = 0.0;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) z += expf((float)(x[q] - mt));
-      norm = mt + (double)logf(warp_sum(z));
+      for (int q = 0; q < kPer; ++q) z += (double)expf((float)(x[q] - mt));
+      norm = mt + log(warp_sum(z));
     }
     double sum = 0.0;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int j = q * kWarp + t;
-      const float lp = x[q] == -INFINITY ? -INFINITY : (float)(x[q] - norm);
-      const float pj = lp == -INFINITY ? 0.f : expf(lp);
-      if (j < p.k) {
-        s.lp[j] = lp;
-        s.p[j] = pj;
-      }
+      const float pj = x[q] == -INFINITY ? 0.f : expf((float)(x[q] - norm));
+      if (j < p.k) s.p[j] = pj;
       sum += (double)pj;
     }
     sum = warp_sum(sum);
-    if (t == 0) s.p_rest = p.top_lse && s.used < p.V ? (float)fmax(0.0, 1.0 - sum) : 0.f;
+    if (t == 0) {
+      s.norm = norm;
+      s.p_rest = p.top_lse && s.used < p.V ? fmax(0.0, 1.0 - sum) : 0.0;
+    }
   }
+}
+
+// The loss of a row, by one warp.  The logarithms' differences are taken in 64
+// bits: where student and teacher agree the loss is far below its terms.
+__device__ double row_loss(const DistillShared& s, const DistillParams& p) {
+  const int lane = lane_id();
+  const double mine = log(lane == 0 ? s.Z : lane == 1 ? s.S : s.p_rest > 0.0 ? s.p_rest : 1.0);
+  const double lz = __shfl_sync(0xffffffffu, mine, 0), ls = __shfl_sync(0xffffffffu, mine, 1),
+               lr = __shfl_sync(0xffffffffu, mine, 2);
+  double loss = 0.0;
+  for (int j = lane; j < p.k; j += kWarp)
+    if (s.p[j] > 0.f) {
+      const double log_q = ((double)s.sv[j] - (double)s.M) * p.inv_t - lz;
+      loss += (double)s.p[j] * (((double)s.t[j] * p.inv_t - s.norm) - log_q);
+    }
+  loss = warp_sum(loss);
+  if (s.p_rest > 0.0)
+    loss += s.m == -INFINITY
+                ? INFINITY
+                : s.p_rest * (lr - (ls + ((double)s.m - (double)s.M) * p.inv_t - lz));
+  return loss;
 }
 
 template <typename T, bool kAligned, int kMode>
@@ -309,7 +332,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       // the rest: its max m and sum S over the cluster's slices
       const float4 v = lane < C ? s.part[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
       const float m = warp_max_nan(v.x);
-      const float S = warp_sum(v.y * to_frame(v.x, m, p.cc));
+      const double S = warp_sum((double)(v.y * to_frame(v.x, m, p.cc)));
       // the record, and both together in the frame of M
       constexpr int kPer = SV_MAX_TOP / kWarp;
       float x[kPer], M = -INFINITY;
@@ -323,37 +346,35 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       }
       M = fmaxf(warp_max(M), m);
       wrong = __any_sync(0xffffffffu, wrong) || M == -INFINITY;
-      float z = 0.f;
+      double z = 0.0;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) z += ex2((x[q] - M) * p.cc);
-      const float rest = m == -INFINITY ? 0.f : S * ex2((m - M) * p.cc);
-      const float Z = warp_sum(z) + rest;
-      const float q_rest = rest / Z;
-      const float lz = logf(Z);
-      const float p_rest = s.p_rest;
-      double loss = 0.0;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int j = q * kWarp + lane;
-        if (j < p.k && s.p[j] > 0.f)
-          loss += (double)(s.p[j] * (s.lp[j] - (kLn2 * ((x[q] - M) * p.cc) - lz)));
-      }
-      loss = warp_sum(loss);
-      if (p_rest > 0.f)  // log q_rest = log S + (m - M) / T - log Z, whatever underflowed
-        loss += m == -INFINITY
-                    ? INFINITY
-                    : (double)(p_rest * (logf(p_rest) - (logf(S) + kLn2 * ((m - M) * p.cc) - lz)));
+      for (int q = 0; q < kPer; ++q) z += (double)ex2((x[q] - M) * p.cc);
+      const double rest = m == -INFINITY ? 0.0 : S * (double)ex2((m - M) * p.cc);
+      const double Z = warp_sum(z) + rest;
       if (lane == 0) {
-        const float beta = m == -INFINITY ? 0.f : (q_rest - p_rest) / S;
-        s.stat = make_float4(frame_of(m), beta, M, wrong ? qnan() : 1.f / Z);
+        const float beta = m == -INFINITY ? 0.f : (float)((rest / Z - s.p_rest) / S);
+        s.m = m;
+        s.M = M;
+        s.S = m == -INFINITY ? 1.0 : S;
+        s.Z = Z;
+        s.stat = make_float4(frame_of(m), beta, M, wrong ? qnan() : (float)(1.0 / Z));
         if (rank == 0) {
-          p.out_loss[row] = wrong ? qnan() : (float)loss;
           if (p.out_stats) p.out_stats[row] = wrong ? make_float4(0.f, 0.f, 0.f, qnan()) : s.stat;
           if (p.out_status) p.out_status[row] = wrong ? SV_REQ_BAD_LOGITS : 0;
+          if (wrong) p.out_loss[row] = qnan();
         }
       }
     }
-    if (kMode == kLoss) return;
+    if (kMode == kLoss) {
+      if (rank == 0 && warp == 0) {
+        __syncwarp();
+        if (s.stat.w == s.stat.w) {
+          const double loss = row_loss(s, p);
+          if (lane == 0) p.out_loss[row] = (float)loss;
+        }
+      }
+      return;
+    }
     __syncthreads();
   }
 
@@ -378,6 +399,10 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
   }
   __syncthreads();
   store_slice(grad, slice, bytes);
+  if (kMode == kLossGrad && rank == 0 && warp == 0) {  // nothing waits for the loss here
+    const double loss = row_loss(s, p);
+    if (lane == 0) p.out_loss[row] = (float)loss;
+  }
 }
 
 constexpr int kSharedHead = (int)(sizeof(DistillShared) + 15) / 16 * 16;
