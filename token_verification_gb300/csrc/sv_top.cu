@@ -32,11 +32,10 @@ namespace {
 
 constexpr int kTopThreads = 256;
 constexpr int kTopWarps = kTopThreads / kWarp;
-constexpr int kTopSpan = 8192;        // elements a CTA reads per iteration
+constexpr int kTopSpan = 8192;        // elements of a CTA's iteration: 32 a thread
 constexpr int kMaxItems = 64;         // (row, slice) items per cluster
-constexpr int kMaxUnits = 512;        // thread-max units per cluster (4 per kept element)
-constexpr int kMaxHits = 1024;        // 32-element groups a CTA reads again
-constexpr int kMaxCands = 2048;       // candidates of a cluster
+constexpr int kMaxUnits = 512;        // units per cluster
+constexpr int kMaxCands = 1024;       // candidates of a cluster, 32-element groups of a CTA
 constexpr int kMaxTables = 320;       // iterations of a CTA over its items: 512 bytes each
 constexpr int kRankAll = 384;         // lists longer than this are cut to the bound first
 
@@ -60,18 +59,19 @@ struct TopParams {
   RowSpan span;
 };
 
-struct TopShared {
+struct alignas(16) TopShared {
+  unsigned long long key[kMaxCands];  // candidates; record: (ordered logit, ~index), a total
+                                      // order; beams: the ordered score, idx = w * V + v
+  int idx[kMaxCands];
+  int rank[kMaxCands];                // until the list is sorted: the groups to read again
   float2 part[kMaxItems][kTopWarps];  // per item and warp: {max, sum of 2^((l - max) c)}
   float unit[kMaxUnits];              // unit maxes, item by item
-  double off[SV_MAX_BEAMS];           // score - lse of each row
-  double lse[SV_MAX_BEAMS];
+  double off[SV_MAX_BEAMS];           // beams: score - lse of each row (-inf: no candidates)
+  float off_down[SV_MAX_BEAMS];       // the same rounded down
   float thr[SV_MAX_BEAMS];            // the lowest logit a candidate of the row can have
-  unsigned hit[kMaxHits];
-  unsigned long long key[kMaxCands];  // candidates: ordered score, flat index w * V + v
-  int idx[kMaxCands];
+  float lse;                          // record
   unsigned hist[256];
   int n_hits, n_cands, overflow, bad, pick[4];
-  float bound;
 };
 
 // The upper 16 bits of v rounded up: a bf16 value >= v (v itself for bf16).
@@ -79,33 +79,46 @@ __device__ __forceinline__ uint16_t up_bf16(float v) {
   const uint32_t b = __float_as_uint(v);
   return (uint16_t)((b & 0x80000000u) ? b >> 16 : (b + 0xffffu) >> 16);
 }
-__device__ __forceinline__ float of_bf16(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 
-// The n-th largest of the cluster's unit bounds to 16 bits (rounded down), by
-// bisection on ordered keys; -inf when fewer than n are finite.  One warp.
+// The n-th largest of kPer * 32 units to 16 bits (rounded down), by bisection
+// on ordered keys below their common prefix; -inf when fewer than n are
+// finite.  One warp.
+template <int kPer>
 __device__ float unit_bound(const float* unit, int units, int n) {
-  constexpr int kPer = kMaxUnits / kWarp;
-  uint32_t k[kPer];
+  uint32_t k[kPer], hi = 0, lo = 0xffffu;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = j * kWarp + lane_id();
     const float v = i < units ? unit[i] : -INFINITY;
-    k[j] = v > -INFINITY ? ordered(v) >> 16 : 0u;  // -inf (key 0x007f) sorts below every value
+    k[j] = v > -INFINITY ? ordered(v) >> 16 : 0u;  // below every finite value's key
+    hi = max(hi, k[j]);
+    lo = min(lo, k[j]);
   }
-  uint32_t t = 0;
-  for (uint32_t bit = 0x8000u; bit; bit >>= 1) {
-    const uint32_t at = t | bit;
-    int c = 0;
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  const int top = 32 - __clz(hi ^ lo);  // bits below the common prefix
+  uint32_t t = top ? hi >> top << top : hi;
+  for (int b = top - 1; b >= 0; --b) {
+    const uint32_t at = t | (1u << b);
+    unsigned c = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) c += k[j] >= at ? 1 : 0;
-    if ((int)__reduce_add_sync(0xffffffffu, (unsigned)c) >= n) t = at;
+    for (int j = 0; j < kPer; ++j) c += k[j] >= at ? 1u : 0u;
+    if ((int)__reduce_add_sync(0xffffffffu, c) >= n) t = at;
   }
-  return t ? of_ordered(t << 16) : -INFINITY;
+  // fewer than n units in all, or fewer than n finite ones
+  return units >= n && t ? of_ordered(t << 16) : -INFINITY;
+}
+
+template <bool kBeam>
+__device__ __forceinline__ void set_candidate(TopShared& s, int o, float l, double off, int idx) {
+  s.key[o] = kBeam ? ordered(off + (double)l)
+                   : ((unsigned long long)ordered(l) << 32) | (uint32_t)~idx;
+  s.idx[o] = idx;
 }
 
 // One row's n largest finite elements by radix descent, appended to the list
 // from `at` on (a whole-CTA call); returns how many.
-template <typename T>
+template <typename T, bool kBeam>
 __device__ int select_row_slow(TopShared& s, const T* row, int V, int n, double off, int base,
                                int at) {
   const int t = threadIdx.x;
@@ -154,23 +167,50 @@ __device__ int select_row_slow(TopShared& s, const T* row, int V, int n, double 
     const unsigned long long k = key_of(j0 + t);
     if (k != 0 && k >= cut) {
       const int o = atomicAdd(&s.pick[3], 1);
-      s.key[o] = ordered(off + (double)load_logit(row, j0 + t));
-      s.idx[o] = base + j0 + t;
+      set_candidate<kBeam>(s, o, load_logit(row, j0 + t), off, base + j0 + t);
     }
   }
   __syncthreads();
   return s.pick[3] - at;
 }
 
-// How many of the list's entries come before entry i.
-__device__ __forceinline__ int rank_of(const TopShared& s, int count, unsigned long long key,
-                                       int idx) {
-  int r = 0;
-  for (int j = 0; j < count; ++j) {
-    const unsigned long long kj = s.key[j];
-    r += (kj > key || (kj == key && s.idx[j] < idx)) ? 1 : 0;
+// Whether entry j of the list comes before an entry of (key, idx).
+template <bool kBeam>
+__device__ __forceinline__ bool before(const TopShared& s, int j, unsigned long long key, int idx) {
+  const unsigned long long kj = s.key[j];
+  return kj > key || (kBeam && kj == key && s.idx[j] < idx);
+}
+
+// rank[i] = the number of entries that come before entry i, i < count: the
+// whole CTA, each entry's comparisons shared by as many threads as there are
+// warps for all entries.
+template <bool kBeam>
+__device__ void rank_list(TopShared& s, int count) {
+  const int t = threadIdx.x;
+  for (int i = t; i < count; i += kTopThreads) s.rank[i] = 0;
+  __syncthreads();
+  const int width = (count + kWarp - 1) / kWarp * kWarp;
+  if (width <= kTopThreads / 2) {
+    const int ways = kTopThreads / width, way = t / width, i = t - way * width;
+    if (way < ways && i < count) {
+      const unsigned long long key = s.key[i];
+      const int idx = s.idx[i];
+      int r = 0;
+#pragma unroll 4
+      for (int j = way; j < count; j += ways) r += before<kBeam>(s, j, key, idx) ? 1 : 0;
+      atomicAdd(&s.rank[i], r);
+    }
+  } else {
+    for (int i = t; i < count; i += kTopThreads) {
+      const unsigned long long key = s.key[i];
+      const int idx = s.idx[i];
+      int r = 0;
+#pragma unroll 4
+      for (int j = 0; j < count; ++j) r += before<kBeam>(s, j, key, idx) ? 1 : 0;
+      s.rank[i] = r;
+    }
   }
-  return r;
+  __syncthreads();
 }
 
 // Cuts the list to the entries at or above its n-th largest 32-bit key prefix.
@@ -202,7 +242,7 @@ __device__ int prune(TopShared& s, int count, int n) {
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < kPer; ++q)
-    if (k[q] != 0 && (uint32_t)(k[q] >> 32) >= t) {
+    if (q * kTopThreads + threadIdx.x < count && (uint32_t)(k[q] >> 32) >= t) {
       const int o = atomicAdd(&s.pick[1], 1);
       s.key[o] = k[q];
       s.idx[o] = ix[q];
@@ -218,15 +258,52 @@ __device__ __forceinline__ void write_slot(const TopParams& p, long long grp, in
   const int w = kBeam && idx >= 0 ? idx / p.V : 0;
   p.out_ids[o] = idx < 0 ? -1 : idx - w * p.V;
   if (kBeam) p.out_parents[o] = idx < 0 ? -1 : w;
-  p.out_values[o] = idx < 0 ? -INFINITY : (float)of_ordered(key);
+  p.out_values[o] = idx < 0 ? -INFINITY
+                    : kBeam ? (float)of_ordered(key)
+                            : of_ordered((uint32_t)(key >> 32));
+}
+
+// A warp's sum as hi + lo, the additions' roundings kept in lo.
+__device__ __forceinline__ float2 warp_sum_pair(float x) {
+  float hi = x, lo = 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, hi, o), yl = __shfl_xor_sync(0xffffffffu, lo, o);
+    const float sum = __fadd_rn(hi, y);
+    // both lanes of a pair take the larger first: the same rounding in each
+    const float a = fmaxf(hi, y), b = fminf(hi, y);
+    lo = __fadd_rn(__fadd_rn(lo, yl), __fadd_rn(b, -__fadd_rn(sum, -a)));
+    hi = sum;
+  }
+  return make_float2(hi, lo);
+}
+
+// log(hi + lo) as an exact multiple of the leading bits of ln 2 plus a float
+// below 0.36 in size: good to about 5e-8 without 64-bit logarithms, which
+// cost microseconds here.  1 <= hi < 2^31.
+__device__ __forceinline__ float2 log_pair(float2 s) {
+  const uint32_t b = __float_as_uint(s.x);
+  int e = (int)(b >> 23) - 127;
+  float f = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);  // [1, 2)
+  if (f > 1.41421356f) {
+    f *= 0.5f;
+    e += 1;
+  }
+  const float scale = __uint_as_float((uint32_t)(127 - e) << 23);
+  // ln 2 = 0.693145751953125 (15 bits) + 1.42860682030941723e-6
+  const float hi = (float)e * 0.693145751953125f;
+  return make_float2(hi, logf(f) + fmaf((float)e, 1.42860682e-6f, s.y * scale / f));
 }
 
 template <typename T, bool kAligned, bool kBeam>
 __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) {
   constexpr int VEC = Group<T>::VEC;
-  constexpr int UN = kTopSpan / (kTopThreads * VEC);  // 4 (bf16) or 8 (fp32): 32 elements
+  constexpr int UN = 4;                                        // 16-byte groups per load batch
+  constexpr int kBatches = kTopSpan / (kTopThreads * VEC * UN);  // 1 (bf16) or 2 per iteration
+  constexpr int kGroups = UN * kBatches;                       // of a table entry: 32 elements
   extern __shared__ __align__(16) unsigned char smem[];
   TopShared& s = *reinterpret_cast<TopShared*>(smem);
+  // per iteration over this CTA's items, the thread's 32 elements' max
   uint16_t* table = reinterpret_cast<uint16_t*>(smem + sizeof(TopShared));
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -251,73 +328,91 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
     }
   }
   if (t == 0) s.n_hits = s.n_cands = s.overflow = s.bad = 0;
-  // every CTA of the cluster has started (and cleared its counters) before any writes to another
-  if (C > 1) cluster.sync();
+  // no CTA writes into another's shared memory before that one has started
+  if (C > 1) cluster_arrive();
 
   // One pass over each item.
+  const int fold = kTopThreads / p.upi;
   for (int it = rank, mine = 0; it < items; it += C, ++mine) {
     const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
     const int e1 = min(e0 + p.slice, p.V);
     const long long rowid = grp * p.W + w;
     const T* row = reinterpret_cast<const T*>(p.logits) + rowid * (long long)p.V;
-    const float score = kBeam ? p.scores[rowid] : 0.f;
+    uint16_t* mine_table = table + mine * p.iters * kTopThreads + t;
+    const bool live = !kBeam || p.scores[rowid] != -INFINITY;
     RunningSum r;
-    if (score != -INFINITY) {
-      for (int i = 0; i < p.iters; ++i) {
-        uint4 g[UN];
+    if (live) {
+      // two register buffers: a batch's loads are in flight while the one
+      // before it is reduced
+      uint4 g0[UN], g1[UN];
+      auto load = [&](uint4(&g)[UN], int i) {
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
           const int j = e0 + ((i * UN + u) * kTopThreads + t) * VEC;
           g[u] = j < e1 ? load_group<T, kAligned>(row, j, p.V, p.span) : Lane<T, VEC>::pad();
         }
-        const float gm = r.add(g, p.cc, tag);
-        table[(mine * p.iters + i) * kTopThreads + t] = up_bf16(gm);
+      };
+      const int batches = p.iters * kBatches;
+      load(g0, 0);
+      for (int i = 0; i < batches; i += 2) {
+        if (i + 1 < batches) load(g1, i + 1);
+        float gm = r.add(g0, p.cc, tag);
+        if (kBatches == 1) mine_table[i * kTopThreads] = up_bf16(gm);
+        if (i + 1 >= batches) break;
+        if (i + 2 < batches) load(g0, i + 2);
+        const float gm1 = r.add(g1, p.cc, tag);
+        if (kBatches == 1) mine_table[(i + 1) * kTopThreads] = up_bf16(gm1);
+        else mine_table[i / 2 * kTopThreads] = up_bf16(max_nan(gm, gm1));
       }
     } else {
-      for (int i = 0; i < p.iters; ++i)
-        table[(mine * p.iters + i) * kTopThreads + t] = 0xff80u;
+      for (int i = 0; i < p.iters; ++i) mine_table[i * kTopThreads] = 0xff80u;
     }
     const float2 wr = warp_running(r, p.cc);
-    const int fold = kTopThreads / p.upi;
     float um = r.m;
     for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
+    if (C > 1 && mine == 0) cluster_wait();
     for (int c = 0; c < C; ++c) {
       TopShared* to = C > 1 ? cluster.map_shared_rank(&s, c) : &s;
       if (lane == 0) to->part[it][warp] = wr;
       if ((t & (fold - 1)) == 0) to->unit[it * p.upi + t / fold] = um;
     }
   }
-  if (C > 1) cluster.sync(); else __syncthreads();
+  if (C > 1) {
+    if (rank >= items) cluster_wait();
+    cluster.sync();
+  } else {
+    __syncthreads();
+  }
 
   // Each row's log-sum-exp and offset (every CTA for itself).
   const int parts = p.slices * kTopWarps;  // <= 64
   for (int w = warp; w < p.W; w += kTopWarps) {
-    float m = -INFINITY;
     const float2* pt = &s.part[w * p.slices][0];
-    for (int q = lane; q < parts; q += kWarp) m = max_nan(m, pt[q].x);
-    m = warp_max_nan(m);
-    double sum = 0.0;
-    for (int q = lane; q < parts; q += kWarp)
-      sum += (double)(pt[q].y * to_frame(pt[q].x, m, p.cc));
-    sum = warp_sum(sum);
+    const float2 a = lane < parts ? pt[lane] : make_float2(-INFINITY, 0.f);
+    const float2 b = lane + kWarp < parts ? pt[lane + kWarp] : make_float2(-INFINITY, 0.f);
+    const float m = warp_max_nan(max_nan(a.x, b.x));
+    const float2 sum = warp_sum_pair(a.y * to_frame(a.x, m, p.cc) + b.y * to_frame(b.x, m, p.cc));
     if (lane == 0) {
+      const float2 l = log_pair(sum);
       const float score = kBeam ? p.scores[grp * p.W + w] : 0.f;
       const bool dead = kBeam && score == -INFINITY;
-      const bool bad = !dead && (m != m || m == INFINITY || score != score || score == INFINITY);
-      if (bad) s.bad = 1;
-      const double lse = m == -INFINITY ? -INFINITY : (double)m / (double)p.T + log(sum);
-      s.lse[w] = lse;
-      s.off[w] = kBeam ? (dead || m == -INFINITY ? -INFINITY : (double)score - lse) : 0.0;
+      if (!dead && (m != m || m == INFINITY || score != score || score == INFINITY)) s.bad = 1;
+      if (kBeam) {
+        double off = -INFINITY;
+        if (!dead && m != -INFINITY) off = ((double)score - (double)m) - ((double)l.x + (double)l.y);
+        s.off[w] = off;
+        s.off_down[w] = __double2float_rd(off);
+      } else {
+        s.lse = m == -INFINITY ? -INFINITY : m / p.T + (l.x + l.y);
+      }
     }
   }
   __syncthreads();
   const bool bad = s.bad != 0;
-  if (!kBeam && rank == 0 && t == 0) {
-    p.out_lse[grp] = bad ? qnan() : (float)s.lse[0];
+  if (rank == 0 && t == 0) {
+    if (!kBeam) p.out_lse[grp] = bad ? qnan() : s.lse;
     if (p.out_status) p.out_status[grp] = bad ? SV_REQ_BAD_LOGITS : 0;
   }
-  if (kBeam && rank == 0 && t == 0 && p.out_status)
-    p.out_status[grp] = bad ? SV_REQ_BAD_LOGITS : 0;
   if (bad) {  // the same in every CTA
     if (rank == 0)
       for (int j = t; j < p.n; j += kTopThreads) write_slot<kBeam>(p, grp, j, 0, -1);
@@ -328,77 +423,81 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
   const int units = items * p.upi;
   if (kBeam) {
     for (int u = t; u < units; u += kTopThreads) {
-      const float l = s.unit[u];
-      const double off = s.off[u / (p.upi * p.slices)];
-      s.unit[u] = l == -INFINITY || off == -INFINITY ? -INFINITY
-                                                     : __fadd_rd(__double2float_rd(off), l);
+      const float l = s.unit[u], off = s.off_down[u / (p.upi * p.slices)];
+      s.unit[u] = l == -INFINITY || off == -INFINITY ? -INFINITY : __fadd_rd(off, l);
     }
     __syncthreads();
   }
   if (warp == 0) {
-    const float b = unit_bound(s.unit, units, p.n);
-    if (lane == 0) s.bound = b;
+    const float b = units <= 64    ? unit_bound<2>(s.unit, units, p.n)
+                    : units <= 256 ? unit_bound<8>(s.unit, units, p.n)
+                                   : unit_bound<16>(s.unit, units, p.n);
     for (int w = lane; w < p.W; w += kWarp) {
-      float thr = b;
+      // -inf never passes: at least the lowest finite value
+      float thr = fmaxf(b, -FLT_MAX);
       if (kBeam) {
         const double off = s.off[w];
         // below it, off + l rounds below the bound (the slack covers the roundings)
         thr = off == -INFINITY ? INFINITY
-              : b == -INFINITY ? -INFINITY
-                               : __double2float_rd(((double)b - off) -
-                                                   1e-7 * (fabs((double)b) + fabs(off)));
+              : b == -INFINITY ? -FLT_MAX
+                               : fmaxf(-FLT_MAX,
+                                       __double2float_rd(((double)b - off) -
+                                                         1e-7 * (fabs((double)b) + fabs(off))));
       }
       s.thr[w] = thr;
     }
   }
   __syncthreads();
 
-  // The groups that reach it.
-  {
-    int mine = 0;
-    for (int it = rank; it < items; it += C, ++mine) {
-      const float thr = s.thr[it / p.slices];
-      for (int i = 0; i < p.iters; ++i) {
-        const int at = (mine * p.iters + i) * kTopThreads + t;
-        const float gm = of_bf16(table[at]);
-        if (gm >= thr && gm > -INFINITY) {
-          const int h = atomicAdd(&s.n_hits, 1);
-          if (h < kMaxHits) s.hit[h] = (unsigned)at;
-        }
-      }
+  // The groups that reach it, eight table entries a thread.
+  const int mine_items = rank < items ? (items - rank + C - 1) / C : 0;
+  for (int v = t; v < mine_items * p.iters * (kTopThreads / 8); v += kTopThreads) {
+    const uint4 e = load128(table + 8 * v);
+    const int mine = v / (p.iters * (kTopThreads / 8));
+    const float thr = s.thr[(rank + mine * C) / p.slices];
+    const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+    unsigned hits = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      hits |= (bf16_lo(w[q]) >= thr ? 1u : 0u) << (2 * q) | (bf16_hi(w[q]) >= thr ? 2u : 0u) << (2 * q);
+    if (hits) {
+      int h = atomicAdd(&s.n_hits, __popc(hits));
+      for (; hits; hits &= hits - 1u, ++h)
+        if (h < kMaxCands) s.rank[h] = 8 * v + __ffs(hits) - 1;
     }
   }
   __syncthreads();
   TopShared* lead = C > 1 ? cluster.map_shared_rank(&s, 0) : &s;
-  {
-    const int hits = s.n_hits;
-    if (hits > kMaxHits) {
-      if (t == 0) lead->overflow = 1;
-    } else {
-      for (int q = t; q < hits * UN; q += kTopThreads) {
-        const unsigned at = s.hit[q / UN];
-        const int u = q % UN;
-        const int ti = (int)(at % kTopThreads), mi = (int)(at / kTopThreads);
-        const int mine = mi / p.iters, i = mi - mine * p.iters;
-        const int it = rank + mine * C;
-        const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
-        const int e1 = min(e0 + p.slice, p.V);
-        const int j = e0 + ((i * UN + u) * kTopThreads + ti) * VEC;
-        if (j >= e1) continue;
-        const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
-        const uint4 g = load_group<T, kAligned>(row, j, p.V, p.span);
-        const float thr = s.thr[w];
+  const int hits = s.n_hits;
+  if (hits > kMaxCands) {
+    if (t == 0) lead->overflow = 1;
+  } else {
+    for (int q = t; q < hits * kGroups; q += kTopThreads) {
+      const int at = s.rank[q / kGroups], u = q % kGroups;
+      const int mi = at / kTopThreads, ti = at % kTopThreads;
+      const int mine = mi / p.iters, i = mi - mine * p.iters;
+      const int it = rank + mine * C;
+      const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
+      const int j = e0 + ((i * kGroups + u) * kTopThreads + ti) * VEC;
+      if (j >= min(e0 + p.slice, p.V)) continue;
+      const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
+      const uint4 g = load_group<T, kAligned>(row, j, p.V, p.span);
+      const float thr = s.thr[w];
+      unsigned in = 0;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float l = Lane<T, VEC>::get(g, e);
-          if (l >= thr && l > -INFINITY) {
-            const int o = atomicAdd(&lead->n_cands, 1);
+      for (int e = 0; e < VEC; ++e) in |= (Lane<T, VEC>::get(g, e) >= thr ? 1u : 0u) << e;
+      if (in) {
+        int o = atomicAdd(&lead->n_cands, __popc(in));
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (in >> e & 1u) {
+            // the logit now, the key when the list is complete
             if (o < kMaxCands) {
-              lead->key[o] = ordered(s.off[w] + (double)l);
+              lead->key[o] = __float_as_uint(Lane<T, VEC>::get(g, e));
               lead->idx[o] = w * p.V + j + e;
             }
+            ++o;
           }
-        }
       }
     }
   }
@@ -407,21 +506,18 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
 
   int count = s.n_cands;
   if (s.overflow || count > kMaxCands) {
+    __syncthreads();
     count = 0;
     for (int w = 0; w < p.W; ++w) {
-      const double off = s.off[w];
+      const double off = kBeam ? s.off[w] : 0.0;
       if (off == -INFINITY) continue;
       const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
-      const int got = select_row_slow<T>(s, row, p.V, p.n, off, w * p.V, count);
+      const int got = select_row_slow<T, kBeam>(s, row, p.V, p.n, off, w * p.V, count);
       // keep the n best of the rows so far (at most 2 n <= 256 entries, one a thread)
       const int total = count + got;
-      unsigned long long key = 0;
-      int idx = 0, r = p.n;
-      if (t < total) {
-        key = s.key[t];
-        idx = s.idx[t];
-        r = rank_of(s, total, key, idx);
-      }
+      rank_list<kBeam>(s, total);
+      const unsigned long long key = t < total ? s.key[t] : 0;
+      const int idx = t < total ? s.idx[t] : 0, r = t < total ? s.rank[t] : p.n;
       __syncthreads();
       if (r < p.n) {
         s.key[r] = key;
@@ -430,11 +526,18 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
       count = min(total, p.n);
       __syncthreads();
     }
-  } else if (count > kRankAll) {
-    count = prune(s, count, p.n);
+  } else {
+    for (int i = t; i < count; i += kTopThreads) {
+      const int idx = s.idx[i];
+      set_candidate<kBeam>(s, i, __uint_as_float((uint32_t)s.key[i]),
+                           kBeam ? s.off[idx / p.V] : 0.0, idx);
+    }
+    __syncthreads();
+    if (count > kRankAll) count = prune(s, count, p.n);
   }
+  rank_list<kBeam>(s, count);
   for (int i = t; i < count; i += kTopThreads) {
-    const int r = rank_of(s, count, s.key[i], s.idx[i]);
+    const int r = s.rank[i];
     if (r < p.n) write_slot<kBeam>(p, grp, r, s.key[i], s.idx[i]);
   }
   for (int j = count + t; j < p.n; j += kTopThreads) write_slot<kBeam>(p, grp, j, 0, -1);
@@ -487,8 +590,10 @@ sv_status run_top(TopParams& p, sv_dtype dtype, long long groups, cudaStream_t s
   const int items = p.W * p.slices;
   if (items > kMaxItems || (long long)((items + C - 1) / C) * p.iters > kMaxTables)
     return SV_ERR_SHAPE;
+  // four units per kept candidate (or the finest there are), at least one a warp
   p.upi = kTopThreads;
-  while (items * p.upi > kMaxUnits) p.upi /= 2;
+  while (p.upi > kTopWarps && items * p.upi > kMaxUnits) p.upi /= 2;
+  while (p.upi > kTopWarps && items * p.upi / 2 >= 4 * p.n) p.upi /= 2;
   const size_t esz = dtype == SV_BF16 ? 2 : 4;
   const char* first = static_cast<const char*>(p.logits);
   p.span.first = first;

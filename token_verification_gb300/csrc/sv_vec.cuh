@@ -217,6 +217,14 @@ __device__ __forceinline__ float2 warp_running(const RunningSum& r, float c) {
   return make_float2(wm, warp_sum(r.s * to_frame(r.m, wm, c)));
 }
 
+// The two halves of a cluster barrier (release / acquire).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
