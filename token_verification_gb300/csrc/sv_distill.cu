@@ -265,11 +265,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
   const T* src = reinterpret_cast<const T*>(p.student) + row * (long long)p.V;
   for (int j0 = e0; j0 < e1; j0 += kDistillThreads * VEC * UN) {
     uint4 g[UN];
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int j = j0 + (u * kDistillThreads + t) * VEC;
-      if (j < e1) g[u] = load_group<T, kAligned>(src, j, p.V, p.span);
-    }
+    load_groups<T, kAligned>(g, src, j0 + t * VEC, kDistillThreads * VEC, e1, p.V, p.span);
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       const int j = j0 + (u * kDistillThreads + t) * VEC;

@@ -346,11 +346,8 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
       // before it is reduced
       uint4 g0[UN], g1[UN];
       auto load = [&](uint4(&g)[UN], int i) {
-#pragma unroll
-        for (int u = 0; u < UN; ++u) {
-          const int j = e0 + ((i * UN + u) * kTopThreads + t) * VEC;
-          g[u] = j < e1 ? load_group<T, kAligned>(row, j, p.V, p.span) : Lane<T, VEC>::pad();
-        }
+        load_groups<T, kAligned>(g, row, e0 + (i * UN * kTopThreads + t) * VEC, kTopThreads * VEC,
+                                 e1, p.V, p.span);
       };
       const int batches = p.iters * kBatches;
       load(g0, 0);
