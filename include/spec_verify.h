@@ -447,7 +447,8 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
  *               (SV_ERR_ALIAS).
  *   out_status  [B, P] int32 or NULL: SV_REQ_BAD_LOGITS (student NaN, +inf or no
  *               finite logit; a used entry's logit NaN or +inf, or a top_lse beside
- *               it that is not finite), SV_REQ_BAD_TOKEN (a token outside [-1, V) or
+ *               it that is not finite, or without one no finite logit),
+ *               SV_REQ_BAD_TOKEN (a token outside [-1, V) or
  *               given twice), SV_REQ_BAD_DRAFT_LEN.  Such a row has loss NaN and
  *               gradient 0.
  *   k, B, P, V, temperature: as in spec_top_logits.  No workspace. */

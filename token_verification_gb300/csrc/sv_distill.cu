@@ -28,8 +28,6 @@ namespace {
 constexpr int kDistillThreads = 256;
 constexpr int kDistillWarps = kDistillThreads / kWarp;
 constexpr int kMaxCluster = 8;
-constexpr float kLn2 = 0.6931471805599453f;
-
 enum DistillMode : int { kLoss = 0, kLossGrad = 1, kGradOnly = 2 };
 
 struct DistillParams {
@@ -45,25 +43,24 @@ struct DistillParams {
   void* out_grad;           // [B*P, V]
   int* out_status;          // [B*P] or null
   int P, V, k;
-  int slice;                // elements per CTA (a multiple of VEC)
+  int slice;                // 16-byte words per CTA
   float cc;                 // log2(e) / T
-  double inv_t;             // 1 / T
-  RowSpan span;
+  float T, inv_t;           // T and 1 / T
 };
 
-struct DistillShared {
+struct alignas(16) DistillShared {
   float4 part[kMaxCluster];      // each CTA's {max, sum, -, -} over its slice without the record
   float2 warp_part[kDistillWarps];
+  float4 stat;                   // {m, beta, M, 1/Z}
   int id[SV_MAX_TOP];            // the record (-1: unused)
   float t[SV_MAX_TOP];           // its logits (-inf: unused)
   float p[SV_MAX_TOP];           // its teacher probabilities
   float sv[SV_MAX_TOP];          // the student's logits at its tokens
   int bad, used;
-  double norm;                   // the teacher's log-sum-exp: log p_j = t_j / T - norm
-  double p_rest;
+  float norm, norm_lo;           // the teacher's log-sum-exp: log p_j = t_j / T - norm
+  float p_rest;
   float m, M;                    // the student's max outside the record, and over all
-  double S, Z;                   // its sums there, in the frames of m and M
-  float4 stat;                   // {m, beta, M, 1/Z}
+  float2 S, Z;                   // its sums there, in the frames of m and M (hi, lo)
 };
 
 // Writes `bytes` bytes of zeros at `dst` (2-byte aligned).
@@ -79,22 +76,20 @@ __device__ void zero_bytes(char* dst, long long bytes) {
     *reinterpret_cast<uint16_t*>(dst + i) = 0;
 }
 
-// The slice of `bytes` bytes at shared address `src` (16-byte aligned) goes to
-// global `dst` (2-byte aligned).
+// `bytes` bytes from shared memory go to global `dst` (both 2-byte aligned;
+// the aligned 16-byte words around the source are readable).
 __device__ void store_slice(char* dst, const unsigned char* src, int bytes) {
   const int t = threadIdx.x;
   const int head = min(bytes, (int)((16u - ((uint32_t)(uintptr_t)dst & 15u)) & 15u));
   for (int i = 2 * t; i < head; i += 2 * kDistillThreads)
     *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
   const int vecs = (bytes - head) / 16;
-  if (head == 0) {
-    for (int i = t; i < vecs; i += kDistillThreads)
-      *reinterpret_cast<uint4*>(dst + 16 * i) = *reinterpret_cast<const uint4*>(src + 16 * i);
-  } else {  // the 16 bytes from src + head + 16 i span two shared words
-    for (int i = t; i < vecs; i += kDistillThreads) {
-      const uint4* a = reinterpret_cast<const uint4*>(src + 16 * i);
-      *reinterpret_cast<uint4*>(dst + head + 16 * i) = shift_pair(a[0], a[1], (uint32_t)head);
-    }
+  const uint32_t r = (uint32_t)(uintptr_t)(src + head) & 15u;
+  const unsigned char* words = src + head - r;
+  for (int i = t; i < vecs; i += kDistillThreads) {
+    const uint4 a = load128(words + 16 * i);
+    *reinterpret_cast<uint4*>(dst + head + 16 * i) =
+        r == 0 ? a : shift_pair(a, load128(words + 16 * i + 16), r);
   }
   for (int i = head + 16 * vecs + 2 * t; i < bytes; i += 2 * kDistillThreads)
     *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
@@ -134,10 +129,17 @@ __device__ __forceinline__ uint4 scaled_group(const uint4& g, float c, float m, 
   return make_uint4(f(g.x), f(g.y), f(g.z), f(g.w));
 }
 
+// x / T as hi + lo.
+__device__ __forceinline__ void add_ratio(Pair& a, float x, const DistillParams& p, float sign) {
+  const float q = x / p.T;
+  a.add(sign * q);
+  a.add(sign * (fmaf(-q, p.T, x) * p.inv_t));
+}
+
 // The teacher's side of a row: its record and probabilities.  Sets s.bad for
 // a token out of range or given twice, for a NaN or +inf logit, and for a
-// log-sum-exp that is not finite beside a used entry.  By the
-// first warps; the caller synchronises around it.
+// log-sum-exp that is not finite beside a used entry.  A whole-CTA call; the
+// last part is the first warp's.
 __device__ void load_record(DistillShared& s, const DistillParams& p, long long row) {
   const int t = threadIdx.x;
   const float lse = p.top_lse ? p.top_lse[row] : 0.f;
@@ -146,99 +148,137 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     const float v = p.top_logits[row * p.k + t];
     s.id[t] = id;
     s.t[t] = id < 0 ? -INFINITY : v;
-    if (id < -1 || id >= p.V) atomicOr(&s.bad, SV_REQ_BAD_TOKEN);
+    int bad = 0;
+    if (id < -1 || id >= p.V) bad |= SV_REQ_BAD_TOKEN;
     if (id >= 0) {
-      atomicAdd(&s.used, 1);
-      if (v != v || v == INFINITY) atomicOr(&s.bad, SV_REQ_BAD_LOGITS);
+      if (v != v || v == INFINITY) bad |= SV_REQ_BAD_LOGITS;
+      if (p.top_lse && !is_finite(lse)) bad |= SV_REQ_BAD_LOGITS;
+      s.used = 1;
     }
+    if (bad) atomicOr(&s.bad, bad);
   }
   __syncthreads();
-  if (t == 0 && s.used > 0 && p.top_lse && !is_finite(lse)) atomicOr(&s.bad, SV_REQ_BAD_LOGITS);
-  if (t < p.k && s.id[t] >= 0)
-    for (int j = 0; j < t; ++j)
-      if (s.id[j] == s.id[t]) atomicOr(&s.bad, SV_REQ_BAD_TOKEN);
+  // pairs of entries: the CTA's upper half compares with the entries before,
+  // the lower half's first warp goes on to the probabilities
+  if (t >= kDistillThreads / 2 && t - kDistillThreads / 2 < p.k) {
+    const int i = t - kDistillThreads / 2, id = s.id[i];
+    bool twice = false;
+    if (id >= 0)
+      for (int j = 0; j < i; ++j) twice = twice || s.id[j] == id;
+    if (twice) atomicOr(&s.bad, SV_REQ_BAD_TOKEN);
+  }
   if (t < kWarp) {
     constexpr int kPer = SV_MAX_TOP / kWarp;
-    double x[kPer];
-    float m = -INFINITY;
+    float v[kPer], m = -INFINITY;
+    int used = 0;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int j = q * kWarp + t;
-      const float v = j < p.k ? s.t[j] : -INFINITY;
-      x[q] = (double)v * p.inv_t;
-      m = fmaxf(m, v);
+      v[q] = j < p.k ? s.t[j] : -INFINITY;
+      used += j < p.k && s.id[j] >= 0 ? 1 : 0;
+      m = fmaxf(m, v[q]);
     }
-    double norm = (double)lse;
-    if (!p.top_lse) {
+    Pair norm;
+    norm.add(lse);
+    if (!p.top_lse) {  // the record's own: max / T + log of the sum in its frame
       m = warp_max(m);
-      const double mt = m == -INFINITY ? 0.0 : (double)m * p.inv_t;
-      double z = 0.0;
+      float z = 0.f;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) z += (double)expf((float)(x[q] - mt));
-      norm = mt + log(warp_sum(z));
+      for (int q = 0; q < kPer; ++q) z += expf((v[q] - frame_of(m)) * p.inv_t);
+      if (t == 0 && s.used && m == -INFINITY) atomicOr(&s.bad, SV_REQ_BAD_LOGITS);
+      const float2 l = log_pair(warp_sum_pair(z));
+      norm = Pair();
+      add_ratio(norm, frame_of(m), p, 1.f);
+      norm.add(l.x);
+      norm.add(l.y);
     }
-    double sum = 0.0;
+    float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int j = q * kWarp + t;
-      const float pj = x[q] == -INFINITY ? 0.f : expf((float)(x[q] - norm));
+      const float pj =
+          v[q] == -INFINITY ? 0.f : expf(fmaf(v[q], p.inv_t, -norm.hi) - norm.lo);
       if (j < p.k) s.p[j] = pj;
-      sum += (double)pj;
+      sum += pj;
     }
-    sum = warp_sum(sum);
+    const float2 total = warp_sum_pair(sum);
+    used = (int)__reduce_add_sync(0xffffffffu, (unsigned)used);
     if (t == 0) {
-      s.norm = norm;
-      s.p_rest = p.top_lse && s.used < p.V ? fmax(0.0, 1.0 - sum) : 0.0;
+      s.norm = norm.hi;
+      s.norm_lo = norm.lo;
+      s.p_rest = p.top_lse && used < p.V ? fmaxf(0.f, (1.f - total.x) - total.y) : 0.f;
     }
   }
 }
 
-// The loss of a row, by one warp.  The logarithms' differences are taken in 64
-// bits: where student and teacher agree the loss is far below its terms.
-__device__ double row_loss(const DistillShared& s, const DistillParams& p) {
+// The loss of a row, by one warp:
+//   sum_j p_j ((t_j - s_j) / T - K) + p_rest (log p_rest - log q_rest)
+// with K = norm - (M / T + log Z).  The differences are taken before anything
+// is rounded to their terms' size: where student and teacher agree the loss
+// is far below its terms.
+__device__ float row_loss(const DistillShared& s, const DistillParams& p) {
   const int lane = lane_id();
-  const double mine = log(lane == 0 ? s.Z : lane == 1 ? s.S : s.p_rest > 0.0 ? s.p_rest : 1.0);
-  const double lz = __shfl_sync(0xffffffffu, mine, 0), ls = __shfl_sync(0xffffffffu, mine, 1),
-               lr = __shfl_sync(0xffffffffu, mine, 2);
-  double loss = 0.0;
+  // lane 0: log Z, lane 1: log S
+  const float2 mine = log_pair(lane == 1 ? s.S : s.Z);
+  const float2 lz = make_float2(__shfl_sync(0xffffffffu, mine.x, 0),
+                                __shfl_sync(0xffffffffu, mine.y, 0));
+  const float2 ls = make_float2(__shfl_sync(0xffffffffu, mine.x, 1),
+                                __shfl_sync(0xffffffffu, mine.y, 1));
+  Pair K;
+  K.add(s.norm);
+  add_ratio(K, s.M, p, -1.f);
+  K.add(-lz.x);
+  K.add(-lz.y);
+  K.add(s.norm_lo);
+  const float k = K.value();
+  float loss = 0.f;
   for (int j = lane; j < p.k; j += kWarp)
-    if (s.p[j] > 0.f) {
-      const double log_q = ((double)s.sv[j] - (double)s.M) * p.inv_t - lz;
-      loss += (double)s.p[j] * (((double)s.t[j] * p.inv_t - s.norm) - log_q);
-    }
+    if (s.p[j] > 0.f) loss = fmaf(s.p[j], (s.t[j] - s.sv[j]) * p.inv_t - k, loss);
   loss = warp_sum(loss);
-  if (s.p_rest > 0.0)
-    loss += s.m == -INFINITY
-                ? INFINITY
-                : s.p_rest * (lr - (ls + ((double)s.m - (double)s.M) * p.inv_t - lz));
+  if (s.p_rest > 0.f) {
+    if (s.m == -INFINITY) return INFINITY;
+    Pair d;  // log q_rest = log S + (m - M) / T - log Z, whatever underflowed
+    add_ratio(d, s.m - s.M, p, -1.f);
+    d.add(lz.x - ls.x);
+    d.add(lz.y);
+    d.add(-ls.y);
+    d.add(logf(s.p_rest));
+    loss += s.p_rest * d.value();
+  }
   return loss;
 }
 
-template <typename T, bool kAligned, int kMode>
-__global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const DistillParams p) {
-  constexpr int VEC = Group<T>::VEC;
+template <typename T, int kMode>
+__global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const DistillParams p) {
+  constexpr int VEC = Group<T>::VEC, kSize = (int)sizeof(T);
   constexpr int UN = 4;
   extern __shared__ __align__(16) unsigned char smem[];
   DistillShared& s = *reinterpret_cast<DistillShared*>(smem);
-  unsigned char* slice = smem + (sizeof(DistillShared) + 15) / 16 * 16;
+  unsigned char* words = smem + sizeof(DistillShared);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const long long row = blockIdx.x / C;
   const int t = threadIdx.x, lane = lane_id(), warp = t / kWarp;
-  const int e0 = min(rank * p.slice, p.V), e1 = min(e0 + p.slice, p.V);
   const T* tag = nullptr;
-  char* grad = kMode == kLoss ? nullptr
-                              : static_cast<char*>(p.out_grad) +
-                                    (row * (long long)p.V + e0) * (long long)sizeof(T);
-  const int bytes = (e1 - e0) * (int)sizeof(T);
+
+  // The row in aligned 16-byte words: byte x of the row is byte x + r of word
+  // 0 on, r its misalignment.  This CTA has words w0 .. w1 - 1, row bytes
+  // x0 .. x1 - 1.
+  const int nb = p.V * kSize;
+  const char* src = static_cast<const char*>(p.student) + row * (long long)nb;
+  const int r = (int)((uintptr_t)src & 15u);
+  const int all = (r + nb + 15) / 16;
+  const int w0 = min(rank * p.slice, all), w1 = min(w0 + p.slice, all), nw = w1 - w0;
+  const int x0 = min(nb, max(0, 16 * w0 - r)), x1 = max(x0, min(nb, 16 * w1 - r));
+  char* grad = kMode == kLoss ? nullptr : static_cast<char*>(p.out_grad) + row * (long long)nb;
 
   // A row without loss or gradient (not needed, or a data error seen by
   // every CTA of the cluster alike).
   auto leave = [&](float loss, int status) {
-    if (kMode != kLoss) zero_bytes(grad, bytes);
+    if (kMode != kLoss) zero_bytes(grad + x0, x1 - x0);
     if (kMode != kGradOnly && rank == 0 && t == 0) {
       p.out_loss[row] = loss;
-      // beta 0 and 1/Z NaN: a later backward pass writes zeros
+      // 1/Z NaN: a later backward pass writes zeros
       if (p.out_stats) p.out_stats[row] = make_float4(0.f, 0.f, 0.f, qnan());
       if (p.out_status) p.out_status[row] = status;
     }
@@ -261,56 +301,67 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     if (t == 0) s.stat = st;
   }
 
-  // The slice, and the record while it is under way.
-  const T* src = reinterpret_cast<const T*>(p.student) + row * (long long)p.V;
-  for (int j0 = e0; j0 < e1; j0 += kDistillThreads * VEC * UN) {
-    uint4 g[UN];
-    load_groups<T, kAligned>(g, src, j0 + t * VEC, kDistillThreads * VEC, e1, p.V, p.span);
+  // The slice on its way into shared memory: the words inside the row as
+  // they are, the row's first and last word by element, -inf around them.
+  for (int i = t; i < nw; i += kDistillThreads) {
+    const int x = 16 * (w0 + i) - r;
+    if (x >= 0 && x + 16 <= nb) {
+      copy16_async(smem_u32(words + 16 * i), src + x);
+    } else {
+      uint4 v = Lane<T, VEC>::pad();
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int j = j0 + (u * kDistillThreads + t) * VEC;
-      if (j < e1) *reinterpret_cast<uint4*>(slice + (size_t)(j - e0) * sizeof(T)) = g[u];
+      for (int e = 0; e < VEC; ++e) {
+        const int y = x + e * kSize;
+        if (y >= 0 && y < nb) put(v, e, *reinterpret_cast<const T*>(src + y));
+      }
+      *reinterpret_cast<uint4*>(words + 16 * i) = v;
     }
   }
   if (t == 0) s.bad = s.used = 0;
+  // (no CTA writes into another's shared memory before that one has started)
+  if (kMode != kGradOnly && C > 1) cluster_arrive();
   __syncthreads();
   load_record(s, p, row);
+  copies_wait();
+  if (kMode != kGradOnly && C > 1) cluster_wait();
   __syncthreads();
   const int bad_record = s.bad, used = s.used;
   if (bad_record || used == 0) {
     leave(bad_record ? qnan() : 0.f, bad_record);
     return;
   }
-  if (kMode != kGradOnly && C > 1) cluster.sync();  // every CTA has started
 
   // The student's logits at the recorded tokens leave the slice.
-  if (t < p.k) {
-    const int id = s.id[t];
-    if (id >= e0 && id < e1) {
-      T* at = reinterpret_cast<T*>(slice) + (id - e0);
-      const float v = widen(*at);
-      if (kMode != kGradOnly && C > 1) {
-        for (int c = 0; c < C; ++c) cluster.map_shared_rank(&s, c)->sv[t] = v;
+  const int my_id = t < p.k ? s.id[t] : -1;
+  const int my_x = my_id * kSize;  // < 2^21
+  const bool mine = my_id >= 0 && my_x >= x0 && my_x < x1;
+  T* my_at = reinterpret_cast<T*>(words + (my_x + r - 16 * w0));
+  float my_v = 0.f;
+  if (mine) {
+    my_v = widen(*my_at);
+    if (kMode != kGradOnly) {
+      if (C > 1) {
+        for (int c = 0; c < C; ++c) cluster.map_shared_rank(&s, c)->sv[t] = my_v;
       } else {
-        s.sv[t] = v;
+        s.sv[t] = my_v;
       }
-      store_value(at, -INFINITY);
     }
+    store_value(my_at, -INFINITY);
   }
   __syncthreads();
 
   if (kMode != kGradOnly) {
-    RunningSum r;
-    for (int j0 = 0; j0 < e1 - e0; j0 += kDistillThreads * VEC * UN) {
+    RunningSum run;
+    for (int i0 = t; i0 < nw; i0 += kDistillThreads * UN) {
       uint4 g[UN];
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
-        const int j = j0 + (u * kDistillThreads + t) * VEC;
-        g[u] = j < e1 - e0 ? load128(slice + (size_t)j * sizeof(T)) : Lane<T, VEC>::pad();
+        const int i = i0 + u * kDistillThreads;
+        g[u] = i < nw ? load128(words + 16 * i) : Lane<T, VEC>::pad();
       }
-      r.add(g, p.cc, tag);
+      run.add(g, p.cc, tag);
     }
-    const float2 wr = warp_running(r, p.cc);
+    const float2 wr = warp_running(run, p.cc);
     if (lane == 0) s.warp_part[warp] = wr;
     __syncthreads();
     if (warp == 0) {
@@ -328,7 +379,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       // the rest: its max m and sum S over the cluster's slices
       const float4 v = lane < C ? s.part[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
       const float m = warp_max_nan(v.x);
-      const double S = warp_sum((double)(v.y * to_frame(v.x, m, p.cc)));
+      const float2 S = warp_sum_pair(v.y * to_frame(v.x, m, p.cc));
       // the record, and both together in the frame of M
       constexpr int kPer = SV_MAX_TOP / kWarp;
       float x[kPer], M = -INFINITY;
@@ -342,18 +393,25 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       }
       M = fmaxf(warp_max(M), m);
       wrong = __any_sync(0xffffffffu, wrong) || M == -INFINITY;
-      double z = 0.0;
+      float z = 0.f;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) z += (double)ex2((x[q] - M) * p.cc);
-      const double rest = m == -INFINITY ? 0.0 : S * (double)ex2((m - M) * p.cc);
-      const double Z = warp_sum(z) + rest;
+      for (int q = 0; q < kPer; ++q) z += ex2((x[q] - frame_of(M)) * p.cc);
+      const float2 zk = warp_sum_pair(z);
+      const float down = m == -INFINITY ? 0.f : ex2((m - M) * p.cc);
+      const float rest = S.x * down;
+      Pair Z;
+      Z.add(zk.x);
+      Z.add(rest);
+      Z.add(zk.y);
+      Z.add(fmaf(S.x, down, -rest) + S.y * down);
       if (lane == 0) {
-        const float beta = m == -INFINITY ? 0.f : (float)((rest / Z - s.p_rest) / S);
+        const float zv = Z.value();
         s.m = m;
         s.M = M;
-        s.S = m == -INFINITY ? 1.0 : S;
-        s.Z = Z;
-        s.stat = make_float4(frame_of(m), beta, M, wrong ? qnan() : (float)(1.0 / Z));
+        s.S = m == -INFINITY ? make_float2(1.f, 0.f) : S;
+        s.Z = make_float2(Z.hi, Z.lo);
+        s.stat = make_float4(frame_of(m), m == -INFINITY ? 0.f : (rest / zv - s.p_rest) / S.x, M,
+                             wrong ? qnan() : 1.f / zv);
         if (rank == 0) {
           if (p.out_stats) p.out_stats[row] = wrong ? make_float4(0.f, 0.f, 0.f, qnan()) : s.stat;
           if (p.out_status) p.out_status[row] = wrong ? SV_REQ_BAD_LOGITS : 0;
@@ -365,8 +423,8 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       if (rank == 0 && warp == 0) {
         __syncwarp();
         if (s.stat.w == s.stat.w) {
-          const double loss = row_loss(s, p);
-          if (lane == 0) p.out_loss[row] = (float)loss;
+          const float loss = row_loss(s, p);
+          if (lane == 0) p.out_loss[row] = loss;
         }
       }
       return;
@@ -374,50 +432,64 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     __syncthreads();
   }
 
-  // The gradient: the slice in place, then the recorded tokens, then out.
+  // The gradient.
   const float4 st = s.stat;
   if (st.w != st.w) {
-    zero_bytes(grad, bytes);
+    zero_bytes(grad + x0, x1 - x0);
     return;
   }
-  const float scale = (float)((double)p.grad_loss[row] * p.inv_t);
+  const float scale = p.grad_loss[row] / p.T;
   const float beta = st.y * scale;
-  for (int j = t * VEC; j < e1 - e0; j += kDistillThreads * VEC) {
-    uint4* at = reinterpret_cast<uint4*>(slice + (size_t)j * sizeof(T));
-    *at = scaled_group(*at, p.cc, st.x, beta, tag);
+  const float my_grad = (ex2((my_v - st.z) * p.cc) * st.w - (t < p.k ? s.p[t] : 0.f)) * scale;
+  if (((uintptr_t)grad & 15u) == (uint32_t)r) {
+    // word for word as the student's row; the recorded tokens after the words they lie in
+    for (int i = t; i < nw; i += kDistillThreads) {
+      const uint4 g = scaled_group(load128(words + 16 * i), p.cc, st.x, beta, tag);
+      const int x = 16 * (w0 + i) - r;
+      if (x >= 0 && x + 16 <= nb) {
+        *reinterpret_cast<uint4*>(grad + x) = g;
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int y = x + e * kSize;
+          if (y >= 0 && y < nb) store_value(reinterpret_cast<T*>(grad + y), Lane<T, VEC>::get(g, e));
+        }
+      }
+    }
+    __syncthreads();
+    if (mine) store_value(reinterpret_cast<T*>(grad + my_x), my_grad);
+  } else {  // in place, then shifted out
+    for (int i = t; i < nw; i += kDistillThreads) {
+      uint4* at = reinterpret_cast<uint4*>(words + 16 * i);
+      *at = scaled_group(*at, p.cc, st.x, beta, tag);
+    }
+    __syncthreads();
+    if (mine) store_value(my_at, my_grad);
+    __syncthreads();
+    store_slice(grad + x0, words + (x0 + r - 16 * w0), x1 - x0);
   }
-  __syncthreads();
-  if (t < p.k) {
-    const int id = s.id[t];
-    if (id >= e0 && id < e1)
-      store_value(reinterpret_cast<T*>(slice) + (id - e0),
-                  (ex2((s.sv[t] - st.z) * p.cc) * st.w - s.p[t]) * scale);
-  }
-  __syncthreads();
-  store_slice(grad, slice, bytes);
   if (kMode == kLossGrad && rank == 0 && warp == 0) {  // nothing waits for the loss here
-    const double loss = row_loss(s, p);
-    if (lane == 0) p.out_loss[row] = (float)loss;
+    const float loss = row_loss(s, p);
+    if (lane == 0) p.out_loss[row] = loss;
   }
 }
 
-constexpr int kSharedHead = (int)(sizeof(DistillShared) + 15) / 16 * 16;
-constexpr int kMaxSliceBytes = SV_MAX_DISTILL_ROW / kMaxCluster + 256;
+constexpr int kMaxSliceBytes = SV_MAX_DISTILL_ROW / kMaxCluster + 64;
 
-template <typename T, bool kAligned, int kMode>
+template <typename T, int kMode>
 cudaError_t launch_distill(const DistillParams& p, long long rows, int C, cudaStream_t stream) {
   static PerDevice once;
-  auto* fn = distill_kernel<T, kAligned, kMode>;
+  auto* fn = distill_kernel<T, kMode>;
   cudaError_t err = per_device(once, nullptr, [&](int&) {
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSharedHead + kMaxSliceBytes);
+                                (int)sizeof(DistillShared) + kMaxSliceBytes);
   });
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * C));
   cfg.blockDim = dim3(kDistillThreads);
-  // 16 bytes past the slice: the last shifted store reads the word after it
-  cfg.dynamicSmemBytes = kSharedHead + (size_t)p.slice * sizeof(T) + 16;
+  // a word past the slice: the last shifted store reads it
+  cfg.dynamicSmemBytes = sizeof(DistillShared) + 16 * ((size_t)p.slice + 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -435,25 +507,17 @@ sv_status run_distill(DistillParams& p, sv_dtype dtype, long long rows, cudaStre
   if (device_info(&dev) != cudaSuccess) return SV_ERR_CUDA;
   const int esz = dtype == SV_BF16 ? 2 : 4;
   // A slice of at most 40 KB leaves five CTAs on an SM; few rows are spread
-  // over more CTAs while a slice still gives every thread a group.
+  // over more CTAs while a slice still gives every thread two words.
   int C = 1;
   while (C < kMaxCluster && ((long long)p.V * esz > 40960LL * C ||
                              (rows * C < 2LL * dev.sms && (long long)p.V * esz > 8192LL * C)))
     C *= 2;
-  const int vec = 16 / esz;
-  p.slice = ((p.V + C - 1) / C + vec - 1) / vec * vec;
-  const char* first = static_cast<const char*>(p.student);
-  const size_t bytes = (size_t)rows * (size_t)p.V * esz;
-  p.span.first = first;
-  p.span.last = first + bytes;
-  const bool aligned = ((uintptr_t)first & 15u) == 0 && ((size_t)p.V * esz) % 16 == 0;
-  cudaError_t err;
-  if (dtype == SV_BF16)
-    err = aligned ? launch_distill<uint16_t, true, kMode>(p, rows, C, stream)
-                  : launch_distill<uint16_t, false, kMode>(p, rows, C, stream);
-  else
-    err = aligned ? launch_distill<float, true, kMode>(p, rows, C, stream)
-                  : launch_distill<float, false, kMode>(p, rows, C, stream);
+  // words of a row at the worst alignment
+  const bool aligned = ((uintptr_t)p.student & 15u) == 0 && (long long)p.V * esz % 16 == 0;
+  const int all = (int)(((long long)p.V * esz + (aligned ? 0 : 16 - esz) + 15) / 16);
+  p.slice = (all + C - 1) / C;
+  const cudaError_t err = dtype == SV_BF16 ? launch_distill<uint16_t, kMode>(p, rows, C, stream)
+                                           : launch_distill<float, kMode>(p, rows, C, stream);
   return err == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
@@ -486,7 +550,8 @@ DistillParams distill_params(const void* student, const int32_t* ids, const floa
   p.V = V;
   p.k = k;
   p.cc = exponent_scale(temperature);
-  p.inv_t = 1.0 / (double)temperature;
+  p.T = temperature;
+  p.inv_t = (float)(1.0 / (double)temperature);
   return p;
 }
 

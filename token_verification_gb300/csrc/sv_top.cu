@@ -71,6 +71,7 @@ struct alignas(16) TopShared {
   float thr[SV_MAX_BEAMS];            // the lowest logit a candidate of the row can have
   float lse;                          // record
   unsigned hist[256];
+  int flag[2][kTopWarps];
   int n_hits, n_cands, overflow, bad, pick[4];
 };
 
@@ -80,33 +81,42 @@ __device__ __forceinline__ uint16_t up_bf16(float v) {
   return (uint16_t)((b & 0x80000000u) ? b >> 16 : (b + 0xffffu) >> 16);
 }
 
-// The n-th largest of kPer * 32 units to 16 bits (rounded down), by bisection
-// on ordered keys below their common prefix; -inf when fewer than n are
-// finite.  One warp.
+// The n-th largest of the cluster's unit bounds to 16 bits (rounded down); -inf
+// when fewer than n are finite.  A whole-CTA call: each warp holds all units
+// as ordered keys, and every round tests one threshold per warp, so the range
+// of keys shrinks ninefold (a bisection by one warp took 4000 cycles of a
+// row's 87000; this takes a quarter).
 template <int kPer>
-__device__ float unit_bound(const float* unit, int units, int n) {
-  uint32_t k[kPer], hi = 0, lo = 0xffffu;
+__device__ float unit_bound(TopShared& s, int units, int n) {
+  const int warp = threadIdx.x / kWarp;
+  int k[kPer], hi = 0, lo = 0xffff;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = j * kWarp + lane_id();
-    const float v = i < units ? unit[i] : -INFINITY;
-    k[j] = v > -INFINITY ? ordered(v) >> 16 : 0u;  // below every finite value's key
+    const float v = i < units ? s.unit[i] : -INFINITY;
+    k[j] = v > -INFINITY ? (int)(ordered(v) >> 16) : 0;  // below every finite value's key
     hi = max(hi, k[j]);
     lo = min(lo, k[j]);
   }
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  const int top = 32 - __clz(hi ^ lo);  // bits below the common prefix
-  uint32_t t = top ? hi >> top << top : hi;
-  for (int b = top - 1; b >= 0; --b) {
-    const uint32_t at = t | (1u << b);
+  if (units < n) return -INFINITY;
+  lo = __reduce_min_sync(0xffffffffu, lo);       // at least n units reach lo
+  hi = __reduce_max_sync(0xffffffffu, hi) + 1;   // fewer than n reach hi
+  for (int round = 0; hi - lo > 1; ++round) {
+    const int step = (hi - lo + kTopWarps) / (kTopWarps + 1), at = lo + step * (warp + 1);
     unsigned c = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) c += k[j] >= at ? 1u : 0u;
-    if ((int)__reduce_add_sync(0xffffffffu, c) >= n) t = at;
+    const bool ok = at < hi && (int)__reduce_add_sync(0xffffffffu, c) >= n;
+    // the warps' answers are monotone; two sets of flags need one barrier a round
+    if (lane_id() == 0) s.flag[round & 1][warp] = ok ? 1 : 0;
+    __syncthreads();
+    const unsigned yes = __ballot_sync(0xffffffffu, lane_id() < kTopWarps &&
+                                                        s.flag[round & 1][lane_id() % kTopWarps]);
+    const int up = __popc(yes);
+    hi = min(hi, lo + step * (up + 1));
+    lo += step * up;
   }
-  // fewer than n units in all, or fewer than n finite ones
-  return units >= n && t ? of_ordered(t << 16) : -INFINITY;
+  return lo ? of_ordered((uint32_t)lo << 16) : -INFINITY;
 }
 
 template <bool kBeam>
@@ -263,38 +273,6 @@ __device__ __forceinline__ void write_slot(const TopParams& p, long long grp, in
                             : of_ordered((uint32_t)(key >> 32));
 }
 
-// A warp's sum as hi + lo, the additions' roundings kept in lo.
-__device__ __forceinline__ float2 warp_sum_pair(float x) {
-  float hi = x, lo = 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float y = __shfl_xor_sync(0xffffffffu, hi, o), yl = __shfl_xor_sync(0xffffffffu, lo, o);
-    const float sum = __fadd_rn(hi, y);
-    // both lanes of a pair take the larger first: the same rounding in each
-    const float a = fmaxf(hi, y), b = fminf(hi, y);
-    lo = __fadd_rn(__fadd_rn(lo, yl), __fadd_rn(b, -__fadd_rn(sum, -a)));
-    hi = sum;
-  }
-  return make_float2(hi, lo);
-}
-
-// log(hi + lo) as an exact multiple of the leading bits of ln 2 plus a float
-// below 0.36 in size: good to about 5e-8 without 64-bit logarithms, which
-// cost microseconds here.  1 <= hi < 2^31.
-__device__ __forceinline__ float2 log_pair(float2 s) {
-  const uint32_t b = __float_as_uint(s.x);
-  int e = (int)(b >> 23) - 127;
-  float f = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);  // [1, 2)
-  if (f > 1.41421356f) {
-    f *= 0.5f;
-    e += 1;
-  }
-  const float scale = __uint_as_float((uint32_t)(127 - e) << 23);
-  // ln 2 = 0.693145751953125 (15 bits) + 1.42860682030941723e-6
-  const float hi = (float)e * 0.693145751953125f;
-  return make_float2(hi, logf(f) + fmaf((float)e, 1.42860682e-6f, s.y * scale / f));
-}
-
 template <typename T, bool kAligned, bool kBeam>
 __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) {
   constexpr int VEC = Group<T>::VEC;
@@ -425,42 +403,42 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
     }
     __syncthreads();
   }
-  if (warp == 0) {
-    const float b = units <= 64    ? unit_bound<2>(s.unit, units, p.n)
-                    : units <= 256 ? unit_bound<8>(s.unit, units, p.n)
-                                   : unit_bound<16>(s.unit, units, p.n);
-    for (int w = lane; w < p.W; w += kWarp) {
-      // -inf never passes: at least the lowest finite value
-      float thr = fmaxf(b, -FLT_MAX);
-      if (kBeam) {
-        const double off = s.off[w];
-        // below it, off + l rounds below the bound (the slack covers the roundings)
-        thr = off == -INFINITY ? INFINITY
-              : b == -INFINITY ? -FLT_MAX
-                               : fmaxf(-FLT_MAX,
-                                       __double2float_rd(((double)b - off) -
-                                                         1e-7 * (fabs((double)b) + fabs(off))));
-      }
-      s.thr[w] = thr;
+  const float bound = units <= 64    ? unit_bound<2>(s, units, p.n)
+                      : units <= 256 ? unit_bound<8>(s, units, p.n)
+                                     : unit_bound<16>(s, units, p.n);
+  if (kBeam) {
+    for (int w = t; w < p.W; w += kTopThreads) {
+      const double off = s.off[w];
+      // below it, off + l rounds below the bound (the slack covers the roundings); -inf never
+      // passes: at least the lowest finite value
+      s.thr[w] = off == -INFINITY ? INFINITY
+                 : bound == -INFINITY
+                     ? -FLT_MAX
+                     : fmaxf(-FLT_MAX,
+                             __double2float_rd(((double)bound - off) -
+                                               1e-7 * (fabs((double)bound) + fabs(off))));
     }
+    __syncthreads();
   }
-  __syncthreads();
+  auto threshold = [&](int w) { return kBeam ? s.thr[w] : fmaxf(bound, -FLT_MAX); };
 
   // The groups that reach it, eight table entries a thread.
-  const int mine_items = rank < items ? (items - rank + C - 1) / C : 0;
-  for (int v = t; v < mine_items * p.iters * (kTopThreads / 8); v += kTopThreads) {
-    const uint4 e = load128(table + 8 * v);
-    const int mine = v / (p.iters * (kTopThreads / 8));
-    const float thr = s.thr[(rank + mine * C) / p.slices];
-    const uint32_t w[4] = {e.x, e.y, e.z, e.w};
-    unsigned hits = 0;
+  for (int it = rank, mine = 0; it < items; it += C, ++mine) {
+    const float thr = threshold(it / p.slices);
+    const uint16_t* entries = table + mine * p.iters * kTopThreads;
+    for (int v = t; v < p.iters * (kTopThreads / 8); v += kTopThreads) {
+      const uint4 e = load128(entries + 8 * v);
+      const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+      unsigned hits = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      hits |= (bf16_lo(w[q]) >= thr ? 1u : 0u) << (2 * q) | (bf16_hi(w[q]) >= thr ? 2u : 0u) << (2 * q);
-    if (hits) {
-      int h = atomicAdd(&s.n_hits, __popc(hits));
-      for (; hits; hits &= hits - 1u, ++h)
-        if (h < kMaxCands) s.rank[h] = 8 * v + __ffs(hits) - 1;
+      for (int q = 0; q < 4; ++q)
+        hits |= (bf16_lo(w[q]) >= thr ? 1u << (2 * q) : 0u) |
+                (bf16_hi(w[q]) >= thr ? 2u << (2 * q) : 0u);
+      if (hits) {
+        int h = atomicAdd(&s.n_hits, __popc(hits));
+        for (; hits; hits &= hits - 1u, ++h)
+          if (h < kMaxCands) s.rank[h] = mine * p.iters * kTopThreads + 8 * v + __ffs(hits) - 1;
+      }
     }
   }
   __syncthreads();
@@ -479,7 +457,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
       if (j >= min(e0 + p.slice, p.V)) continue;
       const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
       const uint4 g = load_group<T, kAligned>(row, j, p.V, p.span);
-      const float thr = s.thr[w];
+      const float thr = threshold(w);
       unsigned in = 0;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) in |= (Lane<T, VEC>::get(g, e) >= thr ? 1u : 0u) << e;

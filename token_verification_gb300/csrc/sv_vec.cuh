@@ -254,12 +254,66 @@ __device__ __forceinline__ float2 warp_running(const RunningSum& r, float c) {
   return make_float2(wm, warp_sum(r.s * to_frame(r.m, wm, c)));
 }
 
+// 16 bytes from global into shared memory, asynchronously; copies_wait waits
+// for all of this thread's copies.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // The two halves of a cluster barrier (release / acquire).
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// hi + lo, |lo| about half a step of hi: sums of a few fp32 values without
+// their roundings (Dekker 1971; Knuth's two-sum).  64-bit arithmetic is two
+// orders slower than fp32 on this GPU: a logarithm in it takes a microsecond.
+struct Pair {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float s = __fadd_rn(hi, x), b = __fadd_rn(s, -hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(hi, -__fadd_rn(s, -b)), __fadd_rn(x, -b)));
+    hi = s;
+  }
+  __device__ __forceinline__ float value() const { return hi + lo; }
+};
+
+// A warp's sum as hi + lo, the additions' roundings kept in lo.
+__device__ __forceinline__ float2 warp_sum_pair(float x) {
+  float hi = x, lo = 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, hi, o), yl = __shfl_xor_sync(0xffffffffu, lo, o);
+    const float sum = __fadd_rn(hi, y);
+    // both lanes of a pair take the larger first: the same rounding in each
+    const float a = fmaxf(hi, y), b = fminf(hi, y);
+    lo = __fadd_rn(__fadd_rn(lo, yl), __fadd_rn(b, -__fadd_rn(sum, -a)));
+    hi = sum;
+  }
+  return make_float2(hi, lo);
+}
+
+// log(hi + lo) as an exact multiple of the leading bits of ln 2 plus a float
+// below 0.36 in size: good to about 5e-8 without 64-bit logarithms, which
+// cost microseconds here.  1 <= hi < 2^31.
+__device__ __forceinline__ float2 log_pair(float2 s) {
+  const uint32_t b = __float_as_uint(s.x);
+  int e = (int)(b >> 23) - 127;
+  float f = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);  // [1, 2)
+  if (f > 1.41421356f) {
+    f *= 0.5f;
+    e += 1;
+  }
+  const float scale = __uint_as_float((uint32_t)(127 - e) << 23);
+  // ln 2 = 0.693145751953125 (15 bits) + 1.42860682030941723e-6
+  const float hi = (float)e * 0.693145751953125f;
+  return make_float2(hi, logf(f) + fmaf((float)e, 1.42860682e-6f, s.y * scale / f));
 }
 
 __device__ __forceinline__ float warp_max(float x) {
