@@ -484,7 +484,7 @@ sv_status spec_distill_grad(const void* student_logits, const int32_t* top_ids,
  *   out_status  [B] int32 or NULL: SV_REQ_BAD_LOGITS when a live beam's row has NaN
  *               or +inf, or a score is NaN or +inf; nothing is kept then.
  *   1 <= W <= SV_MAX_BEAMS, 1 <= n <= SV_MAX_TOP, 0 <= B <= SV_MAX_B, and
- *   ceil(W / 8) * ceil(V / 8192) <= 320 (V <= 2621440 up to 8 beams, 327680 with
+ *   ceil(W / 8) * ceil(V / 8192) <= 256 (V <= 2097152 up to 8 beams, 262144 with
  *   64).  Scores are compared in 64 bits (their row sums are of 32-bit terms).
  * No workspace. */
 sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out_tokens,

@@ -85,7 +85,7 @@ def beam(lib, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(W=0), SHAPE), (dict(W=65), SHAPE), (dict(n=0), SHAPE), (dict(n=129), SHAPE),
-    (dict(V=0), SHAPE), (dict(W=64, V=327681), SHAPE), (dict(W=8, V=2621441), SHAPE),
+    (dict(V=0), SHAPE), (dict(W=64, V=262145), SHAPE), (dict(W=8, V=2097153), SHAPE),
     (dict(dtype=9), DTYPE), (dict(x=None), NULL), (dict(sc=None), NULL), (dict(tok=None), NULL),
     (dict(par=None), NULL), (dict(out=None), NULL), (dict(x=ODD), NULL), (dict(B=0, x=None), 0)])
 def test_beam_select_codes(lib, kw, code):

@@ -401,27 +401,41 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without the Stream object around it (2 us of a
+# 15 us call), where this PyTorch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(device, fn, *args):
     """fn(*args, stream) on the device's current stream, with the device current."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream)
+            rc = fn(*args, _raw_stream(index))
     if rc:
         raise VerifyError(rc)
 
 
+def _need(t, name, device, dtype, shape):
+    """_check, quick where nothing is wrong."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        _check(t, name, device, dtype, shape)
+
+
 def _rows(logits, name, shape):
-    """(dims..., device) of a [B, P, V] / [B, W, V] CUDA logit tensor."""
+    """(dims..., device, dtype code) of a [B, P, V] / [B, W, V] CUDA logit tensor."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
         raise ValueError("%s must be a %s tensor" % (name, shape))
     device = logits.device
     if device.type != "cuda":
         raise ValueError("%s must be a CUDA tensor" % name)
-    _check(logits, name, device)
-    return (*logits.shape, device)
+    if not logits.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return (*logits.shape, device, _dtype_code(logits))
 
 
 def _count(k):
@@ -437,7 +451,7 @@ def _given(out, device, **like):
     for name, (dtype, shape) in like.items():
         t = getattr(out, name)
         if t is not None:
-            _check(t, "out." + name, device, dtype, shape)
+            _need(t, "out." + name, device, dtype, shape)
 
 
 @dataclass
@@ -454,10 +468,10 @@ def spec_top_logits(logits, k, temperature=1.0, out: Optional[TopLogits] = None,
     spec_verify.h): logits [B, P, V] bf16/fp32 CUDA, 1 <= k <= 128, temperature
     > 0 (of the log-sum-exp), lens [B] int32 or None (rows i >= lens[b] are not
     read: pass accept_len to record a verify call's accepted positions)."""
-    B, P, V, device = _rows(logits, "logits", "[B, P, V]")
+    B, P, V, device, code = _rows(logits, "logits", "[B, P, V]")
     k = _count(k)
     if lens is not None:
-        _check(lens, "lens", device, torch.int32, (B,))
+        _need(lens, "lens", device, torch.int32, (B,))
     if out is None:
         shape = (B, P, k)
         out = TopLogits(torch.empty(shape, dtype=torch.int32, device=device),
@@ -469,7 +483,7 @@ def spec_top_logits(logits, k, temperature=1.0, out: Optional[TopLogits] = None,
                lse=(torch.float32, (B, P)), status=(torch.int32, (B, P)))
     _launch(device, _native.lib().spec_top_logits, logits.data_ptr(), k, float(temperature),
             _addr(lens), out.ids.data_ptr(), out.logits.data_ptr(), out.lse.data_ptr(),
-            _addr(out.status), _dtype_code(logits), B, P, V)
+            _addr(out.status), code, B, P, V)
     return out
 
 
@@ -482,18 +496,19 @@ class DistillOutputs:
 
 
 def _distill_args(student_logits, top_ids, top_logits, top_lse, lens, grad_loss):
-    B, P, V, device = _rows(student_logits, "student_logits", "[B, P, V]")
+    B, P, V, device, code = _rows(student_logits, "student_logits", "[B, P, V]")
     if not isinstance(top_ids, torch.Tensor) or top_ids.dim() != 3:
         raise ValueError("top_ids must be a [B, P, k] tensor")
     k = top_ids.shape[2]
-    _check(top_ids, "top_ids", device, torch.int32, (B, P, k))
-    _check(top_logits, "top_logits", device, torch.float32, (B, P, k))
-    for t, name, shape, dtype in ((top_lse, "top_lse", (B, P), torch.float32),
-                                  (lens, "lens", (B,), torch.int32),
-                                  (grad_loss, "grad_loss", (B, P), torch.float32)):
-        if t is not None:
-            _check(t, name, device, dtype, shape)
-    return B, P, V, k, device
+    _need(top_ids, "top_ids", device, torch.int32, (B, P, k))
+    _need(top_logits, "top_logits", device, torch.float32, (B, P, k))
+    if top_lse is not None:
+        _need(top_lse, "top_lse", device, torch.float32, (B, P))
+    if lens is not None:
+        _need(lens, "lens", device, torch.int32, (B,))
+    if grad_loss is not None:
+        _need(grad_loss, "grad_loss", device, torch.float32, (B, P))
+    return B, P, V, k, device, code
 
 
 def spec_distill(student_logits, top_ids, top_logits, temperature=1.0,
@@ -506,16 +521,16 @@ def spec_distill(student_logits, top_ids, top_logits, temperature=1.0,
     or None.  With grad_loss [B, P] fp32 the same pass also writes out.grad,
     the gradient of (grad_loss * loss).sum() in the student's type, for
     ``student_logits.backward(out.grad)``; out.grad may be student_logits."""
-    B, P, V, k, device = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
+    B, P, V, k, device, code = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
                                        grad_loss)
     if out is None:
-        f32 = dict(dtype=torch.float32, device=device)
+        f32 = torch.float32
         out = DistillOutputs(
-            loss=torch.empty((B, P), **f32),
-            stats=torch.empty((B, P, 4), **f32) if stats else None,
-            grad=torch.empty((B, P, V), dtype=student_logits.dtype, device=device)
+            torch.empty((B, P), dtype=f32, device=device),
+            torch.empty((B, P, 4), dtype=f32, device=device) if stats else None,
+            torch.empty((B, P, V), dtype=student_logits.dtype, device=device)
             if grad_loss is not None else None,
-            status=torch.empty((B, P), dtype=torch.int32, device=device) if status else None)
+            torch.empty((B, P), dtype=torch.int32, device=device) if status else None)
     else:
         _given(out, device, loss=(torch.float32, (B, P)), stats=(torch.float32, (B, P, 4)),
                grad=(student_logits.dtype, (B, P, V)), status=(torch.int32, (B, P)))
@@ -523,7 +538,7 @@ def spec_distill(student_logits, top_ids, top_logits, temperature=1.0,
             top_logits.data_ptr(), _addr(top_lse), _addr(lens), _addr(grad_loss),
             float(temperature), out.loss.data_ptr(), _addr(out.stats),
             _addr(out.grad) if grad_loss is not None else None, _addr(out.status),
-            _dtype_code(student_logits), B, P, V, k)
+            code, B, P, V, k)
     return out
 
 
@@ -535,17 +550,17 @@ def spec_distill_grad(student_logits, top_ids, top_logits, temperature, stats, g
     itself is allowed), or None for a new one."""
     if grad_loss is None or stats is None:
         raise ValueError("stats and grad_loss are required")
-    B, P, V, k, device = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
+    B, P, V, k, device, code = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
                                        grad_loss)
-    _check(stats, "stats", device, torch.float32, (B, P, 4))
+    _need(stats, "stats", device, torch.float32, (B, P, 4))
     if grad is None:
         grad = torch.empty((B, P, V), dtype=student_logits.dtype, device=device)
     else:
-        _check(grad, "grad", device, student_logits.dtype, (B, P, V))
+        _need(grad, "grad", device, student_logits.dtype, (B, P, V))
     _launch(device, _native.lib().spec_distill_grad, student_logits.data_ptr(),
             top_ids.data_ptr(), top_logits.data_ptr(), _addr(top_lse), _addr(lens),
             stats.data_ptr(), grad_loss.data_ptr(), float(temperature), grad.data_ptr(),
-            _dtype_code(student_logits), B, P, V, k)
+            code, B, P, V, k)
     return grad
 
 
@@ -562,9 +577,9 @@ def spec_beam_select(logits, scores, n, out: Optional[BeamOutputs] = None, *,
     """One step of beam selection (see spec_verify.h): logits [B, W, V]
     bf16/fp32 CUDA, scores [B, W] fp32 (-inf: a finished beam, not read); the
     n best continuations by scores + log_softmax(logits), best first."""
-    B, W, V, device = _rows(logits, "logits", "[B, W, V]")
+    B, W, V, device, code = _rows(logits, "logits", "[B, W, V]")
     n = _count(n)
-    _check(scores, "scores", device, torch.float32, (B, W))
+    _need(scores, "scores", device, torch.float32, (B, W))
     if out is None:
         shape = (B, n)
         out = BeamOutputs(torch.empty(shape, dtype=torch.int32, device=device),
@@ -576,7 +591,7 @@ def spec_beam_select(logits, scores, n, out: Optional[BeamOutputs] = None, *,
                scores=(torch.float32, (B, n)), status=(torch.int32, (B,)))
     _launch(device, _native.lib().spec_beam_select, logits.data_ptr(), scores.data_ptr(),
             out.tokens.data_ptr(), out.parents.data_ptr(), out.scores.data_ptr(),
-            _addr(out.status), _dtype_code(logits), B, W, V, n)
+            _addr(out.status), code, B, W, V, n)
     return out
 
 
@@ -602,29 +617,31 @@ def spec_beam_reorder(state, parents, out=None, *, lens=None, status=None) -> to
     if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
         raise ValueError("parents must be a [B, W_out] tensor")
     W_out = parents.shape[1]
-    _check(parents, "parents", device, torch.int32, (B, W_out))
+    _need(parents, "parents", device, torch.int32, (B, W_out))
     if lens is not None:
-        _check(lens, "lens", device, torch.int32, (B,))
+        _need(lens, "lens", device, torch.int32, (B,))
     if status is not None:
-        _check(status, "status", device, torch.int32, (B,))
+        _need(status, "status", device, torch.int32, (B,))
+    shape = (G, B, W_out, H, L, D)
     if out is None:
-        out = torch.zeros((G, B, W_out, H, L, D), dtype=state.dtype, device=device)
+        out = torch.zeros(shape, dtype=state.dtype, device=device)
     elif not isinstance(out, torch.Tensor) or out.device != device:
         raise ValueError("out must be a tensor on %s" % device)
     elif out.dtype != state.dtype:
         raise TypeError("out must be %s (got %s)" % (state.dtype, out.dtype))
-    elif tuple(out.shape) != (G, B, W_out, H, L, D):
-        raise ValueError("out must have shape %s (got %s)" % ((G, B, W_out, H, L, D),
-                                                             tuple(out.shape)))
-    for t, name in ((state, "state"), (out, "out")):
-        if D > 1 and t.stride(5) != 1:
-            raise ValueError("the last dimension of %s must be contiguous" % name)
-    size = state.element_size()
-    row_bytes = D * size
+    elif out.shape != shape:
+        raise ValueError("out must have shape %s (got %s)" % (shape, tuple(out.shape)))
     if D == 0:
         raise ValueError("state must have entries of at least one element")
+    size = state.element_size()
+    a0, a1, a2, a3, a4, a5 = state.stride()
+    b0, b1, b2, b3, b4, b5 = out.stride()
+    if D > 1 and (a5 != 1 or b5 != 1):
+        raise ValueError("the last dimension of %s must be contiguous"
+                         % ("state" if a5 != 1 else "out"))
     _launch(device, _native.lib().spec_beam_reorder, state.data_ptr(),
-            _Strides(*[x * size for x in state.stride()[:5]]), _addr(parents), _addr(lens),
-            out.data_ptr(), _Strides(*[x * size for x in out.stride()[:5]]), _addr(status), G, B,
-            W, W_out, H, L, row_bytes)
+            _Strides(a0 * size, a1 * size, a2 * size, a3 * size, a4 * size), _addr(parents),
+            _addr(lens), out.data_ptr(),
+            _Strides(b0 * size, b1 * size, b2 * size, b3 * size, b4 * size), _addr(status), G, B,
+            W, W_out, H, L, D * size)
     return out

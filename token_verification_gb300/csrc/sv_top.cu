@@ -30,13 +30,18 @@
 namespace sv {
 namespace {
 
+#ifndef RING_BF16
+#define RING_BF16 3
+#define RING_F32 2
+#define TOPB 3
+#endif
 constexpr int kTopThreads = 256;
 constexpr int kTopWarps = kTopThreads / kWarp;
 constexpr int kTopSpan = 8192;        // elements of a CTA's iteration: 32 a thread
 constexpr int kMaxItems = 64;         // (row, slice) items per cluster
 constexpr int kMaxUnits = 512;        // units per cluster
 constexpr int kMaxCands = 1024;       // candidates of a cluster, 32-element groups of a CTA
-constexpr int kMaxTables = 320;       // iterations of a CTA over its items: 512 bytes each
+constexpr int kMaxTables = 256;       // iterations of a CTA over its items: 512 bytes each
 constexpr int kRankAll = 384;         // lists longer than this are cut to the bound first
 
 struct TopParams {
@@ -54,16 +59,13 @@ struct TopParams {
   int slices, slice;    // slices per row, elements per slice (a multiple of 256)
   int iters;            // iterations per item
   int upi;              // units per item (a power of two)
+  int table_bytes;
   float cc;             // log2(e) / T
   float T;
   RowSpan span;
 };
 
 struct alignas(16) TopShared {
-  unsigned long long key[kMaxCands];  // candidates; record: (ordered logit, ~index), a total
-                                      // order; beams: the ordered score, idx = w * V + v
-  int idx[kMaxCands];
-  int rank[kMaxCands];                // until the list is sorted: the groups to read again
   float2 part[kMaxItems][kTopWarps];  // per item and warp: {max, sum of 2^((l - max) c)}
   float unit[kMaxUnits];              // unit maxes, item by item
   double off[SV_MAX_BEAMS];           // beams: score - lse of each row (-inf: no candidates)
@@ -73,6 +75,25 @@ struct alignas(16) TopShared {
   unsigned hist[256];
   int flag[2][kTopWarps];
   int n_hits, n_cands, overflow, bad, pick[4];
+};
+
+// The candidates, in the memory of the load stages once all are consumed.
+struct alignas(16) Lists {
+  unsigned long long key[kMaxCands];  // record: (ordered logit, ~index), a total order;
+                                      // beams: the ordered score, idx = w * V + v
+  int idx[kMaxCands];
+  int rank[kMaxCands];                // until the list is sorted: the groups to read again
+};
+
+// Load stages: each warp streams 1024-element chunks through its own ring by
+// asynchronous copies (a word more than a chunk, for rows off 16-byte
+// boundaries); no barrier but the warp's own.
+template <typename T>
+struct Ring {
+  static constexpr int kBytes = kChunk * (int)sizeof(T) + 16;
+  static constexpr int kStages = sizeof(T) == 2 ? RING_BF16 : RING_F32;
+  static constexpr int kWarpBytes = kBytes * kStages;
+  static constexpr int kTotal = kWarpBytes * kTopWarps;
 };
 
 // The upper 16 bits of v rounded up: a bf16 value >= v (v itself for bf16).
@@ -120,7 +141,7 @@ __device__ float unit_bound(TopShared& s, int units, int n) {
 }
 
 template <bool kBeam>
-__device__ __forceinline__ void set_candidate(TopShared& s, int o, float l, double off, int idx) {
+__device__ __forceinline__ void set_candidate(Lists& s, int o, float l, double off, int idx) {
   s.key[o] = kBeam ? ordered(off + (double)l)
                    : ((unsigned long long)ordered(l) << 32) | (uint32_t)~idx;
   s.idx[o] = idx;
@@ -129,8 +150,8 @@ __device__ __forceinline__ void set_candidate(TopShared& s, int o, float l, doub
 // One row's n largest finite elements by radix descent, appended to the list
 // from `at` on (a whole-CTA call); returns how many.
 template <typename T, bool kBeam>
-__device__ int select_row_slow(TopShared& s, const T* row, int V, int n, double off, int base,
-                               int at) {
+__device__ int select_row_slow(TopShared& s, Lists& ls, const T* row, int V, int n, double off,
+                               int base, int at) {
   const int t = threadIdx.x;
   auto key_of = [&](int j) {  // (logit in order, index from the end), 0 if not finite
     const float l = j < V ? load_logit(row, j) : -INFINITY;
@@ -177,7 +198,7 @@ __device__ int select_row_slow(TopShared& s, const T* row, int V, int n, double 
     const unsigned long long k = key_of(j0 + t);
     if (k != 0 && k >= cut) {
       const int o = atomicAdd(&s.pick[3], 1);
-      set_candidate<kBeam>(s, o, load_logit(row, j0 + t), off, base + j0 + t);
+      set_candidate<kBeam>(ls, o, load_logit(row, j0 + t), off, base + j0 + t);
     }
   }
   __syncthreads();
@@ -186,7 +207,7 @@ __device__ int select_row_slow(TopShared& s, const T* row, int V, int n, double 
 
 // Whether entry j of the list comes before an entry of (key, idx).
 template <bool kBeam>
-__device__ __forceinline__ bool before(const TopShared& s, int j, unsigned long long key, int idx) {
+__device__ __forceinline__ bool before(const Lists& s, int j, unsigned long long key, int idx) {
   const unsigned long long kj = s.key[j];
   return kj > key || (kBeam && kj == key && s.idx[j] < idx);
 }
@@ -195,7 +216,7 @@ __device__ __forceinline__ bool before(const TopShared& s, int j, unsigned long 
 // whole CTA, each entry's comparisons shared by as many threads as there are
 // warps for all entries.
 template <bool kBeam>
-__device__ void rank_list(TopShared& s, int count) {
+__device__ void rank_list(Lists& s, int count) {
   const int t = threadIdx.x;
   for (int i = t; i < count; i += kTopThreads) s.rank[i] = 0;
   __syncthreads();
@@ -224,15 +245,15 @@ __device__ void rank_list(TopShared& s, int count) {
 }
 
 // Cuts the list to the entries at or above its n-th largest 32-bit key prefix.
-__device__ int prune(TopShared& s, int count, int n) {
+__device__ int prune(TopShared& s, Lists& ls, int count, int n) {
   constexpr int kPer = kMaxCands / kTopThreads;
   unsigned long long k[kPer];
   int ix[kPer];
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     const int i = q * kTopThreads + threadIdx.x;
-    k[q] = i < count ? s.key[i] : 0ull;
-    ix[q] = i < count ? s.idx[i] : 0;
+    k[q] = i < count ? ls.key[i] : 0ull;
+    ix[q] = i < count ? ls.idx[i] : 0;
   }
   uint32_t t = 0;
   for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
@@ -254,8 +275,8 @@ __device__ int prune(TopShared& s, int count, int n) {
   for (int q = 0; q < kPer; ++q)
     if (q * kTopThreads + threadIdx.x < count && (uint32_t)(k[q] >> 32) >= t) {
       const int o = atomicAdd(&s.pick[1], 1);
-      s.key[o] = k[q];
-      s.idx[o] = ix[q];
+      ls.key[o] = k[q];
+      ls.idx[o] = ix[q];
     }
   __syncthreads();
   return s.pick[1];
@@ -274,15 +295,16 @@ __device__ __forceinline__ void write_slot(const TopParams& p, long long grp, in
 }
 
 template <typename T, bool kAligned, bool kBeam>
-__global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) {
+__global__ void __launch_bounds__(kTopThreads, TOPB) top_kernel(const TopParams p) {
   constexpr int VEC = Group<T>::VEC;
-  constexpr int UN = 4;                                        // 16-byte groups per load batch
-  constexpr int kBatches = kTopSpan / (kTopThreads * VEC * UN);  // 1 (bf16) or 2 per iteration
-  constexpr int kGroups = UN * kBatches;                       // of a table entry: 32 elements
+  constexpr int kGroups = kChunk / (kWarp * VEC);  // 16-byte groups of a lane: 32 elements
+  using R = Ring<T>;
   extern __shared__ __align__(16) unsigned char smem[];
   TopShared& s = *reinterpret_cast<TopShared*>(smem);
   // per iteration over this CTA's items, the thread's 32 elements' max
   uint16_t* table = reinterpret_cast<uint16_t*>(smem + sizeof(TopShared));
+  unsigned char* rings = smem + sizeof(TopShared) + p.table_bytes;
+  Lists& ls = *reinterpret_cast<Lists*>(rings);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const long long grp = blockIdx.x / C;
@@ -320,25 +342,41 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
     const bool live = !kBeam || p.scores[rowid] != -INFINITY;
     RunningSum r;
     if (live) {
-      // two register buffers: a batch's loads are in flight while the one
-      // before it is reduced
-      uint4 g0[UN], g1[UN];
-      auto load = [&](uint4(&g)[UN], int i) {
-        load_groups<T, kAligned>(g, row, e0 + (i * UN * kTopThreads + t) * VEC, kTopThreads * VEC,
-                                 e1, p.V, p.span);
+      const int chunks = (e1 - e0 + kChunk - 1) / kChunk;
+      const int todo = (chunks - warp + kTopWarps - 1) / kTopWarps;  // this warp's (may be <= 0)
+      const uint32_t off = kAligned ? 0u : (uint32_t)(uintptr_t)row & 15u;
+      const uint32_t ring = smem_u32(rings) + warp * R::kWarpBytes;
+      auto issue = [&](int i) {  // iteration i's chunk into its stage
+        if (i < todo) {
+          const int j = e0 + (i * kTopWarps + warp) * kChunk;
+          load_chunk_async<T, kAligned>(ring + i % R::kStages * R::kBytes, row, j, min(j + kChunk, e1),
+                                        off, p.span);
+        }
+        copies_commit();
       };
-      const int batches = p.iters * kBatches;
-      load(g0, 0);
-      for (int i = 0; i < batches; i += 2) {
-        if (i + 1 < batches) load(g1, i + 1);
-        float gm = r.add(g0, p.cc, tag);
-        if (kBatches == 1) mine_table[i * kTopThreads] = up_bf16(gm);
-        if (i + 1 >= batches) break;
-        if (i + 2 < batches) load(g0, i + 2);
-        const float gm1 = r.add(g1, p.cc, tag);
-        if (kBatches == 1) mine_table[(i + 1) * kTopThreads] = up_bf16(gm1);
-        else mine_table[i / 2 * kTopThreads] = up_bf16(max_nan(gm, gm1));
+#pragma unroll
+      for (int i = 0; i < R::kStages - 1; ++i) issue(i);
+      for (int i = 0; i < p.iters; ++i) {
+        if (i >= todo) {
+          mine_table[i * kTopThreads] = 0xff80u;
+          continue;
+        }
+        copies_wait_but<R::kStages - 2>();
+        __syncwarp();  // every lane's copies of this stage landed; the stage before is read
+        uint4 g[kGroups];
+        const uint32_t stage = ring + i % R::kStages * R::kBytes;
+        const int j = e0 + (i * kTopWarps + warp) * kChunk;
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+          const uint32_t at = stage + (u * kWarp + lane) * 16;
+          g[u] = lds128(at);
+          if (!kAligned && off) g[u] = shift_pair(g[u], lds128(at + 16), off);
+        }
+        if (j + kChunk > e1) clip_chunk<T>(g, j, e1);
+        issue(i + R::kStages - 1);
+        mine_table[i * kTopThreads] = up_bf16(r.add(g, p.cc, tag));
       }
+      __syncwarp();  // (the next item refills the stages)
     } else {
       for (int i = 0; i < p.iters; ++i) mine_table[i * kTopThreads] = 0xff80u;
     }
@@ -437,23 +475,24 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
       if (hits) {
         int h = atomicAdd(&s.n_hits, __popc(hits));
         for (; hits; hits &= hits - 1u, ++h)
-          if (h < kMaxCands) s.rank[h] = mine * p.iters * kTopThreads + 8 * v + __ffs(hits) - 1;
+          if (h < kMaxCands) ls.rank[h] = mine * p.iters * kTopThreads + 8 * v + __ffs(hits) - 1;
       }
     }
   }
   __syncthreads();
   TopShared* lead = C > 1 ? cluster.map_shared_rank(&s, 0) : &s;
+  Lists* lead_ls = C > 1 ? cluster.map_shared_rank(&ls, 0) : &ls;
   const int hits = s.n_hits;
   if (hits > kMaxCands) {
     if (t == 0) lead->overflow = 1;
   } else {
     for (int q = t; q < hits * kGroups; q += kTopThreads) {
-      const int at = s.rank[q / kGroups], u = q % kGroups;
+      const int at = ls.rank[q / kGroups], u = q % kGroups;
       const int mi = at / kTopThreads, ti = at % kTopThreads;
       const int mine = mi / p.iters, i = mi - mine * p.iters;
       const int it = rank + mine * C;
       const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
-      const int j = e0 + ((i * kGroups + u) * kTopThreads + ti) * VEC;
+      const int j = e0 + (i * kTopWarps + ti / kWarp) * kChunk + (u * kWarp + ti % kWarp) * VEC;
       if (j >= min(e0 + p.slice, p.V)) continue;
       const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
       const uint4 g = load_group<T, kAligned>(row, j, p.V, p.span);
@@ -468,8 +507,8 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
           if (in >> e & 1u) {
             // the logit now, the key when the list is complete
             if (o < kMaxCands) {
-              lead->key[o] = __float_as_uint(Lane<T, VEC>::get(g, e));
-              lead->idx[o] = w * p.V + j + e;
+              lead_ls->key[o] = __float_as_uint(Lane<T, VEC>::get(g, e));
+              lead_ls->idx[o] = w * p.V + j + e;
             }
             ++o;
           }
@@ -487,35 +526,40 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const TopParams p) 
       const double off = kBeam ? s.off[w] : 0.0;
       if (off == -INFINITY) continue;
       const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
-      const int got = select_row_slow<T, kBeam>(s, row, p.V, p.n, off, w * p.V, count);
+      const int got = select_row_slow<T, kBeam>(s, ls, row, p.V, p.n, off, w * p.V, count);
       // keep the n best of the rows so far (at most 2 n <= 256 entries, one a thread)
       const int total = count + got;
-      rank_list<kBeam>(s, total);
-      const unsigned long long key = t < total ? s.key[t] : 0;
-      const int idx = t < total ? s.idx[t] : 0, r = t < total ? s.rank[t] : p.n;
+      rank_list<kBeam>(ls, total);
+      const unsigned long long key = t < total ? ls.key[t] : 0;
+      const int idx = t < total ? ls.idx[t] : 0, r = t < total ? ls.rank[t] : p.n;
       __syncthreads();
       if (r < p.n) {
-        s.key[r] = key;
-        s.idx[r] = idx;
+        ls.key[r] = key;
+        ls.idx[r] = idx;
       }
       count = min(total, p.n);
       __syncthreads();
     }
   } else {
     for (int i = t; i < count; i += kTopThreads) {
-      const int idx = s.idx[i];
-      set_candidate<kBeam>(s, i, __uint_as_float((uint32_t)s.key[i]),
+      const int idx = ls.idx[i];
+      set_candidate<kBeam>(ls, i, __uint_as_float((uint32_t)ls.key[i]),
                            kBeam ? s.off[idx / p.V] : 0.0, idx);
     }
     __syncthreads();
-    if (count > kRankAll) count = prune(s, count, p.n);
+    if (count > kRankAll) count = prune(s, ls, count, p.n);
   }
-  rank_list<kBeam>(s, count);
+  rank_list<kBeam>(ls, count);
   for (int i = t; i < count; i += kTopThreads) {
-    const int r = s.rank[i];
-    if (r < p.n) write_slot<kBeam>(p, grp, r, s.key[i], s.idx[i]);
+    const int r = ls.rank[i];
+    if (r < p.n) write_slot<kBeam>(p, grp, r, ls.key[i], ls.idx[i]);
   }
   for (int j = count + t; j < p.n; j += kTopThreads) write_slot<kBeam>(p, grp, j, 0, -1);
+}
+
+template <typename T>
+constexpr int union_bytes() {
+  return Ring<T>::kTotal > (int)sizeof(Lists) ? Ring<T>::kTotal : (int)sizeof(Lists);
 }
 
 template <typename T, bool kAligned, bool kBeam>
@@ -524,11 +568,11 @@ cudaError_t launch_top(const TopParams& p, long long groups, int C, cudaStream_t
   auto* fn = top_kernel<T, kAligned, kBeam>;
   const cudaError_t err = per_device(once, nullptr, [&](int&) {
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(TopShared) + kMaxTables * kTopThreads * 2);
+                                (int)sizeof(TopShared) + kMaxTables * kTopThreads * 2 +
+                                    union_bytes<T>());
   });
   if (err != cudaSuccess) return err;
-  const int per_cta = (p.W * p.slices + C - 1) / C;
-  const size_t smem = sizeof(TopShared) + (size_t)per_cta * p.iters * kTopThreads * 2;
+  const size_t smem = sizeof(TopShared) + p.table_bytes + union_bytes<T>();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * C));
   cfg.blockDim = dim3(kTopThreads);
@@ -569,6 +613,7 @@ sv_status run_top(TopParams& p, sv_dtype dtype, long long groups, cudaStream_t s
   p.upi = kTopThreads;
   while (p.upi > kTopWarps && items * p.upi > kMaxUnits) p.upi /= 2;
   while (p.upi > kTopWarps && items * p.upi / 2 >= 4 * p.n) p.upi /= 2;
+  p.table_bytes = (items + C - 1) / C * p.iters * kTopThreads * 2;
   const size_t esz = dtype == SV_BF16 ? 2 : 4;
   const char* first = static_cast<const char*>(p.logits);
   p.span.first = first;

@@ -263,6 +263,67 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>  // all but the last N committed groups
+__device__ __forceinline__ void copies_wait_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A warp's copies of elements j .. end - 1 (at most a chunk) of a row into the
+// stage at `dst`: the aligned words around them, `off` the misalignment of
+// element j.  A word that is not all inside the tensor goes by element.
+template <typename T, bool kAligned>
+__device__ __forceinline__ void load_chunk_async(uint32_t dst, const T* row, int j, int end,
+                                                 uint32_t off, const RowSpan& span) {
+  const char* a = reinterpret_cast<const char*>(row + j) - off;
+  const int words = ((end - j) * (int)sizeof(T) + (int)off + 15) / 16;
+  constexpr int kFull = kChunk * (int)sizeof(T) / 16;
+  if (words >= kFull && a >= span.first && a + 16 * (kFull + 1) <= span.last) {
+#pragma unroll
+    for (int q = 0; q < kFull / kWarp; ++q) {
+      const int w = q * kWarp + lane_id();
+      copy16_async(dst + 16 * w, a + 16 * w);
+    }
+    if (!kAligned && words > kFull && lane_id() == 0) copy16_async(dst + 16 * kFull, a + 16 * kFull);
+    return;
+  }
+  for (int w = lane_id(); w < words; w += kWarp) {
+    const char* p = a + 16 * w;
+    if (p >= span.first && p + 16 <= span.last) {
+      copy16_async(dst + 16 * w, p);
+    } else {
+      uint4 v = Lane<T, Group<T>::VEC>::pad();
+#pragma unroll
+      for (int e = 0; e < Group<T>::VEC; ++e) {
+        const char* x = p + e * (int)sizeof(T);
+        if (x >= span.first && x < span.last) put(v, e, *reinterpret_cast<const T*>(x));
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 16 * w), "r"(v.x),
+                   "r"(v.y), "r"(v.z), "r"(v.w)
+                   : "memory");
+    }
+  }
+}
+
+// A lane's groups of the chunk at element j: elements from `end` on become -inf.
+template <typename T, int N>
+__device__ __forceinline__ void clip_chunk(uint4 (&g)[N], int j, int end) {
+  constexpr int VEC = Group<T>::VEC;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int first = j + (u * kWarp + lane_id()) * VEC;
+    if (first >= end) {
+      g[u] = Lane<T, VEC>::pad();
+    } else if (first + VEC > end) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (first + e >= end) Lane<T, VEC>::kill(g[u], e);
+    }
+  }
+}
+
 // The two halves of a cluster barrier (release / acquire).
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
