@@ -486,10 +486,15 @@ sv_status spec_distill_grad(const void* student_logits, const int32_t* top_ids,
  *   1 <= W <= SV_MAX_BEAMS, 1 <= n <= SV_MAX_TOP, 0 <= B <= SV_MAX_B, and
  *   ceil(W / 8) * ceil(V / 8192) <= 256 (V <= 2097152 up to 8 beams, 262144 with
  *   64).  Scores are compared in 64 bits (their row sums are of 32-bit terms).
- * No workspace. */
+ *   workspace   >= spec_beam_workspace_size(dtype, B, W, V, n) bytes (0 for small
+ *               calls), 16-byte aligned; SV_ERR_WORKSPACE otherwise.  It needs no
+ *               preparation and holds nothing between calls; calls that may
+ *               overlap need one each. */
+size_t spec_beam_workspace_size(sv_dtype dtype, int B, int W, int V, int n);
 sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out_tokens,
                            int32_t* out_parents, float* out_scores, int32_t* out_status,
-                           sv_dtype dtype, int B, int W, int V, int n, sv_stream_t stream);
+                           sv_dtype dtype, int B, int W, int V, int n, void* workspace,
+                           size_t ws_bytes, sv_stream_t stream);
 
 /* Reordering of per-beam states: out[g, b, w, h, l] = state[g, b, parents[b, w],
  * h, l] for l < lens[b], each entry a run of row_bytes contiguous bytes.  It

@@ -77,10 +77,11 @@ def test_distill_grad_codes(lib, kw, code):
 
 
 def beam(lib, **kw):
-    a = dict(x=FAKE, sc=FAKE, tok=FAKE, par=FAKE, out=FAKE, dtype=1, B=2, W=4, V=100, n=8)
+    a = dict(x=FAKE, sc=FAKE, tok=FAKE, par=FAKE, out=FAKE, dtype=1, B=2, W=4, V=100, n=8,
+             ws=None, ws_bytes=0)
     a.update(kw)
     return lib.spec_beam_select(a["x"], a["sc"], a["tok"], a["par"], a["out"], None, a["dtype"],
-                                a["B"], a["W"], a["V"], a["n"], None)
+                                a["B"], a["W"], a["V"], a["n"], a["ws"], a["ws_bytes"], None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -90,6 +91,17 @@ def beam(lib, **kw):
     (dict(par=None), NULL), (dict(out=None), NULL), (dict(x=ODD), NULL), (dict(B=0, x=None), 0)])
 def test_beam_select_codes(lib, kw, code):
     assert beam(lib, **kw) == code
+
+
+def test_beam_workspace(lib):
+    assert lib.spec_beam_workspace_size(1, 1, 4, 32000, 8) == 0
+    big = dict(B=256, W=8, V=128256, n=16)
+    need = lib.spec_beam_workspace_size(1, 256, 8, 128256, 16)
+    assert need >= 256 * 8 * 16 * 8
+    assert beam(lib, **big) == 6
+    assert beam(lib, ws=FAKE, ws_bytes=need - 1, **big) == 6
+    assert beam(lib, ws=FAKE + 8, ws_bytes=need, **big) == 6
+    assert lib.spec_beam_workspace_size(1, 256, 65, 128256, 16) == 0
 
 
 I5 = ctypes.c_int64 * 5

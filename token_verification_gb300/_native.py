@@ -19,6 +19,7 @@ SYMBOLS = (
     "spec_verify_typical", "spec_verify_tree_typical", "spec_verify_tree_workspace_size",
     "spec_verify_tree_sample", "spec_verify_set_wait_limit_ns", "spec_verify_wait_limit_ns",
     "spec_top_logits", "spec_distill", "spec_distill_grad", "spec_beam_select",
+    "spec_beam_workspace_size",
     "spec_beam_reorder",
 )
 
@@ -82,7 +83,9 @@ def lib():
         l.spec_distill.restype = I
         l.spec_distill_grad.argtypes = [P, P, P, P, P, P, P, F, P, I, I, I, I, I, P]
         l.spec_distill_grad.restype = I
-        l.spec_beam_select.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P]
+        l.spec_beam_workspace_size.argtypes = [I, I, I, I, I]
+        l.spec_beam_workspace_size.restype = Z
+        l.spec_beam_select.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, Z, P]
         l.spec_beam_select.restype = I
         l.spec_beam_reorder.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]
         l.spec_beam_reorder.restype = I

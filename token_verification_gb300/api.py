@@ -589,9 +589,13 @@ def spec_beam_select(logits, scores, n, out: Optional[BeamOutputs] = None, *,
     else:
         _given(out, device, tokens=(torch.int32, (B, n)), parents=(torch.int32, (B, n)),
                scores=(torch.float32, (B, n)), status=(torch.int32, (B,)))
-    _launch(device, _native.lib().spec_beam_select, logits.data_ptr(), scores.data_ptr(),
+    lib = _native.lib()
+    need = lib.spec_beam_workspace_size(code, B, W, V, n)
+    # scratch of this call alone (stream-ordered, and a captured graph's own)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _launch(device, lib.spec_beam_select, logits.data_ptr(), scores.data_ptr(),
             out.tokens.data_ptr(), out.parents.data_ptr(), out.scores.data_ptr(),
-            _addr(out.status), code, B, W, V, n)
+            _addr(out.status), code, B, W, V, n, _addr(ws), need)
     return out
 
 

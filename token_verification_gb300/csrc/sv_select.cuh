@@ -1,0 +1,426 @@
+// sv_select.cuh - selection of the n largest values of streamed rows: the parts
+// shared by the cluster kernel (sv_top.cu) and the row kernel (sv_toprows.cu).
+//
+// One pass over a row reads every logit once and keeps, per thread, a running
+// softmax sum and max, and per 32 elements their max (rounded up to bf16, in
+// shared memory).  The selection follows from the thread maxes alone: if
+// `units` disjoint parts of the data have maxes u_1.., the n-th largest of
+// them is a bound that at least n elements reach, so every kept element is at
+// or above it, and little else is: with n of U parts occupied about
+// U ln(U / (U - n)) elements (74 for n = 64 of 256).  Only the 32-element
+// groups whose max reaches the bound are read again (from L2), their elements
+// at or above it are listed, and the list is sorted by counting.  When the
+// list does not fit (long rows of equal logits), each row is selected by radix
+// descent on whole-number keys, 8 bits a pass.
+#pragma once
+
+#include "../../include/spec_verify.h"
+#include "sv_launch.h"
+#include "sv_rows.cuh"
+#include "sv_vec.cuh"
+
+namespace sv {
+
+constexpr int kTopSpan = 8192;        // elements of a CTA's iteration: 32 a thread
+constexpr int kMaxTables = 256;       // iterations of a CTA over its items: 512 bytes each
+constexpr int kRowsSmem = 112 * 1024;  // shared memory of a CTA of the row kernel: two on an SM
+
+struct TopParams {
+  const void* logits;   // [B*P, V] (record) or [B*W, V] (beams)
+  const int* lens;      // [B] or null (record)
+  const float* scores;  // [B*W] (beams)
+  int* out_ids;         // [rows, n] (record, row kernel), tokens [B, n] (beams)
+  int* out_parents;     // beams: [B, n]
+  float* out_values;    // logits [rows, n], scores [B, n]
+  float* out_lse;       // record: [B*P]
+  double* out_off;      // row kernel for beams: [B*W] score - lse (-inf: no candidates, NaN: bad)
+  int* out_status;
+  int P;                // record: rows per request
+  int W;                // rows per cluster (record: 1)
+  int V, n;
+  int slices, slice;    // slices per row, elements per slice (a multiple of 256)
+  int iters;            // iterations per item
+  int upi;              // units per item (a power of two)
+  int table_bytes;
+  float cc;             // log2(e) / T
+  float T;
+  char* first;          // the logits' memory
+  char* last;
+};
+
+// Whether rows of V logits fit the row kernel's shared memory.
+bool top_rows_fit(sv_dtype dtype, int V);
+// Rows one CTA each, as many CTAs as fit taking row after row (sv_toprows.cu).
+cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long rows,
+                            cudaStream_t stream);
+// The n best of each request's W row selections.
+cudaError_t launch_beam_merge(const TopParams& p, const int* ids, const float* values,
+                              const double* off, int B, cudaStream_t stream);
+
+namespace {
+
+constexpr int kTopThreads = 256;
+constexpr int kTopWarps = kTopThreads / kWarp;
+constexpr int kEntry = 32;            // consecutive elements of a table entry: one lane's of a chunk
+constexpr int kMaxUnits = 512;        // units per cluster
+constexpr int kMaxCands = 1024;       // candidates of a cluster, 32-element groups of a CTA
+constexpr int kRankAll = 384;         // lists longer than this are cut to the bound first
+
+// A barrier of 256 threads: the whole CTA of the cluster kernel (barrier 0),
+// the selecting half of the row kernel's.
+template <int kBar>
+__device__ __forceinline__ void group_sync() {
+  asm volatile("bar.sync %0, 256;" ::"n"(kBar) : "memory");
+}
+
+// Scratch of a selection.
+struct Select {
+  unsigned hist[256];
+  int flag[2][kTopWarps];
+  int n_hits, n_cands, overflow, bad, pick[4];
+};
+
+// The candidates.
+struct alignas(16) Lists {
+  unsigned long long key[kMaxCands];  // record: (ordered logit, ~index), a total order;
+                                      // beams: the ordered score, idx = w * V + v
+  int idx[kMaxCands];
+  int rank[kMaxCands];                // until the list is sorted: the groups to read again
+};
+
+// Load stages: each warp streams 1024-element chunks through its own ring by
+// asynchronous copies (a word more than a chunk, for rows off 16-byte
+// boundaries); no barrier but the warp's own.
+template <typename T>
+struct Ring {
+  static constexpr int kBytes = kChunk * (int)sizeof(T) + 16;
+  static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
+  static constexpr int kWarpBytes = kBytes * kStages;
+  static constexpr int kTotal = kWarpBytes * kTopWarps;
+};
+
+// The upper 16 bits of v rounded up: a bf16 value >= v (v itself for bf16).
+__device__ __forceinline__ uint16_t up_bf16(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return (uint16_t)((b & 0x80000000u) ? b >> 16 : (b + 0xffffu) >> 16);
+}
+
+// The n-th largest of the cluster's unit bounds to 16 bits (rounded down); -inf
+// when fewer than n are finite.  A call of the group: each warp holds all units
+// as ordered keys, and every round tests one threshold per warp, so the range
+// of keys shrinks ninefold (a bisection by one warp took 4000 cycles of a
+// row's 87000; this takes a quarter).
+template <int kPer, int kBar>
+__device__ float unit_bound(Select& s, const float* unit, int units, int n) {
+  const int warp = threadIdx.x % kTopThreads / kWarp;
+  int k[kPer], hi = 0, lo = 0xffff;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = j * kWarp + lane_id();
+    const float v = i < units ? unit[i] : -INFINITY;
+    k[j] = v > -INFINITY ? (int)(ordered(v) >> 16) : 0;  // below every finite value's key
+    hi = max(hi, k[j]);
+    lo = min(lo, k[j]);
+  }
+  if (units < n) return -INFINITY;
+  lo = __reduce_min_sync(0xffffffffu, lo);       // at least n units reach lo
+  hi = __reduce_max_sync(0xffffffffu, hi) + 1;   // fewer than n reach hi
+  for (int round = 0; hi - lo > 1; ++round) {
+    const int step = (hi - lo + kTopWarps) / (kTopWarps + 1), at = lo + step * (warp + 1);
+    unsigned c = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) c += k[j] >= at ? 1u : 0u;
+    const bool ok = at < hi && (int)__reduce_add_sync(0xffffffffu, c) >= n;
+    // the warps' answers are monotone; two sets of flags need one barrier a round
+    if (lane_id() == 0) s.flag[round & 1][warp] = ok ? 1 : 0;
+    group_sync<kBar>();
+    const unsigned yes = __ballot_sync(0xffffffffu, lane_id() < kTopWarps &&
+                                                        s.flag[round & 1][lane_id() % kTopWarps]);
+    const int up = __popc(yes);
+    hi = min(hi, lo + step * (up + 1));
+    lo += step * up;
+  }
+  return lo ? of_ordered((uint32_t)lo << 16) : -INFINITY;
+}
+
+template <int kBar>
+__device__ __forceinline__ float unit_bound(Select& s, const float* unit, int units, int n) {
+  return units <= 64    ? unit_bound<2, kBar>(s, unit, units, n)
+         : units <= 256 ? unit_bound<8, kBar>(s, unit, units, n)
+                        : unit_bound<16, kBar>(s, unit, units, n);
+}
+
+template <bool kBeam>
+__device__ __forceinline__ void set_candidate(Lists& s, int o, float l, double off, int idx) {
+  s.key[o] = kBeam ? ordered(off + (double)l)
+                   : ((unsigned long long)ordered(l) << 32) | (uint32_t)~idx;
+  s.idx[o] = idx;
+}
+
+// One row's n largest finite elements by radix descent, appended to the list
+// from `at` on (a call of the group); returns how many.
+template <typename T, bool kBeam, int kBar>
+__device__ int select_row_slow(Select& s, Lists& ls, const T* row, int V, int n, double off,
+                               int base, int at) {
+  const int t = threadIdx.x % kTopThreads;
+  auto key_of = [&](int j) {  // (logit in order, index from the end), 0 if not finite
+    const float l = j < V ? load_logit(row, j) : -INFINITY;
+    return l > -INFINITY
+               ? ((unsigned long long)ordered(l) << 24) | (unsigned long long)(0xffffff - j)
+               : 0ull;
+  };
+  unsigned long long cut = 0;
+  int need = n;
+  bool all = false;
+  for (int shift = 48; shift >= 0; shift -= 8) {
+    for (int i = t; i < 256; i += kTopThreads) s.hist[i] = 0;
+    group_sync<kBar>();
+    for (int j0 = 0; j0 < V; j0 += kTopThreads) {
+      const unsigned long long k = key_of(j0 + t);
+      const bool in = k != 0 && ((k ^ cut) >> (shift + 8)) == 0;
+      const unsigned digit = in ? (unsigned)(k >> shift) & 255u : 256u;
+      const unsigned peers = __match_any_sync(0xffffffffu, digit);
+      if (in && lane_id() == __ffs(peers) - 1) atomicAdd(&s.hist[digit], (unsigned)__popc(peers));
+    }
+    group_sync<kBar>();
+    if (t == 0) {
+      int d = 255, above = 0;
+      for (; d > 0 && above + (int)s.hist[d] < need; --d) above += (int)s.hist[d];
+      s.pick[0] = d;
+      s.pick[1] = above;
+      s.pick[2] = (int)s.hist[d];
+    }
+    group_sync<kBar>();
+    const int above = s.pick[1], here = s.pick[2];
+    cut |= (unsigned long long)s.pick[0] << shift;
+    group_sync<kBar>();
+    if (above + here < need) {  // (first pass only) fewer than n finite elements: all of them
+      all = true;
+      break;
+    }
+    need -= above;
+    if (here == need) break;  // every element of this prefix is kept
+  }
+  if (all) cut = 1;
+  if (t == 0) s.pick[3] = at;
+  group_sync<kBar>();
+  for (int j0 = 0; j0 < V; j0 += kTopThreads) {
+    const unsigned long long k = key_of(j0 + t);
+    if (k != 0 && k >= cut) {
+      const int o = atomicAdd(&s.pick[3], 1);
+      set_candidate<kBeam>(ls, o, load_logit(row, j0 + t), off, base + j0 + t);
+    }
+  }
+  group_sync<kBar>();
+  return s.pick[3] - at;
+}
+
+// Whether entry j of the list comes before an entry of (key, idx).
+template <bool kBeam>
+__device__ __forceinline__ bool before(const Lists& s, int j, unsigned long long key, int idx) {
+  const unsigned long long kj = s.key[j];
+  return kj > key || (kBeam && kj == key && s.idx[j] < idx);
+}
+
+// rank[i] = the number of entries that come before entry i, i < count: the
+// whole group, each entry's comparisons shared by as many threads as there are
+// warps for all entries.
+template <bool kBeam, int kBar>
+__device__ void rank_list(Lists& s, int count) {
+  const int t = threadIdx.x % kTopThreads;
+  for (int i = t; i < count; i += kTopThreads) s.rank[i] = 0;
+  group_sync<kBar>();
+  const int width = (count + kWarp - 1) / kWarp * kWarp;
+  if (width <= kTopThreads / 2) {
+    const int ways = kTopThreads / width, way = t / width, i = t - way * width;
+    if (way < ways && i < count) {
+      const unsigned long long key = s.key[i];
+      const int idx = s.idx[i];
+      int r = 0;
+#pragma unroll 4
+      for (int j = way; j < count; j += ways) r += before<kBeam>(s, j, key, idx) ? 1 : 0;
+      atomicAdd(&s.rank[i], r);
+    }
+  } else {
+    for (int i = t; i < count; i += kTopThreads) {
+      const unsigned long long key = s.key[i];
+      const int idx = s.idx[i];
+      int r = 0;
+#pragma unroll 4
+      for (int j = 0; j < count; ++j) r += before<kBeam>(s, j, key, idx) ? 1 : 0;
+      s.rank[i] = r;
+    }
+  }
+  group_sync<kBar>();
+}
+
+// Cuts the list to the entries at or above its n-th largest 32-bit key prefix.
+template <int kBar>
+__device__ int prune(Select& s, Lists& ls, int count, int n) {
+  constexpr int kPer = kMaxCands / kTopThreads;
+  const int tid = threadIdx.x % kTopThreads;
+  unsigned long long k[kPer];
+  int ix[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int i = q * kTopThreads + tid;
+    k[q] = i < count ? ls.key[i] : 0ull;
+    ix[q] = i < count ? ls.idx[i] : 0;
+  }
+  uint32_t t = 0;
+  for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+    const uint32_t at = t | bit;
+    int c = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) c += (uint32_t)(k[q] >> 32) >= at ? 1 : 0;
+    c = (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
+    if (tid == 0) s.pick[0] = 0;
+    group_sync<kBar>();
+    if (lane_id() == 0) atomicAdd(&s.pick[0], c);
+    group_sync<kBar>();
+    if (s.pick[0] >= n) t = at;
+    group_sync<kBar>();
+  }
+  if (tid == 0) s.pick[1] = 0;
+  group_sync<kBar>();
+#pragma unroll
+  for (int q = 0; q < kPer; ++q)
+    if (q * kTopThreads + tid < count && (uint32_t)(k[q] >> 32) >= t) {
+      const int o = atomicAdd(&s.pick[1], 1);
+      ls.key[o] = k[q];
+      ls.idx[o] = ix[q];
+    }
+  group_sync<kBar>();
+  return s.pick[1];
+}
+
+// One pass of eight warps over elements e0 .. e1 - 1 of a row: the thread's
+// running sum, and at table[i * 256] the max of its 32 elements of iteration
+// i (elements (i * 256 + t) * 32 on: warp w has chunk i * 8 + w).
+template <typename T, bool kAligned>
+__device__ __forceinline__ RunningSum stream_slice(uint32_t ring, const T* row, int e0, int e1,
+                                                   int iters, float c, uint16_t* table,
+                                                   const RowSpan& span) {
+  constexpr int VEC = Group<T>::VEC;
+  constexpr int kGroups = kEntry / VEC;  // 16-byte groups of a lane: 4 or 8
+  constexpr int kAtOnce = 4;
+  using R = Ring<T>;
+  const int lane = lane_id(), warp = threadIdx.x % kTopThreads / kWarp;
+  const T* tag = nullptr;
+  const int chunks = (e1 - e0 + kChunk - 1) / kChunk;
+  const int todo = (chunks - warp + kTopWarps - 1) / kTopWarps;  // this warp's (may be <= 0)
+  const uint32_t off = kAligned ? 0u : (uint32_t)(uintptr_t)row & 15u;
+  ring += warp * R::kWarpBytes;
+  auto issue = [&](int i) {  // iteration i's chunk into its stage
+    if (i < todo) {
+      const int j = e0 + (i * kTopWarps + warp) * kChunk;
+      load_chunk_async<T, kAligned>(ring + i % R::kStages * R::kBytes, row, j,
+                                    min(j + kChunk, e1), off, span);
+    }
+    copies_commit();
+  };
+  RunningSum r;
+#pragma unroll
+  for (int i = 0; i < R::kStages - 1; ++i) issue(i);
+  for (int i = 0; i < iters; ++i) {
+    if (i >= todo) {
+      table[i * kTopThreads] = 0xff80u;
+      continue;
+    }
+    copies_wait_but<R::kStages - 2>();
+    __syncwarp();  // every lane's copies of this stage landed; the stage before is read
+    issue(i + R::kStages - 1);
+    const uint32_t stage = ring + i % R::kStages * R::kBytes;
+    const int j = e0 + (i * kTopWarps + warp) * kChunk;
+    float gm = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < kGroups; h += kAtOnce) {
+      uint4 g[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        // the lane's groups in an order that keeps a quarter warp off each other's banks
+        const int q = (h + u + (VEC == 8 ? lane >> 1 : lane)) & (kGroups - 1);
+        const uint32_t at = stage + (lane * kGroups + q) * 16;
+        g[u] = lds128(at);
+        if (!kAligned && off) g[u] = shift_pair(g[u], lds128(at + 16), off);
+      }
+      if (j + kChunk > e1) {
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+          clip_group<T>(g[u],
+                        j + lane * kEntry +
+                            ((h + u + (VEC == 8 ? lane >> 1 : lane)) & (kGroups - 1)) * VEC,
+                        e1);
+      }
+      gm = max_nan(gm, r.add(g, c, tag));
+    }
+    table[i * kTopThreads] = up_bf16(gm);
+  }
+  __syncwarp();  // (the next slice refills the stages)
+  return r;
+}
+
+// The table entries at or above thr, eight a thread and step, as `base` plus
+// their number in rank[] (at most kMaxCands; n_hits counts all).
+__device__ __forceinline__ void scan_table(Select& s, Lists& ls, const uint16_t* table, int iters,
+                                           float thr, int base) {
+  for (int v = threadIdx.x % kTopThreads; v < iters * (kTopThreads / 8); v += kTopThreads) {
+    const uint4 e = load128(table + 8 * v);
+    const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+    unsigned hits = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      hits |= (bf16_lo(w[q]) >= thr ? 1u << (2 * q) : 0u) |
+              (bf16_hi(w[q]) >= thr ? 2u << (2 * q) : 0u);
+    if (hits) {
+      int h = atomicAdd(&s.n_hits, __popc(hits));
+      for (; hits; hits &= hits - 1u, ++h)
+        if (h < kMaxCands) ls.rank[h] = base + 8 * v + __ffs(hits) - 1;
+    }
+  }
+}
+
+// The elements of a group at or above thr go to a list (the logit now, the
+// key when the list is complete).
+template <typename T>
+__device__ __forceinline__ void list_group(int* n_cands, Lists* to, const uint4& g, float thr,
+                                           int idx) {
+  constexpr int VEC = Group<T>::VEC;
+  unsigned in = 0;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) in |= (Lane<T, VEC>::get(g, e) >= thr ? 1u : 0u) << e;
+  if (!in) return;
+  int o = atomicAdd(n_cands, __popc(in));
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+    if (in >> e & 1u) {
+      if (o < kMaxCands) {
+        to->key[o] = __float_as_uint(Lane<T, VEC>::get(g, e));
+        to->idx[o] = idx + e;
+      }
+      ++o;
+    }
+}
+
+// A row's {max, sum as a pair} from its warps' parts (one warp, up to 64 parts).
+__device__ __forceinline__ float row_sum(const float2* parts, int n, float c, float2& sum) {
+  const int lane = lane_id();
+  const float2 a = lane < n ? parts[lane] : make_float2(-INFINITY, 0.f);
+  const float2 b = lane + kWarp < n ? parts[lane + kWarp] : make_float2(-INFINITY, 0.f);
+  const float m = warp_max_nan(max_nan(a.x, b.x));
+  sum = warp_sum_pair(a.y * to_frame(a.x, m, c) + b.y * to_frame(b.x, m, c));
+  return m;
+}
+
+// score - lse in 64 bits, with log of the sum as a pair.
+__device__ __forceinline__ double row_offset(float score, float m, float2 log_sum) {
+  return ((double)score - (double)m) - ((double)log_sum.x + (double)log_sum.y);
+}
+
+template <typename T>
+constexpr int ring_bytes() {
+  return Ring<T>::kTotal;
+}
+
+}  // namespace
+}  // namespace sv

@@ -1,0 +1,386 @@
+// sv_toprows.cu - the k largest logits of each of many rows with its
+// log-sum-exp, and the merge of a request's row selections (beams).
+//
+// With a CTA per row (sv_top.cu) all resident CTAs stream at the same pace and
+// then select at the same time, and HBM idles meanwhile: a quarter of the
+// call. Here each CTA has two halves of eight warps: one streams row after
+// row, the other selects from the row before, over two sets of tables and
+// sums, handed over through named barriers. Rows come from the launch's own
+// queue (cluster launch control: a CTA cancels a CTA of the grid that has not
+// started and takes its row), so the last rows spread evenly without a
+// counter in memory; the selecting half asks for them while the other streams,
+// and deals with rows that need no work by itself.
+#include "sv_select.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kRowThreads = 2 * kTopThreads;
+// named barriers, two each but the first
+enum : int { kBarSelect = 1, kBarFull = 2, kBarEmpty = 4, kBarNext = 6 };
+
+struct alignas(16) RowShared {
+  uint4 answer;                 // the queue's answer
+  unsigned long long bar;       // its arrival
+  long long next[2];            // the row to stream next, by parity (-1: none)
+  struct Slot {
+    float2 part[kTopWarps];     // the row's sums by warp
+    float unit[kTopThreads];    // its thread maxes
+  } slot[2];
+  Select sel;
+  float2 log_sum;
+  float m;
+};
+constexpr int kLive = -1;
+
+__device__ __forceinline__ void bar_sync(int bar, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int bar, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+}
+
+// Asks for a CTA of this grid that has not started; the answer (16 bytes)
+// completes on mbarrier `bar`.
+__device__ __forceinline__ void ask_for_cta(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(answer),
+      "r"(bar)
+      : "memory");
+}
+// The CTA taken over (its index in a grid of one dimension), or -1.
+__device__ __forceinline__ long long taken_cta(uint32_t answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 a;\n ld.shared.b128 a, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n"
+      " selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n}"
+      : "=r"(got), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return got ? (long long)x : -1;
+}
+
+// kLive, or the status of a row that is not read.
+__device__ __forceinline__ int row_state(const TopParams& p, long long row) {
+  if (p.scores) return p.scores[row] == -INFINITY ? 0 : kLive;
+  if (!p.lens) return kLive;
+  const int b = (int)(row / p.P), i = (int)(row - (long long)b * p.P), len = p.lens[b];
+  if (len < 0 || len > p.P) return SV_REQ_BAD_DRAFT_LEN;
+  return i < len ? kLive : 0;
+}
+
+__device__ __forceinline__ void fill_slots(const TopParams& p, long long row, int from) {
+  for (int j = from + threadIdx.x % kTopThreads; j < p.n; j += kTopThreads) {
+    p.out_ids[row * p.n + j] = -1;
+    p.out_values[row * p.n + j] = -INFINITY;
+  }
+}
+
+// The next row that needs work, -1 when the queue is empty; the outputs of the
+// others on the way (a call of the selecting half).  `row`: a row taken already,
+// or -1 to ask.
+__device__ long long next_live(RowShared& s, const TopParams& p, long long row, int& asked,
+                               bool& late) {
+  const int t = threadIdx.x % kTopThreads;
+  for (;;) {
+    if (row < 0) {
+      group_sync<kBarSelect>();  // the last answer is read by all
+      if (t == 0) {
+        fence_proxy_async();
+        mbar_arrive_expect_tx(smem_u32(&s.bar), 16);
+        ask_for_cta(smem_u32(&s.answer), smem_u32(&s.bar));
+      }
+      late = !mbar_wait(smem_u32(&s.bar), asked++ & 1);
+      if (late) return -1;
+      row = taken_cta(smem_u32(&s.answer));
+      if (row < 0) return -1;
+    }
+    const int state = row_state(p, row);
+    if (state == kLive) return row;
+    fill_slots(p, row, 0);
+    if (t == 0) {
+      if (p.out_off) p.out_off[row] = -INFINITY;
+      else p.out_lse[row] = -INFINITY;
+      if (p.out_status) p.out_status[row] = state;
+    }
+    row = -1;
+  }
+}
+
+// The selecting half: one row from its table, sums and units.
+template <typename T, bool kAligned>
+__device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot, long long row,
+                           const uint16_t* table, const TopParams& p, const RowSpan& span) {
+  constexpr int VEC = Group<T>::VEC;
+  constexpr int kGroups = kEntry / VEC;
+  const int t = threadIdx.x % kTopThreads;
+  if (t == 0) s.sel.n_hits = s.sel.n_cands = 0;
+  // every warp for itself: the max decides whether there is anything to select
+  float2 sum;
+  const float m = row_sum(slot.part, kTopWarps, p.cc, sum);
+  const float score = p.scores ? p.scores[row] : 0.f;
+  const bool bad = m != m || m == INFINITY || score != score || score == INFINITY;
+  if (t == 0) {
+    const float2 l = log_pair(sum);
+    if (p.out_off) {
+      p.out_off[row] = bad              ? __longlong_as_double(0x7fffffffffffffffll)
+                       : m == -INFINITY ? -INFINITY
+                                        : row_offset(score, m, l);
+    } else {
+      p.out_lse[row] = bad ? qnan() : m == -INFINITY ? -INFINITY : m / p.T + (l.x + l.y);
+      if (p.out_status) p.out_status[row] = bad ? SV_REQ_BAD_LOGITS : 0;
+    }
+  }
+  if (bad || m == -INFINITY) {
+    fill_slots(p, row, 0);
+    return;
+  }
+  const float thr = fmaxf(unit_bound<kBarSelect>(s.sel, slot.unit, p.upi, p.n), -FLT_MAX);
+  group_sync<kBarSelect>();  // (the counters are clear also when no round was needed)
+  scan_table(s.sel, ls, table, p.iters, thr, 0);
+  group_sync<kBarSelect>();
+  const T* data = reinterpret_cast<const T*>(p.logits) + row * (long long)p.V;
+  const int hits = s.sel.n_hits;
+  if (hits <= kMaxCands)
+    for (int q = t; q < hits * kGroups; q += kTopThreads) {
+      const int at = ls.rank[q / kGroups], u = q % kGroups;
+      const int i = at / kTopThreads, ti = at % kTopThreads;
+      const int j = (i * kTopThreads + ti) * kEntry + u * VEC;
+      if (j < p.V)
+        list_group<T>(&s.sel.n_cands, &ls, load_group<T, kAligned>(data, j, p.V, span), thr, j);
+    }
+  group_sync<kBarSelect>();
+  int count = s.sel.n_cands;
+  if (hits > kMaxCands || count > kMaxCands) {
+    group_sync<kBarSelect>();
+    count = select_row_slow<T, false, kBarSelect>(s.sel, ls, data, p.V, p.n, 0.0, 0, 0);
+  } else {
+    for (int i = t; i < count; i += kTopThreads)
+      set_candidate<false>(ls, i, __uint_as_float((uint32_t)ls.key[i]), 0.0, ls.idx[i]);
+    group_sync<kBarSelect>();
+    if (count > kRankAll) count = prune<kBarSelect>(s.sel, ls, count, p.n);
+  }
+  rank_list<false, kBarSelect>(ls, count);
+  for (int i = t; i < count; i += kTopThreads) {
+    const int r = ls.rank[i];
+    if (r < p.n) {
+      p.out_ids[row * p.n + r] = ls.idx[i];
+      p.out_values[row * p.n + r] = of_ordered((uint32_t)(ls.key[i] >> 32));
+    }
+  }
+  fill_slots(p, row, count);
+  group_sync<kBarSelect>();  // the lists are read
+}
+
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  RowShared& s = *reinterpret_cast<RowShared*>(smem);
+  Lists& ls = *reinterpret_cast<Lists*>(smem + sizeof(RowShared));
+  uint16_t* tables = reinterpret_cast<uint16_t*>(smem + sizeof(RowShared) + sizeof(Lists));
+  const int table = p.iters * kTopThreads;
+  unsigned char* rings = smem + sizeof(RowShared) + sizeof(Lists) + 2 * 2 * table;
+  const int t = threadIdx.x % kTopThreads, lane = lane_id(), warp = t / kWarp;
+  const RowSpan span = {p.first, p.last};
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&s.bar), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const bool first_live = row_state(p, blockIdx.x) == kLive;
+
+  if (threadIdx.x >= kTopThreads) {  // the selecting half
+    int asked = 0;
+    bool late = false;
+    long long row = next_live(s, p, blockIdx.x, asked, late);
+    if (!first_live) {
+      if (t == 0) s.next[0] = row;
+      bar_arrive(kBarNext, kRowThreads);
+    }
+    for (int k = 0; row >= 0; ++k) {
+      const int b = k & 1;
+      const long long next = next_live(s, p, -1, asked, late);
+      if (t == 0) s.next[b ^ 1] = next;
+      bar_arrive(kBarNext + (b ^ 1), kRowThreads);
+      bar_sync(kBarFull + b, kRowThreads);
+      select_row<T, kAligned>(s, ls, s.slot[b], row, tables + b * table, p, span);
+      bar_arrive(kBarEmpty + b, kRowThreads);
+      // a device fault: the queue did not answer in two seconds
+      if (late && t == 0 && p.out_status) p.out_status[row] = SV_REQ_TIMEOUT;
+      row = next;
+    }
+    return;
+  }
+
+  // The streaming half.
+  const int fold = kTopThreads / p.upi;
+  long long row = blockIdx.x;
+  if (!first_live) {
+    bar_sync(kBarNext, kRowThreads);
+    row = s.next[0];
+  }
+  int k = 0;
+  for (; row >= 0; ++k) {
+    const int b = k & 1;
+    RowShared::Slot& slot = s.slot[b];
+    if (k >= 2) bar_sync(kBarEmpty + b, kRowThreads);  // row k - 2 is selected
+    const T* data = reinterpret_cast<const T*>(p.logits) + row * (long long)p.V;
+    const RunningSum r = stream_slice<T, kAligned>(smem_u32(rings), data, 0, p.V, p.iters, p.cc,
+                                                   tables + b * table + t, span);
+    const float2 wr = warp_running(r, p.cc);
+    float um = r.m;
+    for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
+    if (lane == 0) slot.part[warp] = wr;
+    if ((t & (fold - 1)) == 0) slot.unit[t / fold] = um;
+    bar_arrive(kBarFull + b, kRowThreads);
+    bar_sync(kBarNext + (b ^ 1), kRowThreads);
+    row = s.next[b ^ 1];
+  }
+  // every arrival is waited for before the CTA ends
+  if (k >= 2) bar_sync(kBarEmpty + (k & 1), kRowThreads);
+  if (k >= 1) bar_sync(kBarEmpty + ((k - 1) & 1), kRowThreads);
+}
+
+template <typename T, bool kAligned>
+cudaError_t launch_rows(TopParams p, long long rows, cudaStream_t stream) {
+  static PerDevice once;
+  auto* fn = top_rows_kernel<T, kAligned>;
+  const size_t fixed = sizeof(RowShared) + sizeof(Lists) + ring_bytes<T>();
+  const cudaError_t err = per_device(once, nullptr, [&](int&) {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
+  });
+  if (err != cudaSuccess) return err;
+  fn<<<dim3((unsigned)rows), kRowThreads, fixed + 4 * (size_t)p.iters * kTopThreads, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// The n best of a request's W selections: every thread takes the candidates
+// of its stride, and the bound of the thread maxes leaves a list that fits
+// (or, with many equal scores, the rows go in one after the other).
+__global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
+    const TopParams p, const int* __restrict__ ids, const float* __restrict__ values,
+    const double* __restrict__ off) {
+  __shared__ Lists ls;
+  __shared__ Select sel;
+  __shared__ float unit[kTopThreads];
+  __shared__ double s_off[SV_MAX_BEAMS];
+  pdl_wait();
+  const long long b = blockIdx.x;
+  const int t = threadIdx.x, all = p.W * p.n;
+  ids += b * all;
+  values += b * all;
+  if (t == 0) sel.n_cands = sel.bad = 0;
+  __syncthreads();
+  if (t < p.W) {
+    const double o = off[b * p.W + t];
+    s_off[t] = o;
+    if (o != o) sel.bad = 1;
+  }
+  __syncthreads();
+  const bool bad = sel.bad != 0;
+  if (t == 0 && p.out_status) p.out_status[b] = bad ? SV_REQ_BAD_LOGITS : 0;
+  auto write = [&](int slot, unsigned long long key, int idx) {
+    const long long o = b * p.n + slot;
+    const int w = idx < 0 ? -1 : idx / p.V;
+    p.out_ids[o] = idx < 0 ? -1 : idx - w * p.V;
+    p.out_parents[o] = w;
+    p.out_values[o] = idx < 0 ? -INFINITY : (float)of_ordered(key);
+  };
+  int count = 0;
+  if (!bad) {
+    // bounds of the scores, rounded down; an empty slot's logit is -inf
+    float um = -INFINITY;
+    for (int i = t; i < all; i += kTopThreads) {
+      const float l = values[i];
+      if (l > -INFINITY) um = fmaxf(um, __fadd_rd(__double2float_rd(s_off[i / p.n]), l));
+    }
+    unit[t] = um;
+    __syncthreads();
+    const float bound = unit_bound<0>(sel, unit, kTopThreads, p.n);
+    for (int i = t; i < all; i += kTopThreads) {
+      const float l = values[i];
+      const int w = i / p.n;
+      if (l > -INFINITY) {
+        const double score = s_off[w] + (double)l;
+        // what rounds below the bound is below n others
+        if (__double2float_ru(score) >= bound) {
+          const int o = atomicAdd(&sel.n_cands, 1);
+          if (o < kMaxCands) {
+            ls.key[o] = ordered(score);
+            ls.idx[o] = w * p.V + ids[i];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    count = sel.n_cands;
+    if (count > kMaxCands) {
+      __syncthreads();
+      count = 0;
+      for (int w = 0; w < p.W; ++w) {
+        if (s_off[w] == -INFINITY) continue;
+        int got = 0;  // (the finite ones come first)
+        if (t < p.n && values[w * p.n + t] > -INFINITY) {
+          ls.key[count + t] = ordered(s_off[w] + (double)values[w * p.n + t]);
+          ls.idx[count + t] = w * p.V + ids[w * p.n + t];
+          got = 1;
+        }
+        got = __syncthreads_count(got);
+        const int total = count + got;
+        rank_list<true, 0>(ls, total);
+        const unsigned long long key = t < total ? ls.key[t] : 0;
+        const int idx = t < total ? ls.idx[t] : 0, r = t < total ? ls.rank[t] : p.n;
+        __syncthreads();
+        if (r < p.n) {
+          ls.key[r] = key;
+          ls.idx[r] = idx;
+        }
+        count = min(total, p.n);
+        __syncthreads();
+      }
+    } else if (count > kRankAll) {
+      count = prune<0>(sel, ls, count, p.n);
+    }
+    rank_list<true, 0>(ls, count);
+    for (int i = t; i < count; i += kTopThreads) {
+      const int r = ls.rank[i];
+      if (r < p.n) write(r, ls.key[i], ls.idx[i]);
+    }
+  }
+  for (int j = count + t; j < p.n; j += kTopThreads) write(j, 0, -1);
+}
+
+}  // namespace
+
+bool top_rows_fit(sv_dtype dtype, int V) {
+  const size_t tables = 4 * (size_t)((V + kTopSpan - 1) / kTopSpan) * kTopThreads;
+  const size_t ring = dtype == SV_BF16 ? ring_bytes<uint16_t>() : ring_bytes<float>();
+  return sizeof(RowShared) + sizeof(Lists) + ring + tables <= (size_t)kRowsSmem;
+}
+
+cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long rows,
+                            cudaStream_t stream) {
+  p.slices = 1;
+  p.slice = (p.V + 255) / 256 * 256;
+  p.iters = (p.V + kTopSpan - 1) / kTopSpan;
+  p.upi = kTopThreads;
+  while (p.upi > 32 && p.upi / 2 >= 4 * p.n) p.upi /= 2;
+  if (dtype == SV_BF16)
+    return aligned ? launch_rows<uint16_t, true>(p, rows, stream)
+                   : launch_rows<uint16_t, false>(p, rows, stream);
+  return aligned ? launch_rows<float, true>(p, rows, stream)
+                 : launch_rows<float, false>(p, rows, stream);
+}
+
+cudaError_t launch_beam_merge(const TopParams& p, const int* ids, const float* values,
+                              const double* off, int B, cudaStream_t stream) {
+  TopParams q = p;
+  void* args[] = {&q, &ids, &values, &off};
+  return launch_pdl(reinterpret_cast<const void*>(beam_merge_kernel), dim3((unsigned)B),
+                    dim3(kTopThreads), stream, args);
+}
+
+}  // namespace sv

@@ -307,20 +307,16 @@ __device__ __forceinline__ void load_chunk_async(uint32_t dst, const T* row, int
   }
 }
 
-// A lane's groups of the chunk at element j: elements from `end` on become -inf.
-template <typename T, int N>
-__device__ __forceinline__ void clip_chunk(uint4 (&g)[N], int j, int end) {
+// Elements from `end` on of the group at element j become -inf.
+template <typename T>
+__device__ __forceinline__ void clip_group(uint4& g, int j, int end) {
   constexpr int VEC = Group<T>::VEC;
+  if (j >= end) {
+    g = Lane<T, VEC>::pad();
+  } else if (j + VEC > end) {
 #pragma unroll
-  for (int u = 0; u < N; ++u) {
-    const int first = j + (u * kWarp + lane_id()) * VEC;
-    if (first >= end) {
-      g[u] = Lane<T, VEC>::pad();
-    } else if (first + VEC > end) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (first + e >= end) Lane<T, VEC>::kill(g[u], e);
-    }
+    for (int e = 0; e < VEC; ++e)
+      if (j + e >= end) Lane<T, VEC>::kill(g, e);
   }
 }
 
