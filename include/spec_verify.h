@@ -404,7 +404,8 @@ sv_status spec_ngram_propose(const int32_t* tokens, const int32_t* lens, int B, 
  *   out_lse     [B, P] fp32: log sum_j exp(l_j / T); -inf for a row that is
  *               not read or has no finite logit.
  *   out_status  [B, P] int32 or NULL: SV_REQ_* bits per row.  A row with NaN or
- *               +inf (SV_REQ_BAD_LOGITS) has no record (-1, -inf) and lse NaN.
+ *               +inf (SV_REQ_BAD_LOGITS), or whose wait for staged logits ran out
+ *               (SV_REQ_TIMEOUT), has no record (-1, -inf) and lse NaN.
  *   B, P, V     0 <= B <= SV_MAX_B, P >= 1, B * P <= SV_MAX_ROWS, 1 <= V <= SV_MAX_V.
  * No workspace: a call keeps nothing, so calls may overlap on any streams. */
 sv_status spec_top_logits(const void* logits, int k, float temperature, const int32_t* lens,
@@ -449,8 +450,8 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
  *               finite logit; a used entry's logit NaN or +inf, or a top_lse beside
  *               it that is not finite, or without one no finite logit),
  *               SV_REQ_BAD_TOKEN (a token outside [-1, V) or
- *               given twice), SV_REQ_BAD_DRAFT_LEN.  Such a row has loss NaN and
- *               gradient 0.
+ *               given twice), SV_REQ_BAD_DRAFT_LEN, SV_REQ_TIMEOUT.  Such a row has
+ *               loss NaN and gradient 0.
  *   k, B, P, V, temperature: as in spec_top_logits.  No workspace. */
 sv_status spec_distill(const void* student_logits, const int32_t* top_ids,
                        const float* top_logits, const float* top_lse, const int32_t* lens,
@@ -460,7 +461,9 @@ sv_status spec_distill(const void* student_logits, const int32_t* top_ids,
 
 /* The backward pass of spec_distill alone: out_grad [B, P, V] = the gradient
  * of sum(grad_loss * loss), from the out_stats of a spec_distill call with the
- * same student_logits, record, lens and temperature. */
+ * same student_logits, record, lens and temperature.  Rows with a data error
+ * there have gradient 0; a part of a row whose wait for staged logits ran out
+ * here has gradient NaN. */
 sv_status spec_distill_grad(const void* student_logits, const int32_t* top_ids,
                             const float* top_logits, const float* top_lse, const int32_t* lens,
                             const float* stats, const float* grad_loss, float temperature,
@@ -482,7 +485,8 @@ sv_status spec_distill_grad(const void* student_logits, const int32_t* top_ids,
  *               candidate; out_scores [B, n] fp32.  Candidates have finite logits; past
  *               the last one the slots hold -1, -1 and -inf.
  *   out_status  [B] int32 or NULL: SV_REQ_BAD_LOGITS when a live beam's row has NaN
- *               or +inf, or a score is NaN or +inf; nothing is kept then.
+ *               or +inf, or a score is NaN or +inf, SV_REQ_TIMEOUT; nothing is kept
+ *               then.
  *   1 <= W <= SV_MAX_BEAMS, 1 <= n <= SV_MAX_TOP, 0 <= B <= SV_MAX_B, and
  *   ceil(W / 8) * ceil(V / 8192) <= 256 (V <= 2097152 up to 8 beams, 262144 with
  *   64).  Scores are compared in 64 bits (their row sums are of 32-bit terms).

@@ -255,3 +255,19 @@ def test_verify_record_distill_a_draft_head():
     # each row's gradient is within 3 SUM of |grad_loss|, the head sums B (K+1) rows of |hid| <= 5
     tol = 5 * float(gl.sum()) * 3 * plain.SUM + 1e-5 * float(h64.grad.abs().max())
     assert float((head.grad.double() - h64.grad).abs().max()) <= tol
+
+
+def test_wait_limit_runs_out():
+    s, ids, t, lse, gl = case(2, 3, 5001, 8, BF16, 1.0, True, 20)
+    fwd = api.spec_distill(s, ids, t, top_lse=lse)
+    old = api.wait_limit_ns()
+    try:
+        api.set_wait_limit_ns(0)
+        out = api.spec_distill(s, ids, t, top_lse=lse, grad_loss=gl)
+        grad = api.spec_distill_grad(s, ids, t, 1.0, fwd.stats, gl, top_lse=lse)
+        torch.cuda.synchronize()
+    finally:
+        api.set_wait_limit_ns(old)
+    assert bool((out.status == api.REQ_TIMEOUT).all()) and bool(torch.isnan(out.loss).all())
+    assert not bool(out.grad.any()) and bool(torch.isnan(grad).all())
+    check(s, ids, t, lse, 1.0, gl)

@@ -46,34 +46,37 @@ struct DistillParams {
   int slice;                // 16-byte words per CTA
   float cc;                 // log2(e) / T
   float T, inv_t;           // T and 1 / T
+  unsigned long long wait_ns;  // limit of the wait for the slice
 };
 
 struct alignas(16) DistillShared {
   float4 part[kMaxCluster];      // each CTA's {max, sum, -, -} over its slice without the record
   float2 warp_part[kDistillWarps];
   float4 stat;                   // {m, beta, M, 1/Z}
+  unsigned long long bar;        // the slice's arrival
   int id[SV_MAX_TOP];            // the record (-1: unused)
   float t[SV_MAX_TOP];           // its logits (-inf: unused)
   float p[SV_MAX_TOP];           // its teacher probabilities
   float sv[SV_MAX_TOP];          // the student's logits at its tokens
-  int bad, used;
+  int bad, used, late;
   float norm, norm_lo;           // the teacher's log-sum-exp: log p_j = t_j / T - norm
   float p_rest;
   float m, M;                    // the student's max outside the record, and over all
   float2 S, Z;                   // its sums there, in the frames of m and M (hi, lo)
 };
 
-// Writes `bytes` bytes of zeros at `dst` (2-byte aligned).
-__device__ void zero_bytes(char* dst, long long bytes) {
+// Writes the 32-bit pattern v (equal halves) over `bytes` bytes at `dst` (2-byte
+// aligned).
+__device__ void fill_bytes(char* dst, int bytes, uint32_t v = 0) {
   const int t = threadIdx.x;
-  const long long head = min(bytes, (long long)((16u - ((uint32_t)(uintptr_t)dst & 15u)) & 15u));
-  for (long long i = 2 * t; i < head; i += 2 * kDistillThreads)
-    *reinterpret_cast<uint16_t*>(dst + i) = 0;
-  const long long vecs = (bytes - head) / 16;
-  for (long long i = t; i < vecs; i += kDistillThreads)
-    *reinterpret_cast<uint4*>(dst + head + 16 * i) = make_uint4(0, 0, 0, 0);
-  for (long long i = head + 16 * vecs + 2 * t; i < bytes; i += 2 * kDistillThreads)
-    *reinterpret_cast<uint16_t*>(dst + i) = 0;
+  const int head = min(bytes, (int)((16u - ((uint32_t)(uintptr_t)dst & 15u)) & 15u));
+  for (int i = 2 * t; i < head; i += 2 * kDistillThreads)
+    *reinterpret_cast<uint16_t*>(dst + i) = (uint16_t)v;
+  const int vecs = (bytes - head) / 16;
+  for (int i = t; i < vecs; i += kDistillThreads)
+    *reinterpret_cast<uint4*>(dst + head + 16 * i) = make_uint4(v, v, v, v);
+  for (int i = head + 16 * vecs + 2 * t; i < bytes; i += 2 * kDistillThreads)
+    *reinterpret_cast<uint16_t*>(dst + i) = (uint16_t)v;
 }
 
 // `bytes` bytes from shared memory go to global `dst` (both 2-byte aligned;
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   // A row without loss or gradient (not needed, or a data error seen by
   // every CTA of the cluster alike).
   auto leave = [&](float loss, int status) {
-    if (kMode != kLoss) zero_bytes(grad + x0, x1 - x0);
+    if (kMode != kLoss) fill_bytes(grad + x0, x1 - x0);
     if (kMode != kGradOnly && rank == 0 && t == 0) {
       p.out_loss[row] = loss;
       // 1/Z NaN: a later backward pass writes zeros
@@ -301,13 +304,23 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
     if (t == 0) s.stat = st;
   }
 
-  // The slice on its way into shared memory: the words inside the row as
-  // they are, the row's first and last word by element, -inf around them.
-  for (int i = t; i < nw; i += kDistillThreads) {
-    const int x = 16 * (w0 + i) - r;
-    if (x >= 0 && x + 16 <= nb) {
-      copy16_async(smem_u32(words + 16 * i), src + x);
-    } else {
+  // The slice on its way into shared memory: the words inside the row as one
+  // bulk copy, the row's first and last word by element, -inf around them.
+  const int lo = nw > 0 && 16 * w0 - r < 0 ? 1 : 0;
+  const int hi = max(lo, nw > 0 && 16 * w1 - r > nb ? nw - 1 : nw);
+  if (t == 0) {
+    s.bad = s.used = s.late = 0;
+    mbar_init(smem_u32(&s.bar), 1);
+    fence_mbar_init();
+    const uint32_t bytes = 16u * (uint32_t)(hi - lo);
+    mbar_arrive_expect_tx(smem_u32(&s.bar), bytes);
+    if (bytes)
+      bulk_copy(smem_u32(words + 16 * lo), src + (16 * (w0 + lo) - r), bytes, smem_u32(&s.bar));
+  }
+  if (t == kWarp || t == kWarp + 1) {
+    const int i = t == kWarp ? (lo > 0 ? 0 : -1) : (hi < nw ? hi : -1);
+    if (i >= 0) {
+      const int x = 16 * (w0 + i) - r;
       uint4 v = Lane<T, VEC>::pad();
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -317,17 +330,25 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
       *reinterpret_cast<uint4*>(words + 16 * i) = v;
     }
   }
-  if (t == 0) s.bad = s.used = 0;
   // (no CTA writes into another's shared memory before that one has started)
   if (kMode != kGradOnly && C > 1) cluster_arrive();
   __syncthreads();
   load_record(s, p, row);
-  copies_wait();
+  if (!mbar_wait(smem_u32(&s.bar), 0, p.wait_ns)) {
+    s.late = 1;
+    mbar_wait(smem_u32(&s.bar), 0);  // the copy lands before the memory is left
+  }
   if (kMode != kGradOnly && C > 1) cluster_wait();
   __syncthreads();
+  const bool late = s.late != 0;
   const int bad_record = s.bad, used = s.used;
   if (bad_record || used == 0) {
     leave(bad_record ? qnan() : 0.f, bad_record);
+    return;
+  }
+
+  if (kMode == kGradOnly && late) {  // no status to say so: NaN (all bits set)
+    fill_bytes(grad + x0, x1 - x0, 0xffffffffu);
     return;
   }
 
@@ -370,7 +391,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
       const float sum = warp_sum(v.y * to_frame(v.x, m, p.cc));
       if (lane < C) {
         DistillShared* to = C > 1 ? cluster.map_shared_rank(&s, lane) : &s;
-        to->part[rank] = make_float4(m, sum, 0.f, 0.f);
+        to->part[rank] = make_float4(m, sum, late ? 1.f : 0.f, 0.f);
       }
     }
     if (C > 1) cluster.sync(); else __syncthreads();
@@ -378,6 +399,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
     if (warp == 0) {
       // the rest: its max m and sum S over the cluster's slices
       const float4 v = lane < C ? s.part[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      const bool any_late = __any_sync(0xffffffffu, v.z != 0.f);
       const float m = warp_max_nan(v.x);
       const float2 S = warp_sum_pair(v.y * to_frame(v.x, m, p.cc));
       // the record, and both together in the frame of M
@@ -392,7 +414,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
         M = fmaxf(M, x[q]);
       }
       M = fmaxf(warp_max(M), m);
-      wrong = __any_sync(0xffffffffu, wrong) || M == -INFINITY;
+      wrong = __any_sync(0xffffffffu, wrong) || M == -INFINITY || any_late;
       float z = 0.f;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) z += ex2((x[q] - frame_of(M)) * p.cc);
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
                              wrong ? qnan() : 1.f / zv);
         if (rank == 0) {
           if (p.out_stats) p.out_stats[row] = wrong ? make_float4(0.f, 0.f, 0.f, qnan()) : s.stat;
-          if (p.out_status) p.out_status[row] = wrong ? SV_REQ_BAD_LOGITS : 0;
+          if (p.out_status) p.out_status[row] = any_late ? SV_REQ_TIMEOUT : wrong ? SV_REQ_BAD_LOGITS : 0;
           if (wrong) p.out_loss[row] = qnan();
         }
       }
@@ -435,7 +457,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   // The gradient.
   const float4 st = s.stat;
   if (st.w != st.w) {
-    zero_bytes(grad + x0, x1 - x0);
+    fill_bytes(grad + x0, x1 - x0);
     return;
   }
   const float scale = p.grad_loss[row] / p.T;
@@ -551,6 +573,7 @@ DistillParams distill_params(const void* student, const int32_t* ids, const floa
   p.k = k;
   p.cc = exponent_scale(temperature);
   p.T = temperature;
+  p.wait_ns = wait_limit_ns();
   p.inv_t = (float)(1.0 / (double)temperature);
   return p;
 }

@@ -23,7 +23,7 @@ namespace sv {
 
 constexpr int kTopSpan = 8192;        // elements of a CTA's iteration: 32 a thread
 constexpr int kMaxTables = 256;       // iterations of a CTA over its items: 512 bytes each
-constexpr int kRowsSmem = 112 * 1024;  // shared memory of a CTA of the row kernel: two on an SM
+constexpr int kRowsSmem = 220 * 1024;  // shared memory of a CTA of the row kernel, at most
 
 struct TopParams {
   const void* logits;   // [B*P, V] (record) or [B*W, V] (beams)
@@ -33,7 +33,7 @@ struct TopParams {
   int* out_parents;     // beams: [B, n]
   float* out_values;    // logits [rows, n], scores [B, n]
   float* out_lse;       // record: [B*P]
-  double* out_off;      // row kernel for beams: [B*W] score - lse (-inf: no candidates, NaN: bad)
+  double* out_off;      // row kernel for beams: [B*W] score - lse (-inf: no candidates, NaN: bad, inf: late)
   int* out_status;
   int P;                // record: rows per request
   int W;                // rows per cluster (record: 1)
@@ -44,6 +44,7 @@ struct TopParams {
   int table_bytes;
   float cc;             // log2(e) / T
   float T;
+  unsigned long long wait_ns;  // limit of the waits for staged logits
   char* first;          // the logits' memory
   char* last;
 };
@@ -67,10 +68,13 @@ constexpr int kMaxCands = 1024;       // candidates of a cluster, 32-element gro
 constexpr int kRankAll = 384;         // lists longer than this are cut to the bound first
 
 // A barrier of 256 threads: the whole CTA of the cluster kernel (barrier 0),
-// the selecting half of the row kernel's.
+// the selecting part of the row kernel's. The form without .aligned: a warp
+// may reach it in parts (after a branch of one lane), which the aligned form
+// counts as a whole warp each.
 template <int kBar>
 __device__ __forceinline__ void group_sync() {
-  asm volatile("bar.sync %0, 256;" ::"n"(kBar) : "memory");
+  if (kBar == 0) __syncthreads();
+  else asm volatile("barrier.sync %0, 256;" ::"n"(kBar) : "memory");
 }
 
 // Scratch of a selection.
@@ -89,14 +93,31 @@ struct alignas(16) Lists {
 };
 
 // Load stages: each warp streams 1024-element chunks through its own ring by
-// asynchronous copies (a word more than a chunk, for rows off 16-byte
-// boundaries); no barrier but the warp's own.
+// bulk copies (a word more than a chunk, for rows off 16-byte boundaries); no
+// barrier but the warp's own.
+constexpr int kMaxStages = 4;
 template <typename T>
 struct Ring {
   static constexpr int kBytes = kChunk * (int)sizeof(T) + 16;
-  static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
+  static constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
   static constexpr int kWarpBytes = kBytes * kStages;
-  static constexpr int kTotal = kWarpBytes * kTopWarps;
+  static_assert(kStages <= kMaxStages, "an mbarrier for each stage");
+
+  uint32_t at, bars;    // this warp's stages and their mbarriers
+  uint32_t chunks = 0;  // consumed so far: the next one's stage and phase
+  bool late = false;    // a copy did not come in time: the ring is not used again
+  __device__ __forceinline__ uint32_t bar(uint32_t n) const { return bars + n % kStages * 8; }
+  __device__ __forceinline__ uint32_t stage(uint32_t n) const {
+    return at + n % kStages * kBytes;
+  }
+  __device__ __forceinline__ Ring(uint32_t stages, uint32_t mbarriers)
+      : at(stages), bars(mbarriers) {
+    if (lane_id() == 0) {
+      for (int q = 0; q < kStages; ++q) mbar_init(bar(q), 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+  }
 };
 
 // The upper 16 bits of v rounded up: a bf16 value >= v (v itself for bf16).
@@ -294,44 +315,49 @@ __device__ int prune(Select& s, Lists& ls, int count, int n) {
   return s.pick[1];
 }
 
-// One pass of eight warps over elements e0 .. e1 - 1 of a row: the thread's
-// running sum, and at table[i * 256] the max of its 32 elements of iteration
-// i (elements (i * 256 + t) * 32 on: warp w has chunk i * 8 + w).
-template <typename T, bool kAligned>
-__device__ __forceinline__ RunningSum stream_slice(uint32_t ring, const T* row, int e0, int e1,
-                                                   int iters, float c, uint16_t* table,
-                                                   const RowSpan& span) {
+// One pass of kWarps warps over elements e0 .. e1 - 1 of a row: the thread's
+// running sum, and at table[i * kWarps * 32] the max of its 32 elements of
+// iteration i (elements (i * kWarps * 32 + t) * 32 on of the slice, t the
+// thread: warp w has chunk i * kWarps + w).  When a copy does not come in time
+// the sum is -1 and the max NaN.
+template <typename T, bool kAligned, int kWarps>
+__device__ __forceinline__ RunningSum stream_slice(Ring<T>& ring, int warp, const T* row, int e0,
+                                                   int e1, int iters, float c, uint16_t* table,
+                                                   const RowSpan& span,
+                                                   unsigned long long wait_ns) {
   constexpr int VEC = Group<T>::VEC;
   constexpr int kGroups = kEntry / VEC;  // 16-byte groups of a lane: 4 or 8
   constexpr int kAtOnce = 4;
-  using R = Ring<T>;
-  const int lane = lane_id(), warp = threadIdx.x % kTopThreads / kWarp;
+  constexpr int kStages = Ring<T>::kStages;
+  const int lane = lane_id();
   const T* tag = nullptr;
   const int chunks = (e1 - e0 + kChunk - 1) / kChunk;
-  const int todo = (chunks - warp + kTopWarps - 1) / kTopWarps;  // this warp's (may be <= 0)
+  const int todo = ring.late ? 0 : (chunks - warp + kWarps - 1) / kWarps;  // may be <= 0
   const uint32_t off = kAligned ? 0u : (uint32_t)(uintptr_t)row & 15u;
-  ring += warp * R::kWarpBytes;
-  auto issue = [&](int i) {  // iteration i's chunk into its stage
-    if (i < todo) {
-      const int j = e0 + (i * kTopWarps + warp) * kChunk;
-      load_chunk_async<T, kAligned>(ring + i % R::kStages * R::kBytes, row, j,
-                                    min(j + kChunk, e1), off, span);
+  int issued = 0;
+  auto issue = [&]() {  // the next chunk into its stage
+    if (issued < todo) {
+      const int j = e0 + (issued * kWarps + warp) * kChunk;
+      const uint32_t n = ring.chunks + issued;
+      load_chunk_async<T, kAligned>(ring.stage(n), ring.bar(n), row, j, min(j + kChunk, e1), off,
+                                    span);
+      ++issued;
     }
-    copies_commit();
   };
   RunningSum r;
 #pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) issue(i);
-  for (int i = 0; i < iters; ++i) {
-    if (i >= todo) {
-      table[i * kTopThreads] = 0xff80u;
-      continue;
+  for (int i = 0; i < kStages - 1; ++i) issue();
+  int i = 0;
+  for (; i < todo; ++i) {
+    const uint32_t n = ring.chunks + i;
+    if (!__all_sync(0xffffffffu, mbar_wait(ring.bar(n), n / kStages & 1u, wait_ns))) {
+      ring.late = true;
+      break;
     }
-    copies_wait_but<R::kStages - 2>();
-    __syncwarp();  // every lane's copies of this stage landed; the stage before is read
-    issue(i + R::kStages - 1);
-    const uint32_t stage = ring + i % R::kStages * R::kBytes;
-    const int j = e0 + (i * kTopWarps + warp) * kChunk;
+    __syncwarp();  // the stage before is read by all lanes: it is filled again
+    issue();
+    const uint32_t stage = ring.stage(n);
+    const int j = e0 + (i * kWarps + warp) * kChunk;
     float gm = -INFINITY;
 #pragma unroll
     for (int h = 0; h < kGroups; h += kAtOnce) {
@@ -354,17 +380,35 @@ __device__ __forceinline__ RunningSum stream_slice(uint32_t ring, const T* row, 
       }
       gm = max_nan(gm, r.add(g, c, tag));
     }
-    table[i * kTopThreads] = up_bf16(gm);
+    table[i * kWarps * kWarp] = up_bf16(gm);
   }
-  __syncwarp();  // (the next slice refills the stages)
+  if (ring.late) {
+    // the copies under way land before the memory is left or used again
+    for (int q = 0; q < issued; ++q) {
+      const uint32_t n = ring.chunks + q;
+      mbar_wait(ring.bar(n), n / kStages & 1u);
+    }
+    r.m = qnan();
+    r.s = -1.f;
+  } else if (todo > 0) {
+    ring.chunks += todo;
+  }
+  for (; i < iters; ++i) table[i * kWarps * kWarp] = 0xff80u;
+  __syncwarp();
   return r;
+}
+
+// The warp's {max, sum}, {NaN, -1} when it was late.
+__device__ __forceinline__ float2 warp_part(const RunningSum& r, bool late, float c) {
+  const float2 v = warp_running(r, c);
+  return late ? make_float2(qnan(), -1.f) : v;
 }
 
 // The table entries at or above thr, eight a thread and step, as `base` plus
 // their number in rank[] (at most kMaxCands; n_hits counts all).
-__device__ __forceinline__ void scan_table(Select& s, Lists& ls, const uint16_t* table, int iters,
-                                           float thr, int base) {
-  for (int v = threadIdx.x % kTopThreads; v < iters * (kTopThreads / 8); v += kTopThreads) {
+__device__ __forceinline__ void scan_table(Select& s, Lists& ls, const uint16_t* table,
+                                           int entries, float thr, int base) {
+  for (int v = threadIdx.x % kTopThreads; v < entries / 8; v += kTopThreads) {
     const uint4 e = load128(table + 8 * v);
     const uint32_t w[4] = {e.x, e.y, e.z, e.w};
     unsigned hits = 0;
@@ -402,12 +446,15 @@ __device__ __forceinline__ void list_group(int* n_cands, Lists* to, const uint4&
     }
 }
 
-// A row's {max, sum as a pair} from its warps' parts (one warp, up to 64 parts).
-__device__ __forceinline__ float row_sum(const float2* parts, int n, float c, float2& sum) {
+// A row's {max, sum as a pair} from its warps' parts (one warp, up to 64 parts);
+// late: a part is missing.
+__device__ __forceinline__ float row_sum(const float2* parts, int n, float c, float2& sum,
+                                         bool& late) {
   const int lane = lane_id();
   const float2 a = lane < n ? parts[lane] : make_float2(-INFINITY, 0.f);
   const float2 b = lane + kWarp < n ? parts[lane + kWarp] : make_float2(-INFINITY, 0.f);
   const float m = warp_max_nan(max_nan(a.x, b.x));
+  late = __any_sync(0xffffffffu, a.y < 0.f || b.y < 0.f);
   sum = warp_sum_pair(a.y * to_frame(a.x, m, c) + b.y * to_frame(b.x, m, c));
   return m;
 }
@@ -418,8 +465,8 @@ __device__ __forceinline__ double row_offset(float score, float m, float2 log_su
 }
 
 template <typename T>
-constexpr int ring_bytes() {
-  return Ring<T>::kTotal;
+constexpr int ring_bytes(int warps) {
+  return Ring<T>::kWarpBytes * warps;
 }
 
 }  // namespace

@@ -30,6 +30,7 @@ struct alignas(16) TopShared {
   float off_down[SV_MAX_BEAMS];       // the same rounded down
   float thr[SV_MAX_BEAMS];            // the lowest logit a candidate of the row can have
   float lse;                          // record
+  unsigned long long bar[kTopWarps][kMaxStages];  // the stages' mbarriers
   Select sel;
 };
 
@@ -82,6 +83,7 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   if (C > 1) cluster_arrive();
 
   // One pass over each item.
+  Ring<T> ring(smem_u32(rings) + warp * Ring<T>::kWarpBytes, smem_u32(s.bar[warp]));
   const int fold = kTopThreads / p.upi;
   for (int it = rank, mine = 0; it < items; it += C, ++mine) {
     const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
@@ -92,11 +94,12 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
     const bool live = !kBeam || p.scores[rowid] != -INFINITY;
     RunningSum r;
     if (live) {
-      r = stream_slice<T, kAligned>(smem_u32(rings), row, e0, e1, p.iters, p.cc, mine_table, span);
+      r = stream_slice<T, kAligned, kTopWarps>(ring, warp, row, e0, e1, p.iters, p.cc, mine_table,
+                                               span, p.wait_ns);
     } else {
       for (int i = 0; i < p.iters; ++i) mine_table[i * kTopThreads] = 0xff80u;
     }
-    const float2 wr = warp_running(r, p.cc);
+    const float2 wr = warp_part(r, ring.late, p.cc);
     float um = r.m;
     for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
     if (C > 1 && mine == 0) cluster_wait();
@@ -117,12 +120,14 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   const int parts = p.slices * kTopWarps;  // <= 64
   for (int w = warp; w < p.W; w += kTopWarps) {
     float2 sum;
-    const float m = row_sum(&s.part[w * p.slices][0], parts, p.cc, sum);
+    bool late;
+    const float m = row_sum(&s.part[w * p.slices][0], parts, p.cc, sum, late);
     if (lane == 0) {
       const float2 l = log_pair(sum);
       const float score = kBeam ? p.scores[grp * p.W + w] : 0.f;
       const bool dead = kBeam && score == -INFINITY;
-      if (!dead && (m != m || m == INFINITY || score != score || score == INFINITY)) s.sel.bad = 1;
+      if (!dead && (m != m || m == INFINITY || score != score || score == INFINITY))
+        atomicOr(&s.sel.bad, late ? SV_REQ_TIMEOUT : SV_REQ_BAD_LOGITS);
       if (kBeam) {
         double off = -INFINITY;
         if (!dead && m != -INFINITY) off = row_offset(score, m, l);
@@ -134,10 +139,10 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
     }
   }
   __syncthreads();
-  const bool bad = s.sel.bad != 0;
+  const int bad = s.sel.bad;
   if (rank == 0 && t == 0) {
     if (!kBeam) p.out_lse[grp] = bad ? qnan() : s.lse;
-    if (p.out_status) p.out_status[grp] = bad ? SV_REQ_BAD_LOGITS : 0;
+    if (p.out_status) p.out_status[grp] = bad;
   }
   if (bad) {  // the same in every CTA
     if (rank == 0)
@@ -173,8 +178,8 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
 
   // The groups that reach it, eight table entries a thread.
   for (int it = rank, mine = 0; it < items; it += C, ++mine) {
-    scan_table(s.sel, ls, table + mine * p.iters * kTopThreads, p.iters, threshold(it / p.slices),
-               mine * p.iters * kTopThreads);
+    scan_table(s.sel, ls, table + mine * p.iters * kTopThreads, p.iters * kTopThreads,
+               threshold(it / p.slices), mine * p.iters * kTopThreads);
   }
   __syncthreads();
   TopShared* lead = C > 1 ? cluster.map_shared_rank(&s, 0) : &s;
@@ -238,10 +243,13 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   for (int j = count + t; j < p.n; j += kTopThreads) write_slot<kBeam>(p, grp, j, 0, -1);
 }
 
-// The candidates lie in the memory of the load stages, which are consumed by then.
+// The candidates lie in the memory of the load stages, which are consumed by
+// then (the stages' mbarriers do not: an mbarrier's memory is for nothing else
+// until it is invalidated).
 template <typename T>
 constexpr int union_bytes() {
-  return ring_bytes<T>() > (int)sizeof(Lists) ? ring_bytes<T>() : (int)sizeof(Lists);
+  return ring_bytes<T>(kTopWarps) > (int)sizeof(Lists) ? ring_bytes<T>(kTopWarps)
+                                                      : (int)sizeof(Lists);
 }
 
 template <typename T, bool kAligned, bool kBeam>
@@ -352,6 +360,7 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
   p.V = V;
   p.n = k;
   p.cc = exponent_scale(temperature);
+  p.wait_ns = wait_limit_ns();
   p.T = temperature;
   const long long rows = (long long)B * P;
   if (by_rows(dtype, rows, V)) {
@@ -395,6 +404,7 @@ sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out
   p.V = V;
   p.n = n;
   p.cc = 1.4426950408889634f;
+  p.wait_ns = wait_limit_ns();
   p.T = 1.f;
   const cudaStream_t st = (cudaStream_t)stream;
   if (need) {  // each beam's n best, then the requests'

@@ -3,41 +3,44 @@
 //
 // With a CTA per row (sv_top.cu) all resident CTAs stream at the same pace and
 // then select at the same time, and HBM idles meanwhile: a quarter of the
-// call. Here each CTA has two halves of eight warps: one streams row after
-// row, the other selects from the row before, over two sets of tables and
+// call. Here each CTA has two parts: sixteen warps stream row after row, eight
+// select from the row before, over two sets of tables and
 // sums, handed over through named barriers. Rows come from the launch's own
 // queue (cluster launch control: a CTA cancels a CTA of the grid that has not
 // started and takes its row), so the last rows spread evenly without a
-// counter in memory; the selecting half asks for them while the other streams,
+// counter in memory; the selecting warps ask for them while the others stream,
 // and deals with rows that need no work by itself.
 #include "sv_select.cuh"
 
 namespace sv {
 namespace {
 
-constexpr int kRowThreads = 2 * kTopThreads;
+constexpr int kStreamWarps = 16;
+constexpr int kRowStreamers = kStreamWarps * kWarp;
+constexpr int kRowThreads = kRowStreamers + kTopThreads;
+constexpr int kRowSpan = kRowStreamers * kEntry;  // elements of an iteration
 // named barriers, two each but the first
 enum : int { kBarSelect = 1, kBarFull = 2, kBarEmpty = 4, kBarNext = 6 };
 
 struct alignas(16) RowShared {
   uint4 answer;                 // the queue's answer
   unsigned long long bar;       // its arrival
+  unsigned long long stage_bar[kStreamWarps][kMaxStages];
   long long next[2];            // the row to stream next, by parity (-1: none)
   struct Slot {
-    float2 part[kTopWarps];     // the row's sums by warp
-    float unit[kTopThreads];    // its thread maxes
+    float2 part[kStreamWarps];  // the row's sums by warp
+    float unit[kRowStreamers];    // its thread maxes
   } slot[2];
   Select sel;
-  float2 log_sum;
-  float m;
+  int late;                     // the queue did not answer in time
 };
 constexpr int kLive = -1;
 
 __device__ __forceinline__ void bar_sync(int bar, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+  asm volatile("barrier.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(int bar, int threads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+  asm volatile("barrier.arrive %0, %1;" ::"r"(bar), "r"(threads) : "memory");
 }
 
 // Asks for a CTA of this grid that has not started; the answer (16 bytes)
@@ -80,10 +83,9 @@ __device__ __forceinline__ void fill_slots(const TopParams& p, long long row, in
 }
 
 // The next row that needs work, -1 when the queue is empty; the outputs of the
-// others on the way (a call of the selecting half).  `row`: a row taken already,
+// others on the way (a call of the selecting part).  `row`: a row taken already,
 // or -1 to ask.
-__device__ long long next_live(RowShared& s, const TopParams& p, long long row, int& asked,
-                               bool& late) {
+__device__ long long next_live(RowShared& s, const TopParams& p, long long row, int& asked) {
   const int t = threadIdx.x % kTopThreads;
   for (;;) {
     if (row < 0) {
@@ -93,8 +95,9 @@ __device__ long long next_live(RowShared& s, const TopParams& p, long long row, 
         mbar_arrive_expect_tx(smem_u32(&s.bar), 16);
         ask_for_cta(smem_u32(&s.answer), smem_u32(&s.bar));
       }
-      late = !mbar_wait(smem_u32(&s.bar), asked++ & 1);
-      if (late) return -1;
+      if (!mbar_wait(smem_u32(&s.bar), asked++ & 1)) s.late = 1;
+      group_sync<kBarSelect>();
+      if (s.late) return -1;
       row = taken_cta(smem_u32(&s.answer));
       if (row < 0) return -1;
     }
@@ -110,7 +113,7 @@ __device__ long long next_live(RowShared& s, const TopParams& p, long long row, 
   }
 }
 
-// The selecting half: one row from its table, sums and units.
+// The selecting part: one row from its table, sums and units.
 template <typename T, bool kAligned>
 __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot, long long row,
                            const uint16_t* table, const TopParams& p, const RowSpan& span) {
@@ -120,18 +123,21 @@ __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot,
   if (t == 0) s.sel.n_hits = s.sel.n_cands = 0;
   // every warp for itself: the max decides whether there is anything to select
   float2 sum;
-  const float m = row_sum(slot.part, kTopWarps, p.cc, sum);
+  bool late;
+  const float m = row_sum(slot.part, kStreamWarps, p.cc, sum, late);
   const float score = p.scores ? p.scores[row] : 0.f;
   const bool bad = m != m || m == INFINITY || score != score || score == INFINITY;
   if (t == 0) {
     const float2 l = log_pair(sum);
     if (p.out_off) {
-      p.out_off[row] = bad              ? __longlong_as_double(0x7fffffffffffffffll)
+      p.out_off[row] = late             ? INFINITY
+                       : bad            ? __longlong_as_double(0x7fffffffffffffffll)
                        : m == -INFINITY ? -INFINITY
                                         : row_offset(score, m, l);
     } else {
       p.out_lse[row] = bad ? qnan() : m == -INFINITY ? -INFINITY : m / p.T + (l.x + l.y);
-      if (p.out_status) p.out_status[row] = bad ? SV_REQ_BAD_LOGITS : 0;
+      if (p.out_status)
+        p.out_status[row] = late ? SV_REQ_TIMEOUT : bad ? SV_REQ_BAD_LOGITS : 0;
     }
   }
   if (bad || m == -INFINITY) {
@@ -140,15 +146,13 @@ __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot,
   }
   const float thr = fmaxf(unit_bound<kBarSelect>(s.sel, slot.unit, p.upi, p.n), -FLT_MAX);
   group_sync<kBarSelect>();  // (the counters are clear also when no round was needed)
-  scan_table(s.sel, ls, table, p.iters, thr, 0);
+  scan_table(s.sel, ls, table, p.iters * kRowStreamers, thr, 0);
   group_sync<kBarSelect>();
   const T* data = reinterpret_cast<const T*>(p.logits) + row * (long long)p.V;
   const int hits = s.sel.n_hits;
   if (hits <= kMaxCands)
     for (int q = t; q < hits * kGroups; q += kTopThreads) {
-      const int at = ls.rank[q / kGroups], u = q % kGroups;
-      const int i = at / kTopThreads, ti = at % kTopThreads;
-      const int j = (i * kTopThreads + ti) * kEntry + u * VEC;
+      const int j = ls.rank[q / kGroups] * kEntry + q % kGroups * VEC;
       if (j < p.V)
         list_group<T>(&s.sel.n_cands, &ls, load_group<T, kAligned>(data, j, p.V, span), thr, j);
     }
@@ -176,47 +180,50 @@ __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot,
 }
 
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParams p) {
+__global__ void __launch_bounds__(kRowThreads, 1) top_rows_kernel(const TopParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   RowShared& s = *reinterpret_cast<RowShared*>(smem);
   Lists& ls = *reinterpret_cast<Lists*>(smem + sizeof(RowShared));
   uint16_t* tables = reinterpret_cast<uint16_t*>(smem + sizeof(RowShared) + sizeof(Lists));
-  const int table = p.iters * kTopThreads;
+  const int table = p.iters * kRowStreamers;
   unsigned char* rings = smem + sizeof(RowShared) + sizeof(Lists) + 2 * 2 * table;
-  const int t = threadIdx.x % kTopThreads, lane = lane_id(), warp = t / kWarp;
+  const bool streams = threadIdx.x < kRowStreamers;
+  const int t = streams ? threadIdx.x : threadIdx.x - kRowStreamers;
+  const int lane = lane_id(), warp = t / kWarp;
   const RowSpan span = {p.first, p.last};
   if (threadIdx.x == 0) {
+    s.late = 0;
     mbar_init(smem_u32(&s.bar), 1);
     fence_mbar_init();
   }
   __syncthreads();
   const bool first_live = row_state(p, blockIdx.x) == kLive;
 
-  if (threadIdx.x >= kTopThreads) {  // the selecting half
+  if (!streams) {  // the selecting part
     int asked = 0;
-    bool late = false;
-    long long row = next_live(s, p, blockIdx.x, asked, late);
+    long long row = next_live(s, p, blockIdx.x, asked);
     if (!first_live) {
       if (t == 0) s.next[0] = row;
       bar_arrive(kBarNext, kRowThreads);
     }
     for (int k = 0; row >= 0; ++k) {
       const int b = k & 1;
-      const long long next = next_live(s, p, -1, asked, late);
+      const long long next = next_live(s, p, -1, asked);
       if (t == 0) s.next[b ^ 1] = next;
       bar_arrive(kBarNext + (b ^ 1), kRowThreads);
       bar_sync(kBarFull + b, kRowThreads);
       select_row<T, kAligned>(s, ls, s.slot[b], row, tables + b * table, p, span);
       bar_arrive(kBarEmpty + b, kRowThreads);
       // a device fault: the queue did not answer in two seconds
-      if (late && t == 0 && p.out_status) p.out_status[row] = SV_REQ_TIMEOUT;
+      if (s.late && t == 0 && p.out_status) p.out_status[row] = SV_REQ_TIMEOUT;
       row = next;
     }
     return;
   }
 
-  // The streaming half.
-  const int fold = kTopThreads / p.upi;
+  // The streaming part.
+  const int fold = kRowStreamers / p.upi;
+  Ring<T> ring(smem_u32(rings) + warp * Ring<T>::kWarpBytes, smem_u32(s.stage_bar[warp]));
   long long row = blockIdx.x;
   if (!first_live) {
     bar_sync(kBarNext, kRowThreads);
@@ -228,9 +235,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParam
     RowShared::Slot& slot = s.slot[b];
     if (k >= 2) bar_sync(kBarEmpty + b, kRowThreads);  // row k - 2 is selected
     const T* data = reinterpret_cast<const T*>(p.logits) + row * (long long)p.V;
-    const RunningSum r = stream_slice<T, kAligned>(smem_u32(rings), data, 0, p.V, p.iters, p.cc,
-                                                   tables + b * table + t, span);
-    const float2 wr = warp_running(r, p.cc);
+    const RunningSum r = stream_slice<T, kAligned, kStreamWarps>(
+        ring, warp, data, 0, p.V, p.iters, p.cc, tables + b * table + t, span, p.wait_ns);
+    const float2 wr = warp_part(r, ring.late, p.cc);
     float um = r.m;
     for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
     if (lane == 0) slot.part[warp] = wr;
@@ -248,12 +255,12 @@ template <typename T, bool kAligned>
 cudaError_t launch_rows(TopParams p, long long rows, cudaStream_t stream) {
   static PerDevice once;
   auto* fn = top_rows_kernel<T, kAligned>;
-  const size_t fixed = sizeof(RowShared) + sizeof(Lists) + ring_bytes<T>();
+  const size_t fixed = sizeof(RowShared) + sizeof(Lists) + ring_bytes<T>(kStreamWarps);
   const cudaError_t err = per_device(once, nullptr, [&](int&) {
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
   });
   if (err != cudaSuccess) return err;
-  fn<<<dim3((unsigned)rows), kRowThreads, fixed + 4 * (size_t)p.iters * kTopThreads, stream>>>(p);
+  fn<<<dim3((unsigned)rows), kRowThreads, fixed + 4 * (size_t)p.iters * kRowStreamers, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -277,11 +284,12 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
   if (t < p.W) {
     const double o = off[b * p.W + t];
     s_off[t] = o;
-    if (o != o) sel.bad = 1;
+    if (o != o) atomicOr(&sel.bad, SV_REQ_BAD_LOGITS);
+    if (o == INFINITY) atomicOr(&sel.bad, SV_REQ_TIMEOUT);
   }
   __syncthreads();
-  const bool bad = sel.bad != 0;
-  if (t == 0 && p.out_status) p.out_status[b] = bad ? SV_REQ_BAD_LOGITS : 0;
+  const int bad = sel.bad;
+  if (t == 0 && p.out_status) p.out_status[b] = bad;
   auto write = [&](int slot, unsigned long long key, int idx) {
     const long long o = b * p.n + slot;
     const int w = idx < 0 ? -1 : idx / p.V;
@@ -356,8 +364,9 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
 }  // namespace
 
 bool top_rows_fit(sv_dtype dtype, int V) {
-  const size_t tables = 4 * (size_t)((V + kTopSpan - 1) / kTopSpan) * kTopThreads;
-  const size_t ring = dtype == SV_BF16 ? ring_bytes<uint16_t>() : ring_bytes<float>();
+  const size_t tables = 4 * (size_t)((V + kRowSpan - 1) / kRowSpan) * kRowStreamers;
+  const size_t ring = dtype == SV_BF16 ? ring_bytes<uint16_t>(kStreamWarps)
+                                       : ring_bytes<float>(kStreamWarps);
   return sizeof(RowShared) + sizeof(Lists) + ring + tables <= (size_t)kRowsSmem;
 }
 
@@ -365,8 +374,8 @@ cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long
                             cudaStream_t stream) {
   p.slices = 1;
   p.slice = (p.V + 255) / 256 * 256;
-  p.iters = (p.V + kTopSpan - 1) / kTopSpan;
-  p.upi = kTopThreads;
+  p.iters = (p.V + kRowSpan - 1) / kRowSpan;
+  p.upi = kRowStreamers;
   while (p.upi > 32 && p.upi / 2 >= 4 * p.n) p.upi /= 2;
   if (dtype == SV_BF16)
     return aligned ? launch_rows<uint16_t, true>(p, rows, stream)
