@@ -404,8 +404,7 @@ sv_status spec_ngram_propose(const int32_t* tokens, const int32_t* lens, int B, 
  *   out_lse     [B, P] fp32: log sum_j exp(l_j / T); -inf for a row that is
  *               not read or has no finite logit.
  *   out_status  [B, P] int32 or NULL: SV_REQ_* bits per row.  A row with NaN or
- *               +inf (SV_REQ_BAD_LOGITS), or whose wait for staged logits ran out
- *               (SV_REQ_TIMEOUT), has no record (-1, -inf) and lse NaN.
+ *               +inf (SV_REQ_BAD_LOGITS) has no record (-1, -inf) and lse NaN.
  *   B, P, V     0 <= B <= SV_MAX_B, P >= 1, B * P <= SV_MAX_ROWS, 1 <= V <= SV_MAX_V.
  * No workspace: a call keeps nothing, so calls may overlap on any streams. */
 sv_status spec_top_logits(const void* logits, int k, float temperature, const int32_t* lens,
@@ -485,8 +484,7 @@ sv_status spec_distill_grad(const void* student_logits, const int32_t* top_ids,
  *               candidate; out_scores [B, n] fp32.  Candidates have finite logits; past
  *               the last one the slots hold -1, -1 and -inf.
  *   out_status  [B] int32 or NULL: SV_REQ_BAD_LOGITS when a live beam's row has NaN
- *               or +inf, or a score is NaN or +inf, SV_REQ_TIMEOUT; nothing is kept
- *               then.
+ *               or +inf, or a score is NaN or +inf; nothing is kept then.
  *   1 <= W <= SV_MAX_BEAMS, 1 <= n <= SV_MAX_TOP, 0 <= B <= SV_MAX_B, and
  *   ceil(W / 8) * ceil(V / 8192) <= 256 (V <= 2097152 up to 8 beams, 262144 with
  *   64).  Scores are compared in 64 bits (their row sums are of 32-bit terms).

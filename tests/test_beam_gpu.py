@@ -253,17 +253,3 @@ def test_beams_grow_a_tree_that_is_verified_and_compacted():
         for d in range(1, n):
             want = want + embed[path[d]]
             assert torch.equal(got[b, d], want)
-
-
-@pytest.mark.parametrize("shape", [(2, 3, 5001), (40, 8, 9001)])
-def test_wait_limit_runs_out(shape):
-    x, s = case(*shape, BF16, 30)
-    old = api.wait_limit_ns()
-    try:
-        api.set_wait_limit_ns(0)
-        out = api.spec_beam_select(x, s, 5)
-        torch.cuda.synchronize()
-    finally:
-        api.set_wait_limit_ns(old)
-    assert bool((out.status == api.REQ_TIMEOUT).all()) and bool((out.tokens == -1).all())
-    check(x[:2].contiguous(), s[:2].contiguous(), 5)

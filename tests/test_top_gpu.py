@@ -170,21 +170,3 @@ def test_two_graphs_on_two_streams():
         want = api.spec_top_logits(x, 40)
         assert torch.equal(out.ids, want.ids) and torch.equal(out.lse, want.lse)
         plain.check_top(x[:2], 40, 1.0, api.spec_top_logits(x[:2].contiguous(), 40))
-
-
-@pytest.mark.parametrize("shape", [(2, 3, 5001), (60, 6, 9001)])
-def test_wait_limit_runs_out(shape):
-    """With a limit of 0 the waits give up at once: every row that is read says so, and the
-    next call is right again."""
-    x = rows(shape, BF16, 30)
-    lens = torch.full((shape[0],), shape[1] - 1, dtype=torch.int32, device="cuda")
-    old = api.wait_limit_ns()
-    try:
-        api.set_wait_limit_ns(0)
-        out = api.spec_top_logits(x, 5, lens=lens)
-        torch.cuda.synchronize()
-    finally:
-        api.set_wait_limit_ns(old)
-    assert bool((out.status[:, :-1] == api.REQ_TIMEOUT).all()) and bool((out.ids == -1).all())
-    assert bool((out.status[:, -1] == 0).all())
-    check(x[:2].contiguous(), 5)

@@ -7,7 +7,7 @@
 // `units` disjoint parts of the data have maxes u_1.., the n-th largest of
 // them is a bound that at least n elements reach, so every kept element is at
 // or above it, and little else is: with n of U parts occupied about
-// U ln(U / (U - n)) elements (74 for n = 64 of 256).  Only the 32-element
+// U ln(U / (U - n)) elements (89 for n = 64 of 128).  Only the 32-element
 // groups whose max reaches the bound are read again (from L2), their elements
 // at or above it are listed, and the list is sorted by counting.  When the
 // list does not fit (long rows of equal logits), each row is selected by radix
@@ -23,7 +23,7 @@ namespace sv {
 
 constexpr int kTopSpan = 8192;        // elements of a CTA's iteration: 32 a thread
 constexpr int kMaxTables = 256;       // iterations of a CTA over its items: 512 bytes each
-constexpr int kRowsSmem = 220 * 1024;  // shared memory of a CTA of the row kernel, at most
+constexpr int kRowsSmem = 112 * 1024;  // shared memory of a CTA of the row kernel: two on an SM
 
 struct TopParams {
   const void* logits;   // [B*P, V] (record) or [B*W, V] (beams)
@@ -33,7 +33,7 @@ struct TopParams {
   int* out_parents;     // beams: [B, n]
   float* out_values;    // logits [rows, n], scores [B, n]
   float* out_lse;       // record: [B*P]
-  double* out_off;      // row kernel for beams: [B*W] score - lse (-inf: no candidates, NaN: bad, inf: late)
+  double* out_off;      // row kernel for beams: [B*W] score - lse (-inf: no candidates, NaN: bad)
   int* out_status;
   int P;                // record: rows per request
   int W;                // rows per cluster (record: 1)
@@ -44,7 +44,6 @@ struct TopParams {
   int table_bytes;
   float cc;             // log2(e) / T
   float T;
-  unsigned long long wait_ns;  // limit of the waits for staged logits
   char* first;          // the logits' memory
   char* last;
 };
@@ -80,7 +79,7 @@ __device__ __forceinline__ void group_sync() {
 // Scratch of a selection.
 struct Select {
   unsigned hist[256];
-  int flag[2][kTopWarps];
+  unsigned bound;  // ordered
   int n_hits, n_cands, overflow, bad, pick[4];
 };
 
@@ -93,32 +92,48 @@ struct alignas(16) Lists {
 };
 
 // Load stages: each warp streams 1024-element chunks through its own ring by
-// bulk copies (a word more than a chunk, for rows off 16-byte boundaries); no
-// barrier but the warp's own.
-constexpr int kMaxStages = 4;
+// 16-byte asynchronous copies (a word more than a chunk, for rows off 16-byte
+// boundaries); no barrier but the warp's own. 2 KB bulk copies into the same
+// ring reached 5.2 TB/s where these reach 6.5 (912 and 2432 rows of 152064
+// bf16 logits, the slope).
 template <typename T>
 struct Ring {
   static constexpr int kBytes = kChunk * (int)sizeof(T) + 16;
-  static constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
+  static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
   static constexpr int kWarpBytes = kBytes * kStages;
-  static_assert(kStages <= kMaxStages, "an mbarrier for each stage");
-
-  uint32_t at, bars;    // this warp's stages and their mbarriers
-  uint32_t chunks = 0;  // consumed so far: the next one's stage and phase
-  bool late = false;    // a copy did not come in time: the ring is not used again
-  __device__ __forceinline__ uint32_t bar(uint32_t n) const { return bars + n % kStages * 8; }
-  __device__ __forceinline__ uint32_t stage(uint32_t n) const {
-    return at + n % kStages * kBytes;
-  }
-  __device__ __forceinline__ Ring(uint32_t stages, uint32_t mbarriers)
-      : at(stages), bars(mbarriers) {
-    if (lane_id() == 0) {
-      for (int q = 0; q < kStages; ++q) mbar_init(bar(q), 1);
-      fence_mbar_init();
-    }
-    __syncwarp();
-  }
 };
+
+// Packed bf16 comparisons (1.0 where true) and additions.
+__device__ __forceinline__ uint32_t gt_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t eq_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("set.eq.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The two halves of w that are >= those of thr, as bits 0 and 1.
+__device__ __forceinline__ unsigned ge_bits_bf16x2(uint32_t w, uint32_t thr) {
+  unsigned r;
+  asm("{\n .reg .pred p, q;\n .reg .u32 h;\n setp.ge.bf16x2 p|q, %1, %2;\n"
+      " selp.u32 %0, 1, 0, p;\n selp.u32 h, 2, 0, q;\n or.b32 %0, %0, h;\n}"
+      : "=&r"(r)
+      : "r"(w), "r"(thr));
+  return r;
+}
+
+// The upper 16 bits of v rounded down: a bf16 value <= v (v itself for bf16).
+__device__ __forceinline__ uint16_t down_bf16(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return (uint16_t)((b & 0x80000000u) ? (b + 0xffffu) >> 16 : b >> 16);
+}
 
 // The upper 16 bits of v rounded up: a bf16 value >= v (v itself for bf16).
 __device__ __forceinline__ uint16_t up_bf16(float v) {
@@ -126,49 +141,35 @@ __device__ __forceinline__ uint16_t up_bf16(float v) {
   return (uint16_t)((b & 0x80000000u) ? b >> 16 : (b + 0xffffu) >> 16);
 }
 
-// The n-th largest of the cluster's unit bounds to 16 bits (rounded down); -inf
-// when fewer than n are finite.  A call of the group: each warp holds all units
-// as ordered keys, and every round tests one threshold per warp, so the range
-// of keys shrinks ninefold (a bisection by one warp took 4000 cycles of a
-// row's 87000; this takes a quarter).
-template <int kPer, int kBar>
-__device__ float unit_bound(Select& s, const float* unit, int units, int n) {
-  const int warp = threadIdx.x % kTopThreads / kWarp;
-  int k[kPer], hi = 0, lo = 0xffff;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = j * kWarp + lane_id();
-    const float v = i < units ? unit[i] : -INFINITY;
-    k[j] = v > -INFINITY ? (int)(ordered(v) >> 16) : 0;  // below every finite value's key
-    hi = max(hi, k[j]);
-    lo = min(lo, k[j]);
-  }
-  if (units < n) return -INFINITY;
-  lo = __reduce_min_sync(0xffffffffu, lo);       // at least n units reach lo
-  hi = __reduce_max_sync(0xffffffffu, hi) + 1;   // fewer than n reach hi
-  for (int round = 0; hi - lo > 1; ++round) {
-    const int step = (hi - lo + kTopWarps) / (kTopWarps + 1), at = lo + step * (warp + 1);
-    unsigned c = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) c += k[j] >= at ? 1u : 0u;
-    const bool ok = at < hi && (int)__reduce_add_sync(0xffffffffu, c) >= n;
-    // the warps' answers are monotone; two sets of flags need one barrier a round
-    if (lane_id() == 0) s.flag[round & 1][warp] = ok ? 1 : 0;
-    group_sync<kBar>();
-    const unsigned yes = __ballot_sync(0xffffffffu, lane_id() < kTopWarps &&
-                                                        s.flag[round & 1][lane_id() % kTopWarps]);
-    const int up = __popc(yes);
-    hi = min(hi, lo + step * (up + 1));
-    lo += step * up;
-  }
-  return lo ? of_ordered((uint32_t)lo << 16) : -INFINITY;
-}
-
+// The n-th largest of up to 512 units (bf16 values in unit[], rounded down);
+// -inf when fewer than n are finite or there are fewer than n. A call of the
+// group: each thread counts how many units are above its own, eight to a
+// 16-byte word, two to an instruction (counts up to 256 are exact in bf16); the
+// least unit with fewer than n above it is the bound.
 template <int kBar>
-__device__ __forceinline__ float unit_bound(Select& s, const float* unit, int units, int n) {
-  return units <= 64    ? unit_bound<2, kBar>(s, unit, units, n)
-         : units <= 256 ? unit_bound<8, kBar>(s, unit, units, n)
-                        : unit_bound<16, kBar>(s, unit, units, n);
+__device__ float unit_bound(Select& s, const uint16_t* unit, int units, int n) {
+  if (units < n) return -INFINITY;
+  const int t = threadIdx.x % kTopThreads;
+  if (t == 0) s.bound = 0xffffffffu;
+  group_sync<kBar>();
+  const uint4* words = reinterpret_cast<const uint4*>(unit);
+  for (int i = t; i < units; i += kTopThreads) {
+    const uint32_t mine = unit[i], both = mine | mine << 16;
+    float above = 0.f;
+    for (int w0 = 0; w0 < units / 8; w0 += 16) {  // units: a multiple of 8
+      uint32_t a = 0, b = 0;                      // two bf16 counts each, up to 32
+#pragma unroll 4
+      for (int w = w0; w < min(w0 + 16, units / 8); ++w) {
+        const uint4 v = words[w];
+        a = add_bf16x2(a, add_bf16x2(gt_bf16x2(v.x, both), gt_bf16x2(v.y, both)));
+        b = add_bf16x2(b, add_bf16x2(gt_bf16x2(v.z, both), gt_bf16x2(v.w, both)));
+      }
+      above += (bf16_lo(a) + bf16_hi(a)) + (bf16_lo(b) + bf16_hi(b));
+    }
+    if (above < (float)n) atomicMin(&s.bound, ordered(bf16_lo(mine)));
+  }
+  group_sync<kBar>();
+  return of_ordered(s.bound);
 }
 
 template <bool kBeam>
@@ -245,16 +246,16 @@ __device__ __forceinline__ bool before(const Lists& s, int j, unsigned long long
 
 // rank[i] = the number of entries that come before entry i, i < count: the
 // whole group, each entry's comparisons shared by as many threads as there are
-// warps for all entries.
+// for all entries.
 template <bool kBeam, int kBar>
 __device__ void rank_list(Lists& s, int count) {
   const int t = threadIdx.x % kTopThreads;
   for (int i = t; i < count; i += kTopThreads) s.rank[i] = 0;
   group_sync<kBar>();
-  const int width = (count + kWarp - 1) / kWarp * kWarp;
-  if (width <= kTopThreads / 2) {
-    const int ways = kTopThreads / width, way = t / width, i = t - way * width;
-    if (way < ways && i < count) {
+  if (count <= kTopThreads / 2) {
+    const int ways = count ? kTopThreads / count : 0, way = count ? t / count : 0;
+    const int i = t - way * count;
+    if (way < ways) {
       const unsigned long long key = s.key[i];
       const int idx = s.idx[i];
       int r = 0;
@@ -318,45 +319,41 @@ __device__ int prune(Select& s, Lists& ls, int count, int n) {
 // One pass of kWarps warps over elements e0 .. e1 - 1 of a row: the thread's
 // running sum, and at table[i * kWarps * 32] the max of its 32 elements of
 // iteration i (elements (i * kWarps * 32 + t) * 32 on of the slice, t the
-// thread: warp w has chunk i * kWarps + w).  When a copy does not come in time
-// the sum is -1 and the max NaN.
+// thread: warp w has chunk i * kWarps + w).
 template <typename T, bool kAligned, int kWarps>
-__device__ __forceinline__ RunningSum stream_slice(Ring<T>& ring, int warp, const T* row, int e0,
+__device__ __forceinline__ RunningSum stream_slice(uint32_t ring, int warp, const T* row, int e0,
                                                    int e1, int iters, float c, uint16_t* table,
-                                                   const RowSpan& span,
-                                                   unsigned long long wait_ns) {
+                                                   const RowSpan& span) {
   constexpr int VEC = Group<T>::VEC;
   constexpr int kGroups = kEntry / VEC;  // 16-byte groups of a lane: 4 or 8
   constexpr int kAtOnce = 4;
-  constexpr int kStages = Ring<T>::kStages;
+  using R = Ring<T>;
   const int lane = lane_id();
   const T* tag = nullptr;
   const int chunks = (e1 - e0 + kChunk - 1) / kChunk;
-  const int todo = ring.late ? 0 : (chunks - warp + kWarps - 1) / kWarps;  // may be <= 0
+  const int todo = (chunks - warp + kWarps - 1) / kWarps;  // this warp's (may be <= 0)
   const uint32_t off = kAligned ? 0u : (uint32_t)(uintptr_t)row & 15u;
-  int issued = 0;
-  auto issue = [&]() {  // the next chunk into its stage
-    if (issued < todo) {
-      const int j = e0 + (issued * kWarps + warp) * kChunk;
-      const uint32_t n = ring.chunks + issued;
-      load_chunk_async<T, kAligned>(ring.stage(n), ring.bar(n), row, j, min(j + kChunk, e1), off,
-                                    span);
-      ++issued;
+  ring += warp * R::kWarpBytes;
+  auto issue = [&](int i) {  // iteration i's chunk into its stage
+    if (i < todo) {
+      const int j = e0 + (i * kWarps + warp) * kChunk;
+      load_chunk_async<T, kAligned>(ring + i % R::kStages * R::kBytes, row, j,
+                                    min(j + kChunk, e1), off, span);
     }
+    copies_commit();
   };
   RunningSum r;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue();
-  int i = 0;
-  for (; i < todo; ++i) {
-    const uint32_t n = ring.chunks + i;
-    if (!__all_sync(0xffffffffu, mbar_wait(ring.bar(n), n / kStages & 1u, wait_ns))) {
-      ring.late = true;
-      break;
+  for (int i = 0; i < R::kStages - 1; ++i) issue(i);
+  for (int i = 0; i < iters; ++i) {
+    if (i >= todo) {
+      table[i * kWarps * kWarp] = 0xff80u;
+      continue;
     }
-    __syncwarp();  // the stage before is read by all lanes: it is filled again
-    issue();
-    const uint32_t stage = ring.stage(n);
+    copies_wait_but<R::kStages - 2>();
+    __syncwarp();  // every lane's copies of this stage landed; the stage before is read
+    issue(i + R::kStages - 1);
+    const uint32_t stage = ring + i % R::kStages * R::kBytes;
     const int j = e0 + (i * kWarps + warp) * kChunk;
     float gm = -INFINITY;
 #pragma unroll
@@ -382,40 +379,19 @@ __device__ __forceinline__ RunningSum stream_slice(Ring<T>& ring, int warp, cons
     }
     table[i * kWarps * kWarp] = up_bf16(gm);
   }
-  if (ring.late) {
-    // the copies under way land before the memory is left or used again
-    for (int q = 0; q < issued; ++q) {
-      const uint32_t n = ring.chunks + q;
-      mbar_wait(ring.bar(n), n / kStages & 1u);
-    }
-    r.m = qnan();
-    r.s = -1.f;
-  } else if (todo > 0) {
-    ring.chunks += todo;
-  }
-  for (; i < iters; ++i) table[i * kWarps * kWarp] = 0xff80u;
-  __syncwarp();
+  __syncwarp();  // (the next slice refills the stages)
   return r;
-}
-
-// The warp's {max, sum}, {NaN, -1} when it was late.
-__device__ __forceinline__ float2 warp_part(const RunningSum& r, bool late, float c) {
-  const float2 v = warp_running(r, c);
-  return late ? make_float2(qnan(), -1.f) : v;
 }
 
 // The table entries at or above thr, eight a thread and step, as `base` plus
 // their number in rank[] (at most kMaxCands; n_hits counts all).
 __device__ __forceinline__ void scan_table(Select& s, Lists& ls, const uint16_t* table,
                                            int entries, float thr, int base) {
+  const uint32_t up = up_bf16(thr), both = up | up << 16;  // entry >= thr: entry >= thr rounded up
   for (int v = threadIdx.x % kTopThreads; v < entries / 8; v += kTopThreads) {
     const uint4 e = load128(table + 8 * v);
-    const uint32_t w[4] = {e.x, e.y, e.z, e.w};
-    unsigned hits = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      hits |= (bf16_lo(w[q]) >= thr ? 1u << (2 * q) : 0u) |
-              (bf16_hi(w[q]) >= thr ? 2u << (2 * q) : 0u);
+    unsigned hits = ge_bits_bf16x2(e.x, both) | ge_bits_bf16x2(e.y, both) << 2 |
+                    ge_bits_bf16x2(e.z, both) << 4 | ge_bits_bf16x2(e.w, both) << 6;
     if (hits) {
       int h = atomicAdd(&s.n_hits, __popc(hits));
       for (; hits; hits &= hits - 1u, ++h)
@@ -424,9 +400,9 @@ __device__ __forceinline__ void scan_table(Select& s, Lists& ls, const uint16_t*
   }
 }
 
-// The elements of a group at or above thr go to a list (the logit now, the
-// key when the list is complete).
-template <typename T>
+// The elements of a group at or above thr go to a list: a record's keys as they
+// are, for beams the logit now and the key when the list is complete.
+template <typename T, bool kBeam>
 __device__ __forceinline__ void list_group(int* n_cands, Lists* to, const uint4& g, float thr,
                                            int idx) {
   constexpr int VEC = Group<T>::VEC;
@@ -439,22 +415,21 @@ __device__ __forceinline__ void list_group(int* n_cands, Lists* to, const uint4&
   for (int e = 0; e < VEC; ++e)
     if (in >> e & 1u) {
       if (o < kMaxCands) {
-        to->key[o] = __float_as_uint(Lane<T, VEC>::get(g, e));
+        const float l = Lane<T, VEC>::get(g, e);
+        to->key[o] = kBeam ? __float_as_uint(l)
+                           : ((unsigned long long)ordered(l) << 32) | (uint32_t)~(idx + e);
         to->idx[o] = idx + e;
       }
       ++o;
     }
 }
 
-// A row's {max, sum as a pair} from its warps' parts (one warp, up to 64 parts);
-// late: a part is missing.
-__device__ __forceinline__ float row_sum(const float2* parts, int n, float c, float2& sum,
-                                         bool& late) {
+// A row's {max, sum as a pair} from its warps' parts (one warp, up to 64 parts).
+__device__ __forceinline__ float row_sum(const float2* parts, int n, float c, float2& sum) {
   const int lane = lane_id();
   const float2 a = lane < n ? parts[lane] : make_float2(-INFINITY, 0.f);
   const float2 b = lane + kWarp < n ? parts[lane + kWarp] : make_float2(-INFINITY, 0.f);
   const float m = warp_max_nan(max_nan(a.x, b.x));
-  late = __any_sync(0xffffffffu, a.y < 0.f || b.y < 0.f);
   sum = warp_sum_pair(a.y * to_frame(a.x, m, c) + b.y * to_frame(b.x, m, c));
   return m;
 }

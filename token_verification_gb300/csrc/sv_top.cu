@@ -25,12 +25,11 @@ constexpr int kManyRows = 152;
 
 struct alignas(16) TopShared {
   float2 part[kMaxItems][kTopWarps];  // per item and warp: {max, sum of 2^((l - max) c)}
-  float unit[kMaxUnits];              // unit maxes, item by item
+  alignas(16) uint16_t unit[kMaxUnits];  // unit maxes, item by item: bf16 rounded down
   double off[SV_MAX_BEAMS];           // beams: score - lse of each row (-inf: no candidates)
   float off_down[SV_MAX_BEAMS];       // the same rounded down
   float thr[SV_MAX_BEAMS];            // the lowest logit a candidate of the row can have
   float lse;                          // record
-  unsigned long long bar[kTopWarps][kMaxStages];  // the stages' mbarriers
   Select sel;
 };
 
@@ -83,7 +82,6 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   if (C > 1) cluster_arrive();
 
   // One pass over each item.
-  Ring<T> ring(smem_u32(rings) + warp * Ring<T>::kWarpBytes, smem_u32(s.bar[warp]));
   const int fold = kTopThreads / p.upi;
   for (int it = rank, mine = 0; it < items; it += C, ++mine) {
     const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
@@ -94,19 +92,19 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
     const bool live = !kBeam || p.scores[rowid] != -INFINITY;
     RunningSum r;
     if (live) {
-      r = stream_slice<T, kAligned, kTopWarps>(ring, warp, row, e0, e1, p.iters, p.cc, mine_table,
-                                               span, p.wait_ns);
+      r = stream_slice<T, kAligned, kTopWarps>(smem_u32(rings), warp, row, e0, e1, p.iters, p.cc,
+                                               mine_table, span);
     } else {
       for (int i = 0; i < p.iters; ++i) mine_table[i * kTopThreads] = 0xff80u;
     }
-    const float2 wr = warp_part(r, ring.late, p.cc);
+    const float2 wr = warp_running(r, p.cc);
     float um = r.m;
     for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
     if (C > 1 && mine == 0) cluster_wait();
     for (int c = 0; c < C; ++c) {
       TopShared* to = C > 1 ? cluster.map_shared_rank(&s, c) : &s;
       if (lane == 0) to->part[it][warp] = wr;
-      if ((t & (fold - 1)) == 0) to->unit[it * p.upi + t / fold] = um;
+      if ((t & (fold - 1)) == 0) to->unit[it * p.upi + t / fold] = down_bf16(um);
     }
   }
   if (C > 1) {
@@ -120,14 +118,13 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   const int parts = p.slices * kTopWarps;  // <= 64
   for (int w = warp; w < p.W; w += kTopWarps) {
     float2 sum;
-    bool late;
-    const float m = row_sum(&s.part[w * p.slices][0], parts, p.cc, sum, late);
+    const float m = row_sum(&s.part[w * p.slices][0], parts, p.cc, sum);
     if (lane == 0) {
       const float2 l = log_pair(sum);
       const float score = kBeam ? p.scores[grp * p.W + w] : 0.f;
       const bool dead = kBeam && score == -INFINITY;
       if (!dead && (m != m || m == INFINITY || score != score || score == INFINITY))
-        atomicOr(&s.sel.bad, late ? SV_REQ_TIMEOUT : SV_REQ_BAD_LOGITS);
+        s.sel.bad = SV_REQ_BAD_LOGITS;
       if (kBeam) {
         double off = -INFINITY;
         if (!dead && m != -INFINITY) off = row_offset(score, m, l);
@@ -152,12 +149,11 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
 
   // The bound that n elements reach, and each row's lowest candidate logit.
   const int units = items * p.upi;
-  if (kBeam) {
+  if (kBeam) {  // the units' scores, rounded down
     for (int u = t; u < units; u += kTopThreads) {
-      const float l = s.unit[u], off = s.off_down[u / (p.upi * p.slices)];
-      s.unit[u] = l == -INFINITY || off == -INFINITY ? -INFINITY : __fadd_rd(off, l);
+      const float l = bf16_lo(s.unit[u]), off = s.off_down[u / (p.upi * p.slices)];
+      s.unit[u] = l == -INFINITY || off == -INFINITY ? 0xff80u : down_bf16(__fadd_rd(off, l));
     }
-    __syncthreads();
   }
   const float bound = unit_bound<0>(s.sel, s.unit, units, p.n);
   if (kBeam) {
@@ -197,7 +193,7 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
       const int j = e0 + (i * kTopThreads + ti) * kEntry + u * VEC;
       if (j >= min(e0 + p.slice, p.V)) continue;
       const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
-      list_group<T>(&lead->sel.n_cands, lead_ls, load_group<T, kAligned>(row, j, p.V, span),
+      list_group<T, kBeam>(&lead->sel.n_cands, lead_ls, load_group<T, kAligned>(row, j, p.V, span),
                     threshold(w), w * p.V + j);
     }
   }
@@ -227,12 +223,13 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
       __syncthreads();
     }
   } else {
-    for (int i = t; i < count; i += kTopThreads) {
-      const int idx = ls.idx[i];
-      set_candidate<kBeam>(ls, i, __uint_as_float((uint32_t)ls.key[i]),
-                           kBeam ? s.off[idx / p.V] : 0.0, idx);
+    if (kBeam) {
+      for (int i = t; i < count; i += kTopThreads) {
+        const int idx = ls.idx[i];
+        set_candidate<true>(ls, i, __uint_as_float((uint32_t)ls.key[i]), s.off[idx / p.V], idx);
+      }
+      __syncthreads();
     }
-    __syncthreads();
     if (count > kRankAll) count = prune<0>(s.sel, ls, count, p.n);
   }
   rank_list<kBeam, 0>(ls, count);
@@ -243,9 +240,7 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   for (int j = count + t; j < p.n; j += kTopThreads) write_slot<kBeam>(p, grp, j, 0, -1);
 }
 
-// The candidates lie in the memory of the load stages, which are consumed by
-// then (the stages' mbarriers do not: an mbarrier's memory is for nothing else
-// until it is invalidated).
+// The candidates lie in the memory of the load stages, which are consumed by then.
 template <typename T>
 constexpr int union_bytes() {
   return ring_bytes<T>(kTopWarps) > (int)sizeof(Lists) ? ring_bytes<T>(kTopWarps)
@@ -313,10 +308,10 @@ sv_status run_top(TopParams& p, sv_dtype dtype, long long groups, cudaStream_t s
   const int items = p.W * p.slices;
   if (items > kMaxItems || (long long)((items + C - 1) / C) * p.iters > kMaxTables)
     return SV_ERR_SHAPE;
-  // four units per kept candidate (or the finest there are), at least one a warp
+  // two units per kept candidate (or the finest there are), at least one a warp
   p.upi = kTopThreads;
   while (p.upi > kTopWarps && items * p.upi > kMaxUnits) p.upi /= 2;
-  while (p.upi > kTopWarps && items * p.upi / 2 >= 4 * p.n) p.upi /= 2;
+  while (p.upi > kTopWarps && items * p.upi / 2 >= 2 * p.n) p.upi /= 2;
   p.table_bytes = (items + C - 1) / C * p.iters * kTopThreads * 2;
   cudaError_t err;
   if (dtype == SV_BF16)
@@ -360,7 +355,6 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
   p.V = V;
   p.n = k;
   p.cc = exponent_scale(temperature);
-  p.wait_ns = wait_limit_ns();
   p.T = temperature;
   const long long rows = (long long)B * P;
   if (by_rows(dtype, rows, V)) {
@@ -404,7 +398,6 @@ sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out
   p.V = V;
   p.n = n;
   p.cc = 1.4426950408889634f;
-  p.wait_ns = wait_limit_ns();
   p.T = 1.f;
   const cudaStream_t st = (cudaStream_t)stream;
   if (need) {  // each beam's n best, then the requests'

@@ -3,19 +3,19 @@
 //
 // With a CTA per row (sv_top.cu) all resident CTAs stream at the same pace and
 // then select at the same time, and HBM idles meanwhile: a quarter of the
-// call. Here each CTA has two parts: sixteen warps stream row after row, eight
-// select from the row before, over two sets of tables and
+// call. Here each CTA has two halves of eight warps: one streams row after
+// row, the other selects from the row before, over two sets of tables and
 // sums, handed over through named barriers. Rows come from the launch's own
 // queue (cluster launch control: a CTA cancels a CTA of the grid that has not
 // started and takes its row), so the last rows spread evenly without a
-// counter in memory; the selecting warps ask for them while the others stream,
+// counter in memory; the selecting half asks for them while the other streams,
 // and deals with rows that need no work by itself.
 #include "sv_select.cuh"
 
 namespace sv {
 namespace {
 
-constexpr int kStreamWarps = 16;
+constexpr int kStreamWarps = 8;
 constexpr int kRowStreamers = kStreamWarps * kWarp;
 constexpr int kRowThreads = kRowStreamers + kTopThreads;
 constexpr int kRowSpan = kRowStreamers * kEntry;  // elements of an iteration
@@ -25,11 +25,10 @@ enum : int { kBarSelect = 1, kBarFull = 2, kBarEmpty = 4, kBarNext = 6 };
 struct alignas(16) RowShared {
   uint4 answer;                 // the queue's answer
   unsigned long long bar;       // its arrival
-  unsigned long long stage_bar[kStreamWarps][kMaxStages];
   long long next[2];            // the row to stream next, by parity (-1: none)
   struct Slot {
     float2 part[kStreamWarps];  // the row's sums by warp
-    float unit[kRowStreamers];    // its thread maxes
+    alignas(16) uint16_t unit[kRowStreamers];  // its unit maxes, bf16 rounded down
   } slot[2];
   Select sel;
   int late;                     // the queue did not answer in time
@@ -83,7 +82,7 @@ __device__ __forceinline__ void fill_slots(const TopParams& p, long long row, in
 }
 
 // The next row that needs work, -1 when the queue is empty; the outputs of the
-// others on the way (a call of the selecting part).  `row`: a row taken already,
+// others on the way (a call of the selecting half).  `row`: a row taken already,
 // or -1 to ask.
 __device__ long long next_live(RowShared& s, const TopParams& p, long long row, int& asked) {
   const int t = threadIdx.x % kTopThreads;
@@ -113,7 +112,7 @@ __device__ long long next_live(RowShared& s, const TopParams& p, long long row, 
   }
 }
 
-// The selecting part: one row from its table, sums and units.
+// The selecting half: one row from its table, sums and units.
 template <typename T, bool kAligned>
 __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot, long long row,
                            const uint16_t* table, const TopParams& p, const RowSpan& span) {
@@ -122,50 +121,55 @@ __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot,
   const int t = threadIdx.x % kTopThreads;
   if (t == 0) s.sel.n_hits = s.sel.n_cands = 0;
   // every warp for itself: the max decides whether there is anything to select
-  float2 sum;
-  bool late;
-  const float m = row_sum(slot.part, kStreamWarps, p.cc, sum, late);
+  const float m = warp_max_nan(lane_id() < kStreamWarps ? slot.part[lane_id()].x : -INFINITY);
   const float score = p.scores ? p.scores[row] : 0.f;
   const bool bad = m != m || m == INFINITY || score != score || score == INFINITY;
-  if (t == 0) {
+  auto row_outputs = [&]() {  // one warp: the log-sum-exp, or the beam's offset
+    float2 sum;
+    row_sum(slot.part, kStreamWarps, p.cc, sum);
+    if (lane_id() != 0) return;
     const float2 l = log_pair(sum);
     if (p.out_off) {
-      p.out_off[row] = late             ? INFINITY
-                       : bad            ? __longlong_as_double(0x7fffffffffffffffll)
+      p.out_off[row] = bad              ? __longlong_as_double(0x7fffffffffffffffll)
                        : m == -INFINITY ? -INFINITY
                                         : row_offset(score, m, l);
     } else {
       p.out_lse[row] = bad ? qnan() : m == -INFINITY ? -INFINITY : m / p.T + (l.x + l.y);
-      if (p.out_status)
-        p.out_status[row] = late ? SV_REQ_TIMEOUT : bad ? SV_REQ_BAD_LOGITS : 0;
+      if (p.out_status) p.out_status[row] = bad ? SV_REQ_BAD_LOGITS : 0;
     }
-  }
+  };
   if (bad || m == -INFINITY) {
+    if (t < kWarp) row_outputs();
     fill_slots(p, row, 0);
     return;
   }
   const float thr = fmaxf(unit_bound<kBarSelect>(s.sel, slot.unit, p.upi, p.n), -FLT_MAX);
-  group_sync<kBarSelect>();  // (the counters are clear also when no round was needed)
+  if (p.upi < p.n) group_sync<kBarSelect>();  // (the bound's barriers were not passed)
   scan_table(s.sel, ls, table, p.iters * kRowStreamers, thr, 0);
   group_sync<kBarSelect>();
   const T* data = reinterpret_cast<const T*>(p.logits) + row * (long long)p.V;
   const int hits = s.sel.n_hits;
-  if (hits <= kMaxCands)
-    for (int q = t; q < hits * kGroups; q += kTopThreads) {
+  if (hits <= kMaxCands) {
+    // two loads in flight a thread: the usual list is one round
+    for (int q = t; q < hits * kGroups; q += 2 * kTopThreads) {
+      const int q2 = q + kTopThreads;
       const int j = ls.rank[q / kGroups] * kEntry + q % kGroups * VEC;
-      if (j < p.V)
-        list_group<T>(&s.sel.n_cands, &ls, load_group<T, kAligned>(data, j, p.V, span), thr, j);
+      const int j2 = q2 < hits * kGroups ? ls.rank[q2 / kGroups] * kEntry + q2 % kGroups * VEC : p.V;
+      uint4 g = Lane<T, VEC>::pad(), g2 = g;
+      if (j < p.V) g = load_group<T, kAligned>(data, j, p.V, span);
+      if (j2 < p.V) g2 = load_group<T, kAligned>(data, j2, p.V, span);
+      list_group<T, false>(&s.sel.n_cands, &ls, g, thr, j);
+      list_group<T, false>(&s.sel.n_cands, &ls, g2, thr, j2);
     }
+  }
+  if (t >= kTopThreads - kWarp) row_outputs();  // the warp with the least to load
   group_sync<kBarSelect>();
   int count = s.sel.n_cands;
   if (hits > kMaxCands || count > kMaxCands) {
     group_sync<kBarSelect>();
     count = select_row_slow<T, false, kBarSelect>(s.sel, ls, data, p.V, p.n, 0.0, 0, 0);
-  } else {
-    for (int i = t; i < count; i += kTopThreads)
-      set_candidate<false>(ls, i, __uint_as_float((uint32_t)ls.key[i]), 0.0, ls.idx[i]);
-    group_sync<kBarSelect>();
-    if (count > kRankAll) count = prune<kBarSelect>(s.sel, ls, count, p.n);
+  } else if (count > kRankAll) {
+    count = prune<kBarSelect>(s.sel, ls, count, p.n);
   }
   rank_list<false, kBarSelect>(ls, count);
   for (int i = t; i < count; i += kTopThreads) {
@@ -180,7 +184,7 @@ __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot,
 }
 
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kRowThreads, 1) top_rows_kernel(const TopParams p) {
+__global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   RowShared& s = *reinterpret_cast<RowShared*>(smem);
   Lists& ls = *reinterpret_cast<Lists*>(smem + sizeof(RowShared));
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) top_rows_kernel(const TopParam
   __syncthreads();
   const bool first_live = row_state(p, blockIdx.x) == kLive;
 
-  if (!streams) {  // the selecting part
+  if (!streams) {  // the selecting half
     int asked = 0;
     long long row = next_live(s, p, blockIdx.x, asked);
     if (!first_live) {
@@ -221,9 +225,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) top_rows_kernel(const TopParam
     return;
   }
 
-  // The streaming part.
+  // The streaming half.
   const int fold = kRowStreamers / p.upi;
-  Ring<T> ring(smem_u32(rings) + warp * Ring<T>::kWarpBytes, smem_u32(s.stage_bar[warp]));
   long long row = blockIdx.x;
   if (!first_live) {
     bar_sync(kBarNext, kRowThreads);
@@ -236,12 +239,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) top_rows_kernel(const TopParam
     if (k >= 2) bar_sync(kBarEmpty + b, kRowThreads);  // row k - 2 is selected
     const T* data = reinterpret_cast<const T*>(p.logits) + row * (long long)p.V;
     const RunningSum r = stream_slice<T, kAligned, kStreamWarps>(
-        ring, warp, data, 0, p.V, p.iters, p.cc, tables + b * table + t, span, p.wait_ns);
-    const float2 wr = warp_part(r, ring.late, p.cc);
+        smem_u32(rings), warp, data, 0, p.V, p.iters, p.cc, tables + b * table + t, span);
+    const float2 wr = warp_running(r, p.cc);
     float um = r.m;
     for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
     if (lane == 0) slot.part[warp] = wr;
-    if ((t & (fold - 1)) == 0) slot.unit[t / fold] = um;
+    if ((t & (fold - 1)) == 0) slot.unit[t / fold] = down_bf16(um);
     bar_arrive(kBarFull + b, kRowThreads);
     bar_sync(kBarNext + (b ^ 1), kRowThreads);
     row = s.next[b ^ 1];
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
     const double* __restrict__ off) {
   __shared__ Lists ls;
   __shared__ Select sel;
-  __shared__ float unit[kTopThreads];
+  __shared__ __align__(16) uint16_t unit[kTopThreads];
   __shared__ double s_off[SV_MAX_BEAMS];
   pdl_wait();
   const long long b = blockIdx.x;
@@ -285,7 +288,6 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
     const double o = off[b * p.W + t];
     s_off[t] = o;
     if (o != o) atomicOr(&sel.bad, SV_REQ_BAD_LOGITS);
-    if (o == INFINITY) atomicOr(&sel.bad, SV_REQ_TIMEOUT);
   }
   __syncthreads();
   const int bad = sel.bad;
@@ -305,8 +307,7 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
       const float l = values[i];
       if (l > -INFINITY) um = fmaxf(um, __fadd_rd(__double2float_rd(s_off[i / p.n]), l));
     }
-    unit[t] = um;
-    __syncthreads();
+    unit[t] = down_bf16(um);
     const float bound = unit_bound<0>(sel, unit, kTopThreads, p.n);
     for (int i = t; i < all; i += kTopThreads) {
       const float l = values[i];
@@ -376,7 +377,7 @@ cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long
   p.slice = (p.V + 255) / 256 * 256;
   p.iters = (p.V + kRowSpan - 1) / kRowSpan;
   p.upi = kRowStreamers;
-  while (p.upi > 32 && p.upi / 2 >= 4 * p.n) p.upi /= 2;
+  while (p.upi > 32 && p.upi / 2 >= 2 * p.n) p.upi /= 2;
   if (dtype == SV_BF16)
     return aligned ? launch_rows<uint16_t, true>(p, rows, stream)
                    : launch_rows<uint16_t, false>(p, rows, stream);

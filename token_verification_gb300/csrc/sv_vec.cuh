@@ -254,45 +254,51 @@ __device__ __forceinline__ float2 warp_running(const RunningSum& r, float c) {
   return make_float2(wm, warp_sum(r.s * to_frame(r.m, wm, c)));
 }
 
+// 16 bytes from global into shared memory, asynchronously, in groups.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>  // waits for all but this thread's last N groups
+__device__ __forceinline__ void copies_wait_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // A warp's copies of elements j .. end - 1 (at most a chunk) of a row into the
 // stage at `dst`: the aligned words around them, `off` the misalignment of
-// element j; completion on `bar`. The words inside the tensor go as one bulk
-// copy (16-byte asynchronous copies by every lane kept the load/store unit
-// waiting on HBM, and with it the shuffles and shared loads of the warps that
-// select); a word across the tensor's edge goes by element.
+// element j. A word that is not all inside the tensor goes by element.
 template <typename T, bool kAligned>
-__device__ __forceinline__ void load_chunk_async(uint32_t dst, uint32_t bar, const T* row, int j,
-                                                 int end, uint32_t off, const RowSpan& span) {
+__device__ __forceinline__ void load_chunk_async(uint32_t dst, const T* row, int j, int end,
+                                                 uint32_t off, const RowSpan& span) {
   const char* a = reinterpret_cast<const char*>(row + j) - off;
   const int words = ((end - j) * (int)sizeof(T) + (int)off + 15) / 16;
-  int lo = 0, hi = words;
-  if (!kAligned) {
-    lo = a < span.first ? 1 : 0;
-    hi = a + 16 * words > span.last ? words - 1 : words;
-    if (lo > 0 || hi < words) {
-      if (lane_id() < 2) {
-        const int w = lane_id() == 0 ? (lo > 0 ? 0 : -1) : (hi < words ? hi : -1);
-        if (w >= 0) {
-          const char* p = a + 16 * w;
-          uint4 v = Lane<T, Group<T>::VEC>::pad();
+  constexpr int kFull = kChunk * (int)sizeof(T) / 16;
+  if (words >= kFull && a >= span.first && a + 16 * (kFull + 1) <= span.last) {
 #pragma unroll
-          for (int e = 0; e < Group<T>::VEC; ++e) {
-            const char* x = p + e * (int)sizeof(T);
-            if (x >= span.first && x < span.last) put(v, e, *reinterpret_cast<const T*>(x));
-          }
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 16 * w), "r"(v.x),
-                       "r"(v.y), "r"(v.z), "r"(v.w)
-                       : "memory");
-        }
-      }
-      hi = max(hi, lo);
+    for (int q = 0; q < kFull / kWarp; ++q) {
+      const int w = q * kWarp + lane_id();
+      copy16_async(dst + 16 * w, a + 16 * w);
     }
+    if (!kAligned && words > kFull && lane_id() == 0) copy16_async(dst + 16 * kFull, a + 16 * kFull);
+    return;
   }
-  if (lane_id() == 0) {
-    const uint32_t bytes = 16u * (uint32_t)(hi - lo);
-    fence_proxy_async();
-    mbar_arrive_expect_tx(bar, bytes);
-    if (bytes) bulk_copy(dst + 16 * lo, a + 16 * lo, bytes, bar);
+  for (int w = lane_id(); w < words; w += kWarp) {
+    const char* p = a + 16 * w;
+    if (p >= span.first && p + 16 <= span.last) {
+      copy16_async(dst + 16 * w, p);
+    } else {
+      uint4 v = Lane<T, Group<T>::VEC>::pad();
+#pragma unroll
+      for (int e = 0; e < Group<T>::VEC; ++e) {
+        const char* x = p + e * (int)sizeof(T);
+        if (x >= span.first && x < span.last) put(v, e, *reinterpret_cast<const T*>(x));
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 16 * w), "r"(v.x),
+                   "r"(v.y), "r"(v.z), "r"(v.w)
+                   : "memory");
+    }
   }
 }
 
