@@ -286,6 +286,8 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
       if (p.out_status) p.out_status[row] = status;
     }
   };
+  pdl_wait();
+  pdl_launch_dependents();
   if (p.lens) {
     const int b = (int)(row / p.P), i = (int)(row - (long long)b * p.P);
     const int len = p.lens[b];
@@ -507,20 +509,9 @@ cudaError_t launch_distill(const DistillParams& p, long long rows, int C, cudaSt
                                 (int)sizeof(DistillShared) + kMaxSliceBytes);
   });
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * C));
-  cfg.blockDim = dim3(kDistillThreads);
   // a word past the slice: the last shifted store reads it
-  cfg.dynamicSmemBytes = sizeof(DistillShared) + 16 * ((size_t)p.slice + 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, p);
+  const size_t smem = sizeof(DistillShared) + 16 * ((size_t)p.slice + 1);
+  return launch_early(fn, (unsigned)(rows * C), kDistillThreads, smem, C, stream, p);
 }
 
 template <int kMode>

@@ -15,6 +15,7 @@
 #include "../../include/spec_verify.h"
 #include "sv_launch.h"
 #include "sv_rows.cuh"
+#include "sv_vec.cuh"
 
 namespace sv {
 namespace {
@@ -39,6 +40,8 @@ struct ReorderParams {
 
 template <typename U>
 __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
   const int t = threadIdx.x;
   if (p.out_status) {
     const long long b = (long long)blockIdx.x * kReorderThreads + t;
@@ -111,8 +114,7 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderP
 
 template <typename U>
 cudaError_t launch_reorder(const ReorderParams& p, unsigned blocks, cudaStream_t stream) {
-  reorder_kernel<U><<<blocks, kReorderThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(reorder_kernel<U>, blocks, kReorderThreads, 0, 1, stream, p);
 }
 
 }  // namespace

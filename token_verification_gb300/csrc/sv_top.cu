@@ -62,6 +62,8 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   const int items = p.W * p.slices;
   const RowSpan span = {p.first, p.last};
 
+  pdl_wait();
+  pdl_launch_dependents();
   if (!kBeam && p.lens) {  // a record's row that is not needed (the whole cluster leaves)
     const int b = (int)(grp / p.P), i = (int)(grp - (long long)b * p.P);
     const int len = p.lens[b];
@@ -258,19 +260,7 @@ cudaError_t launch_top(const TopParams& p, long long groups, int C, cudaStream_t
   });
   if (err != cudaSuccess) return err;
   const size_t smem = sizeof(TopShared) + p.table_bytes + union_bytes<T>();
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * C));
-  cfg.blockDim = dim3(kTopThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, p);
+  return launch_early(fn, (unsigned)(groups * C), kTopThreads, smem, C, stream, p);
 }
 
 // The logits' memory, and whether all rows start on a 16-byte boundary.

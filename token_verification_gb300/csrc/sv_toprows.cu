@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParam
     mbar_init(smem_u32(&s.bar), 1);
     fence_mbar_init();
   }
+  pdl_wait();
   __syncthreads();
   const bool first_live = row_state(p, blockIdx.x) == kLive;
 
@@ -249,6 +250,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParam
     bar_sync(kBarNext + (b ^ 1), kRowThreads);
     row = s.next[b ^ 1];
   }
+  // (sooner, the kernel after this one would take the place of CTAs yet to start)
+  pdl_launch_dependents();
   // every arrival is waited for before the CTA ends
   if (k >= 2) bar_sync(kBarEmpty + (k & 1), kRowThreads);
   if (k >= 1) bar_sync(kBarEmpty + ((k - 1) & 1), kRowThreads);
@@ -263,8 +266,8 @@ cudaError_t launch_rows(TopParams p, long long rows, cudaStream_t stream) {
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
   });
   if (err != cudaSuccess) return err;
-  fn<<<dim3((unsigned)rows), kRowThreads, fixed + 4 * (size_t)p.iters * kRowStreamers, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(fn, (unsigned)rows, kRowThreads,
+                      fixed + 4 * (size_t)p.iters * kRowStreamers, 1, stream, p);
 }
 
 // The n best of a request's W selections: every thread takes the candidates
@@ -278,6 +281,7 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
   __shared__ __align__(16) uint16_t unit[kTopThreads];
   __shared__ double s_off[SV_MAX_BEAMS];
   pdl_wait();
+  pdl_launch_dependents();
   const long long b = blockIdx.x;
   const int t = threadIdx.x, all = p.W * p.n;
   ids += b * all;
@@ -387,10 +391,8 @@ cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long
 
 cudaError_t launch_beam_merge(const TopParams& p, const int* ids, const float* values,
                               const double* off, int B, cudaStream_t stream) {
-  TopParams q = p;
-  void* args[] = {&q, &ids, &values, &off};
-  return launch_pdl(reinterpret_cast<const void*>(beam_merge_kernel), dim3((unsigned)B),
-                    dim3(kTopThreads), stream, args);
+  return launch_early(beam_merge_kernel, (unsigned)B, kTopThreads, 0, 1, stream, p, ids, values,
+                      off);
 }
 
 }  // namespace sv

@@ -315,6 +315,29 @@ __device__ __forceinline__ void clip_group(uint4& g, int j, int end) {
   }
 }
 
+// Launch with programmatic dependent launch, in clusters of C CTAs when C > 1:
+// the launch itself overlaps the kernel before on the stream, and the kernel
+// waits for that one's results first thing (pdl_wait).
+template <class... P, class... A>
+cudaError_t launch_early(void (*fn)(P...), unsigned grid, unsigned block, size_t smem, int C,
+                         cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 // The two halves of a cluster barrier (release / acquire).
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
