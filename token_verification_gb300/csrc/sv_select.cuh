@@ -49,7 +49,7 @@ struct TopParams {
 };
 
 // Whether rows of V logits fit the row kernel's shared memory.
-bool top_rows_fit(sv_dtype dtype, int V);
+bool top_rows_fit(int V);
 // Rows one CTA each, as many CTAs as fit taking row after row (sv_toprows.cu).
 cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long rows,
                             cudaStream_t stream);
@@ -61,7 +61,25 @@ namespace {
 
 constexpr int kTopThreads = 256;
 constexpr int kTopWarps = kTopThreads / kWarp;
-constexpr int kEntry = 32;            // consecutive elements of a table entry: one lane's of a chunk
+constexpr int kEntry = 32;            // elements of a table entry
+// They are one piece of 32 consecutive elements (bf16) or two of 16 (fp32): a
+// lane's 64 bytes of a 2 KB chunk, one chunk or two an entry.
+template <typename T>
+struct Piece {
+  static constexpr int kPieces = (int)sizeof(T) / 2;
+  static constexpr int kSize = kEntry / kPieces;
+  static constexpr int kChunkSize = kSize * kWarp;  // elements of a chunk
+  static constexpr int kWords = 4;                  // 16-byte words of a piece
+};
+// The element (of the slice) at which word q of an entry's kPieces * 4 starts;
+// `threads` the streaming threads.
+template <typename T>
+__device__ __forceinline__ int entry_element(int entry, int q, int threads) {
+  using P = Piece<T>;
+  const int i = entry / threads, t = entry - i * threads;
+  return ((i * P::kPieces + q / P::kWords) * threads + t) * P::kSize +
+         q % P::kWords * Group<T>::VEC;
+}
 constexpr int kMaxUnits = 512;        // units per cluster
 constexpr int kMaxCands = 1024;       // candidates of a cluster, 32-element groups of a CTA
 constexpr int kRankAll = 384;         // lists longer than this are cut to the bound first
@@ -91,15 +109,14 @@ struct alignas(16) Lists {
   int rank[kMaxCands];                // until the list is sorted: the groups to read again
 };
 
-// Load stages: each warp streams 1024-element chunks through its own ring by
-// 16-byte asynchronous copies (a word more than a chunk, for rows off 16-byte
+// Load stages: each warp streams 2 KB chunks through its own ring by 16-byte
+// asynchronous copies (a word more than a chunk, for rows off 16-byte
 // boundaries); no barrier but the warp's own. 2 KB bulk copies into the same
 // ring reached 5.2 TB/s where these reach 6.5 (912 and 2432 rows of 152064
 // bf16 logits, the slope).
-template <typename T>
 struct Ring {
-  static constexpr int kBytes = kChunk * (int)sizeof(T) + 16;
-  static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
+  static constexpr int kBytes = 2048 + 16;
+  static constexpr int kStages = 3;
   static constexpr int kWarpBytes = kBytes * kStages;
 };
 
@@ -289,20 +306,25 @@ __device__ int prune(Select& s, Lists& ls, int count, int n) {
     k[q] = i < count ? ls.key[i] : 0ull;
     ix[q] = i < count ? ls.idx[i] : 0;
   }
+  // three counters in turn: one barrier a round
+  if (tid < 3) s.pick[tid] = 0;
+  group_sync<kBar>();
   uint32_t t = 0;
+  int now = 0;
   for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
     const uint32_t at = t | bit;
-    int c = 0;
+    unsigned c = 0;
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) c += (uint32_t)(k[q] >> 32) >= at ? 1 : 0;
-    c = (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
-    if (tid == 0) s.pick[0] = 0;
+    for (int q = 0; q < kPer; ++q) c += (uint32_t)(k[q] >> 32) >= at ? 1u : 0u;
+    c = __reduce_add_sync(0xffffffffu, c);
+    const int next = now == 2 ? 0 : now + 1;
+    if (lane_id() == 0) atomicAdd(&s.pick[now], (int)c);
+    if (tid == 0) s.pick[next == 2 ? 0 : next + 1] = 0;
     group_sync<kBar>();
-    if (lane_id() == 0) atomicAdd(&s.pick[0], c);
-    group_sync<kBar>();
-    if (s.pick[0] >= n) t = at;
-    group_sync<kBar>();
+    if (s.pick[now] >= n) t = at;
+    now = next;
   }
+  group_sync<kBar>();
   if (tid == 0) s.pick[1] = 0;
   group_sync<kBar>();
 #pragma unroll
@@ -317,68 +339,71 @@ __device__ int prune(Select& s, Lists& ls, int count, int n) {
 }
 
 // One pass of kWarps warps over elements e0 .. e1 - 1 of a row: the thread's
-// running sum, and at table[i * kWarps * 32] the max of its 32 elements of
-// iteration i (elements (i * kWarps * 32 + t) * 32 on of the slice, t the
-// thread: warp w has chunk i * kWarps + w).
+// running sum, and at table[i * kWarps * 32] the max of its entry of iteration
+// i (chunk c of the slice is warp c % kWarps').
 template <typename T, bool kAligned, int kWarps>
 __device__ __forceinline__ RunningSum stream_slice(uint32_t ring, int warp, const T* row, int e0,
                                                    int e1, int iters, float c, uint16_t* table,
                                                    const RowSpan& span) {
   constexpr int VEC = Group<T>::VEC;
-  constexpr int kGroups = kEntry / VEC;  // 16-byte groups of a lane: 4 or 8
-  constexpr int kAtOnce = 4;
-  using R = Ring<T>;
+  using P = Piece<T>;
   const int lane = lane_id();
   const T* tag = nullptr;
-  const int chunks = (e1 - e0 + kChunk - 1) / kChunk;
+  const int chunks = (e1 - e0 + P::kChunkSize - 1) / P::kChunkSize;
   const int todo = (chunks - warp + kWarps - 1) / kWarps;  // this warp's (may be <= 0)
   const uint32_t off = kAligned ? 0u : (uint32_t)(uintptr_t)row & 15u;
-  ring += warp * R::kWarpBytes;
-  auto issue = [&](int i) {  // iteration i's chunk into its stage
+  ring += warp * Ring::kWarpBytes;
+  auto issue = [&](int i) {  // this warp's chunk i into its stage
     if (i < todo) {
-      const int j = e0 + (i * kWarps + warp) * kChunk;
-      load_chunk_async<T, kAligned>(ring + i % R::kStages * R::kBytes, row, j,
-                                    min(j + kChunk, e1), off, span);
+      const int j = e0 + (i * kWarps + warp) * P::kChunkSize;
+      load_chunk_async<T, kAligned>(ring + i % Ring::kStages * Ring::kBytes, row, j,
+                                    min(j + P::kChunkSize, e1), off, span);
     }
     copies_commit();
   };
   RunningSum r;
+  // the chunks, kShift words from where the row's misalignment puts them
+  auto pass = [&](auto kShift) {
+    float entry = -INFINITY;
+    for (int i = 0; i < iters * P::kPieces; ++i) {
+      float gm = -INFINITY;
+      if (i < todo) {
+        copies_wait_but<Ring::kStages - 2>();
+        __syncwarp();  // every lane's copies of this stage landed; the stage before is read
+        issue(i + Ring::kStages - 1);
+        const uint32_t stage = ring + i % Ring::kStages * Ring::kBytes + lane * 64;
+        const int j = e0 + (i * kWarps + warp) * P::kChunkSize + lane * P::kSize;
+        uint4 g[P::kWords];
 #pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) issue(i);
-  for (int i = 0; i < iters; ++i) {
-    if (i >= todo) {
-      table[i * kWarps * kWarp] = 0xff80u;
-      continue;
-    }
-    copies_wait_but<R::kStages - 2>();
-    __syncwarp();  // every lane's copies of this stage landed; the stage before is read
-    issue(i + R::kStages - 1);
-    const uint32_t stage = ring + i % R::kStages * R::kBytes;
-    const int j = e0 + (i * kWarps + warp) * kChunk;
-    float gm = -INFINITY;
+        for (int u = 0; u < P::kWords; ++u) {
+          // the lane's words in an order that keeps a quarter warp off each other's banks
+          const uint32_t at = stage + ((u + (lane >> 1)) & (P::kWords - 1)) * 16;
+          g[u] = lds128(at);
+          if (!kAligned && off) g[u] = shift_words<kShift.value>(g[u], lds128(at + 16), off * 8);
+        }
+        if (e0 + (i * kWarps + warp + 1) * P::kChunkSize > e1) {
 #pragma unroll
-    for (int h = 0; h < kGroups; h += kAtOnce) {
-      uint4 g[kAtOnce];
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        // the lane's groups in an order that keeps a quarter warp off each other's banks
-        const int q = (h + u + (VEC == 8 ? lane >> 1 : lane)) & (kGroups - 1);
-        const uint32_t at = stage + (lane * kGroups + q) * 16;
-        g[u] = lds128(at);
-        if (!kAligned && off) g[u] = shift_pair(g[u], lds128(at + 16), off);
+          for (int u = 0; u < P::kWords; ++u)
+            clip_group<T>(g[u], j + ((u + (lane >> 1)) & (P::kWords - 1)) * VEC, e1);
+        }
+        gm = r.add(g, c, tag);
       }
-      if (j + kChunk > e1) {
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u)
-          clip_group<T>(g[u],
-                        j + lane * kEntry +
-                            ((h + u + (VEC == 8 ? lane >> 1 : lane)) & (kGroups - 1)) * VEC,
-                        e1);
+      if (P::kPieces == 1) {
+        table[i * kWarps * kWarp] = up_bf16(gm);
+      } else if ((i & 1) == 0) {
+        entry = gm;
+      } else {
+        table[(i >> 1) * kWarps * kWarp] = up_bf16(max_nan(entry, gm));
       }
-      gm = max_nan(gm, r.add(g, c, tag));
     }
-    table[i * kWarps * kWarp] = up_bf16(gm);
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < Ring::kStages - 1; ++i) issue(i);
+  // one copy of the loop a shift: the words then need no selection in registers
+  if (kAligned || off < 4) pass(Shift<0>());
+  else if (off < 8) pass(Shift<1>());
+  else if (off < 12) pass(Shift<2>());
+  else pass(Shift<3>());
   __syncwarp();  // (the next slice refills the stages)
   return r;
 }
@@ -439,10 +464,7 @@ __device__ __forceinline__ double row_offset(float score, float m, float2 log_su
   return ((double)score - (double)m) - ((double)log_sum.x + (double)log_sum.y);
 }
 
-template <typename T>
-constexpr int ring_bytes(int warps) {
-  return Ring<T>::kWarpBytes * warps;
-}
+constexpr int ring_bytes(int warps) { return Ring::kWarpBytes * warps; }
 
 }  // namespace
 }  // namespace sv

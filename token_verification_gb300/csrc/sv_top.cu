@@ -48,7 +48,7 @@ __device__ __forceinline__ void write_slot(const TopParams& p, long long grp, in
 template <typename T, bool kAligned, bool kBeam>
 __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) {
   constexpr int VEC = Group<T>::VEC;
-  constexpr int kGroups = kEntry / VEC;  // 16-byte groups of a table entry
+  constexpr int kWords = kEntry / VEC;  // 16-byte words of a table entry
   extern __shared__ __align__(16) unsigned char smem[];
   TopShared& s = *reinterpret_cast<TopShared*>(smem);
   // per iteration over this CTA's items, the thread's 32 elements' max
@@ -186,13 +186,12 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   if (hits > kMaxCands) {
     if (t == 0) lead->sel.overflow = 1;
   } else {
-    for (int q = t; q < hits * kGroups; q += kTopThreads) {
-      const int at = ls.rank[q / kGroups], u = q % kGroups;
-      const int mi = at / kTopThreads, ti = at % kTopThreads;
-      const int mine = mi / p.iters, i = mi - mine * p.iters;
-      const int it = rank + mine * C;
+    for (int q = t; q < hits * kWords; q += kTopThreads) {
+      const int at = ls.rank[q / kWords];
+      const int mine = at / (p.iters * kTopThreads), it = rank + mine * C;
       const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
-      const int j = e0 + (i * kTopThreads + ti) * kEntry + u * VEC;
+      const int j =
+          e0 + entry_element<T>(at - mine * p.iters * kTopThreads, q % kWords, kTopThreads);
       if (j >= min(e0 + p.slice, p.V)) continue;
       const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
       list_group<T, kBeam>(&lead->sel.n_cands, lead_ls, load_group<T, kAligned>(row, j, p.V, span),
@@ -243,11 +242,8 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
 }
 
 // The candidates lie in the memory of the load stages, which are consumed by then.
-template <typename T>
-constexpr int union_bytes() {
-  return ring_bytes<T>(kTopWarps) > (int)sizeof(Lists) ? ring_bytes<T>(kTopWarps)
-                                                      : (int)sizeof(Lists);
-}
+constexpr int kUnionBytes = ring_bytes(kTopWarps) > (int)sizeof(Lists) ? ring_bytes(kTopWarps)
+                                                                      : (int)sizeof(Lists);
 
 template <typename T, bool kAligned, bool kBeam>
 cudaError_t launch_top(const TopParams& p, long long groups, int C, cudaStream_t stream) {
@@ -256,10 +252,10 @@ cudaError_t launch_top(const TopParams& p, long long groups, int C, cudaStream_t
   const cudaError_t err = per_device(once, nullptr, [&](int&) {
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)sizeof(TopShared) + kMaxTables * kTopThreads * 2 +
-                                    union_bytes<T>());
+                                    kUnionBytes);
   });
   if (err != cudaSuccess) return err;
-  const size_t smem = sizeof(TopShared) + p.table_bytes + union_bytes<T>();
+  const size_t smem = sizeof(TopShared) + p.table_bytes + kUnionBytes;
   return launch_early(fn, (unsigned)(groups * C), kTopThreads, smem, C, stream, p);
 }
 
@@ -272,8 +268,8 @@ bool set_span(TopParams& p, sv_dtype dtype, long long rows) {
 }
 
 // Rows enough for the row kernel, whose CTAs take one at a time.
-bool by_rows(sv_dtype dtype, long long rows, int V) {
-  return rows >= kManyRows && V >= kTopSpan && top_rows_fit(dtype, V);
+bool by_rows(long long rows, int V) {
+  return rows >= kManyRows && V >= kTopSpan && top_rows_fit(V);
 }
 
 template <bool kBeam>
@@ -347,7 +343,7 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
   p.cc = exponent_scale(temperature);
   p.T = temperature;
   const long long rows = (long long)B * P;
-  if (by_rows(dtype, rows, V)) {
+  if (by_rows(rows, V)) {
     const bool aligned = set_span(p, dtype, rows);
     return launch_top_rows(dtype, aligned, p, rows, (cudaStream_t)stream) == cudaSuccess
                ? SV_OK
@@ -362,7 +358,7 @@ size_t spec_beam_workspace_size(sv_dtype dtype, int B, int W, int V, int n) {
     return 0;
   const size_t rows = (size_t)B * W;
   // each row's offset, then its n best logits and their tokens
-  return by_rows(dtype, (long long)rows, V) ? rows * (sizeof(double) + 8 * (size_t)n) : 0;
+  return by_rows((long long)rows, V) ? rows * (sizeof(double) + 8 * (size_t)n) : 0;
 }
 
 sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out_tokens,

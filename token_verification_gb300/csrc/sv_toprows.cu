@@ -117,7 +117,7 @@ template <typename T, bool kAligned>
 __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot, long long row,
                            const uint16_t* table, const TopParams& p, const RowSpan& span) {
   constexpr int VEC = Group<T>::VEC;
-  constexpr int kGroups = kEntry / VEC;
+  constexpr int kWords = kEntry / VEC;
   const int t = threadIdx.x % kTopThreads;
   if (t == 0) s.sel.n_hits = s.sel.n_cands = 0;
   // every warp for itself: the max decides whether there is anything to select
@@ -151,10 +151,12 @@ __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot,
   const int hits = s.sel.n_hits;
   if (hits <= kMaxCands) {
     // two loads in flight a thread: the usual list is one round
-    for (int q = t; q < hits * kGroups; q += 2 * kTopThreads) {
+    for (int q = t; q < hits * kWords; q += 2 * kTopThreads) {
       const int q2 = q + kTopThreads;
-      const int j = ls.rank[q / kGroups] * kEntry + q % kGroups * VEC;
-      const int j2 = q2 < hits * kGroups ? ls.rank[q2 / kGroups] * kEntry + q2 % kGroups * VEC : p.V;
+      const int j = entry_element<T>(ls.rank[q / kWords], q % kWords, kRowStreamers);
+      const int j2 = q2 < hits * kWords
+                         ? entry_element<T>(ls.rank[q2 / kWords], q2 % kWords, kRowStreamers)
+                         : p.V;
       uint4 g = Lane<T, VEC>::pad(), g2 = g;
       if (j < p.V) g = load_group<T, kAligned>(data, j, p.V, span);
       if (j2 < p.V) g2 = load_group<T, kAligned>(data, j2, p.V, span);
@@ -261,7 +263,7 @@ template <typename T, bool kAligned>
 cudaError_t launch_rows(TopParams p, long long rows, cudaStream_t stream) {
   static PerDevice once;
   auto* fn = top_rows_kernel<T, kAligned>;
-  const size_t fixed = sizeof(RowShared) + sizeof(Lists) + ring_bytes<T>(kStreamWarps);
+  const size_t fixed = sizeof(RowShared) + sizeof(Lists) + ring_bytes(kStreamWarps);
   const cudaError_t err = per_device(once, nullptr, [&](int&) {
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
   });
@@ -305,9 +307,12 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
   };
   int count = 0;
   if (!bad) {
-    // bounds of the scores, rounded down; an empty slot's logit is -inf
+    // bounds of the scores, rounded down; an empty slot's logit is -inf. Each
+    // row's values are in descending order: a thread's are spread over the
+    // positions (7919 is a prime beyond any factor of W n).
     float um = -INFINITY;
-    for (int i = t; i < all; i += kTopThreads) {
+    for (int q = t; q < all; q += kTopThreads) {
+      const int i = (int)((unsigned)q * 7919u % (unsigned)all);
       const float l = values[i];
       if (l > -INFINITY) um = fmaxf(um, __fadd_rd(__double2float_rd(s_off[i / p.n]), l));
     }
@@ -368,11 +373,10 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
 
 }  // namespace
 
-bool top_rows_fit(sv_dtype dtype, int V) {
+bool top_rows_fit(int V) {
   const size_t tables = 4 * (size_t)((V + kRowSpan - 1) / kRowSpan) * kRowStreamers;
-  const size_t ring = dtype == SV_BF16 ? ring_bytes<uint16_t>(kStreamWarps)
-                                       : ring_bytes<float>(kStreamWarps);
-  return sizeof(RowShared) + sizeof(Lists) + ring + tables <= (size_t)kRowsSmem;
+  return sizeof(RowShared) + sizeof(Lists) + ring_bytes(kStreamWarps) + tables <=
+         (size_t)kRowsSmem;
 }
 
 cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long rows,

@@ -38,6 +38,22 @@ __device__ __forceinline__ uint4 shift_pair(const uint4& a, const uint4& b, uint
   return make_uint4(w0, w1, w2, w3);
 }
 
+// The same with the shift in words known at compile time (4 * kWords + 0 or 2
+// bytes; `bits` is the whole shift times 8).
+template <int kWords>
+struct Shift {
+  static constexpr int value = kWords;
+};
+template <int kWords>
+__device__ __forceinline__ uint4 shift_words(const uint4& a, const uint4& b, uint32_t bits) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const uint32_t half = bits & 16u;  // (a funnel shift by 0 is its first word)
+  return make_uint4(__funnelshift_r(w[kWords], w[kWords + 1], half),
+                    __funnelshift_r(w[kWords + 1], w[kWords + 2], half),
+                    __funnelshift_r(w[kWords + 2], w[kWords + 3], half),
+                    __funnelshift_r(w[kWords + 3], w[kWords + 4], half));
+}
+
 // A tensor of logit rows: [first, last) is its memory, read nowhere else.
 struct RowSpan {
   const char* first;
@@ -266,7 +282,7 @@ __device__ __forceinline__ void copies_wait_but() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's copies of elements j .. end - 1 (at most a chunk) of a row into the
+// A warp's copies of elements j .. end - 1 (at most 2 KB) of a row into the
 // stage at `dst`: the aligned words around them, `off` the misalignment of
 // element j. A word that is not all inside the tensor goes by element.
 template <typename T, bool kAligned>
@@ -274,7 +290,7 @@ __device__ __forceinline__ void load_chunk_async(uint32_t dst, const T* row, int
                                                  uint32_t off, const RowSpan& span) {
   const char* a = reinterpret_cast<const char*>(row + j) - off;
   const int words = ((end - j) * (int)sizeof(T) + (int)off + 15) / 16;
-  constexpr int kFull = kChunk * (int)sizeof(T) / 16;
+  constexpr int kFull = 2048 / 16;
   if (words >= kFull && a >= span.first && a + 16 * (kFull + 1) <= span.last) {
 #pragma unroll
     for (int q = 0; q < kFull / kWarp; ++q) {
