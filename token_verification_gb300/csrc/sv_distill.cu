@@ -50,9 +50,8 @@ struct DistillParams {
 };
 
 struct alignas(16) DistillShared {
-  float4 part[kMaxCluster];      // each CTA's {max, sum, -, -} over its slice without the record
+  float4 part[kMaxCluster];      // each CTA's {max, sum, late, -} over its slice without the record
   float2 warp_part[kDistillWarps];
-  float4 stat;                   // {m, beta, M, 1/Z}
   unsigned long long bar;        // the slice's arrival
   int id[SV_MAX_TOP];            // the record (-1: unused)
   float t[SV_MAX_TOP];           // its logits (-inf: unused)
@@ -60,10 +59,25 @@ struct alignas(16) DistillShared {
   float sv[SV_MAX_TOP];          // the student's logits at its tokens
   int bad, used, late;
   float norm, norm_lo;           // the teacher's log-sum-exp: log p_j = t_j / T - norm
-  float p_rest;
-  float m, M;                    // the student's max outside the record, and over all
-  float2 S, Z;                   // its sums there, in the frames of m and M (hi, lo)
+  float p_sum, p_rest;           // the record's mass and 1 - it
+  float top_m;                   // the student's max on the record (NaN: unusable)
+  float2 top_z;                  // and its sum there in that frame (hi, lo)
 };
+
+__device__ __forceinline__ uint16_t to_bf16(float v) {  // round to nearest even
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = to_bf16(v); }
+__device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
 
 // Writes the 32-bit pattern v (equal halves) over `bytes` bytes at `dst` (2-byte
 // aligned).
@@ -98,21 +112,6 @@ __device__ void store_slice(char* dst, const unsigned char* src, int bytes) {
     *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
 }
 
-__device__ __forceinline__ uint16_t to_bf16(float v) {  // round to nearest even
-  uint16_t r;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ float widen(float v) { return v; }
-__device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = to_bf16(v); }
-__device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
-
 // 2^((l - m) c) * scale of each element of a group.
 __device__ __forceinline__ uint4 scaled_group(const uint4& g, float c, float m, float scale,
                                               const uint16_t*) {
@@ -139,20 +138,25 @@ __device__ __forceinline__ void add_ratio(Pair& a, float x, const DistillParams&
   a.add(sign * (fmaf(-q, p.T, x) * p.inv_t));
 }
 
-// The teacher's side of a row: its record and probabilities.  Sets s.bad for
+// The k-sized part of a row: its record, the teacher's probabilities, and (kStats)
+// the student's logits at the recorded tokens with their max and sum, read
+// straight from the row so that all of it overlaps the slice's copy.  Sets s.bad for
 // a token out of range or given twice, for a NaN or +inf logit, and for a
-// log-sum-exp that is not finite beside a used entry.  A whole-CTA call; the
-// last part is the first warp's.
-__device__ void load_record(DistillShared& s, const DistillParams& p, long long row) {
+// log-sum-exp that is not finite beside a used entry.  A whole-CTA call.
+template <typename T, bool kStats>
+__device__ void load_record(DistillShared& s, const DistillParams& p, long long row,
+                            const T* src) {
   const int t = threadIdx.x;
   const float lse = p.top_lse ? p.top_lse[row] : 0.f;
   if (t < p.k) {
     const int id = p.top_ids[row * p.k + t];
     const float v = p.top_logits[row * p.k + t];
+    const bool in = id >= 0 && id < p.V;
+    if (kStats) s.sv[t] = in ? widen(src[id]) : -INFINITY;
     s.id[t] = id;
     s.t[t] = id < 0 ? -INFINITY : v;
     int bad = 0;
-    if (id < -1 || id >= p.V) bad |= SV_REQ_BAD_TOKEN;
+    if (id >= 0 ? !in : id != -1) bad |= SV_REQ_BAD_TOKEN;
     if (id >= 0) {
       if (v != v || v == INFINITY) bad |= SV_REQ_BAD_LOGITS;
       if (p.top_lse && !is_finite(lse)) bad |= SV_REQ_BAD_LOGITS;
@@ -161,14 +165,33 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     if (bad) atomicOr(&s.bad, bad);
   }
   __syncthreads();
-  // pairs of entries: the CTA's upper half compares with the entries before,
-  // the lower half's first warp goes on to the probabilities
+  // the CTA's upper half looks for an entry's token among those before, its
+  // first warp goes on to the probabilities, its second to the student's sum
   if (t >= kDistillThreads / 2 && t - kDistillThreads / 2 < p.k) {
     const int i = t - kDistillThreads / 2, id = s.id[i];
     bool twice = false;
     if (id >= 0)
       for (int j = 0; j < i; ++j) twice = twice || s.id[j] == id;
     if (twice) atomicOr(&s.bad, SV_REQ_BAD_TOKEN);
+  }
+  if (kStats && t >= kWarp && t < 2 * kWarp) {
+    constexpr int kPer = SV_MAX_TOP / kWarp;
+    float x[kPer], m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int j = q * kWarp + lane_id();
+      x[q] = j < p.k ? s.sv[j] : -INFINITY;
+      m = max_nan(m, x[q]);
+    }
+    m = warp_max_nan(m);
+    float z = 0.f;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) z += ex2((x[q] - frame_of(m)) * p.cc);
+    const float2 sum = warp_sum_pair(z);
+    if (lane_id() == 0) {
+      s.top_m = m == INFINITY ? qnan() : m;
+      s.top_z = sum;
+    }
   }
   if (t < kWarp) {
     constexpr int kPer = SV_MAX_TOP / kWarp;
@@ -209,9 +232,42 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     if (t == 0) {
       s.norm = norm.hi;
       s.norm_lo = norm.lo;
+      s.p_sum = total.x + total.y;
       s.p_rest = p.top_lse && used < p.V ? fmaxf(0.f, (1.f - total.x) - total.y) : 0.f;
     }
   }
+}
+
+// The student's sums: over the tokens outside the record (max m, S in its
+// frame) and over all (M, Z).
+struct Sums {
+  float m, M;
+  float2 S, Z;
+  float beta, inv_z, q_top;  // q_top: the student's mass on the record
+  bool wrong;
+};
+
+// From the record's and the cluster's parts; a call of one warp (all the same).
+__device__ Sums row_sums(const DistillShared& s, int C, float c) {
+  const int lane = lane_id();
+  const float4 v = lane < C ? s.part[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  Sums r;
+  r.m = warp_max_nan(v.x);
+  r.S = warp_sum_pair<kMaxCluster>(v.y * to_frame(v.x, r.m, c));
+  r.M = max_nan(r.m, s.top_m);
+  r.wrong = !is_finite(r.M);
+  const float up = to_frame(s.top_m, r.M, c), down = to_frame(r.m, r.M, c);
+  const float rest = r.S.x * down, top = s.top_z.x * up;
+  Pair Z;
+  Z.add(top);
+  Z.add(rest);
+  Z.add(fmaf(s.top_z.x, up, -top) + s.top_z.y * up);
+  Z.add(fmaf(r.S.x, down, -rest) + r.S.y * down);
+  r.Z = make_float2(Z.hi, Z.lo);
+  r.inv_z = r.wrong ? qnan() : 1.f / Z.value();
+  r.q_top = top * r.inv_z;
+  r.beta = r.m == -INFINITY ? 0.f : (rest * r.inv_z - s.p_rest) / r.S.x;
+  return r;
 }
 
 // The loss of a row, by one warp:
@@ -219,17 +275,18 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
 // with K = norm - (M / T + log Z).  The differences are taken before anything
 // is rounded to their terms' size: where student and teacher agree the loss
 // is far below its terms.
-__device__ float row_loss(const DistillShared& s, const DistillParams& p) {
+__device__ float row_loss(const DistillShared& s, const DistillParams& p, const Sums& r) {
   const int lane = lane_id();
+  const bool rest = r.m != -INFINITY;
   // lane 0: log Z, lane 1: log S
-  const float2 mine = log_pair(lane == 1 ? s.S : s.Z);
+  const float2 mine = log_pair(lane == 1 && rest ? r.S : r.Z);
   const float2 lz = make_float2(__shfl_sync(0xffffffffu, mine.x, 0),
                                 __shfl_sync(0xffffffffu, mine.y, 0));
   const float2 ls = make_float2(__shfl_sync(0xffffffffu, mine.x, 1),
                                 __shfl_sync(0xffffffffu, mine.y, 1));
   Pair K;
   K.add(s.norm);
-  add_ratio(K, s.M, p, -1.f);
+  add_ratio(K, r.M, p, -1.f);
   K.add(-lz.x);
   K.add(-lz.y);
   K.add(s.norm_lo);
@@ -239,13 +296,19 @@ __device__ float row_loss(const DistillShared& s, const DistillParams& p) {
     if (s.p[j] > 0.f) loss = fmaf(s.p[j], (s.t[j] - s.sv[j]) * p.inv_t - k, loss);
   loss = warp_sum(loss);
   if (s.p_rest > 0.f) {
-    if (s.m == -INFINITY) return INFINITY;
-    Pair d;  // log q_rest = log S + (m - M) / T - log Z, whatever underflowed
-    add_ratio(d, s.m - s.M, p, -1.f);
-    d.add(lz.x - ls.x);
-    d.add(lz.y);
-    d.add(-ls.y);
-    d.add(logf(s.p_rest));
+    if (!rest) return INFINITY;
+    // a remainder that is most of the mass: its logarithm from what is left of it
+    const float lp = s.p_sum < 0.5f ? log1pf(-s.p_sum) : logf(s.p_rest);
+    Pair d;  // else log q_rest = log S + (m - M) / T - log Z, whatever underflowed
+    d.add(lp);
+    if (r.q_top < 0.5f) {
+      d.add(-log1pf(-r.q_top));
+    } else {
+      add_ratio(d, r.m - r.M, p, -1.f);
+      d.add(lz.x - ls.x);
+      d.add(lz.y);
+      d.add(-ls.y);
+    }
     loss += s.p_rest * d.value();
   }
   return loss;
@@ -297,13 +360,13 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
       return;
     }
   }
+  float4 st = make_float4(0.f, 0.f, 0.f, 0.f);  // {m, beta, M, 1/Z}
   if (kMode == kGradOnly) {
-    const float4 st = p.stats[row];
+    st = p.stats[row];
     if (st.w != st.w) {
       leave(0.f, 0);
       return;
     }
-    if (t == 0) s.stat = st;
   }
 
   // The slice on its way into shared memory: the words inside the row as one
@@ -335,16 +398,16 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   // (no CTA writes into another's shared memory before that one has started)
   if (kMode != kGradOnly && C > 1) cluster_arrive();
   __syncthreads();
-  load_record(s, p, row);
+  load_record<T, kMode != kGradOnly>(s, p, row, reinterpret_cast<const T*>(src));
   if (!mbar_wait(smem_u32(&s.bar), 0, p.wait_ns)) {
     s.late = 1;
     mbar_wait(smem_u32(&s.bar), 0);  // the copy lands before the memory is left
   }
-  if (kMode != kGradOnly && C > 1) cluster_wait();
   __syncthreads();
   const bool late = s.late != 0;
   const int bad_record = s.bad, used = s.used;
   if (bad_record || used == 0) {
+    if (kMode != kGradOnly && C > 1) cluster_wait();
     leave(bad_record ? qnan() : 0.f, bad_record);
     return;
   }
@@ -362,17 +425,11 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   float my_v = 0.f;
   if (mine) {
     my_v = widen(*my_at);
-    if (kMode != kGradOnly) {
-      if (C > 1) {
-        for (int c = 0; c < C; ++c) cluster.map_shared_rank(&s, c)->sv[t] = my_v;
-      } else {
-        s.sv[t] = my_v;
-      }
-    }
     store_value(my_at, -INFINITY);
   }
   __syncthreads();
 
+  Sums sums;
   if (kMode != kGradOnly) {
     RunningSum run;
     for (int i0 = t; i0 < nw; i0 += kDistillThreads * UN) {
@@ -387,10 +444,11 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
     const float2 wr = warp_running(run, p.cc);
     if (lane == 0) s.warp_part[warp] = wr;
     __syncthreads();
+    if (C > 1) cluster_wait();  // every CTA has started
     if (warp == 0) {
       const float2 v = lane < kDistillWarps ? s.warp_part[lane] : make_float2(-INFINITY, 0.f);
       const float m = warp_max_nan(v.x);
-      const float sum = warp_sum(v.y * to_frame(v.x, m, p.cc));
+      const float sum = warp_sum_pair<kDistillWarps>(v.y * to_frame(v.x, m, p.cc)).x;
       if (lane < C) {
         DistillShared* to = C > 1 ? cluster.map_shared_rank(&s, lane) : &s;
         to->part[rank] = make_float4(m, sum, late ? 1.f : 0.f, 0.f);
@@ -398,66 +456,28 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
     }
     if (C > 1) cluster.sync(); else __syncthreads();
 
-    if (warp == 0) {
-      // the rest: its max m and sum S over the cluster's slices
-      const float4 v = lane < C ? s.part[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      const bool any_late = __any_sync(0xffffffffu, v.z != 0.f);
-      const float m = warp_max_nan(v.x);
-      const float2 S = warp_sum_pair(v.y * to_frame(v.x, m, p.cc));
-      // the record, and both together in the frame of M
-      constexpr int kPer = SV_MAX_TOP / kWarp;
-      float x[kPer], M = -INFINITY;
-      bool wrong = m != m || m == INFINITY;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int j = q * kWarp + lane;
-        x[q] = j < p.k && s.id[j] >= 0 ? s.sv[j] : -INFINITY;
-        wrong = wrong || x[q] != x[q] || x[q] == INFINITY;
-        M = fmaxf(M, x[q]);
-      }
-      M = fmaxf(warp_max(M), m);
-      wrong = __any_sync(0xffffffffu, wrong) || M == -INFINITY || any_late;
-      float z = 0.f;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) z += ex2((x[q] - frame_of(M)) * p.cc);
-      const float2 zk = warp_sum_pair(z);
-      const float down = m == -INFINITY ? 0.f : ex2((m - M) * p.cc);
-      const float rest = S.x * down;
-      Pair Z;
-      Z.add(zk.x);
-      Z.add(rest);
-      Z.add(zk.y);
-      Z.add(fmaf(S.x, down, -rest) + S.y * down);
-      if (lane == 0) {
-        const float zv = Z.value();
-        s.m = m;
-        s.M = M;
-        s.S = m == -INFINITY ? make_float2(1.f, 0.f) : S;
-        s.Z = make_float2(Z.hi, Z.lo);
-        s.stat = make_float4(frame_of(m), m == -INFINITY ? 0.f : (rest / zv - s.p_rest) / S.x, M,
-                             wrong ? qnan() : 1.f / zv);
-        if (rank == 0) {
-          if (p.out_stats) p.out_stats[row] = wrong ? make_float4(0.f, 0.f, 0.f, qnan()) : s.stat;
-          if (p.out_status) p.out_status[row] = any_late ? SV_REQ_TIMEOUT : wrong ? SV_REQ_BAD_LOGITS : 0;
-          if (wrong) p.out_loss[row] = qnan();
-        }
-      }
+    // every warp for itself: no broadcast to wait for
+    sums = row_sums(s, C, p.cc);
+    const bool any_late = __any_sync(0xffffffffu, lane < C && s.part[lane < C ? lane : 0].z != 0.f);
+    if (any_late) sums.inv_z = qnan();
+    st = make_float4(frame_of(sums.m), sums.beta, sums.M, sums.inv_z);
+    const bool wrong = st.w != st.w;
+    if (rank == 0 && t == 0) {
+      if (p.out_stats) p.out_stats[row] = wrong ? make_float4(0.f, 0.f, 0.f, qnan()) : st;
+      if (p.out_status)
+        p.out_status[row] = any_late ? SV_REQ_TIMEOUT : wrong ? SV_REQ_BAD_LOGITS : 0;
+      if (wrong) p.out_loss[row] = qnan();
     }
     if (kMode == kLoss) {
-      if (rank == 0 && warp == 0) {
-        __syncwarp();
-        if (s.stat.w == s.stat.w) {
-          const float loss = row_loss(s, p);
-          if (lane == 0) p.out_loss[row] = loss;
-        }
+      if (rank == 0 && warp == 0 && !wrong) {
+        const float loss = row_loss(s, p, sums);
+        if (lane == 0) p.out_loss[row] = loss;
       }
       return;
     }
-    __syncthreads();
   }
 
   // The gradient.
-  const float4 st = s.stat;
   if (st.w != st.w) {
     fill_bytes(grad + x0, x1 - x0);
     return;
@@ -493,7 +513,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
     store_slice(grad + x0, words + (x0 + r - 16 * w0), x1 - x0);
   }
   if (kMode == kLossGrad && rank == 0 && warp == 0) {  // nothing waits for the loss here
-    const float loss = row_loss(s, p);
+    const float loss = row_loss(s, p, sums);
     if (lane == 0) p.out_loss[row] = loss;
   }
 }

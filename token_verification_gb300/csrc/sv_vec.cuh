@@ -375,11 +375,13 @@ struct Pair {
   __device__ __forceinline__ float value() const { return hi + lo; }
 };
 
-// A warp's sum as hi + lo, the additions' roundings kept in lo.
+// A warp's sum as hi + lo, the additions' roundings kept in lo; of its first
+// kLanes lanes (a power of two) when the others hold 0, in every lane.
+template <int kLanes = kWarp>
 __device__ __forceinline__ float2 warp_sum_pair(float x) {
-  float hi = x, lo = 0.f;
+  float hi = kLanes < kWarp ? __shfl_sync(0xffffffffu, x, lane_id() & (kLanes - 1)) : x, lo = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
     const float y = __shfl_xor_sync(0xffffffffu, hi, o), yl = __shfl_xor_sync(0xffffffffu, lo, o);
     const float sum = __fadd_rn(hi, y);
     // both lanes of a pair take the larger first: the same rounding in each
