@@ -50,18 +50,25 @@ struct DistillParams {
 };
 
 struct alignas(16) DistillShared {
-  float4 part[kMaxCluster];      // each CTA's {max, sum, late, -} over its slice without the record
+  float4 part[kMaxCluster];      // each CTA's {max, sum, status bits, -} of its slice without the record
   float2 warp_part[kDistillWarps];
   unsigned long long bar;        // the slice's arrival
+  unsigned long long part_bar;   // the cluster's parts' arrival
   int id[SV_MAX_TOP];            // the record (-1: unused)
   float t[SV_MAX_TOP];           // its logits (-inf: unused)
   float p[SV_MAX_TOP];           // its teacher probabilities
   float sv[SV_MAX_TOP];          // the student's logits at its tokens
-  int bad, used, late;
+  int bad, used, late, twice;
   float norm, norm_lo;           // the teacher's log-sum-exp: log p_j = t_j / T - norm
   float p_sum, p_rest;           // the record's mass and 1 - it
   float top_m;                   // the student's max on the record (NaN: unusable)
   float2 top_z;                  // and its sum there in that frame (hi, lo)
+  struct Sums {                  // the student's sums:
+    float m, M;                  // max outside the record, and over all
+    float2 S, Z;                 // the sums in their frames
+    float beta, inv_z, q_top;    // q_top: the student's mass on the record
+    int status;
+  } sums;
 };
 
 __device__ __forceinline__ uint16_t to_bf16(float v) {  // round to nearest even
@@ -145,7 +152,7 @@ __device__ __forceinline__ void add_ratio(Pair& a, float x, const DistillParams&
 // log-sum-exp that is not finite beside a used entry.  A whole-CTA call.
 template <typename T, bool kStats>
 __device__ void load_record(DistillShared& s, const DistillParams& p, long long row,
-                            const T* src) {
+                            const T* src, int rank, int C) {
   const int t = threadIdx.x;
   const float lse = p.top_lse ? p.top_lse[row] : 0.f;
   if (t < p.k) {
@@ -165,14 +172,16 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     if (bad) atomicOr(&s.bad, bad);
   }
   __syncthreads();
-  // the CTA's upper half looks for an entry's token among those before, its
-  // first warp goes on to the probabilities, its second to the student's sum
-  if (t >= kDistillThreads / 2 && t - kDistillThreads / 2 < p.k) {
-    const int i = t - kDistillThreads / 2, id = s.id[i];
+  // the CTA's upper half looks for tokens given twice (each CTA of the cluster
+  // for its share of the entries), the first warp goes on to the
+  // probabilities, the second to the student's sum
+  if (kStats && t >= kDistillThreads / 2) {
     bool twice = false;
-    if (id >= 0)
-      for (int j = 0; j < i; ++j) twice = twice || s.id[j] == id;
-    if (twice) atomicOr(&s.bad, SV_REQ_BAD_TOKEN);
+    for (int i = rank; i < p.k; i += C) {
+      const int id = s.id[i], j = t - kDistillThreads / 2;
+      twice = twice || (id >= 0 && j < i && s.id[j] == id);
+    }
+    if (twice) s.twice = 1;
   }
   if (kStats && t >= kWarp && t < 2 * kWarp) {
     constexpr int kPer = SV_MAX_TOP / kWarp;
@@ -238,16 +247,9 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
   }
 }
 
-// The student's sums: over the tokens outside the record (max m, S in its
-// frame) and over all (M, Z).
-struct Sums {
-  float m, M;
-  float2 S, Z;
-  float beta, inv_z, q_top;  // q_top: the student's mass on the record
-  bool wrong;
-};
+using Sums = DistillShared::Sums;
 
-// From the record's and the cluster's parts; a call of one warp (all the same).
+// From the record's and the cluster's parts; a call of one warp.
 __device__ Sums row_sums(const DistillShared& s, int C, float c) {
   const int lane = lane_id();
   const float4 v = lane < C ? s.part[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
@@ -255,7 +257,8 @@ __device__ Sums row_sums(const DistillShared& s, int C, float c) {
   r.m = warp_max_nan(v.x);
   r.S = warp_sum_pair<kMaxCluster>(v.y * to_frame(v.x, r.m, c));
   r.M = max_nan(r.m, s.top_m);
-  r.wrong = !is_finite(r.M);
+  r.status = (int)__reduce_or_sync(0xffffffffu, lane < C ? __float_as_uint(v.z) : 0u);
+  if (!is_finite(r.M) && !(r.status & SV_REQ_TIMEOUT)) r.status |= SV_REQ_BAD_LOGITS;
   const float up = to_frame(s.top_m, r.M, c), down = to_frame(r.m, r.M, c);
   const float rest = r.S.x * down, top = s.top_z.x * up;
   Pair Z;
@@ -264,7 +267,7 @@ __device__ Sums row_sums(const DistillShared& s, int C, float c) {
   Z.add(fmaf(s.top_z.x, up, -top) + s.top_z.y * up);
   Z.add(fmaf(r.S.x, down, -rest) + r.S.y * down);
   r.Z = make_float2(Z.hi, Z.lo);
-  r.inv_z = r.wrong ? qnan() : 1.f / Z.value();
+  r.inv_z = r.status ? qnan() : 1.f / Z.value();
   r.q_top = top * r.inv_z;
   r.beta = r.m == -INFINITY ? 0.f : (rest * r.inv_z - s.p_rest) / r.S.x;
   return r;
@@ -374,9 +377,12 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   const int lo = nw > 0 && 16 * w0 - r < 0 ? 1 : 0;
   const int hi = max(lo, nw > 0 && 16 * w1 - r > nb ? nw - 1 : nw);
   if (t == 0) {
-    s.bad = s.used = s.late = 0;
+    s.bad = s.used = s.late = s.twice = 0;
     mbar_init(smem_u32(&s.bar), 1);
+    if (kMode != kGradOnly && C > 1) mbar_init(smem_u32(&s.part_bar), 1);
     fence_mbar_init();
+    if (kMode != kGradOnly && C > 1)
+      mbar_arrive_expect_tx(smem_u32(&s.part_bar), 16u * (uint32_t)C);
     const uint32_t bytes = 16u * (uint32_t)(hi - lo);
     mbar_arrive_expect_tx(smem_u32(&s.bar), bytes);
     if (bytes)
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   // (no CTA writes into another's shared memory before that one has started)
   if (kMode != kGradOnly && C > 1) cluster_arrive();
   __syncthreads();
-  load_record<T, kMode != kGradOnly>(s, p, row, reinterpret_cast<const T*>(src));
+  load_record<T, kMode != kGradOnly>(s, p, row, reinterpret_cast<const T*>(src), rank, C);
   if (!mbar_wait(smem_u32(&s.bar), 0, p.wait_ns)) {
     s.late = 1;
     mbar_wait(smem_u32(&s.bar), 0);  // the copy lands before the memory is left
@@ -429,7 +435,6 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   }
   __syncthreads();
 
-  Sums sums;
   if (kMode != kGradOnly) {
     RunningSum run;
     for (int i0 = t; i0 < nw; i0 += kDistillThreads * UN) {
@@ -443,38 +448,55 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
     }
     const float2 wr = warp_running(run, p.cc);
     if (lane == 0) s.warp_part[warp] = wr;
-    __syncthreads();
     if (C > 1) cluster_wait();  // every CTA has started
+    __syncthreads();
     if (warp == 0) {
       const float2 v = lane < kDistillWarps ? s.warp_part[lane] : make_float2(-INFINITY, 0.f);
       const float m = warp_max_nan(v.x);
       const float sum = warp_sum_pair<kDistillWarps>(v.y * to_frame(v.x, m, p.cc)).x;
-      if (lane < C) {
-        DistillShared* to = C > 1 ? cluster.map_shared_rank(&s, lane) : &s;
-        to->part[rank] = make_float4(m, sum, late ? 1.f : 0.f, 0.f);
+      const int status = (late ? SV_REQ_TIMEOUT : 0) | (s.twice ? SV_REQ_BAD_TOKEN : 0);
+      const float4 part = make_float4(m, sum, __uint_as_float((uint32_t)status), 0.f);
+      bool came = true;
+      if (C > 1) {
+        if (lane < C)
+          send16(in_cta(smem_u32(&s.part[rank]), lane), in_cta(smem_u32(&s.part_bar), lane), part);
+        // (a peer that does not send has failed; the limit is the waits' default)
+        came = mbar_wait_cluster(smem_u32(&s.part_bar), 0, kWaitLimitNs);
+      } else {
+        if (lane == 0) s.part[0] = part;
+        __syncwarp();
       }
-    }
-    if (C > 1) cluster.sync(); else __syncthreads();
-
-    // every warp for itself: no broadcast to wait for
-    sums = row_sums(s, C, p.cc);
-    const bool any_late = __any_sync(0xffffffffu, lane < C && s.part[lane < C ? lane : 0].z != 0.f);
-    if (any_late) sums.inv_z = qnan();
-    st = make_float4(frame_of(sums.m), sums.beta, sums.M, sums.inv_z);
-    const bool wrong = st.w != st.w;
-    if (rank == 0 && t == 0) {
-      if (p.out_stats) p.out_stats[row] = wrong ? make_float4(0.f, 0.f, 0.f, qnan()) : st;
-      if (p.out_status)
-        p.out_status[row] = any_late ? SV_REQ_TIMEOUT : wrong ? SV_REQ_BAD_LOGITS : 0;
-      if (wrong) p.out_loss[row] = qnan();
+      Sums sums = row_sums(s, C, p.cc);
+      if (!__all_sync(0xffffffffu, came)) {
+        sums.status = SV_REQ_TIMEOUT;
+        sums.inv_z = qnan();
+      }
+      if (lane == 0) {
+        s.sums = sums;
+        if (rank == 0) {
+          const bool wrong = sums.status != 0;
+          if (p.out_stats)
+            p.out_stats[row] =
+                wrong ? make_float4(0.f, 0.f, 0.f, qnan())
+                      : make_float4(frame_of(sums.m), sums.beta, sums.M, sums.inv_z);
+          if (p.out_status) p.out_status[row] = sums.status;
+          if (wrong) p.out_loss[row] = qnan();
+        }
+      }
     }
     if (kMode == kLoss) {
-      if (rank == 0 && warp == 0 && !wrong) {
-        const float loss = row_loss(s, p, sums);
-        if (lane == 0) p.out_loss[row] = loss;
+      if (rank == 0 && warp == 0) {
+        __syncwarp();
+        if (s.sums.status == 0) {
+          const float loss = row_loss(s, p, s.sums);
+          if (lane == 0) p.out_loss[row] = loss;
+        }
       }
+      // (the parts sent here have arrived before the CTA's memory goes: warp 0 saw them)
       return;
     }
+    __syncthreads();
+    st = make_float4(frame_of(s.sums.m), s.sums.beta, s.sums.M, s.sums.inv_z);
   }
 
   // The gradient.
@@ -513,7 +535,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
     store_slice(grad + x0, words + (x0 + r - 16 * w0), x1 - x0);
   }
   if (kMode == kLossGrad && rank == 0 && warp == 0) {  // nothing waits for the loss here
-    const float loss = row_loss(s, p, sums);
+    const float loss = row_loss(s, p, s.sums);
     if (lane == 0) p.out_loss[row] = loss;
   }
 }

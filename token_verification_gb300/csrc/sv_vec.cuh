@@ -354,12 +354,53 @@ cudaError_t launch_early(void (*fn)(P...), unsigned grid, unsigned block, size_t
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// The two halves of a cluster barrier (release / acquire).
+// The two halves of a cluster barrier without memory ordering (the ordering
+// forms drain every access of the warp first): each CTA of the cluster has
+// started, and has initialised its mbarriers before it arrived
+// (fence_mbar_init).
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address in CTA `rank` of the cluster of a shared address of this CTA.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// 16 bytes into another CTA's shared memory, their arrival counted by that
+// CTA's mbarrier: nothing to flush or wait for on this side.
+__device__ __forceinline__ void send16(uint32_t addr, uint32_t bar, const float4& v) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::
+          "r"(addr),
+      "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)),
+      "r"(__float_as_uint(v.w)), "r"(bar)
+      : "memory");
+}
+// mbar_wait for what other CTAs sent.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  unsigned long long limit_ns) {
+  auto arrived = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (arrived()) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (arrived()) return true;
+    if (global_ns() - t0 > limit_ns) return false;
+  }
 }
 
 // hi + lo, |lo| about half a step of hi: sums of a few fp32 values without
