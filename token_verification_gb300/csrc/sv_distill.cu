@@ -119,23 +119,33 @@ __device__ void store_slice(char* dst, const unsigned char* src, int bytes) {
     *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
 }
 
-// 2^((l - m) c) * scale of each element of a group.
+// 2^((l - m) c) * scale of each element of a group, in packed pairs.
+__device__ __forceinline__ f32x2 scaled_pair(float a, float b, f32x2 nm2, f32x2 c2, f32x2 s2) {
+  float x, y;
+  unpack2(mul2(add2(pack2(a, b), nm2), c2), x, y);
+  return mul2(pack2(ex2(x), ex2(y)), s2);
+}
 __device__ __forceinline__ uint4 scaled_group(const uint4& g, float c, float m, float scale,
                                               const uint16_t*) {
+  const f32x2 nm2 = pack2(-m, -m), c2 = pack2(c, c), s2 = pack2(scale, scale);
   const uint32_t w[4] = {g.x, g.y, g.z, g.w};
   uint32_t o[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    o[q] = to_bf16x2(ex2((bf16_lo(w[q]) - m) * c) * scale,
-                     ex2((bf16_hi(w[q]) - m) * c) * scale);
+  for (int q = 0; q < 4; ++q) {
+    float x, y;
+    unpack2(scaled_pair(bf16_lo(w[q]), bf16_hi(w[q]), nm2, c2, s2), x, y);
+    o[q] = to_bf16x2(x, y);
+  }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 __device__ __forceinline__ uint4 scaled_group(const uint4& g, float c, float m, float scale,
                                               const float*) {
-  auto f = [&](uint32_t w) {
-    return __float_as_uint(ex2((__uint_as_float(w) - m) * c) * scale);
-  };
-  return make_uint4(f(g.x), f(g.y), f(g.z), f(g.w));
+  const f32x2 nm2 = pack2(-m, -m), c2 = pack2(c, c), s2 = pack2(scale, scale);
+  float x0, x1, x2, x3;
+  unpack2(scaled_pair(__uint_as_float(g.x), __uint_as_float(g.y), nm2, c2, s2), x0, x1);
+  unpack2(scaled_pair(__uint_as_float(g.z), __uint_as_float(g.w), nm2, c2, s2), x2, x3);
+  return make_uint4(__float_as_uint(x0), __float_as_uint(x1), __float_as_uint(x2),
+                    __float_as_uint(x3));
 }
 
 // x / T as hi + lo.
@@ -405,7 +415,8 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   if (kMode != kGradOnly && C > 1) cluster_arrive();
   __syncthreads();
   load_record<T, kMode != kGradOnly>(s, p, row, reinterpret_cast<const T*>(src), rank, C);
-  if (!mbar_wait(smem_u32(&s.bar), 0, p.wait_ns)) {
+  // one warp waits for the copy, the others at the barrier
+  if (warp == kDistillWarps - 1 && !mbar_wait(smem_u32(&s.bar), 0, p.wait_ns)) {
     s.late = 1;
     mbar_wait(smem_u32(&s.bar), 0);  // the copy lands before the memory is left
   }
@@ -437,13 +448,15 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
 
   if (kMode != kGradOnly) {
     RunningSum run;
-    for (int i0 = t; i0 < nw; i0 += kDistillThreads * UN) {
+    int i = t;
+    for (; i + (UN - 1) * kDistillThreads < nw; i += kDistillThreads * UN) {
       uint4 g[UN];
 #pragma unroll
-      for (int u = 0; u < UN; ++u) {
-        const int i = i0 + u * kDistillThreads;
-        g[u] = i < nw ? load128(words + 16 * i) : Lane<T, VEC>::pad();
-      }
+      for (int u = 0; u < UN; ++u) g[u] = load128(words + 16 * (i + u * kDistillThreads));
+      run.add(g, p.cc, tag);
+    }
+    for (; i < nw; i += kDistillThreads) {
+      const uint4 g[1] = {load128(words + 16 * i)};
       run.add(g, p.cc, tag);
     }
     const float2 wr = warp_running(run, p.cc);
