@@ -5,6 +5,7 @@ There is no fallback: if the library has not been built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -23,8 +24,33 @@ SYMBOLS = (
     "spec_beam_reorder",
 )
 
+BINDING_PATH = os.path.join(HERE, "_binding.so")
+
 _lock = threading.Lock()
 _lib = None
+_binding = None
+
+
+def binding():
+    """The compiled short way to the draft operators (csrc/binding.cpp)."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    l = lib()
+    import torch  # noqa: F401  (its libraries, which the module links against)
+    with _lock:
+        if _binding is None:
+            if not os.path.exists(BINDING_PATH):
+                raise RuntimeError("_binding.so is not built (expected at %s); build it with "
+                                   "token_verification_gb300.build.build()" % BINDING_PATH)
+            spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            m.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                l.spec_top_logits, l.spec_distill, l.spec_distill_grad, l.spec_beam_select,
+                l.spec_beam_workspace_size, l.spec_beam_reorder)))
+            _binding = m
+    return _binding
 
 
 def lib():

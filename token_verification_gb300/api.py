@@ -407,6 +407,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _short(answer, make):
+    """make(*outputs) of the compiled binding's answer to a plain call."""
+    if type(answer) is tuple:
+        return make(*answer)
+    raise VerifyError(answer)
+
+
 def _launch(device, fn, *args):
     """fn(*args, stream) on the device's current stream, with the device current."""
     index = device.index
@@ -468,6 +475,10 @@ def spec_top_logits(logits, k, temperature=1.0, out: Optional[TopLogits] = None,
     spec_verify.h): logits [B, P, V] bf16/fp32 CUDA, 1 <= k <= 128, temperature
     > 0 (of the log-sum-exp), lens [B] int32 or None (rows i >= lens[b] are not
     read: pass accept_len to record a verify call's accepted positions)."""
+    if out is None:
+        r = _native.binding().top_logits(logits, k, temperature, lens, bool(status))
+        if r is not None:
+            return _short(r, TopLogits)
     B, P, V, device, code = _rows(logits, "logits", "[B, P, V]")
     k = _count(k)
     if lens is not None:
@@ -521,8 +532,13 @@ def spec_distill(student_logits, top_ids, top_logits, temperature=1.0,
     or None.  With grad_loss [B, P] fp32 the same pass also writes out.grad,
     the gradient of (grad_loss * loss).sum() in the student's type, for
     ``student_logits.backward(out.grad)``; out.grad may be student_logits."""
+    if out is None:
+        r = _native.binding().distill(student_logits, top_ids, top_logits, temperature, top_lse,
+                                      lens, grad_loss, bool(stats), bool(status))
+        if r is not None:
+            return _short(r, DistillOutputs)
     B, P, V, k, device, code = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
-                                       grad_loss)
+                                             grad_loss)
     if out is None:
         f32 = torch.float32
         out = DistillOutputs(
@@ -548,10 +564,15 @@ def spec_distill_grad(student_logits, top_ids, top_logits, temperature, stats, g
     student_logits, from the stats of a spec_distill call on the same inputs.
     grad: the tensor to write ([B, P, V], the student's type; student_logits
     itself is allowed), or None for a new one."""
+    if grad is None:
+        r = _native.binding().distill_grad(student_logits, top_ids, top_logits, temperature,
+                                           stats, grad_loss, top_lse, lens)
+        if r is not None:
+            return _short(r, lambda g: g)
     if grad_loss is None or stats is None:
         raise ValueError("stats and grad_loss are required")
     B, P, V, k, device, code = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
-                                       grad_loss)
+                                             grad_loss)
     _need(stats, "stats", device, torch.float32, (B, P, 4))
     if grad is None:
         grad = torch.empty((B, P, V), dtype=student_logits.dtype, device=device)
@@ -577,6 +598,10 @@ def spec_beam_select(logits, scores, n, out: Optional[BeamOutputs] = None, *,
     """One step of beam selection (see spec_verify.h): logits [B, W, V]
     bf16/fp32 CUDA, scores [B, W] fp32 (-inf: a finished beam, not read); the
     n best continuations by scores + log_softmax(logits), best first."""
+    if out is None:
+        r = _native.binding().beam_select(logits, scores, n, bool(status))
+        if r is not None:
+            return _short(r, BeamOutputs)
     B, W, V, device, code = _rows(logits, "logits", "[B, W, V]")
     n = _count(n)
     _need(scores, "scores", device, torch.float32, (B, W))
@@ -612,6 +637,12 @@ def spec_beam_reorder(state, parents, out=None, *, lens=None, status=None) -> to
     it is); lens [B] int32 or None; out [G, B, W_out, H, L, D] of the same
     type (None: a new tensor of zeros); status: an int32 [B] tensor to receive
     the request status, or None."""
+    if out is not None and status is None:
+        r = _native.binding().beam_reorder(state, parents, out, lens)
+        if r is not None:
+            if r:
+                raise VerifyError(r)
+            return out
     if not isinstance(state, torch.Tensor) or state.dim() != 6:
         raise ValueError("state must be a [G, B, W, H, L, D] tensor")
     device = state.device
