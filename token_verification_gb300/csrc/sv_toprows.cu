@@ -282,6 +282,8 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
   __shared__ Select sel;
   __shared__ __align__(16) uint16_t unit[kTopThreads];
   __shared__ double s_off[SV_MAX_BEAMS];
+  __shared__ float off_down[SV_MAX_BEAMS];
+  extern __shared__ float score[];  // W n
   pdl_wait();
   pdl_launch_dependents();
   const long long b = blockIdx.x;
@@ -293,6 +295,7 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
   if (t < p.W) {
     const double o = off[b * p.W + t];
     s_off[t] = o;
+    off_down[t] = __double2float_rd(o);
     if (o != o) atomicOr(&sel.bad, SV_REQ_BAD_LOGITS);
   }
   __syncthreads();
@@ -307,29 +310,38 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
   };
   int count = 0;
   if (!bad) {
-    // bounds of the scores, rounded down; an empty slot's logit is -inf. Each
-    // row's values are in descending order: a thread's are spread over the
-    // positions (7919 is a prime beyond any factor of W n).
-    float um = -INFINITY;
-    for (int q = t; q < all; q += kTopThreads) {
-      const int i = (int)((unsigned)q * 7919u % (unsigned)all);
-      const float l = values[i];
-      if (l > -INFINITY) um = fmaxf(um, __fadd_rd(__double2float_rd(s_off[i / p.n]), l));
+    // the scores in fp32, rounded down (-inf for an empty slot)
+    for (int i0 = 0; i0 < all; i0 += 8 * kTopThreads) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int i = i0 + q * kTopThreads + t;
+        v[q] = i < all ? values[i] : -INFINITY;
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int i = i0 + q * kTopThreads + t;
+        if (i < all) score[i] = v[q] > -INFINITY ? __fadd_rd(off_down[i / p.n], v[q]) : -INFINITY;
+      }
     }
+    __syncthreads();
+    // Each row's are in descending order: a thread's are spread over the
+    // positions (steps of 7919, a prime beyond any factor of W n).
+    float um = -INFINITY;
+    const int per = (all + kTopThreads - 1) / kTopThreads;
+    for (int q = t * per; q < min(t * per + per, all); ++q)
+      um = fmaxf(um, score[(unsigned)q * 7919u % (unsigned)all]);
     unit[t] = down_bf16(um);
     const float bound = unit_bound<0>(sel, unit, kTopThreads, p.n);
     for (int i = t; i < all; i += kTopThreads) {
-      const float l = values[i];
-      const int w = i / p.n;
-      if (l > -INFINITY) {
-        const double score = s_off[w] + (double)l;
-        // what rounds below the bound is below n others
-        if (__double2float_ru(score) >= bound) {
-          const int o = atomicAdd(&sel.n_cands, 1);
-          if (o < kMaxCands) {
-            ls.key[o] = ordered(score);
-            ls.idx[o] = w * p.V + ids[i];
-          }
+      const float f = score[i];
+      // what stays below the bound with its roundings given back is below n others
+      if (f > -INFINITY && fmaf(fabsf(f), 1e-6f, f) >= bound) {
+        const int o = atomicAdd(&sel.n_cands, 1);
+        if (o < kMaxCands) {
+          const int w = i / p.n;
+          ls.key[o] = ordered(s_off[w] + (double)values[i]);
+          ls.idx[o] = w * p.V + ids[i];
         }
       }
     }
@@ -395,8 +407,14 @@ cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long
 
 cudaError_t launch_beam_merge(const TopParams& p, const int* ids, const float* values,
                               const double* off, int B, cudaStream_t stream) {
-  return launch_early(beam_merge_kernel, (unsigned)B, kTopThreads, 0, 1, stream, p, ids, values,
-                      off);
+  static PerDevice once;
+  const cudaError_t err = per_device(once, nullptr, [&](int&) {
+    return cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                4 * SV_MAX_BEAMS * SV_MAX_TOP);
+  });
+  if (err != cudaSuccess) return err;
+  return launch_early(beam_merge_kernel, (unsigned)B, kTopThreads, 4 * (size_t)p.W * p.n, 1, stream,
+                      p, ids, values, off);
 }
 
 }  // namespace sv
