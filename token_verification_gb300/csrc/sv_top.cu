@@ -5,10 +5,10 @@
 //
 // A row (of a request's W beams, or the one row of a record) is cut into
 // `slices`; the (row, slice) items are dealt to the cluster's CTAs, which
-// stream them and select as sv_select.cuh describes.  Two cluster barriers:
-// one after the streams, when every CTA has every item's sums and units and
-// works out offsets and bound for itself, one after the candidates have
-// gone to the leader CTA's list.
+// stream them and select as sv_select.cuh describes.  Each CTA sends its items'
+// sums and units to all others (asynchronous remote stores counted by the
+// receiver's mbarrier) and works out offsets and bound for itself; the
+// candidates go to the leader CTA's list, before a cluster barrier.
 //
 // A beam's candidates compare by score = offset + logit with offset =
 // scores[w] - lse[w] in 64 bits; a record's offset is 0.  Bounds are in fp32
@@ -24,12 +24,13 @@ constexpr int kMaxItems = 64;         // (row, slice) items per cluster
 constexpr int kManyRows = 152;
 
 struct alignas(16) TopShared {
-  float2 part[kMaxItems][kTopWarps];  // per item and warp: {max, sum of 2^((l - max) c)}
+  alignas(16) float2 part[kMaxItems][kTopWarps];  // per item and warp: {max, sum of 2^((l - max) c)}
   alignas(16) uint16_t unit[kMaxUnits];  // unit maxes, item by item: bf16 rounded down
   double off[SV_MAX_BEAMS];           // beams: score - lse of each row (-inf: no candidates)
   float off_down[SV_MAX_BEAMS];       // the same rounded down
   float thr[SV_MAX_BEAMS];            // the lowest logit a candidate of the row can have
   float lse;                          // record
+  unsigned long long part_bar;        // the other CTAs' items have come
   Select sel;
 };
 
@@ -79,7 +80,16 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
       return;
     }
   }
-  if (t == 0) s.sel.n_hits = s.sel.n_cands = s.sel.overflow = s.sel.bad = 0;
+  const int own = rank < items ? (items - rank + C - 1) / C : 0;
+  const int sent = 64 + 2 * p.upi;  // bytes of an item's parts and units
+  if (t == 0) {
+    s.sel.n_hits = s.sel.n_cands = s.sel.overflow = s.sel.bad = 0;
+    if (C > 1) {
+      mbar_init(smem_u32(&s.part_bar), 1);
+      fence_mbar_init();
+      mbar_arrive_expect_tx(smem_u32(&s.part_bar), (uint32_t)((items - own) * sent));
+    }
+  }
   // no CTA writes into another's shared memory before that one has started
   if (C > 1) cluster_arrive();
 
@@ -102,17 +112,24 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
     const float2 wr = warp_running(r, p.cc);
     float um = r.m;
     for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
-    if (C > 1 && mine == 0) cluster_wait();
-    for (int c = 0; c < C; ++c) {
-      TopShared* to = C > 1 ? cluster.map_shared_rank(&s, c) : &s;
-      if (lane == 0) to->part[it][warp] = wr;
-      if ((t & (fold - 1)) == 0) to->unit[it * p.upi + t / fold] = down_bf16(um);
-    }
+    if (lane == 0) s.part[it][warp] = wr;
+    if ((t & (fold - 1)) == 0) s.unit[it * p.upi + t / fold] = down_bf16(um);
   }
-  if (C > 1) {
-    if (rank >= items) cluster_wait();
-    cluster.sync();
-  } else {
+  __syncthreads();
+  if (C > 1) {  // this CTA's items to the others, theirs to come
+    cluster_wait();
+    const int pieces = sent / 16;
+    for (int q = t; q < own * pieces * C; q += kTopThreads) {
+      const int c = q % C, it = rank + q / C / pieces * C, piece = q / C % pieces;
+      const void* from = piece < 4 ? reinterpret_cast<const char*>(s.part[it]) + 16 * piece
+                                   : reinterpret_cast<const char*>(s.unit + it * p.upi) +
+                                         16 * (piece - 4);
+      if (c != rank)
+        send16(in_cta(smem_u32(from), c), in_cta(smem_u32(&s.part_bar), c),
+               *reinterpret_cast<const float4*>(from));
+    }
+    if (warp == 0 && !mbar_wait_cluster(smem_u32(&s.part_bar), 0, kWaitLimitNs))
+      s.sel.bad = SV_REQ_TIMEOUT;  // a peer has failed
     __syncthreads();
   }
 
@@ -126,7 +143,7 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
       const float score = kBeam ? p.scores[grp * p.W + w] : 0.f;
       const bool dead = kBeam && score == -INFINITY;
       if (!dead && (m != m || m == INFINITY || score != score || score == INFINITY))
-        s.sel.bad = SV_REQ_BAD_LOGITS;
+        atomicOr(&s.sel.bad, SV_REQ_BAD_LOGITS);
       if (kBeam) {
         double off = -INFINITY;
         if (!dead && m != -INFINITY) off = row_offset(score, m, l);
