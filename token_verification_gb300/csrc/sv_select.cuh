@@ -40,7 +40,7 @@ struct TopParams {
   int V, n;
   int slices, slice;    // slices per row, elements per slice (a multiple of 256)
   int iters;            // iterations per item
-  int upi;              // units per item (a power of two)
+  int upi, fold;        // units per item (a multiple of 8), threads per unit
   int table_bytes;
   float cc;             // log2(e) / T
   float T;
@@ -465,6 +465,23 @@ __device__ __forceinline__ double row_offset(float score, float m, float2 log_su
 }
 
 constexpr int ring_bytes(int warps) { return Ring::kWarpBytes * warps; }
+
+// Units of `fold` threads: two per kept candidate, counting only the threads
+// that a slice gives anything (its 2 KB chunks go to the warps in turn); padded
+// to a multiple of 8 per item (the idle threads' -inf), at most kMaxUnits in
+// all (64 items of 8 fit).
+inline void set_units(TopParams& p, sv_dtype dtype, int items, int slice, int threads) {
+  const int chunk = dtype == SV_BF16 ? Piece<uint16_t>::kChunkSize : Piece<float>::kChunkSize;
+  const int chunks = (slice + chunk - 1) / chunk;
+  const int busy = chunks * kWarp < threads ? chunks * kWarp : threads;
+  const auto units = [&](int fold) { return (busy + fold - 1) / fold; };
+  const auto padded = [&](int fold) { return (units(fold) + 7) / 8 * 8; };
+  p.fold = 1;
+  while (p.fold < kWarp &&
+         (items * padded(p.fold) > kMaxUnits || items * units(2 * p.fold) >= 2 * p.n))
+    p.fold *= 2;
+  p.upi = padded(p.fold);
+}
 
 }  // namespace
 }  // namespace sv

@@ -15,13 +15,14 @@
 // rounded down, which can only lengthen the list.
 #include <string.h>
 
+#include <algorithm>
+
 #include "sv_select.cuh"
 
 namespace sv {
 namespace {
 
 constexpr int kMaxItems = 64;         // (row, slice) items per cluster
-constexpr int kManyRows = 152;
 
 struct alignas(16) TopShared {
   alignas(16) float2 part[kMaxItems][kTopWarps];  // per item and warp: {max, sum of 2^((l - max) c)}
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   if (C > 1) cluster_arrive();
 
   // One pass over each item.
-  const int fold = kTopThreads / p.upi;
+  const int fold = p.fold;
   for (int it = rank, mine = 0; it < items; it += C, ++mine) {
     const int w = it / p.slices, e0 = (it - w * p.slices) * p.slice;
     const int e1 = min(e0 + p.slice, p.V);
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
     float um = r.m;
     for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
     if (lane == 0) s.part[it][warp] = wr;
-    if ((t & (fold - 1)) == 0) s.unit[it * p.upi + t / fold] = down_bf16(um);
+    if ((t & (fold - 1)) == 0 && t / fold < p.upi) s.unit[it * p.upi + t / fold] = down_bf16(um);
   }
   __syncthreads();
   if (C > 1) {  // this CTA's items to the others, theirs to come
@@ -284,9 +285,22 @@ bool set_span(TopParams& p, sv_dtype dtype, long long rows) {
   return ((uintptr_t)p.first & 15u) == 0 && ((size_t)p.V * esz) % 16 == 0;
 }
 
-// Rows enough for the row kernel, whose CTAs take one at a time.
-bool by_rows(long long rows, int V) {
-  return rows >= kManyRows && V >= kTopSpan && top_rows_fit(V);
+// Which kernel. The row kernel streams at HBM's rate but gives a row to one
+// CTA; the cluster kernel spreads a row over eight and ends sooner when there
+// are few. Records (us, cluster / rows kernel, k = 32): 1 to 32 rows of 128256
+// bf16 6.6-8.3 / 10.9-11.0, of 32000 bf16 6.3-6.9 / 6.3-6.6; 64 rows 14.3 / 11.1
+// and 11.7 / 6.5.
+bool record_by_rows(sv_dtype dtype, long long rows, int V) {
+  const long long bytes = (long long)V * (dtype == SV_BF16 ? 2 : 4);
+  return (rows > 32 || bytes < 128000) && top_rows_fit(V);
+}
+// Beams go through the row kernel in two launches. (us, cluster / rows, n = 16,
+// bf16: 1 x 4 of 32000 8.1 / 9.9; 38 x 8 of 32000 (19 MB) 12.6 / 13.4; 16 x 8 of
+// 128256 (33 MB) 17.8 / 15.1; 1 x 16 of 128256 21.6 / 14.9, a cluster's CTAs
+// having two beams each.)
+bool beams_by_rows(sv_dtype dtype, int B, int W, int V) {
+  const long long bytes = (long long)B * W * V * (dtype == SV_BF16 ? 2 : 4);
+  return (W > 8 || bytes > (24ll << 20)) && top_rows_fit(V);
 }
 
 template <bool kBeam>
@@ -311,10 +325,7 @@ sv_status run_top(TopParams& p, sv_dtype dtype, long long groups, cudaStream_t s
   const int items = p.W * p.slices;
   if (items > kMaxItems || (long long)((items + C - 1) / C) * p.iters > kMaxTables)
     return SV_ERR_SHAPE;
-  // two units per kept candidate (or the finest there are), at least one a warp
-  p.upi = kTopThreads;
-  while (p.upi > kTopWarps && items * p.upi > kMaxUnits) p.upi /= 2;
-  while (p.upi > kTopWarps && items * p.upi / 2 >= 2 * p.n) p.upi /= 2;
+  set_units(p, dtype, items, std::min(p.slice, p.V), kTopThreads);
   p.table_bytes = (items + C - 1) / C * p.iters * kTopThreads * 2;
   cudaError_t err;
   if (dtype == SV_BF16)
@@ -360,7 +371,7 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
   p.cc = exponent_scale(temperature);
   p.T = temperature;
   const long long rows = (long long)B * P;
-  if (by_rows(rows, V)) {
+  if (record_by_rows(dtype, rows, V)) {
     const bool aligned = set_span(p, dtype, rows);
     return launch_top_rows(dtype, aligned, p, rows, (cudaStream_t)stream) == cudaSuccess
                ? SV_OK
@@ -375,7 +386,7 @@ size_t spec_beam_workspace_size(sv_dtype dtype, int B, int W, int V, int n) {
     return 0;
   const size_t rows = (size_t)B * W;
   // each row's offset, then its n best logits and their tokens
-  return by_rows((long long)rows, V) ? rows * (sizeof(double) + 8 * (size_t)n) : 0;
+  return beams_by_rows(dtype, B, W, V) ? rows * (sizeof(double) + 8 * (size_t)n) : 0;
 }
 
 sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out_tokens,

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParam
   }
 
   // The streaming half.
-  const int fold = kRowStreamers / p.upi;
+  const int fold = p.fold;
   long long row = blockIdx.x;
   if (!first_live) {
     bar_sync(kBarNext, kRowThreads);
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParam
     float um = r.m;
     for (int o = 1; o < fold; o <<= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
     if (lane == 0) slot.part[warp] = wr;
-    if ((t & (fold - 1)) == 0) slot.unit[t / fold] = down_bf16(um);
+    if ((t & (fold - 1)) == 0 && t / fold < p.upi) slot.unit[t / fold] = down_bf16(um);
     bar_arrive(kBarFull + b, kRowThreads);
     bar_sync(kBarNext + (b ^ 1), kRowThreads);
     row = s.next[b ^ 1];
@@ -396,8 +396,7 @@ cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long
   p.slices = 1;
   p.slice = (p.V + 255) / 256 * 256;
   p.iters = (p.V + kRowSpan - 1) / kRowSpan;
-  p.upi = kRowStreamers;
-  while (p.upi > 32 && p.upi / 2 >= 2 * p.n) p.upi /= 2;
+  set_units(p, dtype, 1, p.V, kRowStreamers);
   if (dtype == SV_BF16)
     return aligned ? launch_rows<uint16_t, true>(p, rows, stream)
                    : launch_rows<uint16_t, false>(p, rows, stream);
