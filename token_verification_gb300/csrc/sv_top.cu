@@ -286,21 +286,22 @@ bool set_span(TopParams& p, sv_dtype dtype, long long rows) {
 }
 
 // Which kernel. The row kernel streams at HBM's rate but gives a row to one
-// CTA; the cluster kernel spreads a row over eight and ends sooner when there
-// are few. Records (us, cluster / rows kernel, k = 32): 1 to 32 rows of 128256
-// bf16 6.6-8.3 / 10.9-11.0, of 32000 bf16 6.3-6.9 / 6.3-6.6; 64 rows 14.3 / 11.1
-// and 11.7 / 6.5.
+// CTA; the cluster kernel spreads a row over four or eight and ends sooner when
+// there are few and long ones. Records (us, cluster / row kernel, k = 32): 32
+// rows of 128256 bf16 8.2 / 11.0, 96 rows 10.7 / 11.3, 128 rows 13.9 / 11.4; 96
+// rows of 50001 fp32 10.1 / 11.1; of 32000 bf16 (64 KB) 6.9 / 6.6 at 32 rows and
+// 7.5 / 6.6 at 96.
 bool record_by_rows(sv_dtype dtype, long long rows, int V) {
   const long long bytes = (long long)V * (dtype == SV_BF16 ? 2 : 4);
-  return (rows > 32 || bytes < 128000) && top_rows_fit(V);
+  return (rows > 96 || bytes < 128000) && top_rows_fit(V);
 }
 // Beams go through the row kernel in two launches. (us, cluster / rows, n = 16,
-// bf16: 1 x 4 of 32000 8.1 / 9.9; 38 x 8 of 32000 (19 MB) 12.6 / 13.4; 16 x 8 of
+// bf16: 1 x 4 of 32000 8.1 / 9.9; 100 x 4 of 32000 (26 MB) 12.1 / 16.9; 16 x 8 of
 // 128256 (33 MB) 17.8 / 15.1; 1 x 16 of 128256 21.6 / 14.9, a cluster's CTAs
 // having two beams each.)
 bool beams_by_rows(sv_dtype dtype, int B, int W, int V) {
   const long long bytes = (long long)B * W * V * (dtype == SV_BF16 ? 2 : 4);
-  return (W > 8 || bytes > (24ll << 20)) && top_rows_fit(V);
+  return (W > 8 || bytes > (28ll << 20)) && top_rows_fit(V);
 }
 
 template <bool kBeam>
@@ -308,12 +309,13 @@ sv_status run_top(TopParams& p, sv_dtype dtype, long long groups, cudaStream_t s
   const bool aligned = set_span(p, dtype, groups * p.W);
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return SV_ERR_CUDA;
-  // The cluster: 8 CTAs while the rows do not fill the GPU by themselves (or
-  // the row's group maxes need the shared memory of several), else one per row
-  // (beams: one per beam, up to 8).
+  // The cluster: one CTA per row (beams: per beam, up to 8), more while twice
+  // as many still come to at most 2.8 an SM (64 rows of 128256 bf16: 10.5 us with
+  // clusters of 4, 14.5 with 8), or while the rows' tables need the shared memory
+  // of several.
   int C = 1;
   while (C < 8 && C < p.W) C *= 2;
-  while (C < 8 && (groups * C < 2LL * dev.sms ||
+  while (C < 8 && (5LL * groups * C <= 7LL * dev.sms ||
                    ((long long)p.W * ((p.V + kTopSpan - 1) / kTopSpan) + C - 1) / C > kMaxTables))
     C *= 2;
   p.slices = C > p.W ? C / p.W : 1;
