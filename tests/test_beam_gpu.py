@@ -253,3 +253,71 @@ def test_beams_grow_a_tree_that_is_verified_and_compacted():
         for d in range(1, n):
             want = want + embed[path[d]]
             assert torch.equal(got[b, d], want)
+
+
+def test_every_candidate_equal_in_wide_beams():
+    """64 beams of constant rows, 128 kept: the merge of 8192 equal candidates."""
+    x = torch.full((2, 64, 9001), 0.25, dtype=BF16, device="cuda")
+    s = torch.full((2, 64), -1.5, device="cuda")
+    s[1, ::2] = -math.inf
+    check(x, s, 128, moved=0)
+
+
+def test_two_graphs_on_two_streams():
+    """Each captured call has scratch of its own: two graphs replay at once."""
+    ins = [case(24, 16, 9001, BF16, 50 + i, dead=3) for i in range(2)]
+    graphs, outs, streams = [], [], []
+    for x, s in ins:
+        api.spec_beam_select(x, s, 32)
+        g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=st):
+            outs.append(api.spec_beam_select(x, s, 32))
+        graphs.append(g)
+        streams.append(st)
+    for i, (x, s) in enumerate(ins):
+        y, r = case(24, 16, 9001, BF16, 60 + i, dead=3)
+        x.copy_(y)
+        s.copy_(r)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for (x, s), out in zip(ins, outs):
+        want = api.spec_beam_select(x, s, 32)
+        assert torch.equal(out.tokens, want.tokens) and torch.equal(out.parents, want.parents)
+        assert torch.equal(out.scores, want.scores)
+        few = api.BeamOutputs(out.tokens[:2], out.parents[:2], out.scores[:2])
+        plain.check_beam(x[:2], s[:2], 32, few)
+
+
+def test_reorder_offsets_past_32_bits():
+    D = (1 << 30) + 16
+    state = torch.zeros((1, 1, 5, 1, 1, D), dtype=torch.uint8, device="cuda")
+    for w in range(5):
+        state[0, 0, w, 0, 0, 0] = w + 1
+        state[0, 0, w, 0, 0, -1] = 10 * (w + 1)
+        state[0, 0, w, 0, 0, D // 2 + 7] = w + 100
+    p = torch.tensor([[4, 0, 4, -1]], dtype=torch.int32, device="cuda")
+    out = api.spec_beam_reorder(state, p)
+    for w, q in enumerate([4, 0, 4]):
+        assert torch.equal(out[0, 0, w, 0, 0], state[0, 0, q, 0, 0])
+    assert not bool(out[0, 0, 3].any())
+
+
+def test_binding_and_long_way_agree():
+    """Outputs given by the caller take the Python checks, new ones the compiled binding."""
+    x, s = case(2, 4, 3001, BF16, 70)
+    a = api.spec_beam_select(x, s, 9)
+    b = api.BeamOutputs(*(torch.empty_like(t) for t in (a.tokens, a.parents, a.scores, a.status)))
+    api.spec_beam_select(x, s, 9, out=b)
+    for f in ("tokens", "parents", "scores", "status"):
+        assert torch.equal(getattr(a, f), getattr(b, f))
+    assert api.spec_beam_select(x, s, 9, status=False).status is None
+    with pytest.raises(api.VerifyError):  # the C call's own refusal, through the binding
+        api.spec_beam_select(torch.zeros((1, 65, 8), device="cuda"),
+                             torch.zeros((1, 65), device="cuda"), 4)
+    import numpy as np
+    assert torch.equal(api.spec_beam_select(x, s, np.int64(9)).tokens, a.tokens)

@@ -271,3 +271,37 @@ def test_wait_limit_runs_out():
     assert bool((out.status == api.REQ_TIMEOUT).all()) and bool(torch.isnan(out.loss).all())
     assert not bool(out.grad.any()) and bool(torch.isnan(grad).all())
     check(s, ids, t, lse, 1.0, gl)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 student logits: the last rows, and the gradient in place."""
+    B, V = 14200, 152064
+    s = torch.zeros((B, 1, V), dtype=BF16, device="cuda")
+    tail, ids, t, lse, gl = case(2, 1, V, 8, BF16, 1.0, True, 30)
+    s[-2:] = tail
+    ids = torch.cat([torch.full((B - 2, 1, 8), -1, dtype=torch.int32, device="cuda"), ids])
+    t = torch.cat([torch.zeros((B - 2, 1, 8), device="cuda"), t])
+    lse = torch.cat([torch.zeros((B - 2, 1), device="cuda"), lse])
+    gl = torch.cat([torch.ones((B - 2, 1), device="cuda"), gl])
+    out = api.DistillOutputs(torch.empty((B, 1), device="cuda"), None, s)
+    api.spec_distill(s, ids, t, top_lse=lse, grad_loss=gl, out=out)
+    plain.check_distill(tail, ids[-2:], t[-2:], lse[-2:], 1.0, gl[-2:], None, out.loss[-2:],
+                        s[-2:])
+    assert not bool(out.loss[:-2].any()) and not bool(s[:-2].any())
+
+
+def test_two_streams_at_once():
+    """Calls on different streams share nothing."""
+    cases = [case(64, 4, 32000, 32, BF16, 1.0, True, 40 + i) for i in range(2)]
+    want = [api.spec_distill(s, ids, t, top_lse=lse, grad_loss=gl)
+            for s, ids, t, lse, gl in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i, ((s, ids, t, lse, gl), st) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(st):
+                got[i] = api.spec_distill(s, ids, t, top_lse=lse, grad_loss=gl)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a.loss, b.loss) and torch.equal(a.grad, b.grad)

@@ -170,3 +170,22 @@ def test_two_graphs_on_two_streams():
         want = api.spec_top_logits(x, 40)
         assert torch.equal(out.ids, want.ids) and torch.equal(out.lse, want.lse)
         plain.check_top(x[:2], 40, 1.0, api.spec_top_logits(x[:2].contiguous(), 40))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the first and last rows, through both kernels."""
+    n = 14200
+    x = torch.zeros((1, n, 152064), dtype=BF16, device="cuda")
+    for i in (0, n - 1):
+        x[0, i] = rows((152064,), BF16, i)
+    out = api.spec_top_logits(x, 20)
+    pick = torch.tensor([0, n - 1], device="cuda")
+    few = api.TopLogits(out.ids[:, pick], out.logits[:, pick], out.lse[:, pick],
+                        out.status[:, pick])
+    plain.check_top(x[:, pick], 20, 1.0, few)
+    assert bool((out.ids[0, 1:-1] == torch.arange(20, device="cuda")).all())
+    x = torch.zeros((150, 1, 14500001), dtype=BF16, device="cuda")
+    x[149] = rows((1, 14500001), BF16, 3)
+    out = api.spec_top_logits(x, 3)
+    few = api.TopLogits(out.ids[149:], out.logits[149:], out.lse[149:], out.status[149:])
+    plain.check_top(x[149:], 3, 1.0, few)
