@@ -58,7 +58,8 @@ struct alignas(16) DistillShared {
   float t[SV_MAX_TOP];           // its logits (-inf: unused)
   float p[SV_MAX_TOP];           // its teacher probabilities
   float sv[SV_MAX_TOP];          // the student's logits at its tokens
-  int bad, used, late, twice;
+  int bad, late, twice;
+  int used;                      // bit 0: an entry is used, bit 1: with a finite logit
   float norm, norm_lo;           // the teacher's log-sum-exp: log p_j = t_j / T - norm
   float p_sum, p_rest;           // the record's mass and 1 - it
   float top_m;                   // the student's max on the record (NaN: unusable)
@@ -160,16 +161,20 @@ __device__ __forceinline__ void add_ratio(Pair& a, float x, const DistillParams&
 // straight from the row so that all of it overlaps the slice's copy.  Sets s.bad for
 // a token out of range or given twice, for a NaN or +inf logit, and for a
 // log-sum-exp that is not finite beside a used entry.  A whole-CTA call.
-template <typename T, bool kStats>
+template <typename T, int kMode>
 __device__ void load_record(DistillShared& s, const DistillParams& p, long long row,
                             const T* src, int rank, int C) {
+  constexpr bool kStats = kMode != kGradOnly;
+  // for the loss alone the leader CTA has the teacher's part to itself, the
+  // others need the tokens (and look for their share of tokens given twice)
+  const bool full = kMode != kLoss || rank == 0;
   const int t = threadIdx.x;
   const float lse = p.top_lse ? p.top_lse[row] : 0.f;
   if (t < p.k) {
     const int id = p.top_ids[row * p.k + t];
     const float v = p.top_logits[row * p.k + t];
     const bool in = id >= 0 && id < p.V;
-    if (kStats) s.sv[t] = in ? widen(src[id]) : -INFINITY;
+    if (kStats && full) s.sv[t] = in ? widen(src[id]) : -INFINITY;
     s.id[t] = id;
     s.t[t] = id < 0 ? -INFINITY : v;
     int bad = 0;
@@ -177,7 +182,7 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     if (id >= 0) {
       if (v != v || v == INFINITY) bad |= SV_REQ_BAD_LOGITS;
       if (p.top_lse && !is_finite(lse)) bad |= SV_REQ_BAD_LOGITS;
-      s.used = 1;
+      atomicOr(&s.used, v > -INFINITY ? 3 : 1);
     }
     if (bad) atomicOr(&s.bad, bad);
   }
@@ -193,6 +198,7 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     }
     if (twice) s.twice = 1;
   }
+  if (!full) return;
   if (kStats && t >= kWarp && t < 2 * kWarp) {
     constexpr int kPer = SV_MAX_TOP / kWarp;
     float x[kPer], m = -INFINITY;
@@ -230,7 +236,6 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
       float z = 0.f;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) z += expf((v[q] - frame_of(m)) * p.inv_t);
-      if (t == 0 && s.used && m == -INFINITY) atomicOr(&s.bad, SV_REQ_BAD_LOGITS);
       const float2 l = log_pair(warp_sum_pair(z));
       norm = Pair();
       add_ratio(norm, frame_of(m), p, 1.f);
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
     if (kMode != kGradOnly && C > 1) mbar_init(smem_u32(&s.part_bar), 1);
     fence_mbar_init();
     if (kMode != kGradOnly && C > 1)
-      mbar_arrive_expect_tx(smem_u32(&s.part_bar), 16u * (uint32_t)C);
+      mbar_arrive_expect_tx(smem_u32(&s.part_bar), 16u * (uint32_t)(C - 1));
     const uint32_t bytes = 16u * (uint32_t)(hi - lo);
     mbar_arrive_expect_tx(smem_u32(&s.bar), bytes);
     if (bytes)
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   // (no CTA writes into another's shared memory before that one has started)
   if (kMode != kGradOnly && C > 1) cluster_arrive();
   __syncthreads();
-  load_record<T, kMode != kGradOnly>(s, p, row, reinterpret_cast<const T*>(src), rank, C);
+  load_record<T, kMode>(s, p, row, reinterpret_cast<const T*>(src), rank, C);
   // one warp waits for the copy, the others at the barrier
   if (warp == kDistillWarps - 1 && !mbar_wait(smem_u32(&s.bar), 0, p.wait_ns)) {
     s.late = 1;
@@ -422,7 +427,9 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   }
   __syncthreads();
   const bool late = s.late != 0;
-  const int bad_record = s.bad, used = s.used;
+  const int used = s.used;
+  // (without a log-sum-exp the record has to hold some mass)
+  const int bad_record = s.bad | (!p.top_lse && used == 1 ? SV_REQ_BAD_LOGITS : 0);
   if (bad_record || used == 0) {
     if (kMode != kGradOnly && C > 1) cluster_wait();
     leave(bad_record ? qnan() : 0.f, bad_record);
@@ -470,14 +477,15 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
       const int status = (late ? SV_REQ_TIMEOUT : 0) | (s.twice ? SV_REQ_BAD_TOKEN : 0);
       const float4 part = make_float4(m, sum, __uint_as_float((uint32_t)status), 0.f);
       bool came = true;
+      if (lane == 0) s.part[rank] = part;
+      __syncwarp();
       if (C > 1) {
-        if (lane < C)
+        // to all others, or for the loss alone to the leader
+        if (lane != rank && lane < (kMode == kLoss ? 1 : C))
           send16(in_cta(smem_u32(&s.part[rank]), lane), in_cta(smem_u32(&s.part_bar), lane), part);
+        if (kMode == kLoss && rank != 0) return;
         // (a peer that does not send has failed; the limit is the waits' default)
         came = mbar_wait_cluster(smem_u32(&s.part_bar), 0, kWaitLimitNs);
-      } else {
-        if (lane == 0) s.part[0] = part;
-        __syncwarp();
       }
       Sums sums = row_sums(s, C, p.cc);
       if (!__all_sync(0xffffffffu, came)) {
