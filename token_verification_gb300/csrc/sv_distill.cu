@@ -87,6 +87,11 @@ __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = to_bf16(v); }
 __device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
 
+__device__ __forceinline__ void store_bits(uint16_t* p, uint32_t v) { *p = (uint16_t)v; }
+__device__ __forceinline__ void store_bits(float* p, uint32_t v) { *p = __uint_as_float(v); }
+__device__ __forceinline__ uint32_t load_bits(const uint16_t* p) { return *p; }
+__device__ __forceinline__ uint32_t load_bits(const float* p) { return __float_as_uint(*p); }
+
 // Writes the 32-bit pattern v (equal halves) over `bytes` bytes at `dst` (2-byte
 // aligned).
 __device__ void fill_bytes(char* dst, int bytes, uint32_t v = 0) {
@@ -159,14 +164,14 @@ __device__ __forceinline__ void add_ratio(Pair& a, float x, const DistillParams&
 // The k-sized part of a row: its record, the teacher's probabilities, and (kStats)
 // the student's logits at the recorded tokens with their max and sum, read
 // straight from the row so that all of it overlaps the slice's copy.  Sets s.bad for
-// a token out of range or given twice, for a NaN or +inf logit, and for a
+// a token out of range, for a NaN or +inf logit, and for a
 // log-sum-exp that is not finite beside a used entry.  A whole-CTA call.
 template <typename T, int kMode>
 __device__ void load_record(DistillShared& s, const DistillParams& p, long long row,
-                            const T* src, int rank, int C) {
+                            const T* src, int rank) {
   constexpr bool kStats = kMode != kGradOnly;
   // for the loss alone the leader CTA has the teacher's part to itself, the
-  // others need the tokens (and look for their share of tokens given twice)
+  // others need the tokens
   const bool full = kMode != kLoss || rank == 0;
   const int t = threadIdx.x;
   const float lse = p.top_lse ? p.top_lse[row] : 0.f;
@@ -187,17 +192,6 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     if (bad) atomicOr(&s.bad, bad);
   }
   __syncthreads();
-  // the CTA's upper half looks for tokens given twice (each CTA of the cluster
-  // for its share of the entries), the first warp goes on to the
-  // probabilities, the second to the student's sum
-  if (kStats && t >= kDistillThreads / 2) {
-    bool twice = false;
-    for (int i = rank; i < p.k; i += C) {
-      const int id = s.id[i], j = t - kDistillThreads / 2;
-      twice = twice || (id >= 0 && j < i && s.id[j] == id);
-    }
-    if (twice) s.twice = 1;
-  }
   if (!full) return;
   if (kStats && t >= kWarp && t < 2 * kWarp) {
     constexpr int kPer = SV_MAX_TOP / kWarp;
@@ -419,7 +413,7 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   // (no CTA writes into another's shared memory before that one has started)
   if (kMode != kGradOnly && C > 1) cluster_arrive();
   __syncthreads();
-  load_record<T, kMode>(s, p, row, reinterpret_cast<const T*>(src), rank, C);
+  load_record<T, kMode>(s, p, row, reinterpret_cast<const T*>(src), rank);
   // one warp waits for the copy, the others at the barrier
   if (warp == kDistillWarps - 1 && !mbar_wait(smem_u32(&s.bar), 0, p.wait_ns)) {
     s.late = 1;
@@ -447,10 +441,15 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   const bool mine = my_id >= 0 && my_x >= x0 && my_x < x1;
   T* my_at = reinterpret_cast<T*>(words + (my_x + r - 16 * w0));
   float my_v = 0.f;
-  if (mine) {
-    my_v = widen(*my_at);
-    store_value(my_at, -INFINITY);
+  if (mine) my_v = widen(*my_at);
+  if (kMode != kGradOnly) {
+    // a token given twice: of the entries that write their number there, one
+    // does not find its own
+    if (mine) store_bits(my_at, (uint32_t)t);
+    __syncthreads();
+    if (mine && load_bits(my_at) != (uint32_t)t) s.twice = 1;
   }
+  if (mine) store_value(my_at, -INFINITY);
   __syncthreads();
 
   if (kMode != kGradOnly) {
