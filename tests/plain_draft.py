@@ -150,9 +150,10 @@ def beam_scores(logits, scores):
     for b in range(x.shape[0]):
         for w in range(x.shape[1]):
             if s[b, w] > -math.inf:
-                L = lse64(x[b, w])
-                if L > -math.inf:
-                    out[b, w] = s[b, w] - L + (x[b, w] + 0.0)
+                m = x[b, w].max()  # differences first: rows of any magnitude
+                if m > -math.inf:
+                    d = x[b, w] - m
+                    out[b, w] = (s[b, w] - torch.log(torch.exp(d).sum())) + d
     return out
 
 

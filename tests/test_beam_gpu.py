@@ -321,3 +321,20 @@ def test_binding_and_long_way_agree():
                              torch.zeros((1, 65), device="cuda"), 4)
     import numpy as np
     assert torch.equal(api.spec_beam_select(x, s, np.int64(9)).tokens, a.tokens)
+
+
+@pytest.mark.parametrize("W", [4, 16])
+def test_lowest_value_masks(W):
+    """Masks of the type's lowest value beside ordinary logits, and whole rows of it: their
+    tokens are the last candidates, in order."""
+    x, s = case(2, W, 2000, F32, 80 + W)
+    x[0, :, 40:] = torch.finfo(F32).min
+    x[1] = torch.finfo(F32).min
+    out = api.spec_beam_select(x, s, 128)
+    assert not bool(out.status.any())
+    first = min(128, 40 * W)
+    plain.check_beam(x[:1, :, :40].contiguous(), s[:1], first, api.BeamOutputs(
+        out.tokens[:1, :first], out.parents[:1, :first], out.scores[:1, :first]))
+    best = int(s[1].argmax())  # uniform rows: log-probability -log V each
+    assert abs(float(out.scores[1, 0]) - float(s[1].max()) + math.log(2000)) < 1e-4
+    assert out.parents[1].tolist() == [best] * 128 and out.tokens[1].tolist() == list(range(128))

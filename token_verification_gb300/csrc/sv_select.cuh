@@ -33,7 +33,8 @@ struct TopParams {
   int* out_parents;     // beams: [B, n]
   float* out_values;    // logits [rows, n], scores [B, n]
   float* out_lse;       // record: [B*P]
-  double* out_off;      // row kernel for beams: [B*W] score - lse (-inf: no candidates, NaN: bad)
+  double* out_off;      // row kernel for beams: [B*W] offsets (-inf: no candidates, NaN: bad)
+  float* out_max;       // and the rows' maxes
   int* out_status;
   int P;                // record: rows per request
   int W;                // rows per cluster (record: 1)
@@ -55,7 +56,8 @@ cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long
                             cudaStream_t stream);
 // The n best of each request's W row selections.
 cudaError_t launch_beam_merge(const TopParams& p, const int* ids, const float* values,
-                              const double* off, int B, cudaStream_t stream);
+                              const double* off, const float* row_max, int B,
+                              cudaStream_t stream);
 
 namespace {
 
@@ -126,11 +128,6 @@ __device__ __forceinline__ uint32_t gt_bf16x2(uint32_t a, uint32_t b) {
   asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t eq_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("set.eq.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -189,9 +186,25 @@ __device__ float unit_bound(Select& s, const uint16_t* unit, int units, int n) {
   return of_ordered(s.bound);
 }
 
+// A beam's continuation scores offset + (l - m) in 64 bits, with m the row's max
+// and offset = score - log of the row's sum in m's frame (as a pair): l - m
+// first, so that rows of any magnitude keep their scores.
+__device__ __forceinline__ double row_offset(float score, float2 log_sum) {
+  return (double)score - ((double)log_sum.x + (double)log_sum.y);
+}
+__device__ __forceinline__ double beam_score(double off, float m, float l) {
+  return off + ((double)l - (double)m);
+}
+__device__ __forceinline__ float beam_score_down(float off_down, float m, float l) {
+  return __fadd_rd(off_down, __fadd_rd(l, -m));
+}
+
+constexpr int ring_bytes(int warps) { return Ring::kWarpBytes * warps; }
+
 template <bool kBeam>
-__device__ __forceinline__ void set_candidate(Lists& s, int o, float l, double off, int idx) {
-  s.key[o] = kBeam ? ordered(off + (double)l)
+__device__ __forceinline__ void set_candidate(Lists& s, int o, float l, double off, float m,
+                                              int idx) {
+  s.key[o] = kBeam ? ordered(beam_score(off, m, l))
                    : ((unsigned long long)ordered(l) << 32) | (uint32_t)~idx;
   s.idx[o] = idx;
 }
@@ -200,7 +213,7 @@ __device__ __forceinline__ void set_candidate(Lists& s, int o, float l, double o
 // from `at` on (a call of the group); returns how many.
 template <typename T, bool kBeam, int kBar>
 __device__ int select_row_slow(Select& s, Lists& ls, const T* row, int V, int n, double off,
-                               int base, int at) {
+                               float m, int base, int at) {
   const int t = threadIdx.x % kTopThreads;
   auto key_of = [&](int j) {  // (logit in order, index from the end), 0 if not finite
     const float l = j < V ? load_logit(row, j) : -INFINITY;
@@ -247,7 +260,7 @@ __device__ int select_row_slow(Select& s, Lists& ls, const T* row, int V, int n,
     const unsigned long long k = key_of(j0 + t);
     if (k != 0 && k >= cut) {
       const int o = atomicAdd(&s.pick[3], 1);
-      set_candidate<kBeam>(ls, o, load_logit(row, j0 + t), off, base + j0 + t);
+      set_candidate<kBeam>(ls, o, load_logit(row, j0 + t), off, m, base + j0 + t);
     }
   }
   group_sync<kBar>();
@@ -458,13 +471,6 @@ __device__ __forceinline__ float row_sum(const float2* parts, int n, float c, fl
   sum = warp_sum_pair(a.y * to_frame(a.x, m, c) + b.y * to_frame(b.x, m, c));
   return m;
 }
-
-// score - lse in 64 bits, with log of the sum as a pair.
-__device__ __forceinline__ double row_offset(float score, float m, float2 log_sum) {
-  return ((double)score - (double)m) - ((double)log_sum.x + (double)log_sum.y);
-}
-
-constexpr int ring_bytes(int warps) { return Ring::kWarpBytes * warps; }
 
 // Units of `fold` threads: two per kept candidate, counting only the threads
 // that a slice gives anything (its 2 KB chunks go to the warps in turn); padded

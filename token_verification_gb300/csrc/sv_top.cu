@@ -10,9 +10,13 @@
 // receiver's mbarrier) and works out offsets and bound for itself; the
 // candidates go to the leader CTA's list, before a cluster barrier.
 //
-// A beam's candidates compare by score = offset + logit with offset =
-// scores[w] - lse[w] in 64 bits; a record's offset is 0.  Bounds are in fp32
-// rounded down, which can only lengthen the list.
+// It is bound by the chain of its steps - launch, stream, exchange, bound, reload,
+// sort -, not by bytes: 1 to 8 rows of 32000 to 128256 bf16 logits take 6.4 to 6.9
+// us (k = 32), four beams of 32000 7.6 us. Ordering cluster barriers in place of
+// the counted stores cost 0.7 us.
+//
+// A beam's candidates compare by their scores in 64 bits, a record's by their
+// logits.  Bounds are in fp32 rounded down, which can only lengthen the list.
 #include <string.h>
 
 #include <algorithm>
@@ -27,7 +31,8 @@ constexpr int kMaxItems = 64;         // (row, slice) items per cluster
 struct alignas(16) TopShared {
   alignas(16) float2 part[kMaxItems][kTopWarps];  // per item and warp: {max, sum of 2^((l - max) c)}
   alignas(16) uint16_t unit[kMaxUnits];  // unit maxes, item by item: bf16 rounded down
-  double off[SV_MAX_BEAMS];           // beams: score - lse of each row (-inf: no candidates)
+  double off[SV_MAX_BEAMS];           // beams: each row's offset (-inf: no candidates)
+  float max[SV_MAX_BEAMS];            // and its max
   float off_down[SV_MAX_BEAMS];       // the same rounded down
   float thr[SV_MAX_BEAMS];            // the lowest logit a candidate of the row can have
   float lse;                          // record
@@ -147,8 +152,9 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
         atomicOr(&s.sel.bad, SV_REQ_BAD_LOGITS);
       if (kBeam) {
         double off = -INFINITY;
-        if (!dead && m != -INFINITY) off = row_offset(score, m, l);
+        if (!dead && m != -INFINITY) off = row_offset(score, l);
         s.off[w] = off;
+        s.max[w] = m;
         s.off_down[w] = __double2float_rd(off);
       } else {
         s.lse = m == -INFINITY ? -INFINITY : m / p.T + (l.x + l.y);
@@ -171,22 +177,26 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   const int units = items * p.upi;
   if (kBeam) {  // the units' scores, rounded down
     for (int u = t; u < units; u += kTopThreads) {
-      const float l = bf16_lo(s.unit[u]), off = s.off_down[u / (p.upi * p.slices)];
-      s.unit[u] = l == -INFINITY || off == -INFINITY ? 0xff80u : down_bf16(__fadd_rd(off, l));
+      const int w = u / (p.upi * p.slices);
+      const float l = bf16_lo(s.unit[u]), off = s.off_down[w];
+      s.unit[u] = l == -INFINITY || off == -INFINITY
+                      ? 0xff80u
+                      : down_bf16(beam_score_down(off, s.max[w], l));
     }
   }
   const float bound = unit_bound<0>(s.sel, s.unit, units, p.n);
   if (kBeam) {
     for (int w = t; w < p.W; w += kTopThreads) {
       const double off = s.off[w];
-      // below it, off + l rounds below the bound (the slack covers the roundings); -inf never
-      // passes: at least the lowest finite value
+      // below it, the score rounds below the bound (the slack covers the roundings); -inf
+      // never passes: at least the lowest finite value
       s.thr[w] = off == -INFINITY ? INFINITY
                  : bound == -INFINITY
                      ? -FLT_MAX
                      : fmaxf(-FLT_MAX,
-                             __double2float_rd(((double)bound - off) -
-                                               1e-7 * (fabs((double)bound) + fabs(off))));
+                             __double2float_rd((((double)bound - off) -
+                                                1e-7 * (fabs((double)bound) + fabs(off))) +
+                                               (double)s.max[w]));
     }
     __syncthreads();
   }
@@ -227,7 +237,8 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
       const double off = kBeam ? s.off[w] : 0.0;
       if (off == -INFINITY) continue;
       const T* row = reinterpret_cast<const T*>(p.logits) + (grp * p.W + w) * (long long)p.V;
-      const int got = select_row_slow<T, kBeam, 0>(s.sel, ls, row, p.V, p.n, off, w * p.V, count);
+      const int got = select_row_slow<T, kBeam, 0>(s.sel, ls, row, p.V, p.n, off,
+                                                   kBeam ? s.max[w] : 0.f, w * p.V, count);
       // keep the n best of the rows so far (at most 2 n <= 256 entries, one a thread)
       const int total = count + got;
       rank_list<kBeam, 0>(ls, total);
@@ -245,7 +256,8 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
     if (kBeam) {
       for (int i = t; i < count; i += kTopThreads) {
         const int idx = ls.idx[i];
-        set_candidate<true>(ls, i, __uint_as_float((uint32_t)ls.key[i]), s.off[idx / p.V], idx);
+        const int w = idx / p.V;
+        set_candidate<true>(ls, i, __uint_as_float((uint32_t)ls.key[i]), s.off[w], s.max[w], idx);
       }
       __syncthreads();
     }
@@ -387,8 +399,8 @@ size_t spec_beam_workspace_size(sv_dtype dtype, int B, int W, int V, int n) {
       W > SV_MAX_BEAMS || V < 1 || V > SV_MAX_V || n < 1 || n > SV_MAX_TOP)
     return 0;
   const size_t rows = (size_t)B * W;
-  // each row's offset, then its n best logits and their tokens
-  return beams_by_rows(dtype, B, W, V) ? rows * (sizeof(double) + 8 * (size_t)n) : 0;
+  // each row's offset and max, then its n best logits and their tokens
+  return beams_by_rows(dtype, B, W, V) ? rows * (16 + 8 * (size_t)n) : 0;
 }
 
 sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out_tokens,
@@ -419,13 +431,15 @@ sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out
   if (need) {  // each beam's n best, then the requests'
     const long long rows = (long long)B * W;
     double* off = static_cast<double*>(workspace);
-    float* values = reinterpret_cast<float*>(off + rows);
+    float* row_max = reinterpret_cast<float*>(off + rows);
+    float* values = row_max + 2 * rows;
     int* ids = reinterpret_cast<int*>(values + rows * n);
     TopParams q = p;
     q.W = 1;
     q.out_ids = ids;
     q.out_values = values;
     q.out_off = off;
+    q.out_max = row_max;
     const bool aligned = set_span(q, dtype, rows);
     if (launch_top_rows(dtype, aligned, q, rows, st) != cudaSuccess) return SV_ERR_CUDA;
     p.W = W;
@@ -433,7 +447,7 @@ sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out
     p.out_parents = out_parents;
     p.out_values = out_scores;
     p.out_status = out_status;
-    return launch_beam_merge(p, ids, values, off, B, st) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    return launch_beam_merge(p, ids, values, off, row_max, B, st) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
   }
   p.out_ids = out_tokens;
   p.out_parents = out_parents;

@@ -98,43 +98,6 @@ __device__ __forceinline__ uint4 load_group(const T* row, int j, int V, const Ro
   return v;
 }
 
-// N groups of a row, group u at element j + u * step, those at or past `end`
-// (a multiple of VEC, or the row's end V) filled with -inf.  When all of them
-// lie inside the tensor their loads are issued together, without a branch
-// between them; the few threads at a tensor's or row's edge go one by one.
-template <typename T, bool kAligned, int N>
-__device__ __forceinline__ void load_groups(uint4 (&g)[N], const T* row, int j, int step, int end,
-                                            int V, const RowSpan& span) {
-  constexpr int VEC = Group<T>::VEC;
-  if (kAligned) {  // V is a multiple of VEC
-#pragma unroll
-    for (int u = 0; u < N; ++u)
-      g[u] = j + u * step < end ? load128(row + j + u * step) : Lane<T, VEC>::pad();
-    return;
-  }
-  const char* p = reinterpret_cast<const char*>(row + j);
-  const uint32_t r = (uint32_t)(uintptr_t)p & 15u;  // the same for the whole row
-  const int last = j + (N - 1) * step;
-  const char* a = p - r;
-  if (last + VEC <= end && a >= span.first &&
-      a + (long long)(N - 1) * step * (int)sizeof(T) + 32 <= span.last) {
-#pragma unroll
-    for (int u = 0; u < N; ++u) g[u] = load128(a + (long long)u * step * (int)sizeof(T));
-    if (r != 0) {
-      uint4 b[N];
-#pragma unroll
-      for (int u = 0; u < N; ++u) b[u] = load128(a + (long long)u * step * (int)sizeof(T) + 16);
-#pragma unroll
-      for (int u = 0; u < N; ++u) g[u] = shift_pair(g[u], b[u], r);
-    }
-    return;
-  }
-#pragma unroll
-  for (int u = 0; u < N; ++u)
-    g[u] = j + u * step < end ? load_group<T, false>(row, j + u * step, V, span)
-                              : Lane<T, VEC>::pad();
-}
-
 // Unsigned keys in the order of the values (-0.0 counts as +0.0).
 __device__ __forceinline__ uint32_t ordered(float v) {
   uint32_t b = __float_as_uint(v);
