@@ -74,14 +74,16 @@ def check_top(logits, k, T, out, lens=None):
 
 
 def distill_row(s, ids, t, lse, T):
-    """(loss, gradient by s, p by token, share) of one row in float64: `share`
-    is each token's part of the mass outside the record."""
+    """(loss, size of its terms, gradient by s, q, p by token, share, p_rest) of one row
+    in float64: `share` is each token's part of the student's mass outside the record."""
     V = s.numel()
     use = ids >= 0
-    ids, t = ids[use].long(), t[use] / T
-    x = s / T
+    ids, t = ids[use].long(), t[use]
+    x = (s - s.max()) / T  # differences first: rows of any magnitude
     L = lse64(x)
-    logp = t - (lse64(t) if lse is None else lse)
+    top = max(float(t.max()), -torch.finfo(torch.float32).max)
+    t = (t - top) / T
+    logp = t - (lse64(t) if lse is None else lse - top / T)
     p = torch.exp(logp)
     p_rest = 0.0 if lse is None or len(ids) >= V else max(0.0, 1.0 - float(p.sum()))
     logq = x - L
@@ -90,9 +92,11 @@ def distill_row(s, ids, t, lse, T):
     terms = torch.where(p > 0, p * (logp - logq[ids]), torch.zeros_like(p))
     loss, size = float(terms.sum()), float(terms.abs().sum())
     share = torch.zeros(V, dtype=torch.float64)
-    rest = lse64(logq[outside]) if bool(outside.any()) else -math.inf
+    rest = float(x[outside].max()) if bool(outside.any()) else -math.inf
     if rest > -math.inf:
-        share[outside] = torch.exp(logq[outside] - rest)
+        d = x[outside] - rest
+        share[outside] = torch.exp(d - lse64(d))
+        rest += lse64(d) - L
     if p_rest > 0:
         d = p_rest * (math.log(p_rest) - rest)
         loss, size = loss + d, size + abs(d)
@@ -100,7 +104,7 @@ def distill_row(s, ids, t, lse, T):
     pv = torch.zeros(V, dtype=torch.float64)
     pv[ids] = p
     grad = (q - pv - p_rest * share) / T
-    return loss, size, grad, q, pv, share
+    return loss, size, grad, q, pv, share, p_rest
 
 
 def check_distill(student, ids, t, lse, T, grad_loss, lens, loss, grad, status=None):
@@ -118,7 +122,7 @@ def check_distill(student, ids, t, lse, T, grad_loss, lens, loss, grad, status=N
                 assert loss is None or float(loss[b, i]) == 0.0, where
                 assert grad is None or not bool(grad[b, i].any()), where
                 continue
-            L, size, dg, q, p, share = distill_row(
+            L, size, dg, q, p, share, p_rest = distill_row(
                 s[b, i], ids[b, i], t[b, i], None if lse is None else float(lse[b, i]), T)
             if loss is not None:
                 # each log q within SUM, each log p within 2 u |t / T| and p within
@@ -133,8 +137,11 @@ def check_distill(student, ids, t, lse, T, grad_loss, lens, loss, grad, status=N
                 g = float(grad_loss[b, i])
                 got = f64(grad[b, i])
                 want = g * dg
-                # q within 2 SUM, p within 2^-20, p_rest = 1 - sum p within 2^-20 in all
-                tol = abs(g) / T * (2 * SUM * q + 2.0 ** -20 * (p + share))
+                # q within 2 SUM, p within 2^-20, p_rest = 1 - sum p within 2^-20 in all;
+                # share is a weight over a sum of weights as q is: it is within 2 SUM too,
+                # far below the max as well (2^-126: 126 ln 2 u = 5e-6), and p_rest takes that
+                # into p_rest * share
+                tol = abs(g) / T * (2 * SUM * (q + p_rest * share) + 2.0 ** -20 * (p + share))
                 tol = tol * 1.01 + step * want.abs() * 1.01 + 1e-37
                 off = (got - want).abs()
                 j = int((off - tol).argmax())

@@ -305,3 +305,61 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a.loss, b.loss) and torch.equal(a.grad, b.grad)
+
+
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("shift", [0.0, 2.0 ** 10, -(2.0 ** 20)])
+def test_shifted_rows(tail, shift):
+    """Student and teacher far from zero and from each other: the loss is of the differences
+    (on a grid that the shifted rows hold exactly)."""
+    T = 2.0 ** -7 if shift else 1.0
+    s, ids, t, lse, gl = case(2, 3, 1500, 24, F32, 1.0, tail, 13)
+    s, t = (s * 8).round() / 8, (t * 8).round() / 8
+    if tail:  # some log-sum-exp above the record's own
+        lse = (t.double().amax(-1) / T + math.log(24)).ceil().float()
+    one = check(s, ids, t, lse, T, gl)
+    far = check(s + shift, ids, t, lse, T, gl)
+    assert torch.equal(one.loss, far.loss) and torch.equal(one.grad, far.grad)
+    if not tail:
+        far = check(s, ids, t - shift, None, T, gl)
+        assert torch.equal(one.loss, far.loss) and torch.equal(one.grad, far.grad)
+
+
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("T", [1.0, 0.5])
+def test_lowest_value_students(T, tail):
+    """Masks of the type's lowest value: in a whole row, at a recorded token and its like
+    outside the record, and everywhere outside the record."""
+    low = torch.finfo(F32).min
+    s, ids, t, lse, gl = case(1, 3, 2000, 10, F32, T, tail, 14)
+    s[0, 0] = low
+    s[0, 1, 500:] = torch.where(s[0, 1, 500:] > 0, s[0, 1, 500:], torch.full_like(s[0, 1, 500:], low))
+    s[0, 1, ids[0, 1, 3].long()] = low
+    keep = s[0, 2, ids[0, 2].long()].clone()
+    s[0, 2] = low
+    s[0, 2, ids[0, 2].long()] = keep
+    out = api.spec_distill(s, ids, t, T, top_lse=lse, grad_loss=gl)
+    back = api.spec_distill_grad(s, ids, t, T, out.stats, gl, top_lse=lse)
+    x, d, r = plain.f64(s), ids.cpu(), plain.f64(t)
+    plain.check_distill(s, ids, t, lse, T, gl, None, None, out.grad, out.status)
+    plain.check_distill(s, ids, t, lse, T, gl, None, None, back)
+    for i in range(3):
+        L, size = plain.distill_row(x[0, i], d[0, i], r[0, i],
+                                    float(lse[0, i]) if tail else None, T)[:2]
+        # each p and the remainder of them within 2^-20, times the largest |log q|
+        worst = -low / T if size > 1e30 else 0.0
+        tol = 2.0 ** -20 * (size + 32 + worst) + 2 * plain.SUM
+        assert abs(float(out.loss[0, i]) - L) <= tol, (i, out.loss, L, tol)
+    assert float(out.loss[0, 0]) < 40 and float(out.loss[0, 1]) > 1e30
+    assert (float(out.loss[0, 2]) > 1e30) == tail
+
+
+@pytest.mark.parametrize("T", [1e-40, 1e-38, 1e-20, 1e30])
+def test_extreme_temperatures(T):
+    """The largest and smallest: both sides certain of the same token, or both uniform."""
+    T = float(torch.tensor(T, dtype=F32))  # as the kernel gets it
+    s, ids, t, _, gl = case(1, 2, 1000, 6, F32, 1.0, False, 15)
+    best = ids[0, :, 0].long()
+    s[0, torch.arange(2), best] = 50.0
+    both = check(s, ids, t, None, T, gl)
+    assert bool(torch.isfinite(both.loss).all()) and bool(torch.isfinite(both.grad).all())

@@ -22,6 +22,7 @@
 // slices that wait: 38 KB a CTA, five CTAs an SM, each from its copy's issue to
 // its last store. Slices of 76 KB in clusters of four took 141 us, of 25 KB in
 // eight (a 50001-token fp32 row) the same as of 50 KB in four.
+#include <float.h>
 #include <string.h>
 
 #include "../../include/spec_verify.h"
@@ -67,7 +68,9 @@ struct alignas(16) DistillShared {
   float sv[SV_MAX_TOP];          // the student's logits at its tokens
   int bad, late, twice;
   int used;                      // bit 0: an entry is used, bit 1: with a finite logit
-  float norm, norm_lo;           // the teacher's log-sum-exp: log p_j = t_j / T - norm
+  float t_max;                   // the record's largest finite logit (0: none)
+  float norm, norm_lo;           // the teacher's log-sum-exp - t_max / T:
+                                 // log p_j = (t_j - t_max) / T - norm
   float p_sum, p_rest;           // the record's mass and 1 - it
   float top_m;                   // the student's max on the record (NaN: unusable)
   float2 top_z;                  // and its sum there in that frame (hi, lo)
@@ -230,16 +233,17 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
       used += j < p.k && s.id[j] >= 0 ? 1 : 0;
       m = fmaxf(m, v[q]);
     }
+    m = frame_of(warp_max(m));
     Pair norm;
-    norm.add(lse);
-    if (!p.top_lse) {  // the record's own: max / T + log of the sum in its frame
-      m = warp_max(m);
+    if (p.top_lse) {
+      norm.add(lse);
+      if (is_finite(m / p.T)) add_ratio(norm, m, p, -1.f);
+      else norm.hi = m > 0.f ? -INFINITY : INFINITY;
+    } else {  // the record's own
       float z = 0.f;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) z += expf((v[q] - frame_of(m)) * p.inv_t);
+      for (int q = 0; q < kPer; ++q) z += expf((v[q] - m) * p.inv_t);
       const float2 l = log_pair(warp_sum_pair(z));
-      norm = Pair();
-      add_ratio(norm, frame_of(m), p, 1.f);
       norm.add(l.x);
       norm.add(l.y);
     }
@@ -248,13 +252,14 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
     for (int q = 0; q < kPer; ++q) {
       const int j = q * kWarp + t;
       const float pj =
-          v[q] == -INFINITY ? 0.f : expf(fmaf(v[q], p.inv_t, -norm.hi) - norm.lo);
+          v[q] == -INFINITY ? 0.f : expf(fmaf(v[q] - m, p.inv_t, -norm.hi) - norm.lo);
       if (j < p.k) s.p[j] = pj;
       sum += pj;
     }
     const float2 total = warp_sum_pair(sum);
     used = (int)__reduce_add_sync(0xffffffffu, (unsigned)used);
     if (t == 0) {
+      s.t_max = m;
       s.norm = norm.hi;
       s.norm_lo = norm.lo;
       s.p_sum = total.x + total.y;
@@ -290,10 +295,10 @@ __device__ Sums row_sums(const DistillShared& s, int C, float c) {
 }
 
 // The loss of a row, by one warp:
-//   sum_j p_j ((t_j - s_j) / T - K) + p_rest (log p_rest - log q_rest)
-// with K = norm - (M / T + log Z).  The differences are taken before anything
-// is rounded to their terms' size: where student and teacher agree the loss
-// is far below its terms.
+//   sum_j p_j (((t_j - t_max) - (s_j - M)) / T - K) + p_rest (log p_rest - log q_rest)
+// with K = norm - log Z.  The differences are taken before anything is rounded
+// to their terms' size: where student and teacher agree the loss is far below
+// its terms, and neither need be near zero.
 __device__ float row_loss(const DistillShared& s, const DistillParams& p, const Sums& r) {
   const int lane = lane_id();
   const bool rest = r.m != -INFINITY;
@@ -305,17 +310,21 @@ __device__ float row_loss(const DistillShared& s, const DistillParams& p, const 
                                 __shfl_sync(0xffffffffu, mine.y, 1));
   Pair K;
   K.add(s.norm);
-  add_ratio(K, r.M, p, -1.f);
   K.add(-lz.x);
   K.add(-lz.y);
   K.add(s.norm_lo);
   const float k = K.value();
   float loss = 0.f;
   for (int j = lane; j < p.k; j += kWarp)
-    if (s.p[j] > 0.f) loss = fmaf(s.p[j], (s.t[j] - s.sv[j]) * p.inv_t - k, loss);
+    if (s.p[j] > 0.f) {
+      const float d = (s.t[j] - s.t_max) - (s.sv[j] - r.M), x = d * p.inv_t;
+      // (a masked token of the type's lowest value may pass the range before p_j counts)
+      loss = is_finite(x) ? fmaf(s.p[j], x - k, loss) : fmaf(s.p[j] * p.inv_t, d, loss);
+    }
   loss = warp_sum(loss);
   if (s.p_rest > 0.f) {
     if (!rest) return INFINITY;
+    if (!is_finite((r.M - r.m) / p.T)) return fmaf(s.p_rest * p.inv_t, r.M - r.m, loss);
     // a remainder that is most of the mass: its logarithm from what is left of it
     const float lp = s.p_sum < 0.5f ? log1pf(-s.p_sum) : logf(s.p_rest);
     Pair d;  // else log q_rest = log S + (m - M) / T - log Z, whatever underflowed
@@ -531,7 +540,9 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
     fill_bytes(grad + x0, x1 - x0);
     return;
   }
-  const float scale = p.grad_loss[row] / p.T;
+  // (past the range at the smallest temperatures: 0 gradients stay 0)
+  const float g = p.grad_loss[row];
+  const float scale = is_finite(g) ? fminf(fmaxf(g / p.T, -FLT_MAX), FLT_MAX) : g / p.T;
   const float beta = st.y * scale;
   const float my_grad = (ex2((my_v - st.z) * p.cc) * st.w - (t < p.k ? s.p[t] : 0.f)) * scale;
   if (((uintptr_t)grad & 15u) == (uint32_t)r) {
@@ -634,7 +645,8 @@ DistillParams distill_params(const void* student, const int32_t* ids, const floa
   p.cc = exponent_scale(temperature);
   p.T = temperature;
   p.wait_ns = wait_limit_ns();
-  p.inv_t = (float)(1.0 / (double)temperature);
+  const double inv = 1.0 / (double)temperature;
+  p.inv_t = inv < (double)FLT_MAX ? (float)inv : FLT_MAX;
   return p;
 }
 

@@ -134,8 +134,10 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
         send16(in_cta(smem_u32(from), c), in_cta(smem_u32(&s.part_bar), c),
                *reinterpret_cast<const float4*>(from));
     }
-    if (warp == 0 && !mbar_wait_cluster(smem_u32(&s.part_bar), 0, kWaitLimitNs))
+    if (warp == 0 && !mbar_wait_cluster(smem_u32(&s.part_bar), 0, kWaitLimitNs)) {
       s.sel.bad = SV_REQ_TIMEOUT;  // a peer has failed
+      cluster.map_shared_rank(&s, 0)->sel.overflow = 1;  // the leader reads all rows itself
+    }
     __syncthreads();
   }
 
@@ -167,7 +169,8 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
     if (!kBeam) p.out_lse[grp] = bad ? qnan() : s.lse;
     if (p.out_status) p.out_status[grp] = bad;
   }
-  if (bad) {  // the same in every CTA
+  if (bad) {  // (the same in every CTA, or some did not get their parts)
+    if (C > 1) cluster.sync();
     if (rank == 0)
       for (int j = t; j < p.n; j += kTopThreads) write_slot<kBeam>(p, grp, j, 0, -1);
     return;

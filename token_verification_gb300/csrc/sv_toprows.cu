@@ -99,7 +99,10 @@ __device__ long long next_live(RowShared& s, const TopParams& p, long long row, 
         mbar_arrive_expect_tx(smem_u32(&s.bar), 16);
         ask_for_cta(smem_u32(&s.answer), smem_u32(&s.bar));
       }
-      if (!mbar_wait(smem_u32(&s.bar), asked++ & 1)) s.late = 1;
+      // (the limit twice: see mbar_wait_cluster)
+      if (!mbar_wait(smem_u32(&s.bar), asked & 1) && !mbar_wait(smem_u32(&s.bar), asked & 1))
+        s.late = 1;
+      ++asked;
       group_sync<kBarSelect>();
       if (s.late) return -1;
       row = taken_cta(smem_u32(&s.answer));
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParam
       bar_sync(kBarFull + b, kRowThreads);
       select_row<T, kAligned>(s, ls, s.slot[b], row, tables + b * table, p, span);
       bar_arrive(kBarEmpty + b, kRowThreads);
-      // a device fault: the queue did not answer in two seconds
+      // a device fault: the queue did not answer in four seconds
       if (s.late && t == 0) {
         if (p.out_off) p.out_off[row] = (double)qnan();
         else if (p.out_status) p.out_status[row] = SV_REQ_TIMEOUT;

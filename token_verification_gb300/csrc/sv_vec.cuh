@@ -343,7 +343,8 @@ __device__ __forceinline__ void send16(uint32_t addr, uint32_t bar, const float4
       "r"(__float_as_uint(v.w)), "r"(bar)
       : "memory");
 }
-// mbar_wait for what other CTAs sent.
+// mbar_wait for what other CTAs sent, with the limit twice: of a context that was
+// switched out as a whole, the clock alone goes on.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
                                                   unsigned long long limit_ns) {
   auto arrived = [&]() {
@@ -358,12 +359,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     return ok != 0;
   };
   if (arrived()) return true;
-  const unsigned long long t0 = global_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (arrived()) return true;
-    if (global_ns() - t0 > limit_ns) return false;
+  for (int turn = 0; turn < 2; ++turn) {
+    const unsigned long long t0 = global_ns();
+    do {
+      for (int i = 0; i < 64; ++i)
+        if (arrived()) return true;
+    } while (global_ns() - t0 <= limit_ns);
   }
+  return false;
 }
 
 // hi + lo, |lo| about half a step of hi: sums of a few fp32 values without
@@ -396,8 +399,8 @@ __device__ __forceinline__ float2 warp_sum_pair(float x) {
   return make_float2(hi, lo);
 }
 
-// log(hi + lo) as an exact multiple of the leading bits of ln 2 plus a float
-// below 0.36 in size: good to about 5e-8 without 64-bit logarithms, which
+// log(hi + lo) as an exact multiple of the leading bits of ln 2 (Cody and Waite
+// 1980) plus a float below 0.36 in size: good to about 5e-8 without 64-bit logarithms, which
 // cost microseconds here.  1 <= hi < 2^31.
 __device__ __forceinline__ float2 log_pair(float2 s) {
   const uint32_t b = __float_as_uint(s.x);
@@ -416,12 +419,6 @@ __device__ __forceinline__ float2 log_pair(float2 s) {
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
