@@ -61,7 +61,7 @@ def build_binding(cc: str) -> str:
            "-I" + sysconfig.get_paths()["include"], "-I" + cuda_inc,
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + torch_lib,
            "-Wl,-rpath," + torch_lib, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
-           "-ltorch_python"]
+           "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for binding.cpp:\n%s%s" % (r.stdout, r.stderr))

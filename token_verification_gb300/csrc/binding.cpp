@@ -13,7 +13,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -93,7 +93,7 @@ T* data(const Tensor* t) {
 }
 
 Tensor make(c10::Device d, at::ScalarType type, at::IntArrayRef shape) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(d));
+  return Tensor(at::detail::empty_cuda(shape, type, d, std::nullopt));
 }
 
 sv_stream_t stream_of(c10::Device d) {
