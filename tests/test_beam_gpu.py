@@ -338,3 +338,16 @@ def test_lowest_value_masks(W):
     best = int(s[1].argmax())  # uniform rows: log-probability -log V each
     assert abs(float(out.scores[1, 0]) - float(s[1].max()) + math.log(2000)) < 1e-4
     assert out.parents[1].tolist() == [best] * 128 and out.tokens[1].tolist() == list(range(128))
+
+
+@pytest.mark.parametrize("W", [4, 16])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scores_that_cancel(W, dtype):
+    """Every other beam has a score of 2^24 and a first token 2^24 above all others: the other
+    tokens' scores are differences of those, and compete with the other beams'."""
+    x, s = case(3, W, 500, dtype, 90 + W)
+    x[:, ::2, 0] = 2.0 ** 24
+    s[:, ::2] += 2.0 ** 24
+    out = api.spec_beam_select(x, s, 96)
+    assert not bool(out.status.any())
+    plain.check_beam(x, s, 96, out)

@@ -284,31 +284,56 @@ cudaError_t launch_rows(TopParams p, long long rows, cudaStream_t stream) {
                       fixed + 4 * (size_t)p.iters * kRowStreamers, 1, stream, p);
 }
 
-// The n best of a request's W selections: every thread takes the candidates
-// of its stride, and the bound of the thread maxes leaves a list that fits
-// (or, with many equal scores, the rows go in one after the other).
-__global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
-    const TopParams p, const int* __restrict__ ids, const float* __restrict__ values,
-    const double* __restrict__ off, const float* __restrict__ row_max) {
+// The n best of a request's W selections.  Four threads to each of 256 units,
+// whose elements (up to 32) lie at different places of different rows; the
+// bound of the unit maxes leaves a list that fits (or, with many equal scores,
+// the rows go in one after the other).  Bound by the latency of its steps, so a
+// request has 1024 threads: 24 x 32 beams of 50001 fp32 logits, n = 64, both
+// launches, 37.9 us; 48.8 with 256 threads that worked through eight elements each.
+constexpr int kMergeThreads = 1024;
+constexpr int kMergePer = SV_MAX_BEAMS * SV_MAX_TOP / kMergeThreads;  // elements a thread
+
+__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(
+    const TopParams p, const FastDiv div_n, const FastDiv div_w, const int* __restrict__ ids,
+    const float* __restrict__ values, const double* __restrict__ off,
+    const float* __restrict__ row_max) {
   __shared__ Lists ls;
   __shared__ Select sel;
   __shared__ __align__(16) uint16_t unit[kTopThreads];
   __shared__ double s_off[SV_MAX_BEAMS];
   __shared__ float off_down[SV_MAX_BEAMS], s_max[SV_MAX_BEAMS];
-  extern __shared__ float score[];  // W n
   pdl_wait();
   pdl_launch_dependents();
   const long long b = blockIdx.x;
   const int t = threadIdx.x, all = p.W * p.n;
   ids += b * all;
   values += b * all;
+  // Each row's are in descending order: place r of row w is taken for r + w n / W
+  // (mod n), so that a unit's elements, 256 apart, are of all ranks.
+  int row[kMergePer];    // -1: none
+  int place[kMergePer];  // in all rows
+  float v[kMergePer];
+#pragma unroll
+  for (int q = 0; q < kMergePer; ++q) {
+    const uint32_t i = (uint32_t)(4 * q + t % 4) * kTopThreads + t / 4;
+    row[q] = -1;
+    if (i < (uint32_t)all) {
+      const uint32_t w = fast_div(i, div_n);
+      uint32_t r = i - w * p.n + fast_div(w * p.n, div_w);
+      if (r >= (uint32_t)p.n) r -= p.n;
+      row[q] = (int)w;
+      place[q] = (int)(w * p.n + r);
+      v[q] = values[place[q]];
+    }
+  }
+  const double o = t < p.W ? off[b * p.W + t] : 0.0;
+  const float m = t < p.W ? row_max[b * p.W + t] : 0.f;
   if (t == 0) sel.n_cands = sel.bad = 0;
   __syncthreads();
   if (t < p.W) {
-    const double o = off[b * p.W + t];
     s_off[t] = o;
     off_down[t] = __double2float_rd(o);
-    s_max[t] = o == -INFINITY ? 0.f : row_max[b * p.W + t];  // (a row not read has none)
+    s_max[t] = o == -INFINITY ? 0.f : m;  // (a row not read has none)
     if (o != o) atomicOr(&sel.bad, SV_REQ_BAD_LOGITS);
   }
   __syncthreads();
@@ -324,46 +349,36 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
   int count = 0;
   if (!bad) {
     // the scores in fp32, rounded down to -FLT_MAX at least (-inf for an empty slot)
-    for (int i0 = 0; i0 < all; i0 += 8 * kTopThreads) {
-      float v[8];
+    float score[kMergePer], um = -INFINITY;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int i = i0 + q * kTopThreads + t;
-        v[q] = i < all ? values[i] : -INFINITY;
-      }
+    for (int q = 0; q < kMergePer; ++q) {
+      score[q] = -INFINITY;
+      if (row[q] >= 0 && v[q] > -INFINITY)
+        score[q] = fmaxf(beam_score_down(off_down[row[q]], s_max[row[q]], v[q]), -FLT_MAX);
+      um = fmaxf(um, score[q]);
+    }
+    um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
+    um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
+    if (t % 4 == 0) unit[t / 4] = down_bf16(um);
+    __syncthreads();
+    if (t < kTopThreads) unit_bound<kBarSelect>(sel, unit, kTopThreads, p.n);
+    __syncthreads();
+    const float bound = of_ordered(sel.bound);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int i = i0 + q * kTopThreads + t;
-        if (i < all) {
-          const int w = i / p.n;
-          score[i] = v[q] > -INFINITY
-                         ? fmaxf(beam_score_down(off_down[w], s_max[w], v[q]), -FLT_MAX)
-                         : -INFINITY;
+    for (int q = 0; q < kMergePer; ++q) {
+      const float f = score[q];
+      // what stays below the bound with its roundings given back - of the offset, of
+      // l - m, at most |score| + |offset|, and of their sum - is below n others
+      if (f > -INFINITY && fmaf(fabsf(f) + fabsf(off_down[row[q]]), 1e-6f, f) >= bound) {
+        const int at = atomicAdd(&sel.n_cands, 1);
+        if (at < kMaxCands) {
+          ls.key[at] = ordered(beam_score(s_off[row[q]], s_max[row[q]], v[q]));
+          ls.idx[at] = row[q] * p.V + ids[place[q]];
         }
       }
     }
     __syncthreads();
-    // Each row's are in descending order: a thread's are spread over the
-    // positions (steps of 7919, a prime beyond any factor of W n).
-    float um = -INFINITY;
-    const int per = (all + kTopThreads - 1) / kTopThreads;
-    for (int q = t * per; q < min(t * per + per, all); ++q)
-      um = fmaxf(um, score[(unsigned)q * 7919u % (unsigned)all]);
-    unit[t] = down_bf16(um);
-    const float bound = unit_bound<0>(sel, unit, kTopThreads, p.n);
-    for (int i = t; i < all; i += kTopThreads) {
-      const float f = score[i];
-      // what stays below the bound with its roundings given back is below n others
-      if (f > -INFINITY && fmaf(fabsf(f), 1e-6f, f) >= bound) {
-        const int o = atomicAdd(&sel.n_cands, 1);
-        if (o < kMaxCands) {
-          const int w = i / p.n;
-          ls.key[o] = ordered(beam_score(s_off[w], s_max[w], values[i]));
-          ls.idx[o] = w * p.V + ids[i];
-        }
-      }
-    }
-    __syncthreads();
+    if (t >= kTopThreads) return;  // the list is the first 256 threads' from here on
     count = sel.n_cands;
     if (count > kMaxCands) {
       __syncthreads();
@@ -398,7 +413,8 @@ __global__ void __launch_bounds__(kTopThreads) beam_merge_kernel(
       if (r < p.n) write(r, ls.key[i], ls.idx[i]);
     }
   }
-  for (int j = count + t; j < p.n; j += kTopThreads) write(j, 0, -1);
+  if (t < kTopThreads)
+    for (int j = count + t; j < p.n; j += kTopThreads) write(j, 0, -1);
 }
 
 }  // namespace
@@ -425,14 +441,9 @@ cudaError_t launch_top_rows(sv_dtype dtype, bool aligned, TopParams p, long long
 cudaError_t launch_beam_merge(const TopParams& p, const int* ids, const float* values,
                               const double* off, const float* row_max, int B,
                               cudaStream_t stream) {
-  static PerDevice once;
-  const cudaError_t err = per_device(once, nullptr, [&](int&) {
-    return cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                4 * SV_MAX_BEAMS * SV_MAX_TOP);
-  });
-  if (err != cudaSuccess) return err;
-  return launch_early(beam_merge_kernel, (unsigned)B, kTopThreads, 4 * (size_t)p.W * p.n, 1, stream,
-                      p, ids, values, off, row_max);
+  return launch_early(beam_merge_kernel, (unsigned)B, kMergeThreads, 0, 1, stream, p,
+                      make_fastdiv((uint32_t)p.n), make_fastdiv((uint32_t)p.W), ids, values, off,
+                      row_max);
 }
 
 }  // namespace sv
