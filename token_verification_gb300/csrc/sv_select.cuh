@@ -105,9 +105,9 @@ struct Select {
 
 // The candidates.
 struct alignas(16) Lists {
-  unsigned long long key[kMaxCands];  // record: (ordered logit, ~index), a total order;
+  unsigned long long key[kMaxCands + 4];  // record: (ordered logit, ~index), a total order;
                                       // beams: the ordered score, idx = w * V + v
-  int idx[kMaxCands];
+  int idx[kMaxCands + 4];
   int rank[kMaxCands];                // until the list is sorted: the groups to read again
 };
 
@@ -267,41 +267,35 @@ __device__ int select_row_slow(Select& s, Lists& ls, const T* row, int V, int n,
   return s.pick[3] - at;
 }
 
-// Whether entry j of the list comes before an entry of (key, idx).
-template <bool kBeam>
-__device__ __forceinline__ bool before(const Lists& s, int j, unsigned long long key, int idx) {
-  const unsigned long long kj = s.key[j];
-  return kj > key || (kBeam && kj == key && s.idx[j] < idx);
-}
-
 // rank[i] = the number of entries that come before entry i, i < count: the
-// whole group, each entry's comparisons shared by as many threads as there are
-// for all entries.
+// whole group, each entry's comparisons shared by 2^k neighbouring threads, four
+// keys at a time (those past the list are 0: before none). The code runs once
+// or a few times a launch: kept short, as its first run waits for instructions.
 template <bool kBeam, int kBar>
 __device__ void rank_list(Lists& s, int count) {
   const int t = threadIdx.x % kTopThreads;
-  for (int i = t; i < count; i += kTopThreads) s.rank[i] = 0;
+  if (t < 4) s.key[count + t] = 0;
   group_sync<kBar>();
-  if (count <= kTopThreads / 2) {
-    const int ways = count ? kTopThreads / count : 0, way = count ? t / count : 0;
-    const int i = t - way * count;
-    if (way < ways) {
-      const unsigned long long key = s.key[i];
-      const int idx = s.idx[i];
-      int r = 0;
-#pragma unroll 4
-      for (int j = way; j < count; j += ways) r += before<kBeam>(s, j, key, idx) ? 1 : 0;
-      atomicAdd(&s.rank[i], r);
+  const int k = min(5, max(0, __clz(count - 1) - 24)), way = t & ((1 << k) - 1);
+  for (int i0 = 0; i0 < count; i0 += kTopThreads >> k) {
+    const int i = i0 + (t >> k);
+    const unsigned long long key = i < count ? s.key[i] : ~0ull;
+    const int idx = kBeam && i < count ? s.idx[i] : 0;
+    int r = 0;
+#pragma unroll 1
+    for (int j = 4 * way; j < count; j += 4 << k) {
+      const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&s.key[j]);
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s.key[j + 2]);
+      if (kBeam) {
+        const int4 x = *reinterpret_cast<const int4*>(&s.idx[j]);
+        r += (a.x > key || (a.x == key && x.x < idx)) + (a.y > key || (a.y == key && x.y < idx)) +
+             (b.x > key || (b.x == key && x.z < idx)) + (b.y > key || (b.y == key && x.w < idx));
+      } else {
+        r += (a.x > key) + (a.y > key) + (b.x > key) + (b.y > key);
+      }
     }
-  } else {
-    for (int i = t; i < count; i += kTopThreads) {
-      const unsigned long long key = s.key[i];
-      const int idx = s.idx[i];
-      int r = 0;
-#pragma unroll 4
-      for (int j = 0; j < count; ++j) r += before<kBeam>(s, j, key, idx) ? 1 : 0;
-      s.rank[i] = r;
-    }
+    for (int o = 1; o < 1 << k; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    if (i < count && way == 0) s.rank[i] = r;
   }
   group_sync<kBar>();
 }
