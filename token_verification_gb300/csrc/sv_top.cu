@@ -35,7 +35,6 @@ struct alignas(16) TopShared {
   float max[SV_MAX_BEAMS];            // and its max
   float off_down[SV_MAX_BEAMS];       // the same rounded down
   float thr[SV_MAX_BEAMS];            // the lowest logit a candidate of the row can have
-  float lse;                          // record
   unsigned long long part_bar;        // the other CTAs' items have come
   Select sel;
 };
@@ -141,32 +140,38 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
     __syncthreads();
   }
 
-  // Each row's log-sum-exp and offset (every CTA for itself).
+  // Beams: each row's offset (every CTA for itself). A record's log-sum-exp is for
+  // the leader to write when it has loads to wait for; here every warp sees by the
+  // max whether there is anything to select.
   const int parts = p.slices * kTopWarps;  // <= 64
-  for (int w = warp; w < p.W; w += kTopWarps) {
-    float2 sum;
-    const float m = row_sum(&s.part[w * p.slices][0], parts, p.cc, sum);
-    if (lane == 0) {
-      const float2 l = log_pair(sum);
-      const float score = kBeam ? p.scores[grp * p.W + w] : 0.f;
-      const bool dead = kBeam && score == -INFINITY;
-      if (!dead && (m != m || m == INFINITY || score != score || score == INFINITY))
-        atomicOr(&s.sel.bad, SV_REQ_BAD_LOGITS);
-      if (kBeam) {
+  int bad = 0;
+  float m = -INFINITY;
+  if (kBeam) {
+    for (int w = warp; w < p.W; w += kTopWarps) {
+      float2 sum;
+      const float mw = row_sum(&s.part[w * p.slices][0], parts, p.cc, sum);
+      if (lane == 0) {
+        const float2 l = log_pair(sum);
+        const float score = p.scores[grp * p.W + w];
+        const bool dead = score == -INFINITY;
+        if (!dead && (mw != mw || mw == INFINITY || score != score || score == INFINITY))
+          atomicOr(&s.sel.bad, SV_REQ_BAD_LOGITS);
         double off = -INFINITY;
-        if (!dead && m != -INFINITY) off = row_offset(score, l);
+        if (!dead && mw != -INFINITY) off = row_offset(score, l);
         s.off[w] = off;
-        s.max[w] = m;
+        s.max[w] = mw;
         s.off_down[w] = __double2float_rd(off);
-      } else {
-        s.lse = m == -INFINITY ? -INFINITY : m / p.T + (l.x + l.y);
       }
     }
+    __syncthreads();
+    bad = s.sel.bad;
+  } else {
+    m = warp_max_nan(max_nan(lane < parts ? (&s.part[0][0])[lane].x : -INFINITY,
+                             lane + kWarp < parts ? (&s.part[0][0])[lane + kWarp].x : -INFINITY));
+    bad = s.sel.bad | (m != m || m == INFINITY ? SV_REQ_BAD_LOGITS : 0);
   }
-  __syncthreads();
-  const int bad = s.sel.bad;
   if (rank == 0 && t == 0) {
-    if (!kBeam) p.out_lse[grp] = bad ? qnan() : s.lse;
+    if (!kBeam && bad) p.out_lse[grp] = qnan();
     if (p.out_status) p.out_status[grp] = bad;
   }
   if (bad) {  // (the same in every CTA, or some did not get their parts)
@@ -228,6 +233,12 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
       list_group<T, kBeam>(&lead->sel.n_cands, lead_ls, load_group<T, kAligned>(row, j, p.V, span),
                     threshold(w), w * p.V + j);
     }
+  }
+  if (!kBeam && rank == 0 && warp == kTopWarps - 1) {  // the warp with the least to load
+    float2 sum;
+    row_sum(&s.part[0][0], parts, p.cc, sum);
+    const float2 l = log_pair(sum);
+    if (lane == 0) p.out_lse[grp] = m == -INFINITY ? -INFINITY : m / p.T + (l.x + l.y);
   }
   if (C > 1) cluster.sync(); else __syncthreads();
   if (rank != 0) return;
