@@ -17,7 +17,7 @@
 // statistics.
 //
 // What it measured (1024 rows of 152064 bf16 logits, k = 64): loss and gradient
-// 109 us (5.7 TB/s), the loss alone 56 us (5.5 TB/s), the gradient alone 91 us
+// 111 us (5.6 TB/s), the loss alone 56 us (5.6 TB/s), the gradient alone 91 us
 // (6.8 TB/s, the copy rate). What bounds the first two is the shared memory of
 // slices that wait: 38 KB a CTA, five CTAs an SM, each from its copy's issue to
 // its last store. Slices of 76 KB in clusters of four took 141 us, of 25 KB in
