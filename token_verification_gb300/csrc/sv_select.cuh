@@ -313,7 +313,9 @@ __device__ int prune(Select& s, Lists& ls, int count, int n) {
     k[q] = i < count ? ls.key[i] : 0ull;
     ix[q] = i < count ? ls.idx[i] : 0;
   }
-  // three counters in turn: one barrier a round
+  // Three counters in turn, one barrier a round. A round clears the counter of the next
+  // one, last read before the barrier of the round before; the counter of the round
+  // before may still be read by other warps.
   if (tid < 3) s.pick[tid] = 0;
   group_sync<kBar>();
   uint32_t t = 0;
@@ -326,7 +328,7 @@ __device__ int prune(Select& s, Lists& ls, int count, int n) {
     c = __reduce_add_sync(0xffffffffu, c);
     const int next = now == 2 ? 0 : now + 1;
     if (lane_id() == 0) atomicAdd(&s.pick[now], (int)c);
-    if (tid == 0) s.pick[next == 2 ? 0 : next + 1] = 0;
+    if (tid == 0) s.pick[next] = 0;
     group_sync<kBar>();
     if (s.pick[now] >= n) t = at;
     now = next;
