@@ -290,7 +290,11 @@ __device__ Sums row_sums(const DistillShared& s, int C, float c) {
   r.Z = make_float2(Z.hi, Z.lo);
   r.inv_z = r.status ? qnan() : 1.f / Z.value();
   r.q_top = top * r.inv_z;
-  r.beta = r.m == -INFINITY ? 0.f : (rest * r.inv_z - s.p_rest) / r.S.x;
+  // q_rest - p_rest, of the two masses outside the record or of the two on it, whichever
+  // are smaller: the roundings of two masses near 1 would be most of a small difference
+  const float out = s.p_rest > 0.f && s.p_sum + r.q_top < 1.f ? s.p_sum - r.q_top
+                                                              : rest * r.inv_z - s.p_rest;
+  r.beta = r.m == -INFINITY ? 0.f : out / r.S.x;
   return r;
 }
 
