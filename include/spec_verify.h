@@ -425,8 +425,10 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
  *     (a record of all V tokens has no rest);
  *   top_lse NULL: p is the softmax of t / T over the record alone and
  *       loss = sum_j p_j (log p_j - log q_j).
- *   gradient by s_i: (q_i - p_i) / T on recorded tokens, elsewhere
- *     (q_i - p_rest q_i / q_rest) / T, each times grad_loss of the row.
+ *   gradient by s_i: (P q_i - p_i) / T on recorded tokens, elsewhere
+ *     (P q_i - p_rest q_i / q_rest) / T, each times grad_loss of the row, where
+ *     P = sum_j p_j + p_rest: 1, or the record's own mass where that is more than
+ *     top_lse leaves room for or the record holds all V tokens.
  * A term with p = 0 is 0.  A recorded token with p_j > 0 whose student logit is
  * -inf gives loss +inf (the gradient stays finite).
  *
@@ -447,7 +449,8 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
  *               (SV_ERR_ALIAS).
  *   out_status  [B, P] int32 or NULL: SV_REQ_BAD_LOGITS (student NaN, +inf or no
  *               finite logit; a used entry's logit NaN or +inf, or a top_lse beside
- *               it that is not finite, or without one no finite logit),
+ *               it that is not finite or so far below them that sum_j p_j is not,
+ *               or without one no finite logit),
  *               SV_REQ_BAD_TOKEN (a token outside [-1, V) or
  *               given twice), SV_REQ_BAD_DRAFT_LEN, SV_REQ_TIMEOUT.  Such a row has
  *               loss NaN and gradient 0.

@@ -1,5 +1,6 @@
-"""Gradients of spec_distill where they are differences of nearly equal masses,
-against the definition in float64 (needs a GPU).
+"""Gradients and losses of spec_distill where they are differences of nearly
+equal masses and where the record's mass is not 1, against the definition in
+float64 (needs a GPU).
 
 Bounds, u = 2^-24.  A weight is 2^a, a = (l - m) c: the difference, c and the
 product each round, 3 |a| ln 2 u in all, and the exponential is good to 4 u.
@@ -19,8 +20,9 @@ import torch
 from token_verification_gb300 import api
 
 pytestmark = pytest.mark.gpu
-F32 = torch.float32
+BF16, F32 = torch.bfloat16, torch.float32
 U = 2.0 ** -24
+HALF_STEP = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
 
 
 def gen(seed):
@@ -89,3 +91,63 @@ def test_small_differences_of_large_remainders(V, k, T):
     for _, grad in both_ways(s, ids, t, lse, T, gl):
         off = (grad.double() - want).abs() * outside
         assert bool((off <= tol).all()), float((off / tol.clamp(min=1e-300)).max())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V,k,shift", [(1000, 32, -0.4), (1000, 128, -0.05), (50001, 64, -1.0),
+                                       (100, 100, -0.3), (100, 100, 0.3), (64, 64, -0.01)])
+def test_records_of_another_mass(V, k, shift, dtype):
+    """A log-sum-exp that does not fit the record (taken at another temperature, or rounded far
+    from zero): sum p is not 1, and the gradient is still the derivative of the loss."""
+    T = 1.0
+    s, ids, t, lse, gl = case(2, 3, V, k, dtype, T, V + k)
+    if k < V:  # from the record's own log-sum-exp: sum p = e^-shift > 1
+        lse = torch.logsumexp(t.double() / T, -1).float()
+    lse = lse + shift
+    x = s.double().requires_grad_()
+    loss, q, pv, p_rest, share = definition(x, ids, t, lse, T)
+    (gl.double() * loss).sum().backward()
+    want = x.grad
+    mass = (pv.sum(-1) + p_rest)[..., None]
+    assert float((mass - 1).abs().min()) > 0.005
+    scale = (gl.double() / T)[..., None]
+    tol = scale * (2 * ratio(30) * (mass * q + p_rest[..., None] * share) + 100 * U * pv)
+    tol = 1.01 * (tol + HALF_STEP[dtype] * want.abs()) + 1e-37
+    size = (pv * (pv.clamp(min=1e-300).log().abs() + q.log().abs())).sum(-1)
+    for got, grad in both_ways(s, ids, t, lse, T, gl):
+        off = (grad.double() - want).abs()
+        assert bool((off <= tol).all()), float((off / tol).max())
+        assert bool(((got.double() - loss).abs() <= 2 * ratio(30) * (1 + size)).all())
+
+
+def test_differences_of_a_loss_of_another_mass():
+    """Central differences of the loss itself, sum p = e^0.5: as for records of mass 1, the third
+    derivative along a direction of entries at most 1 is at most 8 for each log-sum-exp, times
+    the mass."""
+    T, h = 1.0, 0.05
+    s, ids, t, _, gl = case(2, 3, 1001, 16, F32, T, 9)
+    lse = torch.logsumexp(t.double(), -1).float() - 0.5
+    one = torch.ones_like(gl)
+    grad = api.spec_distill(s, ids, t, T, top_lse=lse, grad_loss=one).grad
+    d = torch.rand(s.shape, generator=gen(10), device="cuda") * 2 - 1
+    up = api.spec_distill(s + h * d, ids, t, T, top_lse=lse).loss.double()
+    down = api.spec_distill(s - h * d, ids, t, T, top_lse=lse).loss.double()
+    want = (up - down) / (2 * h)
+    got = (grad.double() * d.double()).sum(-1)
+    mass = math.exp(0.5)
+    tol = h * h / 6 * 8 * mass + 2 * 2 * ratio(30) * 48 * mass / (2 * h)
+    assert bool(((got - want).abs() <= tol).all()), (got, want, tol)
+
+
+def test_mass_past_the_range():
+    """A log-sum-exp so far below its record that a probability is no fp32 number: a data error."""
+    s, ids, t, lse, gl = case(1, 3, 1000, 8, F32, 1.0, 11)
+    lse[0, 1] -= 200.0
+    out = api.spec_distill(s, ids, t, top_lse=lse, grad_loss=gl)
+    fwd = api.spec_distill(s, ids, t, top_lse=lse)
+    grad = api.spec_distill_grad(s, ids, t, 1.0, fwd.stats, gl, top_lse=lse)
+    for o in (out, fwd):
+        assert o.status.tolist() == [[0, api.REQ_BAD_LOGITS, 0]]
+        assert torch.isnan(o.loss).tolist() == [[False, True, False]]
+    for g in (out.grad, grad):
+        assert not bool(g[0, 1].any()) and bool(g[0, 0].any())

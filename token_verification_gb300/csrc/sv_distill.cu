@@ -11,10 +11,10 @@
 //
 // With m and S the max and the sum of 2^((s_i - m) c) over the tokens outside
 // the record (c = log2(e) / T), the gradient outside the record is
-//   2^((s_i - m) c) * beta * grad_loss / T,   beta = (q_rest - p_rest) / S,
-// and on a recorded token (2^((s_j - M) c) / Z - p_j) * grad_loss / T with M
-// and Z the max and sum over all tokens.  {m, beta, M, 1/Z} are the row's
-// statistics.
+//   2^((s_i - m) c) * beta * grad_loss / T,   beta = (P q_rest - p_rest) / S,
+// and on a recorded token (P 2^((s_j - M) c) / Z - p_j) * grad_loss / T with M
+// and Z the max and sum over all tokens and P = sum p_j + p_rest the teacher's
+// mass.  {m, beta, M, 1/Z} are the row's statistics.
 //
 // What it measured (1024 rows of 152064 bf16 logits, k = 64): loss and gradient
 // 111 us (5.6 TB/s), the loss alone 56 us (5.6 TB/s), the gradient alone 91 us
@@ -72,6 +72,7 @@ struct alignas(16) DistillShared {
   float norm, norm_lo;           // the teacher's log-sum-exp - t_max / T:
                                  // log p_j = (t_j - t_max) / T - norm
   float p_sum, p_rest;           // the record's mass and 1 - it
+  float mass;                    // the teacher's: 1, or a record's whose mass does not fit its log-sum-exp
   float top_m;                   // the student's max on the record (NaN: unusable)
   float2 top_z;                  // and its sum there in that frame (hi, lo)
   struct Sums {                  // the student's sums:
@@ -264,6 +265,7 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
       s.norm_lo = norm.lo;
       s.p_sum = total.x + total.y;
       s.p_rest = p.top_lse && used < p.V ? fmaxf(0.f, (1.f - total.x) - total.y) : 0.f;
+      s.mass = p.top_lse && s.p_rest == 0.f ? s.p_sum : 1.f;
     }
   }
 }
@@ -279,7 +281,9 @@ __device__ Sums row_sums(const DistillShared& s, int C, float c) {
   r.S = warp_sum_pair<kMaxCluster>(v.y * to_frame(v.x, r.m, c));
   r.M = max_nan(r.m, s.top_m);
   r.status = (int)__reduce_or_sync(0xffffffffu, lane < C ? __float_as_uint(v.z) : 0u);
-  if (!is_finite(r.M) && !(r.status & SV_REQ_TIMEOUT)) r.status |= SV_REQ_BAD_LOGITS;
+  // (a teacher mass past the range: a log-sum-exp far below its record)
+  if (!(is_finite(r.M) && is_finite(s.p_sum)) && !(r.status & SV_REQ_TIMEOUT))
+    r.status |= SV_REQ_BAD_LOGITS;
   const float up = to_frame(s.top_m, r.M, c), down = to_frame(r.m, r.M, c);
   const float rest = r.S.x * down, top = s.top_z.x * up;
   Pair Z;
@@ -293,7 +297,7 @@ __device__ Sums row_sums(const DistillShared& s, int C, float c) {
   // q_rest - p_rest, of the two masses outside the record or of the two on it, whichever
   // are smaller: the roundings of two masses near 1 would be most of a small difference
   const float out = s.p_rest > 0.f && s.p_sum + r.q_top < 1.f ? s.p_sum - r.q_top
-                                                              : rest * r.inv_z - s.p_rest;
+                                                              : s.mass * (rest * r.inv_z) - s.p_rest;
   r.beta = r.m == -INFINITY ? 0.f : out / r.S.x;
   return r;
 }
@@ -548,7 +552,8 @@ __global__ void __launch_bounds__(kDistillThreads, 5) distill_kernel(const Disti
   const float g = p.grad_loss[row];
   const float scale = is_finite(g) ? fminf(fmaxf(g / p.T, -FLT_MAX), FLT_MAX) : g / p.T;
   const float beta = st.y * scale;
-  const float my_grad = (ex2((my_v - st.z) * p.cc) * st.w - (t < p.k ? s.p[t] : 0.f)) * scale;
+  const float my_q = ex2((my_v - st.z) * p.cc) * st.w;
+  const float my_grad = (s.mass * my_q - (t < p.k ? s.p[t] : 0.f)) * scale;
   if (((uintptr_t)grad & 15u) == (uint32_t)r) {
     // word for word as the student's row; the recorded tokens after the words they lie in
     for (int i = t; i < nw; i += kDistillThreads) {
