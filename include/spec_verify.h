@@ -430,7 +430,10 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
  *     P = sum_j p_j + p_rest: 1, or the record's own mass where that is more than
  *     top_lse leaves room for or the record holds all V tokens.
  * A term with p = 0 is 0.  A recorded token with p_j > 0 whose student logit is
- * -inf gives loss +inf (the gradient stays finite).
+ * -inf gives loss +inf (the gradient stays finite), and so does p_rest > 0 where
+ * the student is -inf on every token outside the record; there a p_rest of up to
+ * 2^-20 + 2^-23 |top_lse|, the rounding of a record that holds all of the
+ * teacher's mass (rows masked to fewer tokens than k), counts as 0.
  *
  *   student_logits [B, P, V] dtype, V * sizeof(logit) <= SV_MAX_DISTILL_ROW.
  *   top_ids     [B, P, k] int32: distinct tokens in [0, V); -1 marks an unused

@@ -1,6 +1,6 @@
 """Gradients and losses of spec_distill where they are differences of nearly
-equal masses and where the record's mass is not 1, against the definition in
-float64 (needs a GPU).
+equal masses, where the record's mass is not 1, and where teacher and student
+are masked alike, against the definition in float64 (needs a GPU).
 
 Bounds, u = 2^-24.  A weight is 2^a, a = (l - m) c: the difference, c and the
 product each round, 3 |a| ln 2 u in all, and the exponential is good to 4 u.
@@ -137,6 +137,46 @@ def test_differences_of_a_loss_of_another_mass():
     mass = math.exp(0.5)
     tol = h * h / 6 * 8 * mass + 2 * 2 * ratio(30) * 48 * mass / (2 * h)
     assert bool(((got - want).abs() <= tol).all()), (got, want, tol)
+
+
+@pytest.mark.parametrize("T,at", [(1.0, 0.0), (0.7, 0.0), (1.0, 150.0), (2.0, -900.0)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_teacher_and_student_masked_alike(dtype, T, at):
+    """A grammar leaves fewer tokens than the record keeps, on both sides: the record holds all
+    of the teacher's mass, and what the rounding of its log-sum-exp leaves of 1 - sum p is no
+    mass on tokens that the student rules out."""
+    B, P, V, k = 16, 8, 3001, 24
+    g = gen(5)
+    allow = torch.arange(B * P, device="cuda").view(B, P) % 23 + 1  # 1 to 23 tokens
+    order = torch.rand((B, P, V), generator=g, device="cuda").argsort(-1).argsort(-1)
+    mask = order >= allow[..., None]
+    def rows(noise):
+        x = torch.randn((B, P, V), generator=g, device="cuda") * noise + at
+        return x.to(dtype).masked_fill(mask, -math.inf)
+    rec = api.spec_top_logits(rows(3.0), k, T)
+    s = rows(2.0)
+    gl = torch.ones((B, P), device="cuda")
+    assert torch.equal((rec.ids >= 0).sum(-1), allow)
+    use = rec.ids >= 0
+    ids = rec.ids.long().clamp(min=0)
+    logp = (rec.logits.double() / T - rec.lse.double()[..., None]).masked_fill(~use, -math.inf)
+    p = logp.exp()
+    assert bool((p.sum(-1) < 1).any()) and bool((p.sum(-1) > 1).any())  # the roundings
+    logq = torch.log_softmax(s.double() / T, -1).gather(-1, ids).masked_fill(~use, 0.0)
+    terms = torch.where(use, p * (logp - logq), 0.0)
+    grads = torch.zeros(s.shape, dtype=torch.float64, device="cuda")
+    grads.scatter_add_(-1, ids, torch.where(use, (logq.exp() * p.sum(-1, keepdim=True) - p) / T, 0.0))
+    tol = 2 * ratio(30) * (1 + terms.abs().sum(-1))
+    for loss, grad in both_ways(s, rec.ids, rec.logits, rec.lse, T, gl):
+        assert bool(torch.isfinite(loss).all()), int((~torch.isfinite(loss)).sum())
+        assert bool(((loss.double() - terms.sum(-1)).abs() <= tol).all())
+        # each p and q at most 1 and 2 ratios off; what is left of 1 - sum p is up to 2^-20 + 2^-23 |lse|
+        room = 4 * ratio(30) + 2.0 ** -20 + 2.0 ** -23 * rec.lse.abs().double()[..., None]
+        off = (grad.double() - grads).abs()
+        assert bool((off <= room / T + HALF_STEP[dtype] * grads.abs() * 1.01).all())
+    # a remainder that is more than rounding stays what it is
+    far = api.spec_distill(s, rec.ids, rec.logits, T, top_lse=rec.lse + 0.01 + rec.lse.abs() * 1e-4)
+    assert bool((far.loss == math.inf).all())
 
 
 def test_mass_past_the_range():

@@ -72,6 +72,7 @@ struct alignas(16) DistillShared {
   float norm, norm_lo;           // the teacher's log-sum-exp - t_max / T:
                                  // log p_j = (t_j - t_max) / T - norm
   float p_sum, p_rest;           // the record's mass and 1 - it
+  float p_slack;                 // what rounding can make of a p_rest of 0
   float mass;                    // the teacher's: 1, or a record's whose mass does not fit its log-sum-exp
   float top_m;                   // the student's max on the record (NaN: unusable)
   float2 top_z;                  // and its sum there in that frame (hi, lo)
@@ -266,6 +267,8 @@ __device__ void load_record(DistillShared& s, const DistillParams& p, long long 
       s.p_sum = total.x + total.y;
       s.p_rest = p.top_lse && used < p.V ? fmaxf(0.f, (1.f - total.x) - total.y) : 0.f;
       s.mass = p.top_lse && s.p_rest == 0.f ? s.p_sum : 1.f;
+      // log-sum-exp: half a step of it, and as much in a sum it was rounded from; the p_j: 2^-20
+      s.p_slack = 0x1p-20f + 0x1p-23f * fabsf(lse);
     }
   }
 }
@@ -331,7 +334,7 @@ __device__ float row_loss(const DistillShared& s, const DistillParams& p, const 
     }
   loss = warp_sum(loss);
   if (s.p_rest > 0.f) {
-    if (!rest) return INFINITY;
+    if (!rest) return s.p_rest > s.p_slack ? INFINITY : loss;
     if (!is_finite((r.M - r.m) / p.T)) return fmaf(s.p_rest * p.inv_t, r.M - r.m, loss);
     // a remainder that is most of the mass: its logarithm from what is left of it
     const float lp = s.p_sum < 0.5f ? log1pf(-s.p_sum) : logf(s.p_rest);
