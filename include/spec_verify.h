@@ -346,12 +346,15 @@ sv_status spec_verify_tree(const void* target_logits, const int32_t* tree_parent
                            int max_depth, int32_t* out_path, int32_t* out_status,
                            sv_stream_t stream);
 
-/* The longest time a kernel waits for logits it staged in shared memory
- * before it gives up: the call then marks every request SV_REQ_TIMEOUT (the
+/* The longest time a kernel waits for logits it staged in shared memory (in
+ * spec_top_logits and spec_beam_select, for what CTAs send each other or ask
+ * of the launch) before it gives up: the call then marks every request
+ * SV_REQ_TIMEOUT, calls of rows or beams those whose wait ran out (the
  * workspace stays usable; the next call starts clean).  Default 2 s, which
  * only a device fault can exhaust; a serving loop with a watchdog may set
  * less.  0 makes the waits give up at once, without polling - every call
- * then reports SV_REQ_TIMEOUT, which is how the timeout path is tested.
+ * that waits then reports SV_REQ_TIMEOUT, which is how the timeout path is
+ * tested.
  * Process-wide; applies to the calls queued after it.  Always SV_OK. */
 sv_status spec_verify_set_wait_limit_ns(uint64_t limit_ns);
 uint64_t spec_verify_wait_limit_ns(void);
@@ -404,7 +407,8 @@ sv_status spec_ngram_propose(const int32_t* tokens, const int32_t* lens, int B, 
  *   out_lse     [B, P] fp32: log sum_j exp(l_j / T); -inf for a row that is
  *               not read or has no finite logit.
  *   out_status  [B, P] int32 or NULL: SV_REQ_* bits per row.  A row with NaN or
- *               +inf (SV_REQ_BAD_LOGITS) has no record (-1, -inf) and lse NaN.
+ *               +inf (SV_REQ_BAD_LOGITS), or with a wait that ran out
+ *               (SV_REQ_TIMEOUT), has no record (-1, -inf) and lse NaN.
  *   B, P, V     0 <= B <= SV_MAX_B, P >= 1, B * P <= SV_MAX_ROWS, 1 <= V <= SV_MAX_V.
  * No workspace: a call keeps nothing, so calls may overlap on any streams. */
 sv_status spec_top_logits(const void* logits, int k, float temperature, const int32_t* lens,
@@ -490,7 +494,8 @@ sv_status spec_distill_grad(const void* student_logits, const int32_t* top_ids,
  *               candidate; out_scores [B, n] fp32.  Candidates have finite logits; past
  *               the last one the slots hold -1, -1 and -inf.
  *   out_status  [B] int32 or NULL: SV_REQ_BAD_LOGITS when a live beam's row has NaN
- *               or +inf, or a score is NaN or +inf; nothing is kept then.
+ *               or +inf, or a score is NaN or +inf, SV_REQ_TIMEOUT when a wait of
+ *               its rows ran out; nothing is kept then.
  *   1 <= W <= SV_MAX_BEAMS, 1 <= n <= SV_MAX_TOP, 0 <= B <= SV_MAX_B, and
  *   ceil(W / 8) * ceil(V / 8192) <= 256 (V <= 2097152 up to 8 beams, 262144 with
  *   64).  Scores are compared in 64 bits (their row sums are of 32-bit terms).

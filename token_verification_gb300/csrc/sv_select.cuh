@@ -33,7 +33,7 @@ struct TopParams {
   int* out_parents;     // beams: [B, n]
   float* out_values;    // logits [rows, n], scores [B, n]
   float* out_lse;       // record: [B*P]
-  double* out_off;      // row kernel for beams: [B*W] offsets (-inf: no candidates, NaN: bad)
+  double* out_off;      // row kernel for beams: [B*W] offsets (-inf: no candidates, NaN: kOff*)
   float* out_max;       // and the rows' maxes
   int* out_status;
   int P;                // record: rows per request
@@ -45,6 +45,7 @@ struct TopParams {
   int table_bytes;
   float cc;             // log2(e) / T
   float T;
+  unsigned long long wait_ns;  // limit of the waits
   char* first;          // the logits' memory
   char* last;
 };
@@ -185,6 +186,9 @@ __device__ float unit_bound(Select& s, const uint16_t* unit, int units, int n) {
   group_sync<kBar>();
   return of_ordered(s.bound);
 }
+
+// Offsets that are no number: a bad row or score, and a row whose wait ran out.
+constexpr unsigned long long kOffBad = 0x7fffffffffffffffull, kOffLate = 0x7ff8000000000001ull;
 
 // A beam's continuation scores offset + (l - m) in 64 bits, with m the row's max
 // and offset = score - log of the row's sum in m's frame (as a pair): l - m

@@ -133,9 +133,11 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
         send16(in_cta(smem_u32(from), c), in_cta(smem_u32(&s.part_bar), c),
                *reinterpret_cast<const float4*>(from));
     }
-    if (warp == 0 && !mbar_wait_cluster(smem_u32(&s.part_bar), 0, kWaitLimitNs)) {
-      s.sel.bad = SV_REQ_TIMEOUT;  // a peer has failed
+    if (warp == 0 && !mbar_wait_cluster(smem_u32(&s.part_bar), 0, p.wait_ns)) {
+      s.sel.bad = SV_REQ_TIMEOUT;
       cluster.map_shared_rank(&s, 0)->sel.overflow = 1;  // the leader reads all rows itself
+      // what was sent lands before the CTA leaves; a peer that has not sent by then has failed
+      mbar_wait_cluster(smem_u32(&s.part_bar), 0, kWaitLimitNs);
     }
     __syncthreads();
   }
@@ -398,6 +400,7 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
   p.n = k;
   p.cc = exponent_scale(temperature);
   p.T = temperature;
+  p.wait_ns = wait_limit_ns();
   const long long rows = (long long)B * P;
   if (record_by_rows(dtype, rows, V)) {
     const bool aligned = set_span(p, dtype, rows);
@@ -441,6 +444,7 @@ sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out
   p.n = n;
   p.cc = 1.4426950408889634f;
   p.T = 1.f;
+  p.wait_ns = wait_limit_ns();
   const cudaStream_t st = (cudaStream_t)stream;
   if (need) {  // each beam's n best, then the requests'
     const long long rows = (long long)B * W;

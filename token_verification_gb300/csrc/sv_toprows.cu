@@ -36,7 +36,9 @@ struct alignas(16) RowShared {
     alignas(16) uint16_t unit[kRowStreamers];  // its unit maxes, bf16 rounded down
   } slot[2];
   Select sel;
-  int late;                     // the queue did not answer in time
+  int late;                     // the queue did not answer in time: this CTA's rows from there on
+                                // are marked SV_REQ_TIMEOUT
+  int lost;                     // nor within the waits' default limit
 };
 constexpr int kLive = -1;
 
@@ -86,6 +88,17 @@ __device__ __forceinline__ void fill_slots(const TopParams& p, long long row, in
   }
 }
 
+// The outputs of a row that is not selected from (a call of the selecting half).
+__device__ __forceinline__ void leave_row(const TopParams& p, long long row, int status) {
+  fill_slots(p, row, 0);
+  if (threadIdx.x % kTopThreads == 0) {
+    const bool late = status == SV_REQ_TIMEOUT;
+    if (p.out_off) p.out_off[row] = late ? __longlong_as_double((long long)kOffLate) : -INFINITY;
+    else p.out_lse[row] = late ? qnan() : -INFINITY;
+    if (p.out_status) p.out_status[row] = status;
+  }
+}
+
 // The next row that needs work, -1 when the queue is empty; the outputs of the
 // others on the way (a call of the selecting half).  `row`: a row taken already,
 // or -1 to ask.
@@ -100,22 +113,21 @@ __device__ long long next_live(RowShared& s, const TopParams& p, long long row, 
         ask_for_cta(smem_u32(&s.answer), smem_u32(&s.bar));
       }
       // (the limit twice: see mbar_wait_cluster)
-      if (!mbar_wait(smem_u32(&s.bar), asked & 1) && !mbar_wait(smem_u32(&s.bar), asked & 1))
+      const uint32_t bar = smem_u32(&s.bar), phase = asked & 1;
+      if (!mbar_wait(bar, phase, p.wait_ns) && !mbar_wait(bar, phase, p.wait_ns)) {
         s.late = 1;
+        // the answer lands before the next question or the CTA's end
+        if (!mbar_wait(bar, phase) && !mbar_wait(bar, phase)) s.lost = 1;
+      }
       ++asked;
       group_sync<kBarSelect>();
-      if (s.late) return -1;
+      if (s.lost) return -1;
       row = taken_cta(smem_u32(&s.answer));
       if (row < 0) return -1;
     }
     const int state = row_state(p, row);
-    if (state == kLive) return row;
-    fill_slots(p, row, 0);
-    if (t == 0) {
-      if (p.out_off) p.out_off[row] = -INFINITY;
-      else p.out_lse[row] = -INFINITY;
-      if (p.out_status) p.out_status[row] = state;
-    }
+    if (state == kLive && !s.late) return row;
+    leave_row(p, row, state == kLive ? SV_REQ_TIMEOUT : state);
     row = -1;
   }
 }
@@ -138,7 +150,7 @@ __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot,
     if (lane_id() != 0) return;
     const float2 l = log_pair(sum);
     if (p.out_off) {
-      p.out_off[row] = bad              ? __longlong_as_double(0x7fffffffffffffffll)
+      p.out_off[row] = bad              ? __longlong_as_double((long long)kOffBad)
                        : m == -INFINITY ? -INFINITY
                                         : row_offset(score, l);
       p.out_max[row] = m;
@@ -207,7 +219,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParam
   const int lane = lane_id(), warp = t / kWarp;
   const RowSpan span = {p.first, p.last};
   if (threadIdx.x == 0) {
-    s.late = 0;
+    s.late = s.lost = 0;
     mbar_init(smem_u32(&s.bar), 1);
     fence_mbar_init();
   }
@@ -228,13 +240,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_rows_kernel(const TopParam
       if (t == 0) s.next[b ^ 1] = next;
       bar_arrive(kBarNext + (b ^ 1), kRowThreads);
       bar_sync(kBarFull + b, kRowThreads);
-      select_row<T, kAligned>(s, ls, s.slot[b], row, tables + b * table, p, span);
+      if (s.late) leave_row(p, row, SV_REQ_TIMEOUT);
+      else select_row<T, kAligned>(s, ls, s.slot[b], row, tables + b * table, p, span);
       bar_arrive(kBarEmpty + b, kRowThreads);
-      // a device fault: the queue did not answer in four seconds
-      if (s.late && t == 0) {
-        if (p.out_off) p.out_off[row] = (double)qnan();
-        else if (p.out_status) p.out_status[row] = SV_REQ_TIMEOUT;
-      }
       row = next;
     }
     return;
@@ -335,7 +343,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(
     s_off[t] = o;
     off_down[t] = __double2float_rd(o);
     s_max[t] = o == -INFINITY ? 0.f : m;  // (a row not read has none)
-    if (o != o) atomicOr(&sel.bad, SV_REQ_BAD_LOGITS);
+    if (o != o)
+      atomicOr(&sel.bad, (unsigned long long)__double_as_longlong(o) == kOffLate
+                             ? SV_REQ_TIMEOUT
+                             : SV_REQ_BAD_LOGITS);
   }
   __syncthreads();
   const int bad = sel.bad;

@@ -343,8 +343,9 @@ __device__ __forceinline__ void send16(uint32_t addr, uint32_t bar, const float4
       "r"(__float_as_uint(v.w)), "r"(bar)
       : "memory");
 }
-// mbar_wait for what other CTAs sent, with the limit twice: of a context that was
-// switched out as a whole, the clock alone goes on.
+// mbar_wait for what other CTAs sent (a limit of 0 gives up without polling here too),
+// with the limit twice: of a context that was switched out as a whole, the clock alone
+// goes on.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
                                                   unsigned long long limit_ns) {
   auto arrived = [&]() {
@@ -358,6 +359,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         : "memory");
     return ok != 0;
   };
+  if (limit_ns == 0) return false;
   if (arrived()) return true;
   for (int turn = 0; turn < 2; ++turn) {
     const unsigned long long t0 = global_ns();
