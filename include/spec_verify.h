@@ -482,8 +482,10 @@ sv_status spec_distill_grad(const void* student_logits, const int32_t* top_ids,
 /* One step of beam selection: of all continuations (beam w, token v) of a
  * request, the n of largest score
  *     scores[b, w] + l[b, w, v] - log sum_j exp(l[b, w, j]),
- * in descending order, equal scores by ascending w * V + v.  With a draft
- * model's logits each call is one level of a candidate tree (the kept
+ * in descending order.  Equal scores go by ascending beam; a beam's tokens whose
+ * scores are equal (by rounding: a score of -1e30 swallows every difference of
+ * logits) by descending logit, and of equal logits by ascending token.  With a
+ * draft model's logits each call is one level of a candidate tree (the kept
  * (parent, token) pairs are its nodes) for spec_verify_tree and its kin.
  *
  *   logits      [B, W, V] dtype.

@@ -14,6 +14,8 @@
 // descent on whole-number keys, 8 bits a pass.
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/spec_verify.h"
 #include "sv_launch.h"
 #include "sv_rows.cuh"
@@ -111,6 +113,13 @@ struct alignas(16) Lists {
   int idx[kMaxCands + 4];
   int rank[kMaxCands];                // until the list is sorted: the groups to read again
 };
+// Beams' also have their logits, in order: of a beam's tokens whose scores round to
+// one 64-bit number (a score of -1e30, say) the larger logit is the better.
+struct alignas(16) BeamLists : Lists {
+  uint32_t logit[kMaxCands];
+};
+template <bool kBeam>
+using ListOf = std::conditional_t<kBeam, BeamLists, Lists>;
 
 // Load stages: each warp streams 2 KB chunks through its own ring by 16-byte
 // asynchronous copies (a word more than a chunk, for rows off 16-byte
@@ -206,18 +215,19 @@ __device__ __forceinline__ float beam_score_down(float off_down, float m, float 
 constexpr int ring_bytes(int warps) { return Ring::kWarpBytes * warps; }
 
 template <bool kBeam>
-__device__ __forceinline__ void set_candidate(Lists& s, int o, float l, double off, float m,
-                                              int idx) {
+__device__ __forceinline__ void set_candidate(ListOf<kBeam>& s, int o, float l, double off,
+                                              float m, int idx) {
   s.key[o] = kBeam ? ordered(beam_score(off, m, l))
                    : ((unsigned long long)ordered(l) << 32) | (uint32_t)~idx;
   s.idx[o] = idx;
+  if constexpr (kBeam) s.logit[o] = ordered(l);
 }
 
 // One row's n largest finite elements by radix descent, appended to the list
 // from `at` on (a call of the group); returns how many.
 template <typename T, bool kBeam, int kBar>
-__device__ int select_row_slow(Select& s, Lists& ls, const T* row, int V, int n, double off,
-                               float m, int base, int at) {
+__device__ int select_row_slow(Select& s, ListOf<kBeam>& ls, const T* row, int V, int n,
+                               double off, float m, int base, int at) {
   const int t = threadIdx.x % kTopThreads;
   auto key_of = [&](int j) {  // (logit in order, index from the end), 0 if not finite
     const float l = j < V ? load_logit(row, j) : -INFINITY;
@@ -271,12 +281,20 @@ __device__ int select_row_slow(Select& s, Lists& ls, const T* row, int V, int n,
   return s.pick[3] - at;
 }
 
+// Whether entry j of a beam list comes before entry i of the same score: the
+// earlier beam, in a beam the larger logit, of equal ones the lower token.
+__device__ __forceinline__ bool tied_before(const BeamLists& s, int j, int i, int V) {
+  const int a = s.idx[j], b = s.idx[i];
+  const uint32_t x = s.logit[j], y = s.logit[i];
+  return x == y || a / V != b / V ? a < b : x > y;
+}
+
 // rank[i] = the number of entries that come before entry i, i < count: the
 // whole group, each entry's comparisons shared by 2^k neighbouring threads, four
 // keys at a time (those past the list are 0: before none). The code runs once
 // or a few times a launch: kept short, as its first run waits for instructions.
 template <bool kBeam, int kBar>
-__device__ void rank_list(Lists& s, int count) {
+__device__ void rank_list(ListOf<kBeam>& s, int count, int V) {
   const int t = threadIdx.x % kTopThreads;
   if (t < 4) s.key[count + t] = 0;
   group_sync<kBar>();
@@ -284,18 +302,19 @@ __device__ void rank_list(Lists& s, int count) {
   for (int i0 = 0; i0 < count; i0 += kTopThreads >> k) {
     const int i = i0 + (t >> k);
     const unsigned long long key = i < count ? s.key[i] : ~0ull;
-    const int idx = kBeam && i < count ? s.idx[i] : 0;
     int r = 0;
 #pragma unroll 1
     for (int j = 4 * way; j < count; j += 4 << k) {
       const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&s.key[j]);
       const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s.key[j + 2]);
-      if (kBeam) {
-        const int4 x = *reinterpret_cast<const int4*>(&s.idx[j]);
-        r += (a.x > key || (a.x == key && x.x < idx)) + (a.y > key || (a.y == key && x.y < idx)) +
-             (b.x > key || (b.x == key && x.z < idx)) + (b.y > key || (b.y == key && x.w < idx));
-      } else {
-        r += (a.x > key) + (a.y > key) + (b.x > key) + (b.y > key);
+      r += (a.x > key) + (a.y > key) + (b.x > key) + (b.y > key);
+      if constexpr (kBeam) {  // (seldom: scores equal to 64 bits)
+        const int ties = (a.x == key) + (a.y == key) + (b.x == key) + (b.y == key);
+        if (ties > ((unsigned)(i - j) < 4u ? 1 : 0)) {
+#pragma unroll 1
+          for (int q = j; q < j + 4; ++q)
+            if (s.key[q] == key && tied_before(s, q, i, V)) ++r;
+        }
       }
     }
     for (int o = 1; o < 1 << k; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
@@ -304,18 +323,39 @@ __device__ void rank_list(Lists& s, int count) {
   group_sync<kBar>();
 }
 
+// The n best of a list of at most 256 entries, to its front; returns how many.
+template <bool kBeam, int kBar>
+__device__ int keep_best(ListOf<kBeam>& ls, int total, int n, int V) {
+  rank_list<kBeam, kBar>(ls, total, V);
+  const int t = threadIdx.x % kTopThreads, r = t < total ? ls.rank[t] : n;
+  const unsigned long long key = t < total ? ls.key[t] : 0;
+  const int idx = t < total ? ls.idx[t] : 0;
+  uint32_t logit = 0;
+  if constexpr (kBeam) logit = t < total ? ls.logit[t] : 0;
+  group_sync<kBar>();
+  if (r < n) {
+    ls.key[r] = key;
+    ls.idx[r] = idx;
+    if constexpr (kBeam) ls.logit[r] = logit;
+  }
+  group_sync<kBar>();
+  return total < n ? total : n;
+}
+
 // Cuts the list to the entries at or above its n-th largest 32-bit key prefix.
-template <int kBar>
-__device__ int prune(Select& s, Lists& ls, int count, int n) {
+template <bool kBeam, int kBar>
+__device__ int prune(Select& s, ListOf<kBeam>& ls, int count, int n) {
   constexpr int kPer = kMaxCands / kTopThreads;
   const int tid = threadIdx.x % kTopThreads;
   unsigned long long k[kPer];
   int ix[kPer];
+  uint32_t lx[kPer];
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     const int i = q * kTopThreads + tid;
     k[q] = i < count ? ls.key[i] : 0ull;
     ix[q] = i < count ? ls.idx[i] : 0;
+    if constexpr (kBeam) lx[q] = i < count ? ls.logit[i] : 0;
   }
   // Three counters in turn, one barrier a round. A round clears the counter of the next
   // one, last read before the barrier of the round before; the counter of the round
@@ -346,6 +386,7 @@ __device__ int prune(Select& s, Lists& ls, int count, int n) {
       const int o = atomicAdd(&s.pick[1], 1);
       ls.key[o] = k[q];
       ls.idx[o] = ix[q];
+      if constexpr (kBeam) ls.logit[o] = lx[q];
     }
   group_sync<kBar>();
   return s.pick[1];

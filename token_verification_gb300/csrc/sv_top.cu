@@ -15,8 +15,8 @@
 // us (k = 32), four beams of 32000 7.6 us. Ordering cluster barriers in place of
 // the counted stores cost 0.7 us.
 //
-// A beam's candidates compare by their scores in 64 bits, a record's by their
-// logits.  Bounds are in fp32 rounded down, which can only lengthen the list.
+// A beam's candidates compare by their scores in 64 bits (tied_before: and then), a
+// record's by their logits.  Bounds are in fp32 rounded down, which can only lengthen the list.
 #include <string.h>
 
 #include <algorithm>
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   // per iteration over this CTA's items, the thread's 32 elements' max
   uint16_t* table = reinterpret_cast<uint16_t*>(smem + sizeof(TopShared));
   unsigned char* rings = smem + sizeof(TopShared) + p.table_bytes;
-  Lists& ls = *reinterpret_cast<Lists*>(rings);
+  ListOf<kBeam>& ls = *reinterpret_cast<ListOf<kBeam>*>(rings);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const long long grp = blockIdx.x / C;
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
   }
   __syncthreads();
   TopShared* lead = C > 1 ? cluster.map_shared_rank(&s, 0) : &s;
-  Lists* lead_ls = C > 1 ? cluster.map_shared_rank(&ls, 0) : &ls;
+  ListOf<kBeam>* lead_ls = C > 1 ? cluster.map_shared_rank(&ls, 0) : &ls;
   const int hits = s.sel.n_hits;
   if (hits > kMaxCands) {
     if (t == 0) lead->sel.overflow = 1;
@@ -256,30 +256,20 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
       const int got = select_row_slow<T, kBeam, 0>(s.sel, ls, row, p.V, p.n, off,
                                                    kBeam ? s.max[w] : 0.f, w * p.V, count);
       // keep the n best of the rows so far (at most 2 n <= 256 entries, one a thread)
-      const int total = count + got;
-      rank_list<kBeam, 0>(ls, total);
-      const unsigned long long key = t < total ? ls.key[t] : 0;
-      const int idx = t < total ? ls.idx[t] : 0, r = t < total ? ls.rank[t] : p.n;
-      __syncthreads();
-      if (r < p.n) {
-        ls.key[r] = key;
-        ls.idx[r] = idx;
-      }
-      count = min(total, p.n);
-      __syncthreads();
+      count = keep_best<kBeam, 0>(ls, count + got, p.n, p.V);
     }
   } else {
     if (kBeam) {
       for (int i = t; i < count; i += kTopThreads) {
         const int idx = ls.idx[i];
         const int w = idx / p.V;
-        set_candidate<true>(ls, i, __uint_as_float((uint32_t)ls.key[i]), s.off[w], s.max[w], idx);
+        set_candidate<kBeam>(ls, i, __uint_as_float((uint32_t)ls.key[i]), s.off[w], s.max[w], idx);
       }
       __syncthreads();
     }
-    if (count > kRankAll) count = prune<0>(s.sel, ls, count, p.n);
+    if (count > kRankAll) count = prune<kBeam, 0>(s.sel, ls, count, p.n);
   }
-  rank_list<kBeam, 0>(ls, count);
+  rank_list<kBeam, 0>(ls, count, p.V);
   for (int i = t; i < count; i += kTopThreads) {
     const int r = ls.rank[i];
     if (r < p.n) write_slot<kBeam>(p, grp, r, ls.key[i], ls.idx[i]);
@@ -288,8 +278,9 @@ __global__ void __launch_bounds__(kTopThreads, 3) top_kernel(const TopParams p) 
 }
 
 // The candidates lie in the memory of the load stages, which are consumed by then.
-constexpr int kUnionBytes = ring_bytes(kTopWarps) > (int)sizeof(Lists) ? ring_bytes(kTopWarps)
-                                                                      : (int)sizeof(Lists);
+constexpr int kUnionBytes = ring_bytes(kTopWarps) > (int)sizeof(BeamLists)
+                                ? ring_bytes(kTopWarps)
+                                : (int)sizeof(BeamLists);
 
 template <typename T, bool kAligned, bool kBeam>
 cudaError_t launch_top(const TopParams& p, long long groups, int C, cudaStream_t stream) {

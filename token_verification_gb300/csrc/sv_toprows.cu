@@ -192,9 +192,9 @@ __device__ void select_row(RowShared& s, Lists& ls, const RowShared::Slot& slot,
     group_sync<kBarSelect>();
     count = select_row_slow<T, false, kBarSelect>(s.sel, ls, data, p.V, p.n, 0.0, 0.f, 0, 0);
   } else if (count > kRankAll) {
-    count = prune<kBarSelect>(s.sel, ls, count, p.n);
+    count = prune<false, kBarSelect>(s.sel, ls, count, p.n);
   }
-  rank_list<false, kBarSelect>(ls, count);
+  rank_list<false, kBarSelect>(ls, count, p.V);
   for (int i = t; i < count; i += kTopThreads) {
     const int r = ls.rank[i];
     if (r < p.n) {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(
     const TopParams p, const FastDiv div_n, const FastDiv div_w, const int* __restrict__ ids,
     const float* __restrict__ values, const double* __restrict__ off,
     const float* __restrict__ row_max) {
-  __shared__ Lists ls;
+  __shared__ BeamLists ls;
   __shared__ Select sel;
   __shared__ __align__(16) uint16_t unit[kTopThreads];
   __shared__ double s_off[SV_MAX_BEAMS];
@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(
       if (f > -INFINITY && fmaf(fabsf(f) + fabsf(off_down[row[q]]), 1e-6f, f) >= bound) {
         const int at = atomicAdd(&sel.n_cands, 1);
         if (at < kMaxCands) {
-          ls.key[at] = ordered(beam_score(s_off[row[q]], s_max[row[q]], v[q]));
-          ls.idx[at] = row[q] * p.V + ids[place[q]];
+          set_candidate<true>(ls, at, v[q], s_off[row[q]], s_max[row[q]],
+                              row[q] * p.V + ids[place[q]]);
         }
       }
     }
@@ -399,27 +399,17 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(
         if (s_off[w] == -INFINITY) continue;
         int got = 0;  // (the finite ones come first)
         if (t < p.n && values[w * p.n + t] > -INFINITY) {
-          ls.key[count + t] = ordered(beam_score(s_off[w], s_max[w], values[w * p.n + t]));
-          ls.idx[count + t] = w * p.V + ids[w * p.n + t];
+          set_candidate<true>(ls, count + t, values[w * p.n + t], s_off[w], s_max[w],
+                              w * p.V + ids[w * p.n + t]);
           got = 1;
         }
         got = __syncthreads_count(got);
-        const int total = count + got;
-        rank_list<true, 0>(ls, total);
-        const unsigned long long key = t < total ? ls.key[t] : 0;
-        const int idx = t < total ? ls.idx[t] : 0, r = t < total ? ls.rank[t] : p.n;
-        __syncthreads();
-        if (r < p.n) {
-          ls.key[r] = key;
-          ls.idx[r] = idx;
-        }
-        count = min(total, p.n);
-        __syncthreads();
+        count = keep_best<true, 0>(ls, count + got, p.n, p.V);
       }
     } else if (count > kRankAll) {
-      count = prune<0>(sel, ls, count, p.n);
+      count = prune<true, 0>(sel, ls, count, p.n);
     }
-    rank_list<true, 0>(ls, count);
+    rank_list<true, 0>(ls, count, p.V);
     for (int i = t; i < count; i += kTopThreads) {
       const int r = ls.rank[i];
       if (r < p.n) write(r, ls.key[i], ls.idx[i]);
