@@ -520,8 +520,9 @@ sv_status spec_beam_select(const void* logits, const float* scores, int32_t* out
  *   state       G x B x W x H x L entries at byte strides state_strides[5].
  *   out         G x B x W_out x H x L entries at byte strides out_strides[5].
  *               Strides are >= 0 and may come in any order (heads before or after
- *               beams); entries of `out` must not overlap each other, nor state's
- *               memory (SV_ERR_ALIAS).
+ *               beams); entries of `out` must not overlap each other, nor entries
+ *               of state (SV_ERR_ALIAS); the two may be interleaved parts of one
+ *               allocation.
  *   parents     [B, W_out] int32: -1 leaves the slot as it is.
  *   lens        [B] int32 or NULL (all L): entries l >= lens[b] of out are left as
  *               they are.

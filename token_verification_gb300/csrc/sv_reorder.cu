@@ -118,6 +118,56 @@ cudaError_t launch_reorder(const ReorderParams& p, unsigned blocks, cudaStream_t
   return launch_early(reorder_kernel<U>, blocks, kReorderThreads, 0, 1, stream, p);
 }
 
+// Whether an entry of one tensor shares a byte with an entry of another: whether
+//   at + sum_k c_k stride_k,  lo_k <= c_k <= hi_k,
+// (the distance of two entries, one term a dimension of each tensor, one for
+// both where their strides agree) comes closer to 0 than row_bytes. Terms by
+// falling stride, each tried only where the rest can still reach 0: a handful
+// of nodes for the views of a dense cache. A search that grows past kMeetNodes
+// (strides that interleave in other ways) says yes.
+constexpr int kMeetNodes = 4096;
+typedef __int128 Wide;  // (sums of ten extents of up to 2^60)
+struct Term {
+  long long stride, lo, hi;
+};
+struct Meet {
+  Term term[10];
+  Wide low[11], high[11];  // the sums of term k on, at least and at most
+  int n = 0, nodes = 0;
+  long long row_bytes;
+  static Wide div_down(Wide a, long long b) { return a >= 0 ? a / b : -((-a + b - 1) / b); }
+  bool from(int k, Wide at) {
+    if (++nodes > kMeetNodes) return true;
+    if (k == n) return at > -row_bytes && at < row_bytes;
+    const Term& t = term[k];
+    const Wide first = -div_down(-(-(Wide)row_bytes + 1 - high[k + 1] - at), t.stride);
+    const Wide last = div_down((Wide)row_bytes - 1 - low[k + 1] - at, t.stride);
+    for (Wide c = std::max(first, (Wide)t.lo); c <= std::min(last, (Wide)t.hi); ++c)
+      if (from(k + 1, at + c * t.stride)) return true;
+    return false;
+  }
+};
+bool entries_meet(long long at, const int64_t* in, const long long* n_in, const int64_t* out,
+                  const long long* n_out, long long row_bytes) {
+  Meet m;
+  m.row_bytes = row_bytes;
+  for (int i = 0; i < 5; ++i) {
+    if (in[i] == out[i]) {
+      if (in[i] > 0) m.term[m.n++] = {in[i], 1 - n_out[i], n_in[i] - 1};
+    } else {
+      if (in[i] > 0 && n_in[i] > 1) m.term[m.n++] = {in[i], 0, n_in[i] - 1};
+      if (out[i] > 0 && n_out[i] > 1) m.term[m.n++] = {out[i], 1 - n_out[i], 0};
+    }
+  }
+  std::sort(m.term, m.term + m.n, [](const Term& a, const Term& b) { return a.stride > b.stride; });
+  m.low[m.n] = m.high[m.n] = 0;
+  for (int k = m.n - 1; k >= 0; --k) {
+    m.low[k] = m.low[k + 1] + (Wide)m.term[k].lo * m.term[k].stride;
+    m.high[k] = m.high[k + 1] + (Wide)m.term[k].hi * m.term[k].stride;
+  }
+  return m.from(0, at);
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -167,7 +217,9 @@ extern "C" sv_status spec_beam_reorder(const void* state, const int64_t* state_s
         ext_in += (n_in[i] - 1) * state_strides[i];
       }
     const uintptr_t a = (uintptr_t)state, b = (uintptr_t)out;
-    if (a < b + (uintptr_t)ext_out && b < a + (uintptr_t)ext_in) return SV_ERR_ALIAS;
+    if (a < b + (uintptr_t)ext_out && b < a + (uintptr_t)ext_in &&
+        entries_meet((long long)(a - b), state_strides, n_in, out_strides, n_out, row_bytes))
+      return SV_ERR_ALIAS;
     p.state = static_cast<const char*>(state);
     p.out = static_cast<char*>(out);
     align = (unsigned long long)a | b | (unsigned long long)row_bytes;
