@@ -453,6 +453,14 @@ def _count(k):
     return k
 
 
+def _written(*tensors):
+    """Tell autograd that caller-given tensors were written in place: a backward pass that
+    saved one of them then refuses to run on the new contents."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _given(out, device, **like):
     """Check caller-given output tensors: name -> (dtype, shape), None fields are left out."""
     for name, (dtype, shape) in like.items():
@@ -481,9 +489,10 @@ def spec_top_logits(logits, k, temperature=1.0, out: Optional[TopLogits] = None,
             return _short(r, TopLogits)
     B, P, V, device, code = _rows(logits, "logits", "[B, P, V]")
     k = _count(k)
+    given = out is not None
     if lens is not None:
         _need(lens, "lens", device, torch.int32, (B,))
-    if out is None:
+    if not given:
         shape = (B, P, k)
         out = TopLogits(torch.empty(shape, dtype=torch.int32, device=device),
                         torch.empty(shape, dtype=torch.float32, device=device),
@@ -495,6 +504,8 @@ def spec_top_logits(logits, k, temperature=1.0, out: Optional[TopLogits] = None,
     _launch(device, _native.lib().spec_top_logits, logits.data_ptr(), k, float(temperature),
             _addr(lens), out.ids.data_ptr(), out.logits.data_ptr(), out.lse.data_ptr(),
             _addr(out.status), code, B, P, V)
+    if given:
+        _written(out.ids, out.logits, out.lse, out.status)
     return out
 
 
@@ -531,7 +542,9 @@ def spec_distill(student_logits, top_ids, top_logits, temperature=1.0,
     (top_lse None: the teacher renormalised over its record); lens [B] int32
     or None.  With grad_loss [B, P] fp32 the same pass also writes out.grad,
     the gradient of (grad_loss * loss).sum() in the student's type, for
-    ``student_logits.backward(out.grad)``; out.grad may be student_logits."""
+    ``student_logits.backward(out.grad)``; out.grad may be student_logits (an
+    operation that saved those logits for its own backward pass then refuses it,
+    as after any write in place)."""
     if out is None:
         r = _native.binding().distill(student_logits, top_ids, top_logits, temperature, top_lse,
                                       lens, grad_loss, bool(stats), bool(status))
@@ -539,7 +552,8 @@ def spec_distill(student_logits, top_ids, top_logits, temperature=1.0,
             return _short(r, DistillOutputs)
     B, P, V, k, device, code = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
                                              grad_loss)
-    if out is None:
+    given = out is not None
+    if not given:
         f32 = torch.float32
         out = DistillOutputs(
             torch.empty((B, P), dtype=f32, device=device),
@@ -555,6 +569,8 @@ def spec_distill(student_logits, top_ids, top_logits, temperature=1.0,
             float(temperature), out.loss.data_ptr(), _addr(out.stats),
             _addr(out.grad) if grad_loss is not None else None, _addr(out.status),
             code, B, P, V, k)
+    if given:
+        _written(out.loss, out.stats, out.grad if grad_loss is not None else None, out.status)
     return out
 
 
@@ -574,7 +590,8 @@ def spec_distill_grad(student_logits, top_ids, top_logits, temperature, stats, g
     B, P, V, k, device, code = _distill_args(student_logits, top_ids, top_logits, top_lse, lens,
                                              grad_loss)
     _need(stats, "stats", device, torch.float32, (B, P, 4))
-    if grad is None:
+    given = grad is not None
+    if not given:
         grad = torch.empty((B, P, V), dtype=student_logits.dtype, device=device)
     else:
         _need(grad, "grad", device, student_logits.dtype, (B, P, V))
@@ -582,6 +599,8 @@ def spec_distill_grad(student_logits, top_ids, top_logits, temperature, stats, g
             top_ids.data_ptr(), top_logits.data_ptr(), _addr(top_lse), _addr(lens),
             stats.data_ptr(), grad_loss.data_ptr(), float(temperature), grad.data_ptr(),
             code, B, P, V, k)
+    if given:
+        _written(grad)
     return grad
 
 
@@ -605,7 +624,8 @@ def spec_beam_select(logits, scores, n, out: Optional[BeamOutputs] = None, *,
     B, W, V, device, code = _rows(logits, "logits", "[B, W, V]")
     n = _count(n)
     _need(scores, "scores", device, torch.float32, (B, W))
-    if out is None:
+    given = out is not None
+    if not given:
         shape = (B, n)
         out = BeamOutputs(torch.empty(shape, dtype=torch.int32, device=device),
                           torch.empty(shape, dtype=torch.int32, device=device),
@@ -621,6 +641,8 @@ def spec_beam_select(logits, scores, n, out: Optional[BeamOutputs] = None, *,
     _launch(device, lib.spec_beam_select, logits.data_ptr(), scores.data_ptr(),
             out.tokens.data_ptr(), out.parents.data_ptr(), out.scores.data_ptr(),
             _addr(out.status), code, B, W, V, n, _addr(ws), need)
+    if given:
+        _written(out.tokens, out.parents, out.scores, out.status)
     return out
 
 
@@ -658,7 +680,8 @@ def spec_beam_reorder(state, parents, out=None, *, lens=None, status=None) -> to
     if status is not None:
         _need(status, "status", device, torch.int32, (B,))
     shape = (G, B, W_out, H, L, D)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.zeros(shape, dtype=state.dtype, device=device)
     elif not isinstance(out, torch.Tensor) or out.device != device:
         raise ValueError("out must be a tensor on %s" % device)
@@ -679,4 +702,5 @@ def spec_beam_reorder(state, parents, out=None, *, lens=None, status=None) -> to
             _addr(lens), out.data_ptr(),
             _Strides(b0 * size, b1 * size, b2 * size, b3 * size, b4 * size), _addr(status), G, B,
             W, W_out, H, L, D * size)
+    _written(out if given else None, status)
     return out

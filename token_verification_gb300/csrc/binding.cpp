@@ -278,10 +278,12 @@ PyObject* beam_reorder(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ss[i] = s->stride(i) * e;
       os[i] = out->stride(i) * e;
     }
-    return PyLong_FromLong(g_reorder(s->data_ptr(), ss, data<int32_t>(parents),
-                                     data<int32_t>(lens), out->data_ptr(), os, nullptr, (int)G,
-                                     (int)B, (int)W, (int)Wo, (int)H, (int)L, (int)(D * e),
-                                     stream_of(d)));
+    const sv_status rc = g_reorder(s->data_ptr(), ss, data<int32_t>(parents), data<int32_t>(lens),
+                                   out->data_ptr(), os, nullptr, (int)G, (int)B, (int)W, (int)Wo,
+                                   (int)H, (int)L, (int)(D * e), stream_of(d));
+    // autograd notices the write (inference tensors have no version)
+    if (rc == SV_OK && !out->is_inference()) out->unsafeGetTensorImpl()->bump_version();
+    return PyLong_FromLong(rc);
   });
 }
 
