@@ -452,8 +452,9 @@ sv_status spec_top_logits(const void* logits, int k, float temperature, const in
  *   out_stats   [B, P, 4] fp32 (16-byte aligned) or NULL: what spec_distill_grad
  *               needs of this call.
  *   out_grad    [B, P, V] dtype: written when grad_loss is given (every row).
- *               It may be student_logits itself, and overlap it in no other way
- *               (SV_ERR_ALIAS).
+ *               It may be student_logits itself, and overlap it in no other way;
+ *               the other outputs must not overlap grad_loss (SV_ERR_ALIAS), and no
+ *               output any other input.
  *   out_status  [B, P] int32 or NULL: SV_REQ_BAD_LOGITS (student NaN, +inf or no
  *               finite logit; a used entry's logit NaN or +inf, or a top_lse beside
  *               it that is not finite or so far below them that sum_j p_j is not,

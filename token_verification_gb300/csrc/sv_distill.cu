@@ -635,10 +635,15 @@ sv_status check_distill(float temperature, sv_dtype dtype, int B, int P, int V, 
   return SV_OK;
 }
 
+// Whether two pieces of memory overlap (b may be null: no).
+bool meet(const void* a, long long a_bytes, const void* b, long long b_bytes) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return b && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 // out_grad may be the student's logits themselves, or lie apart from them.
 bool grad_overlaps(const void* student, const void* grad, size_t bytes) {
-  const uintptr_t a = (uintptr_t)student, b = (uintptr_t)grad;
-  return a != b && a < b + bytes && b < a + bytes;
+  return student != grad && meet(student, (long long)bytes, grad, (long long)bytes);
 }
 
 DistillParams distill_params(const void* student, const int32_t* ids, const float* logits,
@@ -689,7 +694,11 @@ sv_status spec_distill(const void* student_logits, const int32_t* top_ids,
   const long long rows = (long long)B * P;
   if (!grad_loss) return run_distill<kLoss>(p, dtype, rows, (cudaStream_t)stream);
   if ((uintptr_t)out_grad & mask) return SV_ERR_NULL;
-  if (grad_overlaps(student_logits, out_grad, (size_t)rows * V * (dtype == SV_BF16 ? 2 : 4)))
+  // (a row's CTAs read its weight until the end, after the leader wrote the row's loss)
+  if (grad_overlaps(student_logits, out_grad, (size_t)rows * V * (dtype == SV_BF16 ? 2 : 4)) ||
+      meet(grad_loss, 4 * rows, out_loss, 4 * rows) ||
+      meet(grad_loss, 4 * rows, out_stats, 16 * rows) ||
+      meet(grad_loss, 4 * rows, out_status, 4 * rows))
     return SV_ERR_ALIAS;
   p.grad_loss = grad_loss;
   p.out_grad = out_grad;
