@@ -616,7 +616,8 @@ def spec_beam_select(logits, scores, n, out: Optional[BeamOutputs] = None, *,
                      status=True) -> BeamOutputs:
     """One step of beam selection (see spec_verify.h): logits [B, W, V]
     bf16/fp32 CUDA, scores [B, W] fp32 (-inf: a finished beam, not read); the
-    n best continuations by scores + log_softmax(logits), best first."""
+    n best continuations by scores + log_softmax(logits), best first (equal scores
+    by beam, in a beam by logit, then by token)."""
     if out is None:
         r = _native.binding().beam_select(logits, scores, n, bool(status))
         if r is not None:
@@ -657,8 +658,9 @@ def spec_beam_reorder(state, parents, out=None, *, lens=None, status=None) -> to
     the others at any strides (a permuted view of a cache is fine; a dimension
     the state does not have is 1); parents [B, W_out] int32 (-1 leaves a slot as
     it is); lens [B] int32 or None; out [G, B, W_out, H, L, D] of the same
-    type (None: a new tensor of zeros); status: an int32 [B] tensor to receive
-    the request status, or None."""
+    type (None: a new tensor of zeros; no entry of it may overlap one of the
+    state's, interleaved parts of one cache are fine); status: an int32 [B]
+    tensor to receive the request status, or None."""
     if out is not None and status is None:
         r = _native.binding().beam_reorder(state, parents, out, lens)
         if r is not None:

@@ -9,9 +9,13 @@
 // or above it, and little else is: with n of U parts occupied about
 // U ln(U / (U - n)) elements (89 for n = 64 of 128).  Only the 32-element
 // groups whose max reaches the bound are read again (from L2), their elements
-// at or above it are listed, and the list is sorted by counting.  When the
-// list does not fit (long rows of equal logits), each row is selected by radix
-// descent on whole-number keys, 8 bits a pass.
+// at or above it are listed, and the list is sorted by counting.  When large
+// logits crowd at neighbouring tokens the list is longer (logits that fall with
+// the token's id, 912 rows of 152064 bf16, k = 64: 54 us with a spread of 3 around
+// the slope, 85 us with 1.5, against 51 us shuffled).  When the list does not fit
+// (long rows of equal logits, sorted rows, steep slopes), each row is selected by
+// radix descent on whole-number keys, 8 bits a pass, by one CTA: 1.3 ms a row of
+// 152064 logits, 5.7 ms for 912.
 #pragma once
 
 #include <type_traits>

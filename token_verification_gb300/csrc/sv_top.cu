@@ -11,9 +11,9 @@
 // candidates go to the leader CTA's list, before a cluster barrier.
 //
 // It is bound by the chain of its steps - launch, stream, exchange, bound, reload,
-// sort -, not by bytes: 1 to 8 rows of 32000 to 128256 bf16 logits take 6.4 to 6.9
-// us (k = 32), four beams of 32000 7.6 us. Ordering cluster barriers in place of
-// the counted stores cost 0.7 us.
+// sort -, not by bytes: 1 to 8 rows of 64000 to 128256 bf16 logits take 6.0 to 6.4
+// us (k = 32, calls of a captured graph), four beams of 32000 7.8 us. Ordering
+// cluster barriers in place of the counted stores cost 0.7 us.
 //
 // A beam's candidates compare by their scores in 64 bits (tied_before: and then), a
 // record's by their logits.  Bounds are in fp32 rounded down, which can only lengthen the list.
@@ -316,8 +316,11 @@ bool record_by_rows(sv_dtype dtype, long long rows, int V) {
 }
 // Beams go through the row kernel in two launches. (us, cluster / rows, n = 16,
 // bf16: 1 x 4 of 32000 8.1 / 9.9; 100 x 4 of 32000 (26 MB) 12.1 / 16.9; 16 x 8 of
-// 128256 (33 MB) 17.8 / 15.1; 1 x 16 of 128256 21.6 / 14.9, a cluster's CTAs
-// having two beams each.)
+// 128256 (33 MB) 17.8 / 15.1.  Past 8 beams a cluster's CTAs have two or more
+// each, at any V: one request of 9, 16, 32, 64 beams of 1000 tokens 10.0 / 9.8,
+// 10.5 / 9.9, 15.9 / 10.1, 27.3 / 10.1; of 32000 11.8 / 10.5, 12.3 / 10.8, 19.1 /
+// 11.0, 33.6 / 11.0; eight requests of 9 and 64 beams of 8000 10.1 / 9.8 and
+// 29.3 / 14.3.)
 bool beams_by_rows(sv_dtype dtype, int B, int W, int V) {
   const long long bytes = (long long)B * W * V * (dtype == SV_BF16 ? 2 : 4);
   return (W > 8 || bytes > (28ll << 20)) && top_rows_fit(V);
