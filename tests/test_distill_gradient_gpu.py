@@ -191,3 +191,18 @@ def test_mass_past_the_range():
         assert torch.isnan(o.loss).tolist() == [[False, True, False]]
     for g in (out.grad, grad):
         assert not bool(g[0, 1].any()) and bool(g[0, 0].any())
+
+
+@pytest.mark.parametrize("T", [1.0, 64.0, 1e6])
+def test_ruled_out_token_of_the_least_mass(T):
+    """A recorded token of a probability near fp32's least, which the student rules out: the
+    loss is +inf, as for any p > 0."""
+    s, ids, t, _, gl = case(1, 2, 1000, 4, F32, T, 12)
+    t[:, :, 0] = 0.0
+    t[:, :, 1:] = torch.tensor([-101.0, -102.0, -400.0], device="cuda") * T  # p: 1e-44, 6e-45, 0
+    s[0, 0, ids[0, 0, 1].long()] = -math.inf
+    s[0, 1, ids[0, 1, 3].long()] = -math.inf  # (no mass there: a term of 0)
+    out = api.spec_distill(s, ids, t, T, grad_loss=gl)
+    assert not bool(out.status.any())
+    assert float(out.loss[0, 0]) == math.inf and math.isfinite(float(out.loss[0, 1]))
+    assert bool(torch.isfinite(out.grad).all())

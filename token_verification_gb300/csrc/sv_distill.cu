@@ -330,7 +330,10 @@ __device__ float row_loss(const DistillShared& s, const DistillParams& p, const 
     if (s.p[j] > 0.f) {
       const float d = (s.t[j] - s.t_max) - (s.sv[j] - r.M), x = d * p.inv_t;
       // (a masked token of the type's lowest value may pass the range before p_j counts)
-      loss = is_finite(x) ? fmaf(s.p[j], x - k, loss) : fmaf(s.p[j] * p.inv_t, d, loss);
+      // (and one of no student mass is +inf, where p_j / T may be 0)
+      loss = is_finite(x)      ? fmaf(s.p[j], x - k, loss)
+             : d == INFINITY ? INFINITY
+                             : fmaf(s.p[j] * p.inv_t, d, loss);
     }
   loss = warp_sum(loss);
   if (s.p_rest > 0.f) {
