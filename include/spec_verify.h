@@ -66,7 +66,8 @@ typedef enum sv_status {
   SV_ERR_WORKSPACE = 6,   /* workspace NULL, not 256-byte aligned, or too small */
   SV_ERR_CUDA = 7,        /* a CUDA runtime call or kernel launch failed */
   SV_ERR_FILTER = 8,      /* top_k negative, top_p outside (0, 1], or eps / delta negative */
-  SV_ERR_ALIAS = 9        /* an output overlaps an input that it must not overlap */
+  SV_ERR_ALIAS = 9,       /* an output overlaps an input that it must not overlap */
+  SV_ERR_SCORE = 10       /* attention scale or softcap not finite, softcap or window negative */
 } sv_status;
 
 typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
@@ -78,6 +79,7 @@ typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_REQ_TIMEOUT 8       /* a bounded wait for staged logits gave up (device fault, or
                                   the limit of spec_verify_set_wait_limit_ns ran out) */
 #define SV_REQ_BAD_TREE 16     /* the request's parent array is not a tree of depth <= max_depth */
+#define SV_REQ_BAD_PAGE 32     /* a page that the request needs is not one of the cache's */
 
 /* Limits. */
 #define SV_MAX_K 31             /* draft positions per request */
@@ -89,6 +91,9 @@ typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_MAX_BEAMS 64         /* beams per request */
 #define SV_MAX_ROWS (1 << 27)   /* rows (B * P) of a top-logits or distillation call */
 #define SV_MAX_DISTILL_ROW 1572864 /* bytes of a student row (V * sizeof(logit)) */
+#define SV_MAX_STEP 257         /* tokens of a verification step: a tree's nodes and its root */
+#define SV_MAX_HEADS 1024       /* heads of a layer */
+#define SV_MAX_SLOTS (1 << 27)  /* tokens a request's page table can hold */
 
 /* Bytes of workspace that spec_verify_sample / _greedy need for B requests
  * of K draft positions over a vocabulary of V (the dense-draft sampling case,
@@ -536,6 +541,112 @@ sv_status spec_beam_reorder(const void* state, const int64_t* state_strides,
                             const int32_t* parents, const int32_t* lens, void* out,
                             const int64_t* out_strides, int32_t* out_status, int G, int B, int W,
                             int W_out, int H, int L, int row_bytes, sv_stream_t stream);
+
+/* A key/value cache held in 4 bits, for the layer that scores a step's tokens.
+ *
+ * The cache is `pages` pages of page_size tokens, each token's keys and values of
+ * every head quantised in groups of 32 values: a scale byte c stands for
+ *     s = (1 + (c mod 8) / 8) * 2^(floor(c / 8) - 20),   c = 0..238 (s up to 896),
+ * the least with 7 s >= the group's largest magnitude, and each value for the nearest
+ * whole multiple q of s, ties to even, q = -7..7 (magnitudes above 7 * 896 = 6272
+ * become 6272).  A token of which a head's keys or values hold NaN or infinity reads
+ * back as NaN throughout that head, and attention rows that see it are NaN there.
+ *
+ *   cache       `pages` pages, page_stride bytes apart (a multiple of 16; the
+ *               layers of a model may be interleaved), 16-byte aligned.  A page is
+ *               [kv_heads, 2 (keys, values), spec_cache_page_bytes]: for each
+ *               head, page_size rows of head_dim / 2 code bytes, then scale bytes
+ *               [page_size / 16, head_dim / 32, 16 (tokens)].  A row is
+ *               little-endian words of 8 values, value i's q + 8 in bits
+ *               4 (i / 2 + 4 (i mod 2)) onwards.
+ *   table       [B, M] int32: the pages of request b's slots 0 .. M * page_size - 1.
+ *               A page that is written belongs to one request; pages that are
+ *               only read (a shared prefix) may occur in any number of rows.
+ *               Entries whose slots a call does not touch are not read.
+ *   start       [B] int32: the first slot of the request that the call touches.
+ *   page_size   16, 32, 64, 128 or 256; head_dim 64, 128 or 256; M * page_size <=
+ *               SV_MAX_SLOTS, kv_heads <= SV_MAX_HEADS, 0 <= B <= SV_MAX_B.
+ *   out_status  [B] int32 or NULL: SV_REQ_BAD_DRAFT_LEN (slots or lengths out of
+ *               range: nothing is done for the request), SV_REQ_BAD_PAGE (tokens
+ *               on such pages are skipped; attention rows that would see them are NaN).
+ * Calls need no workspace unless they name one, and none of the cache's contents
+ * is ever read beyond the slots in use. */
+
+/* Bytes of a page of one head's keys (or values); 0 when not supported. */
+size_t spec_cache_page_bytes(int page_size, int head_dim);
+
+/* Writes tokens: request b's token i < lens[b] (NULL: N) goes to slot start[b] + i.
+ *
+ *   k, v        [B, N, kv_heads, head_dim] dtype at byte strides k_strides[3],
+ *               v_strides[3] of b, n and h (>= 0, multiples of 16, 16-byte aligned; each
+ *               row of head_dim values contiguous).
+ * B * N * kv_heads < 2^31. */
+sv_status spec_cache_write(void* cache, int64_t page_stride, const void* k,
+                           const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                           const int32_t* table, const int32_t* start, const int32_t* lens,
+                           int32_t* out_status, sv_dtype dtype, int pages, int page_size, int B,
+                           int N, int M, int kv_heads, int head_dim, sv_stream_t stream);
+
+/* Reads tokens back: k[b, i] and v[b, i] of slot start[b] + i (NULL: slot i) for
+ * i < lens[b] (NULL: N); rows behind lens[b] are left as they are.  Every value is exact in
+ * either type.  k and v as in spec_cache_write; rows of one must not overlap each
+ * other (SV_ERR_ALIAS), nor the other's or the cache. */
+sv_status spec_cache_read(const void* cache, int64_t page_stride, void* k,
+                          const int64_t* k_strides, void* v, const int64_t* v_strides,
+                          const int32_t* table, const int32_t* start, const int32_t* lens,
+                          int32_t* out_status, sv_dtype dtype, int pages, int page_size, int B,
+                          int N, int M, int kv_heads, int head_dim, sv_stream_t stream);
+
+/* Keeps the accepted path of a tree whose nodes lie in slots start[b] + node: slot
+ * start[b] + path[b, i] moves to start[b] + i, for the entries before the first -1
+ * (path = out_path of a tree call).  The request then has start[b] + accept_len
+ * tokens.  Entries must ascend from 0 or above: SV_REQ_BAD_TREE otherwise, and nothing is
+ * moved for the request.  0 <= P <= SV_MAX_STEP. */
+sv_status spec_cache_keep(void* cache, int64_t page_stride, const int32_t* table,
+                          const int32_t* start, const int32_t* path, int32_t* out_status,
+                          int pages, int page_size, int B, int P, int M, int kv_heads,
+                          int head_dim, sv_stream_t stream);
+
+/* Attention of a step's tokens over the cache, which holds them already ("推测解码与
+ * MTP" §3.3 "Tree Attention": a node sees its ancestors only).  Request b's token i < n
+ * (n = q_lens[b], NULL: N) is in slot base + i, base = lens[b] - n, and
+ *     out[b, i, h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(x_j),
+ *     x_j = c(scale * q . k_j) - slopes[h] * (at_i - at_j),
+ * over the slots j that it sees, c(x) = softcap * tanh(x / softcap) or x itself.  It sees
+ * every slot before base; of the step's own, those up to itself, or in a tree
+ * its ancestors and itself.  A slot's position at_j is j before base, base + i for
+ * the i-th token of a chain, base + depth for a tree's node.  With a window, only
+ * slots with at_i - at_j < window are seen.
+ *
+ *   q           [B, N, q_heads, head_dim] dtype at byte strides q_strides[3] as of
+ *               k; q_heads a multiple of kv_heads, heads in groups of q_heads /
+ *               kv_heads to a key/value head; 0 <= N <= SV_MAX_STEP.
+ *   lens        [B] int32: slots in use, the step's own among them.  lens[b]
+ *               outside [n, M * page_size] or q_lens[b] outside [0, N]:
+ *               SV_REQ_BAD_DRAFT_LEN, and the request's rows are 0.
+ *   tree_parent, parent_stride (0 or N - 1): as in spec_verify_tree for a tree of
+ *               N - 1 candidate nodes, n - 1 of them in use; NULL: a chain.  No tree:
+ *               SV_REQ_BAD_TREE, and the request's rows are 0.
+ *   slopes      [q_heads] fp32 or NULL (no bias).
+ *   scale       finite.  softcap finite, 0: none.  window 0: none.
+ *   out         [B, N, q_heads, head_dim] dtype, contiguous, 16-byte aligned; rows
+ *               behind q_lens[b] are left as they are.
+ *   out_lse     [B, N, q_heads] fp32 or NULL: log sum_j exp(x_j).
+ *   workspace   >= spec_cache_attention_workspace_size bytes (of the current
+ *               device), 16-byte aligned.  It needs no preparation and holds nothing
+ *               between calls; calls that may overlap need one each.
+ * Sums are of 32-bit terms; weights are rounded to 11 bits before they meet the
+ * values (22 bits in fp32).  Results do not vary between calls of the same lengths. */
+size_t spec_cache_attention_workspace_size(sv_dtype dtype, int N, int q_heads, int kv_heads,
+                                           int head_dim);
+sv_status spec_cache_attention(const void* q, const int64_t* q_strides, const void* cache,
+                               int64_t page_stride, const int32_t* table, const int32_t* lens,
+                               const int32_t* q_lens, const int32_t* tree_parent,
+                               int parent_stride, const float* slopes, float scale, float softcap,
+                               int window, void* out, float* out_lse, int32_t* out_status,
+                               sv_dtype dtype, int pages, int page_size, int B, int N, int M,
+                               int q_heads, int kv_heads, int head_dim, void* workspace,
+                               size_t ws_bytes, sv_stream_t stream);
 
 /* Allocation-free variant of spec_verify_sample.  The pages have no
  * counterpart to this entry point; it exists for callers that cannot

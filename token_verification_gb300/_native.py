@@ -21,7 +21,8 @@ SYMBOLS = (
     "spec_verify_tree_sample", "spec_verify_set_wait_limit_ns", "spec_verify_wait_limit_ns",
     "spec_top_logits", "spec_distill", "spec_distill_grad", "spec_beam_select",
     "spec_beam_workspace_size",
-    "spec_beam_reorder",
+    "spec_beam_reorder", "spec_cache_page_bytes", "spec_cache_write", "spec_cache_read",
+    "spec_cache_keep", "spec_cache_attention", "spec_cache_attention_workspace_size",
 )
 
 BINDING_PATH = os.path.join(HERE, "_binding.so")
@@ -115,6 +116,20 @@ def lib():
         l.spec_beam_select.restype = I
         l.spec_beam_reorder.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]
         l.spec_beam_reorder.restype = I
+        L = ctypes.c_int64
+        l.spec_cache_page_bytes.argtypes = [I, I]
+        l.spec_cache_page_bytes.restype = Z
+        l.spec_cache_write.argtypes = [P, L, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P]
+        l.spec_cache_write.restype = I
+        l.spec_cache_read.argtypes = l.spec_cache_write.argtypes
+        l.spec_cache_read.restype = I
+        l.spec_cache_keep.argtypes = [P, L, P, P, P, P, I, I, I, I, I, I, I, P]
+        l.spec_cache_keep.restype = I
+        l.spec_cache_attention_workspace_size.argtypes = [I, I, I, I, I]
+        l.spec_cache_attention_workspace_size.restype = Z
+        l.spec_cache_attention.argtypes = [P, P, P, L, P, P, P, P, I, P, F, F, I, P, P, P, I, I, I,
+                                           I, I, I, I, I, I, P, Z, P]
+        l.spec_cache_attention.restype = I
         l.spec_verify_status_string.argtypes = [I]
         l.spec_verify_status_string.restype = ctypes.c_char_p
         l.spec_verify_version.argtypes = []

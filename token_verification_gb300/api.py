@@ -22,6 +22,7 @@ REQ_BAD_LOGITS = 2
 REQ_BAD_DRAFT_LEN = 4
 REQ_TIMEOUT = 8
 REQ_BAD_TREE = 16
+REQ_BAD_PAGE = 32
 MAX_K = 31
 
 
@@ -705,4 +706,212 @@ def spec_beam_reorder(state, parents, out=None, *, lens=None, status=None) -> to
             _Strides(b0 * size, b1 * size, b2 * size, b3 * size, b4 * size), _addr(status), G, B,
             W, W_out, H, L, D * size)
     _written(out if given else None, status)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the 4-bit key/value cache
+# ---------------------------------------------------------------------------
+
+_Strides3 = ctypes.c_int64 * 3
+
+
+def spec_cache_alloc(pages, kv_heads, head_dim, page_size=64, device="cuda") -> torch.Tensor:
+    """A cache of `pages` pages for one layer (see spec_verify.h): zeros, uint8
+    [pages, kv_heads, 2, page bytes].  The cache calls also take a layer's part of a larger
+    tensor, [pages, layers, kv_heads, 2, page bytes][:, layer] for one."""
+    size = int(_native.lib().spec_cache_page_bytes(int(page_size), int(head_dim)))
+    if size == 0:
+        raise ValueError("unsupported page_size=%s head_dim=%s" % (page_size, head_dim))
+    return torch.zeros((pages, kv_heads, 2, size), dtype=torch.uint8, device=device)
+
+
+def _cache_args(cache, table, head_dim):
+    """(device, page stride, pages, page size, B, M, kv heads) of a cache and its table."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 4:
+        raise ValueError("cache must be a [pages, kv_heads, 2, page bytes] tensor")
+    device = cache.device
+    if device.type != "cuda":
+        raise ValueError("cache must be a CUDA tensor")
+    if cache.dtype != torch.uint8:
+        raise TypeError("cache must be torch.uint8 (got %s)" % cache.dtype)
+    pages, heads, two, size = cache.shape
+    head_dim = int(head_dim)
+    token = head_dim // 2 + head_dim // 32
+    page_size = size // token if token > 0 else 0
+    if two != 2 or _native.lib().spec_cache_page_bytes(page_size, head_dim) != size:
+        raise ValueError("cache %s does not hold pages of head_dim %d" % (tuple(cache.shape),
+                                                                          head_dim))
+    if cache.stride()[1:] != (2 * size, size, 1):
+        raise ValueError("the pages of cache must be contiguous")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be a [B, M] tensor")
+    B, M = table.shape
+    _need(table, "table", device, torch.int32, (B, M))
+    return device, cache.stride(0), pages, page_size, B, M, heads
+
+
+def _dense(t, name, device, dtype, shape):
+    """Byte strides of a [B, N, H, D] tensor with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError("%s must be a [B, N, heads, head_dim] tensor" % name)
+    if t.device != device:
+        raise ValueError("%s must be on %s (got %s)" % (name, device, t.device))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    a, b, c, d = t.stride()
+    if t.shape[3] > 1 and d != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    e = t.element_size()
+    if t.data_ptr() % 16 or any(t.shape[i] > 1 and s * e % 16 for i, s in enumerate((a, b, c))):
+        raise ValueError("the rows of %s must start on 16-byte boundaries" % name)
+    return _Strides3(a * e, b * e, c * e)
+
+
+def _per_request(device, B, **named):
+    for name, t in named.items():
+        if t is not None:
+            _need(t, name, device, torch.int32, (B,))
+
+
+def spec_cache_write(cache, k, v, table, start, *, lens=None, status=None) -> torch.Tensor:
+    """Quantise a step's (or a prompt's) keys and values into the cache (see
+    spec_verify.h): token i of request b goes to slot start[b] + i.
+
+    cache: as spec_cache_alloc makes it; k, v [B, N, kv_heads, head_dim] CUDA
+    bf16/fp32 with contiguous rows on 16-byte boundaries, at any strides (parts of a
+    fused projection are fine); table [B, M] int32 page ids; start [B] int32; lens
+    [B] int32 (tokens i >= lens[b] are left out) or None; status: an int32 [B]
+    tensor to receive the request status, or None.  Returns cache."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, N, kv_heads, head_dim] tensor")
+    D = k.shape[3]
+    device, stride, pages, page_size, B, M, H = _cache_args(cache, table, D)
+    N = k.shape[1]
+    code = _dtype_code(k)
+    ks = _dense(k, "k", device, None, (B, N, H, D))
+    vs = _dense(v, "v", device, k.dtype, (B, N, H, D))
+    if start is None:
+        raise ValueError("start is required")
+    _per_request(device, B, start=start, lens=lens, status=status)
+    _launch(device, _native.lib().spec_cache_write, cache.data_ptr(), stride, k.data_ptr(), ks,
+            v.data_ptr(), vs, _addr(table), _addr(start), _addr(lens), _addr(status), code, pages,
+            page_size, B, N, M, H, D)
+    _written(cache, status)
+    return cache
+
+
+def spec_cache_read(cache, table, n, head_dim, k=None, v=None, *, start=None, lens=None,
+                    dtype=torch.bfloat16, status=None):
+    """Read n tokens of each request back (see spec_verify.h): (k, v), each
+    [B, n, kv_heads, head_dim], token i of slot start[b] + i (start None: slot i)
+    for i < lens[b] (None: n).  k, v: tensors to write, rows behind lens[b]
+    left as they are; None: new ones of `dtype`, zero there."""
+    device, stride, pages, page_size, B, M, H = _cache_args(cache, table, head_dim)
+    n, D = int(n), int(head_dim)
+    if n < 0:
+        raise ValueError("n must be >= 0")
+    if (k is None) != (v is None):
+        raise ValueError("k and v must be given together")
+    _per_request(device, B, start=start, lens=lens, status=status)
+    given = k is not None
+    if not given:
+        # (every row is written where there are no lens and nothing is out of range)
+        k, v = (torch.zeros((B, n, H, D), dtype=dtype, device=device) for _ in range(2))
+    code = _dtype_code(k)
+    ks = _dense(k, "k", device, None, (B, n, H, D))
+    vs = _dense(v, "v", device, k.dtype, (B, n, H, D))
+    _launch(device, _native.lib().spec_cache_read, cache.data_ptr(), stride, k.data_ptr(), ks,
+            v.data_ptr(), vs, _addr(table), _addr(start), _addr(lens), _addr(status), code, pages,
+            page_size, B, n, M, H, D)
+    _written(*((k, v) if given else ()), status)
+    return k, v
+
+
+def spec_cache_keep(cache, table, start, path, head_dim, *, status=None) -> torch.Tensor:
+    """Keep a verified tree's accepted path (see spec_verify.h): slot start[b] +
+    path[b, i] moves to slot start[b] + i, up to the first -1.  path [B, P]
+    int32, out_path of a tree call; the request then has start + accept_len tokens.
+    Returns cache."""
+    device, stride, pages, page_size, B, M, H = _cache_args(cache, table, head_dim)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be a [B, P] tensor")
+    P = path.shape[1]
+    _need(path, "path", device, torch.int32, (B, P))
+    if start is None:
+        raise ValueError("start is required")
+    _per_request(device, B, start=start, status=status)
+    _launch(device, _native.lib().spec_cache_keep, cache.data_ptr(), stride, _addr(table),
+            _addr(start), _addr(path), _addr(status), pages, page_size, B, P, M, H, int(head_dim))
+    _written(cache, status)
+    return cache
+
+
+@dataclass
+class AttentionOutputs:
+    out: torch.Tensor                     # [B, N, q_heads, head_dim]
+    lse: Optional[torch.Tensor] = None    # [B, N, q_heads] fp32
+    status: Optional[torch.Tensor] = None  # [B]
+
+
+def spec_cache_attention(q, cache, table, lens, out: Optional[AttentionOutputs] = None, *,
+                         q_lens=None, parent=None, scale=None, softcap=0.0, window=0, slopes=None,
+                         lse=False, status=True) -> AttentionOutputs:
+    """Attention of a step's tokens over the 4-bit cache that holds them (see
+    spec_verify.h): q [B, N, q_heads, head_dim] CUDA bf16/fp32, lens [B] int32
+    slots in use (the step's own among them), q_lens [B] int32 tokens of the step or
+    None (N); parent [N-1] or [B, N-1] int32, the candidate tree as
+    spec_verify_tree takes it (None: a chain); scale None: head_dim ** -0.5;
+    softcap: scores become softcap * tanh(score / softcap); window: slots further back
+    are not seen; slopes [q_heads] fp32: scores lose slope * distance.  Rows behind
+    q_lens[b] are left as they are in a given out, and zero in a new one."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, N, q_heads, head_dim] tensor")
+    B, N, Hq, D = q.shape
+    device, stride, pages, page_size, Bt, M, H = _cache_args(cache, table, D)
+    if Bt != B:
+        raise ValueError("table must have %d rows (got %d)" % (B, Bt))
+    code = _dtype_code(q)
+    qs = _dense(q, "q", device, None, None)
+    if H == 0 or Hq % H:
+        raise ValueError("q_heads %d must be a multiple of kv_heads %d" % (Hq, H))
+    if lens is None:
+        raise ValueError("lens is required")
+    _per_request(device, B, lens=lens, q_lens=q_lens)
+    parent_stride = 0
+    if parent is not None:
+        if not isinstance(parent, torch.Tensor) or parent.dim() not in (1, 2):
+            raise ValueError("parent must be a [N-1] or [B, N-1] tensor")
+        _need(parent, "parent", device, torch.int32,
+              (N - 1,) if parent.dim() == 1 else (B, N - 1))
+        if parent.dim() == 2:
+            parent_stride = N - 1
+        if N < 2:
+            parent = None
+    if slopes is not None:
+        _need(slopes, "slopes", device, torch.float32, (Hq,))
+    given = out is not None
+    if not given:
+        make = torch.empty if q_lens is None else torch.zeros
+        out = AttentionOutputs(
+            make((B, N, Hq, D), dtype=q.dtype, device=device),
+            make((B, N, Hq), dtype=torch.float32, device=device) if lse else None,
+            torch.empty((B,), dtype=torch.int32, device=device) if status else None)
+    else:
+        _need(out.out, "out.out", device, q.dtype, (B, N, Hq, D))
+        _given(out, device, lse=(torch.float32, (B, N, Hq)), status=(torch.int32, (B,)))
+    lib = _native.lib()
+    with torch.cuda.device(device):
+        need = lib.spec_cache_attention_workspace_size(code, N, Hq, H, D)
+    # scratch of this call alone (stream-ordered, and a captured graph's own)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    _launch(device, lib.spec_cache_attention, q.data_ptr(), qs, cache.data_ptr(), stride,
+            _addr(table), _addr(lens), _addr(q_lens), _addr(parent), parent_stride, _addr(slopes),
+            float(D ** -0.5 if scale is None else scale), float(softcap), int(window),
+            out.out.data_ptr(), _addr(out.lse), _addr(out.status), code, pages, page_size, B, N, M,
+            Hq, H, D, _addr(ws), need)
+    if given:
+        _written(out.out, out.lse, out.status)
     return out

@@ -1,0 +1,227 @@
+// sv_attend.cuh - attention over the 4-bit cache: parameters, the split of a
+// call's work over CTAs, masks and scores, shared by the kernels; internal.
+//
+// A unit of work is a tile of query rows (of the step's tokens and the
+// heads of one key/value head) against the slots that its request sees.  The slots come in
+// chunks; all chunks of all units, laid end to end, are cut into equal shares,
+// one a CTA, so that ragged lengths and few long requests keep every SM busy alike.
+// A CTA walks its share's pieces (runs of chunks of one unit).  A piece that
+// is not a whole unit leaves its rows' running max, sum and weighted values in
+// the workspace, and a second kernel joins a unit's pieces in order.  Which
+// CTA does what depends on the lengths alone, so results do not vary from run to run.
+#pragma once
+
+#include "sv_cache.cuh"
+#include "sv_launch.h"
+
+namespace sv {
+
+constexpr int kMaxStep = 257;                    // tokens of a step (a tree of 256 nodes and its root)
+constexpr int kSeenWords = (kMaxStep + 31) / 32;  // bits of one node's ancestors
+// Weights are 2^(score - max + kShift), at most 2^15: fp16's least step of 2^-24
+// is then 2^-39 of the row's largest weight.
+constexpr float kShift = 15.f;
+
+struct AttendParams {
+  CacheView cache;
+  const void* q;             // [B, N, Hq, D] at element strides
+  long long qb, qn, qh;
+  void* out;                 // [B, N, Hq, D]
+  float* out_lse;            // [B, N, Hq] or null
+  int* out_status;           // [B] or null
+  const int* lens;           // [B] slots in use, the step's own among them
+  const int* q_lens;         // [B] tokens of the step, or null (N)
+  const int* parent;         // request b's tree at parent + b * parent_stride, or null (a chain)
+  int parent_stride;
+  const float* slopes;       // [Hq] or null
+  int B, N, Hq, group;       // group = Hq / Hkv
+  int window;                // 0: none
+  float scale, softcap;      // softcap 0: none
+  // the split
+  int rows;                  // query rows of a unit
+  int chunk;                 // slots of a chunk
+  int least;                 // chunks that are worth a CTA
+  int* desc;                 // [G][4] the split unit that begins in each CTA's share: b, head, row tile, pieces
+  float* part;               // [2 G][rows][D + 4] unfinished rows: values, max, sum
+};
+
+// What a request's arguments come to.
+struct Request {
+  int len, nq, base;  // slots, tokens of the step, slot of the first of them
+  int lo;             // first slot that any of them sees
+  int chunks, tiles;  // of each of its units; units of a head
+  bool ok;
+};
+
+__device__ __forceinline__ Request request_of(const AttendParams& p, int b) {
+  Request r;
+  r.len = p.lens[b];
+  r.nq = p.q_lens ? p.q_lens[b] : p.N;
+  r.ok = r.nq >= 0 && r.nq <= p.N && r.len >= r.nq &&
+         r.len <= ((long long)p.cache.M << p.cache.shift);
+  if (!r.ok) {  // (its rows come out as rows that see nothing)
+    r.len = 0;
+    r.nq = p.N;
+  }
+  r.base = r.len - r.nq;
+  r.lo = 0;
+  if (!r.ok) {
+    r.base = 0;
+  } else if (p.window > 0) {
+    r.lo = max(0, r.base - (p.window - 1));
+  }
+  r.tiles = (r.nq * p.group + p.rows - 1) / p.rows;
+  r.chunks = r.tiles == 0 ? 0 : max(1, (r.len + p.chunk - 1) / p.chunk - r.lo / p.chunk);
+  return r;
+}
+
+__device__ __forceinline__ long long work_of(const AttendParams& p, int b) {
+  const Request r = request_of(p, b);
+  return (long long)r.chunks * r.tiles * p.cache.Hkv;
+}
+
+// The CTA's share [begin, end) of the call's chunks, and the request and offset in
+// it where the share begins.  Every thread of the block (T of them) takes part; smem: T / 32 + 3
+// long longs.
+struct Share {
+  long long begin, end, total;
+  int b;          // request of `begin`
+  long long at;   // `begin` counted from that request's first chunk
+  int G;          // CTAs with a share
+};
+
+template <int T>
+__device__ __forceinline__ long long block_scan(long long x, long long* smem, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) smem[warp] = x;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) {
+    if (w < warp) before += smem[w];
+    all += smem[w];
+  }
+  *total = all;
+  return x + before;
+}
+
+template <int T>
+__device__ __forceinline__ Share find_share(const AttendParams& p, int cta, int ctas,
+                                            long long* smem) {
+  Share s;
+  const int t = threadIdx.x;
+  long long mine = t < p.B ? work_of(p, t) : 0, total;
+  const long long first_scan = block_scan<T>(mine, smem, &total);
+  const long long first_total = total;
+  for (int b0 = T; b0 < p.B; b0 += T) {
+    long long part;
+    block_scan<T>(b0 + t < p.B ? work_of(p, b0 + t) : 0, smem, &part);
+    total += part;
+  }
+  s.total = total;
+  const long long want = (total + p.least - 1) / p.least;
+  s.G = (int)(want < ctas ? want : ctas);
+  s.begin = s.end = s.at = 0;
+  s.b = 0;
+  if (cta >= s.G) return s;
+  s.begin = total * cta / s.G;
+  s.end = total * (cta + 1) / s.G;
+  long long before = 0, scan = first_scan, part = first_total;
+  long long* found = smem + T / 32;
+  for (int b0 = 0;; b0 += T) {
+    if (b0 > 0) {
+      mine = b0 + t < p.B ? work_of(p, b0 + t) : 0;
+      scan = block_scan<T>(mine, smem, &part);
+    }
+    if (s.begin < before + part) {
+      const long long from = before + scan - mine;
+      if (from <= s.begin && s.begin < from + mine) {
+        found[0] = b0 + t;
+        found[1] = s.begin - from;
+      }
+      __syncthreads();
+      s.b = (int)found[0];
+      s.at = found[1];
+      __syncthreads();
+      return s;
+    }
+    before += part;
+  }
+}
+
+// How many CTAs' shares meet the unit [u0, u1) of whose chunks CTA `cta` holds the first.
+__device__ __forceinline__ int pieces_of(const Share& s, int cta, long long u1) {
+  int n = 1;
+  while (s.total * (cta + n) / s.G < u1) ++n;
+  return n;
+}
+
+// A request's tree in shared memory: which nodes each node sees, and its depth.
+struct TreeView {
+  uint32_t seen[kMaxStep][kSeenWords];
+  int depth[kMaxStep];
+  int parent[kMaxStep];
+  int bad;
+};
+
+// Builds it with the block's T threads; false when the parents are no tree.
+template <int T>
+__device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq, TreeView& tree) {
+  __syncthreads();
+  if (threadIdx.x == 0) tree.bad = 0;
+  __syncthreads();
+  const int* parent = p.parent + (long long)b * p.parent_stride;
+  for (int n = threadIdx.x; n < nq; n += T) {
+    const int up = n ? parent[n - 1] : -1;
+    tree.parent[n] = up;
+    if (n && (up < 0 || up >= n)) tree.bad = 1;
+  }
+  __syncthreads();
+  if (tree.bad) return false;
+  for (int n = threadIdx.x; n < nq; n += T) {
+#pragma unroll
+    for (int w = 0; w < kSeenWords; ++w) tree.seen[n][w] = 0;
+    int d = -1;
+    for (int at = n; at >= 0; at = tree.parent[at], ++d)
+      tree.seen[n][at >> 5] |= 1u << (at & 31);
+    tree.depth[n] = d;
+  }
+  __syncthreads();
+  return true;
+}
+
+// tanh by one exponential; 2^-22 of 1.
+__device__ __forceinline__ float tanh_fast(float x) {
+  return 1.f - __fdividef(2.f, ex2(x * (2.f * kLog2e)) + 1.f);
+}
+
+// A score in units of log2: scaled, capped, biased by the distance of the two positions.
+template <bool EXACT>
+__device__ __forceinline__ float score_of(const AttendParams& p, float x) {
+  if (p.softcap > 0.f) {
+    x = x * p.scale / p.softcap;
+    x = p.softcap * (EXACT ? tanhf(x) : tanh_fast(x));
+    return x * kLog2e;
+  }
+  return x * (p.scale * kLog2e);
+}
+
+// Joins the pieces of split units (launched behind either kernel).
+cudaError_t launch_join(const AttendParams& p, int D, int dtype, int ctas, int units,
+                        cudaStream_t stream);
+
+// The kernel for tiles of few rows and the one for many (tensor memory); they fill in the split.
+struct AttendPlan {
+  int rows, chunk, least, ctas;
+};
+cudaError_t plan_few(int D, int dtype, int rows, AttendPlan* plan);
+cudaError_t launch_few(const AttendParams& p, int D, int dtype, const AttendPlan& plan,
+                       cudaStream_t stream);
+
+}  // namespace sv

@@ -1,0 +1,82 @@
+// sv_cache.cuh - the 4-bit key/value cache: format, and what a request's
+// arguments say about its slots; internal.
+//
+// A page holds `page` tokens of each head: keys, then values, each as page
+// rows of D / 2 code bytes followed by scale bytes [page / 16][D / 32][16]
+// (tokens last, so that four tokens' scales of one group are one word).  A word
+// of codes holds 8 values, value i in nibble i / 2 + 4 (i % 2): masking a word
+// shifted by 4 p leaves values 2 p and 2 p + 1 in its two halves, as the low
+// bits of two 16-bit floats.
+//
+// A code c stands for (c - 8) s.  s has 4 significant bits and lies in
+// [2^-20, 896], so (c - 8) s has 7 and is exact in bf16 and in fp16 (the least,
+// 2^-23, is a multiple of fp16's 2^-24), and so are 136 s in bf16 and 72 s in
+// fp16 (at most 64512): one fused multiply-add turns 128 + c (bf16) or 64 + c
+// (fp16) into the exact value.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sv_common.cuh"
+
+namespace sv {
+
+constexpr int kGroup = 32;       // values of a token under one scale
+constexpr int kTopScale = 238;   // the largest scale byte: 896
+constexpr int kScaleBias = 856;  // byte + kScaleBias = the scale's fp32 bits >> 20
+constexpr int kNanScale = 255;   // keys of a token that held NaN or infinity
+constexpr int kBadPage = 32;     // SV_REQ_BAD_PAGE
+
+__host__ __device__ constexpr int page_bytes(int page, int D) {
+  return page * (D / 2 + D / kGroup);
+}
+
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return __uint_as_float((byte + kScaleBias) << 20);
+}
+
+// The least scale byte whose scale s has 7 s >= top (finite, >= 0).  7 s is
+// exact in fp32; top / 7 rounded to nearest is >= s exactly when top / 7 is
+// (s is an fp32 number), so cutting it to 4 bits gives the byte or the one below.
+__device__ __forceinline__ int scale_byte(float top) {
+  int b = (int)(__float_as_uint(__fdiv_rn(top, 7.f)) >> 20) - kScaleBias;
+  b = min(max(b, 0), kTopScale);
+  if (b < kTopScale && 7.f * scale_of(b) < top) ++b;
+  return b;
+}
+
+// Where tokens of a cache lie.
+struct CacheView {
+  char* data;
+  long long page_stride;  // bytes from one page to the next
+  const int* table;       // [B, M] page ids
+  int M;                  // pages a request can hold
+  int pages;              // pages of the cache
+  int shift;              // log2(tokens per page)
+  int Hkv;
+};
+
+// The block of page `id` for head h, keys (0) or values (1).
+template <int D>
+__device__ __forceinline__ char* page_block(const CacheView& c, int id, int h, int kv) {
+  return c.data + id * c.page_stride + (long long)((h * 2 + kv) * page_bytes(1, D)) * (1 << c.shift);
+}
+
+// Offset of the 16 scale bytes (16 tokens) of a group in a block, `token` = slot in the page.
+template <int D>
+__device__ __forceinline__ int scale_at(const CacheView& c, int token, int group) {
+  return (D / 2 << c.shift) + ((token >> 4) * (D / kGroup) + group) * 16;
+}
+
+// Request b's bits for the pages that hold slots [first, first + count): the
+// caller has checked that they lie inside the table.
+__device__ __forceinline__ int page_status(const CacheView& c, long long b, int first, int count) {
+  if (count <= 0) return 0;
+  int bad = 0;
+  for (int i = first >> c.shift; i <= (first + count - 1) >> c.shift; ++i)
+    bad |= (unsigned)c.table[b * c.M + i] >= (unsigned)c.pages;
+  return bad ? kBadPage : 0;
+}
+
+}  // namespace sv
