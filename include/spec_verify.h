@@ -552,8 +552,8 @@ sv_status spec_beam_reorder(const void* state, const int64_t* state_strides,
  * become 6272).  A token of which a head's keys or values hold NaN or infinity reads
  * back as NaN throughout that head, and attention rows that see it are NaN there.
  *
- *   cache       `pages` pages, page_stride bytes apart (a multiple of 16; the
- *               layers of a model may be interleaved), 16-byte aligned.  A page is
+ *   cache       `pages` pages, page_stride bytes apart (a multiple of 16 below
+ *               2^32; the layers of a model may be interleaved), 16-byte aligned.  A page is
  *               [kv_heads, 2 (keys, values), spec_cache_page_bytes]: for each
  *               head, page_size rows of head_dim / 2 code bytes, then scale bytes
  *               [page_size / 16, head_dim / 32, 16 (tokens)].  A row is

@@ -10,9 +10,13 @@ and the bias are roundings of at most 4 u of their own sizes; the cap's tanh is 
 exponent rounded by 2 u (|x| + |m|).  So a weight is off by E = the sum of these,
 relative; it is rounded to fp16 (2^-11; 2^-22 where a second fp16 takes the rest, in
 fp32), or lies where fp16's steps end: weights are scaled by 2^15, so a part is off by at
-most half of fp16's least step, 2^-25, which is 2^-40 of the row's largest weight.  The running sums add n terms in steps of 16 or more: (64 + n / 4) u.
+most half of fp16's least step, 2^-25, which is 2^-40 of the row's largest weight.  Calls of
+bf16 with more than 16 rows a key/value head scale by 2^7 against a reference that the
+row's max may exceed by up to 2^8: the largest weight is 2^7 or more there, and a weight off by
+at most 2^-25 / 2^7 = 2^-32 of it.  The running sums add n terms in steps of 16 or more: (64 + n / 4) u.
 With p the exact weights, o their result and W = sum_j p_j |v_j|:
-    |out - o| <= (round + 2 E + 2 (64 + n / 4) u) W + n 2^-40 max |v| + half a step of o,
+(step = 2^-40 or 2^-32)
+    |out - o| <= (round + 2 E + 2 (64 + n / 4) u) W + n step max |v| + half a step of o,
 and the log of the sum is within E + (64 + n / 4) u + 2 u |lse|.
 """
 import math
@@ -60,7 +64,7 @@ def decode(cache, page, D):
         s = scales[..., d // 32, :].flatten(-2)
         out[..., d] = ((byte >> (4 * (nib % 2))) & 15).double() - 8
         out[..., d] *= SCALES[s.clamp(max=TOP)]
-    nan = (scales[:, :, 0] == 255).any(-2).flatten(-2)
+    nan = (scales[:, :, 0] == 247).any(-2).flatten(-2)
     out[nan[:, :, None].expand(-1, -1, 2, -1)] = math.nan
     return out
 
@@ -87,7 +91,7 @@ def ancestors(parent, n):
     return sees, depth
 
 
-def attention(q, kv, base, sees, depth, scale, softcap, window, slopes, dtype):
+def attention(q, kv, base, sees, depth, scale, softcap, window, slopes, dtype, step=2.0 ** -40):
     """One request: q [n, Hq, D], kv [L, H, 2, D] float64.  (out, lse, tol, lse tol), rows that
     see nothing 0 and -inf."""
     n, Hq, D = q.shape
@@ -139,7 +143,7 @@ def attention(q, kv, base, sees, depth, scale, softcap, window, slopes, dtype):
         W = p @ v.abs()
         rounding = 2.0 ** (-22 if exact else -11)
         tol[:, h] = ((rounding + 2 * top + 2 * steps) * W
-                     + L * 2.0 ** -40 * v.abs().max()
+                     + L * step * v.abs().max()
                      + HALF_STEP[dtype] * o.abs() * 1.01 + 1e-37)
         ltol[:, h] = (top[:, 0] + steps + 2 * U * lse[:, h].abs().nan_to_num(0.0, 0.0, 0.0))
     return out, lse, tol, ltol
@@ -151,6 +155,8 @@ def check_attention(q, cache, page, table, lens, got, lse=None, q_lens=None, par
     B, N, Hq, D = q.shape
     dec = decode(cache, page, D)
     lens = lens.cpu()
+    many = q.dtype == torch.bfloat16 and D <= 128 and N * Hq // cache.shape[1] > 16
+    step = 2.0 ** (-32 if many else -40)
     got64 = got.cpu().double()
     for b in range(B):
         n = N if q_lens is None else int(q_lens[b])
@@ -164,7 +170,7 @@ def check_attention(q, cache, page, table, lens, got, lse=None, q_lens=None, par
         o, l, tol, ltol = attention(
             q[b, :n].cpu().double(), slots(dec, table[b], L), L - n, sees, depth,
             D ** -0.5 if scale is None else scale, softcap, window,
-            None if slopes is None else slopes.cpu().double(), q.dtype)
+            None if slopes is None else slopes.cpu().double(), q.dtype, step)
         off = (got64[b, :n] - o).abs()
         bad = ~(off <= tol)
         bad &= ~(torch.isnan(o) & torch.isnan(got64[b, :n]))

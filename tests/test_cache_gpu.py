@@ -49,7 +49,7 @@ def expected(cache, k, v, table, start, lens, page):
         x = torch.where(bad[..., None], 0.0, x.cpu().double())
         q, byte, _ = plain.quantise(x)
         if part == 0:
-            byte[bad] = 255
+            byte[bad] = 247
         w = (q + 8).unflatten(-1, (-1, 8))
         word = torch.zeros(w.shape[:-1], dtype=torch.int64)
         for i in range(8):

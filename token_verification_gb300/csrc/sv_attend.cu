@@ -5,8 +5,8 @@
 // Few rows (a token or a few drafts of a group of heads): bound by HBM, if the
 // decoding of the codes keeps up.  So no code passes through shared memory: a
 // warp's lanes load the cache's words straight into the registers of the tensor
-// instruction's fragments (m16n8k16) and decode them there, 1.4 instructions a value.
-//   S^T = K Q^T   A = 16 slots x 16 dimensions of keys in bf16, B = 8 query rows.
+// instruction's fragments (m16n8k16) and decode them there, 11 instructions a word of 8.
+//   S^T = K Q^T   A = 16 slots x 16 dimensions of keys in fp16, B = 8 query rows.
 //                 The order of the dimensions is free as long as Q's agrees: the
 //                 four lanes of a slot each take a quarter of its row, which is
 //                 one 16-byte load and one scale a slot at D = 128.
@@ -18,7 +18,7 @@
 // its 16-side would.  The weights move from the result's layout to the operand's by
 // movmatrix.  Scores are sums of exact products in 32 bits; weights are rounded to fp16
 // (2^-11 of each, against 2^-8 of the bf16 result; fp32 calls add a second
-// fp16 for the rest, and take Q as three bf16 numbers, which is exact).
+// fp16 number for the rest, of the weights and of Q).
 //
 // Each of the four warps of a CTA walks its own chunks of 32 slots with its own
 // running max and sum; the warps join at the end of a piece.
@@ -39,37 +39,13 @@ constexpr int kFewThreads = 128;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
@@ -79,7 +55,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// NW words from an address aligned to them.
+// NW words of shared memory, aligned to them.
 template <int NW>
 __device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[NW]) {
   if constexpr (NW == 1) {
@@ -96,87 +72,98 @@ __device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[NW]) {
   }
 }
 
-// A lane's words of 16 slots.  g = lane / 4, t = lane % 4; slots 4 (g / 2) + g % 2 and two on
-// of the keys, slots 4 t .. 4 t + 3 of the values.
+// 16 slots of a head in shared memory: key codes, value codes, their scales.  A lane takes (g =
+// lane / 4, t = lane % 4) a quarter of the keys of slots 4 (g / 2) + g % 2 and two on, and an eighth of
+// the values of slots 4 t .. 4 t + 3.  Every four rows a gap of 32 bytes (64 for keys of
+// 32-byte rows) keeps those loads off each other's banks.
 template <int D>
-struct Raw {
-  static constexpr int KW = D / 32, VW = D / 64;  // words of a slot
-  static constexpr int KG = KW > 4 ? KW / 4 : 1;  // groups of the lane's keys
-  uint32_t k[2][KW], v[4][VW], ks[KG], vs;
+struct Tile {
+  static constexpr int kRow = D / 2, kKeyGap = D == 64 ? 64 : 0, kValueGap = 32;
+  static constexpr int kValues = 16 * kRow + 4 * kKeyGap;            // offset of the values
+  static constexpr int kScales = kValues + 16 * kRow + 4 * kValueGap;  // and of the scales
+  static constexpr int kScaleBytes = D / 2;                          // of the keys (16 D / 32)
+  static constexpr int kBytes = kScales + 2 * kScaleBytes;
+  static constexpr int KW = D / 32, VW = D / 64;  // words a lane takes of a slot
+  static __device__ __forceinline__ int key(int n) { return n * kRow + (n >> 2) * kKeyGap; }
+  static __device__ __forceinline__ int value(int n) {
+    return kValues + n * kRow + (n >> 2) * kValueGap;
+  }
 };
 
-template <int D>
-__device__ __forceinline__ void load_raw(const CacheView& c, int id, int token, int h, Raw<D>& r) {
-  const int lane = lane_id(), g = lane / 4, t = lane % 4;
-  if ((unsigned)id >= (unsigned)c.pages) {  // no such page: slots of NaN
-#pragma unroll
-    for (int w = 0; w < Raw<D>::KW; ++w) r.k[0][w] = r.k[1][w] = 0;
-#pragma unroll
-    for (int w = 0; w < Raw<D>::VW; ++w) r.v[0][w] = r.v[1][w] = r.v[2][w] = r.v[3][w] = 0;
-#pragma unroll
-    for (int i = 0; i < Raw<D>::KG; ++i) r.ks[i] = 0xffffffffu;
-    r.vs = 0;
-    return;
-  }
-  const char* kb = page_block<D>(c, id, h, 0);
-  const char* vb = page_block<D>(c, id, h, 1);
-  constexpr int kRow = D / 2;
-  const int slot = token + 4 * (g >> 1) + (g & 1);
-  load_words<Raw<D>::KW>(kb + slot * kRow + t * (kRow / 4), r.k[0]);
-  load_words<Raw<D>::KW>(kb + (slot + 2) * kRow + t * (kRow / 4), r.k[1]);
-#pragma unroll
-  for (int i = 0; i < Raw<D>::KG; ++i) {
-    const int group = t * (D / 4) / kGroup + i;
-    r.ks[i] = *reinterpret_cast<const uint32_t*>(kb + scale_at<D>(c, token, group) + 4 * (g >> 1));
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    load_words<Raw<D>::VW>(vb + (token + 4 * t + i) * kRow + g * (kRow / 8), r.v[i]);
-  r.vs = *reinterpret_cast<const uint32_t*>(vb + scale_at<D>(c, token, g * (D / 8) / kGroup) + 4 * t);
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// A key scale byte as a pair of bf16, and -136 times it.
-__device__ __forceinline__ void key_scale(uint32_t byte, uint32_t& s, uint32_t& off) {
-  uint32_t x = (byte + kScaleBias) << 4;
-  if (byte == kNanScale) x = 0x7fff;
-  s = x | x << 16;
-  off = fma_bf16x2(s, 0xc308c308u, 0x80008000u);  // -136 s
+// Queues the copies of KT tiles of page `id` from `token` on (`head`: the head's keys in page 0); a
+// page that is none, or past the last slot in use (-1), gives keys of NaN and values that are finite.
+template <int D, int KT>
+__device__ __forceinline__ void queue_tiles(const CacheView& c, const char* head, int block,
+                                            int id, int token, char* stage) {
+  const int lane = lane_id();
+  constexpr int kPer = D / 32;       // 16-byte units of a row, and of a tile's scales
+  constexpr int kUnits = KT * kPer;  // of the tiles' scales
+  const int unit = lane % kUnits;
+  char* scales = stage + unit / kPer * Tile<D>::kBytes + Tile<D>::kScales + unit % kPer * 16 +
+                 (lane < kUnits ? 0 : Tile<D>::kScaleBytes);
+  if ((unsigned)id >= (unsigned)c.pages) {
+    const uint32_t x = lane < kUnits ? kNanScale * 0x01010101u : 0u;
+    if (lane < 2 * kUnits) *reinterpret_cast<uint4*>(scales) = make_uint4(x, x, x, x);
+    return;
+  }
+  const char* base = head + (unsigned long long)(unsigned)id * c.page_stride;
+  const char* k = base + (token * (D / 2) + lane * 16);
+  const char* v = k + block;
+  const int row = lane / kPer, x = lane % kPer * 16;
+  const uint32_t to = smem_u32(stage);
+#pragma unroll
+  for (int i = 0; i < KT * D / 64; ++i) {
+    const int tile = i / (D / 64), n = row + i % (D / 64) * (32 / kPer);
+    copy16(to + tile * Tile<D>::kBytes + Tile<D>::key(n) + x, k + i * 512);
+    copy16(to + tile * Tile<D>::kBytes + Tile<D>::value(n) + x, v + i * 512);
+  }
+  if (lane < 2 * kUnits)
+    copy16(smem_u32(scales), base + (((D / 2) << c.shift) + token * (D / kGroup) + unit * 16 +
+                                     (lane < kUnits ? 0 : block)));
 }
 
 template <int D, int NT, int NS>
-struct Query {  // B fragments of NT tiles of 8 rows, NS bf16 parts each
+struct Query {  // B fragments of NT tiles of 8 rows, NS fp16 parts each
   uint32_t b[NT][NS][D / 16][2];
 };
 
 // S^T of 16 slots: s[n] = {slot, row 2 t}, {slot, row 2 t + 1}, and the same two slots on.
 template <int D, int NT, int NS>
-__device__ __forceinline__ void scores(const Raw<D>& r, const Query<D, NT, NS>& q,
+__device__ __forceinline__ void scores(const char* tile, const Query<D, NT, NS>& q,
                                        float (&s)[NT][4]) {
-  const int g = lane_id() / 4;
+  const int lane = lane_id(), g = lane / 4, t = lane % 4;
+  const uint32_t sel = (g & 1) * 0x0101u;
 #pragma unroll
   for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-  uint32_t s0 = 0, o0 = 0, s1 = 0, o1 = 0;
+  using Q = Tile<D>;
+  uint32_t k[2][Q::KW];
+  const char* row = tile + Q::key(4 * (g >> 1) + (g & 1)) + t * (D / 8);
+  load_words<Q::KW>(row, k[0]);
+  load_words<Q::KW>(row + 2 * Q::kRow, k[1]);
+  const char* scales = tile + Q::kScales + t * (D / 4) / kGroup * 16 + 4 * (g >> 1);
+  Scale2 s0, s1;
 #pragma unroll
-  for (int w = 0; w < Raw<D>::KW; ++w) {
+  for (int w = 0; w < Q::KW; ++w) {
     if (w % 4 == 0) {
-      const uint32_t pair = r.ks[w / 4] >> ((g & 1) * 8);
-      key_scale(pair & 255, s0, o0);
-      key_scale((pair >> 16) & 255, s1, o1);
+      const uint32_t four = *reinterpret_cast<const uint32_t*>(scales + w / 4 * 16);
+      s0 = Scale2(four, 0x4040 + sel);
+      s1 = Scale2(four, 0x4242 + sel);
     }
+    uint32_t x0[4], x1[4];
+    decode_word(k[0][w], s0, x0);
+    decode_word(k[1][w], s1, x1);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      uint32_t a[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int sh = 8 * half + 4 * j;
-        a[2 * j] = fma_bf16x2(((r.k[0][w] >> sh) & 0x000f000fu) | 0x43004300u, s0, o0);
-        a[2 * j + 1] = fma_bf16x2(((r.k[1][w] >> sh) & 0x000f000fu) | 0x43004300u, s1, o1);
-      }
+      const uint32_t a[4] = {x0[2 * half], x1[2 * half], x0[2 * half + 1], x1[2 * half + 1]};
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < NS; ++i)
-          mma_bf16(s[n], a, q.b[n][i][2 * w + half][0], q.b[n][i][2 * w + half][1]);
+          mma_f16(s[n], a, q.b[n][i][2 * w + half][0], q.b[n][i][2 * w + half][1]);
     }
   }
 }
@@ -184,31 +171,31 @@ __device__ __forceinline__ void scores(const Raw<D>& r, const Query<D, NT, NS>& 
 // O^T += V^T P^T of 16 slots; P: operand fragments, NP fp16 parts.  Slots whose bit of `dead` (of
 // the lane's four) is set count as zeros whatever they hold.
 template <int D, int NT, int NP>
-__device__ __forceinline__ void values(const Raw<D>& r, const uint32_t (&P)[NT][NP][2],
+__device__ __forceinline__ void values(const char* tile, const uint32_t (&P)[NT][NP][2],
                                        uint32_t dead, float (&o)[NT][D / 16][4]) {
-  float f[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = scale_of((r.vs >> (8 * i)) & 255);
-    if (dead >> i & 1) f[i] = 0.f;
+  const int lane = lane_id(), g = lane / 4, t = lane % 4;
+  using Q = Tile<D>;
+  const uint32_t four = *reinterpret_cast<const uint32_t*>(
+      tile + Q::kScales + Q::kScaleBytes + g * (D / 8) / kGroup * 16 + 4 * t);
+  Scale2 sa(four, kPair01), sb(four, kPair23);
+  if (dead) {
+    sa.set(sa.s & ~((dead & 1) * 0xffffu | (dead >> 1 & 1) * 0xffff0000u));
+    sb.set(sb.s & ~((dead >> 2 & 1) * 0xffffu | (dead >> 3 & 1) * 0xffff0000u));
   }
-  const uint32_t sa = pack_f16(f[0], f[1]), sb = pack_f16(f[2], f[3]);
-  const uint32_t oa = fma_f16x2(sa, 0xd480d480u, 0x80008000u);  // -72 s
-  const uint32_t ob = fma_f16x2(sb, 0xd480d480u, 0x80008000u);
+  uint32_t v[4][Q::VW];
 #pragma unroll
-  for (int w = 0; w < Raw<D>::VW; ++w) {
-    const uint32_t x[4] = {__byte_perm(r.v[0][w], r.v[1][w], 0x5410),
-                           __byte_perm(r.v[0][w], r.v[1][w], 0x7632),
-                           __byte_perm(r.v[2][w], r.v[3][w], 0x5410),
-                           __byte_perm(r.v[2][w], r.v[3][w], 0x7632)};
+  for (int i = 0; i < 4; ++i)
+    load_words<Q::VW>(tile + Q::value(4 * t) + i * Q::kRow + g * (D / 16), v[i]);
+#pragma unroll
+  for (int w = 0; w < Q::VW; ++w) {
+    uint32_t x[4][4];
+    decode_word(__byte_perm(v[0][w], v[1][w], 0x5410), sa, x[0]);
+    decode_word(__byte_perm(v[0][w], v[1][w], 0x7632), sa, x[1]);
+    decode_word(__byte_perm(v[2][w], v[3][w], 0x5410), sb, x[2]);
+    decode_word(__byte_perm(v[2][w], v[3][w], 0x7632), sb, x[3]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t a[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t y = i == 0 ? x[j] << 4 : x[j] >> (4 * i - 4);
-        a[j] = fma_f16x2((y & 0x00f000f0u) | 0x54005400u, j < 2 ? sa : sb, j < 2 ? oa : ob);
-      }
+      const uint32_t a[4] = {x[0][i], x[1][i], x[2][i], x[3][i]};
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -235,9 +222,13 @@ __device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
   return make_float2(bf16_lo(w), bf16_hi(w));
 }
 
+// The rows' operand fragments in fp16.  A row is scaled by a power of two that takes its
+// largest value to [2^14, 2^15): bf16 values are then exact down to 2^-28 of it, and
+// fp32 values, in two parts, good to 2^-24 of themselves; what is lost below is 2^-39 of the
+// largest.  unscale[n][e] (of rows 2 t and 2 t + 1) takes the scores back.
 template <int D, int NT, int NS, typename T>
 __device__ __forceinline__ void load_query(const AttendParams& p, int b, int h, int row0, int rows,
-                                           Query<D, NT, NS>& q) {
+                                           Query<D, NT, NS>& q, float (&unscale)[NT][2]) {
   const int lane = lane_id(), g = lane / 4, t = lane % 4;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -246,20 +237,36 @@ __device__ __forceinline__ void load_query(const AttendParams& p, int b, int h, 
     const int i = row / p.group, j = row - i * p.group;
     const T* src = static_cast<const T*>(p.q) + b * p.qb + i * p.qn +
                    (long long)(h * p.group + j) * p.qh + t * (D / 4);
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k) {
+      const float2 x = ok ? load2<T>(src + 2 * k) : make_float2(0.f, 0.f);
+      top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+    top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+    // 2^(14 - e) for top in [2^e, 2^(e + 1)); rows of zeros or subnormals, and of infinity, by 2^+-112
+    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -98), 126);
+    float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+    if (!is_finite(top)) up = qnan();  // (infinities as NaN: their products with codes of 0 are)
+    if (p.scale < 0.f) up = -up;       // scores go on with the scale's magnitude
+    const float down = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+    unscale[n][0] = __shfl_sync(kAll, down, 8 * t);
+    unscale[n][1] = __shfl_sync(kAll, down, 8 * t + 4);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float2 x = ok ? load2<T>(src + 4 * k + 2 * e) : make_float2(0.f, 0.f);
+      for (int x2 = 0; x2 < 2; ++x2) {
+        float2 x = ok ? load2<T>(src + 4 * k + 2 * x2) : make_float2(0.f, 0.f);
+        x.x *= up;
+        x.y *= up;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {  // the next 8 bits of what is left
-          const uint32_t w = pack_bf16(x.x, x.y);
-          q.b[n][s][k][e] = w;
-          if (NS > 1) {
-            // (infinity minus itself would leave NaN in the parts that follow)
-            x.x = is_finite(x.x) ? x.x - bf16_lo(w) : 0.f;
-            x.y = is_finite(x.y) ? x.y - bf16_hi(w) : 0.f;
-          }
+        for (int s = 0; s < NS; ++s) {
+          const uint32_t w = pack_f16(x.x, x.y);
+          q.b[n][s][k][x2] = w;
+          const float2 got = unpack_f16(w);
+          x.x -= got.x;
+          x.y -= got.y;
         }
       }
   }
@@ -277,31 +284,51 @@ struct Where {  // of a tile's rows: the step's token and its position, a slope
   float slope[2];
 };
 
+// Shared memory of a CTA: the scan, each warp's stages (the warps' rows of a
+// finished piece take their place), a tree where the call has one.
+constexpr int kStages = 3;
 template <int D>
-struct FewSmem {
-  long long scan[kFewWarps + 3];
-  TreeView tree;
-  alignas(16) float o[1];  // [warps][rows][D + 4]
-};
-
+__host__ __device__ constexpr int few_tiles() {  // of 16 slots, a chunk
+  return D == 256 ? 1 : 2;
+}
+constexpr int kFewScan = 64;
+static_assert(sizeof(long long) * (kFewWarps + 3) <= kFewScan, "");
 template <int D, int NT>
-constexpr size_t few_smem() {
-  return offsetof(FewSmem<D>, o) + sizeof(float) * kFewWarps * 8 * NT * (D + 4);
+__host__ __device__ constexpr int few_ring() {
+  const int ring = kFewWarps * kStages * few_tiles<D>() * Tile<D>::kBytes;
+  const int rows = kFewWarps * 8 * NT * (D + 4) * (int)sizeof(float);
+  return ring > rows ? ring : rows;
+}
+template <int D, int NT>
+constexpr size_t few_smem(bool tree) {
+  return kFewScan + few_ring<D, NT>() + (tree ? sizeof(TreeView) : 0);
+}
+
+// CTAs an SM holds: as many as their registers allow without spills to speak of.
+template <int D, int NT, typename T>
+constexpr int few_blocks() {
+#ifdef FEWB
+  if (NT == 1 && D <= 128) return FEWB;
+#endif
+  return D == 256 || (D == 128 && NT == 2) ? 2 : D == 64 || sizeof(T) == 2 ? 4 - (NT - 1) : 3;
 }
 
 template <int D, int NT, typename T>
-__global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kernel(const AttendParams p) {
   constexpr bool kExact = sizeof(T) == 4;
-  constexpr int NS = kExact ? 3 : 1, NP = kExact ? 2 : 1;
-  constexpr int kTiles = D == 256 ? 1 : 2;  // of 16 slots, a chunk
+  constexpr int NS = kExact ? 2 : 1, NP = NS;
+  constexpr int kTiles = few_tiles<D>();
   constexpr int kChunkSlots = 16 * kTiles;
   extern __shared__ __align__(16) char raw_smem[];
-  FewSmem<D>& sm = *reinterpret_cast<FewSmem<D>*>(raw_smem);
+  long long* scan = reinterpret_cast<long long*>(raw_smem);
+  char* ring = raw_smem + kFewScan;
+  float* rows_out = reinterpret_cast<float*>(ring);
+  TreeView& tree = *reinterpret_cast<TreeView*>(ring + few_ring<D, NT>());  // (if p.parent)
   pdl_wait();
   pdl_launch_dependents();
   const int cta = blockIdx.x, lane = lane_id(), warp = threadIdx.x / 32;
   const int g = lane / 4, t = lane % 4;
-  const Share share = find_share<kFewThreads>(p, cta, gridDim.x, sm.scan);
+  const Share share = find_share<kFewThreads>(p, cta, gridDim.x, scan);
   if (threadIdx.x == 0) p.desc[4 * cta + 3] = 0;
   if (cta >= share.G) return;
 
@@ -323,10 +350,11 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
     const int row0 = tile * 8 * NT;
 
     bool sees = r.ok && r.len > 0;
-    if (p.parent && sees) sees = build_tree<kFewThreads>(p, b, r.nq, sm.tree);
+    if (p.parent && sees) sees = build_tree<kFewThreads>(p, b, r.nq, tree);
 
     Query<D, NT, NS> q;
-    load_query<D, NT, NS, T>(p, b, h, row0, r.ok ? rows : 0, q);
+    float unscale[NT][2];
+    load_query<D, NT, NS, T>(p, b, h, row0, r.ok ? rows : 0, q, unscale);
     Rows<D, NT> acc;
     Where where[NT];
 #pragma unroll
@@ -338,7 +366,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
         const int row = min(row0 + 8 * n + 2 * t + e, max(rows - 1, 0));
         const int i = row / p.group;
         where[n].node[e] = i;
-        where[n].pos[e] = r.base + (p.parent && sees ? sm.tree.depth[i] : i);
+        where[n].pos[e] = r.base + (p.parent && sees ? tree.depth[i] : i);
         where[n].slope[e] = p.slopes ? p.slopes[h * p.group + row - i * p.group] * kLog2e : 0.f;
       }
 #pragma unroll
@@ -350,43 +378,75 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
       const int from = r.lo / kChunkSlots;
       const int* table = p.cache.table + (long long)b * p.cache.M;
       const int mask = (1 << p.cache.shift) - 1;
-      auto fetch_ids = [&](int c, int (&id)[kTiles]) {
+      // scores before the cap, or in units of log2 where there is none
+      const float unit_scale = fabsf(p.scale) * (p.softcap > 0.f ? 1.f / p.softcap : kLog2e);
 #pragma unroll
-        for (int k = 0; k < kTiles; ++k) {
-          const int slot = (from + c) * kChunkSlots + 16 * k;
-          id[k] = c < c1 && slot < r.len ? table[slot >> p.cache.shift] : -1;
+      for (int n = 0; n < NT; ++n) unscale[n][0] *= unit_scale, unscale[n][1] *= unit_scale;
+      // The warp's stages: chunk c's copies are queued kStages - 1 chunks ahead, its page ids
+      // read one chunk before that.
+      constexpr int kStageBytes = kTiles * Tile<D>::kBytes;
+      char* stages = ring + warp * kStages * kStageBytes;
+      const int block = page_bytes(1, D) << p.cache.shift;
+      const char* head = p.cache.data + (long long)(2 * h) * block;
+      const bool one_page = kTiles == 1 || p.cache.shift >= 5;  // a chunk lies in one page
+      int next[kTiles];
+      auto queue = [&](int c, char* stage) {
+        if (c < c1) {
+          const int token = ((from + c) * kChunkSlots) & mask;
+          if (one_page) {
+            queue_tiles<D, kTiles>(p.cache, head, block, next[0], token, stage);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kTiles; ++k)
+              queue_tiles<D, 1>(p.cache, head, block, next[k], (token + 16 * k) & mask,
+                                stage + k * Tile<D>::kBytes);
+          }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      auto fetch = [&](int c, const int (&id)[kTiles], Raw<D> (&raw)[kTiles]) {
+      auto fetch_ids = [&](int c) {
+        const int slot = (from + c) * kChunkSlots;
+        next[0] = c < c1 && slot < r.len ? table[slot >> p.cache.shift] : -1;
+        if (!one_page)
 #pragma unroll
-        for (int k = 0; k < kTiles; ++k)
-          load_raw<D>(p.cache, id[k], ((from + c) * kChunkSlots + 16 * k) & mask, h, raw[k]);
+          for (int k = 1; k < kTiles; ++k)
+            next[k] = c < c1 && slot + 16 * k < r.len ? table[(slot + 16 * k) >> p.cache.shift] : -1;
       };
-      int id[kTiles];
-      Raw<D> next[kTiles];
-      fetch_ids(c0 + warp, id);
-      fetch(c0 + warp, id, next);
-      fetch_ids(c0 + warp + kFewWarps, id);
+#pragma unroll
+      for (int st = 0; st < kStages - 1; ++st) {
+        fetch_ids(c0 + warp + st * kFewWarps);
+        queue(c0 + warp + st * kFewWarps, stages + st * kStageBytes);
+      }
+      fetch_ids(c0 + warp + (kStages - 1) * kFewWarps);
+      int now = 0, then = kStages - 1;
       for (int c = c0 + warp; c < c1; c += kFewWarps) {
-        Raw<D> now[kTiles];
-#pragma unroll
-        for (int k = 0; k < kTiles; ++k) now[k] = next[k];
-        if (c + kFewWarps < c1) {
-          fetch(c + kFewWarps, id, next);
-          fetch_ids(c + 2 * kFewWarps, id);
-        }
+        const int slot0 = (from + c) * kChunkSlots;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();  // (every lane's copies are in, and its loads of the stage before done)
+        queue(c + (kStages - 1) * kFewWarps, stages + then * kStageBytes);
+        fetch_ids(c + kStages * kFewWarps);
+        const char* stage = stages + now * kStageBytes;
+        now = now + 1 == kStages ? 0 : now + 1;
+        then = then + 1 == kStages ? 0 : then + 1;
         float s[kTiles][NT][4];
 #pragma unroll
-        for (int k = 0; k < kTiles; ++k) scores<D, NT, NS>(now[k], q, s[k]);
-        const int slot0 = (from + c) * kChunkSlots;
+        for (int k = 0; k < kTiles; ++k)
+          scores<D, NT, NS>(stage + k * Tile<D>::kBytes, q, s[k]);
         // a chunk before the step's tokens that every row sees whole needs no masks
         const bool edge = slot0 + kChunkSlots > r.base || p.window > 0 || p.slopes;
+        const bool plain = !edge && p.softcap == 0.f;
+        if (!plain) {
 #pragma unroll
-        for (int k = 0; k < kTiles; ++k)
+          for (int k = 0; k < kTiles; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[k][n][e] = score_of<kExact>(p, s[k][n][e]);
+              for (int e = 0; e < 4; ++e) {
+                float y = s[k][n][e] * unscale[n][e & 1];
+                if (p.softcap > 0.f) y = cap_of<kExact>(p.softcap * kLog2e, y);
+                s[k][n][e] = y;
+              }
+        }
         if (edge) {
 #pragma unroll
           for (int k = 0; k < kTiles; ++k)
@@ -396,14 +456,14 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
               const int node = slot - r.base;
               const bool there = slot < r.len;
               int pos = slot;
-              if (p.parent && node >= 0 && there) pos = r.base + sm.tree.depth[node];
+              if (p.parent && node >= 0 && there) pos = r.base + tree.depth[node];
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   bool seen = there;
                   if (node >= 0 && there)
-                    seen = p.parent ? (sm.tree.seen[where[n].node[e]][node >> 5] >> (node & 31)) & 1
+                    seen = p.parent ? (tree.seen[where[n].node[e]][node >> 5] >> (node & 31)) & 1
                                     : node <= where[n].node[e];
                   const int far = where[n].pos[e] - pos;
                   if (p.window > 0 && far >= p.window) seen = false;
@@ -412,34 +472,45 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
                 }
             }
         }
-        // the running max of each row, over the lanes of a column
         uint32_t P[kTiles][NT][NP][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          // the running max of each row: the lanes of a column meet only where one of them
+          // found a larger score
+          float f[2], top[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(s[0][n][e], s[0][n][e + 2]);
+            f[e] = plain ? unscale[n][e] : 1.f;
+            top[e] = fmaxf(s[0][n][e], s[0][n][e + 2]);
 #pragma unroll
-            for (int k = 1; k < kTiles; ++k) top = fmaxf(top, fmaxf(s[k][n][e], s[k][n][e + 2]));
+            for (int k = 1; k < kTiles; ++k)
+              top[e] = fmaxf(top[e], fmaxf(s[k][n][e], s[k][n][e + 2]));
+            top[e] *= f[e];
+          }
+          if (__any_sync(kAll, top[0] > acc.m[n][0] || top[1] > acc.m[n][1])) {
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
-            const float m = fmaxf(acc.m[n][e], top);
-            if (__any_sync(kAll, m > acc.m[n][e])) {
-              const float f = acc.m[n][e] == -INFINITY ? 0.f : ex2(acc.m[n][e] - m);
+            for (int e = 0; e < 2; ++e) {
+              float m = fmaxf(top[e], acc.m[n][e]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, x));
+              const float g1 = acc.m[n][e] == -INFINITY ? 0.f : ex2(acc.m[n][e] - m);
               acc.m[n][e] = m;
-              acc.l[n][e] *= f;
+              acc.l[n][e] *= g1;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
-                acc.o[n][i][e] *= f;
-                acc.o[n][i][e + 2] *= f;
+                acc.o[n][i][e] *= g1;
+                acc.o[n][i][e + 2] *= g1;
               }
             }
-            const float off = m == -INFINITY ? 0.f : kShift - m;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float off = acc.m[n][e] == -INFINITY ? 0.f : kFewShift - acc.m[n][e];
 #pragma unroll
             for (int k = 0; k < kTiles; ++k)
 #pragma unroll
               for (int x = 0; x < 4; x += 2) {
-                const float w = ex2(s[k][n][e + x] + off);
+                const float w = ex2(fmaf(s[k][n][e + x], f[e], off));
                 s[k][n][e + x] = w;
                 acc.l[n][e] += w;
               }
@@ -453,11 +524,9 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
               for (int part = 0; part < NP; ++part) {
                 const uint32_t w = pack_f16(w0, w1);
                 P[k][n][part][x] = transpose8(w);
-                if (NP > 1) {
-                  const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                  w0 -= back.x;
-                  w1 -= back.y;
-                }
+                const float2 got = unpack_f16(w);
+                w0 -= got.x;
+                w1 -= got.y;
               }
             }
         }
@@ -471,10 +540,12 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
               dead |= (slot < r.lo || slot >= r.len ? 1u : 0u) << i;
             }
           }
-          values<D, NT, NP>(now[k], P[k], dead, acc.o);
+          values<D, NT, NP>(stage + k * Tile<D>::kBytes, P[k], dead, acc.o);
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
+    __syncthreads();  // (the stages are read)
 
     // join the warps: each leaves its rows in shared memory
     constexpr int kRows = 8 * NT, kStep = D + 4;
@@ -485,7 +556,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
         float l = acc.l[n][e];
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(kAll, l, x);
-        float* row = sm.o + (warp * kRows + 8 * n + 2 * t + e) * kStep;
+        float* row = rows_out + (warp * kRows + 8 * n + 2 * t + e) * kStep;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
           *reinterpret_cast<float2*>(row + dim_of<D>(i)) =
@@ -502,12 +573,12 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
       const int row = x / (D / 4), d = x % (D / 4) * 4;
       float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) m = fmaxf(m, sm.o[(w * kRows + row) * kStep + D]);
+      for (int w = 0; w < kFewWarps; ++w) m = fmaxf(m, rows_out[(w * kRows + row) * kStep + D]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       float l = 0.f;
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) {
-        const float* src = sm.o + (w * kRows + row) * kStep;
+        const float* src = rows_out + (w * kRows + row) * kStep;
         const float f = src[D] == -INFINITY ? (src[D + 1] == 0.f ? 0.f : 1.f) : ex2(src[D] - m);
         const float4 v = *reinterpret_cast<const float4*>(src + d);
         o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y);
@@ -527,7 +598,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const AttendParams p) 
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to * D + d) =
               make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
         if (p.out_lse && d == 0)
-          p.out_lse[to] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+          p.out_lse[to] = l == 0.f ? -INFINITY : (m - kFewShift + log2f(l)) * 0.6931471805599453f;
       } else {
         float* dst = part + row * kStep;
         *reinterpret_cast<float4*>(dst + d) = o;
@@ -562,13 +633,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
   if (p.out_status && blockIdx.y == 0) {
     for (int b = blockIdx.x * kJoinThreads + threadIdx.x; b < p.B; b += gridDim.x * kJoinThreads) {
       const Request r = request_of(p, b);
+      int late = 0;
+      if (p.late)  // (a wait that ran out is every request's, so seldom is it)
+        for (int i = 0; i < (int)gridDim.x; ++i) late |= p.late[i];
       int st = r.ok ? page_status(p.cache, b, r.lo, r.len - r.lo) : kBadDraftLen;
       if (r.ok && p.parent) {
         const int* parent = p.parent + (long long)b * p.parent_stride;
         for (int n = 1; n < r.nq; ++n)
           if (parent[n - 1] < 0 || parent[n - 1] >= n) st |= kBadTree;
       }
-      p.out_status[b] = st;
+      p.out_status[b] = st | (late ? kTimeout : 0);
     }
   }
   const int cta = blockIdx.x;
@@ -617,13 +691,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
             pack_bf16(o[e] * inv, o[e + 1] * inv);
     }
     if (p.out_lse && lane == 0)
-      p.out_lse[to] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+      p.out_lse[to] = l == 0.f ? -INFINITY : (m - p.shift + log2f(l)) * 0.6931471805599453f;
   }
 }
 
-// Resident CTAs of a kernel on the current device.
+// Resident CTAs of a kernel on the current device (with `smem`; `most` is what a launch may ask for).
 template <class K>
-cudaError_t resident(K fn, int threads, size_t smem, std::atomic<int>* cache, int* ctas) {
+cudaError_t resident(K fn, int threads, size_t smem, size_t most, std::atomic<int>* cache,
+                     int* ctas) {
   DeviceInfo info;
   cudaError_t err = device_info(&info);
   if (err != cudaSuccess) return err;
@@ -631,7 +706,7 @@ cudaError_t resident(K fn, int threads, size_t smem, std::atomic<int>* cache, in
   if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
   int n = cache[dev].load(std::memory_order_relaxed);  // (device_info: dev < 64)
   if (!n) {
-    err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (err != cudaSuccess) return err;
     err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem);
     if (err != cudaSuccess) return err;
@@ -648,7 +723,9 @@ cudaError_t plan_one(AttendPlan* plan) {
   plan->rows = 8 * NT;
   plan->chunk = D == 256 ? 16 : 32;
   plan->least = kFewWarps;
-  return resident(few_kernel<D, NT, T>, kFewThreads, few_smem<D, NT>(), cache, &plan->ctas);
+  plan->shift = kFewShift;
+  return resident(few_kernel<D, NT, T>, kFewThreads, few_smem<D, NT>(false), few_smem<D, NT>(true),
+                  cache, &plan->ctas);
 }
 
 }  // namespace
@@ -679,7 +756,8 @@ cudaError_t launch_few(const AttendParams& p, int D, int dtype, const AttendPlan
                        cudaStream_t stream) {
   const int rows = plan.rows;
 #define SV_LAUNCH(d, n, T) \
-  (launch_early(few_kernel<d, n, T>, plan.ctas, kFewThreads, few_smem<d, n>(), 1, stream, p))
+  (launch_early(few_kernel<d, n, T>, plan.ctas, kFewThreads, few_smem<d, n>(p.parent != nullptr), 1, \
+                stream, p))
   SV_FEW(SV_LAUNCH)
 #undef SV_LAUNCH
 }
@@ -687,7 +765,7 @@ cudaError_t launch_few(const AttendParams& p, int D, int dtype, const AttendPlan
 cudaError_t launch_join(const AttendParams& p, int D, int dtype, int ctas, int units,
                         cudaStream_t stream) {
   // where units are few, each is in many pieces: a warp a row of every tile
-  const dim3 grid(ctas, units * 4 <= ctas ? (p.rows + 7) / 8 : 1);
+  const dim3 grid(ctas, units * 4 <= ctas || p.rows > 16 ? (p.rows + 7) / 8 : 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kJoinThreads);
@@ -711,14 +789,21 @@ sv_status check_cache(CacheView* c, const void* cache, int64_t page_stride, cons
 
 namespace {
 
-// The kernel and split of a call; 0 CTAs when nothing has to run.
-cudaError_t plan_of(sv_dtype dtype, int rows, int head_dim, AttendPlan* plan) {
-  return plan_few(head_dim, dtype, rows, plan);
+// The kernel and split of a call of `rows` query rows a key/value head.  ROWS_RULE
+bool many_rows(sv_dtype dtype, int rows, int D) {
+  return dtype == SV_BF16 && D <= 128 && rows > 16;
+}
+cudaError_t plan_of(sv_dtype dtype, int rows, int D, AttendPlan* plan) {
+  return many_rows(dtype, rows, D) ? plan_many(D, plan) : plan_few(D, dtype, rows, plan);
 }
 
-size_t desc_bytes(const AttendPlan& plan) { return (size_t)plan.ctas * 16; }
+// The workspace: the split units, a flag for each CTA, the unfinished rows.
+size_t flag_offset(const AttendPlan& plan) { return (size_t)plan.ctas * 16; }
+size_t part_offset(const AttendPlan& plan) {
+  return flag_offset(plan) + ((size_t)plan.ctas * 4 + 15) / 16 * 16;
+}
 size_t workspace_bytes(const AttendPlan& plan, int D) {
-  return desc_bytes(plan) + (size_t)plan.ctas * 2 * plan.rows * (D + 4) * sizeof(float);
+  return part_offset(plan) + (size_t)plan.ctas * 2 * plan.rows * (D + 4) * sizeof(float);
 }
 
 bool shape_ok(int N, int Hq, int Hkv, int D) {
@@ -797,11 +882,18 @@ extern "C" sv_status spec_cache_attention(
   p.least = plan.least;
   if (!workspace || ((uintptr_t)workspace & 15) || ws_bytes < workspace_bytes(plan, head_dim))
     return SV_ERR_WORKSPACE;
-  p.desc = static_cast<int*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + desc_bytes(plan));
+  char* ws = static_cast<char*>(workspace);
+  const bool many = many_rows(dtype, N * p.group, head_dim);
+  p.desc = reinterpret_cast<int*>(ws);
+  p.late = many ? reinterpret_cast<int*>(ws + flag_offset(plan)) : nullptr;
+  p.part = reinterpret_cast<float*>(ws + part_offset(plan));
+  p.shift = plan.shift;
+  p.wait_ns = wait_limit_ns();
   const cudaStream_t s = (cudaStream_t)stream;
-  if (launch_few(p, head_dim, dtype, plan, s) != cudaSuccess) return SV_ERR_CUDA;
+  if ((many ? launch_many(p, head_dim, plan, s) : launch_few(p, head_dim, dtype, plan, s)) !=
+      cudaSuccess)
+    return SV_ERR_CUDA;
   const long long units = (long long)B * kv_heads * ((N * p.group + p.rows - 1) / p.rows);
-  const int many = (int)std::min(units, (long long)plan.ctas);
-  return launch_join(p, head_dim, dtype, plan.ctas, many, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  const int some = (int)std::min(units, (long long)plan.ctas);
+  return launch_join(p, head_dim, dtype, plan.ctas, some, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

@@ -18,9 +18,9 @@ namespace sv {
 
 constexpr int kMaxStep = 257;                    // tokens of a step (a tree of 256 nodes and its root)
 constexpr int kSeenWords = (kMaxStep + 31) / 32;  // bits of one node's ancestors
-// Weights are 2^(score - max + kShift), at most 2^15: fp16's least step of 2^-24
-// is then 2^-39 of the row's largest weight.
-constexpr float kShift = 15.f;
+// Weights are 2^(score - max + shift).  With a shift of 15 the largest is 2^15, and fp16's
+// least step of 2^-24 is 2^-39 of it.
+constexpr float kFewShift = 15.f;
 
 struct AttendParams {
   CacheView cache;
@@ -42,6 +42,9 @@ struct AttendParams {
   int chunk;                 // slots of a chunk
   int least;                 // chunks that are worth a CTA
   int* desc;                 // [G][4] the split unit that begins in each CTA's share: b, head, row tile, pieces
+  int* late;                 // [G] whether a wait in the CTA ran out, or null
+  float shift;               // of the weights' exponents
+  unsigned long long wait_ns;  // limit of the waits
   float* part;               // [2 G][rows][D + 4] unfinished rows: values, max, sum
 };
 
@@ -155,6 +158,36 @@ __device__ __forceinline__ Share find_share(const AttendParams& p, int cta, int 
   }
 }
 
+// A walk over the chunks of a share.
+struct Walk {
+  Request r;
+  int b, h, tile, c;  // the chunk's request, head, row tile, and place in the unit
+  long long left;     // chunks from here on
+  __device__ __forceinline__ Walk(const AttendParams& p, const Share& s)
+      : r(request_of(p, s.b)), b(s.b), left(s.end - s.begin) {
+    const int unit = (int)(s.at / r.chunks);
+    c = (int)(s.at - (long long)unit * r.chunks);
+    h = unit / r.tiles;
+    tile = unit - h * r.tiles;
+  }
+  __device__ __forceinline__ void step(const AttendParams& p) {
+    --left;
+    if (++c < r.chunks) return;
+    next_unit(p);
+  }
+  __device__ __forceinline__ void next_unit(const AttendParams& p) {
+    c = 0;
+    if (++tile < r.tiles) return;
+    tile = 0;
+    if (++h < p.cache.Hkv) return;
+    h = 0;
+    while (left > 0) {
+      r = request_of(p, ++b);
+      if (r.tiles > 0) break;
+    }
+  }
+};
+
 // How many CTAs' shares meet the unit [u0, u1) of whose chunks CTA `cta` holds the first.
 __device__ __forceinline__ int pieces_of(const Share& s, int cta, long long u1) {
   int n = 1;
@@ -170,19 +203,20 @@ struct TreeView {
   int bad;
 };
 
-// Builds it with the block's T threads; false when the parents are no tree.
+// Builds it with the block's first T threads; false when the parents are no tree.
 template <int T>
 __device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq, TreeView& tree) {
-  __syncthreads();
+  auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(T) : "memory"); };
+  meet();
   if (threadIdx.x == 0) tree.bad = 0;
-  __syncthreads();
+  meet();
   const int* parent = p.parent + (long long)b * p.parent_stride;
   for (int n = threadIdx.x; n < nq; n += T) {
     const int up = n ? parent[n - 1] : -1;
     tree.parent[n] = up;
     if (n && (up < 0 || up >= n)) tree.bad = 1;
   }
-  __syncthreads();
+  meet();
   if (tree.bad) return false;
   for (int n = threadIdx.x; n < nq; n += T) {
 #pragma unroll
@@ -192,8 +226,56 @@ __device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq,
       tree.seen[n][at >> 5] |= 1u << (at & 31);
     tree.depth[n] = d;
   }
-  __syncthreads();
+  meet();
   return true;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+  return d;
+}
+
+// A pair of scales (64 s in fp16) and -9 / 8 of them.
+struct Scale2 {
+  uint32_t s, off;
+  __device__ __forceinline__ Scale2() {}
+  // The two bytes of `word` that the low bits of the selector name.
+  __device__ __forceinline__ Scale2(uint32_t word, uint32_t sel) {
+    set(__byte_perm(word, 0, sel) * 128u + 0x04000400u);
+  }
+  __device__ __forceinline__ void set(uint32_t pair) {
+    s = pair;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(off) : "r"(pair), "r"(0xbc80bc80u));
+  }
+};
+constexpr uint32_t kPair01 = 0x4140, kPair23 = 0x4342;
+
+// The 8 values of a word, pairs (2 i, 2 i + 1) in x[i].  A code in the low four bits of an fp16
+// number of exponent 2^4 is 16 + c / 64, one four bits up in one of 2^0 it is 1 + c / 64: two of
+// four pairs need no shift, and one shift serves the other two.  (16 + 8 / 64) 64 s would
+// not be exact, so those pairs take a subtraction and a product.
+__device__ __forceinline__ void decode_word(uint32_t w, const Scale2& sc, uint32_t (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t y = i == 0 ? w : w >> 8;
+    const uint32_t low = and_or(y, 0x000f000fu, 0x4c004c00u);
+    const uint32_t high = and_or(y, 0x00f000f0u, 0x3c003c00u);
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(low), "r"(0xcc08cc08u));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x[2 * i]) : "r"(d), "r"(sc.s));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(x[2 * i + 1]) : "r"(high), "r"(sc.s), "r"(sc.off));
+  }
 }
 
 // tanh by one exponential; 2^-22 of 1.
@@ -202,14 +284,10 @@ __device__ __forceinline__ float tanh_fast(float x) {
 }
 
 // A score in units of log2: scaled, capped, biased by the distance of the two positions.
+// cap * tanh(x).
 template <bool EXACT>
-__device__ __forceinline__ float score_of(const AttendParams& p, float x) {
-  if (p.softcap > 0.f) {
-    x = x * p.scale / p.softcap;
-    x = p.softcap * (EXACT ? tanhf(x) : tanh_fast(x));
-    return x * kLog2e;
-  }
-  return x * (p.scale * kLog2e);
+__device__ __forceinline__ float cap_of(float cap, float x) {
+  return cap * (EXACT ? tanhf(x) : tanh_fast(x));
 }
 
 // Joins the pieces of split units (launched behind either kernel).
@@ -219,9 +297,12 @@ cudaError_t launch_join(const AttendParams& p, int D, int dtype, int ctas, int u
 // The kernel for tiles of few rows and the one for many (tensor memory); they fill in the split.
 struct AttendPlan {
   int rows, chunk, least, ctas;
+  float shift;
 };
 cudaError_t plan_few(int D, int dtype, int rows, AttendPlan* plan);
 cudaError_t launch_few(const AttendParams& p, int D, int dtype, const AttendPlan& plan,
                        cudaStream_t stream);
+cudaError_t plan_many(int D, AttendPlan* plan);
+cudaError_t launch_many(const AttendParams& p, int D, const AttendPlan& plan, cudaStream_t stream);
 
 }  // namespace sv

@@ -306,12 +306,13 @@ sv_status check_cache(CacheView* c, const void* cache, int64_t page_stride, cons
   if (!bytes || pages < 0 || B < 0 || B > SV_MAX_B || M < 0 || kv_heads < 1 ||
       kv_heads > SV_MAX_HEADS || (long long)M * page_size > SV_MAX_SLOTS)
     return SV_ERR_SHAPE;
-  if (page_stride % 16 || page_stride < 0 ||
+  if (pages <= 1) page_stride = 0;
+  if (page_stride % 16 || page_stride < 0 || page_stride > UINT32_MAX ||
       (pages > 1 && page_stride < (int64_t)(2 * bytes * kv_heads)))
     return SV_ERR_SHAPE;
   if (B > 0 && ((pages > 0 && !cache) || (M > 0 && !table) || !aligned16(cache))) return SV_ERR_NULL;
   c->data = static_cast<char*>(const_cast<void*>(cache));
-  c->page_stride = page_stride;
+  c->page_stride = (uint32_t)page_stride;
   c->table = table;
   c->M = M;
   c->pages = pages;

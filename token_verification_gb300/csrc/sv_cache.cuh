@@ -10,9 +10,10 @@
 //
 // A code c stands for (c - 8) s.  s has 4 significant bits and lies in
 // [2^-20, 896], so (c - 8) s has 7 and is exact in bf16 and in fp16 (the least,
-// 2^-23, is a multiple of fp16's 2^-24), and so are 136 s in bf16 and 72 s in
-// fp16 (at most 64512): one fused multiply-add turns 128 + c (bf16) or 64 + c
-// (fp16) into the exact value.
+// 2^-23, is a multiple of fp16's 2^-24).  64 s is an fp16 number whose bits are
+// (byte + 8) << 7, and so is 72 s (at most 64512): codes in the low mantissa
+// bits of an fp16 number near 16 or 1 stand for (c - 8) / 64 after a subtraction, or
+// one fused multiply-add turns them into the exact value.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,7 +26,7 @@ namespace sv {
 constexpr int kGroup = 32;       // values of a token under one scale
 constexpr int kTopScale = 238;   // the largest scale byte: 896
 constexpr int kScaleBias = 856;  // byte + kScaleBias = the scale's fp32 bits >> 20
-constexpr int kNanScale = 255;   // keys of a token that held NaN or infinity
+constexpr int kNanScale = 247;   // keys of a token that held NaN or infinity: 64 s would be NaN
 constexpr int kBadPage = 32;     // SV_REQ_BAD_PAGE
 
 __host__ __device__ constexpr int page_bytes(int page, int D) {
@@ -49,7 +50,7 @@ __device__ __forceinline__ int scale_byte(float top) {
 // Where tokens of a cache lie.
 struct CacheView {
   char* data;
-  long long page_stride;  // bytes from one page to the next
+  uint32_t page_stride;   // bytes from one page to the next
   const int* table;       // [B, M] page ids
   int M;                  // pages a request can hold
   int pages;              // pages of the cache
@@ -60,7 +61,8 @@ struct CacheView {
 // The block of page `id` for head h, keys (0) or values (1).
 template <int D>
 __device__ __forceinline__ char* page_block(const CacheView& c, int id, int h, int kv) {
-  return c.data + id * c.page_stride + (long long)((h * 2 + kv) * page_bytes(1, D)) * (1 << c.shift);
+  return c.data + (unsigned long long)(unsigned)id * c.page_stride +
+         (long long)((h * 2 + kv) * page_bytes(1, D)) * (1 << c.shift);
 }
 
 // Offset of the 16 scale bytes (16 tokens) of a group in a block, `token` = slot in the page.
