@@ -794,7 +794,7 @@ bool many_rows(sv_dtype dtype, int rows, int D) {
   return dtype == SV_BF16 && D <= 128 && rows > 16;
 }
 cudaError_t plan_of(sv_dtype dtype, int rows, int D, AttendPlan* plan) {
-  return many_rows(dtype, rows, D) ? plan_many(D, plan) : plan_few(D, dtype, rows, plan);
+  return many_rows(dtype, rows, D) ? plan_many(rows, plan) : plan_few(D, dtype, rows, plan);
 }
 
 // The workspace: the split units, a flag for each CTA, the unfinished rows.

@@ -302,7 +302,7 @@ struct AttendPlan {
 cudaError_t plan_few(int D, int dtype, int rows, AttendPlan* plan);
 cudaError_t launch_few(const AttendParams& p, int D, int dtype, const AttendPlan& plan,
                        cudaStream_t stream);
-cudaError_t plan_many(int D, AttendPlan* plan);
+cudaError_t plan_many(int rows, AttendPlan* plan);
 cudaError_t launch_many(const AttendParams& p, int D, const AttendPlan& plan, cudaStream_t stream);
 
 }  // namespace sv
