@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
   pdl_launch_dependents();
   const int cta = blockIdx.x, lane = lane_id(), warp = threadIdx.x / 32;
   const int g = lane / 4, t = lane % 4;
-  const Share share = find_share<kFewThreads>(p, cta, gridDim.x, scan);
+  const int ctas[1] = {cta};
+  const Share share = find_share<kFewThreads>(p, ctas, 0, gridDim.x, scan);
   if (threadIdx.x == 0) p.desc[4 * cta + 3] = 0;
   if (cta >= share.G) return;
 
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
     const int row0 = tile * 8 * NT;
 
     bool sees = r.ok && r.len > 0;
-    if (p.parent && sees) sees = build_tree<kFewThreads>(p, b, r.nq, tree);
+    if (p.parent && sees) sees = build_tree<kFewThreads>(p, b, r.nq, tree, threadIdx.x, 1);
 
     Query<D, NT, NS> q;
     float unscale[NT][2];

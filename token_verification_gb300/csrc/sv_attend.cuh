@@ -84,8 +84,7 @@ __device__ __forceinline__ long long work_of(const AttendParams& p, int b) {
 }
 
 // The CTA's share [begin, end) of the call's chunks, and the request and offset in
-// it where the share begins.  Every thread of the block (T of them) takes part; smem: T / 32 + 3
-// long longs.
+// it where the share begins.  Every thread of the block (T of them) takes part.
 struct Share {
   long long begin, end, total;
   int b;          // request of `begin`
@@ -114,48 +113,58 @@ __device__ __forceinline__ long long block_scan(long long x, long long* smem, lo
   return x + before;
 }
 
-template <int T>
-__device__ __forceinline__ Share find_share(const AttendParams& p, int cta, int ctas,
-                                            long long* smem) {
-  Share s;
+// smem: T / 32 + 2 K long longs.  K shares are found at once, those of CTAs cta[0 .. K - 1]; a
+// thread gets that of cta[mine].
+template <int T, int K>
+__device__ __forceinline__ Share find_share(const AttendParams& p, const int (&cta)[K], int mine,
+                                            int ctas, long long* smem) {
   const int t = threadIdx.x;
-  long long mine = t < p.B ? work_of(p, t) : 0, total;
-  const long long first_scan = block_scan<T>(mine, smem, &total);
-  const long long first_total = total;
+  const long long first = t < p.B ? work_of(p, t) : 0;
+  long long total, part;
+  const long long first_scan = block_scan<T>(first, smem, &total), first_total = total;
   for (int b0 = T; b0 < p.B; b0 += T) {
-    long long part;
     block_scan<T>(b0 + t < p.B ? work_of(p, b0 + t) : 0, smem, &part);
     total += part;
   }
-  s.total = total;
+  Share s[K];
   const long long want = (total + p.least - 1) / p.least;
-  s.G = (int)(want < ctas ? want : ctas);
-  s.begin = s.end = s.at = 0;
-  s.b = 0;
-  if (cta >= s.G) return s;
-  s.begin = total * cta / s.G;
-  s.end = total * (cta + 1) / s.G;
-  long long before = 0, scan = first_scan, part = first_total;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    s[k].total = total;
+    s[k].G = (int)(want < ctas ? want : ctas);
+    s[k].begin = s[k].end = s[k].at = 0;
+    s[k].b = 0;
+    if (cta[k] < s[k].G) {
+      s[k].begin = total * cta[k] / s[k].G;
+      s[k].end = total * (cta[k] + 1) / s[k].G;
+    }
+  }
   long long* found = smem + T / 32;
-  for (int b0 = 0;; b0 += T) {
-    if (b0 > 0) {
-      mine = b0 + t < p.B ? work_of(p, b0 + t) : 0;
-      scan = block_scan<T>(mine, smem, &part);
-    }
-    if (s.begin < before + part) {
-      const long long from = before + scan - mine;
-      if (from <= s.begin && s.begin < from + mine) {
-        found[0] = b0 + t;
-        found[1] = s.begin - from;
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += T) {
+    const long long work = b0 == 0 ? first : b0 + t < p.B ? work_of(p, b0 + t) : 0;
+    part = first_total;
+    const long long scan = b0 == 0 ? first_scan : block_scan<T>(work, smem, &part);
+    const long long from = before + scan - work;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (from <= s[k].begin && s[k].begin < from + work) {
+        found[2 * k] = b0 + t;
+        found[2 * k + 1] = s[k].begin - from;
       }
-      __syncthreads();
-      s.b = (int)found[0];
-      s.at = found[1];
-      __syncthreads();
-      return s;
-    }
     before += part;
   }
+  __syncthreads();
+  Share r = s[0];
+#pragma unroll
+  for (int k = 1; k < K; ++k)
+    if (mine == k) r = s[k];
+  if (r.begin < r.end) {
+    r.b = (int)found[2 * mine];
+    r.at = found[2 * mine + 1];
+  }
+  __syncthreads();
+  return r;
 }
 
 // A walk over the chunks of a share.
@@ -163,8 +172,12 @@ struct Walk {
   Request r;
   int b, h, tile, c;  // the chunk's request, head, row tile, and place in the unit
   long long left;     // chunks from here on
-  __device__ __forceinline__ Walk(const AttendParams& p, const Share& s)
-      : r(request_of(p, s.b)), b(s.b), left(s.end - s.begin) {
+  __device__ __forceinline__ Walk(const AttendParams& p, const Share& s, bool has)
+      : r(request_of(p, s.b)), b(s.b), left(has ? s.end - s.begin : 0) {
+    if (!has) {
+      h = tile = c = 0;
+      return;
+    }
     const int unit = (int)(s.at / r.chunks);
     c = (int)(s.at - (long long)unit * r.chunks);
     h = unit / r.tiles;
@@ -203,22 +216,23 @@ struct TreeView {
   int bad;
 };
 
-// Builds it with the block's first T threads; false when the parents are no tree.
+// Builds it with T threads (this one: t) that share a named barrier; false when the parents are no tree.
 template <int T>
-__device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq, TreeView& tree) {
-  auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(T) : "memory"); };
+__device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq, TreeView& tree,
+                                           int t, int barrier) {
+  auto meet = [=] { asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(T) : "memory"); };
   meet();
-  if (threadIdx.x == 0) tree.bad = 0;
+  if (t == 0) tree.bad = 0;
   meet();
   const int* parent = p.parent + (long long)b * p.parent_stride;
-  for (int n = threadIdx.x; n < nq; n += T) {
+  for (int n = t; n < nq; n += T) {
     const int up = n ? parent[n - 1] : -1;
     tree.parent[n] = up;
     if (n && (up < 0 || up >= n)) tree.bad = 1;
   }
   meet();
   if (tree.bad) return false;
-  for (int n = threadIdx.x; n < nq; n += T) {
+  for (int n = t; n < nq; n += T) {
 #pragma unroll
     for (int w = 0; w < kSeenWords; ++w) tree.seen[n][w] = 0;
     int d = -1;
