@@ -172,12 +172,8 @@ struct Walk {
   Request r;
   int b, h, tile, c;  // the chunk's request, head, row tile, and place in the unit
   long long left;     // chunks from here on
-  __device__ __forceinline__ Walk(const AttendParams& p, const Share& s, bool has)
-      : r(request_of(p, s.b)), b(s.b), left(has ? s.end - s.begin : 0) {
-    if (!has) {
-      h = tile = c = 0;
-      return;
-    }
+  __device__ __forceinline__ Walk(const AttendParams& p, const Share& s)
+      : r(request_of(p, s.b)), b(s.b), left(s.end - s.begin) {
     const int unit = (int)(s.at / r.chunks);
     c = (int)(s.at - (long long)unit * r.chunks);
     h = unit / r.tiles;
