@@ -114,6 +114,33 @@ __device__ __forceinline__ void tmem_stored() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+// mbar_wait for waits that are long as a rule: the warp sleeps (for 20 us at a time) instead of asking
+// again, which would take issue slots from the others.
+__device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity, unsigned long long limit) {
+  if (limit == 0) return false;
+  auto ask = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (ask()) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    if (ask()) return true;
+    if (global_ns() - t0 > limit) return false;
+  }
+}
+__device__ __forceinline__ void store16(uint32_t addr, const uint32_t (&x)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3])
+               : "memory");
+}
+
 // Shared-memory descriptors: 128-byte swizzle, version 1.  Keys and queries (K-major): 8 rows of 128
 // bytes every 1024.  Values (MN-major): 64 dimensions a block, blocks 16384 bytes
 // apart, 8 slots every 1024.
@@ -126,6 +153,15 @@ constexpr uint32_t kBlockBytes = 128 * 128;  // 128 rows or slots of 64 dimensio
 __host__ __device__ constexpr uint32_t idesc(int n, bool mn_major) {
   return 1u << 4 | (mn_major ? 3u << 15 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
 }
+
+// A chunk ahead: addresses of each 16 slots' key codes and key scales (of some page where there is
+// none), which of them are pages (bits), and which slots are seen by anybody (first <= slot in the chunk
+// < last); whole: every slot is.
+struct ChunkRef {
+  unsigned long long codes[8], scales[8];
+  uint32_t valid;
+  int first, last, whole;
+};
 
 template <int D, int NC>
 struct ManySmem {
@@ -142,6 +178,7 @@ struct ManySmem {
   int pos[NC], node[NC], out_row[NC];
   float part[4][NC];
   alignas(8) unsigned long long qk_done, pv_done, drained;  // completed by the tensor pipe
+  ChunkRef refs[2];  // of even and odd chunks
   uint32_t tmem;
   long long scan[kManyThreads / 32 + 2];
 };
@@ -164,26 +201,6 @@ struct Part {
   uint32_t scale[kU];  // bytes
   uint32_t off;        // bit i: row i counts as NaN (keys) or 0 (values), whatever its byte
 };
-
-// Loads that nothing waits for until their registers are used: where `ok`, else zeros.
-__device__ __forceinline__ uint4 load16_if(const char* p, bool ok) {
-  uint4 v;
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n"
-      " mov.u32 %2, 0;\n mov.u32 %3, 0;\n @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"((uint32_t)ok));
-  return v;
-}
-__device__ __forceinline__ uint32_t load_byte_if(const char* p, bool ok) {
-  uint32_t v;
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, 0;\n"
-      " @p ld.global.u8 %0, [%1];\n}"
-      : "=&r"(v)
-      : "l"(p), "r"((uint32_t)ok));
-  return v;
-}
 
 // NC / 2 columns of tensor memory from `addr` on.
 template <int N>
@@ -230,7 +247,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   if (tid == 0) {
     mbar_init(smem_u32(&sm.qk_done), 1);
     mbar_init(smem_u32(&sm.pv_done), 1);
-    mbar_init(smem_u32(&sm.drained), 1);
+    mbar_init(smem_u32(&sm.drained), 2);
     fence_mbar_init();
   }
   pdl_wait();
@@ -253,58 +270,87 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   // decoding: rows 8 (blk + 16 i) + r8 of the chunk's 128 slots, group g
   const int r8 = tid & 7, g = (tid >> 3) % G, blk = (tid >> 3) / G;
   constexpr int kBlk = 32 / G;  // 8-row blocks that the threads cover at once
-  const int block = page_bytes(1, D) << p.cache.shift, scales = (D / 2) << p.cache.shift;
-  const int mask = (1 << p.cache.shift) - 1;
+  const int block = page_bytes(1, D) << p.cache.shift;
   Part<D> keys, vals;
-  int id[kU];
-  auto fetch_ids = [&](const Walk& w) {
-    if (w.left <= 0) return;
-    const int* table = p.cache.table + (long long)w.b * p.cache.M;
-    const int slot0 = (w.r.lo / kSlotsTile + w.c) * kSlotsTile;
+  // Warp 7 finds the addresses (lane k < 8 of the k-th 16 slots' codes, lane k + 8 of their scales),
+  // two chunks ahead, from page ids that it read a chunk before that.
+  Walk ahead(p, share);
+  unsigned j_ahead = 0;
+  int id = -1;
+  auto fetch_id = [&] {
+    const int slot = (ahead.r.lo / kSlotsTile + ahead.c) * kSlotsTile + 16 * (lane & 7);
+    id = ahead.left > 0 && slot < ahead.r.len
+             ? p.cache.table[(long long)ahead.b * p.cache.M + (slot >> p.cache.shift)]
+             : -1;
+  };
+  auto find = [&] {
+    if (warp != 7 || ahead.left <= 0) return;
+    const int slot0 = (ahead.r.lo / kSlotsTile + ahead.c) * kSlotsTile;
+    const bool ok = (unsigned)id < (unsigned)p.cache.pages;
+    const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffu;
+    const int token = (slot0 + 16 * (lane & 7)) & ((1 << p.cache.shift) - 1);
+    const unsigned long long at =
+        reinterpret_cast<unsigned long long>(p.cache.data) +
+        (unsigned long long)(ok ? (unsigned)id : 0u) * p.cache.page_stride +
+        (long long)(2 * ahead.h) * block +
+        (lane & 8 ? ((D / 2) << p.cache.shift) + token * (D / kGroup) : token * (D / 2));
+    ChunkRef& ref = sm.refs[j_ahead & 1];
+    if (lane < 8) ref.codes[lane] = at;
+    if (lane >= 8 && lane < 16) ref.scales[lane - 8] = at;
+    if (lane == 0) {
+      ref.valid = valid;
+      ref.first = max(0, ahead.r.lo - slot0);
+      ref.last = min(kSlotsTile, ahead.r.len - slot0);
+      ref.whole = valid == 0xffu && slot0 >= ahead.r.lo && slot0 + kSlotsTile <= ahead.r.len;
+    }
+    ++j_ahead;
+    ahead.step(p);
+    fetch_id();
+  };
+  const int code_at = (blk & 1) * 4 * D + r8 * (D / 2) + g * 16;  // from the 16 slots' first codes
+  const int scale_off = (blk & 1) * 8 + r8 + g * 16;              // and from their scales
+  static_assert(kBlk % 2 == 0, "");
+  auto load = [&](const ChunkRef& ref, Part<D>& x, bool values) {
+    x.off = 0;
+    if (ref.valid) {  // (the cache has a page at all)
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int slot = slot0 + 8 * (blk + kBlk * i);
-      id[i] = slot < w.r.len ? table[slot >> p.cache.shift] : -1;
+      for (int i = 0; i < kU; ++i) {
+        const int k = (blk + kBlk * i) >> 1, more = values ? block : 0;
+        x.w[i] = *reinterpret_cast<const uint4*>(ref.codes[k] + (code_at + more));
+        x.scale[i] = *reinterpret_cast<const unsigned char*>(ref.scales[k] + (scale_off + more));
+      }
+    }
+    if (!ref.whole) {
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        const int b8 = blk + kBlk * i, slot = 8 * b8 + r8;
+        const bool there = ref.valid >> (b8 >> 1) & 1;
+        if (!there || (values && (slot < ref.first || slot >= ref.last))) x.off |= 1u << i;
+      }
     }
   };
-  // (the chunk that `w` stands at, its page ids in `id`)
-  auto load = [&](const Walk& w) {
-    const int slot0 = (w.r.lo / kSlotsTile + w.c) * kSlotsTile;
-    keys.off = vals.off = 0;
+  // where the thread's four words of a row go (the rows of a tile's next blocks follow at a stride)
+  uint32_t row_to[4];
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int slot = slot0 + 8 * (blk + kBlk * i) + r8;
-      const bool ok = (unsigned)id[i] < (unsigned)p.cache.pages;
-      const char* base = p.cache.data + (unsigned long long)(unsigned)id[i] * p.cache.page_stride +
-                         (long long)(2 * w.h) * block;
-      const int token = slot & mask;
-      const char* codes = base + (token * (D / 2) + g * 16);
-      const char* bytes = base + (scales + (token >> 4) * (D / 2) + g * 16 + (token & 15));
-      keys.w[i] = load16_if(codes, ok);
-      vals.w[i] = load16_if(codes + block, ok);
-      keys.scale[i] = load_byte_if(bytes, ok);
-      vals.scale[i] = load_byte_if(bytes + block, ok);
-      keys.off |= (ok ? 0u : 1u) << i;
-      vals.off |= (ok && slot >= w.r.lo && slot < w.r.len ? 0u : 1u) << i;
-    }
-  };
-  // `nothing`: the scale of a row that has none
-  auto put = [&](const Part<D>& x, char* tile, uint32_t nothing) {
+  for (int q = 0; q < 4; ++q)
+    row_to[q] = smem_u32(sm.v) + (g >> 1) * kBlockBytes + (8 * blk + r8) * 128 +
+                ((((g & 1) * 4 + q) ^ r8) << 4);
+  // `tile`: bytes from the values' tile on; `nothing`: the scale of a row that has none
+  auto put = [&](const Part<D>& x, int tile, uint32_t nothing) {
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       Scale2 sc;
       sc.set((x.off >> i & 1 ? nothing : x.scale[i] * 128u + 0x400u) * 0x10001u);
-      char* row = tile + (g >> 1) * kBlockBytes + (8 * (blk + kBlk * i) + r8) * 128;
       const uint32_t words[4] = {x.w[i].x, x.w[i].y, x.w[i].z, x.w[i].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t d[4];
         decode_word(words[q], sc, d);
-        *reinterpret_cast<uint4*>(row + ((((g & 1) * 4 + q) ^ r8) << 4)) =
-            make_uint4(d[0], d[1], d[2], d[3]);
+        store16(row_to[q] + tile + 8 * kBlk * i * 128, d);
       }
     }
   };
+  constexpr int kKeyTile = D / 64 * (int)kBlockBytes;  // (behind the values')
 
   // Q and the constants of the rows of the piece that `w` stands at: D / 8 threads a row
   auto bring_rows = [&](const Walk& w, bool sees) {
@@ -372,11 +418,13 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + row_at;
   const float cap = p.softcap * kLog2e;
 
-  Walk w(p, share), ahead = w;  // `ahead`: the chunk whose page ids come next
-  fetch_ids(ahead);
-  load(ahead);
-  ahead.step(p);
-  fetch_ids(ahead);
+  Walk w(p, share);
+  if (warp == 7) fetch_id();
+  find();
+  find();
+  __syncthreads();
+  load(sm.refs[0], keys, false);
+  load(sm.refs[0], vals, true);
   unsigned j = 0;       // chunks so far
   bool late = false;    // a wait ran out (the same in every thread)
   while (w.left > 0) {
@@ -388,11 +436,11 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     bool sees = r.ok && r.len > 0;
     if (p.parent && sees) sees = build_tree<kManyThreads>(p, b, r.nq, tree, tid, 1);
     bring_rows(w, sees);
-    put(keys, sm.k, 0x7fffu);
+    put(keys, kKeyTile, 0x7fffu);
     fence_proxy_async();
     fence_before();
     __syncthreads();
-    if (warp == 0 && !late && elect_one()) {
+    if (warp == 4 && !late && elect_one()) {
       fence_after();
       issue_scores();
     }
@@ -402,15 +450,14 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     for (int i = 0; i < NH / 2; ++i) l[i] = pack2(0.f, 0.f);
     int c = c0;
     for (; c < c1 && !late; ++c, ++j) {
-      // the values, in the place of the last chunk's
-      bool out_of_time = j > 0 && !mbar_wait(pv_bar, (j - 1) & 1, limit);
-      put(vals, sm.v, 0u);
       w.step(p);  // (stands at the next chunk from here on)
-      if (w.left > 0) load(ahead);
-      ahead.step(p);
-      fetch_ids(ahead);
-
-      out_of_time = out_of_time || !mbar_wait(qk_bar, j & 1, limit);
+      const ChunkRef& next = sm.refs[(j + 1) & 1];
+      if (w.left > 0) load(next, keys, false);
+      // the values, in the place of the last chunk's
+      bool out_of_time = j > 0 && !sleep_wait(pv_bar, (j - 1) & 1, limit);
+      put(vals, 0, 0u);
+      if (w.left > 0) load(next, vals, true);
+      out_of_time = out_of_time || !sleep_wait(qk_bar, j & 1, limit);
       fence_after();
       const int slot0 = (r.lo / kSlotsTile + c) * kSlotsTile, slot = slot0 + slot_at;
       const bool edge = !sees || slot0 + kSlotsTile > r.base ||
@@ -444,14 +491,23 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
         load_scores();
         // exponents of the weights; is one too large for its row's reference?
         float top[2] = {-INFINITY, -INFINITY};
+        if (plain) {
 #pragma unroll
-        for (int i = 0; i < NH / 2; ++i) {
-          const float4 fo = sm.fo[row_at / 2 + i];
-          const f32x2 f = plain ? pack2(fo.x, fo.y) : pack2(1.f, 1.f);
-          unpack2(fma2(pack2(s[2 * i], s[2 * i + 1]), f, pack2(fo.z, fo.w)), s[2 * i],
-                  s[2 * i + 1]);
-          top[i & 1] = max3(top[i & 1], s[2 * i], s[2 * i + 1]);
+          for (int i = 0; i < NH / 2; ++i) {
+            const float4 fo = sm.fo[row_at / 2 + i];
+            unpack2(fma2(pack2(s[2 * i], s[2 * i + 1]), pack2(fo.x, fo.y), pack2(fo.z, fo.w)),
+                    s[2 * i], s[2 * i + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NH / 2; ++i) {
+            const float4 fo = sm.fo[row_at / 2 + i];
+            s[2 * i] += fo.z;
+            s[2 * i + 1] += fo.w;
+          }
         }
+#pragma unroll
+        for (int i = 0; i < NH / 2; ++i) top[i & 1] = max3(top[i & 1], s[2 * i], s[2 * i + 1]);
         if (!__syncthreads_or(fmaxf(top[0], top[1]) > kManyShift + kSlack)) break;
         // each row's max over the chunk's slots
         load_scores();
@@ -486,7 +542,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           tmem_store(mine + kOCol, o);
         }
       }
-      char* to = sm.p + slot_at * 128;
+      find();  // (in the place of this chunk's)
+      const uint32_t to = smem_u32(sm.p) + slot_at * 128;
 #pragma unroll
       for (int i = 0; i < NH / 8; ++i) {
         uint32_t x[4];
@@ -496,18 +553,21 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           l[4 * i + e] = add2(l[4 * i + e], pack2(w0, w1));
           x[e] = pack_f16(w0, w1);
         }
-        *reinterpret_cast<uint4*>(to + (((row_at / 8 + i) ^ (slot_at & 7)) << 4)) =
-            make_uint4(x[0], x[1], x[2], x[3]);
+        store16(to + (((row_at / 8 + i) ^ (slot_at & 7)) << 4), x);
       }
       // the next chunk's keys (its scores' operand is free: this chunk's are out)
-      if (c + 1 < c1) put(keys, sm.k, 0x7fffu);
+      if (c + 1 < c1) put(keys, kKeyTile, 0x7fffu);
       fence_proxy_async();
       fence_before();
       late = __syncthreads_or(out_of_time);
+      // (from two warps, so that one's issuing does not wait for the other's)
       if (warp == 0 && !late && elect_one()) {
         fence_after();
         issue_out(c > c0);
-        if (c + 1 < c1) issue_scores();
+      }
+      if (warp == 4 && !late && c + 1 < c1 && elect_one()) {
+        fence_after();
+        issue_scores();
       }
       __syncwarp();
     }
@@ -590,9 +650,11 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   }
   if (late && tid == 0) p.late[cta] = 1;
   // nothing is in flight when tensor memory is freed
-  if (warp == 0) {
+  if (warp == 0 || warp == 4) {
     if (elect_one()) mma_commit(smem_u32(&sm.drained));
     __syncwarp();
+  }
+  if (warp == 0) {
     mbar_wait(smem_u32(&sm.drained), 0);
     __syncwarp();
     tmem_free(tmem);
