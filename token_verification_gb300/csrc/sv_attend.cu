@@ -300,8 +300,8 @@ __host__ __device__ constexpr int few_ring() {
   return ring > rows ? ring : rows;
 }
 template <int D, int NT>
-constexpr size_t few_smem(bool tree) {
-  return kFewScan + few_ring<D, NT>() + (tree ? sizeof(TreeView) : 0);
+constexpr size_t few_smem() {
+  return kFewScan + few_ring<D, NT>();
 }
 
 // CTAs an SM holds: as many as their registers allow without spills to speak of.
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
   long long* scan = reinterpret_cast<long long*>(raw_smem);
   char* ring = raw_smem + kFewScan;
   float* rows_out = reinterpret_cast<float*>(ring);
-  TreeView& tree = *reinterpret_cast<TreeView*>(ring + few_ring<D, NT>());  // (if p.parent)
+  const TreeView tree(ring + few_ring<D, NT>(), p.N);  // (if p.parent)
   pdl_wait();
   pdl_launch_dependents();
   const int cta = blockIdx.x, lane = lane_id(), warp = threadIdx.x / 32;
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
         const int row = min(row0 + 8 * n + 2 * t + e, max(rows - 1, 0));
         const int i = row / p.group;
         where[n].node[e] = i;
-        where[n].pos[e] = r.base + (p.parent && sees ? tree.depth[i] : i);
+        where[n].pos[e] = r.base + (p.parent && sees ? tree.depth(i) : i);
         where[n].slope[e] = p.slopes ? p.slopes[h * p.group + row - i * p.group] * kLog2e : 0.f;
       }
 #pragma unroll
@@ -457,14 +457,14 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
               const int node = slot - r.base;
               const bool there = slot < r.len;
               int pos = slot;
-              if (p.parent && node >= 0 && there) pos = r.base + tree.depth[node];
+              if (p.parent && node >= 0 && there) pos = r.base + tree.depth(node);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   bool seen = there;
                   if (node >= 0 && there)
-                    seen = p.parent ? (tree.seen[where[n].node[e]][node >> 5] >> (node & 31)) & 1
+                    seen = p.parent ? tree.sees(where[n].node[e], node)
                                     : node <= where[n].node[e];
                   const int far = where[n].pos[e] - pos;
                   if (p.window > 0 && far >= p.window) seen = false;
@@ -631,19 +631,24 @@ template <int D, typename T>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  if (p.out_status && blockIdx.y == 0) {
-    for (int b = blockIdx.x * kJoinThreads + threadIdx.x; b < p.B; b += gridDim.x * kJoinThreads) {
+  if (p.out_status && blockIdx.y == 0) {  // (a warp a request)
+    const int lane = lane_id();
+    bool late = false;  // (a wait that ran out is every request's, so seldom is it)
+    if (p.late)
+      for (int i = lane; i < (int)gridDim.x; i += 32) late = late || p.late[i];
+    const int ran_out = __any_sync(kAll, late) ? kTimeout : 0;
+    for (int b = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; b < p.B;
+         b += gridDim.x * (kJoinThreads / 32)) {
       const Request r = request_of(p, b);
-      int late = 0;
-      if (p.late)  // (a wait that ran out is every request's, so seldom is it)
-        for (int i = 0; i < (int)gridDim.x; ++i) late |= p.late[i];
       int st = r.ok ? page_status(p.cache, b, r.lo, r.len - r.lo) : kBadDraftLen;
       if (r.ok && p.parent) {
         const int* parent = p.parent + (long long)b * p.parent_stride;
-        for (int n = 1; n < r.nq; ++n)
-          if (parent[n - 1] < 0 || parent[n - 1] >= n) st |= kBadTree;
+        bool bad = false;
+        for (int n = 1 + lane; n < r.nq; n += 32)
+          bad = bad || parent[n - 1] < 0 || parent[n - 1] >= n;
+        if (__any_sync(kAll, bad)) st |= kBadTree;
       }
-      p.out_status[b] = st | (late ? kTimeout : 0);
+      if (lane == 0) p.out_status[b] = st | ran_out;
     }
   }
   const int cta = blockIdx.x;
@@ -725,8 +730,8 @@ cudaError_t plan_one(AttendPlan* plan) {
   plan->chunk = D == 256 ? 16 : 32;
   plan->least = kFewWarps;
   plan->shift = kFewShift;
-  return resident(few_kernel<D, NT, T>, kFewThreads, few_smem<D, NT>(false), few_smem<D, NT>(true),
-                  cache, &plan->ctas);
+  return resident(few_kernel<D, NT, T>, kFewThreads, few_smem<D, NT>(),
+                  few_smem<D, NT>() + tree_bytes(SV_MAX_STEP), cache, &plan->ctas);
 }
 
 }  // namespace
@@ -757,8 +762,8 @@ cudaError_t launch_few(const AttendParams& p, int D, int dtype, const AttendPlan
                        cudaStream_t stream) {
   const int rows = plan.rows;
 #define SV_LAUNCH(d, n, T) \
-  (launch_early(few_kernel<d, n, T>, plan.ctas, kFewThreads, few_smem<d, n>(p.parent != nullptr), 1, \
-                stream, p))
+  (launch_early(few_kernel<d, n, T>, plan.ctas, kFewThreads, \
+                few_smem<d, n>() + (p.parent ? tree_bytes(p.N) : 0), 1, stream, p))
   SV_FEW(SV_LAUNCH)
 #undef SV_LAUNCH
 }

@@ -16,8 +16,6 @@
 
 namespace sv {
 
-constexpr int kMaxStep = 257;                    // tokens of a step (a tree of 256 nodes and its root)
-constexpr int kSeenWords = (kMaxStep + 31) / 32;  // bits of one node's ancestors
 // Weights are 2^(score - max + shift).  With a shift of 15 the largest is 2^15, and fp16's
 // least step of 2^-24 is 2^-39 of it.
 constexpr float kFewShift = 15.f;
@@ -204,37 +202,43 @@ __device__ __forceinline__ int pieces_of(const Share& s, int cta, long long u1) 
   return n;
 }
 
-// A request's tree in shared memory: which nodes each node sees, and its depth.
+// A request's tree in shared memory: which nodes each node sees (bits), and its depth.
 struct TreeView {
-  uint32_t seen[kMaxStep][kSeenWords];
-  int depth[kMaxStep];
-  int parent[kMaxStep];
-  int bad;
+  int* mem;  // [N] depths, [N] parents, whether they are no tree, [N][words] bits
+  int N, words;
+  __device__ __forceinline__ TreeView(void* at, int n)
+      : mem(static_cast<int*>(at)), N(n), words((n + 31) / 32) {}
+  __device__ __forceinline__ int& depth(int n) const { return mem[n]; }
+  __device__ __forceinline__ int& parent(int n) const { return mem[N + n]; }
+  __device__ __forceinline__ int& bad() const { return mem[2 * N]; }
+  __device__ __forceinline__ int& bits(int n, int w) const { return mem[2 * N + 1 + n * words + w]; }
+  __device__ __forceinline__ bool sees(int n, int other) const {
+    return bits(n, other >> 5) >> (other & 31) & 1;
+  }
 };
+inline size_t tree_bytes(int N) { return ((size_t)N * (2 + (N + 31) / 32) + 1) * sizeof(int); }
 
 // Builds it with T threads (this one: t) that share a named barrier; false when the parents are no tree.
 template <int T>
-__device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq, TreeView& tree,
-                                           int t, int barrier) {
+__device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq,
+                                           const TreeView& tree, int t, int barrier) {
   auto meet = [=] { asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(T) : "memory"); };
   meet();
-  if (t == 0) tree.bad = 0;
+  if (t == 0) tree.bad() = 0;
   meet();
   const int* parent = p.parent + (long long)b * p.parent_stride;
   for (int n = t; n < nq; n += T) {
     const int up = n ? parent[n - 1] : -1;
-    tree.parent[n] = up;
-    if (n && (up < 0 || up >= n)) tree.bad = 1;
+    tree.parent(n) = up;
+    if (n && (up < 0 || up >= n)) tree.bad() = 1;
   }
   meet();
-  if (tree.bad) return false;
+  if (tree.bad()) return false;
   for (int n = t; n < nq; n += T) {
-#pragma unroll
-    for (int w = 0; w < kSeenWords; ++w) tree.seen[n][w] = 0;
+    for (int w = 0; w < tree.words; ++w) tree.bits(n, w) = 0;
     int d = -1;
-    for (int at = n; at >= 0; at = tree.parent[at], ++d)
-      tree.seen[n][at >> 5] |= 1u << (at & 31);
-    tree.depth[n] = d;
+    for (int at = n; at >= 0; at = tree.parent(at), ++d) tree.bits(n, at >> 5) |= 1 << (at & 31);
+    tree.depth(n) = d;
   }
   meet();
   return true;

@@ -170,6 +170,7 @@ struct ManySmem {
   alignas(1024) char k[kTileBytes];
   alignas(1024) char p[kBlockBytes];  // weights [slot][64 rows]; a finished piece's rows
   alignas(1024) char q[D / 64 * NC * 128];
+  uint4 raw[2][D / 64][kManyThreads];  // the codes of keys and values on their way
   // the piece's rows: {factor of scores, the same, shift - reference, the same} of pairs of rows,
   // the reference, the last change of it, 1 / sum, a slope, the position, the step's
   // token, the row of `out` counted from the request's first; what the warps leave to be joined
@@ -178,13 +179,13 @@ struct ManySmem {
   int pos[NC], node[NC], out_row[NC];
   float part[4][NC];
   alignas(8) unsigned long long qk_done, pv_done, drained;  // completed by the tensor pipe
-  ChunkRef refs[2];  // of even and odd chunks
+  ChunkRef refs[4];  // of chunk j in j mod 4
   uint32_t tmem;
   long long scan[kManyThreads / 32 + 2];
 };
 template <int D, int NC>
-constexpr size_t many_smem(bool tree) {
-  return 1024 + (sizeof(ManySmem<D, NC>) + 15) / 16 * 16 + (tree ? sizeof(TreeView) : 0);
+constexpr size_t many_smem() {
+  return 1024 + sizeof(ManySmem<D, NC>);
 }
 
 __device__ __forceinline__ float warp_top(float x) {
@@ -197,10 +198,18 @@ __device__ __forceinline__ float warp_top(float x) {
 template <int D>
 struct Part {
   static constexpr int kU = D / 64;
-  uint4 w[kU];
   uint32_t scale[kU];  // bytes
   uint32_t off;        // bit i: row i counts as NaN (keys) or 0 (values), whatever its byte
 };
+__device__ __forceinline__ void copy16(uint32_t dst, unsigned long long src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// (volatile: where it stands, not where its result is used)
+__device__ __forceinline__ uint32_t load_byte(unsigned long long src) {
+  uint32_t x;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(x) : "l"(src) : "memory");
+  return x;
+}
 
 // NC / 2 columns of tensor memory from `addr` on.
 template <int N>
@@ -237,8 +246,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   extern __shared__ __align__(16) char many_raw[];
   ManySmem<D, NC>& sm = *reinterpret_cast<ManySmem<D, NC>*>(
       many_raw + ((1024 - (smem_u32(many_raw) & 1023)) & 1023));
-  TreeView& tree = *reinterpret_cast<TreeView*>(reinterpret_cast<char*>(&sm) +
-                                                (sizeof(sm) + 15) / 16 * 16);  // (if p.parent)
+  const TreeView tree(reinterpret_cast<char*>(&sm) + sizeof(sm), p.N);  // (if p.parent)
   constexpr int G = D / 32;     // groups of a row
   constexpr int kU = Part<D>::kU;
   constexpr int NH = NC / 2;    // rows of a thread
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const int block = page_bytes(1, D) << p.cache.shift;
   Part<D> keys, vals;
   // Warp 7 finds the addresses (lane k < 8 of the k-th 16 slots' codes, lane k + 8 of their scales),
-  // two chunks ahead, from page ids that it read a chunk before that.
+  // three chunks ahead, from page ids that it read a chunk before that.
   Walk ahead(p, share);
   unsigned j_ahead = 0;
   int id = -1;
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
         (unsigned long long)(ok ? (unsigned)id : 0u) * p.cache.page_stride +
         (long long)(2 * ahead.h) * block +
         (lane & 8 ? ((D / 2) << p.cache.shift) + token * (D / kGroup) : token * (D / 2));
-    ChunkRef& ref = sm.refs[j_ahead & 1];
+    ChunkRef& ref = sm.refs[j_ahead & 3];
     if (lane < 8) ref.codes[lane] = at;
     if (lane >= 8 && lane < 16) ref.scales[lane - 8] = at;
     if (lane == 0) {
@@ -310,14 +318,16 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const int code_at = (blk & 1) * 4 * D + r8 * (D / 2) + g * 16;  // from the 16 slots' first codes
   const int scale_off = (blk & 1) * 8 + r8 + g * 16;              // and from their scales
   static_assert(kBlk % 2 == 0, "");
+  const uint32_t raw_at = smem_u32(&sm.raw[0][0][tid]);
   auto load = [&](const ChunkRef& ref, Part<D>& x, bool values) {
     x.off = 0;
     if (ref.valid) {  // (the cache has a page at all)
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
         const int k = (blk + kBlk * i) >> 1, more = values ? block : 0;
-        x.w[i] = *reinterpret_cast<const uint4*>(ref.codes[k] + (code_at + more));
-        x.scale[i] = *reinterpret_cast<const unsigned char*>(ref.scales[k] + (scale_off + more));
+        copy16(raw_at + (values ? kU * kManyThreads * 16 : 0) + i * kManyThreads * 16,
+               ref.codes[k] + (code_at + more));
+        x.scale[i] = load_byte(ref.scales[k] + (scale_off + more));
       }
     }
     if (!ref.whole) {
@@ -328,6 +338,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
         if (!there || (values && (slot < ref.first || slot >= ref.last))) x.off |= 1u << i;
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // where the thread's four words of a row go (the rows of a tile's next blocks follow at a stride)
   uint32_t row_to[4];
@@ -336,12 +347,15 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     row_to[q] = smem_u32(sm.v) + (g >> 1) * kBlockBytes + (8 * blk + r8) * 128 +
                 ((((g & 1) * 4 + q) ^ r8) << 4);
   // `tile`: bytes from the values' tile on; `nothing`: the scale of a row that has none
+  // (keys and values come in turn: the copies behind the wanted ones are the other's)
   auto put = [&](const Part<D>& x, int tile, uint32_t nothing) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       Scale2 sc;
       sc.set((x.off >> i & 1 ? nothing : x.scale[i] * 128u + 0x400u) * 0x10001u);
-      const uint32_t words[4] = {x.w[i].x, x.w[i].y, x.w[i].z, x.w[i].w};
+      const uint4 w4 = sm.raw[tile == 0][i][tid];
+      const uint32_t words[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t d[4];
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
         sm.m[at] = -INFINITY;
         sm.slope[at] = p.slopes ? p.slopes[head] * kLog2e : 0.f;
         sm.node[at] = i;
-        sm.pos[at] = w.r.base + (p.parent && sees ? tree.depth[i] : i);
+        sm.pos[at] = w.r.base + (p.parent && sees ? tree.depth(i) : i);
         sm.out_row[at] = i * p.Hq + head;
       }
     }
@@ -422,9 +436,26 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   if (warp == 7) fetch_id();
   find();
   find();
+  find();
   __syncthreads();
   load(sm.refs[0], keys, false);
   load(sm.refs[0], vals, true);
+  // (a chunk's worth of work lies between a load and the use of it)
+  const unsigned n = (unsigned)w.left;
+  auto put_keys = [&](unsigned i) {  // of chunk i, then the next one's are on their way
+    put(keys, kKeyTile, 0x7fffu);
+    if (i + 1 < n)
+      load(sm.refs[(i + 1) & 3], keys, false);
+    else
+      asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto put_values = [&](unsigned i) {
+    put(vals, 0, 0u);
+    if (i + 1 < n)
+      load(sm.refs[(i + 1) & 3], vals, true);
+    else
+      asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   unsigned j = 0;       // chunks so far
   bool late = false;    // a wait ran out (the same in every thread)
   while (w.left > 0) {
@@ -436,11 +467,11 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     bool sees = r.ok && r.len > 0;
     if (p.parent && sees) sees = build_tree<kManyThreads>(p, b, r.nq, tree, tid, 1);
     bring_rows(w, sees);
-    put(keys, kKeyTile, 0x7fffu);
+    put_keys(j);
     fence_proxy_async();
     fence_before();
     __syncthreads();
-    if (warp == 4 && !late && elect_one()) {
+    if (warp == 0 && !late && elect_one()) {
       fence_after();
       issue_scores();
     }
@@ -451,12 +482,9 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     int c = c0;
     for (; c < c1 && !late; ++c, ++j) {
       w.step(p);  // (stands at the next chunk from here on)
-      const ChunkRef& next = sm.refs[(j + 1) & 1];
-      if (w.left > 0) load(next, keys, false);
       // the values, in the place of the last chunk's
       bool out_of_time = j > 0 && !sleep_wait(pv_bar, (j - 1) & 1, limit);
-      put(vals, 0, 0u);
-      if (w.left > 0) load(next, vals, true);
+      put_values(j);
       out_of_time = out_of_time || !sleep_wait(qk_bar, j & 1, limit);
       fence_after();
       const int slot0 = (r.lo / kSlotsTile + c) * kSlotsTile, slot = slot0 + slot_at;
@@ -471,7 +499,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
         const bool there = sees && slot < r.len;
         const int node = slot - r.base;
         int at = slot;
-        if (p.parent && there && node >= 0) at = r.base + tree.depth[node];
+        if (p.parent && there && node >= 0) at = r.base + tree.depth(node);
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
           const int row = row_at + i;
@@ -481,7 +509,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           bool seen = there;
           if (edge && there && node >= 0) {
             const int other = sm.node[row];
-            seen = p.parent ? tree.seen[other][node >> 5] >> (node & 31) & 1 : node <= other;
+            seen = p.parent ? tree.sees(other, node) : node <= other;
           }
           if (edge && p.window > 0 && sm.pos[row] - at >= p.window) seen = false;
           s[i] = seen ? y : -INFINITY;
@@ -556,7 +584,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
         store16(to + (((row_at / 8 + i) ^ (slot_at & 7)) << 4), x);
       }
       // the next chunk's keys (its scores' operand is free: this chunk's are out)
-      if (c + 1 < c1) put(keys, kKeyTile, 0x7fffu);
+      if (c + 1 < c1) put_keys(j + 1);
       fence_proxy_async();
       fence_before();
       late = __syncthreads_or(out_of_time);
@@ -564,10 +592,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
       if (warp == 0 && !late && elect_one()) {
         fence_after();
         issue_out(c > c0);
-      }
-      if (warp == 4 && !late && c + 1 < c1 && elect_one()) {
-        fence_after();
-        issue_scores();
+        if (c + 1 < c1) issue_scores();
       }
       __syncwarp();
     }
@@ -670,12 +695,12 @@ cudaError_t launch_one(const AttendParams& p, const AttendPlan& plan, cudaStream
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_relaxed)) {
     err = cudaFuncSetAttribute(many_kernel<D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)many_smem<D, NC>(true));
+                               (int)(many_smem<D, NC>() + tree_bytes(SV_MAX_STEP)));
     if (err != cudaSuccess) return err;
     ready[dev].store(1, std::memory_order_relaxed);
   }
   return launch_early(many_kernel<D, NC>, plan.ctas, kManyThreads,
-                      many_smem<D, NC>(p.parent != nullptr), 1, stream, p);
+                      many_smem<D, NC>() + (p.parent ? tree_bytes(p.N) : 0), 1, stream, p);
 }
 
 }  // namespace
@@ -685,7 +710,7 @@ cudaError_t plan_many(int rows, AttendPlan* plan) {
   const cudaError_t err = device_info(&info);
   if (err != cudaSuccess) return err;
   // as few tiles as tiles of 64 would be, with few rows of them empty
-  const int tiles = (rows + 63) / 64, each = (rows + tiles - 1) / tiles;
+  const int tiles = (rows + 47) / 48, each = (rows + tiles - 1) / tiles;
   plan->rows = each <= 32 ? 32 : each <= 48 ? 48 : 64;
   plan->chunk = kSlotsTile;
   plan->least = 1;

@@ -46,12 +46,14 @@ __device__ __forceinline__ int2 request_slots(const CacheParams& p, long long b)
   return make_int2(first, n);
 }
 
+// (a warp a request)
 __device__ __forceinline__ void write_status(const CacheParams& p) {
   if (!p.out_status) return;
-  for (long long b = (long long)blockIdx.x * kCacheThreads + threadIdx.x; b < p.B;
-       b += (long long)gridDim.x * kCacheThreads) {
+  for (long long b = (long long)blockIdx.x * (kCacheThreads / 32) + threadIdx.x / 32; b < p.B;
+       b += (long long)gridDim.x * (kCacheThreads / 32)) {
     const int2 s = request_slots(p, b);
-    p.out_status[b] = s.y < 0 ? kBadDraftLen : page_status(p.cache, b, s.x, s.y);
+    const int st = s.y < 0 ? kBadDraftLen : page_status(p.cache, b, s.x, s.y);
+    if (lane_id() == 0) p.out_status[b] = st;
   }
 }
 
@@ -236,27 +238,25 @@ __global__ void __launch_bounds__(kCacheThreads) keep_kernel(const KeepParams p)
   pdl_wait();
   pdl_launch_dependents();
   const CacheView& c = p.cache;
-  if (p.out_status) {
-    for (long long b = (long long)blockIdx.x * kCacheThreads + threadIdx.x; b < p.B;
-         b += (long long)gridDim.x * kCacheThreads) {
-      const int n = path_length(p, b);
-      int st = n == -1 ? kBadTree : n == -2 ? kBadDraftLen : 0;
-      for (int i = 0; i < n; ++i) {
-        st |= page_status(c, b, p.start[b] + i, 1);
-        st |= page_status(c, b, p.start[b] + p.path[b * p.P + i], 1);
-      }
-      p.out_status[b] = st;
-    }
-  }
   const unsigned unit = blockIdx.x * (kCacheThreads / 32) + threadIdx.x / 32;
   if (unit >= p.units) return;
   const long long b = fast_div(unit, p.div_h);
   const int h = (int)(unit - (unsigned)b * p.div_h.d);
   const int n = path_length(p, b);
-  if (n <= 0) return;
   const int* path = p.path + b * p.P;
   const int* table = c.table + b * c.M;
-  const int start = p.start[b], mask = (1 << c.shift) - 1;
+  const int start = p.start[b];
+  if (p.out_status && h == 0) {
+    bool bad = false;
+    for (int i = lane_id(); i < n; i += 32)
+      bad = bad || (unsigned)table[(start + i) >> c.shift] >= (unsigned)c.pages ||
+            (unsigned)table[(start + path[i]) >> c.shift] >= (unsigned)c.pages;
+    bad = __any_sync(kAll, bad);
+    if (lane_id() == 0)
+      p.out_status[b] = n == -1 ? kBadTree : n == -2 ? kBadDraftLen : bad ? kBadPage : 0;
+  }
+  if (n <= 0) return;
+  const int mask = (1 << c.shift) - 1;
   // units of a token: words of 16 code bytes, and scale bytes, of keys and of values
   constexpr int kCodes = D / 32, kPer = kCodes + D / kGroup;
   for (int u = lane_id(); u < 2 * kPer; u += 32) {

@@ -71,14 +71,14 @@ __device__ __forceinline__ int scale_at(const CacheView& c, int token, int group
   return (D / 2 << c.shift) + ((token >> 4) * (D / kGroup) + group) * 16;
 }
 
-// Request b's bits for the pages that hold slots [first, first + count): the
+// Request b's bits for the pages that hold slots [first, first + count), found by a warp: the
 // caller has checked that they lie inside the table.
 __device__ __forceinline__ int page_status(const CacheView& c, long long b, int first, int count) {
-  if (count <= 0) return 0;
-  int bad = 0;
-  for (int i = first >> c.shift; i <= (first + count - 1) >> c.shift; ++i)
-    bad |= (unsigned)c.table[b * c.M + i] >= (unsigned)c.pages;
-  return bad ? kBadPage : 0;
+  bool bad = false;
+  if (count > 0)
+    for (int i = (first >> c.shift) + lane_id(); i <= (first + count - 1) >> c.shift; i += 32)
+      bad = bad || (unsigned)c.table[b * c.M + i] >= (unsigned)c.pages;
+  return __any_sync(0xffffffffu, bad) ? kBadPage : 0;
 }
 
 }  // namespace sv
