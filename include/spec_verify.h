@@ -588,14 +588,14 @@ sv_status spec_cache_write(void* cache, int64_t page_stride, const void* k,
                            int N, int M, int kv_heads, int head_dim, sv_stream_t stream);
 
 /* Reads tokens back: k[b, i] and v[b, i] of slot start[b] + i (NULL: slot i) for
- * i < lens[b] (NULL: N); rows behind lens[b] are left as they are.  Every value is exact in
- * either type.  k and v as in spec_cache_write; rows of one must not overlap each
+ * i < lens[b] (NULL: N); the other rows are left as they are, or with fill != 0 set to 0.
+ * Every value is exact in either type.  k and v as in spec_cache_write; rows of one must not overlap each
  * other (SV_ERR_ALIAS), nor the other's or the cache. */
 sv_status spec_cache_read(const void* cache, int64_t page_stride, void* k,
                           const int64_t* k_strides, void* v, const int64_t* v_strides,
                           const int32_t* table, const int32_t* start, const int32_t* lens,
-                          int32_t* out_status, sv_dtype dtype, int pages, int page_size, int B,
-                          int N, int M, int kv_heads, int head_dim, sv_stream_t stream);
+                          int fill, int32_t* out_status, sv_dtype dtype, int pages, int page_size,
+                          int B, int N, int M, int kv_heads, int head_dim, sv_stream_t stream);
 
 /* Keeps the accepted path of a tree whose nodes lie in slots start[b] + node: slot
  * start[b] + path[b, i] moves to start[b] + i, for the entries before the first -1

@@ -121,7 +121,7 @@ def lib():
         l.spec_cache_page_bytes.restype = Z
         l.spec_cache_write.argtypes = [P, L, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P]
         l.spec_cache_write.restype = I
-        l.spec_cache_read.argtypes = l.spec_cache_write.argtypes
+        l.spec_cache_read.argtypes = [P, L, P, P, P, P, P, P, P, I, P, I, I, I, I, I, I, I, I, P]
         l.spec_cache_read.restype = I
         l.spec_cache_keep.argtypes = [P, L, P, P, P, P, I, I, I, I, I, I, I, P]
         l.spec_cache_keep.restype = I

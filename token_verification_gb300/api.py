@@ -818,14 +818,13 @@ def spec_cache_read(cache, table, n, head_dim, k=None, v=None, *, start=None, le
     _per_request(device, B, start=start, lens=lens, status=status)
     given = k is not None
     if not given:
-        # (every row is written where there are no lens and nothing is out of range)
-        k, v = (torch.zeros((B, n, H, D), dtype=dtype, device=device) for _ in range(2))
+        k, v = (torch.empty((B, n, H, D), dtype=dtype, device=device) for _ in range(2))
     code = _dtype_code(k)
     ks = _dense(k, "k", device, None, (B, n, H, D))
     vs = _dense(v, "v", device, k.dtype, (B, n, H, D))
     _launch(device, _native.lib().spec_cache_read, cache.data_ptr(), stride, k.data_ptr(), ks,
-            v.data_ptr(), vs, _addr(table), _addr(start), _addr(lens), _addr(status), code, pages,
-            page_size, B, n, M, H, D)
+            v.data_ptr(), vs, _addr(table), _addr(start), _addr(lens), int(not given),
+            _addr(status), code, pages, page_size, B, n, M, H, D)
     _written(*((k, v) if given else ()), status)
     return k, v
 

@@ -2,10 +2,11 @@
 // tree's path in it (spec_cache_write, spec_cache_read, spec_cache_keep).
 //
 // All three move bytes and are bound by HBM (or by the launch for a step's few
-// tokens).  A thread takes 8 values of a token's head, keys and values both:
-// a 16-byte load of bf16 and a 4-byte store of codes (or the reverse) each, the
-// D / 8 threads of a token side by side.  Consecutive tokens of a head go to
-// consecutive threads, so that a page's code rows are read and written whole.
+// tokens).  A thread takes the same 8 values of four neighbouring slots of a head,
+// keys and values both: of each token a 16-byte load of bf16 and a 4-byte store of codes
+// (or the reverse), of all four the scale bytes of a group as one word where all four are
+// touched.  The D / 8 threads of a token lie side by side, consecutive slots in consecutive
+// threads, so that a page's code rows are read and written whole.
 #include <string.h>
 
 #include <algorithm>
@@ -34,8 +35,9 @@ struct CacheParams {
   const int* lens;   // [B] or null (N)
   int* out_status;   // [B] or null
   int B, N;
-  FastDiv div_n, div_h;
-  unsigned long long units;  // B * Hkv * N
+  FastDiv div_n, div_h;      // four slots of a request, heads
+  unsigned long long units;  // B * Hkv * four slots
+  int fill;                  // rows that are not read become 0
 };
 
 // Request b's first slot and count of tokens; count -1 when they do not fit.
@@ -57,53 +59,111 @@ __device__ __forceinline__ void write_status(const CacheParams& p) {
   }
 }
 
-// 8 values at a 16-byte (bf16) or 32-byte (fp32) step.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(u[i]);
-    x[2 * i + 1] = bf16_hi(u[i]);
+constexpr int kSlots = 4;  // neighbouring slots of a thread
+
+// A thread's place: request, head, its first slot's token (may lie before the request's first or
+// behind its last), and where that slot is.
+template <int D>
+struct Place {
+  long long b;
+  int h, lane, first, n, token;  // token: of the thread's first slot
+  int slot;                      // that slot in its page
+  char *k, *v;                   // blocks of the page, null where there is none
+  bool in;                       // a place at all
+};
+
+template <int D>
+__device__ __forceinline__ Place<D> place_of(const CacheParams& p) {
+  constexpr int kLanes = D / 8;
+  Place<D> x;
+  const unsigned long long unit =
+      (unsigned long long)blockIdx.x * (kCacheThreads / kLanes) + threadIdx.x / kLanes;
+  x.lane = threadIdx.x % kLanes;
+  x.in = unit < p.units;
+  x.k = x.v = nullptr;
+  x.first = x.n = x.token = x.slot = 0;
+  x.b = x.h = 0;
+  if (!x.in) return x;
+  const uint32_t bh = fast_div((uint32_t)unit, p.div_n);
+  const int i = (int)((uint32_t)unit - bh * p.div_n.d);
+  x.b = fast_div(bh, p.div_h);
+  x.h = (int)(bh - (uint32_t)x.b * p.div_h.d);
+  const int2 s = request_slots(p, x.b);
+  x.first = s.x;
+  x.n = s.y;
+  const int slot = (s.x & ~(kSlots - 1)) + kSlots * i;
+  x.token = slot - s.x;
+  if (x.token < s.y) {  // (then some of its slots are the request's)
+    const int id = p.cache.table[x.b * p.cache.M + (slot >> p.cache.shift)];
+    if ((unsigned)id < (unsigned)p.cache.pages) {
+      x.slot = slot & ((1 << p.cache.shift) - 1);
+      x.k = page_block<D>(p.cache, id, x.h, 0);
+      x.v = page_block<D>(p.cache, id, x.h, 1);
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)),
-               b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {  // (exact: 7 significant bits)
-    u[i] = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
-  }
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(u[0], u[1], u[2], u[3]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
-  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+  return x;
 }
 
-// Codes and scale byte of 8 values, with the three other threads of their group.
-__device__ __forceinline__ uint32_t encode8(const float (&x)[8], int* byte) {
-  float top = 0.f;
+// 8 values as fp32 bit patterns' source: bf16 pairs, or fp32.
+struct Eight16 {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    w = __ldcs(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
+  // the largest magnitude's bits (an fp32 number; NaN above infinity)
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t u = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+    return i & 1 ? bf16_hi(u) : bf16_lo(u);
+  }
+};
+struct Eight32 {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-  top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-  const int b = scale_byte(top);
-  const float s = scale_of(b);
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(get(i)) & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w
+         : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+  }
+};
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> : Eight16 {};
+template <>
+struct Eight<float> : Eight32 {};
+
+// Codes of 8 values at scale s (r = 1 / s to nearest; limit: above which magnitudes are cut).  The
+// quotient's first value x r, corrected by its exact remainder, is x / s to nearest (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), so it
+// is a half only where x / s is: a half h has 4 bits and s has 4, so an fp32 x beside h s
+// gives a quotient beside h.  Adding 1.5 * 2^23 + 8 leaves the whole number (ties to even) plus 8 in
+// the low bits, and the codes meet in one word by multiplications.
+template <typename T>
+__device__ __forceinline__ uint32_t encode8(const Eight<T>& x, float s, float r, float limit) {
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    // the quotient rounded to fp32 lies at or beside a half exactly when x / s does:
-    // a half h has 4 bits and s 4, so x nearest to h s differs from it by 2^-24 of it
-    const float q = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -7.f), 7.f);
-    w |= (uint32_t)((int)q + 8) << (4 * (i / 2 + 4 * (i % 2)));
+    const float v = fminf(fmaxf(x.get(i), -limit), limit);
+    const float t = v * r;
+    const float q = fmaf(fmaf(-t, s, v), r, t);
+    const int at = 4 * (i / 2 + 4 * (i % 2));
+    w += (__float_as_uint(q + 12582920.f) - 0x4b400000u) << at;
   }
-  *byte = b;
   return w;
 }
 
@@ -113,58 +173,87 @@ __global__ void __launch_bounds__(kCacheThreads) write_kernel(const CacheParams 
   pdl_launch_dependents();
   write_status(p);
   constexpr int kLanes = D / 8;  // threads of a token
-  const unsigned long long unit =
-      (unsigned long long)blockIdx.x * (kCacheThreads / kLanes) + threadIdx.x / kLanes;
-  const int lane = threadIdx.x % kLanes;
-  const CacheView& c = p.cache;
-  float k[8] = {}, v[8] = {};
-  char *kb = nullptr, *vb = nullptr;
-  int token = 0;
-  if (unit < p.units) {
-    const uint32_t bh = fast_div((uint32_t)unit, p.div_n);
-    const int i = (int)((uint32_t)unit - bh * p.div_n.d);
-    const long long b = fast_div(bh, p.div_h);
-    const int h = (int)(bh - (uint32_t)b * p.div_h.d);
-    const int2 s = request_slots(p, b);
-    if (i < s.y) {
-      const int slot = s.x + i;
-      const int id = c.table[b * c.M + (slot >> c.shift)];
-      if ((unsigned)id < (unsigned)c.pages) {
-        token = slot & ((1 << c.shift) - 1);
-        kb = page_block<D>(c, id, h, 0);
-        vb = page_block<D>(c, id, h, 1);
-        load8(static_cast<const T*>(p.k.data) + b * p.k.sb + i * p.k.sn + h * p.k.sh + lane * 8, k);
-        load8(static_cast<const T*>(p.v.data) + b * p.v.sb + i * p.v.sn + h * p.v.sh + lane * 8, v);
-      }
+  const Place<D> x = place_of<D>(p);
+  Eight<T> k[kSlots], v[kSlots];
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) {
+    const int i = x.token + j;
+    if (x.k && i >= 0 && i < x.n) {
+      k[j].load(static_cast<const T*>(p.k.data) + x.b * p.k.sb + i * p.k.sn + x.h * p.k.sh + x.lane * 8);
+      v[j].load(static_cast<const T*>(p.v.data) + x.b * p.v.sb + i * p.v.sn + x.h * p.v.sh + x.lane * 8);
+    } else {
+      k[j].clear();
+      v[j].clear();
     }
   }
-  bool ok = true;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) ok = ok && is_finite(k[j]) && is_finite(v[j]);
   const unsigned mine = kLanes == 32 ? kAll
                                      : ((1u << (kLanes % 32)) - 1) << (lane_id() / kLanes * kLanes);
-  const bool bad = (__ballot_sync(kAll, !ok) & mine) != 0;
-  if (bad) {
+  uint32_t kbytes = 0, vbytes = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) k[j] = v[j] = 0.f;
+  for (int j = 0; j < kSlots; ++j) {
+    uint32_t tk = k[j].top(), tv = v[j].top();
+    // a token of which anything is not finite: values of 0 under the scale that says so
+    const bool bad = (__ballot_sync(kAll, max(tk, tv) >= 0x7f800000u) & mine) != 0;
+    tk = max(tk, __shfl_xor_sync(kAll, tk, 1));
+    tv = max(tv, __shfl_xor_sync(kAll, tv, 1));
+    tk = max(tk, __shfl_xor_sync(kAll, tk, 2));
+    tv = max(tv, __shfl_xor_sync(kAll, tv, 2));
+    if (bad) {
+      tk = tv = 0;
+      k[j].clear();
+      v[j].clear();
+    }
+    const uint32_t bk = scale_byte(__uint_as_float(tk)), bv = scale_byte(__uint_as_float(tv));
+    const float sk = scale_of(bk), sv = scale_of(bv);
+    const int i = x.token + j;
+    const uint32_t wk = encode8<T>(k[j], sk, __frcp_rn(sk), 7.f * sk);
+    const uint32_t wv = encode8<T>(v[j], sv, __frcp_rn(sv), 7.f * sv);
+    if (x.k && i >= 0 && i < x.n) {
+      reinterpret_cast<uint32_t*>(x.k + (x.slot + j) * (D / 2))[x.lane] = wk;
+      reinterpret_cast<uint32_t*>(x.v + (x.slot + j) * (D / 2))[x.lane] = wv;
+    }
+    kbytes |= (bad ? (uint32_t)kNanScale : bk) << (8 * j);
+    vbytes |= bv << (8 * j);
   }
-  int kbyte, vbyte;
-  const uint32_t kw = encode8(k, &kbyte), vw = encode8(v, &vbyte);
-  if (kb) {
-    reinterpret_cast<uint32_t*>(kb + token * (D / 2))[lane] = kw;
-    reinterpret_cast<uint32_t*>(vb + token * (D / 2))[lane] = vw;
-    if (lane % 4 == 0) {
-      const int at = scale_at<D>(c, token, lane / 4) + (token & 15);
-      kb[at] = (char)(bad ? kNanScale : kbyte);
-      vb[at] = (char)vbyte;
+  if (x.k && x.lane % 4 == 0) {
+    const int at = scale_at<D>(p.cache, x.slot, x.lane / 4) + (x.slot & 15);
+    if (x.token >= 0 && x.token + kSlots <= x.n) {
+      *reinterpret_cast<uint32_t*>(x.k + at) = kbytes;
+      *reinterpret_cast<uint32_t*>(x.v + at) = vbytes;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (x.token + j >= 0 && x.token + j < x.n) {
+          x.k[at + j] = (char)(kbytes >> (8 * j));
+          x.v[at + j] = (char)(vbytes >> (8 * j));
+        }
     }
   }
 }
 
-// 8 values of a word of codes.
-__device__ __forceinline__ void decode8(uint32_t w, float s, float (&x)[8]) {
+// The 8 values of a word of codes in bf16, times the scale byte's scale: 128 + c is a bf16 number
+// whose low bits are the code, and (128 + c) s - 136 s is exact (136 s has 8 bits).
+__device__ __forceinline__ uint4 decode8(uint32_t w, uint32_t byte) {
+  uint32_t s = byte * 16 + (kScaleBias << 4);
+  if (byte == kNanScale) s = 0x7fff;
+  s *= 0x10001u;
+  uint32_t off, d[4];
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(off) : "r"(s), "r"(0xc308c308u));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = (float)((int)((w >> (4 * (i / 2 + 4 * (i % 2)))) & 15) - 8) * s;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d[i]) : "r"(c), "r"(s), "r"(off));
+  }
+  return make_uint4(d[0], d[1], d[2], d[3]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const uint4& x) {
+  __stcs(reinterpret_cast<uint4*>(p), x);
+}
+__device__ __forceinline__ void store8(float* p, const uint4& x) {
+  __stcs(reinterpret_cast<float4*>(p),
+         make_float4(bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)));
+  __stcs(reinterpret_cast<float4*>(p) + 1,
+         make_float4(bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)));
 }
 
 template <int D, typename T>
@@ -172,32 +261,35 @@ __global__ void __launch_bounds__(kCacheThreads) read_kernel(const CacheParams p
   pdl_wait();
   pdl_launch_dependents();
   write_status(p);
-  constexpr int kLanes = D / 8;
-  const unsigned long long unit =
-      (unsigned long long)blockIdx.x * (kCacheThreads / kLanes) + threadIdx.x / kLanes;
-  const int lane = threadIdx.x % kLanes;
-  const CacheView& c = p.cache;
-  if (unit >= p.units) return;
-  const uint32_t bh = fast_div((uint32_t)unit, p.div_n);
-  const int i = (int)((uint32_t)unit - bh * p.div_n.d);
-  const long long b = fast_div(bh, p.div_h);
-  const int h = (int)(bh - (uint32_t)b * p.div_h.d);
-  const int2 s = request_slots(p, b);
-  if (i >= s.y) return;
-  const int slot = s.x + i;
-  const int id = c.table[b * c.M + (slot >> c.shift)];
-  if ((unsigned)id >= (unsigned)c.pages) return;
-  const int token = slot & ((1 << c.shift) - 1);
-  const char *kb = page_block<D>(c, id, h, 0), *vb = page_block<D>(c, id, h, 1);
-  const int at = scale_at<D>(c, token, lane / 4) + (token & 15);
-  const uint32_t kw = reinterpret_cast<const uint32_t*>(kb + token * (D / 2))[lane];
-  const uint32_t vw = reinterpret_cast<const uint32_t*>(vb + token * (D / 2))[lane];
-  const int kbyte = (unsigned char)kb[at], vbyte = (unsigned char)vb[at];
-  float k[8], v[8];
-  decode8(kw, kbyte == kNanScale ? qnan() : scale_of(kbyte), k);
-  decode8(vw, kbyte == kNanScale ? qnan() : scale_of(vbyte), v);
-  store8(static_cast<T*>(p.k.data) + b * p.k.sb + i * p.k.sn + h * p.k.sh + lane * 8, k);
-  store8(static_cast<T*>(p.v.data) + b * p.v.sb + i * p.v.sn + h * p.v.sh + lane * 8, v);
+  const Place<D> x = place_of<D>(p);
+  if (!x.in) return;
+  uint32_t kw[kSlots], vw[kSlots], kbytes = 0, vbytes = 0;
+  if (x.k) {
+    // (all four slots lie in the page, whichever of them are wanted)
+    const int at = scale_at<D>(p.cache, x.slot, x.lane / 4) + (x.slot & 15);
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      kw[j] = reinterpret_cast<const uint32_t*>(x.k + (x.slot + j) * (D / 2))[x.lane];
+      vw[j] = reinterpret_cast<const uint32_t*>(x.v + (x.slot + j) * (D / 2))[x.lane];
+    }
+    kbytes = *reinterpret_cast<const uint32_t*>(x.k + at);
+    vbytes = *reinterpret_cast<const uint32_t*>(x.v + at);
+  }
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) {
+    const int i = x.token + j;
+    if (i < 0 || i >= p.N) continue;
+    const bool there = x.k && i < x.n;
+    if (!there && !p.fill) continue;
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    if (there) {
+      const uint32_t bk = kbytes >> (8 * j) & 255, bv = vbytes >> (8 * j) & 255;
+      k = decode8(kw[j], bk);
+      v = decode8(vw[j], bk == kNanScale ? bk : bv);
+    }
+    store8(static_cast<T*>(p.k.data) + x.b * p.k.sb + i * p.k.sn + x.h * p.k.sh + x.lane * 8, k);
+    store8(static_cast<T*>(p.v.data) + x.b * p.v.sb + i * p.v.sn + x.h * p.v.sh + x.lane * 8, v);
+  }
 }
 
 struct KeepParams {
@@ -360,8 +452,8 @@ struct Dense {
 
 sv_status move(bool write, const void* cache, int64_t page_stride, const Dense& t,
                const int32_t* table, const int32_t* start, const int32_t* lens,
-               int32_t* out_status, sv_dtype dtype, int pages, int page_size, int B, int N, int M,
-               int kv_heads, int head_dim, sv_stream_t stream) {
+               int32_t* out_status, int fill, sv_dtype dtype, int pages, int page_size, int B,
+               int N, int M, int kv_heads, int head_dim, sv_stream_t stream) {
   CacheParams p;
   memset(&p, 0, sizeof p);
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
@@ -370,8 +462,11 @@ sv_status move(bool write, const void* cache, int64_t page_stride, const Dense& 
                              head_dim);
   if (rc != SV_OK) return rc;
   if (B == 0) return SV_OK;
-  const unsigned long long units = (unsigned long long)B * kv_heads * N;
-  if (units >= 1ull << 31) return SV_ERR_SHAPE;
+  if ((unsigned long long)B * kv_heads * N >= 1ull << 31) return SV_ERR_SHAPE;
+  // the most aligned fours that N slots can touch
+  const unsigned fours = N == 0 ? 0 : ((unsigned)N + 2 * (kSlots - 1)) / kSlots;
+  const unsigned long long units = (unsigned long long)B * kv_heads * fours;
+  if (units >= 1ull << 32) return SV_ERR_SHAPE;
   const int esize = dtype == SV_F32 ? 4 : 2;
   if (units > 0) {
     if (!t.ks || !t.vs) return SV_ERR_NULL;
@@ -387,7 +482,8 @@ sv_status move(bool write, const void* cache, int64_t page_stride, const Dense& 
   p.B = B;
   p.N = N;
   p.units = units;
-  p.div_n = make_fastdiv((uint32_t)std::max(N, 1));
+  p.fill = fill;
+  p.div_n = make_fastdiv(std::max(fours, 1u));
   p.div_h = make_fastdiv((uint32_t)kv_heads);
   const unsigned per = kCacheThreads / (head_dim / 8);
   unsigned blocks = (unsigned)((units + per - 1) / per);
@@ -431,17 +527,17 @@ extern "C" sv_status spec_cache_write(void* cache, int64_t page_stride, const vo
                                       int head_dim, sv_stream_t stream) {
   if (B > 0 && !start) return SV_ERR_NULL;
   return move(true, cache, page_stride, {k, v, k_strides, v_strides}, table, start, lens,
-              out_status, dtype, pages, page_size, B, N, M, kv_heads, head_dim, stream);
+              out_status, 0, dtype, pages, page_size, B, N, M, kv_heads, head_dim, stream);
 }
 
 extern "C" sv_status spec_cache_read(const void* cache, int64_t page_stride, void* k,
                                      const int64_t* k_strides, void* v, const int64_t* v_strides,
                                      const int32_t* table, const int32_t* start,
-                                     const int32_t* lens, int32_t* out_status, sv_dtype dtype,
-                                     int pages, int page_size, int B, int N, int M, int kv_heads,
-                                     int head_dim, sv_stream_t stream) {
+                                     const int32_t* lens, int fill, int32_t* out_status,
+                                     sv_dtype dtype, int pages, int page_size, int B, int N, int M,
+                                     int kv_heads, int head_dim, sv_stream_t stream) {
   return move(false, cache, page_stride, {k, v, k_strides, v_strides}, table, start, lens,
-              out_status, dtype, pages, page_size, B, N, M, kv_heads, head_dim, stream);
+              out_status, fill, dtype, pages, page_size, B, N, M, kv_heads, head_dim, stream);
 }
 
 extern "C" sv_status spec_cache_keep(void* cache, int64_t page_stride, const int32_t* table,

@@ -37,14 +37,15 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
   return __uint_as_float((byte + kScaleBias) << 20);
 }
 
-// The least scale byte whose scale s has 7 s >= top (finite, >= 0).  7 s is
-// exact in fp32; top / 7 rounded to nearest is >= s exactly when top / 7 is
-// (s is an fp32 number), so cutting it to 4 bits gives the byte or the one below.
+// The least scale byte whose scale s has 7 s >= top (finite, >= 0).  7 s is exact in
+// fp32.  top times 1 / 7, off by 2^-23 of it at most and cut to 4 bits, is that scale or at most
+// two below it.
 __device__ __forceinline__ int scale_byte(float top) {
-  int b = (int)(__float_as_uint(__fdiv_rn(top, 7.f)) >> 20) - kScaleBias;
+  int b = (int)(__float_as_uint(top * 0.142857142857f) >> 20) - kScaleBias;
   b = min(max(b, 0), kTopScale);
-  if (b < kTopScale && 7.f * scale_of(b) < top) ++b;
-  return b;
+  b += 7.f * scale_of(b) < top;
+  b += 7.f * scale_of(b) < top;
+  return min(b, kTopScale);
 }
 
 // Where tokens of a cache lie.
