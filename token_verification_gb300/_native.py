@@ -33,7 +33,7 @@ _binding = None
 
 
 def binding():
-    """The compiled short way to the draft operators (csrc/binding.cpp)."""
+    """The compiled short way to the draft and cache operators (csrc/binding.cpp)."""
     global _binding
     if _binding is not None:
         return _binding
@@ -49,7 +49,9 @@ def binding():
             spec.loader.exec_module(m)
             m.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 l.spec_top_logits, l.spec_distill, l.spec_distill_grad, l.spec_beam_select,
-                l.spec_beam_workspace_size, l.spec_beam_reorder)))
+                l.spec_beam_workspace_size, l.spec_beam_reorder, l.spec_cache_page_bytes,
+                l.spec_cache_write, l.spec_cache_read, l.spec_cache_keep, l.spec_cache_attention,
+                l.spec_cache_attention_workspace_size)))
             _binding = m
     return _binding
 

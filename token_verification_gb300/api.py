@@ -785,6 +785,12 @@ def spec_cache_write(cache, k, v, table, start, *, lens=None, status=None) -> to
     fused projection are fine); table [B, M] int32 page ids; start [B] int32; lens
     [B] int32 (tokens i >= lens[b] are left out) or None; status: an int32 [B]
     tensor to receive the request status, or None.  Returns cache."""
+    if status is None:
+        r = _native.binding().cache_write(cache, k, v, table, start, lens)
+        if r is not None:
+            if r:
+                raise VerifyError(r)
+            return cache
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a [B, N, kv_heads, head_dim] tensor")
     D = k.shape[3]
@@ -809,6 +815,11 @@ def spec_cache_read(cache, table, n, head_dim, k=None, v=None, *, start=None, le
     [B, n, kv_heads, head_dim], token i of slot start[b] + i (start None: slot i)
     for i < lens[b] (None: n).  k, v: tensors to write, rows behind lens[b]
     left as they are; None: new ones of `dtype`, zero there."""
+    if k is None and v is None and status is None and dtype in (torch.bfloat16, torch.float32):
+        r = _native.binding().cache_read(cache, table, n, head_dim, start, lens,
+                                         dtype is torch.float32)
+        if r is not None:
+            return _short(r, lambda *kv: kv)
     device, stride, pages, page_size, B, M, H = _cache_args(cache, table, head_dim)
     n, D = int(n), int(head_dim)
     if n < 0:
@@ -834,6 +845,12 @@ def spec_cache_keep(cache, table, start, path, head_dim, *, status=None) -> torc
     path[b, i] moves to slot start[b] + i, up to the first -1.  path [B, P]
     int32, out_path of a tree call; the request then has start + accept_len tokens.
     Returns cache."""
+    if status is None:
+        r = _native.binding().cache_keep(cache, table, start, path, head_dim)
+        if r is not None:
+            if r:
+                raise VerifyError(r)
+            return cache
     device, stride, pages, page_size, B, M, H = _cache_args(cache, table, head_dim)
     if not isinstance(path, torch.Tensor) or path.dim() != 2:
         raise ValueError("path must be a [B, P] tensor")
@@ -866,6 +883,11 @@ def spec_cache_attention(q, cache, table, lens, out: Optional[AttentionOutputs] 
     softcap: scores become softcap * tanh(score / softcap); window: slots further back
     are not seen; slopes [q_heads] fp32: scores lose slope * distance.  Rows behind
     q_lens[b] are left as they are in a given out, and zero in a new one."""
+    if out is None and q_lens is None:
+        r = _native.binding().cache_attention(q, cache, table, lens, parent, scale, softcap, window,
+                                              slopes, bool(lse), bool(status))
+        if r is not None:
+            return _short(r, AttentionOutputs)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, N, q_heads, head_dim] tensor")
     B, N, Hq, D = q.shape
