@@ -434,8 +434,9 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
         for (int k = 0; k < kTiles; ++k)
           scores<D, NT, NS>(stage + k * Tile<D>::kBytes, q, s[k]);
         // a chunk before the step's tokens that every row sees whole needs no masks
-        const bool edge = slot0 + kChunkSlots > r.base || p.window > 0 || p.slopes;
-        const bool plain = !edge && p.softcap == 0.f;
+        const bool edge = slot0 + kChunkSlots > r.base ||
+                          (p.window > 0 && slot0 <= r.base + r.nq - 1 - p.window);
+        const bool plain = !edge && p.softcap == 0.f && !p.slopes;
         if (!plain) {
 #pragma unroll
           for (int k = 0; k < kTiles; ++k)
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
                 s[k][n][e] = y;
               }
         }
-        if (edge) {
+        if (edge || p.slopes) {
 #pragma unroll
           for (int k = 0; k < kTiles; ++k)
 #pragma unroll
@@ -462,14 +463,16 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  bool seen = there;
-                  if (node >= 0 && there)
-                    seen = p.parent ? tree.sees(where[n].node[e], node)
-                                    : node <= where[n].node[e];
                   const int far = where[n].pos[e] - pos;
-                  if (p.window > 0 && far >= p.window) seen = false;
                   float& y = s[k][n][2 * x + e];
-                  y = seen ? fmaf(-where[n].slope[e], (float)far, y) : -INFINITY;
+                  if (p.slopes) y = fmaf(-where[n].slope[e], (float)far, y);
+                  if (edge) {
+                    bool seen = there;
+                    if (node >= 0 && there)
+                      seen = p.parent ? tree.sees(where[n].node[e], node) : node <= where[n].node[e];
+                    if (p.window > 0 && far >= p.window) seen = false;
+                    if (!seen) y = -INFINITY;
+                  }
                 }
             }
         }
@@ -669,20 +672,30 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
     float m = -INFINITY;
     for (int k = lane; k < pieces; k += 32) m = fmaxf(m, src_of(k)[D]);
     m = warp_max_nan(m);
+    // 32 pieces at a time: a lane works out one's factor, then every lane adds its dimensions of them
+    // all, whose loads wait for nothing
     float o[kVec] = {}, l = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < pieces; ++k) {
-      const float* src = src_of(k);
-      const float pm = src[D], pl = src[D + 1];
-      const float f = pm == -INFINITY ? (pl == 0.f ? 0.f : 1.f) : ex2(pm - m);
-      l = fmaf(pl, f, l);
+    for (int k0 = 0; k0 < pieces; k0 += 32) {
+      float f = 0.f;
+      if (k0 + lane < pieces) {
+        const float2 ml = *reinterpret_cast<const float2*>(src_of(k0 + lane) + D);
+        f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m);
+        l = fmaf(ml.y, f, l);
+      }
+      const int n = min(32, pieces - k0);
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const float g = __shfl_sync(kAll, f, k);
+        const float* src = src_of(k0 + k) + lane * kVec;
 #pragma unroll
-      for (int e = 0; e < kVec; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + lane * kVec + e);
-        o[e] = fmaf(v.x, f, o[e]);
-        o[e + 1] = fmaf(v.y, f, o[e + 1]);
+        for (int e = 0; e < kVec; e += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src + e);
+          o[e] = fmaf(v.x, g, o[e]);
+          o[e + 1] = fmaf(v.y, g, o[e + 1]);
+        }
       }
     }
+    l = warp_sum(l);
     const int global = tile * p.rows + row;
     const int i = global / p.group, j = global - i * p.group;
     const long long to = ((long long)b * p.N + i) * p.Hq + h * p.group + j;

@@ -125,7 +125,21 @@ __device__ __forceinline__ Share find_share(const AttendParams& p, const int (&c
     total += part;
   }
   Share s[K];
-  const long long want = (total + p.least - 1) / p.least;
+  // `least` chunks a CTA, but a CTA for every unit: a CTA walks its units one after the other
+  long long want = (total + p.least - 1) / p.least;
+  if (want < ctas) {
+    long long units = 0;
+    for (int b = 0; b < p.B; b += T) {
+      long long some = 0;
+      if (b + t < p.B) {
+        const Request r = request_of(p, b + t);
+        some = (long long)r.tiles * p.cache.Hkv;
+      }
+      block_scan<T>(some, smem, &part);
+      units += part;
+    }
+    if (units > want) want = units;
+  }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     s[k].total = total;
