@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
   long long* scan = reinterpret_cast<long long*>(raw_smem);
   char* ring = raw_smem + kFewScan;
   float* rows_out = reinterpret_cast<float*>(ring);
-  const TreeView tree(ring + few_ring<D, NT>(), p.N);  // (if p.parent)
+  const TreeView tree(ring + few_ring<D, NT>(), ring, p.N);  // (if p.parent)
   pdl_wait();
   pdl_launch_dependents();
   const int cta = blockIdx.x, lane = lane_id(), warp = threadIdx.x / 32;
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
       const int block = page_bytes(1, D) << p.cache.shift;
       const char* head = p.cache.data + (long long)(2 * h) * block;
       const bool one_page = kTiles == 1 || p.cache.shift >= 5;  // a chunk lies in one page
-      int next[kTiles];
+      int next[kTiles] = {};
       auto queue = [&](int c, char* stage) {
         if (c < c1) {
           const int token = ((from + c) * kChunkSlots) & mask;
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
     const int lane = lane_id();
     bool late = false;  // (a wait that ran out is every request's, so seldom is it)
     if (p.late)
-      for (int i = lane; i < (int)gridDim.x; i += 32) late = late || p.late[i];
+      for (int i = lane; i < (int)gridDim.x; i += 32) late |= p.late[i] != 0;
     const int ran_out = __any_sync(kAll, late) ? kTimeout : 0;
     for (int b = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; b < p.B;
          b += gridDim.x * (kJoinThreads / 32)) {
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
         const int* parent = p.parent + (long long)b * p.parent_stride;
         bool bad = false;
         for (int n = 1 + lane; n < r.nq; n += 32)
-          bad = bad || parent[n - 1] < 0 || parent[n - 1] >= n;
+          bad |= (parent[n - 1] < 0) | (parent[n - 1] >= n);
         if (__any_sync(kAll, bad)) st |= kBadTree;
       }
       if (lane == 0) p.out_status[b] = st | ran_out;

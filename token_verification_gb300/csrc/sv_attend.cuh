@@ -216,21 +216,23 @@ __device__ __forceinline__ int pieces_of(const Share& s, int cta, long long u1) 
   return n;
 }
 
-// A request's tree in shared memory: which nodes each node sees (bits), and its depth.
+// A request's tree in shared memory: which nodes each node sees (bits), and its depth.  The
+// parents and whether they are no tree lie elsewhere, where they are needed no longer than it
+// takes to build.
 struct TreeView {
-  int* mem;  // [N] depths, [N] parents, whether they are no tree, [N][words] bits
+  int *mem, *scratch;  // [N] depths, [N][words] bits; [N + 1]
   int N, words;
-  __device__ __forceinline__ TreeView(void* at, int n)
-      : mem(static_cast<int*>(at)), N(n), words((n + 31) / 32) {}
+  __device__ __forceinline__ TreeView(void* at, void* build, int n)
+      : mem(static_cast<int*>(at)), scratch(static_cast<int*>(build)), N(n), words((n + 31) / 32) {}
   __device__ __forceinline__ int& depth(int n) const { return mem[n]; }
-  __device__ __forceinline__ int& parent(int n) const { return mem[N + n]; }
-  __device__ __forceinline__ int& bad() const { return mem[2 * N]; }
-  __device__ __forceinline__ int& bits(int n, int w) const { return mem[2 * N + 1 + n * words + w]; }
+  __device__ __forceinline__ int& parent(int n) const { return scratch[n + 1]; }
+  __device__ __forceinline__ int& bad() const { return scratch[0]; }
+  __device__ __forceinline__ int& bits(int n, int w) const { return mem[N + n * words + w]; }
   __device__ __forceinline__ bool sees(int n, int other) const {
     return bits(n, other >> 5) >> (other & 31) & 1;
   }
 };
-inline size_t tree_bytes(int N) { return ((size_t)N * (2 + (N + 31) / 32) + 1) * sizeof(int); }
+inline size_t tree_bytes(int N) { return (size_t)N * (1 + (N + 31) / 32) * sizeof(int); }
 
 // Builds it with T threads (this one: t) that share a named barrier; false when the parents are no tree.
 template <int T>
@@ -247,7 +249,11 @@ __device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq,
     if (n && (up < 0 || up >= n)) tree.bad() = 1;
   }
   meet();
-  if (tree.bad()) return false;
+  const bool bad = tree.bad() != 0;
+  if (bad) {
+    meet();
+    return false;
+  }
   for (int n = t; n < nq; n += T) {
     for (int w = 0; w < tree.words; ++w) tree.bits(n, w) = 0;
     int d = -1;

@@ -1,7 +1,7 @@
 // sv_attend_many.cu - attention over the 4-bit cache for many query rows
 // (spec_cache_attention): tensor memory and tcgen05 instructions.
 //
-// A unit is a tile of 32, 48 or 64 query rows of a key/value head (tokens of the step times the
+// A unit is a tile of 32 or 48 query rows of a key/value head (tokens of the step times the
 // heads of the group), a chunk 128 slots, which takes
 //   S^T = K Q^T    128 slots x rows x D, both operands in shared memory
 //   O^T += V^T P^T  D x rows x 128 slots, values and weights P in shared memory
@@ -168,24 +168,34 @@ struct ManySmem {
   static constexpr int kTileBytes = D / 64 * (int)kBlockBytes;
   alignas(1024) char v[kTileBytes];  // (first: at D = 64 a descriptor reaches one tile on)
   alignas(1024) char k[kTileBytes];
-  alignas(1024) char p[kBlockBytes];  // weights [slot][64 rows]; a finished piece's rows
+  // weights [slot][64 rows]; at other times a finished piece's rows (or their sums), behind them
+  // what the warps leave to be joined, or a tree's parents
+  alignas(1024) char p[kBlockBytes];
+  static_assert(64 * NC * 4 + 16 * NC <= (int)kBlockBytes && NC * D * 2 <= 64 * NC * 4, "");
   alignas(1024) char q[D / 64 * NC * 128];
   uint4 raw[2][D / 64][kManyThreads];  // the codes of keys and values on their way
   // the piece's rows: {factor of scores, the same, shift - reference, the same} of pairs of rows,
   // the reference, the last change of it, 1 / sum, a slope, the position, the step's
-  // token, the row of `out` counted from the request's first; what the warps leave to be joined
+  // token, the row of `out` counted from the request's first
   alignas(16) float4 fo[NC / 2];
   alignas(16) float m[NC], change[NC], inv[NC], slope[NC];
   int pos[NC], node[NC], out_row[NC];
-  float part[4][NC];
   alignas(8) unsigned long long qk_done, pv_done, drained;  // completed by the tensor pipe
   ChunkRef refs[4];  // of chunk j in j mod 4
   uint32_t tmem;
   long long scan[kManyThreads / 32 + 2];
+  static __host__ __device__ constexpr int used() {
+    return (int)(offsetof(ManySmem, scan) + sizeof(scan));
+  }
 };
+// Where the members end (the struct's size is a whole number of 1024), and with what aligns them.
+template <int D, int NC>
+__host__ __device__ constexpr int many_used() {
+  return ManySmem<D, NC>::used();
+}
 template <int D, int NC>
 constexpr size_t many_smem() {
-  return 1024 + sizeof(ManySmem<D, NC>);
+  return 1024 + many_used<D, NC>();
 }
 
 __device__ __forceinline__ float warp_top(float x) {
@@ -246,7 +256,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   extern __shared__ __align__(16) char many_raw[];
   ManySmem<D, NC>& sm = *reinterpret_cast<ManySmem<D, NC>*>(
       many_raw + ((1024 - (smem_u32(many_raw) & 1023)) & 1023));
-  const TreeView tree(reinterpret_cast<char*>(&sm) + sizeof(sm), p.N);  // (if p.parent)
+  const TreeView tree(reinterpret_cast<char*>(&sm) + many_used<D, NC>(), sm.p, p.N);  // (if p.parent)
+  float(&joined)[4][NC] = *reinterpret_cast<float(*)[4][NC]>(sm.p + 64 * NC * sizeof(float));
   constexpr int G = D / 32;     // groups of a row
   constexpr int kU = Part<D>::kU;
   constexpr int NH = NC / 2;    // rows of a thread
@@ -544,13 +555,13 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           float y = s[i];
           if (plain) y *= reinterpret_cast<const float*>(&sm.fo[(row_at + i) / 2])[i & 1];
           y = warp_top(y);
-          if (lane == i) sm.part[quarter][row_at + i] = y;
+          if (lane == i) joined[quarter][row_at + i] = y;
         }
         __syncthreads();
         if (tid < NC) {
           const float old = sm.m[tid];
-          const float m = fmaxf(fmaxf(old, sm.part[0][tid]),
-                                max3(sm.part[1][tid], sm.part[2][tid], sm.part[3][tid]));
+          const float m = fmaxf(fmaxf(old, joined[0][tid]),
+                                max3(joined[1][tid], joined[2][tid], joined[3][tid]));
           sm.m[tid] = m;
           sm.change[tid] = old == -INFINITY ? 0.f : ex2(old - m);
           reinterpret_cast<float*>(&sm.fo[tid / 2])[2 + (tid & 1)] =
@@ -621,11 +632,11 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) sum += sums[(tid / NC * 16 + i) * NC + tid % NC];
-      sm.part[tid / NC][tid % NC] = sum;
+      joined[tid / NC][tid % NC] = sum;
     }
     __syncthreads();
     if (tid < NC) {
-      float sum = (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]);
+      float sum = (joined[0][tid] + joined[1][tid]) + (joined[2][tid] + joined[3][tid]);
       if (late) sum = qnan();
       sm.inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
       if (tid < n_rows) {
@@ -709,9 +720,10 @@ cudaError_t plan_many(int rows, AttendPlan* plan) {
   DeviceInfo info;
   const cudaError_t err = device_info(&info);
   if (err != cudaSuccess) return err;
-  // as few tiles as tiles of 64 would be, with few rows of them empty
+  // as few tiles as tiles of 48 would be (64 rows do not fit the registers: 505 -> 580 us for trees
+  // of 61 nodes), with few rows of them empty
   const int tiles = (rows + 47) / 48, each = (rows + tiles - 1) / tiles;
-  plan->rows = each <= 32 ? 32 : each <= 48 ? 48 : 64;
+  plan->rows = each <= 32 ? 32 : 48;
   plan->chunk = kSlotsTile;
   plan->least = 1;
   plan->shift = kManyShift;
@@ -722,8 +734,7 @@ cudaError_t plan_many(int rows, AttendPlan* plan) {
 cudaError_t launch_many(const AttendParams& p, int D, const AttendPlan& plan, cudaStream_t stream) {
 #define SV_MANY(d, n) \
   if (D == d && plan.rows == n) return launch_one<d, n>(p, plan, stream);
-  SV_MANY(64, 32) SV_MANY(64, 48) SV_MANY(64, 64)
-  SV_MANY(128, 32) SV_MANY(128, 48) SV_MANY(128, 64)
+  SV_MANY(64, 32) SV_MANY(64, 48) SV_MANY(128, 32) SV_MANY(128, 48)
 #undef SV_MANY
   return cudaErrorInvalidValue;
 }

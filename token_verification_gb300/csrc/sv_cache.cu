@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(kCacheThreads) keep_kernel(const KeepParams p)
   if (p.out_status && h == 0) {
     bool bad = false;
     for (int i = lane_id(); i < n; i += 32)
-      bad = bad || (unsigned)table[(start + i) >> c.shift] >= (unsigned)c.pages ||
-            (unsigned)table[(start + path[i]) >> c.shift] >= (unsigned)c.pages;
+      bad |= ((unsigned)table[(start + i) >> c.shift] >= (unsigned)c.pages) |
+             ((unsigned)table[(start + path[i]) >> c.shift] >= (unsigned)c.pages);
     bad = __any_sync(kAll, bad);
     if (lane_id() == 0)
       p.out_status[b] = n == -1 ? kBadTree : n == -2 ? kBadDraftLen : bad ? kBadPage : 0;

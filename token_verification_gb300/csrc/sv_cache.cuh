@@ -78,7 +78,7 @@ __device__ __forceinline__ int page_status(const CacheView& c, long long b, int 
   bool bad = false;
   if (count > 0)
     for (int i = (first >> c.shift) + lane_id(); i <= (first + count - 1) >> c.shift; i += 32)
-      bad = bad || (unsigned)c.table[b * c.M + i] >= (unsigned)c.pages;
+      bad |= (unsigned)c.table[b * c.M + i] >= (unsigned)c.pages;  // (loads that wait for none)
   return __any_sync(0xffffffffu, bad) ? kBadPage : 0;
 }
 
