@@ -569,8 +569,8 @@ sv_status spec_beam_reorder(const void* state, const int64_t* state_strides,
  *   out_status  [B] int32 or NULL: SV_REQ_BAD_DRAFT_LEN (slots or lengths out of
  *               range: nothing is done for the request), SV_REQ_BAD_PAGE (tokens
  *               on such pages are skipped; attention rows that would see them are NaN).
- * Calls need no workspace unless they name one, and none of the cache's contents
- * is ever read beyond the slots in use. */
+ * Calls need no workspace unless they name one, and no result depends on what the cache
+ * holds beyond the slots in use. */
 
 /* Bytes of a page of one head's keys (or values); 0 when not supported. */
 size_t spec_cache_page_bytes(int page_size, int head_dim);
@@ -629,14 +629,18 @@ sv_status spec_cache_keep(void* cache, int64_t page_stride, const int32_t* table
  *               SV_REQ_BAD_TREE, and the request's rows are 0.
  *   slopes      [q_heads] fp32 or NULL (no bias).
  *   scale       finite.  softcap finite, 0: none.  window 0: none.
- *   out         [B, N, q_heads, head_dim] dtype, contiguous, 16-byte aligned; rows
- *               behind q_lens[b] are left as they are.
+ *   out         [B, N, q_heads, head_dim] dtype, contiguous, 16-byte aligned, apart
+ *               from the inputs; rows behind q_lens[b] are left as they are.
  *   out_lse     [B, N, q_heads] fp32 or NULL: log sum_j exp(x_j).
  *   workspace   >= spec_cache_attention_workspace_size bytes (of the current
  *               device), 16-byte aligned.  It needs no preparation and holds nothing
  *               between calls; calls that may overlap need one each.
  * Sums are of 32-bit terms; weights are rounded to 11 bits before they meet the
- * values (22 bits in fp32).  Results do not vary between calls of the same lengths. */
+ * values (22 bits in fp32).  Results do not vary between calls of the same lengths.
+ * bf16 calls of more than 16 query rows a key/value head (N * q_heads / kv_heads) and a
+ * head_dim of 64 or 128 wait for the tensor cores, each time no longer than the limit of
+ * spec_verify_set_wait_limit_ns: a wait that ran out makes rows NaN and sets SV_REQ_TIMEOUT
+ * in every request's status. */
 size_t spec_cache_attention_workspace_size(sv_dtype dtype, int N, int q_heads, int kv_heads,
                                            int head_dim);
 sv_status spec_cache_attention(const void* q, const int64_t* q_strides, const void* cache,

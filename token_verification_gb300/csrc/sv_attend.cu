@@ -292,7 +292,7 @@ __host__ __device__ constexpr int few_tiles() {  // of 16 slots, a chunk
   return D == 256 ? 1 : 2;
 }
 constexpr int kFewScan = 64;
-static_assert(sizeof(long long) * (kFewWarps + 3) <= kFewScan, "");
+static_assert(sizeof(long long) * (kFewWarps + 2) <= kFewScan, "");
 template <int D, int NT>
 __host__ __device__ constexpr int few_ring() {
   const int ring = kFewWarps * kStages * few_tiles<D>() * Tile<D>::kBytes;
@@ -307,9 +307,6 @@ constexpr size_t few_smem() {
 // CTAs an SM holds: as many as their registers allow without spills to speak of.
 template <int D, int NT, typename T>
 constexpr int few_blocks() {
-#ifdef FEWB
-  if (NT == 1 && D <= 128) return FEWB;
-#endif
   return D == 256 || (D == 128 && NT == 2) ? 2 : D == 64 || sizeof(T) == 2 ? 4 - (NT - 1) : 3;
 }
 
@@ -328,8 +325,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
   pdl_launch_dependents();
   const int cta = blockIdx.x, lane = lane_id(), warp = threadIdx.x / 32;
   const int g = lane / 4, t = lane % 4;
-  const int ctas[1] = {cta};
-  const Share share = find_share<kFewThreads>(p, ctas, 0, gridDim.x, scan);
+  const Share share = find_share<kFewThreads>(p, cta, gridDim.x, scan);
   if (threadIdx.x == 0) p.desc[4 * cta + 3] = 0;
   if (cta >= share.G) return;
 
@@ -351,7 +347,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
     const int row0 = tile * 8 * NT;
 
     bool sees = r.ok && r.len > 0;
-    if (p.parent && sees) sees = build_tree<kFewThreads>(p, b, r.nq, tree, threadIdx.x, 1);
+    if (p.parent && sees) sees = build_tree<kFewThreads>(p, b, r.nq, tree);
 
     Query<D, NT, NS> q;
     float unscale[NT][2];
@@ -627,10 +623,13 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
 }
 
 // Joins the pieces of the unit that begins in CTA blockIdx.x's share and is
-// split, one warp a row, and reports the requests' statuses.
-constexpr int kJoinThreads = 256;
+// split, and reports the requests' statuses.  One warp a row; or, where units are few and
+// their pieces many (WIDE), a block of 8 warps a row, the pieces dealt to the warps: a call of a token
+// over 16000 slots for 8 heads (76 pieces each) takes 26 instead of 36 us.  Below 16 pieces a
+// unit one warp is as fast or faster (8.9 instead of 10.1 us at 128 slots).
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
-template <int D, typename T>
+template <int D, typename T, bool WIDE>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p) {
   pdl_wait();
   pdl_launch_dependents();
@@ -640,8 +639,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
     if (p.late)
       for (int i = lane; i < (int)gridDim.x; i += 32) late |= p.late[i] != 0;
     const int ran_out = __any_sync(kAll, late) ? kTimeout : 0;
-    for (int b = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; b < p.B;
-         b += gridDim.x * (kJoinThreads / 32)) {
+    for (int b = blockIdx.x * kJoinWarps + threadIdx.x / 32; b < p.B; b += gridDim.x * kJoinWarps) {
       const Request r = request_of(p, b);
       int st = r.ok ? page_status(p.cache, b, r.lo, r.len - r.lo) : kBadDraftLen;
       if (r.ok && p.parent) {
@@ -663,30 +661,39 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
   constexpr int kStep = D + 4, kVec = D / 32;  // values a lane: D / 32
   const int lane = lane_id();
   const int n_rows = min(p.rows, r.nq * p.group - tile * p.rows);
-  for (int row = blockIdx.y * (kJoinThreads / 32) + threadIdx.x / 32; row < n_rows;
-       row += gridDim.y * (kJoinThreads / 32)) {
+  const int warp = threadIdx.x / 32;
+  __shared__ float sums[WIDE ? kJoinWarps : 1][D + 1], maxes[kJoinWarps];
+  for (int row = WIDE ? blockIdx.y : blockIdx.y * kJoinWarps + warp; row < n_rows;
+       row += WIDE ? gridDim.y : gridDim.y * kJoinWarps) {
     auto src_of = [&](int k) {
       const int slot = k == 0 ? 2 * cta + second : 2 * (cta + k);
       return p.part + ((long long)slot * p.rows + row) * kStep;
     };
+    const int k_first = WIDE ? warp : 0, k_step = WIDE ? kJoinWarps : 1;
     float m = -INFINITY;
-    for (int k = lane; k < pieces; k += 32) m = fmaxf(m, src_of(k)[D]);
+    for (int k = k_first + lane * k_step; k < pieces; k += 32 * k_step) m = fmaxf(m, src_of(k)[D]);
     m = warp_max_nan(m);
+    if (WIDE) {
+      if (lane == 0) maxes[warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, maxes[i]);
+    }
     // 32 pieces at a time: a lane works out one's factor, then every lane adds its dimensions of them
     // all, whose loads wait for nothing
     float o[kVec] = {}, l = 0.f;
-    for (int k0 = 0; k0 < pieces; k0 += 32) {
+    for (int k0 = k_first; k0 < pieces; k0 += 32 * k_step) {
       float f = 0.f;
-      if (k0 + lane < pieces) {
-        const float2 ml = *reinterpret_cast<const float2*>(src_of(k0 + lane) + D);
+      if (k0 + lane * k_step < pieces) {
+        const float2 ml = *reinterpret_cast<const float2*>(src_of(k0 + lane * k_step) + D);
         f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m);
         l = fmaf(ml.y, f, l);
       }
-      const int n = min(32, pieces - k0);
+      const int n = min(32, (pieces - k0 + k_step - 1) / k_step);
 #pragma unroll 8
       for (int k = 0; k < n; ++k) {
         const float g = __shfl_sync(kAll, f, k);
-        const float* src = src_of(k0 + k) + lane * kVec;
+        const float* src = src_of(k0 + k * k_step) + lane * kVec;
 #pragma unroll
         for (int e = 0; e < kVec; e += 2) {
           const float2 v = *reinterpret_cast<const float2*>(src + e);
@@ -696,21 +703,41 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
       }
     }
     l = warp_sum(l);
-    const int global = tile * p.rows + row;
-    const int i = global / p.group, j = global - i * p.group;
-    const long long to = ((long long)b * p.N + i) * p.Hq + h * p.group + j;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (WIDE) {
 #pragma unroll
-    for (int e = 0; e < kVec; e += 2) {
-      if (sizeof(T) == 4)
-        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + to * D + lane * kVec + e) =
-            make_float2(o[e] * inv, o[e + 1] * inv);
-      else
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + to * D + lane * kVec + e) =
-            pack_bf16(o[e] * inv, o[e + 1] * inv);
+      for (int e = 0; e < kVec; ++e) sums[warp][lane * kVec + e] = o[e];
+      if (lane == 0) sums[warp][D] = l;
+      __syncthreads();
+      if (warp == 0) {
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) o[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) {
+          l += sums[i][D];
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) o[e] += sums[i][lane * kVec + e];
+        }
+      }
     }
-    if (p.out_lse && lane == 0)
-      p.out_lse[to] = l == 0.f ? -INFINITY : (m - p.shift + log2f(l)) * 0.6931471805599453f;
+    if (!WIDE || warp == 0) {
+      const int global = tile * p.rows + row;
+      const int i = global / p.group, j = global - i * p.group;
+      const long long to = ((long long)b * p.N + i) * p.Hq + h * p.group + j;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int e = 0; e < kVec; e += 2) {
+        if (sizeof(T) == 4)
+          *reinterpret_cast<float2*>(static_cast<float*>(p.out) + to * D + lane * kVec + e) =
+              make_float2(o[e] * inv, o[e + 1] * inv);
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + to * D + lane * kVec +
+                                       e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
+      }
+      if (p.out_lse && lane == 0)
+        p.out_lse[to] = l == 0.f ? -INFINITY : (m - p.shift + log2f(l)) * 0.6931471805599453f;
+    }
+    if (WIDE) __syncthreads();
   }
 }
 
@@ -783,8 +810,9 @@ cudaError_t launch_few(const AttendParams& p, int D, int dtype, const AttendPlan
 
 cudaError_t launch_join(const AttendParams& p, int D, int dtype, int ctas, int units,
                         cudaStream_t stream) {
-  // where units are few, each is in many pieces: a warp a row of every tile
-  const dim3 grid(ctas, units * 4 <= ctas || p.rows > 16 ? (p.rows + 7) / 8 : 1);
+  const bool wide = units * 16 <= ctas;  // units in 16 pieces or more, or whole
+  const dim3 grid(ctas, wide ? std::min(p.rows, p.N * p.group)
+                             : p.rows > 16 ? (p.rows + kJoinWarps - 1) / kJoinWarps : 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kJoinThreads);
@@ -794,10 +822,14 @@ cudaError_t launch_join(const AttendParams& p, int D, int dtype, int ctas, int u
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-#define SV_JOIN(d)                                                                   \
-  if (D == d)                                                                        \
-    return dtype == SV_F32 ? cudaLaunchKernelEx(&cfg, join_kernel<d, float>, p)      \
-                           : cudaLaunchKernelEx(&cfg, join_kernel<d, __nv_bfloat16>, p);
+#define SV_JOIN(d)                                                                          \
+  if (D == d) {                                                                             \
+    if (dtype == SV_F32)                                                                    \
+      return wide ? cudaLaunchKernelEx(&cfg, join_kernel<d, float, true>, p)                \
+                  : cudaLaunchKernelEx(&cfg, join_kernel<d, float, false>, p);              \
+    return wide ? cudaLaunchKernelEx(&cfg, join_kernel<d, __nv_bfloat16, true>, p)          \
+                : cudaLaunchKernelEx(&cfg, join_kernel<d, __nv_bfloat16, false>, p);        \
+  }
   SV_JOIN(64) SV_JOIN(128) SV_JOIN(256)
 #undef SV_JOIN
   return cudaErrorInvalidValue;
@@ -808,7 +840,11 @@ sv_status check_cache(CacheView* c, const void* cache, int64_t page_stride, cons
 
 namespace {
 
-// The kernel and split of a call of `rows` query rows a key/value head.  ROWS_RULE
+// The kernel and split of a call of `rows` query rows a key/value head.  Tensor memory's tiles of 32 or
+// 48 rows against tiles of 16 whose codes are decoded again for each: 269 against 286 us at 24
+// rows, 273 against 294 at 32, 304 against 419 at 40, 308 against 425 at 48 (64 requests of up to 8192
+// slots, 8 heads of 128), but 164 for the small tiles at 16 rows, which decode once.  Heads of
+// 256 and fp32 (two fp16 parts of everything) have the small tiles only.
 bool many_rows(sv_dtype dtype, int rows, int D) {
   return dtype == SV_BF16 && D <= 128 && rows > 16;
 }

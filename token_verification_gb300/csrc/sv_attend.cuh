@@ -111,11 +111,10 @@ __device__ __forceinline__ long long block_scan(long long x, long long* smem, lo
   return x + before;
 }
 
-// smem: T / 32 + 2 K long longs.  K shares are found at once, those of CTAs cta[0 .. K - 1]; a
-// thread gets that of cta[mine].
-template <int T, int K>
-__device__ __forceinline__ Share find_share(const AttendParams& p, const int (&cta)[K], int mine,
-                                            int ctas, long long* smem) {
+// smem: T / 32 + 2 long longs.
+template <int T>
+__device__ __forceinline__ Share find_share(const AttendParams& p, int cta, int ctas,
+                                            long long* smem) {
   const int t = threadIdx.x;
   const long long first = t < p.B ? work_of(p, t) : 0;
   long long total, part;
@@ -124,7 +123,6 @@ __device__ __forceinline__ Share find_share(const AttendParams& p, const int (&c
     block_scan<T>(b0 + t < p.B ? work_of(p, b0 + t) : 0, smem, &part);
     total += part;
   }
-  Share s[K];
   // `least` chunks a CTA, but a CTA for every unit: a CTA walks its units one after the other
   long long want = (total + p.least - 1) / p.least;
   if (want < ctas) {
@@ -140,16 +138,14 @@ __device__ __forceinline__ Share find_share(const AttendParams& p, const int (&c
     }
     if (units > want) want = units;
   }
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    s[k].total = total;
-    s[k].G = (int)(want < ctas ? want : ctas);
-    s[k].begin = s[k].end = s[k].at = 0;
-    s[k].b = 0;
-    if (cta[k] < s[k].G) {
-      s[k].begin = total * cta[k] / s[k].G;
-      s[k].end = total * (cta[k] + 1) / s[k].G;
-    }
+  Share s;
+  s.total = total;
+  s.G = (int)(want < ctas ? want : ctas);
+  s.begin = s.end = s.at = 0;
+  s.b = 0;
+  if (cta < s.G) {
+    s.begin = total * cta / s.G;
+    s.end = total * (cta + 1) / s.G;
   }
   long long* found = smem + T / 32;
   long long before = 0;
@@ -158,25 +154,19 @@ __device__ __forceinline__ Share find_share(const AttendParams& p, const int (&c
     part = first_total;
     const long long scan = b0 == 0 ? first_scan : block_scan<T>(work, smem, &part);
     const long long from = before + scan - work;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (from <= s[k].begin && s[k].begin < from + work) {
-        found[2 * k] = b0 + t;
-        found[2 * k + 1] = s[k].begin - from;
-      }
+    if (from <= s.begin && s.begin < from + work) {
+      found[0] = b0 + t;
+      found[1] = s.begin - from;
+    }
     before += part;
   }
   __syncthreads();
-  Share r = s[0];
-#pragma unroll
-  for (int k = 1; k < K; ++k)
-    if (mine == k) r = s[k];
-  if (r.begin < r.end) {
-    r.b = (int)found[2 * mine];
-    r.at = found[2 * mine + 1];
+  if (s.begin < s.end) {
+    s.b = (int)found[0];
+    s.at = found[1];
   }
   __syncthreads();
-  return r;
+  return s;
 }
 
 // A walk over the chunks of a share.
@@ -234,24 +224,24 @@ struct TreeView {
 };
 inline size_t tree_bytes(int N) { return (size_t)N * (1 + (N + 31) / 32) * sizeof(int); }
 
-// Builds it with T threads (this one: t) that share a named barrier; false when the parents are no tree.
+// Builds it with the block's T threads; false when the parents are no tree.
 template <int T>
 __device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq,
-                                           const TreeView& tree, int t, int barrier) {
-  auto meet = [=] { asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(T) : "memory"); };
-  meet();
+                                           const TreeView& tree) {
+  const int t = threadIdx.x;
+  __syncthreads();
   if (t == 0) tree.bad() = 0;
-  meet();
+  __syncthreads();
   const int* parent = p.parent + (long long)b * p.parent_stride;
   for (int n = t; n < nq; n += T) {
     const int up = n ? parent[n - 1] : -1;
     tree.parent(n) = up;
     if (n && (up < 0 || up >= n)) tree.bad() = 1;
   }
-  meet();
+  __syncthreads();
   const bool bad = tree.bad() != 0;
   if (bad) {
-    meet();
+    __syncthreads();
     return false;
   }
   for (int n = t; n < nq; n += T) {
@@ -260,7 +250,7 @@ __device__ __forceinline__ bool build_tree(const AttendParams& p, int b, int nq,
     for (int at = n; at >= 0; at = tree.parent(at), ++d) tree.bits(n, at >> 5) |= 1 << (at & 31);
     tree.depth(n) = d;
   }
-  meet();
+  __syncthreads();
   return true;
 }
 

@@ -15,13 +15,15 @@
 // keys, MN-major for the values), and between them the softmax, a thread a slot and half of the
 // rows: scores from tensor memory, weights to shared memory.  One thread then issues O of
 // this chunk and S of the next.  While one CTA waits for the tensor pipe the other decodes.
-// Warps of one task each (softmax, decoding, issuing) took 1.8 times as long: each of their
-// instructions waited to be fetched.
+// Bound by the threads' instructions (about 720 a warp and chunk: 300 for decoding, 150 for
+// loading, 60 for exponentials), not by HBM or the tensor pipe.  Measured: 490 us for trees of 61 nodes
+// over 32 requests of up to 4096 slots (4 heads a group, 8 groups of 128), 305 us for 6
+// tokens each of 64 requests of up to 8192 (8 heads a group).  One CTA an SM took 732 us for those trees, and warps of one task each (softmax,
+// decoding, issuing) 757: each of their instructions waited to be fetched.
 // A row's weights are relative to a reference that follows its running max only when a
 // score exceeds it by 2^8: the weights, at most 2^15 then, stay within fp16, and the
 // threads, which hold one slot of every row, need to agree on a row's max (and to rescale O in
 // tensor memory) a few times a piece instead of every chunk.
-//
 #include <string.h>
 
 #include <algorithm>
@@ -221,18 +223,16 @@ __device__ __forceinline__ uint32_t load_byte(unsigned long long src) {
   return x;
 }
 
-// NC / 2 columns of tensor memory from `addr` on.
+// N columns of tensor memory from `addr` on.
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, float (&x)[N]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(x);
   if constexpr (N == 16) {
     tmem_load16(addr, r);
-  } else if constexpr (N == 24) {
+  } else {
+    static_assert(N == 24, "");
     tmem_load16(addr, r);
     tmem_load8(addr + 16, r + 16);
-  } else {
-    tmem_load16(addr, r);
-    tmem_load16(addr + 16, r + 16);
   }
   tmem_loaded();
 }
@@ -241,12 +241,10 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const float (&x)[N]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
   if constexpr (N == 16) {
     tmem_store16(addr, r);
-  } else if constexpr (N == 24) {
+  } else {
+    static_assert(N == 24, "");
     tmem_store16(addr, r);
     tmem_store8(addr + 16, r + 16);
-  } else {
-    tmem_store16(addr, r);
-    tmem_store16(addr + 16, r + 16);
   }
   tmem_stored();
 }
@@ -266,13 +264,12 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   if (tid == 0) {
     mbar_init(smem_u32(&sm.qk_done), 1);
     mbar_init(smem_u32(&sm.pv_done), 1);
-    mbar_init(smem_u32(&sm.drained), 2);
+    mbar_init(smem_u32(&sm.drained), 1);
     fence_mbar_init();
   }
   pdl_wait();
   pdl_launch_dependents();
-  const int ctas[1] = {cta};
-  const Share share = find_share<kManyThreads>(p, ctas, 0, gridDim.x, sm.scan);
+  const Share share = find_share<kManyThreads>(p, cta, gridDim.x, sm.scan);
   if (tid == 0) {
     p.desc[4 * cta + 3] = 0;
     p.late[cta] = 0;
@@ -476,7 +473,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     const int c1 = (int)min((long long)r.chunks, c0 + left0);
     const int row0 = tile * NC, n_rows = min(NC, r.nq * p.group - row0);
     bool sees = r.ok && r.len > 0;
-    if (p.parent && sees) sees = build_tree<kManyThreads>(p, b, r.nq, tree, tid, 1);
+    if (p.parent && sees) sees = build_tree<kManyThreads>(p, b, r.nq, tree);
     bring_rows(w, sees);
     put_keys(j);
     fence_proxy_async();
@@ -599,7 +596,6 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
       fence_proxy_async();
       fence_before();
       late = __syncthreads_or(out_of_time);
-      // (from two warps, so that one's issuing does not wait for the other's)
       if (warp == 0 && !late && elect_one()) {
         fence_after();
         issue_out(c > c0);
@@ -686,11 +682,9 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   }
   if (late && tid == 0) p.late[cta] = 1;
   // nothing is in flight when tensor memory is freed
-  if (warp == 0 || warp == 4) {
+  if (warp == 0) {
     if (elect_one()) mma_commit(smem_u32(&sm.drained));
     __syncwarp();
-  }
-  if (warp == 0) {
     mbar_wait(smem_u32(&sm.drained), 0);
     __syncwarp();
     tmem_free(tmem);
