@@ -41,8 +41,8 @@ constexpr int kManyThreads = 256;
 constexpr int kSlotsTile = 128;
 constexpr float kManyShift = 7.f, kSlack = 8.f;
 constexpr float kNoRef = 3e38f;  // in place of shift - max for a row without a score yet
-constexpr int kTmemCols = 128;
-constexpr int kOCol = 64;  // O's columns; S: 0
+constexpr int kTmemCols = 256;
+constexpr int kSCol = 64, kOCol = 128;  // columns: S of chunk j at kSCol (j mod 2), O
 
 // ---- tcgen05 -------------------------------------------------------------
 
@@ -283,9 +283,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const unsigned long long limit = p.wait_ns;
   const uint32_t qk_bar = smem_u32(&sm.qk_done), pv_bar = smem_u32(&sm.pv_done);
 
-  // decoding: rows 8 (blk + 16 i) + r8 of the chunk's 128 slots, group g
-  const int r8 = tid & 7, g = (tid >> 3) % G, blk = (tid >> 3) / G;
-  constexpr int kBlk = 32 / G;  // 8-row blocks that the threads cover at once
+  // decoding: rows `slot` and (D = 128) 8 behind it, in one 16 slots' page, of the chunk's; group g
+  const int r8 = tid & 7, g = (tid >> 3) % G, my_slot = (tid >> 3) / G * (8 * kU) + r8;
   const int block = page_bytes(1, D) << p.cache.shift;
   Part<D> keys, vals;
   // Warp 7 finds the addresses (lane k < 8 of the k-th 16 slots' codes, lane k + 8 of their scales),
@@ -323,26 +322,26 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     ahead.step(p);
     fetch_id();
   };
-  const int code_at = (blk & 1) * 4 * D + r8 * (D / 2) + g * 16;  // from the 16 slots' first codes
-  const int scale_off = (blk & 1) * 8 + r8 + g * 16;              // and from their scales
-  static_assert(kBlk % 2 == 0, "");
+  const int code_at = (my_slot & 15) * (D / 2) + g * 16;  // from the 16 slots' first codes
+  const int scale_off = (my_slot & 15) + g * 16;          // and from their scales
   const uint32_t raw_at = smem_u32(&sm.raw[0][0][tid]);
   auto load = [&](const ChunkRef& ref, Part<D>& x, bool values) {
     x.off = 0;
     if (ref.valid) {  // (the cache has a page at all)
+      const int more = values ? block : 0;
+      const unsigned long long codes = ref.codes[my_slot >> 4] + (code_at + more);
+      const unsigned long long scales = ref.scales[my_slot >> 4] + (scale_off + more);
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        const int k = (blk + kBlk * i) >> 1, more = values ? block : 0;
-        copy16(raw_at + (values ? kU * kManyThreads * 16 : 0) + i * kManyThreads * 16,
-               ref.codes[k] + (code_at + more));
-        x.scale[i] = load_byte(ref.scales[k] + (scale_off + more));
+        copy16(raw_at + ((values ? kU : 0) + i) * kManyThreads * 16, codes + i * 4 * D);
+        x.scale[i] = load_byte(scales + i * 8);
       }
     }
     if (!ref.whole) {
+      const bool there = ref.valid >> (my_slot >> 4) & 1;
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        const int b8 = blk + kBlk * i, slot = 8 * b8 + r8;
-        const bool there = ref.valid >> (b8 >> 1) & 1;
+        const int slot = my_slot + 8 * i;
         if (!there || (values && (slot < ref.first || slot >= ref.last))) x.off |= 1u << i;
       }
     }
@@ -352,23 +351,23 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   uint32_t row_to[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    row_to[q] = smem_u32(sm.v) + (g >> 1) * kBlockBytes + (8 * blk + r8) * 128 +
+    row_to[q] = smem_u32(sm.v) + (g >> 1) * kBlockBytes + my_slot * 128 +
                 ((((g & 1) * 4 + q) ^ r8) << 4);
-  // `tile`: bytes from the values' tile on; `nothing`: the scale of a row that has none
-  // (keys and values come in turn: the copies behind the wanted ones are the other's)
+  // `tile`: bytes from the values' tile on; `nothing`: the scale of a row that has none (the codes are in)
   auto put = [&](const Part<D>& x, int tile, uint32_t nothing) {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    uint4 w4[kU];  // (all loads before the stores, behind which the compiler leaves them)
+#pragma unroll
+    for (int i = 0; i < kU; ++i) w4[i] = sm.raw[tile == 0][i][tid];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       Scale2 sc;
       sc.set((x.off >> i & 1 ? nothing : x.scale[i] * 128u + 0x400u) * 0x10001u);
-      const uint4 w4 = sm.raw[tile == 0][i][tid];
-      const uint32_t words[4] = {w4.x, w4.y, w4.z, w4.w};
+      const uint32_t words[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t d[4];
         decode_word(words[q], sc, d);
-        store16(row_to[q] + tile + 8 * kBlk * i * 128, d);
+        store16(row_to[q] + tile + 8 * i * 128, d);
       }
     }
   };
@@ -419,10 +418,10 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const uint64_t q_desc = smem_desc(smem_u32(sm.q), 16), k_desc = smem_desc(smem_u32(sm.k), 16);
   const uint64_t v_desc = smem_desc(smem_u32(sm.v), kBlockBytes);
   const uint64_t p_desc = smem_desc(smem_u32(sm.p), kBlockBytes);
-  auto issue_scores = [&] {
+  auto issue_scores = [&](unsigned j) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
-      mma_ss(tmem, k_desc + (((i / 4) * kBlockBytes + (i % 4) * 32) >> 4),
+      mma_ss(tmem + (j & 1) * kSCol, k_desc + (((i / 4) * kBlockBytes + (i % 4) * 32) >> 4),
              q_desc + (((i / 4) * (NC * 128) + (i % 4) * 32) >> 4), idesc(NC, false), i > 0);
     mma_commit(qk_bar);
   };
@@ -450,7 +449,13 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   load(sm.refs[0], vals, true);
   // (a chunk's worth of work lies between a load and the use of it)
   const unsigned n = (unsigned)w.left;
-  auto put_keys = [&](unsigned i) {  // of chunk i, then the next one's are on their way
+  // (copies of keys and of values are queued in turn, so one group behind the wanted one may be in
+  // flight: the other's; but for a piece's second keys)
+  auto put_keys = [&](unsigned i, bool second) {  // of chunk i, then the next one's are on their way
+    if (second)
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
     put(keys, kKeyTile, 0x7fffu);
     if (i + 1 < n)
       load(sm.refs[(i + 1) & 3], keys, false);
@@ -458,6 +463,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
       asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto put_values = [&](unsigned i) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     put(vals, 0, 0u);
     if (i + 1 < n)
       load(sm.refs[(i + 1) & 3], vals, true);
@@ -475,13 +481,13 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     bool sees = r.ok && r.len > 0;
     if (p.parent && sees) sees = build_tree<kManyThreads>(p, b, r.nq, tree);
     bring_rows(w, sees);
-    put_keys(j);
+    put_keys(j, false);
     fence_proxy_async();
     fence_before();
     __syncthreads();
     if (warp == 0 && !late && elect_one()) {
       fence_after();
-      issue_scores();
+      issue_scores(j);
     }
     __syncwarp();
     f32x2 l[NH / 2];
@@ -490,10 +496,10 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     int c = c0;
     for (; c < c1 && !late; ++c, ++j) {
       w.step(p);  // (stands at the next chunk from here on)
-      // the values, in the place of the last chunk's
-      bool out_of_time = j > 0 && !sleep_wait(pv_bar, (j - 1) & 1, limit);
-      put_values(j);
-      out_of_time = out_of_time || !sleep_wait(qk_bar, j & 1, limit);
+      bool out_of_time = !sleep_wait(qk_bar, j & 1, limit);
+      // the next chunk's keys, whose product runs while this chunk's weights are worked out
+      if (c + 1 < c1) put_keys(j + 1, c == c0);
+      fence_proxy_async();
       fence_after();
       const int slot0 = (r.lo / kSlotsTile + c) * kSlotsTile, slot = slot0 + slot_at;
       const bool edge = !sees || slot0 + kSlotsTile > r.base ||
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
       float s[NH];
       // scores in units of log2, before the rows' factors where plain
       auto load_scores = [&] {
-        tmem_load(mine, s);
+        tmem_load(mine + (j & 1) * kSCol, s);
         if (plain) return;
         const bool there = sees && slot < r.len;
         const int node = slot - r.base;
@@ -523,7 +529,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           s[i] = seen ? y : -INFINITY;
         }
       };
-      for (;;) {
+      for (bool moved = false;;) {
         load_scores();
         // exponents of the weights; is one too large for its row's reference?
         float top[2] = {-INFINITY, -INFINITY};
@@ -542,10 +548,20 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
             s[2 * i + 1] += fo.w;
           }
         }
+        if (moved) break;
 #pragma unroll
         for (int i = 0; i < NH / 2; ++i) top[i & 1] = max3(top[i & 1], s[2 * i], s[2 * i + 1]);
-        if (!__syncthreads_or(fmaxf(top[0], top[1]) > kManyShift + kSlack)) break;
-        // each row's max over the chunk's slots
+        fence_before();
+        moved = __syncthreads_or(fmaxf(top[0], top[1]) > kManyShift + kSlack);
+        if (warp == 0 && !late && c + 1 < c1 && elect_one()) {
+          fence_after();
+          issue_scores(j + 1);
+        }
+        __syncwarp();
+        if (!moved) break;
+        // each row's max over the chunk's slots (`joined` lies in the last chunk's weights)
+        if (c > c0) out_of_time |= !sleep_wait(pv_bar, (j - 1) & 1, limit);
+        fence_after();
         load_scores();
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
@@ -565,7 +581,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
               m == -INFINITY ? kNoRef : kManyShift - m;
         }
         __syncthreads();
-        if (c > c0) {  // the sums and O so far (the last chunk's O is in: its place took this one's values)
+        if (c > c0) {  // the sums and O so far
           float o[NH];
           tmem_load(mine + kOCol, o);
 #pragma unroll
@@ -578,28 +594,28 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           tmem_store(mine + kOCol, o);
         }
       }
-      find();  // (in the place of this chunk's)
+      find();  // (in the place of the chunk before this one)
+      uint32_t x[NH / 2];
+#pragma unroll
+      for (int i = 0; i < NH / 2; ++i) {
+        const float w0 = ex2(s[2 * i]), w1 = ex2(s[2 * i + 1]);
+        l[i] = add2(l[i], pack2(w0, w1));
+        x[i] = pack_f16(w0, w1);
+      }
+      // weights and values in the place of the last chunk's, whose product had the time since
+      if (c > c0) out_of_time |= !sleep_wait(pv_bar, (j - 1) & 1, limit);
       const uint32_t to = smem_u32(sm.p) + slot_at * 128;
 #pragma unroll
-      for (int i = 0; i < NH / 8; ++i) {
-        uint32_t x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w0 = ex2(s[8 * i + 2 * e]), w1 = ex2(s[8 * i + 2 * e + 1]);
-          l[4 * i + e] = add2(l[4 * i + e], pack2(w0, w1));
-          x[e] = pack_f16(w0, w1);
-        }
-        store16(to + (((row_at / 8 + i) ^ (slot_at & 7)) << 4), x);
-      }
-      // the next chunk's keys (its scores' operand is free: this chunk's are out)
-      if (c + 1 < c1) put_keys(j + 1);
+      for (int i = 0; i < NH / 8; ++i)
+        store16(to + (((row_at / 8 + i) ^ (slot_at & 7)) << 4),
+                {x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
+      put_values(j);
       fence_proxy_async();
       fence_before();
       late = __syncthreads_or(out_of_time);
       if (warp == 0 && !late && elect_one()) {
         fence_after();
         issue_out(c > c0);
-        if (c + 1 < c1) issue_scores();
       }
       __syncwarp();
     }
