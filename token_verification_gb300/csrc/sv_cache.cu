@@ -104,13 +104,21 @@ __device__ __forceinline__ Place<D> place_of(const CacheParams& p) {
   return x;
 }
 
-// 8 values as fp32 bit patterns' source: bf16 pairs, or fp32.
+// 8 values as fp32 bit patterns' source: bf16 pairs, or fp32.  cut(): magnitudes above 6272 = 7 * 896
+// become that.
+constexpr uint32_t kMost = 0x45c40000u;  // 6272
 struct Eight16 {
   uint4 w;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     w = __ldcs(reinterpret_cast<const uint4*>(p));
   }
   __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void cut() {
+    auto two = [](uint32_t u) {
+      return __vminu2(u & 0x7fff7fffu, kMost | kMost >> 16) | (u & 0x80008000u);
+    };
+    w = make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
+  }
   // the largest magnitude's bits (an fp32 number; NaN above infinity)
   __device__ __forceinline__ uint32_t top() const {
     const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
@@ -129,6 +137,11 @@ struct Eight32 {
     b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void cut() {
+    float* x[8] = {&a.x, &a.y, &a.z, &a.w, &b.x, &b.y, &b.z, &b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *x[i] = fminf(fmaxf(*x[i], -6272.f), 6272.f);
+  }
   __device__ __forceinline__ uint32_t top() const {
     uint32_t m = 0;
 #pragma unroll
@@ -147,22 +160,22 @@ struct Eight<__nv_bfloat16> : Eight16 {};
 template <>
 struct Eight<float> : Eight32 {};
 
-// Codes of 8 values at scale s (r = 1 / s to nearest; limit: above which magnitudes are cut).  The
+// Codes of 8 values of at most 7 s at scale s (r = 1 / s to nearest).  The
 // quotient's first value x r, corrected by its exact remainder, is x / s to nearest (Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), so it
 // is a half only where x / s is: a half h has 4 bits and s has 4, so an fp32 x beside h s
 // gives a quotient beside h.  Adding 1.5 * 2^23 + 8 leaves the whole number (ties to even) plus 8 in
 // the low bits, and the codes meet in one word by multiplications.
 template <typename T>
-__device__ __forceinline__ uint32_t encode8(const Eight<T>& x, float s, float r, float limit) {
-  uint32_t w = 0;
+__device__ __forceinline__ uint32_t encode8(const Eight<T>& x, float s, float r) {
+  uint32_t w = -0x4b400000u * 0x11111111u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = fminf(fmaxf(x.get(i), -limit), limit);
+    const float v = x.get(i);
     const float t = v * r;
     const float q = fmaf(fmaf(-t, s, v), r, t);
     const int at = 4 * (i / 2 + 4 * (i % 2));
-    w += (__float_as_uint(q + 12582920.f) - 0x4b400000u) << at;
+    w += __float_as_uint(q + 12582920.f) * (1u << at);
   }
   return w;
 }
@@ -174,6 +187,7 @@ __global__ void __launch_bounds__(kCacheThreads) write_kernel(const CacheParams 
   write_status(p);
   constexpr int kLanes = D / 8;  // threads of a token
   const Place<D> x = place_of<D>(p);
+  if (!__any_sync(kAll, x.k != nullptr)) return;  // (of ragged prompts every other warp)
   Eight<T> k[kSlots], v[kSlots];
 #pragma unroll
   for (int j = 0; j < kSlots; ++j) {
@@ -206,8 +220,12 @@ __global__ void __launch_bounds__(kCacheThreads) write_kernel(const CacheParams 
     const uint32_t bk = scale_byte(__uint_as_float(tk)), bv = scale_byte(__uint_as_float(tv));
     const float sk = scale_of(bk), sv = scale_of(bv);
     const int i = x.token + j;
-    const uint32_t wk = encode8<T>(k[j], sk, __frcp_rn(sk), 7.f * sk);
-    const uint32_t wv = encode8<T>(v[j], sv, __frcp_rn(sv), 7.f * sv);
+    const float rk = __frcp_rn(sk), rv = __frcp_rn(sv);
+    if (__any_sync(kAll, max(tk, tv) > kMost)) {  // (seldom)
+      k[j].cut();
+      v[j].cut();
+    }
+    const uint32_t wk = encode8<T>(k[j], sk, rk), wv = encode8<T>(v[j], sv, rv);
     if (x.k && i >= 0 && i < x.n) {
       reinterpret_cast<uint32_t*>(x.k + (x.slot + j) * (D / 2))[x.lane] = wk;
       reinterpret_cast<uint32_t*>(x.v + (x.slot + j) * (D / 2))[x.lane] = wv;
