@@ -180,6 +180,15 @@ __device__ __forceinline__ uint32_t encode8(const Eight<T>& x, float s, float r)
   return w;
 }
 
+// 1 / s to nearest: an approximate one, off by a last place or two, and a Newton step, off by the
+// square of that before it is rounded, 2^-44.  No 1 / s of a 4-bit s lies that near to the middle between
+// two numbers.
+__device__ __forceinline__ float inverse(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return fmaf(fmaf(-s, r, 1.f), r, r);
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kCacheThreads) write_kernel(const CacheParams p) {
   pdl_wait();
@@ -200,37 +209,53 @@ __global__ void __launch_bounds__(kCacheThreads) write_kernel(const CacheParams 
       v[j].clear();
     }
   }
-  const unsigned mine = kLanes == 32 ? kAll
-                                     : ((1u << (kLanes % 32)) - 1) << (lane_id() / kLanes * kLanes);
-  uint32_t kbytes = 0, vbytes = 0;
+  uint32_t tk[kSlots], tv[kSlots], top = 0;  // the slots' largest magnitudes, and that of all
 #pragma unroll
   for (int j = 0; j < kSlots; ++j) {
-    uint32_t tk = k[j].top(), tv = v[j].top();
-    // a token of which anything is not finite: values of 0 under the scale that says so
-    const bool bad = (__ballot_sync(kAll, max(tk, tv) >= 0x7f800000u) & mine) != 0;
-    tk = max(tk, __shfl_xor_sync(kAll, tk, 1));
-    tv = max(tv, __shfl_xor_sync(kAll, tv, 1));
-    tk = max(tk, __shfl_xor_sync(kAll, tk, 2));
-    tv = max(tv, __shfl_xor_sync(kAll, tv, 2));
-    if (bad) {
-      tk = tv = 0;
-      k[j].clear();
-      v[j].clear();
-    }
-    const uint32_t bk = scale_byte(__uint_as_float(tk)), bv = scale_byte(__uint_as_float(tv));
-    const float sk = scale_of(bk), sv = scale_of(bv);
-    const int i = x.token + j;
-    const float rk = __frcp_rn(sk), rv = __frcp_rn(sv);
-    if (__any_sync(kAll, max(tk, tv) > kMost)) {  // (seldom)
+    tk[j] = k[j].top();
+    tv[j] = v[j].top();
+    top = max(top, max(tk[j], tv[j]));
+  }
+  // a token of which anything is not finite: values of 0 under the scale that says so
+  unsigned bad = 0;
+  if (__any_sync(kAll, top > kMost)) {  // (seldom)
+    const unsigned mine = kLanes == 32 ? kAll
+                                       : ((1u << (kLanes % 32)) - 1) << (lane_id() / kLanes * kLanes);
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      if (__ballot_sync(kAll, max(tk[j], tv[j]) >= 0x7f800000u) & mine) {
+        bad |= 1u << j;
+        tk[j] = tv[j] = 0;
+        k[j].clear();
+        v[j].clear();
+      }
       k[j].cut();
       v[j].cut();
     }
-    const uint32_t wk = encode8<T>(k[j], sk, rk), wv = encode8<T>(v[j], sv, rv);
+  }
+  // the four lanes of a group work out one slot's scales each
+  const int t4 = lane_id() & 3;
+  auto spread = [&](const uint32_t (&x)[kSlots]) {  // the group's max of slot t4
+    uint32_t a[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      a[i] = max(t4 & 2 ? x[2 + i] : x[i], __shfl_xor_sync(kAll, t4 & 2 ? x[i] : x[2 + i], 2));
+    return max(t4 & 1 ? a[1] : a[0], __shfl_xor_sync(kAll, t4 & 1 ? a[0] : a[1], 1));
+  };
+  const uint32_t both = (uint32_t)scale_byte(__uint_as_float(spread(tk))) |
+                        (uint32_t)scale_byte(__uint_as_float(spread(tv))) << 8;
+  uint32_t kbytes = 0, vbytes = 0;
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) {
+    const uint32_t mine = __shfl_sync(kAll, both, j, 4), bk = mine & 255, bv = mine >> 8;
+    const float sk = scale_of(bk), sv = scale_of(bv);
+    const int i = x.token + j;
+    const uint32_t wk = encode8<T>(k[j], sk, inverse(sk)), wv = encode8<T>(v[j], sv, inverse(sv));
     if (x.k && i >= 0 && i < x.n) {
       reinterpret_cast<uint32_t*>(x.k + (x.slot + j) * (D / 2))[x.lane] = wk;
       reinterpret_cast<uint32_t*>(x.v + (x.slot + j) * (D / 2))[x.lane] = wv;
     }
-    kbytes |= (bad ? (uint32_t)kNanScale : bk) << (8 * j);
+    kbytes |= (bad >> j & 1 ? (uint32_t)kNanScale : bk) << (8 * j);
     vbytes |= bv << (8 * j);
   }
   if (x.k && x.lane % 4 == 0) {
