@@ -84,10 +84,11 @@ struct Tile {
   static constexpr int kScaleBytes = D / 2;                          // of the keys (16 D / 32)
   static constexpr int kBytes = kScales + 2 * kScaleBytes;
   static constexpr int KW = D / 32, VW = D / 64;  // words a lane takes of a slot
-  static __device__ __forceinline__ int key(int n) { return n * kRow + (n >> 2) * kKeyGap; }
-  static __device__ __forceinline__ int value(int n) {
-    return kValues + n * kRow + (n >> 2) * kValueGap;
+  static __device__ __forceinline__ constexpr int key(int n) { return n * kRow + (n >> 2) * kKeyGap; }
+  static __device__ __forceinline__ constexpr int value_step(int n) {
+    return n * kRow + (n >> 2) * kValueGap;
   }
+  static __device__ __forceinline__ int value(int n) { return kValues + value_step(n); }
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const char* src) {
@@ -113,13 +114,17 @@ __device__ __forceinline__ void queue_tiles(const CacheView& c, const char* head
   const char* base = head + (unsigned long long)(unsigned)id * c.page_stride;
   const char* k = base + (token * (D / 2) + lane * 16);
   const char* v = k + block;
+  // (a lane's rows are a multiple of 4 apart: constants from its first)
+  constexpr int kApart = 32 / kPer, kRows = D / 64;
+  static_assert(kApart % 4 == 0, "");
   const int row = lane / kPer, x = lane % kPer * 16;
-  const uint32_t to = smem_u32(stage);
+  const uint32_t key = smem_u32(stage) + Tile<D>::key(row) + x;
+  const uint32_t value = smem_u32(stage) + Tile<D>::value(row) + x;
 #pragma unroll
-  for (int i = 0; i < KT * D / 64; ++i) {
-    const int tile = i / (D / 64), n = row + i % (D / 64) * (32 / kPer);
-    copy16(to + tile * Tile<D>::kBytes + Tile<D>::key(n) + x, k + i * 512);
-    copy16(to + tile * Tile<D>::kBytes + Tile<D>::value(n) + x, v + i * 512);
+  for (int i = 0; i < KT * kRows; ++i) {
+    const int at = i / kRows * Tile<D>::kBytes, n = i % kRows * kApart;
+    copy16(key + (at + Tile<D>::key(n)), k + i * 512);
+    copy16(value + (at + Tile<D>::value_step(n)), v + i * 512);
   }
   if (lane < 2 * kUnits)
     copy16(smem_u32(scales), base + (((D / 2) << c.shift) + token * (D / kGroup) + unit * 16 +
