@@ -67,7 +67,7 @@ typedef enum sv_status {
   SV_ERR_CUDA = 7,        /* a CUDA runtime call or kernel launch failed */
   SV_ERR_FILTER = 8,      /* top_k negative, top_p outside (0, 1], or eps / delta negative */
   SV_ERR_ALIAS = 9,       /* an output overlaps an input that it must not overlap */
-  SV_ERR_SCORE = 10       /* attention scale or softcap not finite, softcap or window negative */
+  SV_ERR_SCORE = 10       /* attention scale not finite, softcap outside [0, 1e30], window negative */
 } sv_status;
 
 typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
@@ -628,9 +628,10 @@ sv_status spec_cache_keep(void* cache, int64_t page_stride, const int32_t* table
  *               N - 1 candidate nodes, n - 1 of them in use; NULL: a chain.  No tree:
  *               SV_REQ_BAD_TREE, and the request's rows are 0.
  *   slopes      [q_heads] fp32 or NULL (no bias).
- *   scale       finite.  softcap finite, 0: none.  window 0: none.
- *   out         [B, N, q_heads, head_dim] dtype, contiguous, 16-byte aligned, apart
- *               from the inputs; rows behind q_lens[b] are left as they are.
+ *   scale       finite.  softcap up to 1e30, 0: none.  window 0: none.
+ *   out         [B, N, q_heads, head_dim] dtype, contiguous, 16-byte aligned; rows
+ *               behind q_lens[b] are left as they are.  It must not reach into the bytes
+ *               from q's first to its last (SV_ERR_ALIAS), nor into other inputs.
  *   out_lse     [B, N, q_heads] fp32 or NULL: log sum_j exp(x_j).
  *   workspace   >= spec_cache_attention_workspace_size bytes (of the current
  *               device), 16-byte aligned.  It needs no preparation and holds nothing

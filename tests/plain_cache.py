@@ -117,7 +117,8 @@ def attention(q, kv, base, sees, depth, scale, softcap, window, slopes, dtype, s
         E = 2 * (D + 8) * U * A + 4 * U * x.abs()
         if softcap:
             x = softcap * torch.tanh(x / softcap)
-            E = E + 4 * U * x.abs() + softcap * 2.0 ** (-22 if exact else -21)
+            # (tanh to a few last places, or by one exponential where that is 2^-12 at most)
+            E = E + 8 * U * x.abs() + (0 if exact or softcap > 360 else softcap * 2.0 ** -21)
         if slopes is not None:
             b = float(slopes[h]) * far
             x = x - b

@@ -58,7 +58,7 @@ def keep(lib, **kw):
 
 
 def attend(lib, **kw):
-    a = dict(q=FAKE, qs=(128 * ROW, 32 * ROW, ROW), cache=FAKE, stride=1 << 20, table=FAKE,
+    a = dict(q=4 * FAKE, qs=(128 * ROW, 32 * ROW, ROW), cache=FAKE, stride=1 << 20, table=FAKE,
              lens=FAKE, q_lens=None, parent=None, ps=0, slopes=None, scale=0.1, cap=0.0, window=0,
              out=FAKE, lse=None, st=None, dtype=1, pages=9, page=64, B=2, N=4, M=3, Hq=32, H=8,
              D=128)
@@ -121,11 +121,13 @@ def test_keep_codes(lib, kw, code):
     (dict(dtype=2), DTYPE), (dict(N=-1), SHAPE), (dict(N=258), SHAPE), (dict(Hq=0), SHAPE),
     (dict(Hq=30), SHAPE), (dict(Hq=1032), SHAPE), (dict(H=0), SHAPE), (dict(H=64), SHAPE),
     (dict(scale=math.nan), SCORE), (dict(scale=math.inf), SCORE), (dict(cap=-1.0), SCORE),
-    (dict(cap=math.nan), SCORE), (dict(cap=math.inf), SCORE), (dict(window=-1), SCORE),
+    (dict(cap=math.nan), SCORE), (dict(cap=math.inf), SCORE), (dict(cap=2e30), SCORE), (dict(window=-1), SCORE),
     (dict(parent=FAKE, ps=4), TREE), (dict(parent=FAKE, ps=-1), TREE), (dict(q=None), NULL),
     (dict(lens=None), NULL), (dict(out=None), NULL), (dict(qs=(None,)), NULL),
-    (dict(q=FAKE + 8), NULL), (dict(out=FAKE + 8), NULL), (dict(qs=(128 * ROW, 32 * ROW, 8)), NULL),
+    (dict(q=4 * FAKE + 8), NULL), (dict(out=FAKE + 8), NULL), (dict(qs=(128 * ROW, 32 * ROW, 8)), NULL),
     (dict(qs=(-16, 32 * ROW, ROW)), SHAPE), (dict(qs=(1 << 61, 32 * ROW, ROW)), SHAPE),
+    (dict(q=FAKE, out=FAKE + 16), ALIAS), (dict(q=FAKE + 2 * 4 * 32 * ROW - 16, out=FAKE), ALIAS),
+    (dict(q=FAKE, out=FAKE + 7 * 32 * ROW + 31 * ROW), ALIAS), (dict(q=FAKE, out=FAKE), ALIAS),
     (dict(N=0, q=None), 0)])
 def test_attention_codes(lib, kw, code):
     assert attend(lib, **kw) == code

@@ -183,6 +183,17 @@ def test_no_slots_at_all():
     assert not bool(out.out.any()) and bool((out.lse[1] == -math.inf).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("softcap,scale", [(1e-39, 0.1), (1e-39, 0.0), (1e-30, 5.0), (350.0, 0.1),
+                                           (511.0, 0.1), (1e6, 0.1), (1e30, 0.1)])
+def test_caps_of_any_size(softcap, scale, dtype):
+    g = gen(int(softcap) % 1000 + 1)
+    for N, group in ((2, 2), (7, 4)):
+        cache, table = filled(2, 300, 2, 64, 16, g)
+        q = query(2, N, 2 * group, 64, dtype, g)
+        run(q, cache, 16, table, ints([300, 40]), softcap=softcap, scale=scale)
+
+
 @pytest.mark.parametrize("group", [1, 8])
 def test_one_query_for_all(group):
     """A query that is broadcast over requests and tokens."""

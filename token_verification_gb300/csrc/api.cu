@@ -480,7 +480,7 @@ const char* spec_verify_status_string(sv_status s) {
     case SV_ERR_CUDA: return "CUDA launch failed";
     case SV_ERR_FILTER: return "top_k negative or top_p outside (0, 1]";
     case SV_ERR_ALIAS: return "an output overlaps an input or itself";
-    case SV_ERR_SCORE: return "attention scale or softcap not finite, softcap or window negative";
+    case SV_ERR_SCORE: return "attention scale not finite, softcap outside [0, 1e30] or window negative";
   }
   return "unknown status";
 }

@@ -3,8 +3,8 @@
 // units, and the entry point.
 //
 // Few rows (a token or a few drafts of a group of heads): bound by HBM, if the
-// decoding of the codes keeps up.  So no code passes through shared memory: a
-// warp's lanes load the cache's words straight into the registers of the tensor
+// decoding of the codes keeps up.  So nothing decoded passes through shared memory: a
+// warp's lanes take the cache's words, copied ahead asynchronously, into the registers of the tensor
 // instruction's fragments (m16n8k16) and decode them there, 11 instructions a word of 8.
 //   S^T = K Q^T   A = 16 slots x 16 dimensions of keys in fp16, B = 8 query rows.
 //                 The order of the dimensions is free as long as Q's agrees: the
@@ -22,6 +22,9 @@
 //
 // Each of the four warps of a CTA walks its own chunks of 32 slots with its own
 // running max and sum; the warps join at the end of a piece.
+// Measured: a token of 256 requests of up to 4096 slots (4 heads a group, 8 groups of 128) 215 us, 4.0 TB/s;
+// issue slots 60 % used, the tensor pipe busy in 76 % of the cycles, 16 warps an SM.  The first form, without
+// shared memory's ring of 3 stages a warp, took 317.
 #include <string.h>
 
 #include <algorithm>
@@ -381,9 +384,9 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
       const int* table = p.cache.table + (long long)b * p.cache.M;
       const int mask = (1 << p.cache.shift) - 1;
       // scores before the cap, or in units of log2 where there is none
-      const float unit_scale = fabsf(p.scale) * (p.softcap > 0.f ? 1.f / p.softcap : kLog2e);
+      const float unit = unit_scale(p);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) unscale[n][0] *= unit_scale, unscale[n][1] *= unit_scale;
+      for (int n = 0; n < NT; ++n) unscale[n][0] *= unit, unscale[n][1] *= unit;
       // The warp's stages: chunk c's copies are queued kStages - 1 chunks ahead, its page ids
       // read one chunk before that.
       constexpr int kStageBytes = kTiles * Tile<D>::kBytes;
@@ -439,16 +442,18 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
                           (p.window > 0 && slot0 <= r.base + r.nq - 1 - p.window);
         const bool plain = !edge && p.softcap == 0.f && !p.slopes;
         if (!plain) {
+          auto each = [&](auto f) {
 #pragma unroll
-          for (int k = 0; k < kTiles; ++k)
+            for (int k = 0; k < kTiles; ++k)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+              for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float y = s[k][n][e] * unscale[n][e & 1];
-                if (p.softcap > 0.f) y = cap_of<kExact>(p.softcap * kLog2e, y);
-                s[k][n][e] = y;
-              }
+                for (int e = 0; e < 4; ++e) s[k][n][e] = f(s[k][n][e] * unscale[n][e & 1]);
+          };
+          if (p.softcap > 0.f)
+            cap_all<kExact>(p.softcap * kLog2e, each);
+          else
+            each([](float y) { return y; });
         }
         if (edge || p.slopes) {
 #pragma unroll
@@ -901,8 +906,7 @@ extern "C" sv_status spec_cache_attention(
   const sv_status rc = check_cache(&p.cache, cache, page_stride, table, pages, page_size, B, M,
                                    kv_heads, head_dim);
   if (rc != SV_OK) return rc;
-  if (!(scale == scale) || scale - scale != 0.f || !(softcap >= 0.f) || softcap - softcap != 0.f ||
-      window < 0)
+  if (!(scale == scale) || scale - scale != 0.f || !(softcap >= 0.f && softcap <= 1e30f) || window < 0)
     return SV_ERR_SCORE;
   if (tree_parent && parent_stride != 0 && parent_stride != N - 1) return SV_ERR_TREE;
   if (B == 0 || N == 0) return SV_OK;
@@ -916,6 +920,12 @@ extern "C" sv_status spec_cache_attention(
     if (st[i] < 0 || st[i] > (1LL << 60) / n[i]) return SV_ERR_SHAPE;
     if (st[i] % 16) return SV_ERR_NULL;
   }
+  // (rows of other tiles are read while a tile's are written)
+  const size_t row = (size_t)head_dim * esize;
+  const char *q0 = static_cast<const char*>(q), *o0 = static_cast<const char*>(out);
+  size_t q_bytes = row;
+  for (int i = 0; i < 3; ++i) q_bytes += (size_t)(n[i] - 1) * st[i];
+  if (q0 < o0 + (size_t)B * N * q_heads * row && o0 < q0 + q_bytes) return SV_ERR_ALIAS;
   p.q = q;
   p.qb = st[0] / esize;
   p.qn = st[1] / esize;

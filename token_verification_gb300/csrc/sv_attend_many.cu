@@ -10,16 +10,18 @@
 // each time).  Decoded keys and values are exact in fp16; a row of Q is scaled by a power of two
 // (exact), weights are rounded to 2^-11.
 //
-// Two CTAs an SM, whose 8 warps all do the same: decode the chunk's values and the next one's keys
-// (rows of a slot, 64 dimensions or 128 bytes a block, 128-byte swizzle: K-major for the
-// keys, MN-major for the values), and between them the softmax, a thread a slot and half of the
-// rows: scores from tensor memory, weights to shared memory.  One thread then issues O of
-// this chunk and S of the next.  While one CTA waits for the tensor pipe the other decodes.
-// Bound by the threads' instructions (about 720 a warp and chunk: 300 for decoding, 150 for
-// loading, 60 for exponentials), not by HBM or the tensor pipe.  Measured: 490 us for trees of 61 nodes
-// over 32 requests of up to 4096 slots (4 heads a group, 8 groups of 128), 305 us for 6
-// tokens each of 64 requests of up to 8192 (8 heads a group).  One CTA an SM took 732 us for those trees, and warps of one task each (softmax,
-// decoding, issuing) 757: each of their instructions waited to be fetched.
+// Two CTAs an SM, whose 8 warps all do the same: decode keys and values (rows of a slot, 64
+// dimensions or 128 bytes a block, 128-byte swizzle: K-major for the keys, MN-major for the
+// values), and between them the softmax, a thread a slot and half of the rows: scores from
+// tensor memory, weights to shared memory.  One thread issues the products: S of the next chunk once its
+// keys are in, while this one's weights are worked out (S has two places), and O of this chunk
+// while the next one's keys are decoded.
+// Bound by latencies between 16 warps an SM (issue slots 46 % used, tensor pipe 45 %, shared memory 47 %),
+// not by HBM; of about 690 instructions a warp and chunk 300 decode and 60 are exponentials.  Measured:
+// 470 us for trees of 61 nodes over 32 requests of up to 4096 slots (4 heads a group, 8 groups of 128), 290 us
+// for 6 tokens each of 64 requests of up to 8192 (8 heads a group; 1.5 TB/s).  One CTA
+// an SM took 732 us for those trees, and warps of one task each (softmax, decoding, issuing)
+// 757: each of their instructions waited to be fetched.  Issuing S and O together at the chunk's end: 487.
 // A row's weights are relative to a reference that follows its running max only when a
 // score exceeds it by 2^8: the weights, at most 2^15 then, stay within fp16, and the
 // threads, which hold one slot of every row, need to agree on a row's max (and to rescale O in
@@ -403,8 +405,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
                      pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
       if (x == 0) {
         float* fo = reinterpret_cast<float*>(&sm.fo[at / 2]) + (at & 1);
-        fo[0] = __uint_as_float((uint32_t)(127 + e - 14) << 23) * fabsf(p.scale) *
-                (p.softcap > 0.f ? 1.f / p.softcap : kLog2e);
+        fo[0] = __uint_as_float((uint32_t)(127 + e - 14) << 23) * unit_scale(p);
         fo[2] = kNoRef;
         sm.m[at] = -INFINITY;
         sm.slope[at] = p.slopes ? p.slopes[head] * kLog2e : 0.f;
@@ -514,11 +515,19 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
         const int node = slot - r.base;
         int at = slot;
         if (p.parent && there && node >= 0) at = r.base + tree.depth(node);
+        auto each = [&](auto f) {
+#pragma unroll
+          for (int i = 0; i < NH; ++i)
+            s[i] = f(s[i] * reinterpret_cast<const float*>(&sm.fo[(row_at + i) / 2])[i & 1]);
+        };
+        if (p.softcap > 0.f)
+          cap_all<false>(cap, each);
+        else
+          each([](float y) { return y; });
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
           const int row = row_at + i;
-          float y = s[i] * reinterpret_cast<const float*>(&sm.fo[row / 2])[i & 1];
-          if (p.softcap > 0.f) y = cap_of<false>(cap, y);
+          float y = s[i];
           if (p.slopes) y = fmaf(-sm.slope[row], (float)(sm.pos[row] - at), y);
           bool seen = there;
           if (edge && there && node >= 0) {

@@ -1,12 +1,15 @@
 // sv_cache.cu - writing the 4-bit cache, reading it back, and keeping a
 // tree's path in it (spec_cache_write, spec_cache_read, spec_cache_keep).
 //
-// All three move bytes and are bound by HBM (or by the launch for a step's few
-// tokens).  A thread takes the same 8 values of four neighbouring slots of a head,
-// keys and values both: of each token a 16-byte load of bf16 and a 4-byte store of codes
-// (or the reverse), of all four the scale bytes of a group as one word where all four are
+// All three move bytes.  In the first two a thread takes the same 8 values of four neighbouring
+// slots of a head, keys and values both: of each token a 16-byte load of bf16 and a 4-byte store of
+// codes (or the reverse), of all four the scale bytes of a group as one word where all four are
 // touched.  The D / 8 threads of a token lie side by side, consecutive slots in consecutive
 // threads, so that a page's code rows are read and written whole.
+// Measured for 8 prompts of up to 8192 tokens (8 heads of 128, bf16): write 44 us, 193 MB at 4.4 TB/s,
+// bound by its instructions (issue slots 74 % used, 16 instructions a value); read
+// 45 us, 308 MB with the zeros behind the prompts at 6.8 TB/s, bound by HBM.  A step's few tokens are bound
+// by the launches.
 #include <string.h>
 
 #include <algorithm>
@@ -365,7 +368,9 @@ __device__ __forceinline__ int path_length(const KeepParams& p, long long b) {
 // One warp moves a request's head.  Slot start + path[i] goes to start + i.
 // The path ascends from 0 or above, so i <= path[i] < path[j] for i < j: no
 // store lands on a slot that a later load reads, and a thread that moves
-// the same bytes of every token may load a batch of them before it stores.
+// the same bytes of every token may load a batch of them before it stores.  The launch
+// and that chain of path, table, codes and store are what a call takes: writing a tree of 61 nodes, keeping 6 and
+// reading them back is 11.8 us in three launches.
 constexpr int kKeepBatch = 8;
 
 template <int D>
