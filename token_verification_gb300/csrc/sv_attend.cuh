@@ -308,7 +308,8 @@ __device__ __forceinline__ float tanh_fast(float x) {
 }
 
 // cap * tanh(x) of scores.  The fast form is off by 2^-22 cap: 2^-13 of a score's unit at most where it is
-// taken (one branch for all of them: a branch each took 93 us where this takes 91).
+// taken.  One branch for a chunk's scores: a branch each took 93 us instead of 91 for 5 tokens of 16
+// requests (up to 8192 slots, 8 heads of 256, two query heads each).
 constexpr float kFastCap = 512.f;
 template <bool EXACT, class F>
 __device__ __forceinline__ void cap_all(float cap, F each) {
