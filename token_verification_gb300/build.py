@@ -24,9 +24,9 @@ BINDING = os.path.join(HERE, "_binding.so")
 BUILT_FOR = os.path.join(BUILD, "binding.txt")  # the Python and PyTorch that _binding.so was built for
 SOURCES = ["api.cu", "sv_verify.cu", "sv_finalize.cu", "sv_filter.cu", "sv_tree.cu", "sv_noalloc.cu", "sv_ngram.cu",
            "sv_top.cu", "sv_toprows.cu", "sv_distill.cu", "sv_reorder.cu",
-           "sv_cache.cu", "sv_attend.cu", "sv_attend_many.cu"]
+           "sv_cache.cu", "sv_attend.cu", "sv_attend_many.cu", "sv_attend_rows.cu"]
 HEADERS = ["sv_common.cuh", "sv_launch.h", "sv_rows.cuh", "sv_stream.cuh", "sv_vec.cuh", "sv_select.cuh",
-           "sv_cache.cuh", "sv_attend.cuh"]
+           "sv_cache.cuh", "sv_attend.cuh", "sv_attend_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                 "-I" + os.path.join(ROOT, "include")]

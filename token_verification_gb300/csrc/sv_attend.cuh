@@ -338,5 +338,7 @@ cudaError_t launch_few(const AttendParams& p, int D, int dtype, const AttendPlan
                        cudaStream_t stream);
 cudaError_t plan_many(int rows, AttendPlan* plan);
 cudaError_t launch_many(const AttendParams& p, int D, const AttendPlan& plan, cudaStream_t stream);
+// launch_many's kernel of 128 rows a tile.
+cudaError_t launch_rows(const AttendParams& p, int D, const AttendPlan& plan, cudaStream_t stream);
 
 }  // namespace sv

@@ -32,7 +32,7 @@
 #include <atomic>
 
 #include "../../include/spec_verify.h"
-#include "sv_attend.cuh"
+#include "sv_attend_tc.cuh"
 #include "sv_rows.cuh"
 #include "sv_vec.cuh"
 
@@ -40,132 +40,8 @@ namespace sv {
 namespace {
 
 constexpr int kManyThreads = 256;
-constexpr int kSlotsTile = 128;
-constexpr float kManyShift = 7.f, kSlack = 8.f;
-constexpr float kNoRef = 3e38f;  // in place of shift - max for a row without a score yet
 constexpr int kTmemCols = 256;
 constexpr int kSCol = 64, kOCol = 128;  // columns: S of chunk j at kSCol (j mod 2), O
-
-// ---- tcgen05 -------------------------------------------------------------
-
-__device__ __forceinline__ void tmem_alloc(uint32_t dst) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
-               "n"(kTmemCols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-}
-__device__ __forceinline__ void tmem_free(uint32_t addr) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "n"(kTmemCols));
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
-  return r != 0;
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   bar)
-               : "memory");
-}
-__device__ __forceinline__ void fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-      "%10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_load8(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_loaded() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_stored() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-// mbar_wait for waits that are long as a rule: the warp sleeps (for 20 us at a time) instead of asking
-// again, which would take issue slots from the others.
-__device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity, unsigned long long limit) {
-  if (limit == 0) return false;
-  auto ask = [&] {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    return ok != 0;
-  };
-  if (ask()) return true;
-  const unsigned long long t0 = global_ns();
-  for (;;) {
-    if (ask()) return true;
-    if (global_ns() - t0 > limit) return false;
-  }
-}
-__device__ __forceinline__ void store16(uint32_t addr, const uint32_t (&x)[4]) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-               "r"(x[3])
-               : "memory");
-}
-
-// Shared-memory descriptors: 128-byte swizzle, version 1.  Keys and queries (K-major): 8 rows of 128
-// bytes every 1024.  Values (MN-major): 64 dimensions a block, blocks 16384 bytes
-// apart, 8 slots every 1024.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lead >> 4) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-constexpr uint32_t kBlockBytes = 128 * 128;  // 128 rows or slots of 64 dimensions
-// Instruction: fp32 results, fp16 operands, M = 128.
-__host__ __device__ constexpr uint32_t idesc(int n, bool mn_major) {
-  return 1u << 4 | (mn_major ? 3u << 15 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
-}
-
-// A chunk ahead: addresses of each 16 slots' key codes and key scales (of some page where there is
-// none), which of them are pages (bits), and which slots are seen by anybody (first <= slot in the chunk
-// < last); whole: every slot is.
-struct ChunkRef {
-  unsigned long long codes[8], scales[8];
-  uint32_t valid;
-  int first, last, whole;
-};
 
 template <int D, int NC>
 struct ManySmem {
@@ -206,23 +82,6 @@ __device__ __forceinline__ float warp_top(float x) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
-}
-
-// A thread's part of a chunk's keys or values: kU rows of one group of 32 values.
-template <int D>
-struct Part {
-  static constexpr int kU = D / 64;
-  uint32_t scale[kU];  // bytes
-  uint32_t off;        // bit i: row i counts as NaN (keys) or 0 (values), whatever its byte
-};
-__device__ __forceinline__ void copy16(uint32_t dst, unsigned long long src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// (volatile: where it stands, not where its result is used)
-__device__ __forceinline__ uint32_t load_byte(unsigned long long src) {
-  uint32_t x;
-  asm volatile("ld.global.u8 %0, [%1];" : "=r"(x) : "l"(src) : "memory");
-  return x;
 }
 
 // N columns of tensor memory from `addr` on.
@@ -277,7 +136,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     p.late[cta] = 0;
   }
   if (cta >= share.G) return;
-  if (warp == 0) tmem_alloc(smem_u32(&sm.tmem));
+  if (warp == 0) tmem_alloc<kTmemCols>(smem_u32(&sm.tmem));
   fence_before();
   __syncthreads();
   fence_after();
@@ -289,40 +148,9 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const int r8 = tid & 7, g = (tid >> 3) % G, my_slot = (tid >> 3) / G * (8 * kU) + r8;
   const int block = page_bytes(1, D) << p.cache.shift;
   Part<D> keys, vals;
-  // Warp 7 finds the addresses (lane k < 8 of the k-th 16 slots' codes, lane k + 8 of their scales),
-  // three chunks ahead, from page ids that it read a chunk before that.
-  Walk ahead(p, share);
-  unsigned j_ahead = 0;
-  int id = -1;
-  auto fetch_id = [&] {
-    const int slot = (ahead.r.lo / kSlotsTile + ahead.c) * kSlotsTile + 16 * (lane & 7);
-    id = ahead.left > 0 && slot < ahead.r.len
-             ? p.cache.table[(long long)ahead.b * p.cache.M + (slot >> p.cache.shift)]
-             : -1;
-  };
+  Finder<D> finder(p, share);  // (warp 7)
   auto find = [&] {
-    if (warp != 7 || ahead.left <= 0) return;
-    const int slot0 = (ahead.r.lo / kSlotsTile + ahead.c) * kSlotsTile;
-    const bool ok = (unsigned)id < (unsigned)p.cache.pages;
-    const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffu;
-    const int token = (slot0 + 16 * (lane & 7)) & ((1 << p.cache.shift) - 1);
-    const unsigned long long at =
-        reinterpret_cast<unsigned long long>(p.cache.data) +
-        (unsigned long long)(ok ? (unsigned)id : 0u) * p.cache.page_stride +
-        (long long)(2 * ahead.h) * block +
-        (lane & 8 ? ((D / 2) << p.cache.shift) + token * (D / kGroup) : token * (D / 2));
-    ChunkRef& ref = sm.refs[j_ahead & 3];
-    if (lane < 8) ref.codes[lane] = at;
-    if (lane >= 8 && lane < 16) ref.scales[lane - 8] = at;
-    if (lane == 0) {
-      ref.valid = valid;
-      ref.first = max(0, ahead.r.lo - slot0);
-      ref.last = min(kSlotsTile, ahead.r.len - slot0);
-      ref.whole = valid == 0xffu && slot0 >= ahead.r.lo && slot0 + kSlotsTile <= ahead.r.len;
-    }
-    ++j_ahead;
-    ahead.step(p);
-    fetch_id();
+    if (warp == 7) finder.find(p, sm.refs);
   };
   const int code_at = (my_slot & 15) * (D / 2) + g * 16;  // from the 16 slots' first codes
   const int scale_off = (my_slot & 15) + g * 16;          // and from their scales
@@ -387,25 +215,12 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
       if (row < rows && w.r.ok)
         v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + w.b * p.qb +
                                            i * p.qn + (long long)head * p.qh)[x];
-      // (magnitudes of bf16 order as whole numbers)
-      uint32_t top2 = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                               __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-#pragma unroll
-      for (int o = kPer / 2; o > 0; o >>= 1)
-        top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
-      const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-      const int e = min(max((int)(top >> 7) - 127, -98), 126);
-      float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-      if (top >= 0x7f80u) up = qnan();  // (a row with NaN or infinity is NaN)
-      if (p.scale < 0.f) up = -up;
+      float down;
       *reinterpret_cast<uint4*>(sm.q + (x / 8) * (NC * 128) + at * 128 + (((x & 7) ^ (at & 7)) << 4)) =
-          make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
-                     pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                     pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
-                     pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+          scaled_query<kPer>(v, p.scale < 0.f, &down);
       if (x == 0) {
         float* fo = reinterpret_cast<float*>(&sm.fo[at / 2]) + (at & 1);
-        fo[0] = __uint_as_float((uint32_t)(127 + e - 14) << 23) * unit_scale(p);
+        fo[0] = down * unit_scale(p);
         fo[2] = kNoRef;
         sm.m[at] = -INFINITY;
         sm.slope[at] = p.slopes ? p.slopes[head] * kLog2e : 0.f;
@@ -423,14 +238,14 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
       mma_ss(tmem + (j & 1) * kSCol, k_desc + (((i / 4) * kBlockBytes + (i % 4) * 32) >> 4),
-             q_desc + (((i / 4) * (NC * 128) + (i % 4) * 32) >> 4), idesc(NC, false), i > 0);
+             q_desc + (((i / 4) * (NC * 128) + (i % 4) * 32) >> 4), idesc(NC, false, false), i > 0);
     mma_commit(qk_bar);
   };
   // (at D = 64 the second block of dimensions is the next tile, and nothing reads its rows)
   auto issue_out = [&](bool add) {
 #pragma unroll
     for (int i = 0; i < kSlotsTile / 16; ++i)
-      mma_ss(tmem + kOCol, v_desc + (i * 2048 >> 4), p_desc + (i * 2048 >> 4), idesc(NC, true),
+      mma_ss(tmem + kOCol, v_desc + (i * 2048 >> 4), p_desc + (i * 2048 >> 4), idesc(NC, true, true),
              add || i > 0);
     mma_commit(pv_bar);
   };
@@ -441,7 +256,6 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const float cap = p.softcap * kLog2e;
 
   Walk w(p, share);
-  if (warp == 7) fetch_id();
   find();
   find();
   find();
@@ -712,7 +526,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     __syncwarp();
     mbar_wait(smem_u32(&sm.drained), 0);
     __syncwarp();
-    tmem_free(tmem);
+    tmem_free<kTmemCols>(tmem);
   }
 }
 
@@ -735,6 +549,9 @@ cudaError_t launch_one(const AttendParams& p, const AttendPlan& plan, cudaStream
 
 }  // namespace
 
+// ROWS
+constexpr int kFewTiles = 2;
+
 cudaError_t plan_many(int rows, AttendPlan* plan) {
   DeviceInfo info;
   const cudaError_t err = device_info(&info);
@@ -742,7 +559,7 @@ cudaError_t plan_many(int rows, AttendPlan* plan) {
   // as few tiles as tiles of 48 would be (64 rows do not fit the registers: 505 -> 580 us for trees
   // of 61 nodes), with few rows of them empty
   const int tiles = (rows + 47) / 48, each = (rows + tiles - 1) / tiles;
-  plan->rows = each <= 32 ? 32 : 48;
+  plan->rows = rows > kFewTiles * 48 ? 128 : each <= 32 ? 32 : 48;
   plan->chunk = kSlotsTile;
   plan->least = 1;
   plan->shift = kManyShift;
@@ -751,6 +568,7 @@ cudaError_t plan_many(int rows, AttendPlan* plan) {
 }
 
 cudaError_t launch_many(const AttendParams& p, int D, const AttendPlan& plan, cudaStream_t stream) {
+  if (plan.rows == 128) return launch_rows(p, D, plan, stream);
 #define SV_MANY(d, n) \
   if (D == d && plan.rows == n) return launch_one<d, n>(p, plan, stream);
   SV_MANY(64, 32) SV_MANY(64, 48) SV_MANY(128, 32) SV_MANY(128, 48)
