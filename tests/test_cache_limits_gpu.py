@@ -145,6 +145,19 @@ def test_many_requests(B, N, group, D, dtype):
     run(query(B, N, group, D, dtype, g), cache, page, table, lens, parent=tree(B, N, g))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [17, 32, 33, 48, 49, 96, 97, 127, 128, 129, 144, 145, 192, 255, 256, 257])
+def test_tiles_of_rows(rows, D):
+    """Every tile's last row, on a chain and on a tree; one request of several chunks, one of one."""
+    g = gen(rows + D)
+    cache, table = filled(2, 400, 2, D, 32, g)
+    lens = ints([400, rows])
+    spoil(cache, table, lens, 32, D)
+    q = query(2, rows, 2, D, BF16, g)
+    run(q, cache, 32, table, lens)
+    run(q, cache, 32, table, lens, parent=tree(2, rows, g), window=90)
+
+
 @pytest.mark.parametrize("Hq,Hkv,dtype", [(1024, 1, BF16), (1024, 1024, BF16), (1024, 1, F32),
                                           (1000, 8, BF16)])
 def test_many_heads(Hq, Hkv, dtype):

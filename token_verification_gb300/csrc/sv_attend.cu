@@ -820,7 +820,8 @@ cudaError_t launch_few(const AttendParams& p, int D, int dtype, const AttendPlan
 
 cudaError_t launch_join(const AttendParams& p, int D, int dtype, int ctas, int units,
                         cudaStream_t stream) {
-  const bool wide = units * 16 <= ctas;  // units in 16 pieces or more, or whole
+  // units in 16 pieces or more, or whole, and few rows (a block each for many takes longer to launch)
+  const bool wide = p.rows <= 16 && units * 16 <= ctas;
   const dim3 grid(ctas, wide ? std::min(p.rows, p.N * p.group)
                              : p.rows > 16 ? (p.rows + kJoinWarps - 1) / kJoinWarps : 1);
   cudaLaunchConfig_t cfg = {};

