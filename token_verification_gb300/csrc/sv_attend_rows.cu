@@ -7,12 +7,12 @@
 // in fp16 with 32-bit sums.  What the kernel for tiles of 32 or 48 rows (sv_attend_many.cu) spends on
 // decoding a chunk serves 128 rows here.  A thread has a row and half of the chunk's slots, so
 // that a row's factors, max and sum are its own; scores are read from tensor memory twice, once for the
-// largest and once for the weights, 32 at a time.
+// largest and once for the weights, 16 at a time (32: spilled registers, 294 instead of 230 us below).
 // Two CTAs an SM, whose 8 warps all do the same; the next chunk's keys take the place of this one's as
 // soon as S is out, the values' codes wait in registers.
-// Bound by the tensor pipe (busy in 68 % of the cycles; issue slots 38 % used) and what the chain of
-// product, weights, product of two CTAs leaves open.  Measured: 294 us for trees of 61 nodes over 32 requests
-// of up to 4096 slots (4 heads a group, 8 groups of 128), 340 TFLOP/s of the trees' own products.
+// Bound by the tensor pipe (busy in 68 % of the cycles when it took 294) and what the chain of
+// product, weights, product of two CTAs leaves open.  Measured: 230 us for trees of 61 nodes over 32 requests
+// of up to 4096 slots (4 heads a group, 8 groups of 128), 430 TFLOP/s of the trees' own products.
 #include <string.h>
 
 #include <algorithm>
@@ -273,24 +273,24 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
       const bool edge = !sees || slot0 + kSlotsTile > r.base ||
                         (p.window > 0 && slot0 <= r.base + r.nq - 1 - p.window);
       const bool plain = !edge && p.softcap == 0.f && !p.slopes;
-      // scores of 32 slots in units of log2, before the row's factor where plain
-      auto load_scores = [&](int part, float (&s)[32]) {
-        tmem_load32(mine + 32 * part, s);
+      // scores of 16 slots in units of log2, before the row's factor where plain
+      auto load_scores = [&](int part, float (&s)[16]) {
+        tmem_load16(mine + 16 * part, reinterpret_cast<uint32_t*>(s));
         tmem_loaded();
         if (plain) return;
         auto each = [&](auto fn) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = fn(s[i] * f);
+          for (int i = 0; i < 16; ++i) s[i] = fn(s[i] * f);
         };
         if (p.softcap > 0.f)
           cap_all<false>(cap, each);
         else
           each([](float y) { return y; });
         if (!edge && !p.slopes) return;
-        const int first = slot0 + 64 * half + 32 * part, other = sm.node[row], pos = sm.pos[row];
+        const int first = slot0 + 64 * half + 16 * part, other = sm.node[row], pos = sm.pos[row];
         const float slope = sm.slope[row];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
           const int slot = first + i, node = slot - r.base;
           bool seen = sees && slot < r.len;
           int at = slot;
@@ -306,11 +306,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
       const float fe = plain ? f : 1.f;
       float top = -INFINITY;
 #pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        float s[32], t[2] = {-INFINITY, -INFINITY};
+      for (int part = 0; part < 4; ++part) {
+        float s[16], t[2] = {-INFINITY, -INFINITY};
         load_scores(part, s);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) t[i / 2 & 1] = max3(t[i / 2 & 1], s[i], s[i + 1]);
+        for (int i = 0; i < 16; i += 2) t[i / 2 & 1] = max3(t[i / 2 & 1], s[i], s[i + 1]);
         top = max3(top, t[0], t[1]);
       }
       top *= fe;  // (factors are not negative)
@@ -340,13 +340,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
       }
       if (warp == 7) finder.find(p, sm.refs);  // (in the place of the chunk before this one)
 #pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        float s[32];
-        uint32_t x[16];
+      for (int part = 0; part < 4; ++part) {
+        float s[16];
+        uint32_t x[8];
         load_scores(part, s);
         const f32x2 f2 = pack2(fe, fe), off2 = pack2(off, off);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           float w0, w1;
           unpack2(fma2(pack2(s[2 * i], s[2 * i + 1]), f2, off2), w0, w1);
           w0 = ex2(w0);
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
           l = add2(l, pack2(w0, w1));
           x[i] = pack_f16(w0, w1);
         }
-        tmem_store16(mine + 16 * part, x);
+        tmem_store8(mine + 8 * part, x);
       }
       tmem_stored();
       // the next chunk's keys (their place is free: this chunk's scores are out)
