@@ -181,10 +181,11 @@ struct Walk {
     h = unit / r.tiles;
     tile = unit - h * r.tiles;
   }
-  __device__ __forceinline__ void step(const AttendParams& p) {
-    --left;
-    if (++c < r.chunks) return;
-    next_unit(p);
+  // n chunks on, which are of one unit
+  __device__ __forceinline__ void skip(const AttendParams& p, int n) {
+    left -= n;
+    c += n;
+    if (c == r.chunks) next_unit(p);
   }
   __device__ __forceinline__ void next_unit(const AttendParams& p) {
     c = 0;

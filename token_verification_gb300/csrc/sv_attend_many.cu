@@ -62,6 +62,7 @@ struct ManySmem {
   int pos[NC], node[NC], out_row[NC];
   alignas(8) unsigned long long qk_done, pv_done, drained;  // completed by the tensor pipe
   ChunkRef refs[4];  // of chunk j in j mod 4
+  FinderState finder;
   uint32_t tmem;
   long long scan[kManyThreads / 32 + 2];
   static __host__ __device__ constexpr int used() {
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const int r8 = tid & 7, g = (tid >> 3) % G, my_slot = (tid >> 3) / G * (8 * kU) + r8;
   const int block = page_bytes(1, D) << p.cache.shift;
   Part<D> keys, vals;
-  Finder<D> finder(p, share);  // (warp 7)
+  Finder<D> finder;  // (warp 7)
   auto find = [&] {
     if (warp == 7) finder.find(p, sm.refs);
   };
@@ -256,6 +257,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const float cap = p.softcap * kLog2e;
 
   Walk w(p, share);
+  if (warp == 7) finder.start(p, share, &sm.finder);
   find();
   find();
   find();
@@ -265,7 +267,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   // (a chunk's worth of work lies between a load and the use of it)
   const unsigned n = (unsigned)w.left;
   // (copies of keys and of values are queued in turn, so one group behind the wanted one may be in
-  // flight: the other's; but for a piece's second keys)
+  // flight: the other's.  Not behind a piece's second keys, which come right after the first, nor
+  // behind its last values, before which no keys are put.)
   auto put_keys = [&](unsigned i, bool second) {  // of chunk i, then the next one's are on their way
     if (second)
       asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -277,8 +280,11 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     else
       asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto put_values = [&](unsigned i) {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  auto put_values = [&](unsigned i, bool last) {
+    if (last)
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
     put(vals, 0, 0u);
     if (i + 1 < n)
       load(sm.refs[(i + 1) & 3], vals, true);
@@ -308,9 +314,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     f32x2 l[NH / 2];
 #pragma unroll
     for (int i = 0; i < NH / 2; ++i) l[i] = pack2(0.f, 0.f);
-    int c = c0;
-    for (; c < c1 && !late; ++c, ++j) {
-      w.step(p);  // (stands at the next chunk from here on)
+    for (int c = c0; c < c1 && !late; ++c, ++j) {
       bool out_of_time = !sleep_wait(qk_bar, j & 1, limit);
       // the next chunk's keys, whose product runs while this chunk's weights are worked out
       if (c + 1 < c1) put_keys(j + 1, c == c0);
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
       for (int i = 0; i < NH / 8; ++i)
         store16(to + (((row_at / 8 + i) ^ (slot_at & 7)) << 4),
                 {x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
-      put_values(j);
+      put_values(j, c + 1 == c1);
       fence_proxy_async();
       fence_before();
       late = __syncthreads_or(out_of_time);
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
       __syncwarp();
     }
 
-    for (; c < c1; ++c) w.step(p);  // (a piece behind a wait that ran out)
+    w.skip(p, c1 - c0);  // (stands at the next piece from here on)
 
     // the piece's rows: their sums over the slots, by way of the weights' place
     if (!late) late = __syncthreads_or(!mbar_wait(pv_bar, (j - 1) & 1, limit));

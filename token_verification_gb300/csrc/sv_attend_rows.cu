@@ -45,6 +45,7 @@ struct RowsSmem {
   int pos[kTileRows], node[kTileRows], out_row[kTileRows];
   alignas(8) unsigned long long qk_done, pv_done, drained;  // completed by the tensor pipe
   ChunkRef refs[4];  // of chunk j in j mod 4
+  FinderState finder;
   uint32_t tmem;
   long long scan[kRowsThreads / 32 + 2];
   static __host__ __device__ constexpr int used() {
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
   const int block = page_bytes(1, D) << p.cache.shift;
   Part<D> keys, vals;
   uint4 codes[kU];        // of the values
-  Finder<D> finder(p, share);  // (warp 7)
+  Finder<D> finder;       // (warp 7)
   const int code_at = (my_slot & 15) * (D / 2) + g * 16;  // from the 16 slots' first codes
   const int scale_off = (my_slot & 15) + g * 16;          // and from their scales
   const uint32_t raw_at = smem_u32(&sm.raw[0][tid]);
@@ -226,8 +227,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
   const float cap = p.softcap * kLog2e;
 
   Walk w(p, share);
-  if (warp == 7)
+  if (warp == 7) {
+    finder.start(p, share, &sm.finder);
     for (int i = 0; i < 3; ++i) finder.find(p, sm.refs);
+  }
   __syncthreads();
   load_keys(sm.refs[0]);
   load_values(sm.refs[0]);
@@ -254,9 +257,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
     const float f = sm.fo[row];
     float m = -INFINITY, off = kNoRef;
     f32x2 l = pack2(0.f, 0.f);
-    int c = c0;
-    for (; c < c1 && !late; ++c, ++j) {
-      w.step(p);  // (stands at the next chunk from here on)
+    for (int c = c0; c < c1 && !late; ++c, ++j) {
       bool out_of_time = false;
       if (c > c0) {  // the last chunk's product is out: its weights' and values' places are free
         out_of_time = !sleep_wait(pv_bar, (j - 1) & 1, limit);
@@ -369,8 +370,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
       __syncwarp();
     }
 
-    for (; c < c1; ++c) w.step(p);  // (a piece behind a wait that ran out)
-
+    w.skip(p, c1 - c0);  // (stands at the next piece from here on)
     if (!late) late = __syncthreads_or(!mbar_wait(pv_bar, (j - 1) & 1, limit));
     __syncwarp();
     fence_after();

@@ -195,14 +195,27 @@ __device__ __forceinline__ uint4 scaled_query(const uint4& v, bool negative, flo
 }
 
 // Finds the addresses of a share's chunks in turn (one warp; lane k < 8 those of the k-th 16 slots' codes,
-// lane k + 8 of their scales), from page ids that it read a chunk before that.
+// lane k + 8 of their scales), from page ids that it read a chunk before that.  Where it stands
+// lies in shared memory: every thread of the block would hold the registers.
+struct FinderState {
+  Walk ahead;
+  unsigned j;  // the chunk that is next
+};
 template <int D>
 struct Finder {
-  Walk ahead;
-  unsigned j = 0;  // the chunk that is next
+  FinderState* state;
   int id;
-  __device__ __forceinline__ Finder(const AttendParams& p, const Share& s) : ahead(p, s) { fetch(p); }
-  __device__ __forceinline__ void fetch(const AttendParams& p) {
+  __device__ __forceinline__ void start(const AttendParams& p, const Share& s, FinderState* at) {
+    state = at;
+    const Walk ahead(p, s);
+    if (lane_id() == 0) {
+      state->ahead = ahead;
+      state->j = 0;
+    }
+    __syncwarp();
+    fetch(p, ahead);
+  }
+  __device__ __forceinline__ void fetch(const AttendParams& p, const Walk& ahead) {
     const int slot =
         (ahead.r.lo / kSlotsTile + ahead.c) * kSlotsTile + 16 * ((int)lane_id() & 7);
     id = ahead.left > 0 && slot < ahead.r.len
@@ -210,6 +223,9 @@ struct Finder {
              : -1;
   }
   __device__ __forceinline__ void find(const AttendParams& p, ChunkRef (&refs)[4]) {
+    Walk ahead = state->ahead;
+    const unsigned j = state->j;
+    __syncwarp();
     if (ahead.left <= 0) return;
     const int lane = lane_id();
     const int slot0 = (ahead.r.lo / kSlotsTile + ahead.c) * kSlotsTile;
@@ -231,9 +247,13 @@ struct Finder {
       ref.last = min(kSlotsTile, ahead.r.len - slot0);
       ref.whole = valid == 0xffu && slot0 >= ahead.r.lo && slot0 + kSlotsTile <= ahead.r.len;
     }
-    ++j;
-    ahead.step(p);
-    fetch(p);
+    ahead.skip(p, 1);
+    if (lane == 0) {
+      state->ahead = ahead;
+      state->j = j + 1;
+    }
+    __syncwarp();
+    fetch(p, ahead);
   }
 };
 
