@@ -854,7 +854,8 @@ namespace {
 // The kernel and split of a call of `rows` query rows a key/value head.  Tensor memory's tiles of 32 or
 // 48 rows against tiles of 16 whose codes are decoded again for each: 269 against 286 us at 24
 // rows, 273 against 294 at 32, 304 against 419 at 40, 308 against 425 at 48 (64 requests of up to 8192
-// slots, 8 heads of 128), but 164 for the small tiles at 16 rows, which decode once.  Heads of
+// slots, 8 heads of 128; 48 rows have come to 284 since), but 164 for the small tiles at 16 rows, which decode
+// once.  Heads of
 // 256 and fp32 (two fp16 parts of everything) have the small tiles only.
 bool many_rows(sv_dtype dtype, int rows, int D) {
   return dtype == SV_BF16 && D <= 128 && rows > 16;

@@ -174,6 +174,7 @@ struct Walk {
   Request r;
   int b, h, tile, c;  // the chunk's request, head, row tile, and place in the unit
   long long left;     // chunks from here on
+  Walk() = default;
   __device__ __forceinline__ Walk(const AttendParams& p, const Share& s)
       : r(request_of(p, s.b)), b(s.b), left(s.end - s.begin) {
     const int unit = (int)(s.at / r.chunks);

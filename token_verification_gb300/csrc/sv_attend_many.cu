@@ -1,8 +1,8 @@
 // sv_attend_many.cu - attention over the 4-bit cache for many query rows
 // (spec_cache_attention): tensor memory and tcgen05 instructions.
 //
-// A unit is a tile of 32 or 48 query rows of a key/value head (tokens of the step times the
-// heads of the group), a chunk 128 slots, which takes
+// A unit is a tile of 32 or 48 query rows, all that a key/value head has (tokens of the step times the
+// heads of the group; for more see sv_attend_rows.cu), a chunk 128 slots, which takes
 //   S^T = K Q^T    128 slots x rows x D, both operands in shared memory
 //   O^T += V^T P^T  D x rows x 128 slots, values and weights P in shared memory
 // in fp16 with 32-bit sums in tensor memory.  Slots and dimensions lie on the instruction's side of
@@ -18,10 +18,10 @@
 // while the next one's keys are decoded.
 // Bound by latencies between 16 warps an SM (issue slots 46 % used, tensor pipe 45 %, shared memory 47 %),
 // not by HBM; of about 690 instructions a warp and chunk 300 decode and 60 are exponentials.  Measured:
-// 290 us for 6 tokens each of 64 requests of up to 8192 slots (8 heads a group, 8 groups of 128; 1.5 TB/s).
-// For trees of 61 nodes (470 us of 32 requests; tiles of 128 rows, sv_attend_rows.cu, take 292) one CTA
-// an SM took 732 us, and warps of one task each (softmax, decoding, issuing) 757: each of
-// their instructions waited to be fetched.  Issuing S and O together at the chunk's end: 487.
+// 284 us for 6 tokens each of 64 requests of up to 8192 slots (8 heads a group, 8 groups of 128; 1.6 TB/s).
+// In an earlier form, on six tiles of 48 rows of 32 trees (470 us here), one CTA an SM took 732 us, and
+// warps of one task each (softmax, decoding, issuing) 757: each of their instructions waited
+// to be fetched.  Issuing S and O together at the chunk's end: 487.
 // A row's weights are relative to a reference that follows its running max only when a
 // score exceeds it by 2^8: the weights, at most 2^15 then, stay within fp16, and the
 // threads, which hold one slot of every row, need to agree on a row's max (and to rescale O in
@@ -62,7 +62,6 @@ struct ManySmem {
   int pos[NC], node[NC], out_row[NC];
   alignas(8) unsigned long long qk_done, pv_done, drained;  // completed by the tensor pipe
   ChunkRef refs[4];  // of chunk j in j mod 4
-  FinderState finder;
   uint32_t tmem;
   long long scan[kManyThreads / 32 + 2];
   static __host__ __device__ constexpr int used() {
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const int r8 = tid & 7, g = (tid >> 3) % G, my_slot = (tid >> 3) / G * (8 * kU) + r8;
   const int block = page_bytes(1, D) << p.cache.shift;
   Part<D> keys, vals;
-  Finder<D> finder;  // (warp 7)
+  Finder<D, false> finder;  // (warp 7)
   auto find = [&] {
     if (warp == 7) finder.find(p, sm.refs);
   };
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
   const float cap = p.softcap * kLog2e;
 
   Walk w(p, share);
-  if (warp == 7) finder.start(p, share, &sm.finder);
+  finder.start(p, share, nullptr);
   find();
   find();
   find();
@@ -557,15 +556,12 @@ cudaError_t plan_many(int rows, AttendPlan* plan) {
   DeviceInfo info;
   const cudaError_t err = device_info(&info);
   if (err != cudaSuccess) return err;
-  // as few tiles as tiles of 48 would be (64 rows do not fit the registers: 505 -> 580 us for trees
-  // of 61 nodes), with few rows of them empty
-  const int tiles = (rows + 47) / 48, each = (rows + tiles - 1) / tiles;
-  // 128 rows decode a chunk once for what are 3 tiles here: 250 against 166 us at 100 rows (32 trees of up to
-  // 4096 slots, 8 heads), 321 against 278 at 192 rows, 459 against 292 at 244, and for one request
-  // of 244 rows 48.7 against 46.6.  Not where those tiles are hardly filled: 250 against 269 at 144 rows; nor for
-  // two tiles of 48, 183 against 164 in a batch but 32 against 43 for one request of 96 rows.
-  const int tiles128 = (rows + 127) / 128;
-  plan->rows = tiles > 2 && 2 * tiles128 <= tiles ? 128 : each <= 32 ? 32 : 48;
+  // One tile of 32 or 48 rows, or tiles of 128 (sv_attend_rows.cu): of 32 requests of up to 4096 slots, 8 heads of
+  // 128, 32 rows take 92 against 106 us, 48 rows 112 against 111 (but 288 against 302 of 64 requests of up to
+  // 8192); two tiles of 32 take 154 against 115, two of 48 183 against 122, 252 against 200 at 144 rows.  (For
+  // one request of 64 or 96 rows the small tiles would be faster, 28 against 35 us and 32 against
+  // 38, for one of 244 slower, 48 against 42.)
+  plan->rows = rows <= 32 ? 32 : rows <= 48 ? 48 : 128;
   plan->chunk = kSlotsTile;
   plan->least = 1;
   plan->shift = kManyShift;

@@ -10,9 +10,8 @@
 // largest and once for the weights, 16 at a time (32: spilled registers, 294 instead of 230 us below).
 // Two CTAs an SM, whose 8 warps all do the same; the next chunk's keys take the place of this one's as
 // soon as S is out, the values' codes wait in registers.
-// Bound by the tensor pipe (busy in 68 % of the cycles when it took 294) and what the chain of
-// product, weights, product of two CTAs leaves open.  Measured: 230 us for trees of 61 nodes over 32 requests
-// of up to 4096 slots (4 heads a group, 8 groups of 128), 430 TFLOP/s of the trees' own products.
+// Bound by the tensor pipe (busy in 88 % of the cycles; issue slots 46 % used).  Measured: 220 us for trees of 61 nodes over 32 requests
+// of up to 4096 slots (4 heads a group, 8 groups of 128), 450 TFLOP/s of the trees' own products.
 #include <string.h>
 
 #include <algorithm>
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
   const int block = page_bytes(1, D) << p.cache.shift;
   Part<D> keys, vals;
   uint4 codes[kU];        // of the values
-  Finder<D> finder;       // (warp 7)
+  Finder<D, true> finder;  // (warp 7)
   const int code_at = (my_slot & 15) * (D / 2) + g * 16;  // from the 16 slots' first codes
   const int scale_off = (my_slot & 15) + g * 16;          // and from their scales
   const uint32_t raw_at = smem_u32(&sm.raw[0][tid]);

@@ -195,24 +195,33 @@ __device__ __forceinline__ uint4 scaled_query(const uint4& v, bool negative, flo
 }
 
 // Finds the addresses of a share's chunks in turn (one warp; lane k < 8 those of the k-th 16 slots' codes,
-// lane k + 8 of their scales), from page ids that it read a chunk before that.  Where it stands
-// lies in shared memory: every thread of the block would hold the registers.
+// lane k + 8 of their scales), from page ids that it read a chunk before that.  Where it stands is
+// held in registers (of the whole block: the other warps' are idle), or with SHARED in shared memory: tiles of
+// 128 rows have no registers left (attend: 230 -> 220 us), those of 48 are faster with (288, 296).
 struct FinderState {
   Walk ahead;
   unsigned j;  // the chunk that is next
 };
-template <int D>
+template <int D, bool SHARED>
 struct Finder {
-  FinderState* state;
+  FinderState *state, own;
   int id;
+  __device__ __forceinline__ void keep(const Walk& ahead, unsigned j) {
+    if (!SHARED) {
+      own.ahead = ahead;
+      own.j = j;
+    } else {
+      if (lane_id() == 0) {
+        state->ahead = ahead;
+        state->j = j;
+      }
+      __syncwarp();
+    }
+  }
   __device__ __forceinline__ void start(const AttendParams& p, const Share& s, FinderState* at) {
     state = at;
     const Walk ahead(p, s);
-    if (lane_id() == 0) {
-      state->ahead = ahead;
-      state->j = 0;
-    }
-    __syncwarp();
+    keep(ahead, 0);
     fetch(p, ahead);
   }
   __device__ __forceinline__ void fetch(const AttendParams& p, const Walk& ahead) {
@@ -223,9 +232,9 @@ struct Finder {
              : -1;
   }
   __device__ __forceinline__ void find(const AttendParams& p, ChunkRef (&refs)[4]) {
-    Walk ahead = state->ahead;
-    const unsigned j = state->j;
-    __syncwarp();
+    Walk ahead = SHARED ? state->ahead : own.ahead;
+    const unsigned j = SHARED ? state->j : own.j;
+    if (SHARED) __syncwarp();
     if (ahead.left <= 0) return;
     const int lane = lane_id();
     const int slot0 = (ahead.r.lo / kSlotsTile + ahead.c) * kSlotsTile;
@@ -248,11 +257,7 @@ struct Finder {
       ref.whole = valid == 0xffu && slot0 >= ahead.r.lo && slot0 + kSlotsTile <= ahead.r.len;
     }
     ahead.skip(p, 1);
-    if (lane == 0) {
-      state->ahead = ahead;
-      state->j = j + 1;
-    }
-    __syncwarp();
+    keep(ahead, j + 1);
     fetch(p, ahead);
   }
 };
