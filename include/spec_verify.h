@@ -580,7 +580,7 @@ size_t spec_cache_page_bytes(int page_size, int head_dim);
  *   k, v        [B, N, kv_heads, head_dim] dtype at byte strides k_strides[3],
  *               v_strides[3] of b, n and h (>= 0, multiples of 16, 16-byte aligned; each
  *               row of head_dim values contiguous).
- * B * N * kv_heads < 2^31. */
+ * 0 <= N <= SV_MAX_SLOTS, B * N * kv_heads < 2^31. */
 sv_status spec_cache_write(void* cache, int64_t page_stride, const void* k,
                            const int64_t* k_strides, const void* v, const int64_t* v_strides,
                            const int32_t* table, const int32_t* start, const int32_t* lens,

@@ -505,7 +505,8 @@ sv_status move(bool write, const void* cache, int64_t page_stride, const Dense& 
   CacheParams p;
   memset(&p, 0, sizeof p);
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
-  if (N < 0) return SV_ERR_SHAPE;
+  // (a slot of place_of: up to 2 SV_MAX_SLOTS and a few, in 32 bits)
+  if (N < 0 || N > SV_MAX_SLOTS) return SV_ERR_SHAPE;
   sv_status rc = check_cache(&p.cache, cache, page_stride, table, pages, page_size, B, M, kv_heads,
                              head_dim);
   if (rc != SV_OK) return rc;
