@@ -629,6 +629,8 @@ sv_status spec_cache_keep(void* cache, int64_t page_stride, const int32_t* table
  *               SV_REQ_BAD_TREE, and the request's rows are 0.
  *   slopes      [q_heads] fp32 or NULL (no bias).
  *   scale       finite.  softcap up to 1e30, 0: none.  window 0: none.
+ *               Scores and the parts that they are made of, |scale| max |q| of a row among
+ *               them, are to stay below 2^127: other rows have no defined values.
  *   out         [B, N, q_heads, head_dim] dtype, contiguous, 16-byte aligned; rows
  *               behind q_lens[b] are left as they are.  It must not reach into the bytes
  *               from q's first to its last (SV_ERR_ALIAS), nor into other inputs.

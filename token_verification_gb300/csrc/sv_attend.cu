@@ -283,7 +283,7 @@ __device__ __forceinline__ void load_query(const AttendParams& p, int b, int h, 
 // What the lanes of a warp keep of their rows (2 t and 2 t + 1 of each tile).
 template <int D, int NT>
 struct Rows {
-  float m[NT][2], l[NT][2];  // running max (log2), the lane's part of the sum
+  float ref[NT][2], l[NT][2];  // the weights' reference (log2), the lane's part of the sum
   float o[NT][D / 16][4];
 };
 
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        acc.m[n][e] = -INFINITY;
+        acc.ref[n][e] = -INFINITY;
         acc.l[n][e] = 0.f;
         const int row = min(row0 + 8 * n + 2 * t + e, max(rows - 1, 0));
         const int i = row / p.group;
@@ -485,8 +485,8 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
         uint32_t P[kTiles][NT][NP][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          // the running max of each row: the lanes of a column meet only where one of them
-          // found a larger score
+          // each row's reference: 15 below its largest score, rounded up, so that no exponent is above 15. The
+          // lanes of a column meet only where one of them found a larger score
           float f[2], top[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -497,25 +497,39 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
               top[e] = fmaxf(top[e], fmaxf(s[k][n][e], s[k][n][e + 2]));
             top[e] *= f[e];
           }
-          if (__any_sync(kAll, top[0] > acc.m[n][0] || top[1] > acc.m[n][1])) {
+          // (and in every chunk of rows whose references are far from 0)
+          if (__any_sync(kAll, top[0] - acc.ref[n][0] > kFewShift || top[1] - acc.ref[n][1] > kFewShift ||
+                                   fabsf(acc.ref[n][0]) >= kFar || fabsf(acc.ref[n][1]) >= kFar)) {
+            bool far = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float m = fmaxf(top[e], acc.m[n][e]);
+              float ref = fmaxf(__fadd_ru(top[e], -kFewShift), acc.ref[n][e]);
 #pragma unroll
-              for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, x));
-              const float g1 = acc.m[n][e] == -INFINITY ? 0.f : ex2(acc.m[n][e] - m);
-              acc.m[n][e] = m;
+              for (int x = 4; x < 32; x <<= 1) ref = fmaxf(ref, __shfl_xor_sync(kAll, ref, x));
+              const float g1 = acc.ref[n][e] == -INFINITY ? 0.f : ex2(acc.ref[n][e] - ref);
+              acc.ref[n][e] = ref;
               acc.l[n][e] *= g1;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 acc.o[n][i][e] *= g1;
                 acc.o[n][i][e + 2] *= g1;
               }
+              far |= fabsf(ref) >= kFar;
+            }
+            if (__any_sync(kAll, far)) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int k = 0; k < kTiles; ++k)
+#pragma unroll
+                  for (int x = 0; x < 4; x += 2) s[k][n][e + x] = __fmul_rn(s[k][n][e + x], f[e]);
+                f[e] = 1.f;
+              }
             }
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float off = acc.m[n][e] == -INFINITY ? 0.f : kFewShift - acc.m[n][e];
+            const float off = acc.ref[n][e] == -INFINITY ? 0.f : -acc.ref[n][e];
 #pragma unroll
             for (int k = 0; k < kTiles; ++k)
 #pragma unroll
@@ -572,7 +586,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
           *reinterpret_cast<float2*>(row + dim_of<D>(i)) =
               make_float2(acc.o[n][i][e], acc.o[n][i][e + 2]);
         if (g == 0) {
-          row[D] = acc.m[n][e];
+          row[D] = acc.ref[n][e];
           row[D + 1] = l;
         }
       }
@@ -607,8 +621,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
         else
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to * D + d) =
               make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-        if (p.out_lse && d == 0)
-          p.out_lse[to] = l == 0.f ? -INFINITY : (m - kFewShift + log2f(l)) * 0.6931471805599453f;
+        if (p.out_lse && d == 0) p.out_lse[to] = log_sum(m, l, 0.f);
       } else {
         float* dst = part + row * kStep;
         *reinterpret_cast<float4*>(dst + d) = o;
@@ -744,8 +757,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
           *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + to * D + lane * kVec +
                                        e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
       }
-      if (p.out_lse && lane == 0)
-        p.out_lse[to] = l == 0.f ? -INFINITY : (m - p.shift + log2f(l)) * 0.6931471805599453f;
+      if (p.out_lse && lane == 0) p.out_lse[to] = log_sum(m, l, p.shift);
     }
     if (WIDE) __syncthreads();
   }
@@ -779,7 +791,7 @@ cudaError_t plan_one(AttendPlan* plan) {
   plan->rows = 8 * NT;
   plan->chunk = D == 256 ? 16 : 32;
   plan->least = kFewWarps;
-  plan->shift = kFewShift;
+  plan->shift = 0.f;  // (partial rows hold references)
   return resident(few_kernel<D, NT, T>, kFewThreads, few_smem<D, NT>(),
                   few_smem<D, NT>() + tree_bytes(SV_MAX_STEP), cache, &plan->ctas);
 }

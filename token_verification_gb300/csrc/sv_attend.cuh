@@ -16,9 +16,23 @@
 
 namespace sv {
 
-// Weights are 2^(score - max + shift).  With a shift of 15 the largest is 2^15, and fp16's
-// least step of 2^-24 is 2^-39 of it.
+// Weights are 2^(score - reference), the largest of a row 2^15 (few rows) or 2^7 to 2^15 (many): fp16's
+// least step of 2^-24 is 2^-39 or 2^-31 of it.
 constexpr float kFewShift = 15.f;
+// Scores are taken times their factor and less the reference in one step, which keeps places of the
+// product that a max in 32 bits has lost: 2^-11 at a reference of 2^14, 1 (a weight of 2^16, none of
+// fp16's) at 2^24, and all of the weight at 2^28. From kFar on the product is rounded first, so that
+// exponents are differences of 32-bit scores.
+constexpr float kFar = 16384.f;
+constexpr float kLeast = -3.402823466e38f;  // in place of a max of -inf
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m != -INFINITY; }
+__device__ __forceinline__ float far_exponent(float s, float f, float m, float shift) {
+  return __fadd_rn(__fsub_rn(__fmul_rn(s, f), fmaxf(m, kLeast)), shift);
+}
+// The log-sum-exp of weights 2^(x - m + shift), x in units of log2, that add up to l.
+__device__ __forceinline__ float log_sum(float m, float l, float shift) {
+  return l == 0.f ? -INFINITY : (m + (log2f(l) - shift)) * 0.6931471805599453f;
+}
 
 struct AttendParams {
   CacheView cache;
@@ -41,7 +55,7 @@ struct AttendParams {
   int least;                 // chunks that are worth a CTA
   int* desc;                 // [G][4] the split unit that begins in each CTA's share: b, head, row tile, pieces
   int* late;                 // [G] whether a wait in the CTA ran out, or null
-  float shift;               // of the weights' exponents
+  float shift;               // exponent of the weight of a score that equals a partial row's max
   unsigned long long wait_ns;  // limit of the waits
   float* part;               // [2 G][rows][D + 4] unfinished rows: values, max, sum
 };

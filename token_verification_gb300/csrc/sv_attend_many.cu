@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
     f32x2 l[NH / 2];
 #pragma unroll
     for (int i = 0; i < NH / 2; ++i) l[i] = pack2(0.f, 0.f);
+    bool far = false;  // a row's max is (the same in every thread)
     for (int c = c0; c < c1 && !late; ++c, ++j) {
       bool out_of_time = !sleep_wait(qk_bar, j & 1, limit);
       // the next chunk's keys, whose product runs while this chunk's weights are worked out
@@ -359,7 +360,14 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
         load_scores();
         // exponents of the weights; is one too large for its row's reference?
         float top[2] = {-INFINITY, -INFINITY};
-        if (plain) {
+        if (far) {
+#pragma unroll
+          for (int i = 0; i < NH; ++i) {
+            const int row = row_at + i;
+            const float f = plain ? reinterpret_cast<const float*>(&sm.fo[row / 2])[row & 1] : 1.f;
+            s[i] = far_exponent(s[i], f, sm.m[row], kManyShift);
+          }
+        } else if (plain) {
 #pragma unroll
           for (int i = 0; i < NH / 2; ++i) {
             const float4 fo = sm.fo[row_at / 2 + i];
@@ -397,6 +405,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           if (lane == i) joined[quarter][row_at + i] = y;
         }
         __syncthreads();
+        bool mine_far = false;
         if (tid < NC) {
           const float old = sm.m[tid];
           const float m = fmaxf(fmaxf(old, joined[0][tid]),
@@ -405,8 +414,9 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           sm.change[tid] = old == -INFINITY ? 0.f : ex2(old - m);
           reinterpret_cast<float*>(&sm.fo[tid / 2])[2 + (tid & 1)] =
               m == -INFINITY ? kNoRef : kManyShift - m;
+          mine_far = is_far(m);
         }
-        __syncthreads();
+        far = __syncthreads_or(mine_far) != 0;
         if (c > c0) {  // the sums and O so far
           float o[NH];
           tmem_load(mine + kOCol, o);
@@ -482,8 +492,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           part[tid * (D + 4) + D] = sm.m[tid];
           part[tid * (D + 4) + D + 1] = sum;
         } else if (p.out_lse) {
-          p.out_lse[out0 + sm.out_row[tid]] =
-              sum == 0.f ? -INFINITY : (sm.m[tid] - kManyShift + log2f(sum)) * 0.6931471805599453f;
+          p.out_lse[out0 + sm.out_row[tid]] = log_sum(sm.m[tid], sum, kManyShift);
         }
       }
     }

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
     }
     __syncwarp();
     const float f = sm.fo[row];
-    float m = -INFINITY, off = kNoRef;
+    float m = -INFINITY;
     f32x2 l = pack2(0.f, 0.f);
     for (int c = c0; c < c1 && !late; ++c, ++j) {
       bool out_of_time = false;
@@ -314,14 +314,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
         top = max3(top, t[0], t[1]);
       }
       top *= fe;  // (factors are not negative)
-      if (__syncthreads_or(top + off > kManyShift + kSlack)) {
+      if (__syncthreads_or(top - m > kSlack)) {
         // each row's max over the chunk's slots
         sm.joined[half][row] = top;
         __syncthreads();
         const float now = max3(m, top, sm.joined[half ^ 1][row]);
         const float change = m == -INFINITY ? 0.f : ex2(m - now);
         m = now;
-        off = m == -INFINITY ? kNoRef : kManyShift - m;
         l = fma2(l, pack2(change, change), pack2(0.f, 0.f));
         if (c > c0) {
 #pragma unroll 1
@@ -339,23 +338,33 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
         }
       }
       if (warp == 7) finder.find(p, sm.refs);  // (in the place of the chunk before this one)
+      const float off = m == -INFINITY ? kNoRef : kManyShift - m;
+      auto weights = [&](auto exponents) {
 #pragma unroll 1
-      for (int part = 0; part < 4; ++part) {
-        float s[16];
-        uint32_t x[8];
-        load_scores(part, s);
-        const f32x2 f2 = pack2(fe, fe), off2 = pack2(off, off);
+        for (int part = 0; part < 4; ++part) {
+          float s[16];
+          uint32_t x[8];
+          load_scores(part, s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float w0, w1;
-          unpack2(fma2(pack2(s[2 * i], s[2 * i + 1]), f2, off2), w0, w1);
-          w0 = ex2(w0);
-          w1 = ex2(w1);
-          l = add2(l, pack2(w0, w1));
-          x[i] = pack_f16(w0, w1);
+          for (int i = 0; i < 8; ++i) {
+            float w0, w1;
+            unpack2(exponents(s[2 * i], s[2 * i + 1]), w0, w1);
+            w0 = ex2(w0);
+            w1 = ex2(w1);
+            l = add2(l, pack2(w0, w1));
+            x[i] = pack_f16(w0, w1);
+          }
+          tmem_store8(mine + 8 * part, x);
         }
-        tmem_store8(mine + 8 * part, x);
-      }
+      };
+      if (!__any_sync(0xffffffffu, is_far(m)))
+        weights([&](float y0, float y1) {
+          return fma2(pack2(y0, y1), pack2(fe, fe), pack2(off, off));
+        });
+      else
+        weights([&](float y0, float y1) {
+          return pack2(far_exponent(y0, fe, m, kManyShift), far_exponent(y1, fe, m, kManyShift));
+        });
       tmem_stored();
       // the next chunk's keys (their place is free: this chunk's scores are out)
       if (c + 1 < c1) put_keys(j + 1);
@@ -389,8 +398,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
         part[D] = m;
         part[D + 1] = sum;
       } else if (p.out_lse) {
-        p.out_lse[to] =
-            sum == 0.f ? -INFINITY : (m - kManyShift + log2f(sum)) * 0.6931471805599453f;
+        p.out_lse[to] = log_sum(m, sum, kManyShift);
       }
     }
 #pragma unroll 1

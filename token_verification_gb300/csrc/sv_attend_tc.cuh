@@ -9,7 +9,7 @@ namespace sv {
 
 constexpr int kSlotsTile = 128;  // slots of a chunk
 constexpr float kManyShift = 7.f, kSlack = 8.f;  // of the weights' exponents
-constexpr float kNoRef = 3e38f;  // in place of shift - max for a row without a score yet
+constexpr float kNoRef = -kLeast;  // in place of shift - max for a row without a score yet
 
 // ---- tcgen05 -------------------------------------------------------------
 
