@@ -120,3 +120,25 @@ def test_large_scores_capped_biased_and_windowed(D, dtype):
             for e in (24, 27, 30):
                 check(1, N + 400, N, Hq, Hkv, D, dtype, 1.37 * 2.0 ** e, "ties", g, **kw)
                 check(1, N + 400, N, Hq, Hkv, D, dtype, -1.37 * 2.0 ** e, "rising", g, **kw)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_largest_queries(D):
+    """Queries of fp32's largest numbers, whose scores are ordinary ones."""
+    g = gen(D)
+    most = torch.finfo(F32).max
+    for N, Hq, Hkv in SHAPES:
+        for big in (most, -most, 1.75 * 2.0 ** 127):
+            L = N + 90
+            k = torch.zeros((1, L, Hkv, D), device="cuda")
+            i = torch.randint(-17, 0, (L,), generator=g, device="cuda")
+            k[..., 3] = (7 * torch.exp2(i.double())).float()[:, None]
+            v = torch.randn((1, L, Hkv, D), generator=g, device="cuda")
+            cache = api.spec_cache_alloc(4, Hkv, D, 64)
+            table = ints([[3, 0, 1, 2]])
+            api.spec_cache_write(cache, k, v, table, ints([0]))
+            q = torch.zeros((1, N, Hq, D), device="cuda")
+            q[..., 3] = big
+            scale = 2.0 ** -127
+            out = api.spec_cache_attention(q, cache, table, ints([L]), scale=scale, lse=True)
+            plain.check_attention(q, cache, 64, table, ints([L]), out.out, out.lse, scale=scale)

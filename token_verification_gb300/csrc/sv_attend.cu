@@ -253,8 +253,8 @@ __device__ __forceinline__ void load_query(const AttendParams& p, int b, int h, 
     }
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-    // 2^(14 - e) for top in [2^e, 2^(e + 1)); rows of zeros or subnormals, and of infinity, by 2^+-112
-    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -98), 126);
+    // 2^(14 - e) for top in [2^e, 2^(e + 1)); rows of nothing larger than 2^-98 by 2^112
+    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -98), 127);
     float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
     if (!is_finite(top)) up = qnan();  // (infinities as NaN: their products with codes of 0 are)
     if (p.scale < 0.f) up = -up;       // scores go on with the scale's magnitude

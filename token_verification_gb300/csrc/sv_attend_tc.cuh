@@ -183,7 +183,7 @@ __device__ __forceinline__ uint4 scaled_query(const uint4& v, bool negative, flo
 #pragma unroll
   for (int o = PER / 2; o > 0; o >>= 1) top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
   const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-  const int e = min(max((int)(top >> 7) - 127, -98), 126);
+  const int e = min(max((int)(top >> 7) - 127, -98), 127);
   float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
   if (top >= 0x7f80u) up = qnan();
   if (negative) up = -up;
