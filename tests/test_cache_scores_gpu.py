@@ -142,3 +142,27 @@ def test_largest_queries(D):
             scale = 2.0 ** -127
             out = api.spec_cache_attention(q, cache, table, ints([L]), scale=scale, lse=True)
             plain.check_attention(q, cache, 64, table, ints([L]), out.out, out.lse, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_largest_scales(D, dtype):
+    """Scales up to fp32's largest number, over queries that are 0 or give ordinary scores."""
+    g = gen(D + 1)
+    most = torch.finfo(F32).max
+    for N, Hq, Hkv in SHAPES:
+        L = N + 90
+        k = torch.zeros((1, L, Hkv, D), device="cuda")
+        i = torch.randint(-17, 0, (L,), generator=g, device="cuda")
+        k[..., 3] = (7 * torch.exp2(i.double())).float()[:, None]
+        v = torch.randn((1, L, Hkv, D), generator=g, device="cuda")
+        cache = api.spec_cache_alloc(4, Hkv, D, 64)
+        table = ints([[3, 0, 1, 2]])
+        api.spec_cache_write(cache, k, v, table, ints([0]))
+        q = torch.zeros((1, N, Hq, D), device="cuda")
+        zero = q.to(dtype)
+        q[..., 3] = 2.0 ** -126
+        for x in (zero, q.to(dtype)):
+            for scale in (most, -most, 2.5e38):
+                out = api.spec_cache_attention(x, cache, table, ints([L]), scale=scale, lse=True)
+                plain.check_attention(x, cache, 64, table, ints([L]), out.out, out.lse, scale=scale)

@@ -384,9 +384,10 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
       const int* table = p.cache.table + (long long)b * p.cache.M;
       const int mask = (1 << p.cache.shift) - 1;
       // scores before the cap, or in units of log2 where there is none
-      const float unit = unit_scale(p);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) unscale[n][0] *= unit, unscale[n][1] *= unit;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) unscale[n][e] = score_factor(p, unscale[n][e]);
       // The warp's stages: chunk c's copies are queued kStages - 1 chunks ahead, its page ids
       // read one chunk before that.
       constexpr int kStageBytes = kTiles * Tile<D>::kBytes;

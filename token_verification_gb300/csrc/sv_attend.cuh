@@ -334,10 +334,12 @@ __device__ __forceinline__ void cap_all(float cap, F each) {
   else
     each([=](float x) { return cap * tanh_fast(x); });
 }
-// What takes a product q . k to a capped score's tanh, or without a cap to units of log2.  (A cap may be
-// subnormal; scores of 0 stay 0.)
-__device__ __forceinline__ float unit_scale(const AttendParams& p) {
-  return p.softcap > 0.f ? fminf(fabsf(p.scale) / p.softcap, 3e38f) : fabsf(p.scale) * kLog2e;
+// What takes a sum of a row's products, of q scaled down by `down`, to a capped score's tanh, or without a
+// cap to units of log2. (A cap may be subnormal; scores of 0 stay 0. The scale meets `down` first: times
+// log2 e by itself it can be infinity.)
+__device__ __forceinline__ float score_factor(const AttendParams& p, float down) {
+  return p.softcap > 0.f ? down * fminf(fabsf(p.scale) / p.softcap, 3e38f)
+                         : down * fabsf(p.scale) * kLog2e;
 }
 
 // Joins the pieces of split units (launched behind either kernel).

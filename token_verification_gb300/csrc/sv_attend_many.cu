@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) many_kernel(const AttendParam
           scaled_query<kPer>(v, p.scale < 0.f, &down);
       if (x == 0) {
         float* fo = reinterpret_cast<float*>(&sm.fo[at / 2]) + (at & 1);
-        fo[0] = down * unit_scale(p);
+        fo[0] = score_factor(p, down);
         fo[2] = kNoRef;
         sm.m[at] = -INFINITY;
         sm.slope[at] = p.slopes ? p.slopes[head] * kLog2e : 0.f;

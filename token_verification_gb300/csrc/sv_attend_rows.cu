@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const AttendParam
       *reinterpret_cast<uint4*>(sm.q + (x / 8) * kBlockBytes + at * 128 + (((x & 7) ^ (at & 7)) << 4)) =
           scaled_query<kPer>(v, p.scale < 0.f, &down);
       if (x == 0) {
-        sm.fo[at] = down * unit_scale(p);
+        sm.fo[at] = score_factor(p, down);
         sm.slope[at] = p.slopes ? p.slopes[head] * kLog2e : 0.f;
         sm.node[at] = i;
         sm.pos[at] = w.r.base + (p.parent && sees ? tree.depth(i) : i);
