@@ -714,12 +714,20 @@ def spec_beam_reorder(state, parents, out=None, *, lens=None, status=None) -> to
 # ---------------------------------------------------------------------------
 
 _Strides3 = ctypes.c_int64 * 3
+_INT_MAX = 2**31 - 1
+
+
+def _sizes(*n):
+    """Refuse extents past the 32 bits that the C interface has for them (ctypes cuts without a word)."""
+    if n and max(n) > _INT_MAX:
+        raise VerifyError(2)
 
 
 def spec_cache_alloc(pages, kv_heads, head_dim, page_size=64, device="cuda") -> torch.Tensor:
     """A cache of `pages` pages for one layer (see spec_verify.h): zeros, uint8
     [pages, kv_heads, 2, page bytes].  The cache calls also take a layer's part of a larger
     tensor, [pages, layers, kv_heads, 2, page bytes][:, layer] for one."""
+    _sizes(int(page_size), int(head_dim))
     size = int(_native.lib().spec_cache_page_bytes(int(page_size), int(head_dim)))
     if size == 0:
         raise ValueError("unsupported page_size=%s head_dim=%s" % (page_size, head_dim))
@@ -748,6 +756,7 @@ def _cache_args(cache, table, head_dim):
         raise ValueError("table must be a [B, M] tensor")
     B, M = table.shape
     _need(table, "table", device, torch.int32, (B, M))
+    _sizes(pages, heads, B, M)
     return device, cache.stride(0), pages, page_size, B, M, heads
 
 
@@ -761,6 +770,7 @@ def _dense(t, name, device, dtype, shape):
         raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    _sizes(*t.shape)
     a, b, c, d = t.stride()
     if t.shape[3] > 1 and d != 1:
         raise ValueError("the last dimension of %s must be contiguous" % name)
@@ -930,7 +940,8 @@ def spec_cache_attention(q, cache, table, lens, out: Optional[AttentionOutputs] 
     ws = torch.empty(need, dtype=torch.uint8, device=device)
     _launch(device, lib.spec_cache_attention, q.data_ptr(), qs, cache.data_ptr(), stride,
             _addr(table), _addr(lens), _addr(q_lens), _addr(parent), parent_stride, _addr(slopes),
-            float(D ** -0.5 if scale is None else scale), float(softcap), int(window),
+            float(D ** -0.5 if scale is None else scale), float(softcap),
+            max(-1, min(int(window), _INT_MAX)),  # (no slot is further back than that)
             out.out.data_ptr(), _addr(out.lse), _addr(out.status), code, pages, page_size, B, N, M,
             Hq, H, D, _addr(ws), need)
     if given:
