@@ -676,6 +676,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendParams p
       if (lane == 0) p.out_status[b] = st | ran_out;
     }
   }
+  if (!p.desc) return;  // (a step of no tokens: statuses alone)
   const int cta = blockIdx.x;
   const int4 d4 = *reinterpret_cast<const int4*>(p.desc + 4 * cta);
   const int pieces = d4.w;
@@ -924,7 +925,20 @@ extern "C" sv_status spec_cache_attention(
   if (!(scale == scale) || scale - scale != 0.f || !(softcap >= 0.f && softcap <= 1e30f) || window < 0)
     return SV_ERR_SCORE;
   if (tree_parent && parent_stride != 0 && parent_stride != N - 1) return SV_ERR_TREE;
-  if (B == 0 || N == 0) return SV_OK;
+  if (B == 0 || (N == 0 && !out_status)) return SV_OK;
+  if (N == 0) {  // no rows, but the requests' lengths and pages are looked at
+    if (!lens) return SV_ERR_NULL;
+    p.out_status = out_status;
+    p.lens = lens;
+    p.q_lens = q_lens;
+    p.B = B;
+    p.window = window;
+    p.rows = p.chunk = p.group = 1;
+    const int blocks = std::min((B + kJoinWarps - 1) / kJoinWarps, 1024);
+    return launch_join(p, head_dim, dtype, blocks, blocks, (cudaStream_t)stream) == cudaSuccess
+               ? SV_OK
+               : SV_ERR_CUDA;
+  }
   if (!lens || !q || !q_strides || !out || ((uintptr_t)q & 15) || ((uintptr_t)out & 15))
     return SV_ERR_NULL;
   const int esize = dtype == SV_F32 ? 4 : 2;
