@@ -93,3 +93,22 @@ def test_ordinary_and_wide_scores(N, Hq, Hkv, D, dtype):
                 assert float((tol / (o.abs() + 0.01)).median()) < (2.0 ** -9 if dtype == F32 else 2.0 ** -5)
                 assert bool(((out.out[0].double() - o).abs() <= tol).all())
                 assert bool(((out.lse[0].double() - lse).abs() <= ltol).all())
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 1), (128, 4), (256, 2), (128, 24)])
+def test_long_sums_of_fp32(D, Hq):
+    """131072 slots of one CTA each, values of one sign. A lane adds 4096 weights; ordinary additions are off
+    by up to u in either direction, so that n of them come to sqrt(n) u or so: 8 times that, and 2^-17 for
+    the 256 products of the tensor cores between two ordinary additions of the values."""
+    g = gen(D + Hq)
+    L, page, B = 131072, 256, 640
+    cache, table, kv = filled(L, 1, D, page, g, True)
+    q = whole((1, 1, Hq, D), 8, g)
+    scale = float(torch.tensor(0.5 / (22 * D ** 0.5), dtype=torch.float32))
+    out = api.spec_cache_attention(q.expand(B, 1, Hq, D), cache, table.expand(B, -1).contiguous(),
+                                   ints([L] * B), scale=scale, lse=True)
+    far = torch.arange(L - 1, -1, -1, device="cuda")[None].double()
+    o, tol, lse, ltol = expected(q[0], kv, far >= 0, far, scale, F32, sums=8 * 4096 ** 0.5 * U + 2.0 ** -17)
+    assert float((tol / o.abs()).median()) < 2.0 ** -13
+    assert bool(((out.out.double() - o).abs() <= tol).all())
+    assert bool(((out.lse.double() - lse).abs() <= ltol).all())

@@ -307,6 +307,63 @@ __host__ __device__ constexpr int few_ring() {
   const int rows = kFewWarps * 8 * NT * (D + 4) * (int)sizeof(float);
   return ring > rows ? ring : rows;
 }
+// The tensor instruction cuts its sums off: 2^-24 of them a product of 16 slots or so, always towards 0,
+// which was 2^-12 of the result over 131072 slots of one CTA. bf16, whose half step is 2^-9 and more, leaves
+// it at that. In fp32 calls a thread adds what it has of the weighted values to a second sum in the workspace, by
+// ordinary additions, every 256 products (2048 slots of the warp, 8192 of the unit), and starts again
+// from 0: 2^-17 at most. 64 tokens of up to 8192 slots (8 heads of 128) take 136 us, 132 without; every 64 products
+// cost 9 %, products that start from 0 in every tile 6 %, second sums in shared memory a CTA an SM for
+// trees of more than 160 nodes.
+template <int D>
+__host__ __device__ constexpr int fold_chunks() {
+  return 128 / few_tiles<D>();
+}
+template <int D, int NT, typename T>
+__host__ __device__ constexpr int few_fold() {  // a thread's sums and their references
+  return sizeof(T) == 4 ? kFewThreads * NT * (D / 4 + 2) * (int)sizeof(float) : 0;
+}
+template <int D, int NT>
+struct Fold {
+  float* at;  // the thread's first word; word i is kFewThreads i on
+  __device__ __forceinline__ float& word(int i) const { return at[i * kFewThreads]; }
+  static constexpr int kPer = D / 4 + 2;  // of a tile: its sums, two references
+  // sum = sum (`first`: 0) + o, o = 0
+  __device__ __forceinline__ void add(Rows<D, NT>& acc, bool first) const {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float g = factor(n, e, acc.ref[n][e], first);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int x = e; x < 4; x += 2) {
+            float& sum = word(n * kPer + 4 * i + x);
+            sum = first ? acc.o[n][i][x] : fmaf(sum, g, acc.o[n][i][x]);
+            acc.o[n][i][x] = 0.f;
+          }
+        word(n * kPer + D / 4 + e) = acc.ref[n][e];
+      }
+  }
+  // o = sum + o
+  __device__ __forceinline__ void take(Rows<D, NT>& acc) const {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float g = factor(n, e, acc.ref[n][e], false);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int x = e; x < 4; x += 2)
+            acc.o[n][i][x] = fmaf(word(n * kPer + 4 * i + x), g, acc.o[n][i][x]);
+      }
+  }
+  __device__ __forceinline__ float factor(int n, int e, float ref, bool first) const {
+    const float old = first ? -INFINITY : word(n * kPer + D / 4 + e);
+    return old == -INFINITY ? 0.f : ex2(old - ref);  // (NaN stays NaN times 0)
+  }
+};
 template <int D, int NT>
 constexpr size_t few_smem() {
   return kFewScan + few_ring<D, NT>();
@@ -329,6 +386,8 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
   char* ring = raw_smem + kFewScan;
   float* rows_out = reinterpret_cast<float*>(ring);
   const TreeView tree(ring + few_ring<D, NT>(), ring, p.N);  // (if p.parent)
+  const Fold<D, NT> fold{p.fold + (long long)blockIdx.x * (few_fold<D, NT, T>() / (int)sizeof(float)) +
+                         threadIdx.x};
   pdl_wait();
   pdl_launch_dependents();
   const int cta = blockIdx.x, lane = lane_id(), warp = threadIdx.x / 32;
@@ -567,7 +626,12 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks<D, NT, T>()) few_kerne
           }
           values<D, NT, NP>(stage + k * Tile<D>::kBytes, P[k], dead, acc.o);
         }
+        if (kExact) {
+          const int done = (c - c0) / kFewWarps + 1;
+          if (done % fold_chunks<D>() == 0) fold.add(acc, done == fold_chunks<D>());
+        }
       }
+      if (kExact && (c1 - c0 - warp + kFewWarps - 1) / kFewWarps >= fold_chunks<D>()) fold.take(acc);
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncthreads();  // (the stages are read)
@@ -794,6 +858,7 @@ cudaError_t plan_one(AttendPlan* plan) {
   plan->chunk = D == 256 ? 16 : 32;
   plan->least = kFewWarps;
   plan->shift = 0.f;  // (partial rows hold references)
+  plan->fold = few_fold<D, NT, T>();
   return resident(few_kernel<D, NT, T>, kFewThreads, few_smem<D, NT>(),
                   few_smem<D, NT>() + tree_bytes(SV_MAX_STEP), cache, &plan->ctas);
 }
@@ -878,13 +943,16 @@ cudaError_t plan_of(sv_dtype dtype, int rows, int D, AttendPlan* plan) {
   return many_rows(dtype, rows, D) ? plan_many(rows, plan) : plan_few(D, dtype, rows, plan);
 }
 
-// The workspace: the split units, a flag for each CTA, the unfinished rows.
+// The workspace: the split units, a flag for each CTA, the unfinished rows, second sums.
 size_t flag_offset(const AttendPlan& plan) { return (size_t)plan.ctas * 16; }
 size_t part_offset(const AttendPlan& plan) {
   return flag_offset(plan) + ((size_t)plan.ctas * 4 + 15) / 16 * 16;
 }
-size_t workspace_bytes(const AttendPlan& plan, int D) {
+size_t fold_offset(const AttendPlan& plan, int D) {
   return part_offset(plan) + (size_t)plan.ctas * 2 * plan.rows * (D + 4) * sizeof(float);
+}
+size_t workspace_bytes(const AttendPlan& plan, int D) {
+  return fold_offset(plan, D) + (size_t)plan.ctas * plan.fold;
 }
 
 bool shape_ok(int N, int Hq, int Hkv, int D) {
@@ -986,6 +1054,7 @@ extern "C" sv_status spec_cache_attention(
   p.desc = reinterpret_cast<int*>(ws);
   p.late = many ? reinterpret_cast<int*>(ws + flag_offset(plan)) : nullptr;
   p.part = reinterpret_cast<float*>(ws + part_offset(plan));
+  p.fold = reinterpret_cast<float*>(ws + fold_offset(plan, head_dim));
   p.shift = plan.shift;
   p.wait_ns = wait_limit_ns();
   const cudaStream_t s = (cudaStream_t)stream;

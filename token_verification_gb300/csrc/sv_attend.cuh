@@ -58,6 +58,7 @@ struct AttendParams {
   float shift;               // exponent of the weight of a score that equals a partial row's max
   unsigned long long wait_ns;  // limit of the waits
   float* part;               // [2 G][rows][D + 4] unfinished rows: values, max, sum
+  float* fold;               // [G] second sums of the fp32 calls
 };
 
 // What a request's arguments come to.
@@ -349,6 +350,7 @@ cudaError_t launch_join(const AttendParams& p, int D, int dtype, int ctas, int u
 // The kernel for tiles of few rows and the one for many (tensor memory); they fill in the split.
 struct AttendPlan {
   int rows, chunk, least, ctas;
+  int fold;  // bytes of a CTA's second sums
   float shift;
 };
 cudaError_t plan_few(int D, int dtype, int rows, AttendPlan* plan);

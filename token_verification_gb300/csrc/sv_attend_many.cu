@@ -575,6 +575,7 @@ cudaError_t plan_many(int rows, AttendPlan* plan) {
   plan->least = 1;
   plan->shift = kManyShift;
   plan->ctas = 2 * info.sms;
+  plan->fold = 0;
   return cudaSuccess;
 }
 
