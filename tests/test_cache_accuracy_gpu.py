@@ -10,6 +10,8 @@ step: fp16's least step is 2^-24 and a row's largest weight is 2^7 or more (2^14
 rows), so that a small weight is off by 2^-25 and by 2^-32 (2^-39) of the largest at most.
 sums: the weighted values of L slots are added 16 at a time, a step cut off by at most 2^-23 of the sum
 so far; the weights' own sum is off by at most u of it for each of a lane's terms."""
+import math
+
 import pytest
 import torch
 
@@ -112,3 +114,24 @@ def test_long_sums_of_fp32(D, Hq):
     assert float((tol / o.abs()).median()) < 2.0 ** -13
     assert bool(((out.out.double() - o).abs() <= tol).all())
     assert bool(((out.lse.double() - lse).abs() <= ltol).all())
+
+
+@pytest.mark.parametrize("Hq,dtype", [(4, BF16), (24, BF16), (64, BF16), (2, F32)])
+def test_longest_context_of_one_sign(Hq, dtype):
+    """2^27 slots, which all lie in one page, and values of 4 to 7. A block adds the weighted values of 2^27 / 152
+    slots at most, 16 at a time, each time off by up to 2^-23 of the sum: 2^-7.2 of it. In fp32 a lane adds
+    2^27 / 152 / 32 weights, the same few over and over, each time off by up to u: 2^-9.2."""
+    g = gen(Hq)
+    D, page, many = 64, 256, 1 << 19
+    cache, _, kv = filled(page, 1, D, page, g, True)
+    q = whole((1, 1, Hq, D), 8, g)
+    scale = float(torch.tensor(1.0 / (22 * D ** 0.5), dtype=torch.float32))
+    out = api.spec_cache_attention(q.to(dtype), cache, torch.zeros((1, many), dtype=torch.int32, device="cuda"),
+                                   ints([page * many]), scale=scale, lse=True)
+    assert out.status.tolist() == [0]
+    far = torch.zeros((1, page), dtype=torch.float64, device="cuda")
+    sums = 2.0 ** (-7.2 if dtype == BF16 else -9.2)
+    o, tol, lse, ltol = expected(q[0], kv, far >= 0, far, scale, dtype, sums=sums / 2)
+    assert float((tol / o.abs()).median()) < 2.0 ** (-6 if dtype == BF16 else -9)
+    assert bool(((out.out[0].double() - o).abs() <= tol).all())
+    assert bool(((out.lse[0].double() - lse - math.log(many)).abs() <= ltol + sums + 4 * U * math.log(many)).all())
