@@ -643,6 +643,7 @@ sv_status spec_cache_keep(void* cache, int64_t page_stride, const int32_t* table
  * 2^-24 of them for every 16 slots that a warp (more than 16 query rows: a block) adds up: up to
  * 2^-10 of a bf16 result over 2^17 slots that one block has for itself, 2^-8 over 2^19; at most 2^-17 in
  * fp32, whatever the length.  Results do not vary between calls of the same lengths.
+ * There is no backward pass.
  * bf16 calls of more than 16 query rows a key/value head (N * q_heads / kv_heads) and a
  * head_dim of 64 or 128 wait for the tensor cores, each time no longer than the limit of
  * spec_verify_set_wait_limit_ns: a wait that ran out makes rows NaN and sets SV_REQ_TIMEOUT

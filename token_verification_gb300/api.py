@@ -892,7 +892,8 @@ def spec_cache_attention(q, cache, table, lens, out: Optional[AttentionOutputs] 
     spec_verify_tree takes it (None: a chain); scale None: head_dim ** -0.5;
     softcap: scores become softcap * tanh(score / softcap); window: slots further back
     are not seen; slopes [q_heads] fp32: scores lose slope * distance.  Rows behind
-    q_lens[b] are left as they are in a given out, and zero in a new one."""
+    q_lens[b] are left as they are in a given out, and zero in a new one.  Like the other
+    cache calls it is for inference: results have no gradient, also where q requires one."""
     if out is None and q_lens is None:
         r = _native.binding().cache_attention(q, cache, table, lens, parent, scale, softcap, window,
                                               slopes, bool(lse), bool(status))

@@ -22,7 +22,7 @@
 //
 // Each of the four warps of a CTA walks its own chunks of 32 slots with its own
 // running max and sum; the warps join at the end of a piece.
-// Measured: a token of 256 requests of up to 4096 slots (4 heads a group, 8 groups of 128) 215 us, 4.0 TB/s;
+// Measured: a token of 256 requests of up to 4096 slots (4 heads a group, 8 groups of 128) 216 us, 4.0 TB/s;
 // issue slots 60 % used, the tensor pipe busy in 76 % of the cycles, 16 warps an SM.  The first form, without
 // shared memory's ring of 3 stages a warp, took 317.
 #include <string.h>

@@ -18,14 +18,15 @@
 // while the next one's keys are decoded.
 // Bound by latencies between 16 warps an SM (issue slots 46 % used, tensor pipe 45 %, shared memory 47 %),
 // not by HBM; of about 690 instructions a warp and chunk 300 decode and 60 are exponentials.  Measured:
-// 284 us for 6 tokens each of 64 requests of up to 8192 slots (8 heads a group, 8 groups of 128; 1.6 TB/s).
+// 285 us for 6 tokens each of 64 requests of up to 8192 slots (8 heads a group, 8 groups of 128; 1.6 TB/s).
 // In an earlier form, on six tiles of 48 rows of 32 trees (470 us here), one CTA an SM took 732 us, and
 // warps of one task each (softmax, decoding, issuing) 757: each of their instructions waited
 // to be fetched.  Issuing S and O together at the chunk's end: 487.
 // A row's weights are relative to a reference that follows its running max only when a
 // score exceeds it by 2^8: the weights, at most 2^15 then, stay within fp16, and the
 // threads, which hold one slot of every row, need to agree on a row's max (and to rescale O in
-// tensor memory) a few times a piece instead of every chunk.
+// tensor memory) a few times a piece instead of every chunk. Sums in tensor memory are cut off, by 2^-23.3 of them
+// a product of 16 slots: a bf16 result's rounding outweighs that up to some 2^18 slots of one CTA.
 #include <string.h>
 
 #include <algorithm>

@@ -10,7 +10,9 @@
 // largest and once for the weights, 16 at a time (32: spilled registers, 294 instead of 230 us below).
 // Two CTAs an SM, whose 8 warps all do the same; the next chunk's keys take the place of this one's as
 // soon as S is out, the values' codes wait in registers.
-// Bound by the tensor pipe (busy in 88 % of the cycles; issue slots 46 % used).  Measured: 220 us for trees of 61 nodes over 32 requests
+// The tensor pipe counts as busy in 87 % of the cycles, issue slots are 45 % used; a chunk of a tile takes some 4800
+// cycles of an SM where its products at the measured peak rate would take 1300, and whether the products themselves or
+// what they wait for makes the difference has not been measured apart.  Measured: 222 us for trees of 61 nodes over 32 requests
 // of up to 4096 slots (4 heads a group, 8 groups of 128), 450 TFLOP/s of the trees' own products.
 #include <string.h>
 
