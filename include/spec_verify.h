@@ -641,7 +641,7 @@ sv_status spec_cache_keep(void* cache, int64_t page_stride, const int32_t* table
  * Sums are of 32-bit terms; weights are rounded to 11 bits before they meet the
  * values (22 bits in fp32).  The tensor cores cut the sums of weighted values off, by about
  * 2^-24 of them for every 16 slots that a warp (more than 16 query rows: a block) adds up: up to
- * 2^-10 of a bf16 result over 2^17 slots that one block has for itself, 2^-8 over 2^19; at most 2^-17 in
+ * 2^-10 of a bf16 result over 2^17 slots that one block has for itself, 2^-8 over 2^19; some 2^-17 in
  * fp32, whatever the length.  Results do not vary between calls of the same lengths.
  * There is no backward pass.
  * bf16 calls of more than 16 query rows a key/value head (N * q_heads / kv_heads) and a

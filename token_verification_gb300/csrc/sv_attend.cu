@@ -311,7 +311,7 @@ __host__ __device__ constexpr int few_ring() {
 // which was 2^-12 of the result over 131072 slots of one CTA. bf16, whose half step is 2^-9 and more, leaves
 // it at that. In fp32 calls a thread adds what it has of the weighted values to a second sum in the workspace, by
 // ordinary additions, every 256 products (2048 slots of the warp, 8192 of the unit), and starts again
-// from 0: 2^-17 at most. 64 tokens of up to 8192 slots (8 heads of 128) take 136 us, 132 without; every 64 products
+// from 0: some 2^-17. 64 tokens of up to 8192 slots (8 heads of 128) take 136 us, 132 without; every 64 products
 // cost 9 %, products that start from 0 in every tile 6 %, second sums in shared memory a CTA an SM for
 // trees of more than 160 nodes.
 template <int D>

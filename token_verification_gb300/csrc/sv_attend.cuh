@@ -57,7 +57,7 @@ struct AttendParams {
   int* late;                 // [G] whether a wait in the CTA ran out, or null
   float shift;               // exponent of the weight of a score that equals a partial row's max
   unsigned long long wait_ns;  // limit of the waits
-  float* part;               // [2 G][rows][D + 4] unfinished rows: values, max, sum
+  float* part;               // [2 G][rows][D + 4] unfinished rows: values, max or reference, sum
   float* fold;               // [G] second sums of the fp32 calls
 };
 
